@@ -28,6 +28,10 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_HIP, ERR_SCRATCH = 0, -1, -2, -3, -4
 # gemm_test_switches flags
 TEST_FORCE_GENERAL, TEST_NO_SPLITK, TEST_FORCE_STREAMK, TEST_F32_VALU = 1, 2, 4, 8
 NOALLOC_SCRATCH_BYTES = 64 << 20
+# libgemm_experts.h
+INPUT_F32, INPUT_BF16, INPUT_F16 = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ROUTE_MAX_EXPERTS, ROUTE_MAX_TOP_K, ROUTE_MAX_GROUPS = 1024, 32, 64
 
 _lib = None
 
@@ -118,6 +122,31 @@ def library() -> ctypes.CDLL:
         lib.gemm_f32_bf16x3.restype = i32
         lib.gemm_kernel_name_bf16x3.argtypes = common + [i64, i64, i64, i64, vp, sz]
         lib.gemm_kernel_name_bf16x3.restype = ctypes.c_char_p
+        lib.gemm_f8_block_quantize.argtypes = [i64, i64, vp, i64, i32, vp, i64, i32, i64, vp, i64,
+                                               vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i64,
+                                               i64, vp]
+        block = [vp, i64, i32, vp, i64, i64]  # an operand: codes, ld, format, scales, lds, block
+        row_block = [vp, i64, i32, vp, i64]   # the same, always a scale per row
+        f8_block = [i64, i64, i64, f32] + block + block + [f32, vp, i64, i32, i32, i64, i64, i64,
+                                                           i64, i64, i64]
+        experts = [i64, i64, i64, i64, vp, f32] + row_block + block + [i64, i64, f32, vp, i64, i32]
+        wgrad = [i64, i64, i64, i64, vp, f32] + row_block + row_block + [f32, vp, i64, i64, i32]
+        for name, args in (("gemm_f8_block", f8_block), ("gemm_experts_f8", experts),
+                           ("gemm_experts_f8_wgrad", wgrad)):
+            getattr(lib, name).argtypes = args + [vp]
+            getattr(lib, name + "_kernel_name").argtypes = args
+            getattr(lib, name + "_kernel_name").restype = ctypes.c_char_p
+        lib.gemm_experts_rows.argtypes = [i64, i64, i64, i64]
+        lib.gemm_experts_rows.restype = i64
+        lib.gemm_experts_route_workspace_size.argtypes = [i64, i64, i64]
+        lib.gemm_experts_route_workspace_size.restype = sz
+        lib.gemm_experts_route.argtypes = [i64, i64, vp, i64, i32, vp, vp, i32, i64, i64, i64, i64,
+                                           i32, f32, vp, vp, i64, i64, vp, vp, vp, vp, sz, vp]
+        lib.gemm_experts_route_backward.argtypes = [i64, i64, vp, i64, i32, i32, i64, i32, f32, vp,
+                                                    vp, vp, i64, vp]
+        for name in ("gemm_f8_block_quantize", "gemm_f8_block", "gemm_experts_f8",
+                     "gemm_experts_f8_wgrad", "gemm_experts_route", "gemm_experts_route_backward"):
+            getattr(lib, name).restype = i32
         _lib = lib
     return _lib
 
@@ -298,6 +327,123 @@ def mx_kernel_name(M, N, K, alpha, A, lda, format_a, scale_a, ldsa, B, ldb, form
                                           batch, stride_a, stride_b, stride_scale_a,
                                           stride_scale_b, stride_c, workspace, workspace_bytes)
     return None if name is None else name.decode()
+
+
+def gemm_f8_block_quantize(rows, cols, X, ldx, in_type, index, x_rows, format, block, Q, ldq, S,
+                           lds, QT, ldqt, ST, ldst, batch=1, stride_x=0, stride_q=0, stride_s=0,
+                           stride_qt=0, stride_st=0, stream=None, raise_on_error=True):
+    """X (rows x cols of INPUT_*, rows gathered by an int32 index when that is
+    not 0) to F8_* codes and one fp32 scale per 1 x 128 or 128 x 128 block:
+    Q, S along the columns, QT, ST along the rows; 0, 0 for a direction that
+    is not wanted."""
+    st = library().gemm_f8_block_quantize(rows, cols, X, ldx, in_type, index, x_rows, format,
+                                          block, Q, ldq, S, lds, QT, ldqt, ST, ldst, batch,
+                                          stride_x, stride_q, stride_s, stride_qt, stride_st,
+                                          _stream(stream))
+    return _check(st, "gemm_f8_block_quantize", raise_on_error)
+
+
+def gemm_f8_block(M, N, K, alpha, A, lda, format_a, scale_a, ldsa, block_a, B, ldb, format_b,
+                  scale_b, ldsb, block_b, beta, C, ldc, order_c, type_c, batch=1, stride_a=0,
+                  stride_b=0, stride_scale_a=0, stride_scale_b=0, stride_c=0, stream=None,
+                  raise_on_error=True):
+    """C <- alpha * A * B + beta * C for 8-bit operands contiguous along K
+    (A row-major, B column-major) with one fp32 scale per 128 along K, for
+    each row (block 1) or each 128 rows (block 128); C of OUTPUT_*."""
+    st = library().gemm_f8_block(M, N, K, alpha, A, lda, format_a, scale_a, ldsa, block_a, B, ldb,
+                                 format_b, scale_b, ldsb, block_b, beta, C, ldc, order_c, type_c,
+                                 batch, stride_a, stride_b, stride_scale_a, stride_scale_b,
+                                 stride_c, _stream(stream))
+    return _check(st, "gemm_f8_block", raise_on_error)
+
+
+def f8_block_kernel_name(M, N, K, alpha, A, lda, format_a, scale_a, ldsa, block_a, B, ldb,
+                         format_b, scale_b, ldsb, block_b, beta, C, ldc, order_c, type_c, batch=1,
+                         stride_a=0, stride_b=0, stride_scale_a=0, stride_scale_b=0, stride_c=0):
+    """The kernel gemm_f8_block would launch (see kernel_name)."""
+    name = library().gemm_f8_block_kernel_name(M, N, K, alpha, A, lda, format_a, scale_a, ldsa,
+                                               block_a, B, ldb, format_b, scale_b, ldsb, block_b,
+                                               beta, C, ldc, order_c, type_c, batch, stride_a,
+                                               stride_b, stride_scale_a, stride_scale_b, stride_c)
+    return None if name is None else name.decode()
+
+
+def gemm_experts_f8(experts, rows, N, K, offsets, alpha, A, lda, format_a, scale_a, ldsa, B, ldb,
+                    format_b, scale_b, ldsb, block_b, stride_b, stride_scale_b, beta, C, ldc,
+                    type_c, stream=None, raise_on_error=True):
+    """Rows offsets[e] .. offsets[e+1]-1 of A (a scale per row) times B_e, into
+    the same rows of C; offsets is a device address of experts + 1 int32."""
+    st = library().gemm_experts_f8(experts, rows, N, K, offsets, alpha, A, lda, format_a, scale_a,
+                                   ldsa, B, ldb, format_b, scale_b, ldsb, block_b, stride_b,
+                                   stride_scale_b, beta, C, ldc, type_c, _stream(stream))
+    return _check(st, "gemm_experts_f8", raise_on_error)
+
+
+def experts_f8_kernel_name(experts, rows, N, K, offsets, alpha, A, lda, format_a, scale_a, ldsa, B,
+                           ldb, format_b, scale_b, ldsb, block_b, stride_b, stride_scale_b, beta,
+                           C, ldc, type_c):
+    """The kernel gemm_experts_f8 would launch (see kernel_name)."""
+    name = library().gemm_experts_f8_kernel_name(experts, rows, N, K, offsets, alpha, A, lda,
+                                                 format_a, scale_a, ldsa, B, ldb, format_b,
+                                                 scale_b, ldsb, block_b, stride_b, stride_scale_b,
+                                                 beta, C, ldc, type_c)
+    return None if name is None else name.decode()
+
+
+def gemm_experts_f8_wgrad(experts, M, N, rows, offsets, alpha, A, lda, format_a, scale_a, ldsa, B,
+                          ldb, format_b, scale_b, ldsb, beta, C, ldc, stride_c, type_c, stream=None,
+                          raise_on_error=True):
+    """C_e <- alpha * (A's and B's positions offsets[e] .. offsets[e+1]-1
+    contracted) + beta * C_e; a scale per row of A and of B."""
+    st = library().gemm_experts_f8_wgrad(experts, M, N, rows, offsets, alpha, A, lda, format_a,
+                                         scale_a, ldsa, B, ldb, format_b, scale_b, ldsb, beta, C,
+                                         ldc, stride_c, type_c, _stream(stream))
+    return _check(st, "gemm_experts_f8_wgrad", raise_on_error)
+
+
+def experts_f8_wgrad_kernel_name(experts, M, N, rows, offsets, alpha, A, lda, format_a, scale_a,
+                                 ldsa, B, ldb, format_b, scale_b, ldsb, beta, C, ldc, stride_c,
+                                 type_c):
+    """The kernel gemm_experts_f8_wgrad would launch (see kernel_name)."""
+    name = library().gemm_experts_f8_wgrad_kernel_name(experts, M, N, rows, offsets, alpha, A, lda,
+                                                       format_a, scale_a, ldsa, B, ldb, format_b,
+                                                       scale_b, ldsb, beta, C, ldc, stride_c,
+                                                       type_c)
+    return None if name is None else name.decode()
+
+
+def experts_rows(tokens, experts, top_k, align=1) -> int:
+    """Rows that gemm_experts_route's segments need at most."""
+    return library().gemm_experts_rows(tokens, experts, top_k, align)
+
+
+def experts_route_workspace_size(tokens, experts, top_k) -> int:
+    """Bytes of workspace gemm_experts_route needs for its layout."""
+    return library().gemm_experts_route_workspace_size(tokens, experts, top_k)
+
+
+def gemm_experts_route(tokens, experts, logits, ldl, in_type, bias, keep, score, groups, top_groups,
+                       group_top, top_k, renormalise, scale, ids, weights, align=1, rows=0,
+                       offsets=0, row_tokens=0, places=0, workspace=0, workspace_bytes=0,
+                       stream=None, raise_on_error=True):
+    """top_k experts of each token and their weights (ids, weights); with
+    offsets, row_tokens and places, also the rows of each expert.  0 for a
+    bias, keep bytes or layout that is not there."""
+    st = library().gemm_experts_route(tokens, experts, logits, ldl, in_type, bias, keep, score,
+                                      groups, top_groups, group_top, top_k, renormalise, scale,
+                                      ids, weights, align, rows, offsets, row_tokens, places,
+                                      workspace, workspace_bytes, _stream(stream))
+    return _check(st, "gemm_experts_route", raise_on_error)
+
+
+def gemm_experts_route_backward(tokens, experts, logits, ldl, in_type, score, top_k, renormalise,
+                                scale, ids, d_weights, d_logits, ldd, stream=None,
+                                raise_on_error=True):
+    """d_logits from the gradient of gemm_experts_route's weights."""
+    st = library().gemm_experts_route_backward(tokens, experts, logits, ldl, in_type, score, top_k,
+                                               renormalise, scale, ids, d_weights, d_logits, ldd,
+                                               _stream(stream))
+    return _check(st, "gemm_experts_route_backward", raise_on_error)
 
 
 def workspace_size() -> int:

@@ -26,10 +26,12 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "scale.hip", "pack.hip", "noalloc.hip", "sgemm_valu.hip", "sgemm_mfma.hip", "sgemm_splitk.hip", "hgemm_mfma.hip", "hgemm_mfma_dma.hip",
-           "hgemm_splitk.hip", "gemm_skinny.hip", "f8gemm_mfma.hip", "mxgemm.hip", "split_bf16.hip"]
+           "hgemm_splitk.hip", "gemm_skinny.hip", "f8gemm_mfma.hip", "mxgemm.hip", "split_bf16.hip",
+           "f8_block_api.cpp", "f8_block.hip", "f8_block_quantize.hip", "experts_route.hip"]
 # Sources compiled once per part (-D<macro>=k, one object each), so that
 # their many kernel instantiations build in parallel: source -> (macro, parts).
-PARTS = {"hgemm_mfma.hip": ("LIBGEMM_HGEMM_PART", 4), "mxgemm.hip": ("LIBGEMM_MX_PART", 3)}
+PARTS = {"hgemm_mfma.hip": ("LIBGEMM_HGEMM_PART", 4), "mxgemm.hip": ("LIBGEMM_MX_PART", 3),
+         "f8_block.hip": ("LIBGEMM_BLOCK_PART", 4)}
 
 
 def units():

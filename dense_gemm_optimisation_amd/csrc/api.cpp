@@ -10,6 +10,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "arg_checks.hpp"
 #include "gemm_problem.hpp"
 
 namespace libgemm {
@@ -22,32 +23,6 @@ hipError_t launch_pack2(const PackSpec &sa, void *dst_a, const PackSpec &sb, voi
 using namespace libgemm;
 
 namespace {
-
-bool valid_order(int o) { return o == GEMM_ROW_MAJOR || o == GEMM_COL_MAJOR; }
-
-// Elements spanned by one rows x cols matrix stored with leading dimension ld.
-int64_t span(int64_t rows, int64_t cols, int order, int64_t ld) {
-    if (rows == 0 || cols == 0) return 0;
-    const int64_t outer = order == GEMM_ROW_MAJOR ? rows : cols;
-    const int64_t inner = order == GEMM_ROW_MAJOR ? cols : rows;
-    return (outer - 1) * ld + inner;
-}
-
-// Byte range [lo, hi) that a batched operand touches.
-struct Range {
-    uintptr_t lo, hi;
-};
-
-Range range_of(const void *p, int64_t span_elems, int64_t batch, int64_t stride, int esize) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    const int64_t elems = span_elems == 0 ? 0 : (batch - 1) * stride + span_elems;
-    return {lo, lo + static_cast<uintptr_t>(elems) * static_cast<uintptr_t>(esize)};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
-
-// Product of non-negative dimensions overflowing int64 (or the 2^31 grid).
-bool too_big(int64_t a, int64_t b) { return a != 0 && b > INT64_MAX / a; }
 
 // Kernel-choice overrides for testing (gemm_test_switches): one atomic word
 // for the whole process, read on every call.
@@ -729,6 +704,10 @@ gemm_status_t mx_run(const MxProblem &m, Kernel k, void *workspace, hipStream_t 
 }
 
 }  // namespace
+
+namespace libgemm {
+int test_switches() { return g_switches.load(std::memory_order_relaxed); }
+}  // namespace libgemm
 
 extern "C" {
 

@@ -1,0 +1,240 @@
+"""libgemm_experts.h on the CPU: exports, sizes, and every refusal (no call
+here reaches a kernel launch), and the reference's own definitions."""
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import block_reference as ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "libgemm_experts.h")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from dense_gemm_optimisation_amd import binding
+    if not os.path.exists(binding.LIB_PATH):
+        from dense_gemm_optimisation_amd import build
+        build.build()
+    return binding
+
+
+def declared():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    return sorted(set(re.findall(r"\b(gemm_\w+)\s*\(", text)))
+
+
+def test_every_declared_symbol_is_exported(lib):
+    out = subprocess.run(["nm", "-D", "--defined-only", lib.LIB_PATH], capture_output=True, text=True,
+                         check=True).stdout
+    exported = set(re.findall(r"\bT (\w+)$", out, flags=re.M))
+    assert len(declared()) == 11
+    for name in declared():
+        assert name in exported, name
+        assert getattr(lib.library(), name).argtypes is not None
+
+
+def test_header_compiles_as_c(tmp_path):
+    src = tmp_path / "use.c"
+    src.write_text('#include "libgemm_experts.h"\nint f(void){return GEMM_SCORE_SIGMOID;}\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
+                    "-I" + os.path.dirname(HEADER), "-c", str(src), "-o", str(tmp_path / "use.o")], check=True)
+
+
+# ---- the reference's definitions
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", torch.float8_e4m3fn), ("e5m2", torch.float8_e5m2)])
+def test_reference_formats_agree_with_torch(fmt, dtype):
+    bits = torch.arange(256, dtype=torch.uint8)
+    want = bits.view(dtype).to(torch.float64).numpy()
+    np.testing.assert_array_equal(ref.TABLE[fmt], want)
+    x = np.concatenate([np.random.default_rng(1).normal(size=4000) * 10.0 ** np.arange(-4, 4).repeat(500),
+                        want[np.isfinite(want)], (want[:100] + want[1:101]) / 2])
+    x = x[np.abs(x) <= ref.LARGEST[fmt]].astype(np.float32)
+    got = torch.from_numpy(x).to(dtype).view(torch.uint8).numpy()
+    np.testing.assert_array_equal(ref.encode(x.astype(np.float64), fmt), got)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_reference_route_gradient_against_differences(sigmoid, renormalise):
+    g = np.random.default_rng(2)
+    x, dw = g.normal(size=(3, 10)), g.normal(size=(3, 4))
+    args = (sigmoid, 1, 1, 1, 4, renormalise, 1.7)
+    ids, _ = ref.choose(x, None, None, *args)
+
+    def loss(v):
+        p = 1 / (1 + np.exp(-v)) if sigmoid else np.exp(v) / np.exp(v).sum(1, keepdims=True)
+        w = np.take_along_axis(p, ids, 1)
+        return 1.7 * ((w / w.sum(1, keepdims=True) if renormalise else w) * dw).sum()
+    d = ref.route_gradient(x, ids, dw, sigmoid, renormalise, 1.7)
+    h = 1e-6
+    for t in range(3):
+        for e in range(10):
+            up, down = x.copy(), x.copy()
+            up[t, e] += h
+            down[t, e] -= h
+            # the difference's own error: h^2 and 64-bit rounding over h
+            assert abs((loss(up) - loss(down)) / (2 * h) - d[t, e]) < 1e-8
+
+
+# ---- sizes
+def test_sizes(lib):
+    assert lib.experts_rows(0, 8, 2, 128) == 0
+    assert lib.experts_rows(1, 8, 2, 128) == 2 + 2 * 127
+    assert lib.experts_rows(100, 8, 2, 128) == 200 + 8 * 127
+    assert lib.experts_rows(100, 8, 2, 1) == 200
+    assert lib.experts_rows(-1, 8, 2, 1) == 0
+    assert lib.experts_rows(100, 8, 9, 1) == 0
+    assert lib.experts_rows(100, 8, 2, 0) == 0
+    assert lib.experts_route_workspace_size(1, 8, 2) > 0
+    assert lib.experts_route_workspace_size(1, 2000, 2) == 0
+
+
+# ---- refusals: addresses that are never followed
+A, SA, B, SB, C, X, OFF = (i << 32 for i in range(1, 8))
+
+
+def block_call(lib, **k):
+    d = dict(M=64, N=96, K=200, alpha=1.0, A=A, lda=208, format_a=0, scale_a=SA, ldsa=64, block_a=1, B=B, ldb=208,
+             format_b=0, scale_b=SB, ldsb=1, block_b=128, beta=0.0, C=C, ldc=96, order_c=0, type_c=1)
+    d.update(k)
+    return lib.gemm_f8_block(**d, raise_on_error=False)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(M=-1), dict(N=-1), dict(K=-1), dict(batch=-1), dict(A=0), dict(B=0), dict(scale_a=0), dict(scale_b=0), dict(C=0),
+    dict(A=A + 8), dict(B=B + 1), dict(scale_a=SA + 2), dict(scale_b=SB + 1), dict(C=C + 1), dict(lda=192), dict(lda=201),
+    dict(ldb=0), dict(ldb=215), dict(ldsa=63), dict(ldsb=0), dict(block_a=2), dict(block_b=64), dict(block_b=1),
+    dict(format_a=2), dict(format_b=-1), dict(type_c=3), dict(order_c=2), dict(ldc=95), dict(order_c=1, ldc=63),
+    dict(C=A + 64), dict(C=SB), dict(batch=2, stride_c=10), dict(batch=2, stride_a=8, stride_c=64 * 96),
+    dict(stride_b=-16), dict(batch=1 << 62), dict(M=1 << 50), dict(lda=1 << 60),
+    dict(batch=2, stride_a=1 << 62, stride_c=64 * 96),
+])
+def test_block_product_refuses(lib, bad):
+    assert block_call(lib, **bad) == lib.ERR_INVALID_ARG
+    names = dict(M=64, N=96, K=200, alpha=1.0, A=A, lda=208, format_a=0, scale_a=SA, ldsa=64, block_a=1, B=B, ldb=208,
+                 format_b=0, scale_b=SB, ldsb=1, block_b=128, beta=0.0, C=C, ldc=96, order_c=0, type_c=1)
+    names.update(bad)
+    assert lib.f8_block_kernel_name(**names) is None
+
+
+def test_block_product_empty_and_unsupported(lib):
+    for empty in (dict(M=0), dict(N=0), dict(batch=0)):
+        assert block_call(lib, **empty, A=0, C=0) == lib.OK
+    assert block_call(lib, lda=1 << 22) == lib.ERR_UNSUPPORTED
+    with pytest.raises(lib.GemmError):
+        lib.gemm_f8_block(-1, 1, 1, 1.0, A, 16, 0, SA, 1, 1, B, 16, 0, SB, 1, 1, 0.0, C, 1, 0, 0)
+
+
+def experts_call(lib, **k):
+    d = dict(experts=4, rows=64, N=96, K=200, offsets=OFF, alpha=1.0, A=A, lda=208, format_a=0, scale_a=SA, ldsa=64, B=B,
+             ldb=208, format_b=1, scale_b=SB, ldsb=1, block_b=128, stride_b=96 * 208, stride_scale_b=2, beta=0.0, C=C, ldc=96,
+             type_c=1)
+    d.update(k)
+    return lib.gemm_experts_f8(**d, raise_on_error=False)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(experts=-1), dict(rows=-1), dict(N=-1), dict(K=-2), dict(offsets=0), dict(offsets=OFF + 2), dict(offsets=C), dict(A=0),
+    dict(B=0), dict(C=0), dict(scale_a=0), dict(scale_b=0), dict(ldsa=10), dict(lda=200), dict(ldb=192), dict(stride_b=8),
+    dict(stride_b=-16), dict(stride_scale_b=-1), dict(block_b=32), dict(ldc=90), dict(type_c=-1), dict(rows=1 << 31),
+    dict(C=B + 100),
+])
+def test_experts_product_refuses(lib, bad):
+    assert experts_call(lib, **bad) == lib.ERR_INVALID_ARG
+
+
+def wgrad_call(lib, **k):
+    d = dict(experts=4, M=64, N=96, rows=384, offsets=OFF, alpha=1.0, A=A, lda=384, format_a=1, scale_a=SA, ldsa=64, B=B,
+             ldb=384, format_b=0, scale_b=SB, ldsb=96, beta=1.0, C=C, ldc=96, stride_c=64 * 96, type_c=0)
+    d.update(k)
+    return lib.gemm_experts_f8_wgrad(**d, raise_on_error=False)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(experts=-1), dict(M=-1), dict(N=-1), dict(rows=-1), dict(offsets=0), dict(A=0), dict(B=0), dict(C=0), dict(C=C + 2),
+    dict(lda=368), dict(ldsa=63), dict(ldsb=95), dict(ldc=95), dict(stride_c=100), dict(rows=1 << 31), dict(format_b=7),
+    dict(C=SB + 4),
+])
+def test_experts_wgrad_refuses(lib, bad):
+    assert wgrad_call(lib, **bad) == lib.ERR_INVALID_ARG
+
+
+def test_experts_empty(lib):
+    assert experts_call(lib, experts=0, offsets=0) == lib.OK
+    assert experts_call(lib, rows=0, A=0) == lib.OK
+    assert wgrad_call(lib, experts=0, offsets=0) == lib.OK
+    assert wgrad_call(lib, M=0, C=0) == lib.OK
+
+
+Q, S, QT, ST = (i << 32 for i in range(10, 14))
+
+
+def quantize_call(lib, **k):
+    d = dict(rows=100, cols=300, X=X, ldx=300, in_type=1, index=0, x_rows=0, format=0, block=1, Q=Q, ldq=304, S=S, lds=100,
+             QT=QT, ldqt=112, ST=ST, ldst=300)
+    d.update(k)
+    return lib.gemm_f8_block_quantize(**d, raise_on_error=False)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(rows=-1), dict(cols=-1), dict(batch=-1), dict(X=0), dict(X=X + 1), dict(ldx=299), dict(in_type=3), dict(format=2),
+    dict(block=0), dict(block=64), dict(Q=0), dict(S=0), dict(QT=0), dict(ST=0), dict(Q=0, S=0, QT=0, ST=0), dict(ldq=299),
+    dict(lds=99), dict(ldqt=99), dict(ldst=299), dict(S=S + 1), dict(ST=ST + 2), dict(index=OFF, x_rows=-1),
+    dict(index=OFF + 1, x_rows=10), dict(index=OFF, x_rows=10, batch=2), dict(QT=Q + 5), dict(S=X + 4), dict(Q=X),
+    dict(index=OFF, x_rows=10, ST=OFF), dict(batch=2, stride_x=30000, stride_q=1), dict(rows=1 << 60),
+    dict(batch=2, stride_x=-1), dict(ldq=1 << 62),
+])
+def test_quantize_refuses(lib, bad):
+    assert quantize_call(lib, **bad) == lib.ERR_INVALID_ARG
+
+
+def test_quantize_empty(lib):
+    for empty in (dict(rows=0), dict(cols=0), dict(batch=0)):
+        assert quantize_call(lib, **empty, X=0) == lib.OK
+
+
+IDS, WEIGHTS, TOKENS, PLACES, WS, BIAS, KEEP = (i << 32 for i in range(20, 27))
+
+
+def route_call(lib, **k):
+    d = dict(tokens=100, experts=64, logits=X, ldl=64, in_type=0, bias=BIAS, keep=KEEP, score=1, groups=8, top_groups=4,
+             group_top=2, top_k=6, renormalise=True, scale=1.0, ids=IDS, weights=WEIGHTS, align=128, rows=100 * 6 + 64 * 127,
+             offsets=OFF, row_tokens=TOKENS, places=PLACES, workspace=WS, workspace_bytes=1 << 20)
+    d.update(k)
+    return lib.gemm_experts_route(**d, raise_on_error=False)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(tokens=-1), dict(experts=0), dict(top_k=0), dict(top_k=65), dict(groups=0), dict(groups=5), dict(top_groups=0),
+    dict(top_groups=9), dict(group_top=0), dict(group_top=3), dict(top_groups=1, top_k=9), dict(ldl=63), dict(in_type=3),
+    dict(score=2), dict(logits=0), dict(ids=0), dict(weights=0), dict(logits=X + 2), dict(bias=BIAS + 1), dict(ids=IDS + 2),
+    dict(weights=WEIGHTS + 1), dict(align=0), dict(align=65537), dict(rows=100 * 6 + 64 * 127 - 1), dict(offsets=0),
+    dict(row_tokens=0), dict(places=0), dict(workspace=0), dict(workspace_bytes=100), dict(workspace=WS + 8), dict(ids=X),
+    dict(weights=IDS + 4), dict(places=TOKENS), dict(workspace=OFF), dict(offsets=BIAS), dict(rows=1 << 31),
+])
+def test_route_refuses(lib, bad):
+    assert route_call(lib, **bad) == lib.ERR_INVALID_ARG
+
+
+def test_route_unsupported_and_empty(lib):
+    assert route_call(lib, experts=2048, ldl=2048, groups=1) == lib.ERR_UNSUPPORTED
+    assert route_call(lib, groups=1, top_k=33) == lib.ERR_UNSUPPORTED
+    assert route_call(lib, experts=128, ldl=128, groups=128, top_groups=32) == lib.ERR_UNSUPPORTED
+    assert route_call(lib, tokens=0, offsets=0, row_tokens=0, places=0, logits=0, ids=0, weights=0) == lib.OK
+
+
+@pytest.mark.parametrize("bad", [
+    dict(tokens=-1), dict(experts=0), dict(top_k=0), dict(top_k=65), dict(ldl=63), dict(ldd=63), dict(in_type=5), dict(score=-1),
+    dict(logits=0), dict(ids=0), dict(d_weights=0), dict(d_logits=0), dict(d_logits=X), dict(d_logits=IDS), dict(ids=IDS + 1),
+    dict(d_logits=C + 2),
+])
+def test_route_backward_refuses(lib, bad):
+    d = dict(tokens=100, experts=64, logits=X, ldl=64, in_type=0, score=0, top_k=6, renormalise=False, scale=1.0, ids=IDS,
+             d_weights=WEIGHTS, d_logits=C, ldd=64)
+    assert lib.gemm_experts_route_backward(**{**d, **bad}, raise_on_error=False) == lib.ERR_INVALID_ARG
+    assert lib.gemm_experts_route_backward(**{**d, "tokens": 0, "ids": 0}, raise_on_error=False) == lib.OK
