@@ -24,7 +24,7 @@ namespace libgemm {
 // The tile kernel for formats FA, FB (0 E4M3, 1 E5M2), defined in the part of
 // those formats.
 template <int FA, int FB>
-hipError_t block_tile_formats(const BlockProblem &p, hipStream_t stream);
+hipError_t block_tile_formats(BlockKernel k, const BlockProblem &p, hipStream_t stream);
 
 namespace {
 
@@ -37,6 +37,7 @@ using dma::wait_vmcnt;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x4_ea __attribute__((ext_vector_type(4), aligned(2)));
 
 constexpr int UNIT = 0x7F7F7F7F;  // E8M0 2^0 in every byte
 
@@ -45,9 +46,12 @@ struct BlockArgs {
     TileGrid grid;
 };
 
-// 16-byte chunk c of a panel's 128-byte row r sits at c ^ swz(r): the 16 rows
-// one fragment read touches at one chunk fall in distinct banks.
-__device__ inline int swz(int row) { return (row ^ (row >> 3)) & 7; }
+// 16-byte chunk c of a panel's 128-byte row r sits at c ^ swz(r).  The 16 rows
+// one fragment read touches at one chunk differ in (r % 2, swz(r)): they fall
+// in distinct 16-byte groups of the 256 bytes the banks span.  It does not
+// change from one 16-row block to the next, so a lane's address is the same
+// for all blocks but for a constant.
+__device__ inline int swz(int row) { return (row >> 1) & 7; }
 
 // ROWS rows of an operand, 128 k deep, in LDS: direct loads of 1 KiB (8 rows)
 // fill it.
@@ -57,9 +61,13 @@ struct Panel {
     static constexpr int PER_WAVE = ROWS / 8 / WAVES;
     static_assert(PER_WAVE >= 1 && ROWS % (8 * WAVES) == 0, "panel split over waves");
     uint32_t voff[PER_WAVE];
-    int k[PER_WAVE];  // this lane's first k within a stage
     int64_t base;
     int64_t bytes;
+
+    // This lane's first k, within a stage, in load i.
+    __device__ static int lane_k(int i, int wave, int lane) {
+        return ((lane & 7) ^ swz((wave * PER_WAVE + i) * 8 + (lane >> 3))) * 16;
+    }
 
     // Rows r0 .. r0 + nrows - 1 (nrows <= ROWS valid) from byte k0 of each row on, K of them.
     __device__ void init(const uint8_t *x, int64_t ld, int64_t r0, int64_t nrows, int64_t k0,
@@ -69,33 +77,36 @@ struct Panel {
 #pragma unroll
         for (int i = 0; i < PER_WAVE; ++i) {
             const int row = (wave * PER_WAVE + i) * 8 + (lane >> 3);
-            const int c = (lane & 7) ^ swz(row);
-            k[i] = c * 16;
-            voff[i] = row < nrows ? uint32_t(row * ld + c * 16) : OOB;
+            voff[i] = row < nrows ? uint32_t(row * ld + lane_k(i, wave, lane)) : OOB;
         }
     }
 
-    // All of this wave's loads for the stage at k = 128*stage, kleft = K - 128*stage > 0.
-    __device__ void issue(LDS char *dst, int64_t stage, int64_t kleft, int wave) const {
+    // All of this wave's loads for the stage at k = 128*stage, kleft = K - 128*stage > 0;
+    // what lies past K reads as zero but for the rest of K's last chunk.
+    __device__ void issue(uint32_t at, int64_t stage, int64_t kleft, int wave, int lane) const {
         const u32x4 rs = dma::raw_buffer(static_cast<uint64_t>(base + 128 * stage),
                                          static_cast<uint32_t>(bytes - 128 * stage));
-        const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(dst));
 #pragma unroll
-        for (int i = 0; i < PER_WAVE; ++i)
-            direct_load16(rs, at + (wave * PER_WAVE + i) * 1024, k[i] < kleft ? voff[i] : OOB);
-    }
-
-    // The lane's 32 bytes of row row0 + lane % 16: chunks lane/16 and 4 + lane/16.  Both
-    // operands take the same k in the same place, so which k that is does not matter.
-    __device__ static i32x8 frag(const LDS char *panel, int row0, int lane) {
-        const int row = row0 + (lane & 15), c = lane >> 4;
-        const LDS char *r = panel + row * 128;
-        const u32x4 lo = *reinterpret_cast<const LDS u32x4 *>(r + ((c ^ swz(row)) << 4));
-        const u32x4 hi = *reinterpret_cast<const LDS u32x4 *>(r + (((c + 4) ^ swz(row)) << 4));
-        return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]),
-                     int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
+        for (int i = 0; i < PER_WAVE; ++i) {
+            uint32_t v = voff[i];
+            if (kleft < 128) v = lane_k(i, wave, lane) < int(kleft) ? v : OOB;
+            direct_load16(rs, at + (wave * PER_WAVE + i) * 1024, v);
+        }
     }
 };
+
+// The lane's 32 bytes of row row0 + lane % 16 (row0 a multiple of 16): chunks
+// lane/16 and 4 + lane/16.  Both operands take the same k in the same place,
+// so which k that is does not matter.  `at` is lane_chunk(lane).
+__device__ inline int lane_chunk(int lane) {
+    return (lane & 15) * 128 + (((lane >> 4) ^ swz(lane & 15)) << 4);
+}
+__device__ inline i32x8 frag(const LDS char *panel, int row0, int at) {
+    const u32x4 lo = *reinterpret_cast<const LDS u32x4 *>(panel + row0 * 128 + at);
+    const u32x4 hi = *reinterpret_cast<const LDS u32x4 *>(panel + row0 * 128 + (at ^ 64));
+    return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]),
+                 int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
+}
 
 // Segment `e` of the offsets, cut to [0, limit).
 __device__ inline void segment_of(const int32_t *offsets, int64_t e, int64_t limit, int64_t &lo,
@@ -136,35 +147,72 @@ __device__ inline bool find_segment(const BlockProblem &p, int64_t tm, int BM, i
     return false;
 }
 
+// Four consecutive columns of a row of C at element `at`, the first `n` of
+// them inside C (n >= 4: all).
 template <int OUT>
-__device__ inline void store_one(const BlockProblem &p, int64_t at, float v) {
+__device__ inline void store_four(const BlockProblem &p, int64_t at, f32x4 v, int64_t n) {
+    auto old = [](uint16_t b) {
+        return OUT == 1 ? __builtin_bit_cast(float, uint32_t(b) << 16)
+                        : static_cast<float>(__builtin_bit_cast(_Float16, b));
+    };
+    auto bits = [](float x) {
+        return OUT == 1 ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(x))
+                        : __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+    };
     if (OUT == 0) {
         float *c = static_cast<float *>(p.C) + at;
-        *c = p.beta != 0.0f ? __builtin_fmaf(p.beta, *c, v) : v;
+        if (n >= 4) {
+            if (p.beta != 0.0f) {
+                const f32x4 o = *reinterpret_cast<const dmatile::f32x4_ea *>(c);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(p.beta, o[r], v[r]);
+            }
+            *reinterpret_cast<dmatile::f32x4_ea *>(c) = v;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r < n) c[r] = p.beta != 0.0f ? __builtin_fmaf(p.beta, c[r], v[r]) : v[r];
+        }
     } else {
         uint16_t *c = static_cast<uint16_t *>(p.C) + at;
-        if (p.beta != 0.0f) {
-            const float old = OUT == 1 ? __builtin_bit_cast(float, uint32_t(*c) << 16)
-                                       : static_cast<float>(__builtin_bit_cast(_Float16, *c));
-            v = __builtin_fmaf(p.beta, old, v);
+        if (n >= 4) {
+            if (p.beta != 0.0f) {
+                const u16x4_ea o = *reinterpret_cast<const u16x4_ea *>(c);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(p.beta, old(o[r]), v[r]);
+            }
+            *reinterpret_cast<u16x4_ea *>(c) = u16x4_ea{bits(v[0]), bits(v[1]), bits(v[2]), bits(v[3])};
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (r < n) c[r] = bits(p.beta != 0.0f ? __builtin_fmaf(p.beta, old(c[r]), v[r]) : v[r]);
         }
-        *c = OUT == 1 ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(v))
-                      : __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
     }
 }
 
 // One workgroup per BM x BN tile, WAVES_M x WAVES_N waves of FM x FN blocks.
+//
+// Two LDS stages of 128 k, filled by direct loads.  B's fragments stay in
+// registers for a stage, A's rotate through two; the last row's instructions
+// run after the barrier that ends a stage, while the next stage's first
+// fragments are read, and the freed stage is refilled there.  A block's sum
+// is added to its accumulators LAG instructions after it was started, so that
+// neither pipe waits for the other.
 template <int FA, int FB, bool PER_COLUMN, int WAVES_M, int WAVES_N, int FM, int FN>
 __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(BlockArgs a) {
     constexpr int WAVES = WAVES_M * WAVES_N;
     constexpr int WTM = FM * 16, WTN = FN * 16, BM = WAVES_M * WTM, BN = WAVES_N * WTN;
     static_assert(128 % WTN == 0, "a wave's columns lie in one block of 128");
+    static_assert(FM % 2 == 0, "A's fragments alternate between two slots");
     using PA = Panel<BM, WAVES>;
     using PB = Panel<BN, WAVES>;
-    __shared__ __attribute__((aligned(1024))) char smem[PA::BYTES + PB::BYTES + (BM + BN) * 4];
+    constexpr int AT_B = PA::BYTES, AT_S = AT_B + PB::BYTES;  // within a stage
+    constexpr int STAGE = AT_S + (BM + BN) * 4;
+    constexpr int SLOADS = (BM + BN) / 64;  // scale loads of 64 rows, one per wave or less
+    static_assert(SLOADS <= WAVES, "at most one scale load per wave");
+    constexpr int LAG = 3;
+    __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
     LDS char *lds = (LDS char *)smem;
-    LDS char *lds_b = lds + PA::BYTES;
-    LDS float *sc = reinterpret_cast<LDS float *>(lds_b + PB::BYTES);
     const BlockProblem &p = a.p;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -179,7 +227,7 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
         k_lo = uniform(k_lo) & ~int64_t(127);
         k_hi = uniform(k_hi);
     }
-    const int64_t K = k_hi - k_lo, kb0 = k_lo / 128;
+    const int64_t K = k_hi - k_lo;
     const int64_t ea = p.segments == Segments::None ? e : 0;
     const int64_t eb = p.segments == Segments::Contracted ? 0 : e;
     const int64_t ec = p.segments == Segments::Rows ? 0 : e;
@@ -190,64 +238,151 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
     pa.init(p.a.x + ea * p.a.stride, p.a.ld, m0, mrows, k_lo, K, wave, lane);
     pb.init(p.b.x + eb * p.b.stride, p.b.ld, n0, nrows, k_lo, K, wave, lane);
 
+    // Scales: wave w loads those of 64 panel rows (A's first, then B's), one
+    // per lane; panel row r of the tile has the scale (r0 + r) >> shift of its
+    // operand's row of scales.
+    const bool s_on_a = wave < BM / 64;
+    const int s_row = (s_on_a ? wave : wave - BM / 64) * 64 + lane;
+    const int s_shift = s_on_a ? p.a.shift : p.b.shift;
+    const int64_t s_r0 = s_on_a ? m0 : n0, s_rows = s_on_a ? mrows : nrows;
+    const int64_t s_first = s_r0 >> s_shift;
+    const uint32_t s_voff =
+        s_row < s_rows ? uint32_t((((s_r0 + s_row) >> s_shift) - s_first) * 4) : OOB;
+    const int64_t s_ld = (s_on_a ? p.a.lds : p.b.lds) * 4;
+    const int64_t s_base = uniform(
+        reinterpret_cast<int64_t>((s_on_a ? p.a.s + ea * p.a.sstride : p.b.s + eb * p.b.sstride) + s_first) +
+        (k_lo >> 7) * s_ld);
+    const uint32_t s_bytes =
+        uint32_t(uniform((((s_r0 + s_rows - 1) >> s_shift) - s_first + 1) * 4));
+
+    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+    const int64_t steps = (K + 127) / 128;
+    auto issue = [&](int64_t s, int buf) {
+        const uint32_t at = lds0 + buf * STAGE;
+        const int64_t kleft = K - 128 * s;
+        pa.issue(at, s, kleft, wave, lane);
+        pb.issue(at + AT_B, s, kleft, wave, lane);
+        if (SLOADS == WAVES || wave < SLOADS)
+            direct_load4(dma::raw_buffer(static_cast<uint64_t>(s_base + s * s_ld), s_bytes),
+                         at + AT_S + wave * 256, s_voff);
+    };
+    // The chunk that holds the end of K, in the stage of buffer buf: its bytes
+    // from K on are not the operand's.
+    auto clear_tail = [&](int buf) {
+        const int kleft = int(K & 127), c = kleft >> 4;
+        for (int r = tid; r < BM + BN; r += WAVES * 64) {
+            const int rr = r < BM ? r : r - BM;
+            LDS char *chunk = lds + buf * STAGE + r * 128 + ((c ^ swz(rr)) << 4);
+            for (int b = kleft & 15; b < 16; ++b) chunk[b] = 0;
+        }
+        __syncthreads();
+    };
+
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    const int64_t steps = (K + 127) / 128;
-    for (int64_t s = 0; s < steps; ++s) {
-        const int64_t kleft = K - 128 * s;
-        pa.issue(lds, s, kleft, wave);
-        pb.issue(lds_b, s, kleft, wave);
-        // the scales of the panel rows: row m0 + i of A, n0 + i of B
-        for (int i = tid; i < BM + BN; i += WAVES * 64) {
-            const bool on_a = i < BM;
-            const BlockOperand &o = on_a ? p.a : p.b;
-            const int r = on_a ? i : i - BM;
-            const float *src = o.s + (on_a ? ea : eb) * o.sstride + (kb0 + s) * o.lds;
-            sc[i] = r < (on_a ? mrows : nrows) ? src[((on_a ? m0 : n0) + r) >> o.shift] : 0.0f;
+    const int at = lane_chunk(lane);
+    i32x8 fb[FN], fa[2];
+    f32x4 part[LAG + 1];
+    float sa[FM];
+    f32x4 sb[PER_COLUMN ? FN : 1];  // one factor, in [0][0], when the columns share a scale
+    auto read_a = [&](int buf, int i) {
+        fa[i & 1] = frag(lds + buf * STAGE, wm * WTM + i * 16, at);
+    };
+    auto read_b = [&](int buf, int j) {
+        fb[j] = frag(lds + buf * STAGE + AT_B, wn * WTN + j * 16, at);
+    };
+    auto read_scales = [&](int buf) {
+        const LDS float *s = reinterpret_cast<const LDS float *>(lds + buf * STAGE + AT_S);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sa[i] = s[wm * WTM + i * 16 + (lane & 15)];
+        if (PER_COLUMN) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                sb[j] = *reinterpret_cast<const LDS f32x4 *>(s + BM + wn * WTN + j * 16 + 4 * (lane >> 4));
+        } else {
+            const float f = s[BM + wn * WTN];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sa[i] *= f;
         }
+    };
+    auto start = [&](int n) {
+        part[n % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            fb[n % FN], fa[(n / FN) & 1], f32x4{0.0f, 0.0f, 0.0f, 0.0f}, FB, FA, 0, UNIT, 0, UNIT);
+    };
+    // The empty statement takes the sums as operands: without it the compiler
+    // moves a whole stage's instructions past the barrier, to where its sums
+    // are next read, and keeps every fragment of the stage until there.
+    auto add = [&](int n) {
+        const int i = n / FN, j = n % FN;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float f = PER_COLUMN ? sa[i] * sb[PER_COLUMN ? j : 0][r] : sa[i];
+            acc[i][j][r] = __builtin_fmaf(part[n % (LAG + 1)][r], f, acc[i][j][r]);
+        }
+        asm volatile("" : "+v"(acc[i][j]));
+    };
+    // Rows 0 .. FM - 2 of the stage in buffer buf.
+    auto rows = [&](int buf) {
+        read_scales(buf);
+#pragma unroll
+        for (int n = 0; n < (FM - 1) * FN; ++n) {
+            if (n % FN == 0) read_a(buf, n / FN + 1);
+            start(n);
+            if (n >= LAG) add(n - LAG);
+            if (n % FN == FN - 1) __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto finish = [&]() {
+#pragma unroll
+        for (int n = FM * FN - LAG; n < FM * FN; ++n) add(n);
+    };
+
+    if (steps > 0) {
+        issue(0, 0);
+        if (steps > 1) {
+            issue(1, 1);
+            constexpr int PER_STAGE = PA::PER_WAVE + PB::PER_WAVE;  // and a scale load, on some waves
+            if (SLOADS == WAVES || wave < SLOADS) wait_vmcnt<PER_STAGE + 1>();
+            else wait_vmcnt<PER_STAGE>();
+        } else {
+            wait_vmcnt<0>();
+        }
+        __syncthreads();
+        if (steps == 1 && (K & 15) != 0) clear_tail(0);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) read_b(0, j);
+        read_a(0, 0);
+    }
+    int buf = 0;
+    for (int64_t s = 0; s + 1 < steps; ++s) {
+        rows(buf);
         wait_vmcnt<0>();
+        dma::wait_lgkmcnt0();
         __syncthreads();
-        if (kleft < 128 && (K & 15) != 0) {
-            // the chunk that holds the end of K: its bytes from there on are not the operand's
-            const int c = int(kleft >> 4), from = int(kleft & 15);
-            for (int r = tid; r < BM + BN; r += WAVES * 64) {
-                LDS char *row = r < BM ? lds + r * 128 : lds_b + (r - BM) * 128;
-                const int rr = r < BM ? r : r - BM;
-                for (int b = from; b < 16; ++b) row[((c ^ swz(rr)) << 4) + b] = 0;
-            }
-            __syncthreads();
+        if (s + 2 == steps && (K & 15) != 0) clear_tail(buf ^ 1);
+        read_a(buf ^ 1, 0);
+        if (s + 2 < steps) issue(s + 2, buf);
+#pragma unroll
+        for (int n = (FM - 1) * FN; n < FM * FN; ++n) {
+            start(n);
+            read_b(buf ^ 1, n % FN);
+            add(n - LAG);
         }
-        i32x8 fb[FN];
-        f32x4 sb[FN];
+        finish();
+        buf ^= 1;
+    }
+    if (steps > 0) {
+        rows(buf);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            fb[j] = PB::frag(lds_b, wn * WTN + j * 16, lane);
-            sb[j] = *reinterpret_cast<const LDS f32x4 *>(sc + BM + wn * WTN + j * 16 + 4 * (lane >> 4));
+        for (int n = (FM - 1) * FN; n < FM * FN; ++n) {
+            start(n);
+            add(n - LAG);
         }
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const i32x8 fa = PA::frag(lds, wm * WTM + i * 16, lane);
-            const float sa = sc[wm * WTM + i * 16 + (lane & 15)];
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    fb[j], fa, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, FB, FA, 0, UNIT, 0, UNIT);
-                if (PER_COLUMN) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][j][r] = __builtin_fmaf(part[r], sa * sb[j][r], acc[i][j][r]);
-                } else {
-                    const float f = sa * sb[0][0];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(part[r], f, acc[i][j][r]);
-                }
-            }
-        }
-        __syncthreads();
+        finish();
     }
 
 #pragma unroll
@@ -255,23 +390,21 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
         const int64_t m = m0 + wm * WTM + i * 16 + (lane & 15);
         if (m >= m_end) continue;
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t n = n0 + wn * WTN + j * 16 + 4 * (lane >> 4) + r;
-                if (n >= p.N) continue;
-                const int64_t at = ec * p.sC + m * p.ldc + n;
-                const float v = p.alpha * acc[i][j][r];
-                if (p.out == 0) store_one<0>(p, at, v);
-                else if (p.out == 1) store_one<1>(p, at, v);
-                else store_one<2>(p, at, v);
-            }
+        for (int j = 0; j < FN; ++j) {
+            const int64_t n = n0 + wn * WTN + j * 16 + 4 * (lane >> 4);
+            if (n >= p.N) continue;
+            const int64_t c = ec * p.sC + m * p.ldc + n;
+            const f32x4 v = p.alpha * acc[i][j];
+            if (p.out == 0) store_four<0>(p, c, v, p.N - n);
+            else if (p.out == 1) store_four<1>(p, c, v, p.N - n);
+            else store_four<2>(p, c, v, p.N - n);
+        }
     }
 }
 
-template <int FA, int FB, bool PER_COLUMN>
+template <int FA, int FB, bool PER_COLUMN, int WM, int WN, int FM, int FN>
 hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
-    constexpr int WM = 2, WN = 2, FM = 4, FN = 4, BM = WM * FM * 16, BN = WN * FN * 16;
+    constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
     BlockArgs a{};
     a.p = p;
     int64_t tiles_m = (p.M + BM - 1) / BM;
@@ -287,13 +420,20 @@ hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
         dim3(static_cast<unsigned>(a.grid.count())), dim3(WM * WN * 64), args, 0, stream);
 }
 
+template <int FA, int FB, bool PER_COLUMN>
+hipError_t tile_size(BlockKernel k, const BlockProblem &p, hipStream_t stream) {
+    if (k == BlockKernel::Tile256) return tile_go<FA, FB, PER_COLUMN, 2, 4, 8, 4>(p, stream);
+    return tile_go<FA, FB, PER_COLUMN, 2, 2, 4, 4>(p, stream);
+}
+
 }  // namespace
 
 #define LIBGEMM_BLOCK_FORMATS(part, FA, FB)                                               \
     template <>                                                                           \
-    hipError_t block_tile_formats<FA, FB>(const BlockProblem &p, hipStream_t stream) {    \
-        return p.b.shift == 0 ? tile_go<FA, FB, true>(p, stream)                          \
-                              : tile_go<FA, FB, false>(p, stream);                        \
+    hipError_t block_tile_formats<FA, FB>(BlockKernel k, const BlockProblem &p,           \
+                                          hipStream_t stream) {                           \
+        return p.b.shift == 0 ? tile_size<FA, FB, true>(k, p, stream)                     \
+                              : tile_size<FA, FB, false>(k, p, stream);                   \
     }
 #if LIBGEMM_BLOCK_HAS(0)
 LIBGEMM_BLOCK_FORMATS(0, 0, 0)
@@ -312,21 +452,23 @@ LIBGEMM_BLOCK_FORMATS(3, 1, 1)
 BlockKernel block_choose(const BlockProblem &p, bool tiles_only) {
     (void)tiles_only;
     if (p.M == 0 || p.N == 0 || p.batch == 0) return BlockKernel::None;
-    return BlockKernel::Tile;
+    const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256) * (p.segments == Segments::Rows ? 1 : p.batch);
+    return tiles >= 192 ? BlockKernel::Tile256 : BlockKernel::Tile128;
 }
 
 const char *block_kernel_name(BlockKernel k) {
     switch (k) {
     case BlockKernel::None: return "";
-    case BlockKernel::Tile: return "f8block_mfma";
+    case BlockKernel::Tile256: return "f8block_mfma_256";
+    case BlockKernel::Tile128: return "f8block_mfma_128";
     }
     return "";
 }
 
 hipError_t launch_block(BlockKernel k, const BlockProblem &p, hipStream_t stream) {
     if (k == BlockKernel::None) return hipSuccess;
-    if (p.a.e5m2) return p.b.e5m2 ? block_tile_formats<1, 1>(p, stream) : block_tile_formats<1, 0>(p, stream);
-    return p.b.e5m2 ? block_tile_formats<0, 1>(p, stream) : block_tile_formats<0, 0>(p, stream);
+    if (p.a.e5m2) return p.b.e5m2 ? block_tile_formats<1, 1>(k, p, stream) : block_tile_formats<1, 0>(k, p, stream);
+    return p.b.e5m2 ? block_tile_formats<0, 1>(k, p, stream) : block_tile_formats<0, 0>(k, p, stream);
 }
 #endif
 
