@@ -1,11 +1,21 @@
 // Routing tokens to experts: scores, the choice, the weights, and the rows of
 // each expert; and the weights' gradient.
 //
-// One wave chooses for one token, lane l holding experts l, l + 64, ...: the
-// largest key is found top_k times over the wave.  A workgroup's 64 tokens
-// leave one 64-bit mask per expert (bit t: token t of the block chose it), in
-// which a token's rank among the block's is a count of bits; a second kernel
-// adds what earlier blocks hold.  No order of atomics enters a result.
+// The choice.  One wave per token; lane l holds PER consecutive experts from
+// PER*l on, so of equal keys the lowest lane's is the lowest index.  The
+// largest key is found top_k times over the wave with data-parallel moves.
+// Without a bias the logits rank as their scores do and are compared as they
+// are.  With one, keys are computed in fp32, and where two that are compared
+// lie closer than twice their error the token is chosen again in 64 bits:
+// about one token in 500 of 256 experts, and ties.
+//
+// The rows.  A block of 64 tokens leaves one 64-bit mask per expert (bit t:
+// token t of the block chose it), in which a token's rank among the block's
+// is a count of bits; what earlier blocks hold comes from byte counts that the
+// first kernel leaves.  No order of atomics enters a result.
+//
+// Both kernels are bound by latency at the sizes of a decode step and by
+// instruction issue beyond; they read the logits once.
 #include "f8_block.hpp"
 
 #include <cmath>
@@ -13,76 +23,188 @@
 namespace libgemm {
 namespace {
 
-constexpr int WAVES = 4;
+constexpr int BLOCK = ROUTE_BLOCK;
+constexpr int LANES = 64;
+constexpr float NONE = -INFINITY;
 
-__device__ inline float load_logit(const void *x, int64_t at, int type) {
-    if (type == 0) return static_cast<const float *>(x)[at];
-    const uint16_t b = static_cast<const uint16_t *>(x)[at];
+__device__ inline float decode(uint16_t b, int type) {
     return type == 1 ? __builtin_bit_cast(float, uint32_t(b) << 16)
                      : static_cast<float>(__builtin_bit_cast(_Float16, b));
 }
+__device__ inline float load_logit(const void *x, int64_t at, int type) {
+    if (type == 0) return static_cast<const float *>(x)[at];
+    return decode(static_cast<const uint16_t *>(x)[at], type);
+}
+
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x4_t __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+template <int N> struct Vec;
+template <> struct Vec<1> { typedef uint16_t h; typedef float f; };
+template <> struct Vec<2> { typedef u16x2_t h; typedef f32x2_t f; };
+template <> struct Vec<4> { typedef u16x4_t h; typedef f32x4_t f; };
+template <> struct Vec<8> { typedef u16x8_t h; };
+
+// A lane's PER logits from element `at` on, `n` of them there (the others are
+// -infinity).  whole: they may be read in vectors.
+template <int PER>
+__device__ inline void load_logits(const void *x, int64_t at, int type, int n, bool whole, float (&l)[PER]) {
+    if (whole && n >= PER) {
+        if (type == 0) {
+            constexpr int W = PER < 4 ? PER : 4;
+            typedef typename Vec<W>::f V;
+#pragma unroll
+            for (int i = 0; i < PER; i += W) {
+                const V v = *reinterpret_cast<const V *>(static_cast<const float *>(x) + at + i);
+                if constexpr (W == 1) l[i] = v;
+                else
+#pragma unroll
+                    for (int j = 0; j < W; ++j) l[i + j] = v[j];
+            }
+        } else {
+            constexpr int W = PER < 8 ? PER : 8;
+            typedef typename Vec<W>::h V;
+#pragma unroll
+            for (int i = 0; i < PER; i += W) {
+                const V v = *reinterpret_cast<const V *>(static_cast<const uint16_t *>(x) + at + i);
+                if constexpr (W == 1) l[i] = decode(v, type);
+                else
+#pragma unroll
+                    for (int j = 0; j < W; ++j) l[i + j] = decode(v[j], type);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) l[i] = i < n ? load_logit(x, at + i, type) : NONE;
+}
+
+template <int PER>
+__device__ inline void store_logits(void *x, int64_t at, int type, int n, bool whole, const float (&l)[PER]) {
+    auto bits = [&](float v) {
+        return type == 1 ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(v))
+                         : __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+    };
+    if (whole && n >= PER) {
+        if (type == 0) {
+            constexpr int W = PER < 4 ? PER : 4;
+            typedef typename Vec<W>::f V;
+#pragma unroll
+            for (int i = 0; i < PER; i += W) {
+                V v;
+                if constexpr (W == 1) v = l[i];
+                else
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[j] = l[i + j];
+                *reinterpret_cast<V *>(static_cast<float *>(x) + at + i) = v;
+            }
+        } else {
+            constexpr int W = PER < 8 ? PER : 8;
+            typedef typename Vec<W>::h V;
+#pragma unroll
+            for (int i = 0; i < PER; i += W) {
+                V v;
+                if constexpr (W == 1) v = bits(l[i]);
+                else
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[j] = bits(l[i + j]);
+                *reinterpret_cast<V *>(static_cast<uint16_t *>(x) + at + i) = v;
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (i >= n) continue;
+        if (type == 0) static_cast<float *>(x)[at + i] = l[i];
+        else static_cast<uint16_t *>(x)[at + i] = bits(l[i]);
+    }
+}
+
+// x of the lane that a data-parallel move of control CTRL names, `other`
+// where there is none.
+template <int CTRL, int ROWS>
+__device__ inline float moved(float other, float x) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, other), __builtin_bit_cast(int, x),
+                                           CTRL, ROWS, 0xf, false));
+}
+__device__ inline float lane_of(float x, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+// Over the wave, in every lane (row_shr 1, 2, 4, 8, then the rows' last lanes).
+__device__ inline float wave_max(float x) {
+    x = fmaxf(x, moved<0x111, 0xf>(x, x));
+    x = fmaxf(x, moved<0x112, 0xf>(x, x));
+    x = fmaxf(x, moved<0x114, 0xf>(x, x));
+    x = fmaxf(x, moved<0x118, 0xf>(x, x));
+    x = fmaxf(x, moved<0x142, 0xa>(x, x));
+    x = fmaxf(x, moved<0x143, 0xc>(x, x));
+    return lane_of(x, 63);
+}
+__device__ inline float wave_sum(float x) {
+    x += moved<0x111, 0xf>(0.0f, x);
+    x += moved<0x112, 0xf>(0.0f, x);
+    x += moved<0x114, 0xf>(0.0f, x);
+    x += moved<0x118, 0xf>(0.0f, x);
+    x += moved<0x142, 0xa>(0.0f, x);
+    x += moved<0x143, 0xc>(0.0f, x);
+    return lane_of(x, 63);
+}
+
+// e^(a - b) with the rounding of the difference put back.
+__device__ inline float exp_difference(float a, float b) {
+    const float d = a - b, t = d - a;
+    const float rest = (a - (d - t)) - (b + t);
+    const float e = expf(d);
+    return d > -126.0f ? __builtin_fmaf(e, rest, e) : e;  // (a rest of infinities is no number)
+}
+
+// ---- in 64 bits
 
 struct Best {
     double key;
     int at;
 };
+constexpr int NOBODY = 1 << 30;
 // The larger key; of equal ones the lower index.
 __device__ inline Best better(Best a, Best b) {
     return b.key > a.key || (b.key == a.key && b.at < a.at) ? b : a;
 }
 __device__ inline Best wave_best(Best x) {
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x = better(x, Best{__shfl_xor(x.key, d), __shfl_xor(x.at, d)});
-    return x;
-}
-template <typename T>
-__device__ inline T wave_sum(T x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    for (int d = 1; d < LANES; d <<= 1) x = better(x, Best{__shfl_xor(x.key, d), __shfl_xor(x.at, d)});
     return x;
 }
 
-constexpr int NOBODY = 1 << 30;
-
-// PER: experts per lane.
+// Lane j's choice (or -1) of a token whose scores are defined.
 template <int PER>
-__device__ inline void choose(const RouteArgs &a, int64_t t, int lane, unsigned long long *masks, int bit) {
+__device__ int choose_exactly(const RouteArgs &a, const float (&l)[PER], int lane) {
     const double none = -INFINITY;
-    const int E = a.experts;
-    int32_t *ids = a.ids + t * a.top_k;
-    float *weights = a.weights + t * a.top_k;
-    bool live = a.keep == nullptr || a.keep[t] != 0;
-    double l[PER], key[PER];
-    bool odd = false;
-    double top = none;
+    const int E = a.experts, first_e = lane * PER;
+    double key[PER], top = none, sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = e < E && live ? double(load_logit(a.logits, t * a.ldl + e, a.type)) : none;
-        odd = odd || l[i] != l[i] || l[i] == INFINITY;
-        top = l[i] > top ? l[i] : top;
-    }
-    const bool undefined = !a.sigmoid && __ballot(odd) != 0;
-    double sum = 0.0;
+    for (int i = 0; i < PER; ++i) top = double(l[i]) > top ? double(l[i]) : top;
     if (!a.sigmoid) {
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
+        for (int d = 1; d < LANES; d <<= 1) {
             const double o = __shfl_xor(top, d);
             top = o > top ? o : top;
         }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sum += l[i] > none ? exp(l[i] - top) : 0.0;
-        sum = wave_sum(sum);
+        for (int i = 0; i < PER; ++i) sum += l[i] > NONE ? exp(double(l[i]) - top) : 0.0;
+#pragma unroll
+        for (int d = 1; d < LANES; d <<= 1) sum += __shfl_xor(sum, d);
     }
-    auto score = [&](double x) { return a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum; };
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
         key[i] = none;
-        if (e >= E || undefined || !(l[i] > none)) continue;
-        // without a bias or groups the logits rank as their scores do
-        key[i] = a.bias == nullptr && a.groups == 1 ? l[i] : score(l[i]);
-        if (a.bias != nullptr) key[i] += double(a.bias[e]);
+        if (!(l[i] > NONE)) continue;
+        const double x = l[i];
+        key[i] = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum;
+        if (a.bias != nullptr) key[i] += double(a.bias[first_e + i]);
         if (!(key[i] > none)) key[i] = none;
     }
     if (a.groups > 1) {
@@ -91,19 +213,15 @@ __device__ inline void choose(const RouteArgs &a, int64_t t, int lane, unsigned 
         for (int g = 0; g < a.groups; ++g) {
             Best first{none, NOBODY}, second{none, NOBODY};
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = lane + 64 * i;
-                if (e < E && e / per == g && key[i] > none) first = better(first, Best{key[i], e});
-            }
+            for (int i = 0; i < PER; ++i)
+                if ((first_e + i) / per == g && key[i] > none) first = better(first, Best{key[i], first_e + i});
             first = wave_best(first);
             double r = first.key;
             if (a.group_top == 2) {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int e = lane + 64 * i;
-                    if (e < E && e / per == g && e != first.at && key[i] > none)
-                        second = better(second, Best{key[i], e});
-                }
+                for (int i = 0; i < PER; ++i)
+                    if ((first_e + i) / per == g && first_e + i != first.at && key[i] > none)
+                        second = better(second, Best{key[i], first_e + i});
                 second = wave_best(second);
                 if (second.key > none) r += second.key;
             }
@@ -112,167 +230,377 @@ __device__ inline void choose(const RouteArgs &a, int64_t t, int lane, unsigned 
         unsigned long long kept = 0;
         for (int n = 0; n < a.top_groups; ++n) {
             const Best b = wave_best(Best{rank, lane < a.groups && !(kept >> lane & 1) ? lane : NOBODY + lane});
-            // groups with nobody rank -infinity and come last, by index
-            if (b.at < NOBODY) kept |= 1ull << b.at;
+            if (b.at < NOBODY) kept |= 1ull << b.at;  // groups with nobody come last and hold nobody
             if (lane == b.at) rank = none;
         }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = lane + 64 * i;
-            if (e < E && !(kept >> (e / per) & 1)) key[i] = none;
-        }
+        for (int i = 0; i < PER; ++i)
+            if (first_e + i < E && !(kept >> ((first_e + i) / per) & 1)) key[i] = none;
     }
-    double chosen = none;  // lane j's: the logit of choice j
+    if (a.bias == nullptr) {  // the logits rank as their scores do, and do not run together
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = key[i] > none ? double(l[i]) : none;
+    }
     int id = -1;
     for (int j = 0; j < a.top_k; ++j) {
         Best b{none, NOBODY};
-        double logit = none;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (key[i] > none) b = better(b, Best{key[i], lane + 64 * i});
+            if (key[i] > none) b = better(b, Best{key[i], first_e + i});
         b = wave_best(b);
         if (b.at == NOBODY) break;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (lane + 64 * i == b.at) {
-                logit = l[i];
-                key[i] = none;
-            }
-        logit = __shfl(logit, b.at & 63);
-        if (lane == j) {
-            id = b.at;
-            chosen = logit;
-        }
+            if (first_e + i == b.at) key[i] = none;
+        if (lane == j) id = b.at;
     }
-    double w = id >= 0 ? score(chosen) : 0.0;
-    if (a.renormalise) {
-        double first = 0.0;
-        if (!a.sigmoid) {  // relative to the largest chosen: the sum cannot vanish
-            first = id >= 0 ? chosen : none;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const double o = __shfl_xor(first, d);
-                first = o > first ? o : first;
-            }
-            w = id >= 0 ? exp(chosen - first) : 0.0;
-        }
-        const double total = wave_sum(w);
-        w = total > 0.0 ? w / total : 0.0;
-    }
-    w *= double(a.scale);
-    if (id < 0) w = 0.0;
-    if (undefined && live) w = __builtin_nan("");
-    if (lane < a.top_k) {
-        ids[lane] = id;
-        weights[lane] = float(w);
-        if (masks != nullptr && id >= 0) atomicOr(&masks[id], 1ull << bit);
-    }
+    return id;
 }
 
+// ---- in 32 bits
+
+// The rank of group `lane` (its group_top largest keys' sum), -infinity in lanes without one.
 template <int PER>
-__global__ __launch_bounds__(WAVES * 64) void choose_kernel(RouteArgs a) {
-    __shared__ unsigned long long masks[ROUTE_MAX_EXPERTS];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const bool layout = a.masks != nullptr;
-    if (layout) {
-        for (int e = threadIdx.x; e < a.experts; e += WAVES * 64) masks[e] = 0;
+__device__ inline float group_ranks(const RouteArgs &a, const float (&key)[PER], int lane) {
+    const int per = a.experts / a.groups;
+    const int width = per / PER;
+    if (per % PER == 0 && width <= 16 && (width & (width - 1)) == 0) {
+        // a group is `width` lanes, a power of two: its two largest come together in log2 steps
+        float first = NONE, second = NONE;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            second = fmaxf(second, fminf(first, key[i]));
+            first = fmaxf(first, key[i]);
+        }
+        for (int d = 1; d < width; d <<= 1) {
+            const float f = __shfl_xor(first, d), s = __shfl_xor(second, d);
+            second = fmaxf(fmaxf(second, s), fminf(first, f));
+            first = fmaxf(first, f);
+        }
+        if (a.group_top == 2 && second > NONE) first += second;
+        const float r = __shfl(first, lane * width & 63);
+        return lane < a.groups ? r : NONE;
+    }
+    float rank = NONE;
+    for (int g = 0; g < a.groups; ++g) {
+        float first = NONE, second = NONE;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const float k = (lane * PER + i) / per == g ? key[i] : NONE;
+            second = fmaxf(second, fminf(first, k));
+            first = fmaxf(first, k);
+        }
+        const float m = wave_max(first);
+        const int at = __builtin_ctzll(__ballot(first == m));
+        const float s = wave_max(lane == at ? second : first);
+        const float r = a.group_top == 2 && s > NONE ? m + s : m;
+        if (lane == g) rank = r;
+    }
+    return rank;
+}
+
+// Chooses for token t: lane j gets choice j and its weight.
+template <int PER>
+__device__ inline void choose(const RouteArgs &a, int64_t t, int lane, bool whole, int &id, float &w) {
+    const int E = a.experts, first_e = lane * PER;
+    id = -1;
+    w = 0.0f;
+    if (a.keep != nullptr && a.keep[t] == 0) return;
+    float l[PER], key[PER];
+    load_logits<PER>(a.logits, t * a.ldl + first_e, a.type, E - first_e, whole, l);
+    float top = NONE;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        odd = odd || l[i] != l[i] || l[i] == INFINITY;
+        l[i] = l[i] > NONE ? l[i] : NONE;
+        top = fmaxf(top, l[i]);
+    }
+    float sum = 0.0f;
+    if (!a.sigmoid) {
+        if (__ballot(odd) != 0) {
+            w = __builtin_nanf("");
+            return;
+        }
+        top = wave_max(top);
+        if (a.bias != nullptr || !a.renormalise || (a.groups > 1 && a.group_top == 2)) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) sum += l[i] > NONE ? expf(l[i] - top) : 0.0f;
+            sum = wave_sum(sum);
+        }
+    }
+    // The error of a key is below `off` times the largest score plus its own
+    // size: a few roundings, and under softmax the sum's PER + 6.
+    const float off = (a.sigmoid ? 8.0f : PER + 16.0f) * 0x1p-24f;
+    const float largest = a.sigmoid ? 1.0f : 1.0f / sum;
+    const bool exact_keys = a.bias == nullptr;
+    bool near = false;
+    if (exact_keys && !(a.groups > 1 && a.group_top == 2)) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = l[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            key[i] = a.sigmoid ? 1.0f / (1.0f + expf(-l[i])) : expf(l[i] - top) / sum;
+            if (a.bias != nullptr && first_e + i < E) key[i] += a.bias[first_e + i];
+            key[i] = l[i] > NONE && key[i] > NONE ? key[i] : NONE;
+        }
+    }
+    if (a.groups > 1) {
+        const int per = E / a.groups;
+        const float rank = group_ranks<PER>(a, key, lane);
+        const bool exact_ranks = exact_keys && a.group_top == 1;
+        int ahead = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const float r = lane_of(rank, g);
+            ahead += r > rank || (r == rank && g < lane);
+            if (!exact_ranks && g != lane && lane < a.groups && fabsf(r - rank) <= 4.0f * off * (largest + fabsf(r)))
+                near = true;
+        }
+        const unsigned long long kept = __ballot(lane < a.groups && ahead < a.top_groups);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int g = (first_e + i) / per;
+            const bool in = first_e + i < E && (kept >> (g & 63) & 1);
+            key[i] = !in ? NONE : exact_keys ? l[i] : key[i];
+        }
+    }
+    float last = INFINITY;
+    const int rounds = exact_keys || a.top_k == E ? a.top_k : a.top_k + 1;  // one more shows how close the next is
+    for (int j = 0; j < rounds; ++j) {
+        float mine = key[0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) mine = fmaxf(mine, key[i]);
+        const float m = wave_max(mine);
+        if (!(m > NONE)) break;
+        if (!exact_keys && last - m <= 2.0f * off * (largest + fabsf(m))) near = true;
+        last = m;
+        const int owner = __builtin_ctzll(__ballot(mine == m));
+        int at = 0;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) at = key[i] == m ? i : at;
+        const int e = __builtin_amdgcn_readlane(first_e + at, owner);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (first_e + i == e) key[i] = NONE;
+        if (lane == j) id = e;
+    }
+    if (lane >= a.top_k) id = -1;
+    if (__ballot(near) != 0) id = choose_exactly<PER>(a, l, lane);
+
+    const float x = id >= 0 ? load_logit(a.logits, t * a.ldl + id, a.type) : NONE;
+    if (a.sigmoid) {
+        w = id >= 0 ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+    } else {
+        // renormalised: relative to the largest chosen, so the sum cannot vanish
+        if (a.renormalise) top = wave_max(x);
+        w = id >= 0 ? exp_difference(x, top) : 0.0f;
+        if (!a.renormalise) w /= sum;
+    }
+    if (a.renormalise) {
+        const float total = wave_sum(w);
+        w = total > 0.0f ? w / total : 0.0f;
+    }
+    w *= a.scale;
+    if (id < 0) w = 0.0f;
+}
+
+// `span` consecutive tokens per workgroup, its waves taking them in turn.
+// With counts: counts[workgroup][expert], the tokens of the span that chose it.
+template <int PER>
+__global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a, int span, uint8_t *counts) {
+    __shared__ uint32_t count[ROUTE_MAX_EXPERTS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6;
+    if (counts != nullptr) {
+        for (int e = threadIdx.x; e < a.experts; e += blockDim.x) count[e] = 0;
         __syncthreads();
     }
-    for (int i = wave; i < ROUTE_BLOCK; i += WAVES) {
-        const int64_t t = int64_t(blockIdx.x) * ROUTE_BLOCK + i;
-        if (t < a.tokens) choose<PER>(a, t, lane, layout ? masks : nullptr, i);
+    // rows of logits that start where their vectors are aligned
+    const int64_t bytes = int64_t(PER < 4 ? PER : 4) * 4;
+    const bool whole = (reinterpret_cast<uintptr_t>(a.logits) | uint64_t(a.ldl * (a.type == 0 ? 4 : 2))) % bytes == 0;
+    for (int i = wave; i < span; i += waves) {
+        const int64_t t = int64_t(blockIdx.x) * span + i;
+        if (t >= a.tokens) break;
+        int id;
+        float w;
+        choose<PER>(a, t, lane, whole, id, w);
+        if (lane < a.top_k) {
+            a.ids[t * a.top_k + lane] = id;
+            a.weights[t * a.top_k + lane] = w;
+            if (counts != nullptr && id >= 0) atomicAdd(&count[id], 1u);
+        }
     }
-    if (layout) {
+    if (counts != nullptr) {
         __syncthreads();
-        for (int e = threadIdx.x; e < a.experts; e += WAVES * 64)
-            a.masks[int64_t(blockIdx.x) * a.experts + e] = masks[e];
+        for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
+            counts[int64_t(blockIdx.x) * a.experts + e] = uint8_t(count[e]);
     }
 }
 
-// Block b of tokens: where each of its rows goes.
-__global__ __launch_bounds__(256) void place_kernel(RouteArgs a, int64_t blocks) {
-    __shared__ int start[ROUTE_MAX_EXPERTS + 1];   // offsets
-    __shared__ int before[ROUTE_MAX_EXPERTS];      // rows of earlier blocks
-    __shared__ int count[ROUTE_MAX_EXPERTS];
-    const int E = a.experts;
-    const int64_t b = blockIdx.x;
-    for (int e = threadIdx.x; e < E; e += 256) {
-        int all = 0, earlier = 0;
-        for (int64_t o = 0; o < blocks; ++o) {
-            if (o == b) earlier = all;
-            all += __popcll(a.masks[o * E + e]);
+// Workgroup g lays out the 64-token blocks from g*own on, `own` of them.
+// counts: one row of bytes per `span` tokens (a divisor of 64), or null when
+// there is one block, which then counts for itself.
+__global__ __launch_bounds__(1024) void place_kernel(RouteArgs a, int64_t own, int span, const uint8_t *counts) {
+    constexpr int THREADS = 1024;
+    __shared__ unsigned long long mask[ROUTE_MAX_EXPERTS];
+    __shared__ int start[ROUTE_MAX_EXPERTS + 1];  // offsets
+    __shared__ int total[ROUTE_MAX_EXPERTS];
+    __shared__ int next[ROUTE_MAX_EXPERTS];  // rows of earlier blocks
+    __shared__ int wave_total[THREADS / 64];
+    const int E = a.experts, tid = threadIdx.x, lane = tid & 63;
+    const int64_t first_block = int64_t(blockIdx.x) * own;
+    auto fill_masks = [&](int64_t block) {
+        const int64_t t0 = block * BLOCK;
+        const int slots = int((a.tokens - t0 < BLOCK ? a.tokens - t0 : BLOCK) * a.top_k);
+        for (int s = tid; s < slots; s += THREADS) {
+            const int e = a.ids[t0 * a.top_k + s];
+            if (e >= 0) atomicOr(&mask[e], 1ull << (s / a.top_k));
         }
-        count[e] = all;
-        before[e] = earlier;
+    };
+    for (int e = tid; e < E; e += THREADS) {
+        mask[e] = 0;
+        total[e] = next[e] = 0;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        int at = 0;
-        for (int e = 0; e < E; ++e) {
-            start[e] = at;
-            at += (count[e] + a.align - 1) / a.align * a.align;
+    if (counts == nullptr) {
+        fill_masks(0);
+        __syncthreads();
+        for (int e = tid; e < E; e += THREADS) total[e] = __popcll(mask[e]);
+    } else {
+        const int64_t rows = (a.tokens + span - 1) / span, before = first_block * BLOCK / span;
+        const int quads = (E + 3) / 4;
+        if (E % 4 == 0) {  // four experts' bytes at a time; workspace rows start on whole words
+            const int parts = THREADS / quads;
+            const int q = tid % quads, part = tid / quads;
+            if (part < parts) {
+                int sum[4] = {0, 0, 0, 0}, early[4] = {0, 0, 0, 0};
+                for (int64_t r = part; r < rows; r += parts) {
+                    const uint32_t v = reinterpret_cast<const uint32_t *>(counts)[r * quads + q];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = v >> (8 * i) & 255;
+                        sum[i] += c;
+                        early[i] += r < before ? c : 0;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    atomicAdd(&total[4 * q + i], sum[i]);
+                    atomicAdd(&next[4 * q + i], early[i]);
+                }
+            }
+        } else {
+            for (int e = tid; e < E; e += THREADS) {
+                int sum = 0, early = 0;
+                for (int64_t r = 0; r < rows; ++r) {
+                    if (r == before) early = sum;
+                    sum += counts[r * E + e];
+                }
+                total[e] = sum;
+                next[e] = early;
+            }
         }
-        start[E] = at;
     }
     __syncthreads();
-    if (b == 0)
-        for (int e = threadIdx.x; e <= E; e += 256) a.offsets[e] = start[e];
-    // fillings: those of the experts b, b + blocks, ..., and a share of what is behind the last segment
-    for (int64_t e = b; e < E; e += gridDim.x)
-        for (int r = start[e] + count[e] + int(threadIdx.x); r < start[e + 1]; r += 256) a.row_tokens[r] = -1;
-    for (int64_t r = start[E] + b * 256 + threadIdx.x; r < a.rows; r += int64_t(gridDim.x) * 256)
+    // the segments' starts: a scan of the aligned totals, one expert per thread (E <= THREADS)
+    {
+        const int64_t len = tid < E ? (int64_t(total[tid]) + a.align - 1) / a.align * a.align : 0;
+        int sum = int(len);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(sum, d);
+            if (lane >= d) sum += o;
+        }
+        if (lane == 63) wave_total[tid >> 6] = sum;
+        __syncthreads();
+        int add = 0;
+        for (int w = 0; w < tid >> 6; ++w) add += wave_total[w];
+        if (tid < E) start[tid + 1] = add + sum;
+        if (tid == 0) start[0] = 0;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int e = tid; e <= E; e += THREADS) a.offsets[e] = start[e];
+    // fillings, a wave each: experts g, g + grid, ..., and a share of what is behind the last segment
+    if (a.align > 1)
+        for (int64_t e = int64_t(blockIdx.x) * (THREADS / 64) + (tid >> 6); e < E; e += int64_t(gridDim.x) * (THREADS / 64))
+            for (int r = start[e] + total[e] + lane; r < start[e + 1]; r += 64) a.row_tokens[r] = -1;
+    for (int64_t r = start[E] + int64_t(blockIdx.x) * THREADS + tid; r < a.rows; r += int64_t(gridDim.x) * THREADS)
         a.row_tokens[r] = -1;
-    for (int s = threadIdx.x; s < ROUTE_BLOCK * a.top_k; s += 256) {
-        const int i = s / a.top_k;
-        const int64_t t = b * ROUTE_BLOCK + i;
-        if (t >= a.tokens) break;
-        const int64_t slot = t * a.top_k + s % a.top_k;
-        const int e = a.ids[slot];
-        int place = -1;
-        if (e >= 0) {
-            place = start[e] + before[e] + __popcll(a.masks[b * E + e] & ((1ull << i) - 1));
-            a.row_tokens[place] = int(t);
+    for (int64_t i = 0; i < own; ++i) {
+        const int64_t block = first_block + i, t0 = block * BLOCK;
+        if (t0 >= a.tokens) break;
+        if (counts != nullptr) {
+            fill_masks(block);
+            __syncthreads();
         }
-        a.places[slot] = place;
+        const int slots = int((a.tokens - t0 < BLOCK ? a.tokens - t0 : BLOCK) * a.top_k);
+        for (int s = tid; s < slots; s += THREADS) {
+            const int bit = s / a.top_k, e = a.ids[t0 * a.top_k + s];
+            int place = -1;
+            if (e >= 0) {
+                place = start[e] + next[e] + __popcll(mask[e] & ((1ull << bit) - 1));
+                a.row_tokens[place] = int(t0 + bit);
+            }
+            a.places[t0 * a.top_k + s] = place;
+        }
+        if (i + 1 < own) {
+            __syncthreads();
+            for (int e = tid; e < E; e += THREADS) {
+                next[e] += __popcll(mask[e]);
+                mask[e] = 0;
+            }
+            __syncthreads();
+        }
     }
 }
 
 // One wave per token.  With p the scores, c the scale and g = c d_weights:
 //   renormalised, S the sum of the chosen p: dp_i = (g_i - sum_j g_j p_j / S) / S for the chosen
 //   sigmoid: dl_i = dp_i p_i (1 - p_i);  softmax: dl_i = p_i (dp_i - sum_j dp_j p_j)
+constexpr int BACK_WAVES = 4;
 template <int PER>
-__global__ __launch_bounds__(WAVES * 64) void route_backward_kernel(RouteBackwardArgs a) {
+__global__ __launch_bounds__(BACK_WAVES * 64) void route_backward_kernel(RouteBackwardArgs a) {
     const int lane = threadIdx.x & 63;
-    const int64_t t = int64_t(blockIdx.x) * WAVES + (threadIdx.x >> 6);
+    const int64_t t = int64_t(blockIdx.x) * BACK_WAVES + (threadIdx.x >> 6);
     if (t >= a.tokens) return;
-    const int E = a.experts;
+    const int E = a.experts, first_e = lane * PER;
+    const int esize = a.type == 0 ? 4 : 2;
+    const int64_t bytes = int64_t(PER < 4 ? PER : 4) * 4;
+    auto aligned = [&](const void *x, int64_t ld) {
+        return (reinterpret_cast<uintptr_t>(x) | uint64_t(ld * esize)) % bytes == 0;
+    };
     int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
     if (id < 0 || id >= E) id = -1;
     const float g = id >= 0 ? a.scale * a.d_weights[t * a.top_k + lane] : 0.0f;
     const bool any = __ballot(id >= 0) != 0;
-    float l[PER], top = -INFINITY;
+    const bool dense = !a.sigmoid && !a.renormalise && any;  // every logit has a gradient
+    float l[PER], top = NONE;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = e < E && any ? load_logit(a.logits, t * a.ldl + e, a.type) : -INFINITY;
-        top = fmaxf(top, l[i]);
-    }
-    const float mine = id >= 0 ? load_logit(a.logits, t * a.ldl + id, a.type) : -INFINITY;
-    float sum = 1.0f, p;
+    for (int i = 0; i < PER; ++i) l[i] = NONE;
+    if (dense) load_logits<PER>(a.logits, t * a.ldl + first_e, a.type, E - first_e, aligned(a.logits, a.ldl), l);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) top = fmaxf(top, l[i]);
+    const float mine = id >= 0 ? load_logit(a.logits, t * a.ldl + id, a.type) : NONE;
+    float p;
     if (a.sigmoid) {
         p = id >= 0 ? 1.0f / (1.0f + expf(-mine)) : 0.0f;
     } else {
         // renormalised, the other experts' scores cancel: only the chosen matter
-        if (a.renormalise) top = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+        top = wave_max(a.renormalise ? mine : top);
         p = id >= 0 ? expf(mine - top) : 0.0f;
-        if (!a.renormalise) {
-            sum = 0.0f;
+        if (dense) {
+            float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) sum += l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
-            sum = wave_sum(sum);
-            p /= sum;
+            for (int i = 0; i < PER; ++i) {
+                l[i] = l[i] > NONE ? expf(l[i] - top) : l[i] != l[i] ? l[i] : 0.0f;
+                sum += l[i];
+            }
+            const float inverse = 1.0f / wave_sum(sum);
+            p *= inverse;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) l[i] *= inverse;
         }
     }
     float dp = g;
@@ -281,58 +609,56 @@ __global__ __launch_bounds__(WAVES * 64) void route_backward_kernel(RouteBackwar
         const float mean = total > 0.0f ? wave_sum(g * p) / total : 0.0f;
         dp = total > 0.0f ? (g - mean) / total : 0.0f;
     }
-    float d;
-    if (a.sigmoid) d = id >= 0 ? dp * p * (1.0f / (1.0f + expf(mine))) : 0.0f;
-    else d = dp * p;
-    const float inner = a.sigmoid || a.renormalise ? 0.0f : wave_sum(dp * p);
+    const float d = a.sigmoid ? (id >= 0 ? dp * p * (1.0f / (1.0f + expf(mine))) : 0.0f) : dp * p;
+    const float inner = dense ? wave_sum(d) : 0.0f;
     float out[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        out[i] = inner != 0.0f && l[i] > -INFINITY ? -(expf(l[i] - top) / sum) * inner : 0.0f;
+    for (int i = 0; i < PER; ++i) out[i] = dense ? -l[i] * inner : 0.0f;
     for (int j = 0; j < a.top_k; ++j) {
-        const int e = __shfl(id, j);
-        const float v = __shfl(d, j);
+        const int e = __builtin_amdgcn_readlane(id, j);
+        const float v = lane_of(d, j);
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (e >= 0 && lane + 64 * i == e) out[i] += v;
+        for (int i = 0; i < PER; ++i) out[i] += first_e + i == e ? v : 0.0f;
     }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        if (e >= E) continue;
-        const int64_t at = t * a.ldd + e;
-        if (a.type == 0) static_cast<float *>(a.d_logits)[at] = out[i];
-        else if (a.type == 1) static_cast<uint16_t *>(a.d_logits)[at] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(out[i]));
-        else static_cast<uint16_t *>(a.d_logits)[at] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(out[i]));
-    }
+    store_logits<PER>(a.d_logits, t * a.ldd + first_e, a.type, E - first_e, aligned(a.d_logits, a.ldd), out);
 }
 
 template <int PER>
 hipError_t go(const RouteArgs &r, hipStream_t stream) {
     RouteArgs a = r;
-    const int64_t blocks = (a.tokens + ROUTE_BLOCK - 1) / ROUTE_BLOCK;
-    if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    if (blocks > 0) {
-        void *args[] = {&a};
-        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&choose_kernel<PER>),
-                                             dim3(unsigned(blocks)), dim3(WAVES * 64), args, 0, stream);
+    const bool layout = a.offsets != nullptr;
+    const int64_t blocks = (a.tokens + BLOCK - 1) / BLOCK;
+    // A workgroup's tokens: one per wave while that leaves most of the chip
+    // empty, four per wave (and counts of 64) beyond.
+    int span = a.tokens <= BLOCK ? 4 : a.tokens <= 4096 ? 16 : BLOCK;
+    int waves = span < 16 ? span : 16;
+    uint8_t *counts = layout && a.tokens > BLOCK ? static_cast<uint8_t *>(a.workspace) : nullptr;
+    if (a.tokens > 0) {
+        const int64_t grid = (a.tokens + span - 1) / span;
+        if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+        void *args[] = {&a, &span, &counts};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&choose_kernel<PER>), dim3(unsigned(grid)),
+                                             dim3(unsigned(waves) * 64), args, 0, stream);
         if (e != hipSuccess) return e;
     }
-    if (a.offsets == nullptr) return hipSuccess;
-    int64_t n = blocks;
-    void *args[] = {&a, &n};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&place_kernel),
-                           dim3(unsigned(blocks > 0 ? blocks : 1)), dim3(256), args, 0, stream);
+    if (!layout) return hipSuccess;
+    // every workgroup reads all counts: at most 256 of them, so that this does not grow with the square
+    int64_t own = (blocks + 255) / 256;
+    if (own < 1) own = 1;
+    const int64_t grid = blocks > 0 ? (blocks + own - 1) / own : 1;
+    const uint8_t *read = counts;
+    void *args[] = {&a, &own, &span, &read};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&place_kernel), dim3(unsigned(grid)), dim3(1024), args, 0, stream);
 }
 
 template <int PER>
 hipError_t go(const RouteBackwardArgs &r, hipStream_t stream) {
     RouteBackwardArgs a = r;
-    const int64_t blocks = (a.tokens + WAVES - 1) / WAVES;
+    const int64_t blocks = (a.tokens + BACK_WAVES - 1) / BACK_WAVES;
     if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
     void *args[] = {&a};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&route_backward_kernel<PER>),
-                           dim3(unsigned(blocks)), dim3(WAVES * 64), args, 0, stream);
+    return hipLaunchKernel(reinterpret_cast<const void *>(&route_backward_kernel<PER>), dim3(unsigned(blocks)),
+                           dim3(BACK_WAVES * 64), args, 0, stream);
 }
 
 template <typename Args>
@@ -351,6 +677,12 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t stream) { return by_expe
 hipError_t launch_route_backward(const RouteBackwardArgs &a, hipStream_t stream) {
     if (a.tokens == 0) return hipSuccess;
     return by_experts(a, stream);
+}
+
+size_t route_workspace(int64_t tokens, int64_t experts) {
+    // a row of byte counts for each span of tokens, at most one per 16
+    const size_t rows = tokens <= 4096 ? size_t((tokens + 15) / 16) : size_t((tokens + BLOCK - 1) / BLOCK);
+    return ((rows > 0 ? rows : 1) * size_t(experts) + 15) / 16 * 16;
 }
 
 }  // namespace libgemm

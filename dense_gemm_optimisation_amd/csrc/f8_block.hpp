@@ -82,11 +82,12 @@ struct RouteArgs {
     int align;
     int64_t rows;
     int32_t *offsets, *row_tokens, *places;  // all null: no layout
-    unsigned long long *masks;               // workspace
+    void *workspace;
 };
-// Tokens whose choices one workspace word of an expert holds.
+// Tokens whose choices of one expert a 64-bit mask holds.
 constexpr int ROUTE_BLOCK = 64;
 constexpr int ROUTE_MAX_EXPERTS = 1024;
+size_t route_workspace(int64_t tokens, int64_t experts);  // bytes
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
 
 struct RouteBackwardArgs {

@@ -344,8 +344,7 @@ int64_t gemm_experts_rows(int64_t tokens, int64_t experts, int64_t top_k, int64_
 
 size_t gemm_experts_route_workspace_size(int64_t tokens, int64_t experts, int64_t top_k) {
     if (!route_sizes_ok(tokens, experts, top_k)) return 0;
-    const int64_t blocks = ceil_div(tokens, ROUTE_BLOCK);
-    return static_cast<size_t>(blocks > 0 ? blocks : 1) * static_cast<size_t>(experts) * 8;
+    return route_workspace(tokens, experts);
 }
 
 gemm_status_t gemm_experts_route(int64_t tokens, int64_t experts, const void *logits, int64_t ldl,
@@ -402,7 +401,7 @@ gemm_status_t gemm_experts_route(int64_t tokens, int64_t experts, const void *lo
                 score == GEMM_SCORE_SIGMOID, static_cast<int>(groups), static_cast<int>(top_groups),
                 static_cast<int>(group_top), static_cast<int>(top_k), renormalise != 0, scale, ids, weights,
                 static_cast<int>(align), rows, offsets, row_tokens, places,
-                layout ? static_cast<unsigned long long *>(workspace) : nullptr};
+                layout ? workspace : nullptr};
     return status_of(launch_route(a, stream));
 }
 
