@@ -402,6 +402,142 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
     }
 }
 
+// ---- few rows
+
+// The first `valid` (any integer) of a chunk's 16 bytes, the others 0.
+__device__ inline u32x4 first_bytes(u32x4 v, int valid) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int n = valid - 4 * w;
+        v[w] = n >= 4 ? v[w] : n <= 0 ? 0u : v[w] & ((1u << (8 * n)) - 1);
+    }
+    return v;
+}
+
+constexpr int FEW_WAVES = 8;
+
+// For at most a few times 16*FM rows of C: B is read once, straight into
+// registers, 16 columns per workgroup, its blocks of K dealt to the waves in
+// turn, UNROLL of them in flight per wave.  The waves' sums are added in
+// order through LDS.  Bound by reading B: with 16 columns a chip-wide launch
+// needs only 4096 columns, and 128-byte pieces of 16 rows keep whole lines.
+template <int FA, int FB, bool PER_COLUMN, int FM, int UNROLL>
+__global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) {
+    __shared__ f32x4 sums[FEW_WAVES][FM * 64];
+    const BlockProblem &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t e = uniform(int64_t(blockIdx.x) / a.grid.tiles_n);
+    const int64_t n0 = uniform(int64_t(blockIdx.x) - e * a.grid.tiles_n) * 16;
+    const bool rows_cut = p.segments == Segments::Rows;
+    int64_t m_lo = 0, m_hi = p.M;
+    if (rows_cut) {
+        segment_of(p.offsets, e, p.M, m_lo, m_hi);
+        m_lo = uniform(m_lo);
+        m_hi = uniform(m_hi);
+    }
+    const int64_t ea = rows_cut ? 0 : e, ec = rows_cut ? 0 : e;
+    const int64_t kbs = (p.K + 127) / 128;
+    const int c = lane >> 4;  // this lane's chunks of a block: c and 4 + c
+    const int64_t n = n0 + (lane & 15) < p.N ? n0 + (lane & 15) : p.N - 1;  // rows past the end read the last
+    const uint8_t *b = p.b.x + e * p.b.stride + n * p.b.ld;
+    const float *sb = p.b.s + e * p.b.sstride;
+    auto chunk = [&](const uint8_t *row, int64_t kb, int which) {
+        // a chunk past the end of K reads the block's first instead, and is cleared below
+        const int at = 16 * (c + 4 * which);
+        return *reinterpret_cast<const u32x4 *>(row + 128 * kb + (128 * kb + at < p.K ? at : 0));
+    };
+    auto joined = [&](u32x4 lo, u32x4 hi, int64_t kb) {
+        if (128 * kb + 128 > p.K) {
+            lo = first_bytes(lo, int(p.K - 128 * kb) - 16 * c);
+            hi = first_bytes(hi, int(p.K - 128 * kb) - 16 * (c + 4));
+        }
+        return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]),
+                     int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
+    };
+    for (int64_t m0 = m_lo; m0 < m_hi; m0 += 16 * FM) {
+        const uint8_t *ar[FM];
+        int64_t am[FM];
+        f32x4 acc[FM];
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int64_t m = m0 + 16 * i + (lane & 15);
+            am[i] = m < m_hi ? m : m_hi - 1;
+            ar[i] = p.a.x + ea * p.a.stride + am[i] * p.a.ld;
+            acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        for (int64_t k0 = wave; k0 < kbs; k0 += FEW_WAVES * UNROLL) {
+            u32x4 bv[UNROLL][2], av[UNROLL][FM][2];
+            float sa[UNROLL][FM];
+            f32x4 sv[UNROLL];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int64_t kb = k0 + u * FEW_WAVES < kbs ? k0 + u * FEW_WAVES : kbs - 1;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) bv[u][h] = chunk(b, kb, h);
+                if (PER_COLUMN) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int64_t nr = n0 + 4 * c + r;
+                        sv[u][r] = sb[kb * p.b.lds + (nr < p.N ? nr : p.N - 1)];
+                    }
+                } else {
+                    sv[u][0] = sb[kb * p.b.lds + (n0 >> 7)];
+                }
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) av[u][i][h] = chunk(ar[i], kb, h);
+                    sa[u][i] = p.a.s[ea * p.a.sstride + kb * p.a.lds + (am[i] >> p.a.shift)];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                const int64_t kb = k0 + u * FEW_WAVES;
+                if (kb >= kbs) break;
+                const i32x8 fb = joined(bv[u][0], bv[u][1], kb);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        fb, joined(av[u][i][0], av[u][i][1], kb), f32x4{0.0f, 0.0f, 0.0f, 0.0f}, FB, FA, 0, UNIT,
+                        0, UNIT);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][r] = __builtin_fmaf(part[r], sa[u][i] * sv[u][PER_COLUMN ? r : 0], acc[i][r]);
+                }
+            }
+        }
+        if (m0 > m_lo) __syncthreads();  // the last rows' sums have been read
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sums[wave][i * 64 + lane] = acc[i];
+        __syncthreads();
+        if (tid < FM * 64) {
+            f32x4 v = sums[0][tid];
+#pragma unroll
+            for (int w = 1; w < FEW_WAVES; ++w) v += sums[w][tid];
+            const int64_t m = m0 + 16 * (tid >> 6) + (tid & 15), col = n0 + 4 * (tid >> 4 & 3);
+            if (m < m_hi && col < p.N) {
+                const int64_t at = ec * p.sC + m * p.ldc + col;
+                if (p.out == 0) store_four<0>(p, at, p.alpha * v, p.N - col);
+                else if (p.out == 1) store_four<1>(p, at, p.alpha * v, p.N - col);
+                else store_four<2>(p, at, p.alpha * v, p.N - col);
+            }
+        }
+    }
+}
+
+template <int FA, int FB, bool PER_COLUMN, int FM, int UNROLL>
+hipError_t few_go(const BlockProblem &p, hipStream_t stream) {
+    BlockArgs a{};
+    a.p = p;
+    a.grid.tiles_n = (p.N + 15) / 16;
+    const int64_t count = a.grid.tiles_n * p.batch;
+    if (count > 0x7fffffff) return hipErrorInvalidConfiguration;
+    void *args[] = {&a};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&block_few_kernel<FA, FB, PER_COLUMN, FM, UNROLL>),
+                           dim3(static_cast<unsigned>(count)), dim3(FEW_WAVES * 64), args, 0, stream);
+}
+
 template <int FA, int FB, bool PER_COLUMN, int WM, int WN, int FM, int FN>
 hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
     constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
@@ -422,6 +558,9 @@ hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
 
 template <int FA, int FB, bool PER_COLUMN>
 hipError_t tile_size(BlockKernel k, const BlockProblem &p, hipStream_t stream) {
+    if (k == BlockKernel::Few16) return few_go<FA, FB, PER_COLUMN, 1, 4>(p, stream);
+    if (k == BlockKernel::Few32) return few_go<FA, FB, PER_COLUMN, 2, 4>(p, stream);
+    if (k == BlockKernel::Few64) return few_go<FA, FB, PER_COLUMN, 4, 2>(p, stream);
     if (k == BlockKernel::Tile256) return tile_go<FA, FB, PER_COLUMN, 2, 4, 8, 4>(p, stream);
     return tile_go<FA, FB, PER_COLUMN, 2, 2, 4, 4>(p, stream);
 }
@@ -450,8 +589,11 @@ LIBGEMM_BLOCK_FORMATS(3, 1, 1)
 
 #if LIBGEMM_BLOCK_PART <= 0
 BlockKernel block_choose(const BlockProblem &p, bool tiles_only) {
-    (void)tiles_only;
     if (p.M == 0 || p.N == 0 || p.batch == 0) return BlockKernel::None;
+    // rows of C that share a B: all of them, or an expert's share
+    const int64_t rows = p.segments == Segments::Rows ? (p.M + p.batch - 1) / p.batch : p.M;
+    if (!tiles_only && p.segments != Segments::Contracted && rows <= 64)
+        return rows <= 16 ? BlockKernel::Few16 : rows <= 32 ? BlockKernel::Few32 : BlockKernel::Few64;
     const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256) * (p.segments == Segments::Rows ? 1 : p.batch);
     return tiles >= 192 ? BlockKernel::Tile256 : BlockKernel::Tile128;
 }
@@ -460,6 +602,9 @@ const char *block_kernel_name(BlockKernel k) {
     switch (k) {
     case BlockKernel::None: return "";
     case BlockKernel::Tile256: return "f8block_mfma_256";
+    case BlockKernel::Few16: return "f8block_few_16";
+    case BlockKernel::Few32: return "f8block_few_32";
+    case BlockKernel::Few64: return "f8block_few_64";
     case BlockKernel::Tile128: return "f8block_mfma_128";
     }
     return "";

@@ -40,7 +40,7 @@ struct BlockProblem {
     const int32_t *offsets;  // batch + 1, with segments
 };
 
-enum class BlockKernel { None, Tile256, Tile128 };
+enum class BlockKernel { None, Tile256, Tile128, Few16, Few32, Few64 };
 BlockKernel block_choose(const BlockProblem &p, bool tiles_only);
 const char *block_kernel_name(BlockKernel k);
 hipError_t launch_block(BlockKernel k, const BlockProblem &p, hipStream_t stream);

@@ -111,6 +111,14 @@ def product(lib, rng, M, N, K, fa="e4m3", fb="e4m3", block_a=1, block_b=128, out
     assert torch.equal(after[keep], before[keep])
 
 
+@pytest.fixture(params=["chosen", "tiles"])
+def kernels(request, switches, lib):
+    """Each case by the kernel the library chooses, and by the tile kernels alone."""
+    if request.param == "tiles":
+        switches(lib.TEST_FORCE_GENERAL)
+    return request.param
+
+
 SHAPES = [(1, 1, 1), (1, 16, 128), (3, 5, 17), (16, 16, 16), (17, 130, 129), (33, 64, 255), (64, 200, 256), (65, 257, 384),
           (128, 128, 1001), (129, 128, 640), (256, 300, 512), (260, 520, 144), (300, 1, 2050), (1, 700, 4096), (16, 513, 1100),
           (200, 96, 4096)]
@@ -118,7 +126,7 @@ SHAPES = [(1, 1, 1), (1, 16, 128), (3, 5, 17), (16, 16, 16), (17, 130, 129), (33
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
 @pytest.mark.parametrize("blocks", [(1, 128), (1, 1), (128, 128), (128, 1)])
-def test_product_exact(lib, M, N, K, blocks):
+def test_product_exact(lib, kernels, M, N, K, blocks):
     rng = np.random.default_rng(M * 7 + N * 3 + K)
     product(lib, rng, M, N, K, block_a=blocks[0], block_b=blocks[1], out="f32")
 
@@ -126,7 +134,7 @@ def test_product_exact(lib, M, N, K, blocks):
 @pytest.mark.parametrize("M,N,K", [(1, 96, 300), (40, 70, 1001), (150, 260, 520), (300, 400, 256)])
 @pytest.mark.parametrize("fa,fb", [("e4m3", "e5m2"), ("e5m2", "e4m3"), ("e5m2", "e5m2"), ("e4m3", "e4m3")])
 @pytest.mark.parametrize("out", ["f32", "bf16", "f16"])
-def test_product_formats_and_outputs(lib, M, N, K, fa, fb, out):
+def test_product_formats_and_outputs(lib, kernels, M, N, K, fa, fb, out):
     rng = np.random.default_rng(M + N + K)
     product(lib, rng, M, N, K, fa, fb, out=out, alpha=0.5, beta=2.0)
     product(lib, rng, M, N, K, fa, fb, out=out, exact=False, alpha=0.7 if out != "f16" else 1e-3, beta=-0.3)
@@ -134,14 +142,24 @@ def test_product_formats_and_outputs(lib, M, N, K, fa, fb, out):
 
 @pytest.mark.parametrize("M,N,K", [(5, 40, 300), (100, 70, 1001), (270, 150, 520)])
 @pytest.mark.parametrize("blocks", [(1, 128), (1, 1), (128, 1)])
-def test_product_column_major_and_batched(lib, M, N, K, blocks):
+def test_product_column_major_and_batched(lib, kernels, M, N, K, blocks):
     rng = np.random.default_rng(K)
     product(lib, rng, M, N, K, block_a=blocks[0], block_b=blocks[1], order="col", beta=1.0, batch=3)
     product(lib, rng, M, N, K, block_a=blocks[0], block_b=blocks[1], batch=4, share_b=True, out="f32")
 
 
+@pytest.mark.parametrize("M,N,K,batch,kernel", [
+    (1, 40, 300, 1, "f8block_few_16"), (20, 40, 300, 1, "f8block_few_32"), (64, 40, 300, 3, "f8block_few_64"),
+    (65, 40, 300, 1, "f8block_mfma_128"), (3500, 3600, 401, 1, "f8block_mfma_256"), (70, 90, 650, 200, "f8block_mfma_256"),
+])
+@pytest.mark.parametrize("blocks", [(1, 128), (1, 1)])
+def test_product_kernels(lib, M, N, K, batch, kernel, blocks):
+    rng = np.random.default_rng(M)
+    product(lib, rng, M, N, K, block_a=blocks[0], block_b=blocks[1], batch=batch, out="f32", kernel=kernel)
+
+
 @pytest.mark.parametrize("M,N", [(3, 20), (70, 300)])
-def test_product_without_terms(lib, M, N):
+def test_product_without_terms(lib, kernels, M, N):
     rng = np.random.default_rng(5)
     for beta in (0.0, 0.5):
         product(lib, rng, M, N, 0, beta=beta)
@@ -149,7 +167,7 @@ def test_product_without_terms(lib, M, N):
 
 
 @pytest.mark.parametrize("M", [2, 200])
-def test_product_nan_and_infinity(lib, M):
+def test_product_nan_and_infinity(lib, kernels, M):
     rng = np.random.default_rng(6)
     a, b = Operand(rng, M, 300, "e5m2", 1, True), Operand(rng, 140, 300, "e4m3", 128, True)
     c = torch.full((M, 140), float("nan"), device=DEV)  # beta == 0: not read
@@ -207,20 +225,31 @@ COUNTS = [[1], [5, 0, 3], [0, 0, 0], [130, 1, 0, 128, 17], [0, 300, 2], [64] * 5
 
 @pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{sum(c)}")
 @pytest.mark.parametrize("N,K", [(40, 272), (130, 129), (256, 512)])
-def test_experts_exact(lib, counts, N, K):
+def test_experts_exact(lib, kernels, counts, N, K):
     rng = np.random.default_rng(len(counts) + sum(counts) + N)
     experts(lib, rng, counts, N, K, spare_rows=9, out="f32")
     experts(lib, rng, counts, N, K, spare_rows=0, lead=6, block_b=1, beta=1.0)
 
 
 @pytest.mark.parametrize("fa,fb,out", [("e4m3", "e4m3", "bf16"), ("e5m2", "e4m3", "f32"), ("e4m3", "e5m2", "bf16")])
-def test_experts_random(lib, fa, fb, out):
+def test_experts_random(lib, kernels, fa, fb, out):
     rng = np.random.default_rng(11)
     experts(lib, rng, [40, 0, 7, 200, 1], 300, 1001, 5, fa, fb, out=out, exact=False, alpha=0.25, beta=0.5)
 
 
+def test_experts_kernels(lib):
+    rng = np.random.default_rng(21)
+    experts(lib, rng, [1, 0, 9, 30], 70, 300, 0, out="f32", kernel="f8block_few_16")
+    experts(lib, rng, [3, 0, 90, 20], 70, 300, 0, out="f32", kernel="f8block_few_32")
+    experts(lib, rng, [3, 0, 90, 120], 70, 300, 0, out="f32", kernel="f8block_few_64")
+    experts(lib, rng, [300, 0, 90, 120], 70, 300, 0, out="f32", kernel="f8block_mfma_128")
+    experts(lib, rng, [1300, 0, 700, 257], 6000, 200, 11, out="f32", kernel="f8block_mfma_256")
+    wgrad(lib, rng, [256, 0, 128], 1500, 2600, out="f32", kernel="f8block_mfma_256")
+    wgrad(lib, rng, [256, 0, 128], 150, 260, out="f32", kernel="f8block_mfma_128")
+
+
 @pytest.mark.parametrize("off", [[0, 10, 5, 20], [-4, 3, 900, 7], [2000, -1, 5, 30], [0, 0, 0, 2 ** 31 - 1]])
-def test_experts_bad_offsets_stay_inside(lib, off):
+def test_experts_bad_offsets_stay_inside(lib, kernels, off):
     rng = np.random.default_rng(3)
     a, b = Operand(rng, 40, 160, "e4m3", 1, True), Operand(rng, 50, 160, "e4m3", 128, True, 3)
     c = torch.zeros(42, 50, device=DEV)
