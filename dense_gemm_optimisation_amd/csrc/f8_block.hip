@@ -11,6 +11,8 @@
 // two scales, to the fp32 accumulators.  The operands are swapped (B's
 // fragment first), so a lane's four values are consecutive columns of one
 // row of C: with a scale per 128 rows of B all four share one factor.
+#include <type_traits>
+
 #include "dma_tile.hpp"
 #include "f8_block.hpp"
 
@@ -37,7 +39,6 @@ using dma::wait_vmcnt;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint16_t u16x4_ea __attribute__((ext_vector_type(4), aligned(2)));
 
 constexpr int UNIT = 0x7F7F7F7F;  // E8M0 2^0 in every byte
 
@@ -147,46 +148,83 @@ __device__ inline bool find_segment(const BlockProblem &p, int64_t tm, int BM, i
     return false;
 }
 
-// Four consecutive columns of a row of C at element `at`, the first `n` of
-// them inside C (n >= 4: all).
-template <int OUT>
-__device__ inline void store_four(const BlockProblem &p, int64_t at, f32x4 v, int64_t n) {
-    auto old = [](uint16_t b) {
-        return OUT == 1 ? __builtin_bit_cast(float, uint32_t(b) << 16)
-                        : static_cast<float>(__builtin_bit_cast(_Float16, b));
+typedef uint32_t u32x2_ea __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32x4_ea __attribute__((ext_vector_type(4), aligned(2)));
+
+// W consecutive columns (4, or 8 of a 16-bit type) of a row of C at element
+// `at`, the first `n` of them inside C (n >= W: all): v + beta * C, rounded.
+// Rows of C start at any element: the accesses are element-aligned only.
+template <int OUT, int W>
+__device__ inline void store_columns(const BlockProblem &p, int64_t at, const float *v, int64_t n) {
+    auto old = [](uint32_t b) {
+        return OUT == 1 ? __builtin_bit_cast(float, b << 16)
+                        : static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(b)));
     };
     auto bits = [](float x) {
-        return OUT == 1 ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(x))
-                        : __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+        return uint32_t(OUT == 1 ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(x))
+                                 : __builtin_bit_cast(uint16_t, static_cast<_Float16>(x)));
     };
-    if (OUT == 0) {
+    if constexpr (OUT == 0) {
+        static_assert(W == 4, "16 bytes");
         float *c = static_cast<float *>(p.C) + at;
-        if (n >= 4) {
+        if (n >= W) {
+            f32x4 x = {v[0], v[1], v[2], v[3]};
             if (p.beta != 0.0f) {
                 const f32x4 o = *reinterpret_cast<const dmatile::f32x4_ea *>(c);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(p.beta, o[r], v[r]);
+                for (int r = 0; r < 4; ++r) x[r] = __builtin_fmaf(p.beta, o[r], x[r]);
             }
-            *reinterpret_cast<dmatile::f32x4_ea *>(c) = v;
+            *reinterpret_cast<dmatile::f32x4_ea *>(c) = x;
         } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < W - 1; ++r)
                 if (r < n) c[r] = p.beta != 0.0f ? __builtin_fmaf(p.beta, c[r], v[r]) : v[r];
         }
     } else {
+        using V = std::conditional_t<W == 8, u32x4_ea, u32x2_ea>;
         uint16_t *c = static_cast<uint16_t *>(p.C) + at;
-        if (n >= 4) {
+        if (n >= W) {
+            V x;
             if (p.beta != 0.0f) {
-                const u16x4_ea o = *reinterpret_cast<const u16x4_ea *>(c);
+                const V o = *reinterpret_cast<const V *>(c);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(p.beta, old(o[r]), v[r]);
+                for (int r = 0; r < W / 2; ++r)
+                    x[r] = bits(__builtin_fmaf(p.beta, old(o[r] & 0xffffu), v[2 * r])) |
+                           bits(__builtin_fmaf(p.beta, old(o[r] >> 16), v[2 * r + 1])) << 16;
+            } else {
+#pragma unroll
+                for (int r = 0; r < W / 2; ++r) x[r] = bits(v[2 * r]) | bits(v[2 * r + 1]) << 16;
             }
-            *reinterpret_cast<u16x4_ea *>(c) = u16x4_ea{bits(v[0]), bits(v[1]), bits(v[2]), bits(v[3])};
+            *reinterpret_cast<V *>(c) = x;
         } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (r < n) c[r] = bits(p.beta != 0.0f ? __builtin_fmaf(p.beta, old(c[r]), v[r]) : v[r]);
+            for (int r = 0; r < W - 1; ++r)
+                if (r < n) c[r] = uint16_t(bits(p.beta != 0.0f ? __builtin_fmaf(p.beta, old(c[r]), v[r]) : v[r]));
         }
+    }
+}
+
+// 16 rows of a wave's tile (16*FN columns) that it staged in LDS, row by row:
+// 16-byte chunk q of row r at q ^ r, so that neither the columns' writes nor
+// the rows' reads meet in a bank.  A store covers whole rows of the strip.
+template <int OUT, int FN>
+__device__ inline void store_strip(const BlockProblem &p, const LDS float *strip, int64_t slice, int64_t m0,
+                                   int64_t m_end, int64_t n0, int lane) {
+    constexpr int W = OUT == 0 ? 4 : 8;          // columns per lane
+    constexpr int LANES = FN * 16 / W;           // per row
+    constexpr int ROWS = 64 / LANES;             // per store
+    const int64_t n = n0 + W * (lane % LANES);
+#pragma unroll 1
+    for (int r0 = 0; r0 < 16; r0 += ROWS) {
+        const int r = r0 + lane / LANES;
+        float v[W];
+#pragma unroll
+        for (int h = 0; h < W / 4; ++h) {
+            const int q = (lane % LANES) * (W / 4) + h;
+            const f32x4 x = *reinterpret_cast<const LDS f32x4 *>(strip + r * FN * 16 + ((q ^ r) & (FN * 4 - 1)) * 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[4 * h + k] = x[k];
+        }
+        if (m0 + r < m_end && n < p.N) store_columns<OUT, W>(p, slice + (m0 + r) * p.ldc + n, v, p.N - n);
     }
 }
 
@@ -385,20 +423,21 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
         finish();
     }
 
+    // The buffer after the last stage's: nothing reads or fills it any more.
+    static_assert(WAVES * 16 * WTN * 4 <= STAGE, "a strip per wave fits a stage");
+    LDS float *strip = reinterpret_cast<LDS float *>(lds + (buf ^ 1) * STAGE) + wave * 16 * WTN;
+    const int64_t mw = m0 + wm * WTM, nw = n0 + wn * WTN, slice = ec * p.sC;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int64_t m = m0 + wm * WTM + i * 16 + (lane & 15);
-        if (m >= m_end) continue;
+        const int r = lane & 15;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const int64_t n = n0 + wn * WTN + j * 16 + 4 * (lane >> 4);
-            if (n >= p.N) continue;
-            const int64_t c = ec * p.sC + m * p.ldc + n;
-            const f32x4 v = p.alpha * acc[i][j];
-            if (p.out == 0) store_four<0>(p, c, v, p.N - n);
-            else if (p.out == 1) store_four<1>(p, c, v, p.N - n);
-            else store_four<2>(p, c, v, p.N - n);
+            const int q = j * 4 + (lane >> 4);
+            *reinterpret_cast<LDS f32x4 *>(strip + r * WTN + ((q ^ r) & (FN * 4 - 1)) * 4) = p.alpha * acc[i][j];
         }
+        if (p.out == 0) store_strip<0, FN>(p, strip, slice, mw + i * 16, m_end, nw, lane);
+        else if (p.out == 1) store_strip<1, FN>(p, strip, slice, mw + i * 16, m_end, nw, lane);
+        else store_strip<2, FN>(p, strip, slice, mw + i * 16, m_end, nw, lane);
     }
 }
 
@@ -518,9 +557,11 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) 
             const int64_t m = m0 + 16 * (tid >> 6) + (tid & 15), col = n0 + 4 * (tid >> 4 & 3);
             if (m < m_hi && col < p.N) {
                 const int64_t at = ec * p.sC + m * p.ldc + col;
-                if (p.out == 0) store_four<0>(p, at, p.alpha * v, p.N - col);
-                else if (p.out == 1) store_four<1>(p, at, p.alpha * v, p.N - col);
-                else store_four<2>(p, at, p.alpha * v, p.N - col);
+                v *= p.alpha;
+                const float x[4] = {v[0], v[1], v[2], v[3]};
+                if (p.out == 0) store_columns<0, 4>(p, at, x, p.N - col);
+                else if (p.out == 1) store_columns<1, 4>(p, at, x, p.N - col);
+                else store_columns<2, 4>(p, at, x, p.N - col);
             }
         }
     }
