@@ -159,9 +159,18 @@ def abi_version() -> int:
     return library().gemm_abi_version()
 
 
+# The handle of a device's current stream without building a Stream object,
+# which costs as much as a launch; torch builds without it take that way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else 0
+        if not torch.cuda.is_initialized():  # no stream but the default one can be current
+            return 0
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)

@@ -87,11 +87,15 @@ struct Panel {
     __device__ void issue(uint32_t at, int64_t stage, int64_t kleft, int wave, int lane) const {
         const u32x4 rs = dma::raw_buffer(static_cast<uint64_t>(base + 128 * stage),
                                          static_cast<uint32_t>(bytes - 128 * stage));
+        if (kleft >= 128) {
 #pragma unroll
-        for (int i = 0; i < PER_WAVE; ++i) {
-            uint32_t v = voff[i];
-            if (kleft < 128) v = lane_k(i, wave, lane) < int(kleft) ? v : OOB;
-            direct_load16(rs, at + (wave * PER_WAVE + i) * 1024, v);
+            for (int i = 0; i < PER_WAVE; ++i)
+                direct_load16(rs, at + (wave * PER_WAVE + i) * 1024, voff[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER_WAVE; ++i)
+                direct_load16(rs, at + (wave * PER_WAVE + i) * 1024,
+                              lane_k(i, wave, lane) < int(kleft) ? voff[i] : OOB);
         }
     }
 };
@@ -333,18 +337,21 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
     auto read_b = [&](int buf, int j) {
         fb[j] = frag(lds + buf * STAGE + AT_B, wn * WTN + j * 16, at);
     };
+    float nsa[FM], nfactor = 0.0f;  // the next stage's, as stored
     auto read_scales = [&](int buf) {
         const LDS float *s = reinterpret_cast<const LDS float *>(lds + buf * STAGE + AT_S);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) sa[i] = s[wm * WTM + i * 16 + (lane & 15)];
-        if (PER_COLUMN) {
+        for (int i = 0; i < FM; ++i) nsa[i] = s[wm * WTM + i * 16 + (lane & 15)];
+        if (!PER_COLUMN) nfactor = s[BM + wn * WTN];
+    };
+    auto take_scales = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sa[i] = PER_COLUMN ? nsa[i] : nsa[i] * nfactor;
+        if (PER_COLUMN) {  // read here: there are no registers for two stages' columns
+            const LDS float *s = reinterpret_cast<const LDS float *>(lds + buf * STAGE + AT_S);
 #pragma unroll
             for (int j = 0; j < FN; ++j)
                 sb[j] = *reinterpret_cast<const LDS f32x4 *>(s + BM + wn * WTN + j * 16 + 4 * (lane >> 4));
-        } else {
-            const float f = s[BM + wn * WTN];
-#pragma unroll
-            for (int i = 0; i < FM; ++i) sa[i] *= f;
         }
     };
     auto start = [&](int n) {
@@ -365,13 +372,21 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
     };
     // Rows 0 .. FM - 2 of the stage in buffer buf.
     auto rows = [&](int buf) {
-        read_scales(buf);
+        take_scales(buf);
 #pragma unroll
         for (int n = 0; n < (FM - 1) * FN; ++n) {
             if (n % FN == 0) read_a(buf, n / FN + 1);
             start(n);
             if (n >= LAG) add(n - LAG);
-            if (n % FN == FN - 1) __builtin_amdgcn_sched_barrier(0);
+            if (n % FN == FN - 1) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    if (j < 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, PER_COLUMN ? 8 : 4, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
     auto finish = [&]() {
@@ -394,6 +409,7 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
 #pragma unroll
         for (int j = 0; j < FN; ++j) read_b(0, j);
         read_a(0, 0);
+        read_scales(0);
     }
     int buf = 0;
     for (int64_t s = 0; s + 1 < steps; ++s) {
@@ -403,6 +419,7 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
         __syncthreads();
         if (s + 2 == steps && (K & 15) != 0) clear_tail(buf ^ 1);
         read_a(buf ^ 1, 0);
+        read_scales(buf ^ 1);
         if (s + 2 < steps) issue(s + 2, buf);
 #pragma unroll
         for (int n = (FM - 1) * FN; n < FM * FN; ++n) {
