@@ -63,40 +63,34 @@ struct Panel {
     static_assert(PER_WAVE >= 1 && ROWS % (8 * WAVES) == 0, "panel split over waves");
     uint32_t voff[PER_WAVE];
     int64_t base;
-    int64_t bytes;
+    uint32_t bytes;
 
     // This lane's first k, within a stage, in load i.
     __device__ static int lane_k(int i, int wave, int lane) {
         return ((lane & 7) ^ swz((wave * PER_WAVE + i) * 8 + (lane >> 3))) * 16;
     }
 
-    // Rows r0 .. r0 + nrows - 1 (nrows <= ROWS valid) from byte k0 of each row on, K of them.
-    __device__ void init(const uint8_t *x, int64_t ld, int64_t r0, int64_t nrows, int64_t k0,
-                         int64_t K, int wave, int lane) {
+    // Rows r0 .. r0 + nrows - 1 (nrows <= ROWS valid) from byte k0 of each row
+    // on, K of them (ld < 2^22: a tile's rows lie within 2^30 bytes).
+    __device__ void init(const uint8_t *x, int64_t ld, int64_t r0, int nrows, int64_t k0, int K, int wave, int lane) {
         base = uniform(reinterpret_cast<int64_t>(x) + r0 * ld + k0);
-        bytes = uniform((nrows - 1) * ld + ((K + 15) & ~int64_t(15)));
+        const uint32_t pitch = uint32_t(ld);
+        bytes = uint32_t(uniform(int64_t(uint32_t(nrows - 1) * pitch + ((uint32_t(K) + 15) & ~15u))));
 #pragma unroll
         for (int i = 0; i < PER_WAVE; ++i) {
             const int row = (wave * PER_WAVE + i) * 8 + (lane >> 3);
-            voff[i] = row < nrows ? uint32_t(row * ld + lane_k(i, wave, lane)) : OOB;
+            voff[i] = row < nrows ? uint32_t(row) * pitch + lane_k(i, wave, lane) : OOB;
         }
     }
 
-    // All of this wave's loads for the stage at k = 128*stage, kleft = K - 128*stage > 0;
-    // what lies past K reads as zero but for the rest of K's last chunk.
-    __device__ void issue(uint32_t at, int64_t stage, int64_t kleft, int wave, int lane) const {
-        const u32x4 rs = dma::raw_buffer(static_cast<uint64_t>(base + 128 * stage),
-                                         static_cast<uint32_t>(bytes - 128 * stage));
-        if (kleft >= 128) {
-#pragma unroll
-            for (int i = 0; i < PER_WAVE; ++i)
-                direct_load16(rs, at + (wave * PER_WAVE + i) * 1024, voff[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER_WAVE; ++i)
-                direct_load16(rs, at + (wave * PER_WAVE + i) * 1024,
-                              lane_k(i, wave, lane) < int(kleft) ? voff[i] : OOB);
-        }
+    // The stage at k = 128*stage; nothing of it is read where `live` is not set.
+    __device__ u32x4 stage(int stage, bool live) const {
+        return dma::raw_buffer(static_cast<uint64_t>(base + 128 * stage), live ? bytes - 128u * stage : 0u);
+    }
+    // Load i of this wave's for the stage rs with kleft = K - 128*stage; what
+    // lies past K reads as zero but for the rest of K's last chunk.
+    __device__ void load(u32x4 rs, uint32_t at, int i, int kleft, int wave, int lane) const {
+        direct_load16(rs, at + (wave * PER_WAVE + i) * 1024, lane_k(i, wave, lane) < kleft ? voff[i] : OOB);
     }
 };
 
@@ -156,10 +150,11 @@ typedef uint32_t u32x2_ea __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_ea __attribute__((ext_vector_type(4), aligned(2)));
 
 // W consecutive columns (4, or 8 of a 16-bit type) of a row of C at element
-// `at`, the first `n` of them inside C (n >= W: all): v + beta * C, rounded.
-// Rows of C start at any element: the accesses are element-aligned only.
+// `at` of `base`, the first `n` of them inside C (n >= W: all): v + beta * C,
+// rounded.  Rows of C start at any element: the accesses are element-aligned
+// only.
 template <int OUT, int W>
-__device__ inline void store_columns(const BlockProblem &p, int64_t at, const float *v, int64_t n) {
+__device__ inline void store_columns(const BlockProblem &p, char *base, int64_t at, const float *v, int n) {
     auto old = [](uint32_t b) {
         return OUT == 1 ? __builtin_bit_cast(float, b << 16)
                         : static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(b)));
@@ -170,7 +165,7 @@ __device__ inline void store_columns(const BlockProblem &p, int64_t at, const fl
     };
     if constexpr (OUT == 0) {
         static_assert(W == 4, "16 bytes");
-        float *c = static_cast<float *>(p.C) + at;
+        float *c = reinterpret_cast<float *>(base) + at;
         if (n >= W) {
             f32x4 x = {v[0], v[1], v[2], v[3]};
             if (p.beta != 0.0f) {
@@ -185,7 +180,7 @@ __device__ inline void store_columns(const BlockProblem &p, int64_t at, const fl
         }
     } else {
         using V = std::conditional_t<W == 8, u32x4_ea, u32x2_ea>;
-        uint16_t *c = static_cast<uint16_t *>(p.C) + at;
+        uint16_t *c = reinterpret_cast<uint16_t *>(base) + at;
         if (n >= W) {
             V x;
             if (p.beta != 0.0f) {
@@ -207,29 +202,51 @@ __device__ inline void store_columns(const BlockProblem &p, int64_t at, const fl
     }
 }
 
-// 16 rows of a wave's tile (16*FN columns) that it staged in LDS, row by row:
-// 16-byte chunk q of row r at q ^ r, so that neither the columns' writes nor
-// the rows' reads meet in a bank.  A store covers whole rows of the strip.
-template <int OUT, int FN>
-__device__ inline void store_strip(const BlockProblem &p, const LDS float *strip, int64_t slice, int64_t m0,
-                                   int64_t m_end, int64_t n0, int lane) {
+// ROWS rows of a wave's tile (16*FN columns) that it staged in LDS, row by
+// row: 16-byte chunk q of row r at q ^ (r % 16), so that neither the columns'
+// writes nor the rows' reads meet in a bank.  A store covers whole rows of
+// the strip.  c: C's element (0, 0) of the tile, which has mrows x ncols
+// elements; the strip is at (m, n) of it.
+template <int OUT, int FN, int ROWS>
+__device__ inline void store_strip(const BlockProblem &p, const LDS float *strip, char *c, int m, int mrows,
+                                   int n, int ncols, int lane) {
     constexpr int W = OUT == 0 ? 4 : 8;          // columns per lane
     constexpr int LANES = FN * 16 / W;           // per row
-    constexpr int ROWS = 64 / LANES;             // per store
-    const int64_t n = n0 + W * (lane % LANES);
-#pragma unroll 1
-    for (int r0 = 0; r0 < 16; r0 += ROWS) {
-        const int r = r0 + lane / LANES;
-        float v[W];
+    constexpr int STEP = 64 / LANES;             // rows per store
+    n += W * (lane % LANES);
+    float v[ROWS / STEP][W];
+#pragma unroll
+    for (int i = 0; i < ROWS / STEP; ++i) {
+        const int r = i * STEP + lane / LANES;
 #pragma unroll
         for (int h = 0; h < W / 4; ++h) {
             const int q = (lane % LANES) * (W / 4) + h;
             const f32x4 x = *reinterpret_cast<const LDS f32x4 *>(strip + r * FN * 16 + ((q ^ r) & (FN * 4 - 1)) * 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[4 * h + k] = x[k];
+            for (int k = 0; k < 4; ++k) v[i][4 * h + k] = x[k];
         }
-        if (m0 + r < m_end && n < p.N) store_columns<OUT, W>(p, slice + (m0 + r) * p.ldc + n, v, p.N - n);
     }
+#pragma unroll
+    for (int i = 0; i < ROWS / STEP; ++i) {
+        const int r = m + i * STEP + lane / LANES;
+        if (r < mrows && n < ncols) store_columns<OUT, W>(p, c, r * p.ldc + n, v[i], ncols - n);
+    }
+}
+
+// Output tile `id` of the grid, as tile_of numbers them, in 32 bits (the grid
+// has fewer than 2^31 tiles).
+__device__ inline void coordinates(const TileGrid &g, uint32_t wg, uint32_t &batch, uint32_t &tm, uint32_t &tn) {
+    // the dispatcher deals workgroups to the 8 dies in turn: those of one die take neighbouring tiles
+    const uint32_t total = uint32_t(g.count()), q = total / 8, odd = total % 8, x = wg % 8;
+    const uint32_t id = (x < odd ? x * (q + 1) : odd * (q + 1) + (x - odd) * q) + wg / 8;
+    const uint32_t rows = uint32_t(g.tiles_m), cols = uint32_t(g.tiles_n), group = uint32_t(g.group_m);
+    batch = id / (rows * cols);
+    const uint32_t local = id - batch * (rows * cols);
+    const uint32_t n = local / (group * cols), first = n * group;
+    const uint32_t high = rows - first < group ? rows - first : group;  // the last group may be short
+    const uint32_t r = local - n * (group * cols);
+    tn = r / high;
+    tm = first + (r - tn * high);
 }
 
 // One workgroup per BM x BN tile, WAVES_M x WAVES_N waves of FM x FN blocks.
@@ -260,20 +277,21 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
 
-    const TileCoord t = tile_of(a.grid, blockIdx.x);
-    int64_t e = uniform(t.batch), m0 = uniform(t.tm) * BM, m_end = p.M, k_lo = 0, k_hi = p.K;
-    const int64_t n0 = uniform(t.tn) * BN;
-    if (p.segments == Segments::Rows && !find_segment(p, uniform(t.tm), BM, lane, e, m0, m_end)) return;
+    uint32_t te, tm, tn;
+    coordinates(a.grid, blockIdx.x, te, tm, tn);
+    int64_t e = uniform(te), m0 = uniform(tm) * BM, m_end = p.M, k_lo = 0, k_hi = p.K;
+    const int64_t n0 = uniform(tn) * BN;
+    if (p.segments == Segments::Rows && !find_segment(p, uniform(tm), BM, lane, e, m0, m_end)) return;
     if (p.segments == Segments::Contracted) {
         segment_of(p.offsets, e, p.K, k_lo, k_hi);
         k_lo = uniform(k_lo) & ~int64_t(127);
         k_hi = uniform(k_hi);
     }
-    const int64_t K = k_hi - k_lo;
+    const int K = int(uniform(k_hi - k_lo));  // at most ld < 2^22
     const int64_t ea = p.segments == Segments::None ? e : 0;
     const int64_t eb = p.segments == Segments::Contracted ? 0 : e;
     const int64_t ec = p.segments == Segments::Rows ? 0 : e;
-    const int64_t mrows = m_end - m0 < BM ? m_end - m0 : BM, nrows = p.N - n0 < BN ? p.N - n0 : BN;
+    const int mrows = int(m_end - m0 < BM ? m_end - m0 : BM), nrows = int(p.N - n0 < BN ? p.N - n0 : BN);
 
     PA pa;
     PB pb;
@@ -286,7 +304,8 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
     const bool s_on_a = wave < BM / 64;
     const int s_row = (s_on_a ? wave : wave - BM / 64) * 64 + lane;
     const int s_shift = s_on_a ? p.a.shift : p.b.shift;
-    const int64_t s_r0 = s_on_a ? m0 : n0, s_rows = s_on_a ? mrows : nrows;
+    const int64_t s_r0 = s_on_a ? m0 : n0;
+    const int s_rows = s_on_a ? mrows : nrows;
     const int64_t s_first = s_r0 >> s_shift;
     const uint32_t s_voff =
         s_row < s_rows ? uint32_t((((s_r0 + s_row) >> s_shift) - s_first) * 4) : OOB;
@@ -298,20 +317,32 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
         uint32_t(uniform((((s_r0 + s_rows - 1) >> s_shift) - s_first + 1) * 4));
 
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
-    const int64_t steps = (K + 127) / 128;
-    auto issue = [&](int64_t s, int buf) {
+    const int steps = (K + 127) / 128;
+    // The stage that is being loaded.  Its loads (A's, B's, the scales) go out
+    // a few at a time between matrix instructions: all at once they fill the
+    // memory pipe's queue and hold up the matrix pipe.
+    constexpr int LOADS = PA::PER_WAVE + PB::PER_WAVE + 1, EARLY = FN, LOADS_PER_ROW = 2;
+    struct Loading {
+        u32x4 a, b, s;
+        int kleft;
+    };
+    auto loading = [&](int s) {  // stage s; past the last one: loads that read nothing and store zeros
+        const bool live = s < steps;
+        const int kleft = K - 128 * s;
+        return Loading{pa.stage(s, live), pb.stage(s, live),
+                       dma::raw_buffer(static_cast<uint64_t>(s_base + s * s_ld), live ? s_bytes : 0u),
+                       kleft < 128 ? kleft : 128};
+    };
+    auto load = [&](const Loading &l, int buf, int q) {
         const uint32_t at = lds0 + buf * STAGE;
-        const int64_t kleft = K - 128 * s;
-        pa.issue(at, s, kleft, wave, lane);
-        pb.issue(at + AT_B, s, kleft, wave, lane);
-        if (SLOADS == WAVES || wave < SLOADS)
-            direct_load4(dma::raw_buffer(static_cast<uint64_t>(s_base + s * s_ld), s_bytes),
-                         at + AT_S + wave * 256, s_voff);
+        if (q < PA::PER_WAVE) pa.load(l.a, at, q, l.kleft, wave, lane);
+        else if (q < LOADS - 1) pb.load(l.b, at + AT_B, q - PA::PER_WAVE, l.kleft, wave, lane);
+        else if (SLOADS == WAVES || wave < SLOADS) direct_load4(l.s, at + AT_S + wave * 256, s_voff);
     };
     // The chunk that holds the end of K, in the stage of buffer buf: its bytes
     // from K on are not the operand's.
     auto clear_tail = [&](int buf) {
-        const int kleft = int(K & 127), c = kleft >> 4;
+        const int kleft = K & 127, c = kleft >> 4;
         for (int r = tid; r < BM + BN; r += WAVES * 64) {
             const int rr = r < BM ? r : r - BM;
             LDS char *chunk = lds + buf * STAGE + r * 128 + ((c ^ swz(rr)) << 4);
@@ -370,12 +401,18 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
         }
         asm volatile("" : "+v"(acc[i][j]));
     };
-    // Rows 0 .. FM - 2 of the stage in buffer buf.
-    auto rows = [&](int buf) {
+    // Rows 0 .. FM - 2 of stage s, in buffer buf, with the next stage's loads from EARLY on.
+    auto rows = [&](int s, int buf) {
+        const Loading l = loading(s + 1);
         take_scales(buf);
 #pragma unroll
         for (int n = 0; n < (FM - 1) * FN; ++n) {
-            if (n % FN == 0) read_a(buf, n / FN + 1);
+            if (n % FN == 0) {
+                read_a(buf, n / FN + 1);
+#pragma unroll
+                for (int q = EARLY + n / FN * LOADS_PER_ROW; q < EARLY + (n / FN + 1) * LOADS_PER_ROW; ++q)
+                    if (q < LOADS) load(l, buf ^ 1, q);
+            }
             start(n);
             if (n >= LAG) add(n - LAG);
             if (n % FN == FN - 1) {
@@ -389,21 +426,19 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
             }
         }
     };
+    static_assert(EARLY + (FM - 1) * LOADS_PER_ROW >= LOADS, "every load has its place");
     auto finish = [&]() {
 #pragma unroll
         for (int n = FM * FN - LAG; n < FM * FN; ++n) add(n);
     };
 
     if (steps > 0) {
-        issue(0, 0);
-        if (steps > 1) {
-            issue(1, 1);
-            constexpr int PER_STAGE = PA::PER_WAVE + PB::PER_WAVE;  // and a scale load, on some waves
-            if (SLOADS == WAVES || wave < SLOADS) wait_vmcnt<PER_STAGE + 1>();
-            else wait_vmcnt<PER_STAGE>();
-        } else {
-            wait_vmcnt<0>();
-        }
+        const Loading l0 = loading(0), l1 = loading(1);
+#pragma unroll
+        for (int q = 0; q < LOADS; ++q) load(l0, 0, q);
+#pragma unroll
+        for (int q = 0; q < EARLY; ++q) load(l1, 1, q);
+        wait_vmcnt<EARLY>();
         __syncthreads();
         if (steps == 1 && (K & 15) != 0) clear_tail(0);
 #pragma unroll
@@ -412,49 +447,58 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
         read_scales(0);
     }
     int buf = 0;
-    for (int64_t s = 0; s + 1 < steps; ++s) {
-        rows(buf);
+    for (int s = 0; s + 1 < steps; ++s) {
+        rows(s, buf);
         wait_vmcnt<0>();
         dma::wait_lgkmcnt0();
         __syncthreads();
         if (s + 2 == steps && (K & 15) != 0) clear_tail(buf ^ 1);
         read_a(buf ^ 1, 0);
         read_scales(buf ^ 1);
-        if (s + 2 < steps) issue(s + 2, buf);
+        const Loading l = loading(s + 2);
 #pragma unroll
         for (int n = (FM - 1) * FN; n < FM * FN; ++n) {
             start(n);
             read_b(buf ^ 1, n % FN);
+            load(l, buf, n % FN);
             add(n - LAG);
         }
         finish();
         buf ^= 1;
     }
     if (steps > 0) {
-        rows(buf);
+        rows(steps - 1, buf);
 #pragma unroll
         for (int n = (FM - 1) * FN; n < FM * FN; ++n) {
             start(n);
             add(n - LAG);
         }
         finish();
+        // the loads past the last stage have put zeros into the buffer that C goes through
+        wait_vmcnt<0>();
+        __syncthreads();
     }
 
     // The buffer after the last stage's: nothing reads or fills it any more.
-    static_assert(WAVES * 16 * WTN * 4 <= STAGE, "a strip per wave fits a stage");
-    LDS float *strip = reinterpret_cast<LDS float *>(lds + (buf ^ 1) * STAGE) + wave * 16 * WTN;
-    const int64_t mw = m0 + wm * WTM, nw = n0 + wn * WTN, slice = ec * p.sC;
+    constexpr int PAIR = 2;  // strips of 16 rows that leave together
+    static_assert(WAVES * PAIR * 16 * WTN * 4 <= STAGE, "a pair of strips per wave fits a stage");
+    LDS float *strip = reinterpret_cast<LDS float *>(lds + (buf ^ 1) * STAGE) + wave * PAIR * 16 * WTN;
+    char *c = static_cast<char *>(p.C) + (ec * p.sC + m0 * p.ldc + n0) * (p.out == 0 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
+    for (int i = 0; i < FM; i += PAIR) {
         const int r = lane & 15;
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int q = j * 4 + (lane >> 4);
-            *reinterpret_cast<LDS f32x4 *>(strip + r * WTN + ((q ^ r) & (FN * 4 - 1)) * 4) = p.alpha * acc[i][j];
-        }
-        if (p.out == 0) store_strip<0, FN>(p, strip, slice, mw + i * 16, m_end, nw, lane);
-        else if (p.out == 1) store_strip<1, FN>(p, strip, slice, mw + i * 16, m_end, nw, lane);
-        else store_strip<2, FN>(p, strip, slice, mw + i * 16, m_end, nw, lane);
+        for (int k = 0; k < PAIR; ++k)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const int q = j * 4 + (lane >> 4);
+                *reinterpret_cast<LDS f32x4 *>(strip + (k * 16 + r) * WTN + ((q ^ r) & (FN * 4 - 1)) * 4) =
+                    p.alpha * acc[i + k][j];
+            }
+        const int m = wm * WTM + i * 16, n = wn * WTN;
+        if (p.out == 0) store_strip<0, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, lane);
+        else if (p.out == 1) store_strip<1, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, lane);
+        else store_strip<2, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, lane);
     }
 }
 
@@ -574,11 +618,12 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) 
             const int64_t m = m0 + 16 * (tid >> 6) + (tid & 15), col = n0 + 4 * (tid >> 4 & 3);
             if (m < m_hi && col < p.N) {
                 const int64_t at = ec * p.sC + m * p.ldc + col;
+                const int left = p.N - col < 4 ? int(p.N - col) : 4;
                 v *= p.alpha;
                 const float x[4] = {v[0], v[1], v[2], v[3]};
-                if (p.out == 0) store_columns<0, 4>(p, at, x, p.N - col);
-                else if (p.out == 1) store_columns<1, 4>(p, at, x, p.N - col);
-                else store_columns<2, 4>(p, at, x, p.N - col);
+                if (p.out == 0) store_columns<0, 4>(p, static_cast<char *>(p.C), at, x, left);
+                else if (p.out == 1) store_columns<1, 4>(p, static_cast<char *>(p.C), at, x, left);
+                else store_columns<2, 4>(p, static_cast<char *>(p.C), at, x, left);
             }
         }
     }
@@ -607,7 +652,9 @@ hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
         tiles_m = p.M / BM + more < p.M ? p.M / BM + more : p.M;
     }
     a.grid = TileGrid{tiles_m, (p.N + BN - 1) / BN, p.segments == Segments::Rows ? 1 : p.batch, 8, 8};
-    if (a.grid.count() > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (a.grid.tiles_m > 0x7fffffff || a.grid.tiles_n > 0x7fffffff || a.grid.per_batch() > 0x7fffffff ||
+        p.batch > 0x7fffffff || a.grid.count() > 0x7fffffff)
+        return hipErrorInvalidConfiguration;
     void *args[] = {&a};
     return hipLaunchKernel(
         reinterpret_cast<const void *>(&block_tile_kernel<FA, FB, PER_COLUMN, WM, WN, FM, FN>),
