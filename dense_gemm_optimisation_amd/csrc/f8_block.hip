@@ -146,6 +146,20 @@ __device__ inline bool find_segment(const BlockProblem &p, int64_t tm, int BM, i
     return false;
 }
 
+// The n-th longest of at most 64 segments (of equal ones the first): the long
+// ones' tiles start first, so that the short ones fill the end of the launch.
+__device__ inline int64_t by_length(const BlockProblem &p, int64_t n, int lane) {
+    int64_t lo = 0, hi = -1;  // lanes without a segment come last
+    if (lane < p.batch) segment_of(p.offsets, lane, p.K, lo, hi);
+    const int length = int(hi - lo);
+    int ahead = 0;
+    for (int i = 0; i < int(p.batch); ++i) {
+        const int other = __builtin_amdgcn_readlane(length, i);
+        ahead += other > length || (other == length && i < lane);
+    }
+    return uniform(int64_t(__builtin_ctzll(__ballot(lane < p.batch && ahead == int(n)))));
+}
+
 typedef uint32_t u32x2_ea __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_ea __attribute__((ext_vector_type(4), aligned(2)));
 
@@ -236,12 +250,17 @@ __device__ inline void store_strip(const BlockProblem &p, const LDS float *strip
 // Output tile `id` of the grid, as tile_of numbers them, in 32 bits (the grid
 // has fewer than 2^31 tiles).
 __device__ inline void coordinates(const TileGrid &g, uint32_t wg, uint32_t &batch, uint32_t &tm, uint32_t &tn) {
-    // the dispatcher deals workgroups to the 8 dies in turn: those of one die take neighbouring tiles
-    const uint32_t total = uint32_t(g.count()), q = total / 8, odd = total % 8, x = wg % 8;
-    const uint32_t id = (x < odd ? x * (q + 1) : odd * (q + 1) + (x - odd) * q) + wg / 8;
     const uint32_t rows = uint32_t(g.tiles_m), cols = uint32_t(g.tiles_n), group = uint32_t(g.group_m);
-    batch = id / (rows * cols);
-    const uint32_t local = id - batch * (rows * cols);
+    // The dispatcher deals workgroups to the 8 dies in turn: those of one die
+    // take neighbouring tiles, of the whole grid or (g.xcds 0) of every slice
+    // alike: slices of unlike lengths would keep the dies busy for unlike
+    // times.
+    const uint32_t slice = rows * cols, of = g.xcds == 0 ? wg / slice : 0;
+    const uint32_t total = g.xcds == 0 ? slice : uint32_t(g.count()), q = total / 8, odd = total % 8;
+    wg -= of * slice;
+    const uint32_t x = wg % 8, id = (x < odd ? x * (q + 1) : odd * (q + 1) + (x - odd) * q) + wg / 8;
+    batch = g.xcds == 0 ? of : id / slice;
+    const uint32_t local = g.xcds == 0 ? id : id - batch * slice;
     const uint32_t n = local / (group * cols), first = n * group;
     const uint32_t high = rows - first < group ? rows - first : group;  // the last group may be short
     const uint32_t r = local - n * (group * cols);
@@ -283,6 +302,7 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
     const int64_t n0 = uniform(tn) * BN;
     if (p.segments == Segments::Rows && !find_segment(p, uniform(tm), BM, lane, e, m0, m_end)) return;
     if (p.segments == Segments::Contracted) {
+        if (p.batch <= 64) e = by_length(p, e, lane);
         segment_of(p.offsets, e, p.K, k_lo, k_hi);
         k_lo = uniform(k_lo) & ~int64_t(127);
         k_hi = uniform(k_hi);
@@ -617,13 +637,20 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) 
             for (int w = 1; w < FEW_WAVES; ++w) v += sums[w][tid];
             const int64_t m = m0 + 16 * (tid >> 6) + (tid & 15), col = n0 + 4 * (tid >> 4 & 3);
             if (m < m_hi && col < p.N) {
-                const int64_t at = ec * p.sC + m * p.ldc + col;
+                const int64_t at = ec * p.sC + (p.c_turned ? col * p.ldc + m : m * p.ldc + col);
                 const int left = p.N - col < 4 ? int(p.N - col) : 4;
                 v *= p.alpha;
                 const float x[4] = {v[0], v[1], v[2], v[3]};
-                if (p.out == 0) store_columns<0, 4>(p, static_cast<char *>(p.C), at, x, left);
-                else if (p.out == 1) store_columns<1, 4>(p, static_cast<char *>(p.C), at, x, left);
-                else store_columns<2, 4>(p, static_cast<char *>(p.C), at, x, left);
+                auto store = [&](int64_t to, const float *y, int n) {
+                    if (p.out == 0) store_columns<0, 4>(p, static_cast<char *>(p.C), to, y, n);
+                    else if (p.out == 1) store_columns<1, 4>(p, static_cast<char *>(p.C), to, y, n);
+                    else store_columns<2, 4>(p, static_cast<char *>(p.C), to, y, n);
+                };
+                if (!p.c_turned) {
+                    store(at, x, left);
+                } else {
+                    for (int r = 0; r < left; ++r) store(at + r * p.ldc, x + r, 1);
+                }
             }
         }
     }
@@ -651,7 +678,8 @@ hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
         const int64_t more = p.batch < p.M ? p.batch : p.M;
         tiles_m = p.M / BM + more < p.M ? p.M / BM + more : p.M;
     }
-    a.grid = TileGrid{tiles_m, (p.N + BN - 1) / BN, p.segments == Segments::Rows ? 1 : p.batch, 8, 8};
+    a.grid = TileGrid{tiles_m, (p.N + BN - 1) / BN, p.segments == Segments::Rows ? 1 : p.batch, 8,
+                      p.segments == Segments::Contracted ? 0 : 8};
     if (a.grid.tiles_m > 0x7fffffff || a.grid.tiles_n > 0x7fffffff || a.grid.per_batch() > 0x7fffffff ||
         p.batch > 0x7fffffff || a.grid.count() > 0x7fffffff)
         return hipErrorInvalidConfiguration;
@@ -693,20 +721,63 @@ LIBGEMM_BLOCK_FORMATS(3, 1, 1)
 #endif
 
 #if LIBGEMM_BLOCK_PART <= 0
+namespace {
+
+// Tiles of `side` x `side` of a problem (with segments of rows: about as many).
+int64_t tiles_of(const BlockProblem &p, int64_t M, int64_t N, int64_t side) {
+    return ((M + side - 1) / side) * ((N + side - 1) / side) * (p.segments == Segments::Rows ? 1 : p.batch);
+}
+
+// Rows or columns past the last whole 256 that are few enough for the few-rows kernel.
+int64_t edge_of(int64_t n) { return n > 256 && n % 256 <= 64 ? n % 256 : 0; }
+
+// Rows and columns of C that leave the 256 x 256 tiles and run by themselves:
+// a tile that holds few of them takes as long as a whole one, so where they
+// cost a wave of 256 tiles (13 us and more) the few-rows kernel is cheaper
+// (about 5 us for each of the two edges).
+void edges_of(const BlockProblem &p, int64_t &rows, int64_t &cols) {
+    rows = cols = 0;
+    if (p.segments != Segments::None) return;
+    auto waves = [&](int64_t M, int64_t N) { return (tiles_of(p, M, N, 256) + 255) / 256; };
+    const int64_t er = edge_of(p.M), ec = edge_of(p.N), whole = waves(p.M, p.N);
+    if (waves(p.M, p.N - ec) < whole) cols = ec;
+    else if (waves(p.M - er, p.N) < whole) rows = er;
+    else if (waves(p.M - er, p.N - ec) < whole) rows = er, cols = ec;
+}
+
+hipError_t launch_formats(BlockKernel k, const BlockProblem &p, hipStream_t stream) {
+    if (p.a.e5m2) return p.b.e5m2 ? block_tile_formats<1, 1>(k, p, stream) : block_tile_formats<1, 0>(k, p, stream);
+    return p.b.e5m2 ? block_tile_formats<0, 1>(k, p, stream) : block_tile_formats<0, 0>(k, p, stream);
+}
+
+BlockKernel few_for(int64_t rows) {
+    return rows <= 16 ? BlockKernel::Few16 : rows <= 32 ? BlockKernel::Few32 : BlockKernel::Few64;
+}
+
+BlockOperand from_row(BlockOperand o, int64_t row) {  // row: a multiple of 128
+    o.x += row * o.ld;
+    o.s += row >> o.shift;
+    return o;
+}
+
+}  // namespace
+
 BlockKernel block_choose(const BlockProblem &p, bool tiles_only) {
     if (p.M == 0 || p.N == 0 || p.batch == 0) return BlockKernel::None;
     // rows of C that share a B: all of them, or an expert's share
     const int64_t rows = p.segments == Segments::Rows ? (p.M + p.batch - 1) / p.batch : p.M;
-    if (!tiles_only && p.segments != Segments::Contracted && rows <= 64)
-        return rows <= 16 ? BlockKernel::Few16 : rows <= 32 ? BlockKernel::Few32 : BlockKernel::Few64;
-    const int64_t tiles = ((p.M + 255) / 256) * ((p.N + 255) / 256) * (p.segments == Segments::Rows ? 1 : p.batch);
-    return tiles >= 192 ? BlockKernel::Tile256 : BlockKernel::Tile128;
+    if (!tiles_only && p.segments != Segments::Contracted && rows <= 64) return few_for(rows);
+    if (tiles_of(p, p.M, p.N, 256) < 192) return BlockKernel::Tile128;
+    int64_t er = 0, ec = 0;
+    if (!tiles_only) edges_of(p, er, ec);
+    return er + ec > 0 ? BlockKernel::Tile256Edge : BlockKernel::Tile256;
 }
 
 const char *block_kernel_name(BlockKernel k) {
     switch (k) {
     case BlockKernel::None: return "";
     case BlockKernel::Tile256: return "f8block_mfma_256";
+    case BlockKernel::Tile256Edge: return "f8block_mfma_256_edge";
     case BlockKernel::Few16: return "f8block_few_16";
     case BlockKernel::Few32: return "f8block_few_32";
     case BlockKernel::Few64: return "f8block_few_64";
@@ -717,8 +788,31 @@ const char *block_kernel_name(BlockKernel k) {
 
 hipError_t launch_block(BlockKernel k, const BlockProblem &p, hipStream_t stream) {
     if (k == BlockKernel::None) return hipSuccess;
-    if (p.a.e5m2) return p.b.e5m2 ? block_tile_formats<1, 1>(k, p, stream) : block_tile_formats<1, 0>(k, p, stream);
-    return p.b.e5m2 ? block_tile_formats<0, 1>(k, p, stream) : block_tile_formats<0, 0>(k, p, stream);
+    if (k != BlockKernel::Tile256Edge) return launch_formats(k, p, stream);
+    int64_t er, ec;
+    edges_of(p, er, ec);
+    const int64_t M = p.M - er, N = p.N - ec, esize = p.out == 0 ? 4 : 2;
+    BlockProblem q = p;
+    q.M = M;
+    q.N = N;
+    hipError_t e = launch_formats(BlockKernel::Tile256, q, stream);
+    if (e == hipSuccess && er > 0) {  // the last rows, of the tiles' columns
+        q.M = er;
+        if (p.K > 0) q.a = from_row(p.a, M);
+        q.C = static_cast<char *>(p.C) + M * p.ldc * esize;
+        e = launch_formats(few_for(er), q, stream);
+    }
+    if (e == hipSuccess && ec > 0) {  // the last columns, of all rows: as rows of the transpose
+        q = p;
+        q.M = ec;
+        q.N = p.M;
+        q.a = p.K > 0 ? from_row(p.b, N) : p.b;
+        q.b = p.a;
+        q.C = static_cast<char *>(p.C) + N * esize;
+        q.c_turned = true;
+        e = launch_formats(few_for(ec), q, stream);
+    }
+    return e;
 }
 #endif
 

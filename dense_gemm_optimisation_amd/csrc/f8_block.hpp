@@ -36,11 +36,12 @@ struct BlockProblem {
     void *C;
     int64_t ldc, sC;
     int out;  // 0 fp32, 1 bf16, 2 fp16
+    bool c_turned;           // C(i, j) at C[j*ldc + i] (few rows only)
     int64_t batch;           // slices; with segments, the experts
     const int32_t *offsets;  // batch + 1, with segments
 };
 
-enum class BlockKernel { None, Tile256, Tile128, Few16, Few32, Few64 };
+enum class BlockKernel { None, Tile256, Tile256Edge, Tile128, Few16, Few32, Few64 };
 BlockKernel block_choose(const BlockProblem &p, bool tiles_only);
 const char *block_kernel_name(BlockKernel k);
 hipError_t launch_block(BlockKernel k, const BlockProblem &p, hipStream_t stream);

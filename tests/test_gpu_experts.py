@@ -151,11 +151,17 @@ def test_product_column_major_and_batched(lib, kernels, M, N, K, blocks):
 @pytest.mark.parametrize("M,N,K,batch,kernel", [
     (1, 40, 300, 1, "f8block_few_16"), (20, 40, 300, 1, "f8block_few_32"), (64, 40, 300, 3, "f8block_few_64"),
     (65, 40, 300, 1, "f8block_mfma_128"), (3500, 3600, 401, 1, "f8block_mfma_256"), (70, 90, 650, 200, "f8block_mfma_256"),
+    (3840, 4353, 272, 1, "f8block_mfma_256_edge"), (4144, 3900, 300, 1, "f8block_mfma_256_edge"),
+    (4097, 4100, 129, 1, "f8block_mfma_256_edge"), (2049, 2049, 100, 4, "f8block_mfma_256_edge"),
+    (4097, 4100, 0, 1, "f8block_mfma_256_edge"),
 ])
 @pytest.mark.parametrize("blocks", [(1, 128), (1, 1)])
 def test_product_kernels(lib, M, N, K, batch, kernel, blocks):
     rng = np.random.default_rng(M)
-    product(lib, rng, M, N, K, block_a=blocks[0], block_b=blocks[1], batch=batch, out="f32", kernel=kernel)
+    product(lib, rng, M, N, K, "e5m2", block_a=blocks[0], block_b=blocks[1], batch=batch, out="f32", kernel=kernel)
+    if kernel.endswith("edge"):
+        product(lib, rng, M, N, K, block_a=blocks[1], block_b=blocks[0], out="f16", kernel=kernel if batch == 1 else None,
+                alpha=2.0, beta=1.0, order="col")
 
 
 @pytest.mark.parametrize("M,N", [(3, 20), (70, 300)])
