@@ -153,6 +153,54 @@ __device__ inline float wave_sum(float x) {
     x += moved<0x143, 0xc>(0.0f, x);
     return lane_of(x, 63);
 }
+__device__ inline int moved_int(int x, int by) {  // row_ror
+    return by == 1   ? __builtin_amdgcn_update_dpp(0, x, 0x121, 0xf, 0xf, true)
+           : by == 2 ? __builtin_amdgcn_update_dpp(0, x, 0x122, 0xf, 0xf, true)
+           : by == 4 ? __builtin_amdgcn_update_dpp(0, x, 0x124, 0xf, 0xf, true)
+                     : __builtin_amdgcn_update_dpp(0, x, 0x128, 0xf, 0xf, true);
+}
+__device__ inline float turned(float x, int by) {
+    return __builtin_bit_cast(float, moved_int(__builtin_bit_cast(int, x), by));
+}
+
+// The lanes that share a token: a whole wave, or a row of 16 lanes of the
+// data-parallel moves, four tokens to a wave.
+template <int WIDTH>
+struct Team;
+template <>
+struct Team<64> {
+    static __device__ float max(float x) { return wave_max(x); }
+    static __device__ float sum(float x) { return wave_sum(x); }
+    static __device__ unsigned long long ballot(bool b, int) { return __ballot(b); }
+    static __device__ float of(float x, int i, int) { return lane_of(x, i); }
+    // x of the first lane where b is set (in one it is).
+    static __device__ int first(bool b, int x) { return __builtin_amdgcn_readlane(x, __builtin_ctzll(__ballot(b))); }
+};
+template <>
+struct Team<16> {
+    static __device__ float max(float x) {
+        x = fmaxf(x, turned(x, 1));
+        x = fmaxf(x, turned(x, 2));
+        x = fmaxf(x, turned(x, 4));
+        return fmaxf(x, turned(x, 8));
+    }
+    static __device__ float sum(float x) {
+        x += turned(x, 1);
+        x += turned(x, 2);
+        x += turned(x, 4);
+        return x + turned(x, 8);
+    }
+    static __device__ unsigned long long ballot(bool b, int lane) { return __ballot(b) >> (lane & 48) & 0xffff; }
+    static __device__ float of(float x, int i, int lane) { return __shfl(x, (lane & 48) + i); }
+    static __device__ int first(bool b, int x) {  // x rises with the lane
+        auto min = [](int p, int q) { return p < q ? p : q; };
+        x = b ? x : 0x7fffffff;
+        x = min(x, moved_int(x, 1));
+        x = min(x, moved_int(x, 2));
+        x = min(x, moved_int(x, 4));
+        return min(x, moved_int(x, 8));
+    }
+};
 
 // e^(a - b) with the rounding of the difference put back.
 __device__ inline float exp_difference(float a, float b) {
@@ -164,37 +212,40 @@ __device__ inline float exp_difference(float a, float b) {
 
 // ---- in 64 bits
 
-struct Best {
-    double key;
-    int at;
-};
-constexpr int NOBODY = 1 << 30;
-// The larger key; of equal ones the lower index.
-__device__ inline Best better(Best a, Best b) {
-    return b.key > a.key || (b.key == a.key && b.at < a.at) ? b : a;
+// The largest x of the wave, and the first lane that has it.  A double is the
+// sum of three floats, each the rest's nearest: they order as it does, so the
+// largest is found by three reductions of floats, which are far quicker than
+// one of doubles.
+__device__ inline double wave_max(double x, int &owner) {
+    const float a = float(x);
+    const bool whole = !(a > -INFINITY && a < INFINITY);
+    const double rest = whole ? 0.0 : x - double(a);
+    const float b = float(rest), c = float(rest - double(b));
+    const float top_a = wave_max(a);
+    const float top_b = wave_max(a == top_a ? b : NONE);
+    const float top_c = wave_max(a == top_a && b == top_b ? c : NONE);
+    owner = __builtin_ctzll(__ballot(a == top_a && b == top_b && c == top_c));
+    return double(top_a) + (double(top_b) + double(top_c));
 }
-__device__ inline Best wave_best(Best x) {
-#pragma unroll
-    for (int d = 1; d < LANES; d <<= 1) x = better(x, Best{__shfl_xor(x.key, d), __shfl_xor(x.at, d)});
-    return x;
+__device__ inline double lane_of(double x, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(b), lane), hi = __builtin_amdgcn_readlane(uint32_t(b >> 32), lane);
+    return __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
 }
 
-// Lane j's choice (or -1) of a token whose scores are defined.
+// Lane j's choice (or -1) of a token whose scores are defined, over a whole wave.
 template <int PER>
 __device__ int choose_exactly(const RouteArgs &a, const float (&l)[PER], int lane) {
     const double none = -INFINITY;
     const int E = a.experts, first_e = lane * PER;
-    double key[PER], top = none, sum = 0.0;
+    double key[PER], sum = 0.0;
+    float top = NONE;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) top = double(l[i]) > top ? double(l[i]) : top;
+    for (int i = 0; i < PER; ++i) top = fmaxf(top, l[i]);
     if (!a.sigmoid) {
+        top = wave_max(top);
 #pragma unroll
-        for (int d = 1; d < LANES; d <<= 1) {
-            const double o = __shfl_xor(top, d);
-            top = o > top ? o : top;
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) sum += l[i] > NONE ? exp(double(l[i]) - top) : 0.0;
+        for (int i = 0; i < PER; ++i) sum += l[i] > NONE ? exp(double(l[i]) - double(top)) : 0.0;
 #pragma unroll
         for (int d = 1; d < LANES; d <<= 1) sum += __shfl_xor(sum, d);
     }
@@ -203,36 +254,55 @@ __device__ int choose_exactly(const RouteArgs &a, const float (&l)[PER], int lan
         key[i] = none;
         if (!(l[i] > NONE)) continue;
         const double x = l[i];
-        key[i] = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum;
+        key[i] = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - double(top)) / sum;
         if (a.bias != nullptr) key[i] += double(a.bias[first_e + i]);
         if (!(key[i] > none)) key[i] = none;
     }
+    int owner;
     if (a.groups > 1) {
-        const int per = E / a.groups;
+        const int per = E / a.groups, width = per / PER;
         double rank = none;  // lane g's is group g's
-        for (int g = 0; g < a.groups; ++g) {
-            Best first{none, NOBODY}, second{none, NOBODY};
+        auto largest = [](double x, double y) { return x > y ? x : y; };
+        auto smallest = [](double x, double y) { return x > y ? y : x; };
+        if (per % PER == 0 && (width & (width - 1)) == 0) {
+            double first = none, second = none;
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if ((first_e + i) / per == g && key[i] > none) first = better(first, Best{key[i], first_e + i});
-            first = wave_best(first);
-            double r = first.key;
-            if (a.group_top == 2) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    if ((first_e + i) / per == g && first_e + i != first.at && key[i] > none)
-                        second = better(second, Best{key[i], first_e + i});
-                second = wave_best(second);
-                if (second.key > none) r += second.key;
+            for (int i = 0; i < PER; ++i) {
+                second = largest(second, smallest(first, key[i]));
+                first = largest(first, key[i]);
             }
-            if (lane == g) rank = r;
+            for (int d = 1; d < width; d <<= 1) {
+                const double f = __shfl_xor(first, d), s = __shfl_xor(second, d);
+                second = largest(largest(second, s), smallest(first, f));
+                first = largest(first, f);
+            }
+            if (a.group_top == 2 && second > none) first += second;
+            rank = __shfl(first, lane * width & 63);
+            if (lane >= a.groups) rank = none;
+        } else {
+            for (int g = 0; g < a.groups; ++g) {
+                double first = none, second = none;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const double k = (first_e + i) / per == g ? key[i] : none;
+                    second = largest(second, smallest(first, k));
+                    first = largest(first, k);
+                }
+                double r = wave_max(first, owner);
+                if (a.group_top == 2) {
+                    int unused;
+                    const double s = wave_max(lane == owner ? second : first, unused);
+                    if (s > none) r += s;
+                }
+                if (lane == g) rank = r;
+            }
         }
-        unsigned long long kept = 0;
-        for (int n = 0; n < a.top_groups; ++n) {
-            const Best b = wave_best(Best{rank, lane < a.groups && !(kept >> lane & 1) ? lane : NOBODY + lane});
-            if (b.at < NOBODY) kept |= 1ull << b.at;  // groups with nobody come last and hold nobody
-            if (lane == b.at) rank = none;
+        int ahead = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const double r = lane_of(rank, g);
+            ahead += r > rank || (r == rank && g < lane);
         }
+        const unsigned long long kept = __ballot(lane < a.groups && ahead < a.top_groups);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (first_e + i < E && !(kept >> ((first_e + i) / per) & 1)) key[i] = none;
@@ -243,27 +313,37 @@ __device__ int choose_exactly(const RouteArgs &a, const float (&l)[PER], int lan
     }
     int id = -1;
     for (int j = 0; j < a.top_k; ++j) {
-        Best b{none, NOBODY};
+        double mine = key[0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) mine = key[i] > mine ? key[i] : mine;
+        const double m = wave_max(mine, owner);
+        if (!(m > none)) break;
+        int at = 0;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) at = key[i] == mine ? i : at;
+        const int e = __builtin_amdgcn_readlane(first_e + at, owner);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (key[i] > none) b = better(b, Best{key[i], first_e + i});
-        b = wave_best(b);
-        if (b.at == NOBODY) break;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (first_e + i == b.at) key[i] = none;
-        if (lane == j) id = b.at;
+            if (first_e + i == e) key[i] = none;
+        if (lane == j) id = e;
     }
     return id;
 }
 
 // ---- in 32 bits
 
-// The rank of group `lane` (its group_top largest keys' sum), -infinity in lanes without one.
-template <int PER>
-__device__ inline float group_ranks(const RouteArgs &a, const float (&key)[PER], int lane) {
-    const int per = a.experts / a.groups;
-    const int width = per / PER;
+// The rank of group `place` of the team (its group_top largest keys' sum),
+// -infinity in places without one, and what its error goes by.
+template <int PER, int WIDTH>
+__device__ inline void group_ranks(const RouteArgs &a, const float (&key)[PER], int lane, float &rank, float &size) {
+    using T = Team<WIDTH>;
+    const int place = lane & (WIDTH - 1);
+    const int per = a.experts / a.groups, width = per / PER;
+    auto join = [&](float first, float second, float &r, float &z) {
+        const bool two = a.group_top == 2 && second > NONE;
+        r = two ? first + second : first;
+        z = first > NONE ? fabsf(first) + (two ? fabsf(second) : 0.0f) : 0.0f;
+    };
     if (per % PER == 0 && width <= 16 && (width & (width - 1)) == 0) {
         // a group is `width` lanes, a power of two: its two largest come together in log2 steps
         float first = NONE, second = NONE;
@@ -277,37 +357,49 @@ __device__ inline float group_ranks(const RouteArgs &a, const float (&key)[PER],
             second = fmaxf(fmaxf(second, s), fminf(first, f));
             first = fmaxf(first, f);
         }
-        if (a.group_top == 2 && second > NONE) first += second;
-        const float r = __shfl(first, lane * width & 63);
-        return lane < a.groups ? r : NONE;
+        float r, z;
+        join(first, second, r, z);
+        const int from = (lane & ~(WIDTH - 1)) + (place * width & (WIDTH - 1));
+        r = __shfl(r, from);
+        z = __shfl(z, from);
+        rank = place < a.groups ? r : NONE;
+        size = z;
+        return;
     }
-    float rank = NONE;
+    rank = NONE;
+    size = 0.0f;
     for (int g = 0; g < a.groups; ++g) {
         float first = NONE, second = NONE;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const float k = (lane * PER + i) / per == g ? key[i] : NONE;
+            const float k = (place * PER + i) / per == g ? key[i] : NONE;
             second = fmaxf(second, fminf(first, k));
             first = fmaxf(first, k);
         }
-        const float m = wave_max(first);
-        const int at = __builtin_ctzll(__ballot(first == m));
-        const float s = wave_max(lane == at ? second : first);
-        const float r = a.group_top == 2 && s > NONE ? m + s : m;
-        if (lane == g) rank = r;
+        const float m = T::max(first);
+        const int at = T::first(first == m, place);
+        const float s = T::max(place == at ? second : first);
+        float r, z;
+        join(m, s, r, z);
+        if (place == g) {
+            rank = r;
+            size = z;
+        }
     }
-    return rank;
 }
 
-// Chooses for token t: lane j gets choice j and its weight.
-template <int PER>
-__device__ inline void choose(const RouteArgs &a, int64_t t, int lane, bool whole, int &id, float &w) {
-    const int E = a.experts, first_e = lane * PER;
+// Chooses for token t (in a team without one, live is not set): place j of
+// the team gets choice j and its weight.
+template <int PER, int WIDTH>
+__device__ inline void choose(const RouteArgs &a, int64_t t, bool live, int lane, bool whole, int &id, float &w) {
+    using T = Team<WIDTH>;
+    const int E = a.experts, place = lane & (WIDTH - 1), first_e = place * PER;
     id = -1;
     w = 0.0f;
-    if (a.keep != nullptr && a.keep[t] == 0) return;
+    if (live && a.keep != nullptr) live = a.keep[t] != 0;
+    if (WIDTH == 64 && !live) return;
     float l[PER], key[PER];
-    load_logits<PER>(a.logits, t * a.ldl + first_e, a.type, E - first_e, whole, l);
+    load_logits<PER>(a.logits, t * a.ldl + first_e, a.type, live ? E - first_e : 0, whole, l);
     float top = NONE;
     bool odd = false;
 #pragma unroll
@@ -317,21 +409,29 @@ __device__ inline void choose(const RouteArgs &a, int64_t t, int lane, bool whol
         top = fmaxf(top, l[i]);
     }
     float sum = 0.0f;
+    bool undefined = false;
     if (!a.sigmoid) {
-        if (__ballot(odd) != 0) {
-            w = __builtin_nanf("");
-            return;
+        undefined = T::ballot(odd, lane) != 0;
+        if (undefined) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) l[i] = NONE;
+            top = NONE;
         }
-        top = wave_max(top);
+        top = T::max(top);
         if (a.bias != nullptr || !a.renormalise || (a.groups > 1 && a.group_top == 2)) {
 #pragma unroll
             for (int i = 0; i < PER; ++i) sum += l[i] > NONE ? expf(l[i] - top) : 0.0f;
-            sum = wave_sum(sum);
+            sum = T::sum(sum);
         }
     }
-    // The error of a key is below `off` times the largest score plus its own
-    // size: a few roundings, and under softmax the sum's PER + 6.
-    const float off = (a.sigmoid ? 8.0f : PER + 16.0f) * 0x1p-24f;
+    // The error of a key is below off * (the largest score + its own size).
+    // Sigmoid: e^-l within 1 ulp, 1 + e and the quotient rounded: 2 steps of
+    // 2^-24 at most in a score of 1, and one of the sum with the bias.
+    // Softmax: per score the rounding of l - top (weighted by e^(l - top), at
+    // most 0.4 steps), e within 2, the quotient, and the sum: 2 per term, 7 for
+    // the terms' arguments (their mean is the entropy, at most ln 1024) and
+    // PER + 6 additions.
+    const float off = (a.sigmoid ? 2.25f : PER + 20.0f) * 0x1p-24f;
     const float largest = a.sigmoid ? 1.0f : 1.0f / sum;
     const bool exact_keys = a.bias == nullptr;
     bool near = false;
@@ -348,21 +448,23 @@ __device__ inline void choose(const RouteArgs &a, int64_t t, int lane, bool whol
     }
     if (a.groups > 1) {
         const int per = E / a.groups;
-        const float rank = group_ranks<PER>(a, key, lane);
         const bool exact_ranks = exact_keys && a.group_top == 1;
+        float rank, size;
+        group_ranks<PER, WIDTH>(a, key, lane, rank, size);
+        const float error = off * (2.0f * largest + 2.0f * size);  // two keys, and their sum's rounding
         int ahead = 0;
         for (int g = 0; g < a.groups; ++g) {
-            const float r = lane_of(rank, g);
-            ahead += r > rank || (r == rank && g < lane);
-            if (!exact_ranks && g != lane && lane < a.groups && fabsf(r - rank) <= 4.0f * off * (largest + fabsf(r)))
+            const float r = T::of(rank, g, lane);
+            ahead += r > rank || (r == rank && g < place);
+            if (!exact_ranks && g != place && place < a.groups && fabsf(r - rank) <= error + T::of(error, g, lane))
                 near = true;
         }
-        const unsigned long long kept = __ballot(lane < a.groups && ahead < a.top_groups);
+        const unsigned long long kept = T::ballot(place < a.groups && ahead < a.top_groups, lane);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int g = (first_e + i) / per;
             const bool in = first_e + i < E && (kept >> (g & 63) & 1);
-            key[i] = !in ? NONE : exact_keys ? l[i] : key[i];
+            key[i] = !in || !(key[i] > NONE) ? NONE : exact_keys ? l[i] : key[i];
         }
     }
     float last = INFINITY;
@@ -371,47 +473,62 @@ __device__ inline void choose(const RouteArgs &a, int64_t t, int lane, bool whol
         float mine = key[0];
 #pragma unroll
         for (int i = 1; i < PER; ++i) mine = fmaxf(mine, key[i]);
-        const float m = wave_max(mine);
-        if (!(m > NONE)) break;
-        if (!exact_keys && last - m <= 2.0f * off * (largest + fabsf(m))) near = true;
+        const float m = T::max(mine);
+        if (WIDTH == 64 ? !(m > NONE) : __ballot(m > NONE) == 0) break;
+        if (!exact_keys && m > NONE && last - m <= 2.0f * off * (largest + fabsf(m))) near = true;
         last = m;
-        const int owner = __builtin_ctzll(__ballot(mine == m));
         int at = 0;
 #pragma unroll
         for (int i = PER - 1; i >= 0; --i) at = key[i] == m ? i : at;
-        const int e = __builtin_amdgcn_readlane(first_e + at, owner);
+        const int e = T::first(mine == m, first_e + at);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (first_e + i == e) key[i] = NONE;
-        if (lane == j) id = e;
+        if (place == j && m > NONE) id = e;
     }
-    if (lane >= a.top_k) id = -1;
-    if (__ballot(near) != 0) id = choose_exactly<PER>(a, l, lane);
+    if (place >= a.top_k) id = -1;
+    unsigned long long again = __ballot(near);
+    if (again != 0) {
+        constexpr int PER64 = PER * WIDTH / 64 > 0 ? PER * WIDTH / 64 : 1;
+        for (int team = 0; team < 64 / WIDTH; ++team) {
+            if ((again >> (team * (WIDTH & 63)) & (WIDTH == 64 ? ~0ull : 0xffffull)) == 0) continue;
+            const int64_t token = __shfl(t, team * (WIDTH & 63));
+            float x[PER64];
+            load_logits<PER64>(a.logits, token * a.ldl + lane * PER64, a.type, E - lane * PER64, false, x);
+#pragma unroll
+            for (int i = 0; i < PER64; ++i) x[i] = x[i] > NONE ? x[i] : NONE;
+            const int chosen = choose_exactly<PER64>(a, x, lane);
+            const int mine = __shfl(chosen, place);
+            if (lane / WIDTH == team) id = mine;
+        }
+    }
 
     const float x = id >= 0 ? load_logit(a.logits, t * a.ldl + id, a.type) : NONE;
     if (a.sigmoid) {
         w = id >= 0 ? 1.0f / (1.0f + expf(-x)) : 0.0f;
     } else {
         // renormalised: relative to the largest chosen, so the sum cannot vanish
-        if (a.renormalise) top = wave_max(x);
+        if (a.renormalise) top = T::max(x);
         w = id >= 0 ? exp_difference(x, top) : 0.0f;
-        if (!a.renormalise) w /= sum;
+        if (!a.renormalise && id >= 0) w /= sum;
     }
     if (a.renormalise) {
-        const float total = wave_sum(w);
+        const float total = T::sum(w);
         w = total > 0.0f ? w / total : 0.0f;
     }
     w *= a.scale;
     if (id < 0) w = 0.0f;
+    if (undefined) w = __builtin_nanf("");
 }
 
-// `span` consecutive tokens per workgroup, its waves taking them in turn.
+// `span` consecutive tokens per workgroup, its teams taking them in turn.
 // With counts: counts[workgroup][expert], the tokens of the span that chose it.
-template <int PER>
+template <int PER, int WIDTH>
 __global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a, int span, uint8_t *counts) {
     __shared__ uint32_t count[ROUTE_MAX_EXPERTS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
+    constexpr int TEAMS = 64 / WIDTH;  // per wave
+    const int step = (blockDim.x >> 6) * TEAMS, place = lane & (WIDTH - 1);
     if (counts != nullptr) {
         for (int e = threadIdx.x; e < a.experts; e += blockDim.x) count[e] = 0;
         __syncthreads();
@@ -419,15 +536,17 @@ __global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a, int span, uin
     // rows of logits that start where their vectors are aligned
     const int64_t bytes = int64_t(PER < 4 ? PER : 4) * 4;
     const bool whole = (reinterpret_cast<uintptr_t>(a.logits) | uint64_t(a.ldl * (a.type == 0 ? 4 : 2))) % bytes == 0;
-    for (int i = wave; i < span; i += waves) {
-        const int64_t t = int64_t(blockIdx.x) * span + i;
-        if (t >= a.tokens) break;
+    for (int i = wave * TEAMS; i < span; i += step) {
+        const int64_t t0 = int64_t(blockIdx.x) * span + i;
+        if (t0 >= a.tokens) break;
+        const int64_t t = TEAMS == 1 ? t0 : t0 + lane / WIDTH;
+        const bool live = TEAMS == 1 || (t < a.tokens && i + lane / WIDTH < span);
         int id;
         float w;
-        choose<PER>(a, t, lane, whole, id, w);
-        if (lane < a.top_k) {
-            a.ids[t * a.top_k + lane] = id;
-            a.weights[t * a.top_k + lane] = w;
+        choose<PER, WIDTH>(a, live ? t : t0, live, lane, whole, id, w);
+        if (live && place < a.top_k) {
+            a.ids[t * a.top_k + place] = id;
+            a.weights[t * a.top_k + place] = w;
             if (counts != nullptr && id >= 0) atomicAdd(&count[id], 1u);
         }
     }
@@ -623,32 +742,34 @@ __global__ __launch_bounds__(BACK_WAVES * 64) void route_backward_kernel(RouteBa
     store_logits<PER>(a.d_logits, t * a.ldd + first_e, a.type, E - first_e, aligned(a.d_logits, a.ldd), out);
 }
 
-template <int PER>
-hipError_t go(const RouteArgs &r, hipStream_t stream) {
+template <int PER, int WIDTH>
+hipError_t choose_go(const RouteArgs &r, int span, uint8_t *counts, hipStream_t stream) {
     RouteArgs a = r;
-    const bool layout = a.offsets != nullptr;
-    const int64_t blocks = (a.tokens + BLOCK - 1) / BLOCK;
-    // A workgroup's tokens: one per wave while that leaves most of the chip
-    // empty, four per wave (and counts of 64) beyond.
-    int span = a.tokens <= BLOCK ? 4 : a.tokens <= 4096 ? 16 : BLOCK;
-    int waves = span < 16 ? span : 16;
-    uint8_t *counts = layout && a.tokens > BLOCK ? static_cast<uint8_t *>(a.workspace) : nullptr;
-    if (a.tokens > 0) {
-        const int64_t grid = (a.tokens + span - 1) / span;
-        if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
-        void *args[] = {&a, &span, &counts};
-        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&choose_kernel<PER>), dim3(unsigned(grid)),
-                                             dim3(unsigned(waves) * 64), args, 0, stream);
-        if (e != hipSuccess) return e;
+    const int64_t grid = (a.tokens + span - 1) / span;
+    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+    const int tokens_per_wave = 64 / WIDTH, waves = (span + tokens_per_wave - 1) / tokens_per_wave;
+    void *args[] = {&a, &span, &counts};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&choose_kernel<PER, WIDTH>), dim3(unsigned(grid)),
+                           dim3(unsigned(waves < 16 ? waves : 16) * 64), args, 0, stream);
+}
+
+#ifndef ROUTE_TEAMS_FROM
+#define ROUTE_TEAMS_FROM 512
+#endif
+hipError_t choose_by_size(const RouteArgs &a, int span, uint8_t *counts, hipStream_t stream) {
+    // four tokens per wave once there are tokens for every compute unit
+    if (a.tokens >= ROUTE_TEAMS_FROM && a.experts <= 256 && a.top_k <= 16 && a.groups <= 16) {
+        if (a.experts <= 16) return choose_go<1, 16>(a, span, counts, stream);
+        if (a.experts <= 32) return choose_go<2, 16>(a, span, counts, stream);
+        if (a.experts <= 64) return choose_go<4, 16>(a, span, counts, stream);
+        if (a.experts <= 128) return choose_go<8, 16>(a, span, counts, stream);
+        return choose_go<16, 16>(a, span, counts, stream);
     }
-    if (!layout) return hipSuccess;
-    // every workgroup reads all counts: at most 256 of them, so that this does not grow with the square
-    int64_t own = (blocks + 255) / 256;
-    if (own < 1) own = 1;
-    const int64_t grid = blocks > 0 ? (blocks + own - 1) / own : 1;
-    const uint8_t *read = counts;
-    void *args[] = {&a, &own, &span, &read};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&place_kernel), dim3(unsigned(grid)), dim3(1024), args, 0, stream);
+    if (a.experts <= 64) return choose_go<1, 64>(a, span, counts, stream);
+    if (a.experts <= 128) return choose_go<2, 64>(a, span, counts, stream);
+    if (a.experts <= 256) return choose_go<4, 64>(a, span, counts, stream);
+    if (a.experts <= 512) return choose_go<8, 64>(a, span, counts, stream);
+    return choose_go<16, 64>(a, span, counts, stream);
 }
 
 template <int PER>
@@ -661,22 +782,36 @@ hipError_t go(const RouteBackwardArgs &r, hipStream_t stream) {
                            dim3(BACK_WAVES * 64), args, 0, stream);
 }
 
-template <typename Args>
-hipError_t by_experts(const Args &a, hipStream_t stream) {
+}  // namespace
+
+hipError_t launch_route(const RouteArgs &r, hipStream_t stream) {
+    RouteArgs a = r;
+    const bool layout = a.offsets != nullptr;
+    const int64_t blocks = (a.tokens + BLOCK - 1) / BLOCK;
+    // A workgroup's tokens: few while that leaves most of the chip empty.
+    int span = a.tokens <= BLOCK ? 4 : a.tokens <= 4096 ? 16 : BLOCK;
+    uint8_t *counts = layout && a.tokens > BLOCK ? static_cast<uint8_t *>(a.workspace) : nullptr;
+    if (a.tokens > 0) {
+        const hipError_t e = choose_by_size(a, span, counts, stream);
+        if (e != hipSuccess) return e;
+    }
+    if (!layout) return hipSuccess;
+    // every workgroup reads all counts: at most 256 of them, so that this does not grow with the square
+    int64_t own = (blocks + 255) / 256;
+    if (own < 1) own = 1;
+    const int64_t grid = blocks > 0 ? (blocks + own - 1) / own : 1;
+    const uint8_t *read = counts;
+    void *args[] = {&a, &own, &span, &read};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&place_kernel), dim3(unsigned(grid)), dim3(1024), args, 0, stream);
+}
+
+hipError_t launch_route_backward(const RouteBackwardArgs &a, hipStream_t stream) {
+    if (a.tokens == 0) return hipSuccess;
     if (a.experts <= 64) return go<1>(a, stream);
     if (a.experts <= 128) return go<2>(a, stream);
     if (a.experts <= 256) return go<4>(a, stream);
     if (a.experts <= 512) return go<8>(a, stream);
     return go<16>(a, stream);
-}
-
-}  // namespace
-
-hipError_t launch_route(const RouteArgs &a, hipStream_t stream) { return by_experts(a, stream); }
-
-hipError_t launch_route_backward(const RouteBackwardArgs &a, hipStream_t stream) {
-    if (a.tokens == 0) return hipSuccess;
-    return by_experts(a, stream);
 }
 
 size_t route_workspace(int64_t tokens, int64_t experts) {

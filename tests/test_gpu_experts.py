@@ -457,8 +457,8 @@ def route(lib, logits, top_k, bias=None, keep=None, sigmoid=False, groups=1, top
     return got, want_w
 
 
-@pytest.mark.parametrize("T", [1, 5, 64, 65, 300])
-@pytest.mark.parametrize("E,top_k", [(1, 1), (2, 1), (8, 2), (60, 4), (64, 6), (65, 32), (128, 8), (256, 8), (300, 3), (384, 8),
+@pytest.mark.parametrize("T", [1, 5, 64, 65, 300, 515])
+@pytest.mark.parametrize("E,top_k", [(1, 1), (2, 1), (8, 2), (24, 3), (60, 4), (64, 6), (65, 32), (128, 8), (256, 8), (300, 3), (384, 8),
                                      (1000, 10), (1024, 32)])
 def test_route(lib, T, E, top_k):
     rng = np.random.default_rng(T + E)
@@ -473,31 +473,34 @@ def test_route(lib, T, E, top_k):
                                                        (64, 64, 7, 7), (256, 2, 2, 8), (1024, 16, 1, 32), (60, 4, 3, 12)])
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("group_top", [1, 2])
-def test_route_groups(lib, E, groups, top_groups, top_k, sigmoid, group_top):
+@pytest.mark.parametrize("T", [130, 517])
+def test_route_groups(lib, T, E, groups, top_groups, top_k, sigmoid, group_top):
     rng = np.random.default_rng(E + groups)
-    x = torch.from_numpy(rng.normal(size=(130, E)) * 2).float()
+    x = torch.from_numpy(rng.normal(size=(T, E)) * 2).float()
     for bias in (None, rng.normal(size=E) * 0.2):
         route(lib, x, top_k, bias, sigmoid=sigmoid, groups=groups, top_groups=top_groups, group_top=group_top, align=8)
 
 
-def test_route_ties_and_near_ties(lib):
+@pytest.mark.parametrize("T", [70, 601])
+def test_route_ties_and_near_ties(lib, T):
     rng = np.random.default_rng(1)
-    same = torch.zeros(70, 96)
+    same = torch.zeros(T, 96)
     route(lib, same, 8)
     route(lib, same, 8, sigmoid=True, bias=np.zeros(96), groups=8, top_groups=3, group_top=2)
     # scores whose sum with the bias differ far below fp32's step at their size
-    x = torch.from_numpy(rng.normal(size=(200, 64)) * 1e-7).float()
+    x = torch.from_numpy(rng.normal(size=(T, 64)) * 1e-7).float()
     route(lib, x, 8, np.zeros(64) + 0.25, sigmoid=True)
     route(lib, x, 8, np.zeros(64), groups=8, top_groups=4, group_top=2)
     route(lib, x, 8, np.zeros(64), sigmoid=True, groups=8, top_groups=4, group_top=2)
-    steps = torch.from_numpy(rng.integers(0, 3, (200, 64)) * 2.0 ** -22 + 1.0).float()
+    steps = torch.from_numpy(rng.integers(0, 3, (T, 64)) * 2.0 ** -22 + 1.0).float()
     route(lib, steps, 8, np.zeros(64), sigmoid=True, groups=4, top_groups=2, group_top=1)
     route(lib, steps, 8, rng.integers(0, 2, 64) * 1e-8, groups=4, top_groups=2, group_top=2)
 
 
-def test_route_masked(lib):
+@pytest.mark.parametrize("T", [40, 530])
+def test_route_masked(lib, T):
     rng = np.random.default_rng(2)
-    x = torch.from_numpy(rng.normal(size=(40, 64))).float()
+    x = torch.from_numpy(rng.normal(size=(T, 64))).float()
     x[0] = -float("inf")
     x[1, 1:] = -float("inf")
     x[2, 3:] = -float("inf")
@@ -520,7 +523,7 @@ def test_route_masked(lib):
     route(lib, x, 6, bias, sigmoid=True)
 
 
-@pytest.mark.parametrize("T", [1, 64, 200])
+@pytest.mark.parametrize("T", [1, 64, 200, 700])
 def test_route_padding(lib, T):
     rng = np.random.default_rng(T)
     x = torch.from_numpy(rng.normal(size=(T, 32))).float()
