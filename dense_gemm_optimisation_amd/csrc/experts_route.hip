@@ -172,7 +172,9 @@ struct Team<64> {
     static __device__ float max(float x) { return wave_max(x); }
     static __device__ float sum(float x) { return wave_sum(x); }
     static __device__ unsigned long long ballot(bool b, int) { return __ballot(b); }
+    // x of place i.
     static __device__ float of(float x, int i, int) { return lane_of(x, i); }
+    static __device__ int of(int x, int i, int) { return __builtin_amdgcn_readlane(x, i); }
     // x of the first lane where b is set (in one it is).
     static __device__ int first(bool b, int x) { return __builtin_amdgcn_readlane(x, __builtin_ctzll(__ballot(b))); }
 };
@@ -192,6 +194,7 @@ struct Team<16> {
     }
     static __device__ unsigned long long ballot(bool b, int lane) { return __ballot(b) >> (lane & 48) & 0xffff; }
     static __device__ float of(float x, int i, int lane) { return __shfl(x, (lane & 48) + i); }
+    static __device__ int of(int x, int i, int lane) { return __shfl(x, (lane & 48) + i); }
     static __device__ int first(bool b, int x) {  // x rises with the lane
         auto min = [](int p, int q) { return p < q ? p : q; };
         x = b ? x : 0x7fffffff;
@@ -679,35 +682,47 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a, int64_t own, i
 //   renormalised, S the sum of the chosen p: dp_i = (g_i - sum_j g_j p_j / S) / S for the chosen
 //   sigmoid: dl_i = dp_i p_i (1 - p_i);  softmax: dl_i = p_i (dp_i - sum_j dp_j p_j)
 constexpr int BACK_WAVES = 4;
-template <int PER>
+template <int PER, int WIDTH>
 __global__ __launch_bounds__(BACK_WAVES * 64) void route_backward_kernel(RouteBackwardArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = int64_t(blockIdx.x) * BACK_WAVES + (threadIdx.x >> 6);
-    if (t >= a.tokens) return;
-    const int E = a.experts, first_e = lane * PER;
+    using T = Team<WIDTH>;
+    constexpr int TEAMS = 64 / WIDTH;  // tokens per wave
+    const int lane = threadIdx.x & 63, place = lane & (WIDTH - 1);
+    const int64_t t0 = (int64_t(blockIdx.x) * BACK_WAVES + (threadIdx.x >> 6)) * TEAMS;
+    if (t0 >= a.tokens) return;
+    const bool live = t0 + lane / WIDTH < a.tokens;
+    const int64_t t = live ? t0 + lane / WIDTH : t0;
+    const int E = a.experts, first_e = place * PER;
     const int esize = a.type == 0 ? 4 : 2;
     const int64_t bytes = int64_t(PER < 4 ? PER : 4) * 4;
     auto aligned = [&](const void *x, int64_t ld) {
         return (reinterpret_cast<uintptr_t>(x) | uint64_t(ld * esize)) % bytes == 0;
     };
-    int id = lane < a.top_k ? a.ids[t * a.top_k + lane] : -1;
-    if (id < 0 || id >= E) id = -1;
-    const float g = id >= 0 ? a.scale * a.d_weights[t * a.top_k + lane] : 0.0f;
-    const bool any = __ballot(id >= 0) != 0;
-    const bool dense = !a.sigmoid && !a.renormalise && any;  // every logit has a gradient
+    // every logit has a gradient: they are on their way while the ids arrive
+    const bool dense = !a.sigmoid && !a.renormalise;
     float l[PER], top = NONE;
+    if (dense) {
+        load_logits<PER>(a.logits, t * a.ldl + first_e, a.type, E - first_e, aligned(a.logits, a.ldl), l);
+    } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) l[i] = NONE;
-    if (dense) load_logits<PER>(a.logits, t * a.ldl + first_e, a.type, E - first_e, aligned(a.logits, a.ldl), l);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) top = fmaxf(top, l[i]);
+        for (int i = 0; i < PER; ++i) l[i] = NONE;
+    }
+    int id = live && place < a.top_k ? a.ids[t * a.top_k + place] : -1;
+    float g = live && place < a.top_k ? a.d_weights[t * a.top_k + place] : 0.0f;
+    if (id < 0 || id >= E) id = -1;
+    g = id >= 0 ? a.scale * g : 0.0f;
+    const bool any = T::ballot(id >= 0, lane) != 0;
     const float mine = id >= 0 ? load_logit(a.logits, t * a.ldl + id, a.type) : NONE;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (!any) l[i] = NONE;  // nothing flows, whatever the logits are
+        top = fmaxf(top, l[i]);
+    }
     float p;
     if (a.sigmoid) {
         p = id >= 0 ? 1.0f / (1.0f + expf(-mine)) : 0.0f;
     } else {
         // renormalised, the other experts' scores cancel: only the chosen matter
-        top = wave_max(a.renormalise ? mine : top);
+        top = T::max(a.renormalise ? mine : top);
         p = id >= 0 ? expf(mine - top) : 0.0f;
         if (dense) {
             float sum = 0.0f;
@@ -716,7 +731,8 @@ __global__ __launch_bounds__(BACK_WAVES * 64) void route_backward_kernel(RouteBa
                 l[i] = l[i] > NONE ? expf(l[i] - top) : l[i] != l[i] ? l[i] : 0.0f;
                 sum += l[i];
             }
-            const float inverse = 1.0f / wave_sum(sum);
+            sum = T::sum(sum);
+            const float inverse = any ? 1.0f / sum : 0.0f;
             p *= inverse;
 #pragma unroll
             for (int i = 0; i < PER; ++i) l[i] *= inverse;
@@ -724,22 +740,32 @@ __global__ __launch_bounds__(BACK_WAVES * 64) void route_backward_kernel(RouteBa
     }
     float dp = g;
     if (a.renormalise) {
-        const float total = wave_sum(p);
-        const float mean = total > 0.0f ? wave_sum(g * p) / total : 0.0f;
-        dp = total > 0.0f ? (g - mean) / total : 0.0f;
+        const float total = T::sum(p), weighted = T::sum(g * p);
+        dp = total > 0.0f ? (g - weighted / total) / total : 0.0f;
     }
     const float d = a.sigmoid ? (id >= 0 ? dp * p * (1.0f / (1.0f + expf(mine))) : 0.0f) : dp * p;
-    const float inner = dense ? wave_sum(d) : 0.0f;
+    const float inner = dense ? T::sum(d) : 0.0f;
     float out[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) out[i] = dense ? -l[i] * inner : 0.0f;
     for (int j = 0; j < a.top_k; ++j) {
-        const int e = __builtin_amdgcn_readlane(id, j);
-        const float v = lane_of(d, j);
+        const int e = T::of(id, j, lane);
+        const float v = T::of(d, j, lane);
 #pragma unroll
         for (int i = 0; i < PER; ++i) out[i] += first_e + i == e ? v : 0.0f;
     }
-    store_logits<PER>(a.d_logits, t * a.ldd + first_e, a.type, E - first_e, aligned(a.d_logits, a.ldd), out);
+    store_logits<PER>(a.d_logits, t * a.ldd + first_e, a.type, live ? E - first_e : 0, aligned(a.d_logits, a.ldd), out);
+}
+
+template <int PER, int WIDTH>
+hipError_t back_go(const RouteBackwardArgs &r, hipStream_t stream) {
+    RouteBackwardArgs a = r;
+    constexpr int TOKENS = BACK_WAVES * 64 / WIDTH;
+    const int64_t blocks = (a.tokens + TOKENS - 1) / TOKENS;
+    if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
+    void *args[] = {&a};
+    return hipLaunchKernel(reinterpret_cast<const void *>(&route_backward_kernel<PER, WIDTH>), dim3(unsigned(blocks)),
+                           dim3(BACK_WAVES * 64), args, 0, stream);
 }
 
 template <int PER, int WIDTH>
@@ -772,16 +798,6 @@ hipError_t choose_by_size(const RouteArgs &a, int span, uint8_t *counts, hipStre
     return choose_go<16, 64>(a, span, counts, stream);
 }
 
-template <int PER>
-hipError_t go(const RouteBackwardArgs &r, hipStream_t stream) {
-    RouteBackwardArgs a = r;
-    const int64_t blocks = (a.tokens + BACK_WAVES - 1) / BACK_WAVES;
-    if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    void *args[] = {&a};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&route_backward_kernel<PER>), dim3(unsigned(blocks)),
-                           dim3(BACK_WAVES * 64), args, 0, stream);
-}
-
 }  // namespace
 
 hipError_t launch_route(const RouteArgs &r, hipStream_t stream) {
@@ -807,11 +823,18 @@ hipError_t launch_route(const RouteArgs &r, hipStream_t stream) {
 
 hipError_t launch_route_backward(const RouteBackwardArgs &a, hipStream_t stream) {
     if (a.tokens == 0) return hipSuccess;
-    if (a.experts <= 64) return go<1>(a, stream);
-    if (a.experts <= 128) return go<2>(a, stream);
-    if (a.experts <= 256) return go<4>(a, stream);
-    if (a.experts <= 512) return go<8>(a, stream);
-    return go<16>(a, stream);
+    if (a.tokens >= ROUTE_TEAMS_FROM && a.experts <= 256 && a.top_k <= 16) {
+        if (a.experts <= 16) return back_go<1, 16>(a, stream);
+        if (a.experts <= 32) return back_go<2, 16>(a, stream);
+        if (a.experts <= 64) return back_go<4, 16>(a, stream);
+        if (a.experts <= 128) return back_go<8, 16>(a, stream);
+        return back_go<16, 16>(a, stream);
+    }
+    if (a.experts <= 64) return back_go<1, 64>(a, stream);
+    if (a.experts <= 128) return back_go<2, 64>(a, stream);
+    if (a.experts <= 256) return back_go<4, 64>(a, stream);
+    if (a.experts <= 512) return back_go<8, 64>(a, stream);
+    return back_go<16, 64>(a, stream);
 }
 
 size_t route_workspace(int64_t tokens, int64_t experts) {

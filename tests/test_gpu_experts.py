@@ -551,7 +551,8 @@ def test_route_without_tokens(lib):
     assert off.tolist() == [0] * 9 and tok.tolist() == [-1] * 40
 
 
-@pytest.mark.parametrize("T,E,top_k", [(1, 8, 2), (7, 64, 6), (130, 256, 8), (33, 1000, 32), (5, 1, 1), (9, 65, 3)])
+@pytest.mark.parametrize("T,E,top_k", [(1, 8, 2), (7, 64, 6), (130, 256, 8), (33, 1000, 32), (5, 1, 1), (9, 65, 3), (513, 60, 6),
+                                       (515, 16, 16), (600, 200, 8), (514, 24, 2), (513, 128, 4)])
 @pytest.mark.parametrize("type_", QTYPES)
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("renormalise", [False, True])
