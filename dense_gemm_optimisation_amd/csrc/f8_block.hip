@@ -163,6 +163,17 @@ __device__ inline int64_t by_length(const BlockProblem &p, int64_t n, int lane) 
 typedef uint32_t u32x2_ea __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_ea __attribute__((ext_vector_type(4), aligned(2)));
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+// Two values rounded to bf16 (OUT 1) or fp16 (2), the first in the low half.
+template <int OUT>
+__device__ inline uint32_t pack2(float x, float y) {
+    const f32x2 v = {x, y};
+    return OUT == 1 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2))
+                    : __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+
 // W consecutive columns (4, or 8 of a 16-bit type) of a row of C at element
 // `at` of `base`, the first `n` of them inside C (n >= W: all): v + beta * C,
 // rounded.  Rows of C start at any element: the accesses are element-aligned
@@ -201,11 +212,11 @@ __device__ inline void store_columns(const BlockProblem &p, char *base, int64_t 
                 const V o = *reinterpret_cast<const V *>(c);
 #pragma unroll
                 for (int r = 0; r < W / 2; ++r)
-                    x[r] = bits(__builtin_fmaf(p.beta, old(o[r] & 0xffffu), v[2 * r])) |
-                           bits(__builtin_fmaf(p.beta, old(o[r] >> 16), v[2 * r + 1])) << 16;
+                    x[r] = pack2<OUT>(__builtin_fmaf(p.beta, old(o[r] & 0xffffu), v[2 * r]),
+                                      __builtin_fmaf(p.beta, old(o[r] >> 16), v[2 * r + 1]));
             } else {
 #pragma unroll
-                for (int r = 0; r < W / 2; ++r) x[r] = bits(v[2 * r]) | bits(v[2 * r + 1]) << 16;
+                for (int r = 0; r < W / 2; ++r) x[r] = pack2<OUT>(v[2 * r], v[2 * r + 1]);
             }
             *reinterpret_cast<V *>(c) = x;
         } else {
@@ -221,9 +232,12 @@ __device__ inline void store_columns(const BlockProblem &p, char *base, int64_t 
 // writes nor the rows' reads meet in a bank.  A store covers whole rows of
 // the strip.  c: C's element (0, 0) of the tile, which has mrows x ncols
 // elements; the strip is at (m, n) of it.
+// plain: the tile lies whole within C and beta is 0, so that the rows are
+// stored one after another without a look at either (the general way spends
+// four times as long on addresses and predicates as on the stores).
 template <int OUT, int FN, int ROWS>
 __device__ inline void store_strip(const BlockProblem &p, const LDS float *strip, char *c, int m, int mrows,
-                                   int n, int ncols, int lane) {
+                                   int n, int ncols, bool plain, int lane) {
     constexpr int W = OUT == 0 ? 4 : 8;          // columns per lane
     constexpr int LANES = FN * 16 / W;           // per row
     constexpr int STEP = 64 / LANES;             // rows per store
@@ -239,6 +253,23 @@ __device__ inline void store_strip(const BlockProblem &p, const LDS float *strip
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[i][4 * h + k] = x[k];
         }
+    }
+    if (plain) {
+        constexpr int ESIZE = OUT == 0 ? 4 : 2;
+        char *at = c + ((m + lane / LANES) * p.ldc + n) * ESIZE;
+#pragma unroll
+        for (int i = 0; i < ROWS / STEP; ++i) {
+            if constexpr (OUT == 0) {
+                *reinterpret_cast<dmatile::f32x4_ea *>(at) = f32x4{v[i][0], v[i][1], v[i][2], v[i][3]};
+            } else {
+                u32x4_ea w;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = pack2<OUT>(v[i][2 * k], v[i][2 * k + 1]);
+                *reinterpret_cast<u32x4_ea *>(at) = w;
+            }
+            at += STEP * p.ldc * ESIZE;
+        }
+        return;
     }
 #pragma unroll
     for (int i = 0; i < ROWS / STEP; ++i) {
@@ -503,6 +534,7 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
     constexpr int PAIR = 2;  // strips of 16 rows that leave together
     static_assert(WAVES * PAIR * 16 * WTN * 4 <= STAGE, "a pair of strips per wave fits a stage");
     LDS float *strip = reinterpret_cast<LDS float *>(lds + (buf ^ 1) * STAGE) + wave * PAIR * 16 * WTN;
+    const bool plain = mrows == BM && nrows == BN && p.beta == 0.0f;
     char *c = static_cast<char *>(p.C) + (ec * p.sC + m0 * p.ldc + n0) * (p.out == 0 ? 4 : 2);
 #pragma unroll
     for (int i = 0; i < FM; i += PAIR) {
@@ -516,9 +548,9 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
                     p.alpha * acc[i + k][j];
             }
         const int m = wm * WTM + i * 16, n = wn * WTN;
-        if (p.out == 0) store_strip<0, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, lane);
-        else if (p.out == 1) store_strip<1, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, lane);
-        else store_strip<2, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, lane);
+        if (p.out == 0) store_strip<0, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, plain, lane);
+        else if (p.out == 1) store_strip<1, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, plain, lane);
+        else store_strip<2, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, plain, lane);
     }
 }
 
