@@ -794,11 +794,29 @@ BlockOperand from_row(BlockOperand o, int64_t row) {  // row: a multiple of 128
 
 }  // namespace
 
+// Few rows or tiles.  The few-rows kernel reads B at the rate of memory, but
+// once for each chunk of its rows, and a compute unit runs two of its
+// workgroups at a time at about 7 us for each pair, so it wants long rows or
+// few columns; a tile takes about 4 us and 0.7 us for each block of k however
+// few of its rows are there.  Measured in us, few rows and 128 x 128 tiles:
+// 16x4096x4096 7.7 and 26, 16x16384x4096 20 and 32, 16x32768x2048 33 and 21,
+// 64x4096x4096 14 and 26, 128x4096x4096 24 and 26, 192x4096x4096 35 and 27,
+// 48x16384x4096 43 and 33; 64 experts of 2048x4096 at 8 rows each 134 and
+// 193, at 16 188 and 186; 256 of 1024x2048 at 1 row each 127 and 112; 8 of
+// 1024x2048 at 32 rows each 13 and 17.
+// 256 x 256 tiles hold a compute unit each and are the faster ones where they
+// fill three quarters of the chip: at K = 4096, 128 of them take 50 us where
+// four times as many of 128 x 128 take 45, 192 of them 51 where those take 69.
 BlockKernel block_choose(const BlockProblem &p, bool tiles_only) {
     if (p.M == 0 || p.N == 0 || p.batch == 0) return BlockKernel::None;
-    // rows of C that share a B: all of them, or an expert's share
-    const int64_t rows = p.segments == Segments::Rows ? (p.M + p.batch - 1) / p.batch : p.M;
-    if (!tiles_only && p.segments != Segments::Contracted && rows <= 64) return few_for(rows);
+    if (!tiles_only && p.segments != Segments::Contracted) {
+        // rows of C that share a B: all of them, or about a busy expert's
+        const int64_t rows = p.segments == Segments::Rows ? 2 * ((p.M + p.batch - 1) / p.batch) : p.M;
+        const int64_t groups = p.batch * ((p.N + 15) / 16);  // of 16 columns, a workgroup each
+        const int64_t at_once = 512;
+        if (rows <= 16 ? p.K >= 4096 || groups <= at_once : rows <= 128 && groups * ((rows + 63) / 64) <= at_once)
+            return few_for(rows);
+    }
     if (tiles_of(p, p.M, p.N, 256) < 192) return BlockKernel::Tile128;
     int64_t er = 0, ec = 0;
     if (!tiles_only) edges_of(p, er, ec);

@@ -150,7 +150,8 @@ def test_product_column_major_and_batched(lib, kernels, M, N, K, blocks):
 
 @pytest.mark.parametrize("M,N,K,batch,kernel", [
     (1, 40, 300, 1, "f8block_few_16"), (20, 40, 300, 1, "f8block_few_32"), (64, 40, 300, 3, "f8block_few_64"),
-    (65, 40, 300, 1, "f8block_mfma_128"), (3500, 3600, 401, 1, "f8block_mfma_256"), (70, 90, 650, 200, "f8block_mfma_256"),
+    (128, 40, 300, 1, "f8block_few_64"), (129, 40, 300, 1, "f8block_mfma_128"), (16, 8300, 300, 1, "f8block_mfma_128"),
+    (16, 8300, 4100, 1, "f8block_few_16"), (100, 5000, 300, 1, "f8block_mfma_128"), (3500, 3600, 401, 1, "f8block_mfma_256"), (70, 90, 650, 200, "f8block_mfma_256"),
     (3840, 4353, 272, 1, "f8block_mfma_256_edge"), (4144, 3900, 300, 1, "f8block_mfma_256_edge"),
     (4097, 4100, 129, 1, "f8block_mfma_256_edge"), (2049, 2049, 100, 4, "f8block_mfma_256_edge"),
     (4097, 4100, 0, 1, "f8block_mfma_256_edge"),
@@ -245,8 +246,10 @@ def test_experts_random(lib, kernels, fa, fb, out):
 
 def test_experts_kernels(lib):
     rng = np.random.default_rng(21)
-    experts(lib, rng, [1, 0, 9, 30], 70, 300, 0, out="f32", kernel="f8block_few_16")
-    experts(lib, rng, [3, 0, 90, 20], 70, 300, 0, out="f32", kernel="f8block_few_32")
+    experts(lib, rng, [1, 0, 9, 20], 70, 300, 0, out="f32", kernel="f8block_few_16")
+    experts(lib, rng, [3, 0, 36, 20], 70, 300, 0, out="f32", kernel="f8block_few_32")
+    experts(lib, rng, [1, 0, 9, 20], 2200, 300, 0, out="f32", kernel="f8block_mfma_128")
+    experts(lib, rng, [1, 0, 9, 20], 2200, 4096, 0, out="f32", kernel="f8block_few_16")
     experts(lib, rng, [3, 0, 90, 120], 70, 300, 0, out="f32", kernel="f8block_few_64")
     experts(lib, rng, [300, 0, 90, 120], 70, 300, 0, out="f32", kernel="f8block_mfma_128")
     experts(lib, rng, [1300, 0, 700, 257], 6000, 200, 11, out="f32", kernel="f8block_mfma_256")
