@@ -380,6 +380,39 @@ def test_quantize(lib, rows, cols, type_, block):
 
 @pytest.mark.parametrize("type_", QTYPES)
 @pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("both", [True, False])
+def test_quantize_large_as_its_parts(lib, type_, block, both):
+    """A result larger than the caches, the same as those of its parts, bit for bit."""
+    rows, cols, part = (4101 if both else 8197), 4104, 1024
+    x = torch.randn(rows, cols, device=DEV, generator=torch.Generator(DEV).manual_seed(2)).to(TORCH[type_])
+    x[700:712] = 0
+    x[5] *= 2.0 ** -10
+    x[6, 300] = float("nan")
+    in_type = getattr(lib, "INPUT_" + type_.upper())
+
+    def run(part, n):
+        q = torch.full((n, cols + 8), 9, dtype=torch.uint8, device=DEV)
+        s = torch.full((up(cols, 128) // 128, n), 9.0, device=DEV)
+        qt = torch.full((cols, up(n, 16)), 9, dtype=torch.uint8, device=DEV)
+        st = torch.full((up(n, 128) // 128, cols), 9.0, device=DEV)
+        lib.gemm_f8_block_quantize(n, cols, part.data_ptr(), cols, in_type, 0, 0, lib.F8_E4M3, block, q.data_ptr(),
+                                   cols + 8, s.data_ptr(), n, qt.data_ptr() if both else 0, up(n, 16),
+                                   st.data_ptr() if both else 0, cols)
+        return q, s, qt, st
+
+    whole = run(x, rows)
+    for r0 in range(0, rows, part):
+        n = min(part, rows - r0)
+        q, s, qt, st = run(x[r0:], n)
+        assert torch.equal(whole[0][r0:r0 + n], q)
+        s0, sn = (r0, n) if block == 1 else (r0 // 128, up(n, 128) // 128)
+        assert torch.equal(whole[1][:, s0:s0 + sn].nan_to_num(), s[:, :sn].nan_to_num())
+        assert torch.equal(whole[2][:, r0:r0 + n], qt[:, :n])
+        assert torch.equal(whole[3][r0 // 128:r0 // 128 + up(n, 128) // 128].nan_to_num(), st.nan_to_num())
+
+
+@pytest.mark.parametrize("type_", QTYPES)
+@pytest.mark.parametrize("block", [1, 128])
 def test_quantize_gathers(lib, type_, block):
     g = torch.Generator().manual_seed(4)
     x = torch.randn(1, 50, 264, generator=g).to(TORCH[type_])
