@@ -1,7 +1,7 @@
 // Routing tokens to experts: scores, the choice, the weights, and the rows of
 // each expert; and the weights' gradient.
 //
-// The choice.  One wave per token; lane l holds PER consecutive experts from
+// The choice.  One wave per token, or a quarter of one; lane l holds PER consecutive experts from
 // PER*l on, so of equal keys the lowest lane's is the lowest index.  The
 // largest key is found top_k times over the wave with data-parallel moves.
 // Without a bias the logits rank as their scores do and are compared as they
@@ -524,10 +524,18 @@ __device__ inline void choose(const RouteArgs &a, int64_t t, bool live, int lane
     if (undefined) w = __builtin_nanf("");
 }
 
+__host__ __device__ inline int64_t count_pitch(int64_t experts) { return (experts + 3) / 4 * 4; }
+
+// Waves per workgroup at most.  16 experts per lane spill where 16 waves share
+// the registers (65536 tokens of 256 experts, four per wave: 155 us, with 8
+// waves 139); 8 per lane spill a little and still gain by 16 (of 512 experts,
+// one per wave: 240 us, with 8 waves 318).
+constexpr int choose_waves(int per) { return per >= 16 ? 8 : 16; }
+
 // `span` consecutive tokens per workgroup, its teams taking them in turn.
 // With counts: counts[workgroup][expert], the tokens of the span that chose it.
 template <int PER, int WIDTH>
-__global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a, int span, uint8_t *counts) {
+__global__ __launch_bounds__(choose_waves(PER) * 64) void choose_kernel(RouteArgs a, int span, uint8_t *counts) {
     __shared__ uint32_t count[ROUTE_MAX_EXPERTS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     constexpr int TEAMS = 64 / WIDTH;  // per wave
@@ -556,13 +564,14 @@ __global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a, int span, uin
     if (counts != nullptr) {
         __syncthreads();
         for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
-            counts[int64_t(blockIdx.x) * a.experts + e] = uint8_t(count[e]);
+            counts[blockIdx.x * count_pitch(a.experts) + e] = uint8_t(count[e]);
     }
 }
 
 // Workgroup g lays out the 64-token blocks from g*own on, `own` of them.
-// counts: one row of bytes per `span` tokens (a divisor of 64), or null when
-// there is one block, which then counts for itself.
+// counts: one row of E bytes, made up to whole words, per `span` tokens (a
+// divisor of 64), or null when there is one block, which then counts for
+// itself.
 __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a, int64_t own, int span, const uint8_t *counts) {
     constexpr int THREADS = 1024;
     __shared__ unsigned long long mask[ROUTE_MAX_EXPERTS];
@@ -590,37 +599,26 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a, int64_t own, i
         __syncthreads();
         for (int e = tid; e < E; e += THREADS) total[e] = __popcll(mask[e]);
     } else {
+        // four experts' bytes at a time
         const int64_t rows = (a.tokens + span - 1) / span, before = first_block * BLOCK / span;
-        const int quads = (E + 3) / 4;
-        if (E % 4 == 0) {  // four experts' bytes at a time; workspace rows start on whole words
-            const int parts = THREADS / quads;
-            const int q = tid % quads, part = tid / quads;
-            if (part < parts) {
-                int sum[4] = {0, 0, 0, 0}, early[4] = {0, 0, 0, 0};
-                for (int64_t r = part; r < rows; r += parts) {
-                    const uint32_t v = reinterpret_cast<const uint32_t *>(counts)[r * quads + q];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = v >> (8 * i) & 255;
-                        sum[i] += c;
-                        early[i] += r < before ? c : 0;
-                    }
-                }
+        const int quads = (E + 3) / 4, parts = THREADS / quads;
+        const int q = tid % quads, part = tid / quads;
+        if (part < parts) {
+            int sum[4] = {0, 0, 0, 0}, early[4] = {0, 0, 0, 0};
+            for (int64_t r = part; r < rows; r += parts) {
+                const uint32_t v = reinterpret_cast<const uint32_t *>(counts)[r * quads + q];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    atomicAdd(&total[4 * q + i], sum[i]);
-                    atomicAdd(&next[4 * q + i], early[i]);
+                    const int c = v >> (8 * i) & 255;
+                    sum[i] += c;
+                    early[i] += r < before ? c : 0;
                 }
             }
-        } else {
-            for (int e = tid; e < E; e += THREADS) {
-                int sum = 0, early = 0;
-                for (int64_t r = 0; r < rows; ++r) {
-                    if (r == before) early = sum;
-                    sum += counts[r * E + e];
-                }
-                total[e] = sum;
-                next[e] = early;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (4 * q + i >= E) break;
+                atomicAdd(&total[4 * q + i], sum[i]);
+                atomicAdd(&next[4 * q + i], early[i]);
             }
         }
     }
@@ -776,15 +774,17 @@ hipError_t choose_go(const RouteArgs &r, int span, uint8_t *counts, hipStream_t 
     const int tokens_per_wave = 64 / WIDTH, waves = (span + tokens_per_wave - 1) / tokens_per_wave;
     void *args[] = {&a, &span, &counts};
     return hipLaunchKernel(reinterpret_cast<const void *>(&choose_kernel<PER, WIDTH>), dim3(unsigned(grid)),
-                           dim3(unsigned(waves < 16 ? waves : 16) * 64), args, 0, stream);
+                           dim3(unsigned(waves < choose_waves(PER) ? waves : choose_waves(PER)) * 64), args, 0, stream);
 }
 
-#ifndef ROUTE_TEAMS_FROM
-#define ROUTE_TEAMS_FROM 512
-#endif
+// Tokens from which four share a wave, where 16 lanes hold a token's experts:
+// 16384 tokens of 64 experts 21 -> 14 us, their gradient of 128 9.0 -> 6.6;
+// with fewer tokens compute units are idle and a whole wave is done sooner
+// (64 tokens of 256 experts 11.5 us, by fours 16.5).
+constexpr int64_t TEAMS_FROM = 512;
+
 hipError_t choose_by_size(const RouteArgs &a, int span, uint8_t *counts, hipStream_t stream) {
-    // four tokens per wave once there are tokens for every compute unit
-    if (a.tokens >= ROUTE_TEAMS_FROM && a.experts <= 256 && a.top_k <= 16 && a.groups <= 16) {
+    if (a.tokens >= TEAMS_FROM && a.experts <= 256 && a.top_k <= 16 && a.groups <= 16) {
         if (a.experts <= 16) return choose_go<1, 16>(a, span, counts, stream);
         if (a.experts <= 32) return choose_go<2, 16>(a, span, counts, stream);
         if (a.experts <= 64) return choose_go<4, 16>(a, span, counts, stream);
@@ -823,7 +823,7 @@ hipError_t launch_route(const RouteArgs &r, hipStream_t stream) {
 
 hipError_t launch_route_backward(const RouteBackwardArgs &a, hipStream_t stream) {
     if (a.tokens == 0) return hipSuccess;
-    if (a.tokens >= ROUTE_TEAMS_FROM && a.experts <= 256 && a.top_k <= 16) {
+    if (a.tokens >= TEAMS_FROM && a.experts <= 256 && a.top_k <= 16) {
         if (a.experts <= 16) return back_go<1, 16>(a, stream);
         if (a.experts <= 32) return back_go<2, 16>(a, stream);
         if (a.experts <= 64) return back_go<4, 16>(a, stream);
@@ -840,7 +840,7 @@ hipError_t launch_route_backward(const RouteBackwardArgs &a, hipStream_t stream)
 size_t route_workspace(int64_t tokens, int64_t experts) {
     // a row of byte counts for each span of tokens, at most one per 16
     const size_t rows = tokens <= 4096 ? size_t((tokens + 15) / 16) : size_t((tokens + BLOCK - 1) / BLOCK);
-    return ((rows > 0 ? rows : 1) * size_t(experts) + 15) / 16 * 16;
+    return ((rows > 0 ? rows : 1) * size_t(count_pitch(experts)) + 15) / 16 * 16;
 }
 
 }  // namespace libgemm
