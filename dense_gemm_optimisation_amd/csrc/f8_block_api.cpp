@@ -55,7 +55,7 @@ bool operand_ok(const uint8_t *x, int64_t ld, int format, const float *s, int64_
     if (misaligned(x, 16) || misaligned(s, 4) || ld % 16 != 0 || ld < K) return false;
     if (batch > 1 && stride % 16 != 0) return false;
     const int64_t sr = ceil_div(R, block), kb = ceil_div(K, 128);
-    if (lds < sr) return false;
+    if (kb > 1 && lds < sr) return false;
     const int64_t span_x = (R - 1) * ld + K, span_s = (kb - 1) * lds + sr;
     if (extent_over(batch, stride, span_x) || extent_over(batch, sstride, span_s)) return false;
     rx = range_of(x, span_x, batch, stride, 1);
@@ -228,7 +228,7 @@ gemm_status_t gemm_f8_block_quantize(int64_t rows, int64_t cols, const void *X, 
                                Direction{QT, ST, ldqt, ldst, strideQT, strideST, cols, rows}}) {
         if (d.codes == nullptr) continue;
         const int64_t sr = ceil_div(d.outer, block), kb = ceil_div(d.inner, 128);
-        if (any_over({d.ld, d.lds}) || d.ld < d.inner || d.lds < sr || misaligned(d.scales, 4))
+        if (any_over({d.ld, d.lds}) || d.ld < d.inner || (kb > 1 && d.lds < sr) || misaligned(d.scales, 4))
             return GEMM_ERR_INVALID_ARG;
         if (too_big(d.outer, d.ld) || too_big(kb, d.lds)) return GEMM_ERR_INVALID_ARG;
         const int64_t span_q = (d.outer - 1) * d.ld + d.inner, span_s = (kb - 1) * d.lds + sr;

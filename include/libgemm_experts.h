@@ -32,7 +32,7 @@
  *             scale[(k/128)*lds + r/block].  block is 1 (a scale for each
  *             row: activations, gradients) or 128 (a scale for each
  *             128 x 128 block: weights).  4-byte aligned, lds at least
- *             ceil(R/block).
+ *             ceil(R/block) where there is more than one row of scales.
  *   Any K, M and N are accepted; the last block of K may be short.
  *
  * Arithmetic
@@ -101,7 +101,8 @@ typedef enum gemm_score_t {
  *               wanted.  At least one direction must be wanted.  With block
  *               128 the two hold the same codes and scales.
  * ldq >= cols, lds >= ceil(rows/block), ldqt >= rows, ldst >=
- * ceil(cols/block); slices of one output must not overlap when batch > 1.
+ * ceil(cols/block) (lds and ldst only where there is more than one row of
+ * scales); slices of one output must not overlap when batch > 1.
  * Nothing outside the rows x cols codes and their scales is written.
  * rows == 0, cols == 0 or batch == 0: nothing is done. */
 gemm_status_t gemm_f8_block_quantize(int64_t rows, int64_t cols, const void *X, int64_t ldx,

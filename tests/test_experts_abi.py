@@ -184,7 +184,7 @@ def quantize_call(lib, **k):
 @pytest.mark.parametrize("bad", [
     dict(rows=-1), dict(cols=-1), dict(batch=-1), dict(X=0), dict(X=X + 1), dict(ldx=299), dict(in_type=3), dict(format=2),
     dict(block=0), dict(block=64), dict(Q=0), dict(S=0), dict(QT=0), dict(ST=0), dict(Q=0, S=0, QT=0, ST=0), dict(ldq=299),
-    dict(lds=99), dict(ldqt=99), dict(ldst=299), dict(S=S + 1), dict(ST=ST + 2), dict(index=OFF, x_rows=-1),
+    dict(lds=99), dict(ldqt=99), dict(rows=130, lds=130, ldqt=144, ldst=299), dict(S=S + 1), dict(ST=ST + 2), dict(index=OFF, x_rows=-1),
     dict(index=OFF + 1, x_rows=10), dict(index=OFF, x_rows=10, batch=2), dict(QT=Q + 5), dict(S=X + 4), dict(Q=X),
     dict(index=OFF, x_rows=10, ST=OFF), dict(batch=2, stride_x=30000, stride_q=1), dict(rows=1 << 60),
     dict(batch=2, stride_x=-1), dict(ldq=1 << 62),

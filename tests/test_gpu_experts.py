@@ -165,6 +165,27 @@ def test_product_kernels(lib, M, N, K, batch, kernel, blocks):
                 alpha=2.0, beta=1.0, order="col")
 
 
+@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("lds", [0, 1])
+def test_one_row_of_scales_has_no_stride(lib, kernels, M, lds):
+    """As a tensor of one row has any: transposes and slices leave 1 or 0 there."""
+    rng = np.random.default_rng(31)
+    a, b = Operand(rng, M, 100, "e4m3", 1, True), Operand(rng, 140, 100, "e5m2", 1, True)
+    wide, thin = (torch.full((M, 140), 7.0, device=DEV) for _ in range(2))
+    for c, ldsa, ldsb in ((wide, M, 140), (thin, lds, lds)):
+        lib.gemm_f8_block(M, 140, 100, 1.0, a.codes.data_ptr(), a.ld, lib.F8_E4M3, a.scales.data_ptr(), ldsa, 1,
+                          b.codes.data_ptr(), b.ld, lib.F8_E5M2, b.scales.data_ptr(), ldsb, 1, 0.0, c.data_ptr(), 140, 0, 0)
+    assert torch.equal(wide, thin) and wide.abs().max() > 0
+    x = torch.randn(M, 100, device=DEV)
+    outs = [[torch.full((n,), 9, dtype=t, device=DEV) for n, t in
+             ((M * 112, torch.uint8), (M, torch.float32), (100 * up(M, 16), torch.uint8), (up(M, 128) // 128 * 100, torch.float32))]
+            for _ in range(2)]
+    for (q, s, qt, st), lds_ in zip(outs, (M, lds)):
+        lib.gemm_f8_block_quantize(M, 100, x.data_ptr(), 100, lib.INPUT_F32, 0, 0, lib.F8_E4M3, 1, q.data_ptr(), 112,
+                                   s.data_ptr(), lds_, qt.data_ptr(), up(M, 16), st.data_ptr(), lds_ if M <= 128 else 100)
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+
+
 @pytest.mark.parametrize("M,N", [(3, 20), (70, 300)])
 def test_product_without_terms(lib, kernels, M, N):
     rng = np.random.default_rng(5)
