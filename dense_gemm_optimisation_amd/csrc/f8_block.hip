@@ -116,32 +116,48 @@ __device__ inline void segment_of(const int32_t *offsets, int64_t e, int64_t lim
     if (hi < lo) hi = lo;
 }
 
-// The segment that holds tile row `tm` when every segment of the rows starts
-// a tile of its own, and the tile's first row; false when there are fewer
-// tiles.  Each wave finds it alone, 64 segments at a time.
-__device__ inline bool find_segment(const BlockProblem &p, int64_t tm, int BM, int lane, int64_t &e,
-                                    int64_t &m0, int64_t &end) {
-    int64_t before = 0;
-    for (int64_t e0 = 0; e0 < p.batch; e0 += 64) {
-        int64_t lo = 0, hi = 0;
+// 64 segments of rows from e0 on, one per lane, and their tiles when every
+// segment starts a tile of its own: sum counts those of the lanes up to this.
+struct SegmentTiles {
+    int64_t lo, hi;
+    int tiles, sum;
+    __device__ SegmentTiles(const BlockProblem &p, int64_t e0, int BM, int lane) {
+        lo = hi = 0;
         if (e0 + lane < p.batch) segment_of(p.offsets, e0 + lane, p.M, lo, hi);
-        const int tiles = int((hi - lo + BM - 1) / BM);
-        int sum = tiles;
+        sum = tiles = int((hi - lo + BM - 1) / BM);
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const int o = __shfl_up(sum, d);
             if (lane >= d) sum += o;
         }
-        const uint64_t past = __ballot(before + sum > tm);
+    }
+    __device__ int64_t total() const { return __shfl(sum, 63); }
+};
+
+// All segments' tiles (at most `most`); first: the first 64 segments.
+__device__ inline uint32_t tile_rows(const BlockProblem &p, const SegmentTiles &first, int64_t most, int BM, int lane) {
+    int64_t n = first.total();
+    for (int64_t e0 = 64; e0 < p.batch; e0 += 64) n += SegmentTiles(p, e0, BM, lane).total();
+    return uint32_t(uniform(n < most ? n : most));
+}
+
+// The segment that holds tile row `tm`, and the tile's first row; false when
+// there are fewer tiles.  Each wave finds it alone.
+__device__ inline bool find_segment(const BlockProblem &p, SegmentTiles s, int64_t tm, int BM, int lane, int64_t &e,
+                                    int64_t &m0, int64_t &end) {
+    int64_t before = 0;
+    for (int64_t e0 = 0; e0 < p.batch; e0 += 64) {
+        if (e0 > 0) s = SegmentTiles(p, e0, BM, lane);
+        const uint64_t past = __ballot(before + s.sum > tm);
         if (past) {
             const int l = __builtin_ctzll(past);
             e = uniform(e0 + l);
-            const int64_t first = before + __shfl(sum, l) - __shfl(tiles, l);
-            m0 = uniform(__shfl(lo, l) + (tm - first) * BM);
-            end = uniform(__shfl(hi, l));
+            const int64_t first = before + __shfl(s.sum, l) - __shfl(s.tiles, l);
+            m0 = uniform(__shfl(s.lo, l) + (tm - first) * BM);
+            end = uniform(__shfl(s.hi, l));
             return true;
         }
-        before += __shfl(sum, 63);
+        before += s.total();
     }
     return false;
 }
@@ -278,18 +294,20 @@ __device__ inline void store_strip(const BlockProblem &p, const LDS float *strip
     }
 }
 
-// Output tile `id` of the grid, as tile_of numbers them, in 32 bits (the grid
-// has fewer than 2^31 tiles).
-__device__ inline void coordinates(const TileGrid &g, uint32_t wg, uint32_t &batch, uint32_t &tm, uint32_t &tn) {
-    const uint32_t rows = uint32_t(g.tiles_m), cols = uint32_t(g.tiles_n), group = uint32_t(g.group_m);
+// The output tile of workgroup wg, as tile_of numbers them, in 32 bits (the
+// grid has fewer than 2^31 tiles); false past the last of `rows` tile rows.
+__device__ inline bool coordinates(const TileGrid &g, uint32_t rows, uint32_t wg, uint32_t &batch, uint32_t &tm,
+                                   uint32_t &tn) {
+    const uint32_t cols = uint32_t(g.tiles_n), group = uint32_t(g.group_m);
     // The dispatcher deals workgroups to the 8 dies in turn: those of one die
     // take neighbouring tiles, of the whole grid or (g.xcds 0) of every slice
     // alike: slices of unlike lengths would keep the dies busy for unlike
     // times.
     const uint32_t slice = rows * cols, of = g.xcds == 0 ? wg / slice : 0;
-    const uint32_t total = g.xcds == 0 ? slice : uint32_t(g.count()), q = total / 8, odd = total % 8;
+    const uint32_t total = g.xcds == 0 ? slice : slice * uint32_t(g.batch), q = total / 8, odd = total % 8;
     wg -= of * slice;
     const uint32_t x = wg % 8, id = (x < odd ? x * (q + 1) : odd * (q + 1) + (x - odd) * q) + wg / 8;
+    if (wg / 8 >= q + (x < odd ? 1 : 0)) return false;
     batch = g.xcds == 0 ? of : id / slice;
     const uint32_t local = g.xcds == 0 ? id : id - batch * slice;
     const uint32_t n = local / (group * cols), first = n * group;
@@ -297,6 +315,7 @@ __device__ inline void coordinates(const TileGrid &g, uint32_t wg, uint32_t &bat
     const uint32_t r = local - n * (group * cols);
     tn = r / high;
     tm = first + (r - tn * high);
+    return true;
 }
 
 // One workgroup per BM x BN tile, WAVES_M x WAVES_N waves of FM x FN blocks.
@@ -307,12 +326,16 @@ __device__ inline void coordinates(const TileGrid &g, uint32_t wg, uint32_t &bat
 // fragments are read, and the freed stage is refilled there.  A block's sum
 // is added to its accumulators LAG instructions after it was started, so that
 // neither pipe waits for the other.
-template <int FA, int FB, bool PER_COLUMN, int WAVES_M, int WAVES_N, int FM, int FN>
-__global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(BlockArgs a) {
-    constexpr int WAVES = WAVES_M * WAVES_N;
+// TEAMS 2: two such groups of waves, each with its own stages, take the blocks
+// of k in turn; at the end each adds the other's sums of half of the rows to
+// its own and stores them.
+template <int FA, int FB, bool PER_COLUMN, int WAVES_M, int WAVES_N, int FM, int FN, int TEAMS>
+__global__ __launch_bounds__(TEAMS *WAVES_M *WAVES_N * 64) void block_tile_kernel(BlockArgs a) {
+    constexpr int WAVES = WAVES_M * WAVES_N;  // of a team
     constexpr int WTM = FM * 16, WTN = FN * 16, BM = WAVES_M * WTM, BN = WAVES_N * WTN;
     static_assert(128 % WTN == 0, "a wave's columns lie in one block of 128");
     static_assert(FM % 2 == 0, "A's fragments alternate between two slots");
+    static_assert(TEAMS == 1 || TEAMS == 2, "one adds the other's sums");
     using PA = Panel<BM, WAVES>;
     using PB = Panel<BN, WAVES>;
     constexpr int AT_B = PA::BYTES, AT_S = AT_B + PB::BYTES;  // within a stage
@@ -320,18 +343,28 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
     constexpr int SLOADS = (BM + BN) / 64;  // scale loads of 64 rows, one per wave or less
     static_assert(SLOADS <= WAVES, "at most one scale load per wave");
     constexpr int LAG = 3;
-    __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
-    LDS char *lds = (LDS char *)smem;
+    __shared__ __attribute__((aligned(1024))) char smem[TEAMS * 2 * STAGE];
     const BlockProblem &p = a.p;
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int team = TEAMS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / (WAVES * 64));
+    LDS char *lds = (LDS char *)smem + team * 2 * STAGE;
+    const int tid = threadIdx.x - team * WAVES * 64, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
 
+    // With segments of rows the grid has as many tile rows as there can be: the
+    // dies share those that there are.
     uint32_t te, tm, tn;
-    coordinates(a.grid, blockIdx.x, te, tm, tn);
-    int64_t e = uniform(te), m0 = uniform(tm) * BM, m_end = p.M, k_lo = 0, k_hi = p.K;
+    int64_t e, m0, m_end = p.M, k_lo = 0, k_hi = p.K;
+    if (p.segments == Segments::Rows) {
+        const SegmentTiles first(p, 0, BM, lane);
+        if (!coordinates(a.grid, tile_rows(p, first, a.grid.tiles_m, BM, lane), blockIdx.x, te, tm, tn)) return;
+        if (!find_segment(p, first, uniform(tm), BM, lane, e, m0, m_end)) return;
+    } else {
+        if (!coordinates(a.grid, uint32_t(a.grid.tiles_m), blockIdx.x, te, tm, tn)) return;
+        e = uniform(te);
+        m0 = uniform(tm) * BM;
+    }
     const int64_t n0 = uniform(tn) * BN;
-    if (p.segments == Segments::Rows && !find_segment(p, uniform(tm), BM, lane, e, m0, m_end)) return;
     if (p.segments == Segments::Contracted) {
         if (p.batch <= 64) e = by_length(p, e, lane);
         segment_of(p.offsets, e, p.K, k_lo, k_hi);
@@ -368,7 +401,7 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
         uint32_t(uniform((((s_r0 + s_rows - 1) >> s_shift) - s_first + 1) * 4));
 
     const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
-    const int steps = (K + 127) / 128;
+    const int blocks = (K + 127) / 128, steps = (blocks + TEAMS - 1) / TEAMS;
     // The stage that is being loaded.  Its loads (A's, B's, the scales) go out
     // a few at a time between matrix instructions: all at once they fill the
     // memory pipe's queue and hold up the matrix pipe.
@@ -377,8 +410,9 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
         u32x4 a, b, s;
         int kleft;
     };
-    auto loading = [&](int s) {  // stage s; past the last one: loads that read nothing and store zeros
-        const bool live = s < steps;
+    auto loading = [&](int step) {  // past the last block: loads that read nothing and store zeros
+        const int s = step * TEAMS + team;
+        const bool live = s < blocks;
         const int kleft = K - 128 * s;
         return Loading{pa.stage(s, live), pb.stage(s, live),
                        dma::raw_buffer(static_cast<uint64_t>(s_base + s * s_ld), live ? s_bytes : 0u),
@@ -391,10 +425,11 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
         else if (SLOADS == WAVES || wave < SLOADS) direct_load4(l.s, at + AT_S + wave * 256, s_voff);
     };
     // The chunk that holds the end of K, in the stage of buffer buf: its bytes
-    // from K on are not the operand's.
+    // from K on are not the operand's.  (Of the teams the one that has that block.)
     auto clear_tail = [&](int buf) {
         const int kleft = K & 127, c = kleft >> 4;
-        for (int r = tid; r < BM + BN; r += WAVES * 64) {
+        const bool mine = TEAMS == 1 || (steps - 1) * TEAMS + team == blocks - 1;
+        for (int r = mine ? tid : BM + BN; r < BM + BN; r += WAVES * 64) {
             const int rr = r < BM ? r : r - BM;
             LDS char *chunk = lds + buf * STAGE + r * 128 + ((c ^ swz(rr)) << 4);
             for (int b = kleft & 15; b < 16; ++b) chunk[b] = 0;
@@ -534,10 +569,28 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
     constexpr int PAIR = 2;  // strips of 16 rows that leave together
     static_assert(WAVES * PAIR * 16 * WTN * 4 <= STAGE, "a pair of strips per wave fits a stage");
     LDS float *strip = reinterpret_cast<LDS float *>(lds + (buf ^ 1) * STAGE) + wave * PAIR * 16 * WTN;
+    if constexpr (TEAMS == 2) {
+        constexpr int HALF = FM / 2;
+        LDS f32x4 *sums = reinterpret_cast<LDS f32x4 *>(lds + buf * STAGE) + tid;  // this team's of the other's rows
+        LDS f32x4 *others = reinterpret_cast<LDS f32x4 *>((LDS char *)smem + (team ^ 1) * 2 * STAGE + buf * STAGE) + tid;
+        static_assert(HALF * FN * WAVES * 64 * 16 <= STAGE, "half of the sums fit a stage");
+#pragma unroll
+        for (int i = 0; i < HALF; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) sums[(i * FN + j) * WAVES * 64] = team == 0 ? acc[HALF + i][j] : acc[i][j];
+        dma::wait_lgkmcnt0();
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < HALF; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = (team == 0 ? acc[i][j] : acc[HALF + i][j]) + others[(i * FN + j) * WAVES * 64];
+    }
+    constexpr int ROWS = FM / TEAMS;  // of blocks that this team stores
     const bool plain = mrows == BM && nrows == BN && p.beta == 0.0f;
     char *c = static_cast<char *>(p.C) + (ec * p.sC + m0 * p.ldc + n0) * (p.out == 0 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < FM; i += PAIR) {
+    for (int i = 0; i < ROWS; i += PAIR) {
         const int r = lane & 15;
 #pragma unroll
         for (int k = 0; k < PAIR; ++k)
@@ -547,7 +600,7 @@ __global__ __launch_bounds__(WAVES_M *WAVES_N * 64) void block_tile_kernel(Block
                 *reinterpret_cast<LDS f32x4 *>(strip + (k * 16 + r) * WTN + ((q ^ r) & (FN * 4 - 1)) * 4) =
                     p.alpha * acc[i + k][j];
             }
-        const int m = wm * WTM + i * 16, n = wn * WTN;
+        const int m = wm * WTM + (team * ROWS + i) * 16, n = wn * WTN;
         if (p.out == 0) store_strip<0, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, plain, lane);
         else if (p.out == 1) store_strip<1, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, plain, lane);
         else store_strip<2, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, plain, lane);
@@ -568,19 +621,21 @@ __device__ inline u32x4 first_bytes(u32x4 v, int valid) {
 
 constexpr int FEW_WAVES = 8;
 
-// For at most a few times 16*FM rows of C: B is read once, straight into
-// registers, 16 columns per workgroup, its blocks of K dealt to the waves in
-// turn, UNROLL of them in flight per wave.  The waves' sums are added in
-// order through LDS.  Bound by reading B: with 16 columns a chip-wide launch
-// needs only 4096 columns, and 128-byte pieces of 16 rows keep whole lines.
+// For few rows of C: 16 columns by 16*FM rows per workgroup, B and A read
+// straight into registers, the blocks of K dealt to the waves in turn, UNROLL
+// of them in flight per wave.  The waves' sums are added in order through
+// LDS.  Bound by reading B: with 16 columns a chip-wide launch needs only 4096
+// columns, and 128-byte pieces of 16 rows keep whole lines.
 template <int FA, int FB, bool PER_COLUMN, int FM, int UNROLL>
 __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) {
     __shared__ f32x4 sums[FEW_WAVES][FM * 64];
     const BlockProblem &p = a.p;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t e = uniform(int64_t(blockIdx.x) / a.grid.tiles_n);
-    const int64_t n0 = uniform(int64_t(blockIdx.x) - e * a.grid.tiles_n) * 16;
+    // (the parts of the same columns, which read the same B, follow each other at a distance)
+    const uint32_t groups = uint32_t(p.batch * a.grid.tiles_n), part = blockIdx.x / groups, group = blockIdx.x - part * groups;
+    const int64_t e = uniform(group / uint32_t(a.grid.tiles_n));
+    const int64_t n0 = uniform(int64_t(group) - e * a.grid.tiles_n) * 16;
     const bool rows_cut = p.segments == Segments::Rows;
     int64_t m_lo = 0, m_hi = p.M;
     if (rows_cut) {
@@ -607,7 +662,8 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) 
         return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]),
                      int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
     };
-    for (int64_t m0 = m_lo; m0 < m_hi; m0 += 16 * FM) {
+    const int64_t m_first = m_lo + int64_t(part) * 16 * FM;
+    for (int64_t m0 = m_first; m0 < m_hi; m0 += a.grid.tiles_m * 16 * FM) {
         const uint8_t *ar[FM];
         int64_t am[FM];
         f32x4 acc[FM];
@@ -659,7 +715,7 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) 
                 }
             }
         }
-        if (m0 > m_lo) __syncthreads();  // the last rows' sums have been read
+        if (m0 > m_first) __syncthreads();  // the last rows' sums have been read
 #pragma unroll
         for (int i = 0; i < FM; ++i) sums[wave][i * 64 + lane] = acc[i];
         __syncthreads();
@@ -688,19 +744,25 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) 
     }
 }
 
+// The rows of C that share a B: all of them, or about a busy expert's.
+int64_t rows_of(const BlockProblem &p) {
+    return p.segments == Segments::Rows ? 2 * ((p.M + p.batch - 1) / p.batch) : p.M;
+}
+
 template <int FA, int FB, bool PER_COLUMN, int FM, int UNROLL>
 hipError_t few_go(const BlockProblem &p, hipStream_t stream) {
     BlockArgs a{};
     a.p = p;
     a.grid.tiles_n = (p.N + 15) / 16;
-    const int64_t count = a.grid.tiles_n * p.batch;
-    if (count > 0x7fffffff) return hipErrorInvalidConfiguration;
+    a.grid.tiles_m = (rows_of(p) + 16 * FM - 1) / (16 * FM);  // (an expert with more rows takes several turns)
+    if (double(a.grid.tiles_n) * a.grid.tiles_m * p.batch > 0x7fffffff) return hipErrorInvalidConfiguration;
+    const int64_t count = a.grid.tiles_n * a.grid.tiles_m * p.batch;
     void *args[] = {&a};
     return hipLaunchKernel(reinterpret_cast<const void *>(&block_few_kernel<FA, FB, PER_COLUMN, FM, UNROLL>),
                            dim3(static_cast<unsigned>(count)), dim3(FEW_WAVES * 64), args, 0, stream);
 }
 
-template <int FA, int FB, bool PER_COLUMN, int WM, int WN, int FM, int FN>
+template <int FA, int FB, bool PER_COLUMN, int WM, int WN, int FM, int FN, int TEAMS>
 hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
     constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
     BlockArgs a{};
@@ -717,8 +779,8 @@ hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
         return hipErrorInvalidConfiguration;
     void *args[] = {&a};
     return hipLaunchKernel(
-        reinterpret_cast<const void *>(&block_tile_kernel<FA, FB, PER_COLUMN, WM, WN, FM, FN>),
-        dim3(static_cast<unsigned>(a.grid.count())), dim3(WM * WN * 64), args, 0, stream);
+        reinterpret_cast<const void *>(&block_tile_kernel<FA, FB, PER_COLUMN, WM, WN, FM, FN, TEAMS>),
+        dim3(static_cast<unsigned>(a.grid.count())), dim3(TEAMS * WM * WN * 64), args, 0, stream);
 }
 
 template <int FA, int FB, bool PER_COLUMN>
@@ -726,8 +788,9 @@ hipError_t tile_size(BlockKernel k, const BlockProblem &p, hipStream_t stream) {
     if (k == BlockKernel::Few16) return few_go<FA, FB, PER_COLUMN, 1, 4>(p, stream);
     if (k == BlockKernel::Few32) return few_go<FA, FB, PER_COLUMN, 2, 4>(p, stream);
     if (k == BlockKernel::Few64) return few_go<FA, FB, PER_COLUMN, 4, 2>(p, stream);
-    if (k == BlockKernel::Tile256) return tile_go<FA, FB, PER_COLUMN, 2, 4, 8, 4>(p, stream);
-    return tile_go<FA, FB, PER_COLUMN, 2, 2, 4, 4>(p, stream);
+    if (k == BlockKernel::Tile256) return tile_go<FA, FB, PER_COLUMN, 2, 4, 8, 4, 1>(p, stream);
+    if (k == BlockKernel::Tile128) return tile_go<FA, FB, PER_COLUMN, 2, 2, 4, 4, 1>(p, stream);
+    return tile_go<FA, FB, PER_COLUMN, 2, 2, 4, 4, 2>(p, stream);
 }
 
 }  // namespace
@@ -755,10 +818,16 @@ LIBGEMM_BLOCK_FORMATS(3, 1, 1)
 #if LIBGEMM_BLOCK_PART <= 0
 namespace {
 
-// Tiles of `side` x `side` of a problem (with segments of rows: about as many).
+// Tiles of `side` x `side` of a problem.  With segments of rows an estimate
+// for lengths that differ by half: one per expert where they are short, else
+// half a tile more for each.
 int64_t tiles_of(const BlockProblem &p, int64_t M, int64_t N, int64_t side) {
-    return ((M + side - 1) / side) * ((N + side - 1) / side) * (p.segments == Segments::Rows ? 1 : p.batch);
+    const int64_t cols = (N + side - 1) / side;
+    if (p.segments != Segments::Rows) return (M + side - 1) / side * cols * p.batch;
+    const double n = double(p.batch < M ? p.batch : M), rows = double(M) / side + 0.5 * n;
+    return int64_t((4.0 * M <= side * n ? n : rows > 1.06 * n ? rows : 1.06 * n) * cols);
 }
+int64_t rounds_of(int64_t tiles, int64_t at_once) { return (tiles + at_once - 1) / at_once; }
 
 // Rows or columns past the last whole 256 that are few enough for the few-rows kernel.
 int64_t edge_of(int64_t n) { return n > 256 && n % 256 <= 64 ? n % 256 : 0; }
@@ -770,7 +839,7 @@ int64_t edge_of(int64_t n) { return n > 256 && n % 256 <= 64 ? n % 256 : 0; }
 void edges_of(const BlockProblem &p, int64_t &rows, int64_t &cols) {
     rows = cols = 0;
     if (p.segments != Segments::None) return;
-    auto waves = [&](int64_t M, int64_t N) { return (tiles_of(p, M, N, 256) + 255) / 256; };
+    auto waves = [&](int64_t M, int64_t N) { return rounds_of(tiles_of(p, M, N, 256), 256); };
     const int64_t er = edge_of(p.M), ec = edge_of(p.N), whole = waves(p.M, p.N);
     if (waves(p.M, p.N - ec) < whole) cols = ec;
     else if (waves(p.M - er, p.N) < whole) rows = er;
@@ -794,32 +863,39 @@ BlockOperand from_row(BlockOperand o, int64_t row) {  // row: a multiple of 128
 
 }  // namespace
 
-// Few rows or tiles.  The few-rows kernel reads B at the rate of memory, but
-// once for each chunk of its rows, and a compute unit runs two of its
-// workgroups at a time at about 7 us for each pair, so it wants long rows or
-// few columns; a tile takes about 4 us and 0.7 us for each block of k however
-// few of its rows are there.  Measured in us, few rows and 128 x 128 tiles:
-// 16x4096x4096 7.7 and 26, 16x16384x4096 20 and 32, 16x32768x2048 33 and 21,
-// 64x4096x4096 14 and 26, 128x4096x4096 24 and 26, 192x4096x4096 35 and 27,
-// 48x16384x4096 43 and 33; 64 experts of 2048x4096 at 8 rows each 134 and
-// 193, at 16 188 and 186; 256 of 1024x2048 at 1 row each 127 and 112; 8 of
-// 1024x2048 at 32 rows each 13 and 17.
-// 256 x 256 tiles hold a compute unit each and are the faster ones where they
-// fill three quarters of the chip: at K = 4096, 128 of them take 50 us where
-// four times as many of 128 x 128 take 45, 192 of them 51 where those take 69.
-BlockKernel block_choose(const BlockProblem &p, bool tiles_only) {
+// The kernel for a problem, by what was measured (us).
+// Few rows.  The few-rows kernel reads B at the rate of memory, but again for
+// each of its parts of 16, 32 or 64 rows, and its workgroups hold a compute
+// unit each: it wants the lowest parts that all run at once.  Against 128 x
+// 128 tiles of two teams: 64x4096x4096 14 and 19, 256x512x5376 16 and 23,
+// 64x8192x4096 25 and 22, 128x4096x4096 25 and 19.  At 16 rows it gains with
+// more workgroups as well, where they are long: 16x12288x4096 16 and 22,
+// 16x16384x4096 21 and 23, 16x32768x2048 33 and 21; at 8, which are mostly
+// waiting for memory, always (64 experts of 2048x4096: 4 rows each 111 and
+// 142, 8 rows each 127 and 133, 12 rows each 157 and 134).
+// Tiles.  128 x 128 of two teams hold a compute unit each, as 256 x 256 do;
+// of one team two share one.  Teams, two and one: 512x4096x4096 23 and 33,
+// 1536x1536x7552 39 and 54; where there are more than 256 tiles
+// 512x16384x4096 46 and 43.  A round of 256 tiles of 256 x 256 takes 5/4 of the
+// time of one of 512 tiles of 128 x 128: of K = 4096, 128 tiles of 256 50 where
+// 512 of 128 take 45, 192 of 256 51 where 768 of 128 take 69; 64 experts of
+// 2048x4096 at 64 rows each 143 and 177, of 1024x2048 at 128 rows each 57 and 44.
+BlockKernel block_choose(const BlockProblem &p, bool general, bool split) {
     if (p.M == 0 || p.N == 0 || p.batch == 0) return BlockKernel::None;
-    if (!tiles_only && p.segments != Segments::Contracted) {
-        // rows of C that share a B: all of them, or about a busy expert's
-        const int64_t rows = p.segments == Segments::Rows ? 2 * ((p.M + p.batch - 1) / p.batch) : p.M;
-        const int64_t groups = p.batch * ((p.N + 15) / 16);  // of 16 columns, a workgroup each
-        const int64_t at_once = 512;
-        if (rows <= 16 ? p.K >= 4096 || groups <= at_once : rows <= 128 && groups * ((rows + 63) / 64) <= at_once)
-            return few_for(rows);
+    if (general) return BlockKernel::Tile256;
+    if (split && p.segments != Segments::Contracted) {
+        const int64_t rows = rows_of(p), groups = p.batch * ((p.N + 15) / 16);  // of 16 columns, a workgroup each
+        for (int64_t height : {16, 32, 64})
+            if (groups <= 256 && rows <= 4096 && groups * ((rows + height - 1) / height) <= 256) return few_for(height);
+        if ((rows <= 16 && groups <= (p.K >= 4096 ? 1024 : 512)) || (rows <= 8 && p.K >= 4096)) return BlockKernel::Few16;
+        if (rows <= 32 && groups <= 512) return BlockKernel::Few32;
     }
-    if (tiles_of(p, p.M, p.N, 256) < 192) return BlockKernel::Tile128;
+    const int64_t tiles = tiles_of(p, p.M, p.N, 128);
+    if (split && tiles <= 256 && p.K > 128) return BlockKernel::Tile128Two;
     int64_t er = 0, ec = 0;
-    if (!tiles_only) edges_of(p, er, ec);
+    if (split) edges_of(p, er, ec);
+    const int64_t whole = 5 * rounds_of(tiles_of(p, p.M - er, p.N - ec, 256), 256) + (er > 0) + (ec > 0);
+    if (4 * rounds_of(tiles, 512) < whole) return BlockKernel::Tile128;
     return er + ec > 0 ? BlockKernel::Tile256Edge : BlockKernel::Tile256;
 }
 
@@ -832,6 +908,7 @@ const char *block_kernel_name(BlockKernel k) {
     case BlockKernel::Few32: return "f8block_few_32";
     case BlockKernel::Few64: return "f8block_few_64";
     case BlockKernel::Tile128: return "f8block_mfma_128";
+    case BlockKernel::Tile128Two: return "f8block_mfma_128_two";
     }
     return "";
 }

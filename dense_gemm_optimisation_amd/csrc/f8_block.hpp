@@ -41,8 +41,9 @@ struct BlockProblem {
     const int32_t *offsets;  // batch + 1, with segments
 };
 
-enum class BlockKernel { None, Tile256, Tile256Edge, Tile128, Few16, Few32, Few64 };
-BlockKernel block_choose(const BlockProblem &p, bool tiles_only);
+enum class BlockKernel { None, Tile256, Tile256Edge, Tile128, Tile128Two, Few16, Few32, Few64 };
+// general: the general kernel, Tile256; split: K and the edges may be split off.
+BlockKernel block_choose(const BlockProblem &p, bool general, bool split);
 const char *block_kernel_name(BlockKernel k);
 hipError_t launch_block(BlockKernel k, const BlockProblem &p, hipStream_t stream);
 

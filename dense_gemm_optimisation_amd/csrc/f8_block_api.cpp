@@ -138,7 +138,8 @@ gemm_status_t block_plan(Segments segments, int64_t M, int64_t N, int64_t K, con
     p.N = row ? N : M;
     p.a = row ? a : b;
     p.b = row ? b : a;
-    k = block_choose(p, (test_switches() & GEMM_TEST_FORCE_GENERAL) != 0);
+    const int switches = test_switches();
+    k = block_choose(p, (switches & GEMM_TEST_FORCE_GENERAL) != 0, (switches & GEMM_TEST_NO_SPLITK) == 0);
     return GEMM_OK;
 }
 

@@ -42,9 +42,10 @@
  *   A block's 128 products are summed by one matrix instruction into fp32,
  *   with that instruction's precision (see gemm_f8 in libgemm.h: products
  *   below 2^-13 of the largest of 8 neighbours are cut off); the scaled block
- *   sums are added in fp32, in order of k, whatever the kernel's tiling except
- *   that the kernels for few rows add the sums of a fixed split of K; the
- *   result is the same on every run.  The rest is gemm_f8's: alpha*acc +
+ *   sums are added in fp32, in order of k within each of up to 8 shares of the
+ *   blocks, and the shares' sums in a fixed order.  How many shares there are
+ *   goes by the sizes of the call, so the result is the same on every run.
+ *   The rest is gemm_f8's: alpha*acc +
  *   beta*C in fp32, rounded to nearest-even into typeC; beta == 0 does not
  *   read C; alpha == 0 or K == 0 gives beta * C.  NaN and infinite codes and
  *   scales propagate.

@@ -111,17 +111,17 @@ def product(lib, rng, M, N, K, fa="e4m3", fb="e4m3", block_a=1, block_b=128, out
     assert torch.equal(after[keep], before[keep])
 
 
-@pytest.fixture(params=["chosen", "tiles"])
+@pytest.fixture(params=["chosen", "unsplit", "general"])
 def kernels(request, switches, lib):
-    """Each case by the kernel the library chooses, and by the tile kernels alone."""
-    if request.param == "tiles":
-        switches(lib.TEST_FORCE_GENERAL)
+    """Each case by the kernel the library chooses, by the tiles of 128 alone (large ones of 256), and by those of 256."""
+    if request.param != "chosen":
+        switches(lib.TEST_FORCE_GENERAL if request.param == "general" else lib.TEST_NO_SPLITK)
     return request.param
 
 
 SHAPES = [(1, 1, 1), (1, 16, 128), (3, 5, 17), (16, 16, 16), (17, 130, 129), (33, 64, 255), (64, 200, 256), (65, 257, 384),
           (128, 128, 1001), (129, 128, 640), (256, 300, 512), (260, 520, 144), (300, 1, 2050), (1, 700, 4096), (16, 513, 1100),
-          (200, 96, 4096)]
+          (200, 96, 4096), (530, 513, 129), (515, 530, 401), (513, 600, 1025)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -149,9 +149,14 @@ def test_product_column_major_and_batched(lib, kernels, M, N, K, blocks):
 
 
 @pytest.mark.parametrize("M,N,K,batch,kernel", [
-    (1, 40, 300, 1, "f8block_few_16"), (20, 40, 300, 1, "f8block_few_32"), (64, 40, 300, 3, "f8block_few_64"),
-    (128, 40, 300, 1, "f8block_few_64"), (129, 40, 300, 1, "f8block_mfma_128"), (16, 8300, 300, 1, "f8block_mfma_128"),
-    (16, 8300, 4100, 1, "f8block_few_16"), (100, 5000, 300, 1, "f8block_mfma_128"), (3500, 3600, 401, 1, "f8block_mfma_256"), (70, 90, 650, 200, "f8block_mfma_256"),
+    (1, 40, 300, 1, "f8block_few_16"), (128, 40, 300, 1, "f8block_few_16"), (1360, 40, 300, 1, "f8block_few_16"),
+    (16, 8300, 300, 1, "f8block_mfma_128_two"), (16, 8300, 4100, 1, "f8block_few_16"), (8, 17000, 4100, 1, "f8block_few_16"),
+    (40, 2000, 300, 1, "f8block_few_32"), (300, 390, 700, 1, "f8block_few_32"), (20, 5000, 300, 1, "f8block_few_32"),
+    (64, 40, 300, 60, "f8block_few_64"), (511, 500, 300, 1, "f8block_few_64"), (513, 500, 273, 1, "f8block_mfma_128_two"),
+    (100, 9000, 129, 1, "f8block_mfma_128_two"), (300, 400, 273, 6, "f8block_mfma_128_two"),
+    (530, 640, 1025, 1, "f8block_mfma_128_two"), (530, 640, 1163, 1, "f8block_mfma_128_two"),
+    (513, 500, 128, 1, "f8block_mfma_128"), (2300, 2400, 777, 1, "f8block_mfma_128"), (3500, 3600, 401, 1, "f8block_mfma_256"),
+    (70, 90, 650, 200, "f8block_mfma_128_two"), (70, 90, 650, 300, "f8block_mfma_128"),
     (3840, 4353, 272, 1, "f8block_mfma_256_edge"), (4144, 3900, 300, 1, "f8block_mfma_256_edge"),
     (4097, 4100, 129, 1, "f8block_mfma_256_edge"), (2049, 2049, 100, 4, "f8block_mfma_256_edge"),
     (4097, 4100, 0, 1, "f8block_mfma_256_edge"),
@@ -267,15 +272,16 @@ def test_experts_random(lib, kernels, fa, fb, out):
 
 def test_experts_kernels(lib):
     rng = np.random.default_rng(21)
-    experts(lib, rng, [1, 0, 9, 20], 70, 300, 0, out="f32", kernel="f8block_few_16")
-    experts(lib, rng, [3, 0, 36, 20], 70, 300, 0, out="f32", kernel="f8block_few_32")
-    experts(lib, rng, [1, 0, 9, 20], 2200, 300, 0, out="f32", kernel="f8block_mfma_128")
-    experts(lib, rng, [1, 0, 9, 20], 2200, 4096, 0, out="f32", kernel="f8block_few_16")
-    experts(lib, rng, [3, 0, 90, 120], 70, 300, 0, out="f32", kernel="f8block_few_64")
-    experts(lib, rng, [300, 0, 90, 120], 70, 300, 0, out="f32", kernel="f8block_mfma_128")
-    experts(lib, rng, [1300, 0, 700, 257], 6000, 200, 11, out="f32", kernel="f8block_mfma_256")
+    for counts, N, K, kernel in (
+            ([1, 0, 9, 20], 70, 300, "few_16"), ([3, 0, 360, 20], 70, 300, "few_16"), ([1, 0, 9, 20], 2200, 300, "mfma_128_two"),
+            ([1, 0, 9, 20], 2200, 4096, "few_16"), ([1, 0, 9, 3], 4200, 4096, "few_16"), ([3, 0, 36, 20], 1200, 300, "few_32"),
+            ([3, 0, 90, 20], 800, 300, "few_64"), ([300, 0, 90, 120], 800, 300, "mfma_128_two"),
+            ([130, 0, 300, 257, 1, 2, 700, 3], 2600, 200, "mfma_128"), ([1300, 0, 700, 257], 5000, 200, "mfma_256")):
+        experts(lib, rng, counts, N, K, 11 if K == 200 else 0, out="f32", kernel="f8block_" + kernel)
     wgrad(lib, rng, [256, 0, 128], 1500, 2600, out="f32", kernel="f8block_mfma_256")
-    wgrad(lib, rng, [256, 0, 128], 150, 260, out="f32", kernel="f8block_mfma_128")
+    wgrad(lib, rng, [256, 0, 128], 150, 260, out="f32", kernel="f8block_mfma_128_two")
+    wgrad(lib, rng, [128] * 12, 600, 500, out="f32", kernel="f8block_mfma_128_two")
+    wgrad(lib, rng, [128, 0, 384] * 4, 600, 700, out="f32", kernel="f8block_mfma_128")
 
 
 @pytest.mark.parametrize("off", [[0, 10, 5, 20], [-4, 3, 900, 7], [2000, -1, 5, 30], [0, 0, 0, 2 ** 31 - 1]])
