@@ -329,6 +329,16 @@ __device__ inline bool coordinates(const TileGrid &g, uint32_t rows, uint32_t wg
 // TEAMS 2: two such groups of waves, each with its own stages, take the blocks
 // of k in turn; at the end each adds the other's sums of half of the rows to
 // its own and stores them.
+//
+// Why 256 x 256 of eight waves of 128 x 64: a stage is 64 KiB read from the
+// second-level cache and 192 KiB from LDS for 2^23 multiply-adds, half of what
+// 128 x 128 tiles read (4096^3 62 us, with those 91).  A step of k takes 1.85
+// us with one factor per row, 2.1 with one per value, where the matrix
+// instructions alone are 0.85 at 2.4 GHz; without the refill 1.14 of 1.56 us
+// (on zeros) remain.  On random values the socket's power limit sets the clock
+// (2.0 to 2.1 GHz): 4096^3 takes 55 us on zeros, 62 on values, 2.2 PFLOP/s.
+// A tile costs another 8 us: coordinates and addresses 1.5, its first stage
+// 1.2 to 5, C about 3.
 template <int FA, int FB, bool PER_COLUMN, int WAVES_M, int WAVES_N, int FM, int FN, int TEAMS>
 __global__ __launch_bounds__(TEAMS *WAVES_M *WAVES_N * 64) void block_tile_kernel(BlockArgs a) {
     constexpr int WAVES = WAVES_M * WAVES_N;  // of a team
@@ -625,7 +635,9 @@ constexpr int FEW_WAVES = 8;
 // straight into registers, the blocks of K dealt to the waves in turn, UNROLL
 // of them in flight per wave.  The waves' sums are added in order through
 // LDS.  Bound by reading B: with 16 columns a chip-wide launch needs only 4096
-// columns, and 128-byte pieces of 16 rows keep whole lines.
+// columns, and 128-byte pieces of 16 rows keep whole lines.  2 rows each of 64
+// experts of 2048 x 4096 take 94 to 98 us, 4.8 TB/s; 16x4096x4096 7.6 us, of
+// which 3.4 are reading.
 template <int FA, int FB, bool PER_COLUMN, int FM, int UNROLL>
 __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) {
     __shared__ f32x4 sums[FEW_WAVES][FM * 64];
