@@ -837,7 +837,8 @@ int64_t tiles_of(const BlockProblem &p, int64_t M, int64_t N, int64_t side) {
     const int64_t cols = (N + side - 1) / side;
     if (p.segments != Segments::Rows) return (M + side - 1) / side * cols * p.batch;
     const double n = double(p.batch < M ? p.batch : M), rows = double(M) / side + 0.5 * n;
-    return int64_t((4.0 * M <= side * n ? n : rows > 1.06 * n ? rows : 1.06 * n) * cols);
+    const double tiles = (4.0 * M <= side * n ? n : rows > 1.06 * n ? rows : 1.06 * n) * cols;
+    return int64_t(tiles < 1e15 ? tiles : 1e15);
 }
 int64_t rounds_of(int64_t tiles, int64_t at_once) { return (tiles + at_once - 1) / at_once; }
 
@@ -896,9 +897,10 @@ BlockKernel block_choose(const BlockProblem &p, bool general, bool split) {
     if (p.M == 0 || p.N == 0 || p.batch == 0) return BlockKernel::None;
     if (general) return BlockKernel::Tile256;
     if (split && p.segments != Segments::Contracted) {
-        const int64_t rows = rows_of(p), groups = p.batch * ((p.N + 15) / 16);  // of 16 columns, a workgroup each
+        const int64_t rows = rows_of(p);
+        const double groups = double(p.batch) * ((p.N + 15) / 16);  // of 16 columns, a workgroup each
         for (int64_t height : {16, 32, 64})
-            if (groups <= 256 && rows <= 4096 && groups * ((rows + height - 1) / height) <= 256) return few_for(height);
+            if (groups * ((rows + height - 1) / height) <= 256) return few_for(height);
         if ((rows <= 16 && groups <= (p.K >= 4096 ? 1024 : 512)) || (rows <= 8 && p.K >= 4096)) return BlockKernel::Few16;
         if (rows <= 32 && groups <= 512) return BlockKernel::Few32;
     }

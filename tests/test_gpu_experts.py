@@ -170,6 +170,52 @@ def test_product_kernels(lib, M, N, K, batch, kernel, blocks):
                 alpha=2.0, beta=1.0, order="col")
 
 
+def test_rows_past_32_bits(lib, kernels):
+    """Operands and C whose rows reach past 2^32 bytes."""
+    rng = np.random.default_rng(32)
+    M, N, K, ld, ldc = 1100, 140, 300, (1 << 22) - 16, 1 << 21
+    a, b = Operand(rng, M, K, "e4m3", 1, True), Operand(rng, N, K, "e4m3", 128, True)
+    wide = torch.empty(M, ld, dtype=torch.uint8, device=DEV)
+    wide[:, :304] = a.codes[0, :, :304]
+    c = torch.empty(M, ldc, dtype=torch.bfloat16, device=DEV)
+    c[:, :N + 1] = 7.0
+    assert wide.numel() > 1 << 32 and c.numel() * 2 > 1 << 32
+    lib.gemm_f8_block(M, N, K, 1.0, wide.data_ptr(), ld, 0, a.scales.data_ptr(), a.lds, 1, *b.args(lib), 0.0, c.data_ptr(), ldc,
+                      0, lib.OUTPUT_BF16)
+    want = a.values[0] @ b.values[0].T
+    check(c[:, :N], want, None, "bf16", True, 3)
+    assert (c[:, N] == 7.0).all()
+    # the same rows as segments, the experts' B apart by more than 2^32 bytes
+    stride = (1 << 32) + 4096
+    apart = torch.empty(stride + N * b.ld, dtype=torch.uint8, device=DEV)
+    for e in (0, 1):
+        apart[e * stride:e * stride + N * b.ld] = b.codes.reshape(-1)
+    offsets = torch.tensor([0, 500, M], dtype=torch.int32, device=DEV)
+    c[:, :N] = 0
+    lib.gemm_experts_f8(2, M, N, K, offsets.data_ptr(), 1.0, wide.data_ptr(), ld, 0, a.scales.data_ptr(), a.lds, apart.data_ptr(),
+                        b.ld, 0, b.scales.data_ptr(), b.lds, 128, stride, 0, 0.0, c.data_ptr(), ldc, lib.OUTPUT_BF16)
+    check(c[:, :N], want, None, "bf16", True, 3)
+
+
+def test_quantize_rows_past_32_bits(lib):
+    rows, cols, ld = 1100, 264, (1 << 22) + 8
+    x = torch.empty(rows, ld, dtype=torch.bfloat16, device=DEV)
+    x[:, :cols] = torch.randn(rows, cols, generator=torch.Generator(DEV).manual_seed(1), device=DEV)
+    near = x[:, :cols].contiguous()
+    index = torch.arange(rows - 1, -1, -1, dtype=torch.int32, device=DEV)
+    for block in (1, 128):
+        got = []
+        for src, ldx, ldq, gather in ((near, cols, cols, None), (x, ld, ld, None), (x, ld, cols, index)):
+            q = torch.empty(rows, ldq, dtype=torch.uint8, device=DEV)
+            s = torch.zeros(3, rows, device=DEV)
+            lib.gemm_f8_block_quantize(rows, cols, src.data_ptr(), ldx, lib.INPUT_BF16, 0 if gather is None else gather.data_ptr(),
+                                       rows, lib.F8_E4M3, block, q.data_ptr(), ldq, s.data_ptr(), rows, 0, 0, 0, 0)
+            got.append((q[:, :cols].clone(), s))
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        if block == 1:
+            assert torch.equal(got[0][0].flip(0), got[2][0]) and torch.equal(got[0][1].flip(1), got[2][1])
+
+
 @pytest.mark.parametrize("M", [5, 300])
 @pytest.mark.parametrize("lds", [0, 1])
 def test_one_row_of_scales_has_no_stride(lib, kernels, M, lds):
