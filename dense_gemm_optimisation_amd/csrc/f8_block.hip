@@ -295,19 +295,30 @@ __device__ inline void store_strip(const BlockProblem &p, const LDS float *strip
 }
 
 // The output tile of workgroup wg, as tile_of numbers them, in 32 bits (the
-// grid has fewer than 2^31 tiles); false past the last of `rows` tile rows.
-__device__ inline bool coordinates(const TileGrid &g, uint32_t rows, uint32_t wg, uint32_t &batch, uint32_t &tm,
-                                   uint32_t &tn) {
+// grid has fewer than 2^31 tiles), and its quarter; false past the last tile
+// of the part, of `rows` tile rows.
+__device__ inline bool coordinates(const TileGrid &g, TilePart part, uint32_t rows, uint32_t wg, uint32_t &batch,
+                                   uint32_t &tm, uint32_t &tn, uint32_t &quarter) {
     const uint32_t cols = uint32_t(g.tiles_n), group = uint32_t(g.group_m);
     // The dispatcher deals workgroups to the 8 dies in turn: those of one die
     // take neighbouring tiles, of the whole grid or (g.xcds 0) of every slice
     // alike: slices of unlike lengths would keep the dies busy for unlike
     // times.
     const uint32_t slice = rows * cols, of = g.xcds == 0 ? wg / slice : 0;
-    const uint32_t total = g.xcds == 0 ? slice : slice * uint32_t(g.batch), q = total / 8, odd = total % 8;
+    uint32_t total = g.xcds == 0 ? slice : slice * uint32_t(g.batch), before = 0;
+    if (part == TilePart::Rest) {
+        before = total - total % ROUND;
+        total = 4 * (total % ROUND);
+    } else if (part == TilePart::Rounds) {
+        total -= total % ROUND;
+    }
+    const uint32_t q = total / 8, odd = total % 8;
     wg -= of * slice;
-    const uint32_t x = wg % 8, id = (x < odd ? x * (q + 1) : odd * (q + 1) + (x - odd) * q) + wg / 8;
+    const uint32_t x = wg % 8;
+    uint32_t id = (x < odd ? x * (q + 1) : odd * (q + 1) + (x - odd) * q) + wg / 8;
     if (wg / 8 >= q + (x < odd ? 1 : 0)) return false;
+    quarter = id % 4;
+    if (part == TilePart::Rest) id = before + id / 4;
     batch = g.xcds == 0 ? of : id / slice;
     const uint32_t local = g.xcds == 0 ? id : id - batch * slice;
     const uint32_t n = local / (group * cols), first = n * group;
@@ -363,18 +374,27 @@ __global__ __launch_bounds__(TEAMS *WAVES_M *WAVES_N * 64) void block_tile_kerne
 
     // With segments of rows the grid has as many tile rows as there can be: the
     // dies share those that there are.
-    uint32_t te, tm, tn;
+    static_assert(BM == BN && (BM == 128 || BM == 256), "tiles of 256, or quarters of them");
+    const bool quarters = BM == 128 && p.part == TilePart::Rest;
+    const int side = quarters ? 2 * BM : BM;
+    uint32_t te, tm, tn, quarter;
     int64_t e, m0, m_end = p.M, k_lo = 0, k_hi = p.K;
     if (p.segments == Segments::Rows) {
         const SegmentTiles first(p, 0, BM, lane);
-        if (!coordinates(a.grid, tile_rows(p, first, a.grid.tiles_m, BM, lane), blockIdx.x, te, tm, tn)) return;
+        const uint32_t rows = tile_rows(p, first, a.grid.tiles_m, BM, lane);
+        if (!coordinates(a.grid, TilePart::All, rows, blockIdx.x, te, tm, tn, quarter)) return;
         if (!find_segment(p, first, uniform(tm), BM, lane, e, m0, m_end)) return;
     } else {
-        if (!coordinates(a.grid, uint32_t(a.grid.tiles_m), blockIdx.x, te, tm, tn)) return;
+        if (!coordinates(a.grid, p.part, uint32_t(a.grid.tiles_m), blockIdx.x, te, tm, tn, quarter)) return;
         e = uniform(te);
-        m0 = uniform(tm) * BM;
+        m0 = uniform(tm) * side;
     }
-    const int64_t n0 = uniform(tn) * BN;
+    int64_t n0 = uniform(tn) * side;
+    if (quarters) {
+        m0 += uniform(quarter >> 1) * BM;
+        n0 += uniform(quarter & 1) * BN;
+        if (m0 >= p.M || n0 >= p.N) return;
+    }
     if (p.segments == Segments::Contracted) {
         if (p.batch <= 64) e = by_length(p, e, lane);
         segment_of(p.offsets, e, p.K, k_lo, k_hi);
@@ -779,20 +799,23 @@ hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
     constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
     BlockArgs a{};
     a.p = p;
-    int64_t tiles_m = (p.M + BM - 1) / BM;
+    const int64_t side = p.part == TilePart::Rest ? 256 : BM;
+    int64_t tiles_m = (p.M + side - 1) / side;
     if (p.segments == Segments::Rows) {  // every segment that is not empty starts a tile
         const int64_t more = p.batch < p.M ? p.batch : p.M;
-        tiles_m = p.M / BM + more < p.M ? p.M / BM + more : p.M;
+        tiles_m = p.M / side + more < p.M ? p.M / side + more : p.M;
     }
-    a.grid = TileGrid{tiles_m, (p.N + BN - 1) / BN, p.segments == Segments::Rows ? 1 : p.batch, 8,
+    a.grid = TileGrid{tiles_m, (p.N + side - 1) / side, p.segments == Segments::Rows ? 1 : p.batch, 8,
                       p.segments == Segments::Contracted ? 0 : 8};
     if (a.grid.tiles_m > 0x7fffffff || a.grid.tiles_n > 0x7fffffff || a.grid.per_batch() > 0x7fffffff ||
         p.batch > 0x7fffffff || a.grid.count() > 0x7fffffff)
         return hipErrorInvalidConfiguration;
     void *args[] = {&a};
+    const int64_t rest = p.part == TilePart::All ? 0 : a.grid.count() % ROUND;
+    const int64_t count = p.part == TilePart::Rest ? 4 * rest : a.grid.count() - rest;
     return hipLaunchKernel(
         reinterpret_cast<const void *>(&block_tile_kernel<FA, FB, PER_COLUMN, WM, WN, FM, FN, TEAMS>),
-        dim3(static_cast<unsigned>(a.grid.count())), dim3(TEAMS * WM * WN * 64), args, 0, stream);
+        dim3(static_cast<unsigned>(count)), dim3(TEAMS * WM * WN * 64), args, 0, stream);
 }
 
 template <int FA, int FB, bool PER_COLUMN>
@@ -893,6 +916,10 @@ BlockOperand from_row(BlockOperand o, int64_t row) {  // row: a multiple of 128
 // time of one of 512 tiles of 128 x 128: of K = 4096, 128 tiles of 256 50 where
 // 512 of 128 take 45, 192 of 256 51 where 768 of 128 take 69; 64 experts of
 // 2048x4096 at 64 rows each 143 and 177, of 1024x2048 at 128 rows each 57 and 44.
+// Up to a quarter of a round past whole rounds runs in quarters of tiles, by
+// two teams, after them: 4608x4096x4096 102 and 84, 9216x4096x8192 301 and 267,
+// 4608x4096x1024 34.6 and 32.1; half a round would not gain (6144x4096x4096 103
+// and 110), nor would most segments of rows, whose rest the host does not know.
 BlockKernel block_choose(const BlockProblem &p, bool general, bool split) {
     if (p.M == 0 || p.N == 0 || p.batch == 0) return BlockKernel::None;
     if (general) return BlockKernel::Tile256;
@@ -908,8 +935,13 @@ BlockKernel block_choose(const BlockProblem &p, bool general, bool split) {
     if (split && tiles <= 256 && p.K > 128) return BlockKernel::Tile128Two;
     int64_t er = 0, ec = 0;
     if (split) edges_of(p, er, ec);
-    const int64_t whole = 5 * rounds_of(tiles_of(p, p.M - er, p.N - ec, 256), 256) + (er > 0) + (ec > 0);
-    if (4 * rounds_of(tiles, 512) < whole) return BlockKernel::Tile128;
+    const int64_t large = tiles_of(p, p.M, p.N, 256), rest = large % ROUND;
+    const int64_t whole = 10 * rounds_of(tiles_of(p, p.M - er, p.N - ec, 256), 256) + 2 * (er > 0) + 2 * (ec > 0);
+    const int64_t small = 8 * rounds_of(tiles, 512), split_off = 10 * (large / ROUND) + 7;
+    if (split && p.segments == Segments::None && p.K >= 1024 && rest > 0 && rest <= ROUND / 4 && large > ROUND &&
+        split_off < (whole < small ? whole : small))
+        return BlockKernel::Tile256Rest;
+    if (small < whole) return BlockKernel::Tile128;
     return er + ec > 0 ? BlockKernel::Tile256Edge : BlockKernel::Tile256;
 }
 
@@ -918,6 +950,7 @@ const char *block_kernel_name(BlockKernel k) {
     case BlockKernel::None: return "";
     case BlockKernel::Tile256: return "f8block_mfma_256";
     case BlockKernel::Tile256Edge: return "f8block_mfma_256_edge";
+    case BlockKernel::Tile256Rest: return "f8block_mfma_256_rest";
     case BlockKernel::Few16: return "f8block_few_16";
     case BlockKernel::Few32: return "f8block_few_32";
     case BlockKernel::Few64: return "f8block_few_64";
@@ -929,11 +962,18 @@ const char *block_kernel_name(BlockKernel k) {
 
 hipError_t launch_block(BlockKernel k, const BlockProblem &p, hipStream_t stream) {
     if (k == BlockKernel::None) return hipSuccess;
+    BlockProblem q = p;
+    if (k == BlockKernel::Tile256Rest) {
+        q.part = TilePart::Rounds;
+        const hipError_t e = launch_formats(BlockKernel::Tile256, q, stream);
+        if (e != hipSuccess) return e;
+        q.part = TilePart::Rest;
+        return launch_formats(BlockKernel::Tile128Two, q, stream);
+    }
     if (k != BlockKernel::Tile256Edge) return launch_formats(k, p, stream);
     int64_t er, ec;
     edges_of(p, er, ec);
     const int64_t M = p.M - er, N = p.N - ec, esize = p.out == 0 ? 4 : 2;
-    BlockProblem q = p;
     q.M = M;
     q.N = N;
     hipError_t e = launch_formats(BlockKernel::Tile256, q, stream);

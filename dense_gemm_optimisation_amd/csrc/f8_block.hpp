@@ -28,6 +28,11 @@ struct BlockOperand {
     int e5m2;
 };
 
+// Which of the 256 x 256 tiles a launch takes: all; those of whole rounds of
+// ROUND tiles; or, in quarters, the others.
+enum class TilePart { All, Rounds, Rest };
+constexpr uint32_t ROUND = 256;
+
 struct BlockProblem {
     Segments segments;
     int64_t M, N, K;  // K = 0 where nothing is multiplied
@@ -37,11 +42,12 @@ struct BlockProblem {
     int64_t ldc, sC;
     int out;  // 0 fp32, 1 bf16, 2 fp16
     bool c_turned;           // C(i, j) at C[j*ldc + i] (few rows only)
+    TilePart part;           // (All with segments)
     int64_t batch;           // slices; with segments, the experts
     const int32_t *offsets;  // batch + 1, with segments
 };
 
-enum class BlockKernel { None, Tile256, Tile256Edge, Tile128, Tile128Two, Few16, Few32, Few64 };
+enum class BlockKernel { None, Tile256, Tile256Edge, Tile256Rest, Tile128, Tile128Two, Few16, Few32, Few64 };
 // general: the general kernel, Tile256; split: K and the edges may be split off.
 BlockKernel block_choose(const BlockProblem &p, bool general, bool split);
 const char *block_kernel_name(BlockKernel k);

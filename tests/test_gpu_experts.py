@@ -160,6 +160,7 @@ def test_product_column_major_and_batched(lib, kernels, M, N, K, blocks):
     (3840, 4353, 272, 1, "f8block_mfma_256_edge"), (4144, 3900, 300, 1, "f8block_mfma_256_edge"),
     (4097, 4100, 129, 1, "f8block_mfma_256_edge"), (2049, 2049, 100, 4, "f8block_mfma_256_edge"),
     (4097, 4100, 0, 1, "f8block_mfma_256_edge"),
+    (4300, 4000, 1030, 1, "f8block_mfma_256_rest"), (1500, 1430, 1024, 8, "f8block_mfma_256_rest"),
 ])
 @pytest.mark.parametrize("blocks", [(1, 128), (1, 1)])
 def test_product_kernels(lib, M, N, K, batch, kernel, blocks):
