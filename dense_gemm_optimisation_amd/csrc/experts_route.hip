@@ -583,21 +583,29 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a, int64_t own, i
     __shared__ int wave_total[THREADS / 64];
     const int E = a.experts, tid = threadIdx.x, lane = tid & 63;
     const int64_t first_block = int64_t(blockIdx.x) * own;
-    auto fill_masks = [&](int64_t block) {
+    // A block's slots, by thread: their experts, on their way while the counts are read.
+    constexpr int SLOTS = BLOCK * ROUTE_MAX_TOP_K / THREADS;
+    int chosen[SLOTS];
+    auto load_ids = [&](int64_t block) {
         const int64_t t0 = block * BLOCK;
-        const int slots = int((a.tokens - t0 < BLOCK ? a.tokens - t0 : BLOCK) * a.top_k);
-        for (int s = tid; s < slots; s += THREADS) {
-            const int e = a.ids[t0 * a.top_k + s];
-            if (e >= 0) atomicOr(&mask[e], 1ull << (s / a.top_k));
-        }
+        const int slots = t0 < a.tokens ? int((a.tokens - t0 < BLOCK ? a.tokens - t0 : BLOCK) * a.top_k) : 0;
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) chosen[i] = tid + i * THREADS < slots ? a.ids[t0 * a.top_k + tid + i * THREADS] : -1;
+        return slots;
     };
+    auto fill_masks = [&]() {
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i)
+            if (chosen[i] >= 0) atomicOr(&mask[chosen[i]], 1ull << ((tid + i * THREADS) / a.top_k));
+    };
+    int slots = load_ids(first_block);
     for (int e = tid; e < E; e += THREADS) {
         mask[e] = 0;
         total[e] = next[e] = 0;
     }
     __syncthreads();
     if (counts == nullptr) {
-        fill_masks(0);
+        fill_masks();
         __syncthreads();
         for (int e = tid; e < E; e += THREADS) total[e] = __popcll(mask[e]);
     } else {
@@ -650,30 +658,31 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a, int64_t own, i
             for (int r = start[e] + total[e] + lane; r < start[e + 1]; r += 64) a.row_tokens[r] = -1;
     for (int64_t r = start[E] + int64_t(blockIdx.x) * THREADS + tid; r < a.rows; r += int64_t(gridDim.x) * THREADS)
         a.row_tokens[r] = -1;
-    for (int64_t i = 0; i < own; ++i) {
-        const int64_t block = first_block + i, t0 = block * BLOCK;
-        if (t0 >= a.tokens) break;
-        if (counts != nullptr) {
-            fill_masks(block);
-            __syncthreads();
-        }
-        const int slots = int((a.tokens - t0 < BLOCK ? a.tokens - t0 : BLOCK) * a.top_k);
-        for (int s = tid; s < slots; s += THREADS) {
-            const int bit = s / a.top_k, e = a.ids[t0 * a.top_k + s];
-            int place = -1;
-            if (e >= 0) {
-                place = start[e] + next[e] + __popcll(mask[e] & ((1ull << bit) - 1));
-                a.row_tokens[place] = int(t0 + bit);
-            }
-            a.places[t0 * a.top_k + s] = place;
-        }
-        if (i + 1 < own) {
+    for (int64_t block = first_block; block < first_block + own && block * BLOCK < a.tokens; ++block) {
+        const int64_t t0 = block * BLOCK;
+        if (block > first_block) {
+            slots = load_ids(block);
             __syncthreads();
             for (int e = tid; e < E; e += THREADS) {
                 next[e] += __popcll(mask[e]);
                 mask[e] = 0;
             }
             __syncthreads();
+        }
+        if (counts != nullptr) {
+            fill_masks();
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            const int s = tid + i * THREADS, bit = s / a.top_k, e = chosen[i];
+            if (s >= slots) continue;
+            int place = -1;
+            if (e >= 0) {
+                place = start[e] + next[e] + __popcll(mask[e] & ((1ull << bit) - 1));
+                a.row_tokens[place] = int(t0 + bit);
+            }
+            a.places[t0 * a.top_k + s] = place;
         }
     }
 }

@@ -94,7 +94,7 @@ struct RouteArgs {
 };
 // Tokens whose choices of one expert a 64-bit mask holds.
 constexpr int ROUTE_BLOCK = 64;
-constexpr int ROUTE_MAX_EXPERTS = 1024;
+constexpr int ROUTE_MAX_EXPERTS = 1024, ROUTE_MAX_TOP_K = 32;
 size_t route_workspace(int64_t tokens, int64_t experts);  // bytes
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
 

@@ -19,7 +19,8 @@ int test_switches();
 
 namespace {
 
-static_assert(GEMM_ROUTE_MAX_EXPERTS == ROUTE_MAX_EXPERTS, "the header's limit is the kernels'");
+static_assert(GEMM_ROUTE_MAX_EXPERTS == ROUTE_MAX_EXPERTS && GEMM_ROUTE_MAX_TOP_K == ROUTE_MAX_TOP_K,
+              "the header's limits are the kernels'");
 
 gemm_status_t status_of(hipError_t e) {
     if (e == hipErrorInvalidConfiguration) return GEMM_ERR_UNSUPPORTED;
