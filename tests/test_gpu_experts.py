@@ -166,9 +166,9 @@ def test_product_column_major_and_batched(lib, kernels, M, N, K, blocks):
 def test_product_kernels(lib, M, N, K, batch, kernel, blocks):
     rng = np.random.default_rng(M)
     product(lib, rng, M, N, K, "e5m2", block_a=blocks[0], block_b=blocks[1], batch=batch, out="f32", kernel=kernel)
-    if kernel.endswith("edge"):
-        product(lib, rng, M, N, K, block_a=blocks[1], block_b=blocks[0], out="f16", kernel=kernel if batch == 1 else None,
-                alpha=2.0, beta=1.0, order="col")
+    if kernel.endswith(("edge", "rest", "two")):
+        product(lib, rng, M, N, K, block_a=blocks[1], block_b=blocks[0], out="f16",
+                kernel=kernel if batch == 1 and not kernel.endswith("two") else None, alpha=2.0, beta=1.0, order="col")
 
 
 def test_rows_past_32_bits(lib, kernels):
@@ -312,9 +312,10 @@ def test_experts_exact(lib, kernels, counts, N, K):
 
 
 @pytest.mark.parametrize("fa,fb,out", [("e4m3", "e4m3", "bf16"), ("e5m2", "e4m3", "f32"), ("e4m3", "e5m2", "bf16")])
-def test_experts_random(lib, kernels, fa, fb, out):
+@pytest.mark.parametrize("N", [300, 707])
+def test_experts_random(lib, kernels, fa, fb, out, N):
     rng = np.random.default_rng(11)
-    experts(lib, rng, [40, 0, 7, 200, 1], 300, 1001, 5, fa, fb, out=out, exact=False, alpha=0.25, beta=0.5)
+    experts(lib, rng, [40, 0, 7, 200, 1], N, 1001, 5, fa, fb, out=out, exact=False, alpha=0.25, beta=0.5, lead=3)
 
 
 def test_experts_kernels(lib):
