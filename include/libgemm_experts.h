@@ -140,7 +140,10 @@ gemm_status_t gemm_f8_block(int64_t M, int64_t N, int64_t K, float alpha,
  *               falls or leaves [0, rows] is cut to what lies within.
  * Rows of C outside every segment are left as they were.  rows is the
  * number of rows the buffers have: the work goes by the segments.  The
- * gradient with respect to A is this call with B_e quantised the other way. */
+ * kernel is chosen by the mean length, so one expert that has most of a small
+ * call's rows takes longer than as many rows spread out.  lda and ldb as for
+ * gemm_f8_block.  The gradient with respect to A is this call with B_e
+ * quantised the other way. */
 gemm_status_t gemm_experts_f8(int64_t experts, int64_t rows, int64_t N, int64_t K,
                               const int32_t *offsets, float alpha,
                               const uint8_t *A, int64_t lda, gemm_f8_format_t formatA,
@@ -157,7 +160,8 @@ gemm_status_t gemm_experts_f8(int64_t experts, int64_t rows, int64_t N, int64_t 
  * positions with block 1 (QT and ST of gemm_f8_block_quantize).  offsets as
  * for gemm_experts_f8, each a multiple of 128 but for the last, so that no
  * block of 128 holds rows of two experts (gemm_experts_route's align);
- * others give wrong sums.  An empty segment gives beta * C_e. */
+ * others give wrong sums.  An empty segment gives beta * C_e.  lda and ldb as
+ * for gemm_f8_block: fewer than 4 Mi positions. */
 gemm_status_t gemm_experts_f8_wgrad(int64_t experts, int64_t M, int64_t N, int64_t rows,
                                     const int32_t *offsets, float alpha,
                                     const uint8_t *A, int64_t lda, gemm_f8_format_t formatA,

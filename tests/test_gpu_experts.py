@@ -377,15 +377,15 @@ def wgrad(lib, rng, counts, M, N, rows=None, fa="e5m2", fb="e4m3", out="bf16", e
     assert torch.equal(after[keep], before[keep])
 
 
-@pytest.mark.parametrize("counts", [[128], [256, 0, 128], [0, 0], [0, 384, 128, 37], [128] * 9, [1]])
+@pytest.mark.parametrize("counts", [[128], [256, 0, 128], [0, 0], [0, 384, 128, 37], [128] * 9, [1], [128, 0] * 40])
 @pytest.mark.parametrize("M,N", [(16, 16), (70, 200), (260, 130)])
-def test_wgrad_exact(lib, counts, M, N):
+def test_wgrad_exact(lib, kernels, counts, M, N):
     rng = np.random.default_rng(sum(counts) + M)
     wgrad(lib, rng, counts, M, N, out="f32")
     wgrad(lib, rng, counts, M, N, beta=1.0, rows=sum(counts) + 100)
 
 
-def test_wgrad_random(lib):
+def test_wgrad_random(lib, kernels):
     rng = np.random.default_rng(12)
     for fa, fb, out in (("e4m3", "e4m3", "f32"), ("e5m2", "e5m2", "bf16"), ("e5m2", "e4m3", "bf16")):
         wgrad(lib, rng, [256, 0, 512, 200], 150, 300, fa=fa, fb=fb, out=out, exact=False, alpha=0.5, beta=1.0)
