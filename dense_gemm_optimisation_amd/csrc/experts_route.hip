@@ -655,7 +655,7 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a, int64_t own, i
     // fillings, a wave each: experts g, g + grid, ..., and a share of what is behind the last segment
     if (a.align > 1)
         for (int64_t e = int64_t(blockIdx.x) * (THREADS / 64) + (tid >> 6); e < E; e += int64_t(gridDim.x) * (THREADS / 64))
-            for (int r = start[e] + total[e] + lane; r < start[e + 1]; r += 64) a.row_tokens[r] = -1;
+            for (int64_t r = int64_t(start[e]) + total[e] + lane; r < start[e + 1]; r += 64) a.row_tokens[r] = -1;
     for (int64_t r = start[E] + int64_t(blockIdx.x) * THREADS + tid; r < a.rows; r += int64_t(gridDim.x) * THREADS)
         a.row_tokens[r] = -1;
     for (int64_t block = first_block; block < first_block + own && block * BLOCK < a.tokens; ++block) {

@@ -662,6 +662,32 @@ def test_route_without_tokens(lib):
     assert off.tolist() == [0] * 9 and tok.tolist() == [-1] * 40
 
 
+@pytest.mark.parametrize("T,E,align", [(238609291, 9, 4)])
+def test_route_rows_up_to_31_bits(lib, T, E, align):
+    """The last segment's filling ends within a wave's width of 2^31: every token to every expert, in index order."""
+    rows, step = lib.experts_rows(T, E, E, align), up(T, align)
+    assert 2 ** 31 - 64 < E * step <= rows < 2 ** 31 and step > T
+    i32 = dict(dtype=torch.int32, device=DEV)
+    logits = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)
+    ids, w = torch.full((T, E), 99, **i32), torch.full((T, E), 99.0, device=DEV)
+    off, tok, pl = torch.full((E + 1,), 99, **i32), torch.full((rows + 100,), 99, **i32), torch.full((T, E), 99, **i32)
+    ws = torch.empty(lib.experts_route_workspace_size(T, E, E), dtype=torch.uint8, device=DEV)
+    lib.gemm_experts_route(T, E, logits.data_ptr(), E, lib.INPUT_BF16, 0, 0, lib.SCORE_SOFTMAX, 1, 1, 1, E, True, 1.0,
+                           ids.data_ptr(), w.data_ptr(), align, rows, off.data_ptr(), tok.data_ptr(), pl.data_ptr(),
+                           ws.data_ptr(), ws.numel())
+    torch.cuda.synchronize()
+    assert off.tolist() == [e * step for e in range(E + 1)]
+    weight, part = np.float32(1) / np.float32(E), 1 << 27
+    for lo in range(0, T, part):
+        at = torch.arange(lo, min(lo + part, T), **i32)
+        s = slice(lo, lo + len(at))
+        for e in range(E):
+            assert torch.equal(tok[e * step:e * step + T][s], at) and torch.equal(pl[s, e], at + e * step)
+            assert bool((ids[s, e] == e).all()) and bool((w[s, e] == float(weight)).all())
+    filling = torch.stack([tok[e * step + T:(e + 1) * step] for e in range(E)])
+    assert bool((filling == -1).all()) and bool((tok[E * step:rows] == -1).all()) and bool((tok[rows:] == 99).all())
+
+
 @pytest.mark.parametrize("T,E,top_k", [(1, 8, 2), (7, 64, 6), (130, 256, 8), (33, 1000, 32), (5, 1, 1), (9, 65, 3), (513, 60, 6),
                                        (515, 16, 16), (600, 200, 8), (514, 24, 2), (513, 128, 4)])
 @pytest.mark.parametrize("type_", QTYPES)
