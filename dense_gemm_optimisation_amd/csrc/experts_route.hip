@@ -767,26 +767,50 @@ __global__ __launch_bounds__(BACK_WAVES * 64) void route_backward_kernel(RouteBa
     store_logits<PER>(a.d_logits, t * a.ldd + first_e, a.type, live ? E - first_e : 0, aligned(a.d_logits, a.ldd), out);
 }
 
+// A launch has fewer than 2^32 threads: more tokens take several.
+constexpr int64_t LAUNCH_THREADS = int64_t(1) << 31;
+
 template <int PER, int WIDTH>
 hipError_t back_go(const RouteBackwardArgs &r, hipStream_t stream) {
-    RouteBackwardArgs a = r;
     constexpr int TOKENS = BACK_WAVES * 64 / WIDTH;
-    const int64_t blocks = (a.tokens + TOKENS - 1) / TOKENS;
-    if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    void *args[] = {&a};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&route_backward_kernel<PER, WIDTH>), dim3(unsigned(blocks)),
-                           dim3(BACK_WAVES * 64), args, 0, stream);
+    constexpr int64_t step = LAUNCH_THREADS / (BACK_WAVES * 64) * TOKENS;
+    const int esize = r.type == 0 ? 4 : 2;
+    for (int64_t t = 0; t < r.tokens; t += step) {
+        RouteBackwardArgs a = r;
+        a.tokens = r.tokens - t < step ? r.tokens - t : step;
+        a.logits = static_cast<const char *>(r.logits) + t * r.ldl * esize;
+        a.ids = r.ids + t * r.top_k;
+        a.d_weights = r.d_weights + t * r.top_k;
+        a.d_logits = static_cast<char *>(r.d_logits) + t * r.ldd * esize;
+        void *args[] = {&a};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&route_backward_kernel<PER, WIDTH>),
+                                             dim3(unsigned((a.tokens + TOKENS - 1) / TOKENS)), dim3(BACK_WAVES * 64),
+                                             args, 0, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 template <int PER, int WIDTH>
 hipError_t choose_go(const RouteArgs &r, int span, uint8_t *counts, hipStream_t stream) {
-    RouteArgs a = r;
-    const int64_t grid = (a.tokens + span - 1) / span;
-    if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
-    const int tokens_per_wave = 64 / WIDTH, waves = (span + tokens_per_wave - 1) / tokens_per_wave;
-    void *args[] = {&a, &span, &counts};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&choose_kernel<PER, WIDTH>), dim3(unsigned(grid)),
-                           dim3(unsigned(waves < choose_waves(PER) ? waves : choose_waves(PER)) * 64), args, 0, stream);
+    const int tokens_per_wave = 64 / WIDTH, all = (span + tokens_per_wave - 1) / tokens_per_wave;
+    const int waves = all < choose_waves(PER) ? all : choose_waves(PER);
+    const int64_t step = LAUNCH_THREADS / (choose_waves(PER) * 64) * span;
+    for (int64_t t = 0; t < r.tokens; t += step) {
+        RouteArgs a = r;
+        a.tokens = r.tokens - t < step ? r.tokens - t : step;
+        a.logits = static_cast<const char *>(r.logits) + t * r.ldl * (r.type == 0 ? 4 : 2);
+        if (r.keep != nullptr) a.keep = r.keep + t;
+        a.ids = r.ids + t * r.top_k;
+        a.weights = r.weights + t * r.top_k;
+        uint8_t *counted = counts == nullptr ? nullptr : counts + t / span * count_pitch(r.experts);
+        void *args[] = {&a, &span, &counted};
+        const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&choose_kernel<PER, WIDTH>),
+                                             dim3(unsigned((a.tokens + span - 1) / span)), dim3(unsigned(waves) * 64),
+                                             args, 0, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // Tokens from which four share a wave, where 16 lanes hold a token's experts:

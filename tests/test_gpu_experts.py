@@ -662,7 +662,7 @@ def test_route_without_tokens(lib):
     assert off.tolist() == [0] * 9 and tok.tolist() == [-1] * 40
 
 
-@pytest.mark.parametrize("T,E,align", [(238609291, 9, 4)])
+@pytest.mark.parametrize("T,E,align", [(238609291, 9, 4), (2 ** 31 - 7, 1, 7)])
 def test_route_rows_up_to_31_bits(lib, T, E, align):
     """The last segment's filling ends within a wave's width of 2^31: every token to every expert, in index order."""
     rows, step = lib.experts_rows(T, E, E, align), up(T, align)
@@ -722,6 +722,24 @@ def test_route_backward(lib, T, E, top_k, type_, sigmoid, renormalise):
     assert np.all(np.abs(got[:, :E] - want) <= tol)
     assert np.all(got[:, E:] == 9.0)
     assert np.all(got[:, :E][want == 0] == 0)
+
+
+@pytest.mark.parametrize("T,E", [(2 ** 28 + 5, 2), (2 ** 26 + 3, 257)])
+def test_route_backward_of_many_tokens(lib, T, E):
+    """More tokens than one launch takes: d = dw * s * (1 - s), s = 1/2, is exact in bf16."""
+    logits = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)
+    ids = torch.arange(T, dtype=torch.int32, device=DEV) % E
+    dw = (torch.arange(T, dtype=torch.int32, device=DEV) % 251).float()
+    d = torch.full((T + 1, E), 9.0, dtype=torch.bfloat16, device=DEV)
+    lib.gemm_experts_route_backward(T, E, logits.data_ptr(), E, lib.INPUT_BF16, lib.SCORE_SIGMOID, 1, False, 1.0, ids.data_ptr(),
+                                    dw.data_ptr(), d.data_ptr(), E)
+    torch.cuda.synchronize()
+    assert bool((d[T] == 9).all())
+    part = 1 << 20 if E > 2 else 1 << 26
+    for lo in range(0, T, part):
+        want = torch.zeros_like(d[lo:lo + part][:T - lo])
+        want.scatter_(1, ids[lo:lo + part, None].long(), dw[lo:lo + part, None].bfloat16() / 4)
+        assert torch.equal(d[lo:min(lo + part, T)], want)
 
 
 # ---------------------------------------------------------------- together
