@@ -215,6 +215,15 @@ __device__ inline float exp_difference(float a, float b) {
     return d > -126.0f ? __builtin_fmaf(e, rest, e) : e;  // (a rest of infinities is no number)
 }
 
+// The sigmoid of x over e^min(top, 0), for x <= top: e^min(x, 0) / (1 + e^-|x|)
+// is the sigmoid, and e^min(top, 0) the largest's but for a factor of 1 to 2.
+// Where e^-top passes 64 bits' range, and the sigmoid of top with it, 0.
+constexpr float SIGMOID_ZERO = -709.7827f;  // the float below -ln of the largest 64-bit number
+__device__ inline float relative_sigmoid(float x, float top) {
+    const float w = exp_difference(fminf(x, 0.0f), fminf(top, 0.0f)) / (1.0f + expf(-fabsf(x)));
+    return top > SIGMOID_ZERO ? w : 0.0f;
+}
+
 // ---- in 64 bits
 
 // The largest x of the wave, and the first lane that has it.  A double is the
@@ -509,11 +518,11 @@ __device__ inline void choose(const RouteArgs &a, int64_t t, bool live, int lane
     }
 
     const float x = id >= 0 ? load_logit(a.logits, t * a.ldl + id, a.type) : NONE;
+    // renormalised: relative to the largest chosen, so the sum cannot vanish
+    if (a.renormalise) top = T::max(x);
     if (a.sigmoid) {
-        w = id >= 0 ? 1.0f / (1.0f + expf(-x)) : 0.0f;
+        w = id < 0 ? 0.0f : a.renormalise ? relative_sigmoid(x, top) : 1.0f / (1.0f + expf(-x));
     } else {
-        // renormalised: relative to the largest chosen, so the sum cannot vanish
-        if (a.renormalise) top = T::max(x);
         w = id >= 0 ? exp_difference(x, top) : 0.0f;
         if (!a.renormalise && id >= 0) w /= sum;
     }

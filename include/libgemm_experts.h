@@ -213,7 +213,8 @@ size_t gemm_experts_route_workspace_size(int64_t tokens, int64_t experts, int64_
  *               only the top_groups of largest rank take part
  *   choice      the top_k largest keys, in falling order
  *   weights     s of the chosen, divided by their sum when `renormalise`
- *               (0 where that sum is 0), times scale
+ *               (0 where that sum is 0 in 64 bits: sigmoids of logits below
+ *               -709), times scale
  * Keys and ranks are compared as if computed exactly (64 bits decide where
  * 32 are too close); equal ones go to the lower index.  A logit, or a logit's
  * key, of -infinity or NaN marks an expert that cannot be chosen and adds

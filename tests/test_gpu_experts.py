@@ -634,6 +634,30 @@ def test_route_masked(lib, T):
     route(lib, x, 6, bias, sigmoid=True)
 
 
+def low_sigmoid_logits(T, E, rng):
+    """Rows around each of these; some of their scores are subnormal in fp32 or below all of it."""
+    base = np.array([-60.0, -80.0, -88.5, -89.0, -95.0, -104.0, -150.0, -200.0, -600.0, -709.0, 0.0])
+    x = base[np.arange(T) % len(base), None] - 3 * rng.random((T, E))
+    x[5::11] = np.where(rng.random((T, E)) < 0.5, -60, -120)[5::11]  # far apart
+    return np.maximum(x.astype(np.float32), np.float32(-709.5))
+
+
+@pytest.mark.parametrize("T,E,top_k", [(44, 2, 2), (44, 64, 6), (550, 64, 6), (33, 300, 8), (520, 200, 16)])
+def test_route_sigmoid_weights_of_low_logits(lib, T, E, top_k):
+    """Renormalised weights depend on the logits' differences: none vanishes with its score."""
+    x = low_sigmoid_logits(T, E, np.random.default_rng(T + E))
+    x[0, :2] = -89, -90  # e / (1 + e)
+    got, want = route(lib, torch.from_numpy(x), top_k, sigmoid=True, renormalise=True, scale=2.0)
+    assert np.all(got >= 0)
+    np.testing.assert_allclose(want.sum(1), 2.0, rtol=1e-12)
+
+
+def test_route_sigmoid_weights_end_with_64_bits(lib):
+    x = torch.tensor([-709.78, -709.79, -1e5, torch.finfo(torch.float32).min])[:, None].repeat(1, 8)
+    _, want = route(lib, x, 4, sigmoid=True)
+    np.testing.assert_array_equal(want[:, 0] > 0, [True, False, False, False])
+
+
 @pytest.mark.parametrize("T", [1, 64, 200, 700])
 def test_route_padding(lib, T):
     rng = np.random.default_rng(T)
