@@ -748,6 +748,51 @@ def test_route_backward(lib, T, E, top_k, type_, sigmoid, renormalise):
     assert np.all(got[:, :E][want == 0] == 0)
 
 
+def low_sigmoid_gradient(x, ids, dw, scale):
+    """d x of scale * sum(dw * w), w the renormalised sigmoids of x at ids: w_i (1 - s_i) (dw_i - sum dw w)."""
+    c = np.take_along_axis(x, ids, 1)
+    s = 1 / (1 + np.exp(-np.maximum(c, -700)))  # only 1 - s is taken of it
+    w = np.exp(c - c.max(1, keepdims=True)) / (1 + np.exp(np.minimum(c, 700)))
+    w = w / w.sum(1, keepdims=True)
+    d = np.zeros_like(x)
+    np.put_along_axis(d, ids, scale * w * (1 - s) * (dw - (dw * w).sum(1, keepdims=True)), 1)
+    return d, scale * (dw * w).sum(1)
+
+
+@pytest.mark.parametrize("T,E,top_k", [(44, 2, 2), (44, 64, 6), (550, 64, 6), (33, 300, 8), (520, 200, 16)])
+@pytest.mark.parametrize("type_", ["f32", "bf16"])
+def test_route_backward_sigmoid_of_low_logits(lib, T, E, top_k, type_):
+    rng = np.random.default_rng(T + E)
+    x = torch.from_numpy(low_sigmoid_logits(T, E, rng))
+    x[0, :2] = torch.tensor([-88.5, -88.6])
+    x[1] = torch.finfo(TORCH[type_]).min  # past 64 bits' range: the weights are 0, and so is their gradient
+    x = x.to(TORCH[type_])
+    v = x.double().numpy()
+    ids = np.stack([rng.permutation(E)[:top_k] for _ in range(T)]).astype(np.int32)
+    ids[0, :2] = 0, 1
+    ids[0, 2:] = np.arange(2, top_k)
+    dw = rng.normal(size=(T, top_k)).astype(np.float32)
+    dw[0, :2] = 2.5, -3
+    ld, i, w = x.to(DEV), torch.from_numpy(ids).to(DEV), torch.from_numpy(dw).to(DEV)
+    d = torch.full((T, E), 9.0, dtype=x.dtype, device=DEV)
+    lib.gemm_experts_route_backward(T, E, ld.data_ptr(), E, lib.INPUT_F32 if type_ == "f32" else lib.INPUT_BF16,
+                                    lib.SCORE_SIGMOID, top_k, True, 1.5, i.data_ptr(), w.data_ptr(), d.data_ptr(), E)
+    got = d.cpu().double().numpy()
+    want, _ = low_sigmoid_gradient(v, ids.astype(np.int64), dw.astype(float), 1.5)
+    want[1] = 0
+    # as for the gradients of ordinary logits
+    tol = HALF[type_] * np.abs(want) + (top_k + 24 + E / 64) * 2.0 ** -24 * 3 * np.abs(dw).max() + 2.0 ** -126
+    assert np.all(np.abs(got - want) <= tol)
+    # the formula against differences: h^2 and 64-bit rounding over h
+    h = 1e-5
+    for e in range(2):
+        up_, down = v.copy(), v.copy()
+        up_[:, e] += h
+        down[:, e] -= h
+        both = [low_sigmoid_gradient(y, ids.astype(np.int64), dw.astype(float), 1.5)[1] for y in (up_, down)]
+        assert np.all(np.abs((both[0] - both[1]) / (2 * h) - want[:, e])[2:] < 1e-7)
+
+
 @pytest.mark.parametrize("T,E", [(2 ** 28 + 5, 2), (2 ** 26 + 3, 257)])
 def test_route_backward_of_many_tokens(lib, T, E):
     """More tokens than one launch takes: d = dw * s * (1 - s), s = 1/2, is exact in bf16."""
