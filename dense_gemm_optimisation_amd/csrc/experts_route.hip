@@ -357,6 +357,11 @@ __device__ inline void group_ranks(const RouteArgs &a, const float (&key)[PER], 
         const bool two = a.group_top == 2 && second > NONE;
         r = two ? first + second : first;
         z = first > NONE ? fabsf(first) + (two ? fabsf(second) : 0.0f) : 0.0f;
+        // a sum past fp32 (two biases of its lowest value, say) is no rank: its error has no end
+        if (two && fabsf(r) == INFINITY && fabsf(first) < INFINITY) {
+            r = first;
+            z = INFINITY;
+        }
     };
     if (per % PER == 0 && width <= 16 && (width & (width - 1)) == 0) {
         // a group is `width` lanes, a power of two: its two largest come together in log2 steps

@@ -634,6 +634,25 @@ def test_route_masked(lib, T):
     route(lib, x, 6, bias, sigmoid=True)
 
 
+@pytest.mark.parametrize("T,E,groups", [(40, 64, 8), (530, 64, 8), (40, 60, 4), (530, 60, 4), (530, 1000, 10)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_route_groups_with_biases_at_the_ends_of_fp32(lib, T, E, groups, sigmoid):
+    """A group masked by its biases' lowest value ranks behind the others, but before one that has nothing to choose."""
+    rng = np.random.default_rng(E)
+    x = torch.from_numpy(rng.normal(size=(T, E))).float()
+    per, (low, high) = E // groups, (np.finfo(np.float32).min, np.finfo(np.float32).max)
+    x[::3, :per] = -float("inf")
+    bias = rng.normal(size=E) * 0.1
+    bias[per:] = low
+    route(lib, x, 4, bias, sigmoid=sigmoid, groups=groups, top_groups=2, group_top=2)
+    bias[2 * per:] = high / 1.5  # two such sums are equal, a third is larger
+    bias[3 * per:] = high
+    route(lib, x, 4, bias, sigmoid=sigmoid, groups=groups, top_groups=2, group_top=2)
+    bias[2 * per] = bias[2 * per + 1] = np.inf
+    bias[3 * per + 1] = -np.inf
+    route(lib, x, 4, bias, sigmoid=sigmoid, groups=groups, top_groups=3, group_top=2)
+
+
 def low_sigmoid_logits(T, E, rng):
     """Rows around each of these; some of their scores are subnormal in fp32 or below all of it."""
     base = np.array([-60.0, -80.0, -88.5, -89.0, -95.0, -104.0, -150.0, -200.0, -600.0, -709.0, 0.0])
