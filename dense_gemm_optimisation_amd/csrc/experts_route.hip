@@ -226,20 +226,30 @@ __device__ inline float relative_sigmoid(float x, float top) {
 
 // ---- in 64 bits
 
-// The largest x of the wave, and the first lane that has it.  A double is the
-// sum of three floats, each the rest's nearest: they order as it does, so the
-// largest is found by three reductions of floats, which are far quicker than
-// one of doubles.
+// Over the wave, in every lane.
+__device__ inline uint32_t wave_max(uint32_t x) {
+    auto step = [&](int o) { x = uint32_t(o) > x ? uint32_t(o) : x; };
+    step(__builtin_amdgcn_update_dpp(int(x), int(x), 0x111, 0xf, 0xf, false));
+    step(__builtin_amdgcn_update_dpp(int(x), int(x), 0x112, 0xf, 0xf, false));
+    step(__builtin_amdgcn_update_dpp(int(x), int(x), 0x114, 0xf, 0xf, false));
+    step(__builtin_amdgcn_update_dpp(int(x), int(x), 0x118, 0xf, 0xf, false));
+    step(__builtin_amdgcn_update_dpp(int(x), int(x), 0x142, 0xa, 0xf, false));
+    step(__builtin_amdgcn_update_dpp(int(x), int(x), 0x143, 0xc, 0xf, false));
+    return __builtin_amdgcn_readlane(x, 63);
+}
+// The largest x of the wave, and the first lane that has it.  The bits of a
+// number order as it does once a negative one's are all turned and a positive
+// one's sign is, so the largest is found by reductions of their halves, which
+// are far quicker than one of doubles.
 __device__ inline double wave_max(double x, int &owner) {
-    const float a = float(x);
-    const bool whole = !(a > -INFINITY && a < INFINITY);
-    const double rest = whole ? 0.0 : x - double(a);
-    const float b = float(rest), c = float(rest - double(b));
-    const float top_a = wave_max(a);
-    const float top_b = wave_max(a == top_a ? b : NONE);
-    const float top_c = wave_max(a == top_a && b == top_b ? c : NONE);
-    owner = __builtin_ctzll(__ballot(a == top_a && b == top_b && c == top_c));
-    return double(top_a) + (double(top_b) + double(top_c));
+    constexpr uint64_t SIGN = uint64_t(1) << 63;
+    const uint64_t b = __builtin_bit_cast(uint64_t, x + 0.0);  // (-0 as 0)
+    const uint64_t order = b & SIGN ? ~b : b | SIGN;
+    const uint32_t high = uint32_t(order >> 32), low = uint32_t(order);
+    const uint32_t top_high = wave_max(high), top_low = wave_max(high == top_high ? low : 0u);
+    owner = __builtin_ctzll(__ballot(high == top_high && low == top_low));
+    const uint64_t top = uint64_t(top_high) << 32 | top_low;
+    return __builtin_bit_cast(double, top & SIGN ? top ^ SIGN : ~top);
 }
 __device__ inline double lane_of(double x, int lane) {
     const uint64_t b = __builtin_bit_cast(uint64_t, x);

@@ -608,6 +608,24 @@ def test_route_ties_and_near_ties(lib, T):
     route(lib, steps, 8, rng.integers(0, 2, 64) * 1e-8, groups=4, top_groups=2, group_top=2)
 
 
+@pytest.mark.parametrize("T,E", [(40, 64), (530, 64), (33, 300)])
+def test_route_keys_below_fp32(lib, T, E):
+    """Scores that are zero or subnormal in fp32 and differ in 64 bits; the logits' steps are far above 64 bits' errors."""
+    rng = np.random.default_rng(3)
+    steps = np.stack([rng.permutation(E) for _ in range(T)])
+    for low in (-85.0, -95.0, -110.0, -300.0, -600.0):
+        x = torch.from_numpy(low - steps / 4.0).float()
+        route(lib, x, 8, np.zeros(E), sigmoid=True, renormalise=False)
+        x[:, 0] = 0  # softmax: all others small beside it
+        route(lib, x, 8, np.zeros(E), renormalise=False)
+        if E % 4 == 0:
+            route(lib, x, 8, np.zeros(E), sigmoid=True, groups=4, top_groups=2, group_top=2, renormalise=False)
+    # keys that differ in their last bits at a size where fp32 has fewer than three such parts
+    bias = 2.0 ** -130 + rng.integers(0, 4, E) * 2.0 ** -149
+    route(lib, torch.full((T, E), -1000.0), 8, bias, sigmoid=True, renormalise=False)
+    route(lib, torch.full((T, E), -1000.0), 8, -bias, sigmoid=True, renormalise=False)
+
+
 @pytest.mark.parametrize("T", [40, 530])
 def test_route_masked(lib, T):
     rng = np.random.default_rng(2)
