@@ -398,8 +398,9 @@ __global__ __launch_bounds__(TEAMS *WAVES_M *WAVES_N * 64) void block_tile_kerne
     if (p.segments == Segments::Contracted) {
         if (p.batch <= 64) e = by_length(p, e, lane);
         segment_of(p.offsets, e, p.K, k_lo, k_hi);
-        k_lo = uniform(k_lo) & ~int64_t(127);
+        k_lo = uniform(k_lo);
         k_hi = uniform(k_hi);
+        k_lo = k_hi > k_lo ? k_lo & ~int64_t(127) : k_hi;  // (an empty segment may start anywhere)
     }
     const int K = int(uniform(k_hi - k_lo));  // at most ld < 2^22
     const int64_t ea = p.segments == Segments::None ? e : 0;

@@ -158,10 +158,10 @@ gemm_status_t gemm_experts_f8(int64_t experts, int64_t rows, int64_t N, int64_t 
  * alpha * sum over t in [offsets[e], offsets[e+1]) of A(i, t) B(t, j) + beta * C_e.
  * A is an operand of M rows and B one of N rows, both contracted over `rows`
  * positions with block 1 (QT and ST of gemm_f8_block_quantize).  offsets as
- * for gemm_experts_f8, each a multiple of 128 but for the last, so that no
- * block of 128 holds rows of two experts (gemm_experts_route's align);
- * others give wrong sums.  An empty segment gives beta * C_e.  lda and ldb as
- * for gemm_f8_block: fewer than 4 Mi positions. */
+ * for gemm_experts_f8; a segment that is not empty starts at a multiple of
+ * 128, so that no block of 128 holds rows of two experts (gemm_experts_route's
+ * align); others give wrong sums.  An empty segment, wherever it starts, gives
+ * beta * C_e.  lda and ldb as for gemm_f8_block: fewer than 4 Mi positions. */
 gemm_status_t gemm_experts_f8_wgrad(int64_t experts, int64_t M, int64_t N, int64_t rows,
                                     const int32_t *offsets, float alpha,
                                     const uint8_t *A, int64_t lda, gemm_f8_format_t formatA,

@@ -385,6 +385,15 @@ def test_wgrad_exact(lib, kernels, counts, M, N):
     wgrad(lib, rng, counts, M, N, beta=1.0, rows=sum(counts) + 100)
 
 
+@pytest.mark.parametrize("counts", [[256, 37, 0, 0], [256, 44, 0], [1, 0], [5] + [0] * 70, [300] + [0] * 3])
+@pytest.mark.parametrize("M,N", [(16, 16), (260, 130)])
+def test_wgrad_empty_behind_a_ragged_segment(lib, kernels, counts, M, N):
+    """Nothing of the ragged segment's last block comes to the experts behind it."""
+    rng = np.random.default_rng(sum(counts))
+    wgrad(lib, rng, counts, M, N, out="f32")
+    wgrad(lib, rng, counts, M, N, beta=1.0, rows=sum(counts) + 100)
+
+
 def test_wgrad_random(lib, kernels):
     rng = np.random.default_rng(12)
     for fa, fb, out in (("e4m3", "e4m3", "f32"), ("e5m2", "e5m2", "bf16"), ("e5m2", "e4m3", "bf16")):
