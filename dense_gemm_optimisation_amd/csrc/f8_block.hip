@@ -618,6 +618,7 @@ __global__ __launch_bounds__(TEAMS *WAVES_M *WAVES_N * 64) void block_tile_kerne
                 acc[i][j] = (team == 0 ? acc[i][j] : acc[HALF + i][j]) + others[(i * FN + j) * WAVES * 64];
     }
     constexpr int ROWS = FM / TEAMS;  // of blocks that this team stores
+    const float alpha = K > 0 ? p.alpha : 0.0f;  // no terms: beta * C, whatever alpha is
     const bool plain = mrows == BM && nrows == BN && p.beta == 0.0f;
     char *c = static_cast<char *>(p.C) + (ec * p.sC + m0 * p.ldc + n0) * (p.out == 0 ? 4 : 2);
 #pragma unroll
@@ -629,7 +630,7 @@ __global__ __launch_bounds__(TEAMS *WAVES_M *WAVES_N * 64) void block_tile_kerne
             for (int j = 0; j < FN; ++j) {
                 const int q = j * 4 + (lane >> 4);
                 *reinterpret_cast<LDS f32x4 *>(strip + (k * 16 + r) * WTN + ((q ^ r) & (FN * 4 - 1)) * 4) =
-                    p.alpha * acc[i + k][j];
+                    alpha * acc[i + k][j];
             }
         const int m = wm * WTM + (team * ROWS + i) * 16, n = wn * WTN;
         if (p.out == 0) store_strip<0, FN, PAIR * 16>(p, strip, c, m, mrows, n, nrows, plain, lane);
@@ -760,7 +761,7 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) 
             if (m < m_hi && col < p.N) {
                 const int64_t at = ec * p.sC + (p.c_turned ? col * p.ldc + m : m * p.ldc + col);
                 const int left = p.N - col < 4 ? int(p.N - col) : 4;
-                v *= p.alpha;
+                v *= p.K > 0 ? p.alpha : 0.0f;  // no terms: beta * C, whatever alpha is
                 const float x[4] = {v[0], v[1], v[2], v[3]};
                 auto store = [&](int64_t to, const float *y, int n) {
                     if (p.out == 0) store_columns<0, 4>(p, static_cast<char *>(p.C), to, y, n);

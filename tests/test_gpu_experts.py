@@ -246,6 +246,25 @@ def test_product_without_terms(lib, kernels, M, N):
         product(lib, rng, M, N, 256, alpha=0.0, beta=beta)
 
 
+@pytest.mark.parametrize("alpha", [float("inf"), float("nan")])
+def test_no_terms_whatever_alpha_is(lib, kernels, alpha):
+    rng = np.random.default_rng(7)
+    for M, N in ((3, 20), (70, 300), (300, 300)):
+        for beta in (0.0, 0.5):
+            c = start(rng, (M, N), "f32", True)
+            want = beta * c
+            lib.gemm_f8_block(M, N, 0, alpha, 0, 0, 0, 0, 0, 1, 0, 0, 0, 0, 0, 1, beta, c.data_ptr(), N, 0, lib.OUTPUT_F32)
+            assert torch.equal(c, want)
+    # experts with and without rows: the empty ones' gradients have no terms
+    a, b = Operand(rng, 40, 256, "e4m3", 1, True), Operand(rng, 52, 256, "e4m3", 1, True)
+    c = start(rng, (3, 40, 52), "f32", True)
+    want = 2 * c
+    offsets = torch.tensor([0, 0, 256, 256], dtype=torch.int32, device=DEV)
+    lib.gemm_experts_f8_wgrad(3, 40, 52, 256, offsets.data_ptr(), alpha, *a.args(lib, False), *b.args(lib, False), 2.0,
+                              c.data_ptr(), 52, c.stride(0), lib.OUTPUT_F32)
+    assert torch.equal(c[0], want[0]) and torch.equal(c[2], want[2]) and not c[1].isfinite().all()
+
+
 @pytest.mark.parametrize("M", [2, 200])
 def test_product_nan_and_infinity(lib, kernels, M):
     rng = np.random.default_rng(6)
