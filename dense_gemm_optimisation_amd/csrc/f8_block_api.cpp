@@ -42,9 +42,10 @@ bool any_over(std::initializer_list<int64_t> sizes) {
         if (s < 0 || s > MOST) return true;
     return false;
 }
-// (n - 1) * stride + span leaves int64.
+// (n - 1) * stride + span elements, of up to 4 bytes, leave the address space.
+constexpr int64_t MOST_EXTENT = INT64_MAX / 8;
 bool extent_over(int64_t n, int64_t stride, int64_t span) {
-    return n > 1 && (too_big(n - 1, stride) || (n - 1) * stride > INT64_MAX / 8 - span);
+    return span > MOST_EXTENT || (n > 1 && (too_big(n - 1, stride) || (n - 1) * stride > MOST_EXTENT - span));
 }
 
 // Checks one operand of R rows over K and gives the ranges it touches.  The
@@ -100,8 +101,7 @@ gemm_status_t block_plan(Segments segments, int64_t M, int64_t N, int64_t K, con
     const int esize = type_bytes(typeC);
     const int64_t span_c = span(M, N, orderC, ldc);
     if (C == nullptr || misaligned(C, esize)) return GEMM_ERR_INVALID_ARG;
-    if (slices_c > 1 && (strideC < span_c || extent_over(slices_c, strideC, span_c)))
-        return GEMM_ERR_INVALID_ARG;
+    if ((slices_c > 1 && strideC < span_c) || extent_over(slices_c, strideC, span_c)) return GEMM_ERR_INVALID_ARG;
     const Range rc = range_of(C, span_c, slices_c, strideC, esize);
     if (segments != Segments::None) {
         if (offsets == nullptr || misaligned(offsets, 4)) return GEMM_ERR_INVALID_ARG;
@@ -370,6 +370,7 @@ gemm_status_t gemm_experts_route(int64_t tokens, int64_t experts, const void *lo
     const bool layout = offsets != nullptr || row_tokens != nullptr || places != nullptr;
     const int esize = type_bytes(in);
     const int64_t slots = tokens * top_k;
+    if (extent_over(tokens, ldl, experts)) return GEMM_ERR_INVALID_ARG;
     const Range rl = range_of(logits, tokens > 0 ? (tokens - 1) * ldl + experts : 0, 1, 0, esize);
     const Range rb = range_of(bias, bias != nullptr ? experts : 0, 1, 0, 4);
     const Range rk = range_of(keep, keep != nullptr ? tokens : 0, 1, 0, 1);
@@ -425,6 +426,7 @@ gemm_status_t gemm_experts_route_backward(int64_t tokens, int64_t experts, const
         misaligned(logits, esize) || misaligned(d_logits, esize) || misaligned(ids, 4) ||
         misaligned(d_weights, 4))
         return GEMM_ERR_INVALID_ARG;
+    if (extent_over(tokens, ldl, experts) || extent_over(tokens, ldd, experts)) return GEMM_ERR_INVALID_ARG;
     const Range rd = range_of(d_logits, (tokens - 1) * ldd + experts, 1, 0, esize);
     if (overlap(rd, range_of(logits, (tokens - 1) * ldl + experts, 1, 0, esize)) ||
         overlap(rd, range_of(ids, tokens * top_k, 1, 0, 4)) ||

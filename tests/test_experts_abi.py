@@ -238,3 +238,34 @@ def test_route_backward_refuses(lib, bad):
              d_weights=WEIGHTS, d_logits=C, ldd=64)
     assert lib.gemm_experts_route_backward(**{**d, **bad}, raise_on_error=False) == lib.ERR_INVALID_ARG
     assert lib.gemm_experts_route_backward(**{**d, "tokens": 0, "ids": 0}, raise_on_error=False) == lib.OK
+
+
+# ---- extents whose bytes leave the address space
+FAR = 1 << 40
+
+
+@pytest.mark.parametrize("bad", [
+    dict(M=FAR, ldsa=FAR, ldc=1 << 22), dict(M=FAR, ldsa=FAR, ldc=1 << 22, type_c=0), dict(M=1, ldsa=1, N=FAR, ldc=FAR, ldsb=FAR, ldb=1 << 22),
+    dict(M=1, ldsa=1, N=128, K=FAR, lda=FAR, ldb=FAR, ldc=128, ldsb=1 << 29), dict(M=FAR, N=1, ldsa=FAR, K=0, ldc=1 << 22, type_c=0),
+])
+def test_block_product_refuses_extents(lib, bad):
+    assert block_call(lib, **bad) == lib.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [
+    dict(rows=FAR, ldx=1 << 22, Q=0, S=0, ldqt=FAR, in_type=0), dict(rows=FAR, Q=0, S=0, ldqt=FAR, ldst=1 << 29),
+    dict(rows=FAR, QT=0, ST=0, ldq=1 << 22, lds=FAR), dict(index=OFF, x_rows=FAR, ldx=1 << 22, in_type=0),
+])
+def test_quantize_refuses_extents(lib, bad):
+    assert quantize_call(lib, **bad) == lib.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("tokens,ld", [(2 ** 31 - 1, FAR), (1 << 23, FAR), (2 ** 31 - 1, 1 << 31), (1 << 30, 1 << 31)])
+@pytest.mark.parametrize("in_type", [0, 1])
+def test_routing_refuses_extents(lib, tokens, ld, in_type):
+    alone = dict(offsets=0, row_tokens=0, places=0, bias=0, keep=0, ids=1 << 50, weights=1 << 51)
+    assert route_call(lib, tokens=tokens, ldl=ld, in_type=in_type, **alone) == lib.ERR_INVALID_ARG
+    d = dict(tokens=tokens, experts=64, logits=X, ldl=64, in_type=in_type, score=0, top_k=6, renormalise=False, scale=1.0,
+             ids=1 << 50, d_weights=1 << 51, d_logits=1 << 52, ldd=64)
+    for k in ("ldl", "ldd"):
+        assert lib.gemm_experts_route_backward(**{**d, k: ld}, raise_on_error=False) == lib.ERR_INVALID_ARG
