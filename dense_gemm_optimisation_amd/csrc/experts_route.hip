@@ -792,7 +792,7 @@ __global__ __launch_bounds__(BACK_WAVES * 64) void route_backward_kernel(RouteBa
     store_logits<PER>(a.d_logits, t * a.ldd + first_e, a.type, live ? E - first_e : 0, aligned(a.d_logits, a.ldd), out);
 }
 
-// A launch has fewer than 2^32 threads: more tokens take several.
+// Threads of a launch, which has fewer than 2^32: more tokens take several.
 constexpr int64_t LAUNCH_THREADS = int64_t(1) << 31;
 
 template <int PER, int WIDTH>

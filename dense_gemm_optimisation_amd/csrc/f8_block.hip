@@ -789,7 +789,7 @@ hipError_t few_go(const BlockProblem &p, hipStream_t stream) {
     a.p = p;
     a.grid.tiles_n = (p.N + 15) / 16;
     a.grid.tiles_m = (rows_of(p) + 16 * FM - 1) / (16 * FM);  // (an expert with more rows takes several turns)
-    if (double(a.grid.tiles_n) * a.grid.tiles_m * p.batch > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (launch_over(double(a.grid.tiles_n) * a.grid.tiles_m * p.batch, FEW_WAVES * 64)) return hipErrorInvalidConfiguration;
     const int64_t count = a.grid.tiles_n * a.grid.tiles_m * p.batch;
     void *args[] = {&a};
     return hipLaunchKernel(reinterpret_cast<const void *>(&block_few_kernel<FA, FB, PER_COLUMN, FM, UNROLL>),
@@ -798,7 +798,7 @@ hipError_t few_go(const BlockProblem &p, hipStream_t stream) {
 
 template <int FA, int FB, bool PER_COLUMN, int WM, int WN, int FM, int FN, int TEAMS>
 hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
-    constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
+    constexpr int BM = WM * FM * 16;  // tiles are square
     BlockArgs a{};
     a.p = p;
     const int64_t side = p.part == TilePart::Rest ? 256 : BM;
@@ -809,8 +809,8 @@ hipError_t tile_go(const BlockProblem &p, hipStream_t stream) {
     }
     a.grid = TileGrid{tiles_m, (p.N + side - 1) / side, p.segments == Segments::Rows ? 1 : p.batch, 8,
                       p.segments == Segments::Contracted ? 0 : 8};
-    if (a.grid.tiles_m > 0x7fffffff || a.grid.tiles_n > 0x7fffffff || a.grid.per_batch() > 0x7fffffff ||
-        p.batch > 0x7fffffff || a.grid.count() > 0x7fffffff)
+    // (also of the quarters' four times `rest`, which is below ROUND)
+    if (launch_over(double(a.grid.tiles_m) * a.grid.tiles_n * a.grid.batch, TEAMS * WM * WN * 64))
         return hipErrorInvalidConfiguration;
     void *args[] = {&a};
     const int64_t rest = p.part == TilePart::All ? 0 : a.grid.count() % ROUND;
@@ -878,7 +878,11 @@ void edges_of(const BlockProblem &p, int64_t &rows, int64_t &cols) {
     rows = cols = 0;
     if (p.segments != Segments::None) return;
     auto waves = [&](int64_t M, int64_t N) { return rounds_of(tiles_of(p, M, N, 256), 256); };
-    const int64_t er = edge_of(p.M), ec = edge_of(p.N), whole = waves(p.M, p.N);
+    // (an edge that one launch does not take stays in the tiles)
+    auto edge = [&](int64_t n, int64_t other) {
+        return launch_over(double((other + 15) / 16) * p.batch, FEW_WAVES * 64) ? 0 : edge_of(n);
+    };
+    const int64_t er = edge(p.M, p.N), ec = edge(p.N, p.M), whole = waves(p.M, p.N);
     if (waves(p.M, p.N - ec) < whole) cols = ec;
     else if (waves(p.M - er, p.N) < whole) rows = er;
     else if (waves(p.M - er, p.N - ec) < whole) rows = er, cols = ec;

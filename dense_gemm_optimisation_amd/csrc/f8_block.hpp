@@ -17,6 +17,9 @@ namespace libgemm {
 // with its own C).
 enum class Segments : int { None = 0, Rows = 1, Contracted = 2 };
 
+// A launch has fewer than 2^32 threads.
+inline bool launch_over(double workgroups, int threads) { return workgroups * threads >= 4294967296.0; }
+
 // Operand X of R rows: code (r, k) at x[r*ld + k], scale (r, kb) at
 // s[kb*lds + (r >> shift)], shift 0 (a scale per row) or 7 (per 128 rows).
 struct BlockOperand {

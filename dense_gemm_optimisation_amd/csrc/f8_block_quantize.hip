@@ -425,7 +425,7 @@ hipError_t go(const QuantizeArgs &q, hipStream_t stream) {
     const bool by_rows = a.qt == nullptr && a.block == 1;
     const int units = ((a.rows + 63) / 64) * cols * a.batch >= 512 ? 4 : 1;
     const int64_t height = by_rows ? 16 * units : TILE, rows = (a.rows + height - 1) / height;
-    if (double(rows) * cols * a.batch > 0x7fffffff) return hipErrorInvalidConfiguration;
+    if (launch_over(double(rows) * cols * a.batch, 256)) return hipErrorInvalidConfiguration;
     uint32_t grid_rows = uint32_t(rows), grid_cols = uint32_t(cols);
     void *args[] = {&a, &grid_rows, &grid_cols};
     const void *kernel = !by_rows    ? reinterpret_cast<const void *>(&quantize_tile_kernel<TYPE, STREAM>)

@@ -54,6 +54,9 @@
  * owns every buffer, a call only enqueues on `stream`, keeps nothing between
  * calls, and may be captured into a graph; every argument that the host can
  * see is checked before any HIP call, and an invalid call changes nothing.
+ * A call that one launch of fewer than 2^32 threads does not hold (2^23 tiles
+ * of a product, 2^24 blocks of 64 rows and 128 columns to quantise) is
+ * GEMM_ERR_UNSUPPORTED.
  * What only the device can see (offsets, indices) is held within the
  * documented buffers there: bad values give wrong rows, never an access
  * outside.  Two calls that share an output or a workspace must be ordered by

@@ -269,3 +269,27 @@ def test_routing_refuses_extents(lib, tokens, ld, in_type):
              ids=1 << 50, d_weights=1 << 51, d_logits=1 << 52, ldd=64)
     for k in ("ldl", "ldd"):
         assert lib.gemm_experts_route_backward(**{**d, k: ld}, raise_on_error=False) == lib.ERR_INVALID_ARG
+
+
+# ---- calls past one launch
+FAR_C = 1 << 50
+
+
+def test_no_edge_past_one_launch(lib):
+    """The last column as a launch of its own would have 2^24 workgroups; it stays in the tiles."""
+    d = dict(M=1 << 28, N=257, K=16, alpha=1.0, A=A, lda=16, format_a=0, scale_a=SA, ldsa=1 << 28, block_a=1, B=B, ldb=16,
+             format_b=0, scale_b=SB, ldsb=3, block_b=128, beta=0.0, C=FAR_C, ldc=257, order_c=0, type_c=1)
+    assert lib.f8_block_kernel_name(**d) == "f8block_mfma_256"
+    assert lib.f8_block_kernel_name(**{**d, "M": 1 << 20}) == "f8block_mfma_256_edge"
+    col = {**d, "M": 257, "N": 1 << 28, "ldsa": 257, "ldsb": 1 << 21, "ldc": 1 << 28}
+    assert lib.f8_block_kernel_name(**col) == "f8block_mfma_256"
+    assert lib.f8_block_kernel_name(**{**col, "N": 1 << 20}) == "f8block_mfma_256_edge"
+
+
+def test_launches_past_the_limit_are_unsupported(lib):
+    assert block_call(lib, M=300, batch=1 << 23, C=FAR_C, stride_c=300 * 96, ldsa=300) == lib.ERR_UNSUPPORTED
+    assert block_call(lib, M=8, K=8, batch=1 << 24, C=FAR_C, stride_c=8 * 96) == lib.ERR_UNSUPPORTED
+    assert experts_call(lib, experts=1 << 23, N=1024, rows=(1 << 31) - 1, ldsa=1 << 31, C=FAR_C, ldc=1024, ldsb=8, stride_b=0,
+                        stride_scale_b=0, K=16, offsets=1 << 51) == lib.ERR_UNSUPPORTED
+    assert quantize_call(lib, rows=1 << 32, cols=1024, ldx=1024, lds=1 << 32, ldq=1024, QT=0, ST=0, X=FAR_C, Q=1 << 52,
+                         S=1 << 53) == lib.ERR_UNSUPPORTED
