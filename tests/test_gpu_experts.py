@@ -691,6 +691,9 @@ def test_route_groups_with_biases_at_the_ends_of_fp32(lib, T, E, groups, sigmoid
     bias = rng.normal(size=E) * 0.1
     bias[per:] = low
     route(lib, x, 4, bias, sigmoid=sigmoid, groups=groups, top_groups=2, group_top=2)
+    # no rank is finite in fp32: groups with nothing to choose first, then some whose ranks differ
+    route(lib, x, 4, bias, sigmoid=sigmoid, groups=groups, top_groups=1, group_top=2)
+    route(lib, x, 4, np.where(np.arange(E) < E - per, high / 1.5, high), sigmoid=sigmoid, groups=groups, top_groups=1, group_top=2)
     bias[2 * per:] = high / 1.5  # two such sums are equal, a third is larger
     bias[3 * per:] = high
     route(lib, x, 4, bias, sigmoid=sigmoid, groups=groups, top_groups=2, group_top=2)
