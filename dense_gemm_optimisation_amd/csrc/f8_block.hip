@@ -618,7 +618,9 @@ __global__ __launch_bounds__(TEAMS *WAVES_M *WAVES_N * 64) void block_tile_kerne
                 acc[i][j] = (team == 0 ? acc[i][j] : acc[HALF + i][j]) + others[(i * FN + j) * WAVES * 64];
     }
     constexpr int ROWS = FM / TEAMS;  // of blocks that this team stores
-    const float alpha = K > 0 ? p.alpha : 0.0f;  // no terms: beta * C, whatever alpha is
+    // An empty segment has no terms: beta * C, whatever alpha is.  (Asking for K
+    // here in every launch costs 4096^3 0.6 of 62 us; elsewhere the host sets alpha.)
+    const float alpha = p.segments == Segments::Contracted && steps == 0 ? 0.0f : p.alpha;
     const bool plain = mrows == BM && nrows == BN && p.beta == 0.0f;
     char *c = static_cast<char *>(p.C) + (ec * p.sC + m0 * p.ldc + n0) * (p.out == 0 ? 4 : 2);
 #pragma unroll
@@ -761,7 +763,7 @@ __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) 
             if (m < m_hi && col < p.N) {
                 const int64_t at = ec * p.sC + (p.c_turned ? col * p.ldc + m : m * p.ldc + col);
                 const int left = p.N - col < 4 ? int(p.N - col) : 4;
-                v *= p.K > 0 ? p.alpha : 0.0f;  // no terms: beta * C, whatever alpha is
+                v *= p.alpha;
                 const float x[4] = {v[0], v[1], v[2], v[3]};
                 auto store = [&](int64_t to, const float *y, int n) {
                     if (p.out == 0) store_columns<0, 4>(p, static_cast<char *>(p.C), to, y, n);

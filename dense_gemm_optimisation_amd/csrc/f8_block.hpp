@@ -38,7 +38,7 @@ constexpr uint32_t ROUND = 256;
 
 struct BlockProblem {
     Segments segments;
-    int64_t M, N, K;  // K = 0 where nothing is multiplied
+    int64_t M, N, K;  // K = 0, and alpha too, where nothing is multiplied
     float alpha, beta;
     BlockOperand a, b;
     void *C;

@@ -122,7 +122,7 @@ gemm_status_t block_plan(Segments segments, int64_t M, int64_t N, int64_t K, con
     p = BlockProblem{};
     p.segments = segments;
     p.K = reads ? K : 0;
-    p.alpha = alpha;
+    p.alpha = reads ? alpha : 0.0f;
     p.beta = beta;
     p.C = C;
     p.ldc = ldc;
