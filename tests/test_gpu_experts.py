@@ -282,6 +282,66 @@ def test_product_nan_and_infinity(lib, kernels, M):
     assert torch.isfinite(got[rest]).all()
 
 
+def three_octaves(rng, op):
+    """op with codes of magnitudes 1 to 7.5: no product of two is below 2^-13 of another, nor has bits there (they are
+    multiples of 2^-6 below 2^6), so the matrix instruction cuts nothing off and a block's sum, below 2^13, is exact."""
+    v = np.abs(ref.TABLE[op.fmt])
+    shape = op.values.shape
+    codes = rng.choice(np.flatnonzero((v >= 1) & (v < 8)).astype(np.uint8), shape)
+    kb, sr = -(-op.K // 128), -(-op.R // op.block)
+    op.codes[:, :, :op.K] = torch.from_numpy(codes).to(DEV)
+    scales = op.scales.cpu().numpy()
+    op.values = np.stack([ref.values(c, op.fmt, s[:kb, :sr], op.block) for c, s in zip(codes, scales)])
+    return op
+
+
+def check_tight(got, want, den, out, kb):
+    """The product of the scales, kb additions (in up to 8 shares, then 7 more) and alpha, each rounded to fp32."""
+    got, h = got.cpu().double().numpy(), HALF[out]
+    assert np.all(np.abs(got - want) <= h * np.abs(want) + (kb + 9) * 2.0 ** -24 * (1 + h) * den)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 300, 4200), (64, 40, 700), (300, 390, 1001), (530, 640, 1163), (2300, 2400, 777), (3500, 3600, 401)])
+@pytest.mark.parametrize("blocks,fa,fb,out", [((1, 128), "e4m3", "e4m3", "f32"), ((1, 1), "e5m2", "e4m3", "f32"),
+                                              ((128, 128), "e4m3", "e5m2", "bf16")])
+def test_product_to_fp32s_precision(lib, kernels, M, N, K, blocks, fa, fb, out):
+    """Random scales over sums that are exact: every share, scale and order of additions shows at 2^-24."""
+    rng = np.random.default_rng(M + K)
+    a = three_octaves(rng, Operand(rng, M, K, fa, blocks[0], False))
+    b = three_octaves(rng, Operand(rng, N, K, fb, blocks[1], False))
+    c = torch.full((M, N), 9.0, dtype=TORCH[out], device=DEV)
+    lib.gemm_f8_block(M, N, K, 0.7, *a.args(lib), *b.args(lib), 0.0, c.data_ptr(), N, lib.ROW_MAJOR, out_type(lib, out))
+    A, B = a.values[0], b.values[0]
+    alpha = float(np.float32(0.7))
+    check_tight(c, alpha * (A @ B.T), alpha * (np.abs(A) @ np.abs(B).T), out, -(-K // 128))
+
+
+@pytest.mark.parametrize("N", [40, 700])
+def test_experts_to_fp32s_precision(lib, kernels, N):
+    rng = np.random.default_rng(N)
+    counts, K, M = [40, 0, 128, 1, 300], 1001, 150
+    off = boundaries(counts)
+    offsets = torch.from_numpy(off).to(DEV)
+    rows = int(off[-1])
+    a, b = three_octaves(rng, Operand(rng, rows, K, "e4m3", 1, False)), three_octaves(rng, Operand(rng, N, K, "e4m3", 128, False, 5))
+    c = torch.empty(rows, N, device=DEV)
+    lib.gemm_experts_f8(5, rows, N, K, offsets.data_ptr(), 1.0, *a.args(lib, False), *b.args(lib), b.stride, b.sstride, 0.0,
+                        c.data_ptr(), N, lib.OUTPUT_F32)
+    for e in range(5):
+        A, B = a.values[0][off[e]:off[e + 1]], b.values[e]
+        check_tight(c[off[e]:off[e + 1]], A @ B.T, np.abs(A) @ np.abs(B).T, "f32", 8)
+    counts = [256, 0, 640, 77]
+    off = boundaries(counts)
+    offsets, rows = torch.from_numpy(off).to(DEV), int(off[-1])
+    a, b = three_octaves(rng, Operand(rng, M, rows, "e5m2", 1, False)), three_octaves(rng, Operand(rng, N, rows, "e4m3", 1, False))
+    g = torch.empty(4, M, N, device=DEV)
+    lib.gemm_experts_f8_wgrad(4, M, N, rows, offsets.data_ptr(), 1.0, *a.args(lib, False), *b.args(lib, False), 0.0, g.data_ptr(),
+                              N, g.stride(0), lib.OUTPUT_F32)
+    for e in range(4):
+        A, B = a.values[0][:, off[e]:off[e + 1]], b.values[0][:, off[e]:off[e + 1]]
+        check_tight(g[e], A @ B.T, np.abs(A) @ np.abs(B).T, "f32", 5)
+
+
 def boundaries(counts, lead=0):
     return np.concatenate([[0], np.cumsum(counts)]).astype(np.int32) + lead
 
