@@ -16,8 +16,8 @@
 //
 // Both kernels are bound by latency at the sizes of a decode step and by
 // instruction issue beyond; they read the logits once.  64 tokens of 256
-// experts in 8 groups: 7.8 us and 3.4; 16384 tokens of 64: 8.2 and 6.5.  A
-// token chosen again adds 4 us.
+// experts in 8 groups: 8.3 us and 3.2; 16384 tokens of 64: 8.5 and 6.4.  A
+// token chosen again adds 4 us to such a decode step.
 #include "f8_block.hpp"
 
 #include <cmath>
@@ -678,8 +678,11 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a, int64_t own, i
         for (int e = tid; e <= E; e += THREADS) a.offsets[e] = start[e];
     // fillings, a wave each: experts g, g + grid, ..., and a share of what is behind the last segment
     if (a.align > 1)
-        for (int64_t e = int64_t(blockIdx.x) * (THREADS / 64) + (tid >> 6); e < E; e += int64_t(gridDim.x) * (THREADS / 64))
-            for (int64_t r = int64_t(start[e]) + total[e] + lane; r < start[e + 1]; r += 64) a.row_tokens[r] = -1;
+        for (int64_t e = int64_t(blockIdx.x) * (THREADS / 64) + (tid >> 6); e < E; e += int64_t(gridDim.x) * (THREADS / 64)) {
+            // (counted from the filling's start: rows end at 2^31)
+            const int from = start[e] + total[e], n = start[e + 1] - from;
+            for (int i = lane; i < n; i += 64) a.row_tokens[int64_t(from) + i] = -1;
+        }
     for (int64_t r = start[E] + int64_t(blockIdx.x) * THREADS + tid; r < a.rows; r += int64_t(gridDim.x) * THREADS)
         a.row_tokens[r] = -1;
     for (int64_t block = first_block; block < first_block + own && block * BLOCK < a.tokens; ++block) {
@@ -715,7 +718,7 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a, int64_t own, i
 //   d_i = p_i g_i for the chosen; renormalised, S the sum of their p: (p_i / S) (g_i - sum_j g_j p_j / S)
 //   sigmoid: dl_i = d_i (1 - p_i);  softmax: dl_i = d_i - p_i sum_j d_j
 // (renormalised softmax: the d_i sum to 0).  In a share p_i / S any common factor of the p cancels.
-// Bound by the loads' latency: 16384 tokens of 128 experts 6.6 us, 1.4 TB/s.
+// Bound by the loads' latency: 16384 tokens of 128 experts 5.9 to 7 us, 1.3 to 1.6 TB/s.
 constexpr int BACK_WAVES = 4;
 template <int PER, int WIDTH>
 __global__ __launch_bounds__(BACK_WAVES * 64) void route_backward_kernel(RouteBackwardArgs a) {
