@@ -343,13 +343,14 @@ __device__ inline bool coordinates(const TileGrid &g, TilePart part, uint32_t ro
 //
 // Why 256 x 256 of eight waves of 128 x 64: a stage is 64 KiB read from the
 // second-level cache and 192 KiB from LDS for 2^23 multiply-adds, half of what
-// 128 x 128 tiles read (4096^3 62 us, with those 91).  A step of k takes 1.85
-// us with one factor per row, 2.1 with one per value, where the matrix
-// instructions alone are 0.85 at 2.4 GHz; without the refill 1.14 of 1.56 us
-// (on zeros) remain.  On random values the socket's power limit sets the clock
-// (2.0 to 2.1 GHz): 4096^3 takes 55 us on zeros, 62 on values, 2.2 PFLOP/s.
-// A tile costs another 8 us: coordinates and addresses 1.5, its first stage
-// 1.2 to 5, C about 3.
+// 128 x 128 tiles read (4096^3 62 us, with those 91).  4096 x 4096 by K of 1024
+// to 8192, one tile per compute unit, takes 10.7 us and 1.67 per step of k with
+// one factor per row, 10.2 and 1.97 with one per value; the matrix instructions
+// alone are 0.85 at 2.4 GHz.  On random values the socket's power limit sets
+// the clock (2.0 to 2.1 GHz, 2.2 PFLOP/s at 4096^3); on zeros it is 12.7 and
+// 1.33, 12.0 and 1.61, of which a quarter goes without the refill.  Of the part
+// that K does not change, coordinates and addresses are 1.5, the first stage
+// 1.2 to 5, C about 3, the rest the launch.
 template <int FA, int FB, bool PER_COLUMN, int WAVES_M, int WAVES_N, int FM, int FN, int TEAMS>
 __global__ __launch_bounds__(TEAMS *WAVES_M *WAVES_N * 64) void block_tile_kernel(BlockArgs a) {
     constexpr int WAVES = WAVES_M * WAVES_N;  // of a team
@@ -659,9 +660,9 @@ constexpr int FEW_WAVES = 8;
 // straight into registers, the blocks of K dealt to the waves in turn, UNROLL
 // of them in flight per wave.  The waves' sums are added in order through
 // LDS.  Bound by reading B: with 16 columns a chip-wide launch needs only 4096
-// columns, and 128-byte pieces of 16 rows keep whole lines.  2 rows each of 64
-// experts of 2048 x 4096 take 94 to 98 us, 4.8 TB/s; 16x4096x4096 7.6 us, of
-// which 3.4 are reading.
+// columns, and 128-byte pieces of 16 rows keep whole lines.  128 rows dealt at
+// random to 64 experts of 2048 x 4096, about 55 of which have any, take 95 to
+// 104 us, 4.5 to 4.9 TB/s; 16x4096x4096 7.8 us, of which 3.4 are reading.
 template <int FA, int FB, bool PER_COLUMN, int FM, int UNROLL>
 __global__ __launch_bounds__(FEW_WAVES * 64) void block_few_kernel(BlockArgs a) {
     __shared__ f32x4 sums[FEW_WAVES][FM * 64];

@@ -45,6 +45,9 @@
  *   sums are added in fp32, in order of k within each of up to 8 shares of the
  *   blocks, and the shares' sums in a fixed order.  How many shares there are
  *   goes by the sizes of the call, so the result is the same on every run.
+ *   The two scales are multiplied first, in fp32: where their product is
+ *   subnormal, 0 or infinite there, that is what the sum is multiplied by,
+ *   though the sum times both might be in range.
  *   The rest is gemm_f8's: alpha*acc +
  *   beta*C in fp32, rounded to nearest-even into typeC; beta == 0 does not
  *   read C; alpha == 0 or K == 0 gives beta * C.  NaN and infinite codes and

@@ -282,6 +282,20 @@ def test_product_nan_and_infinity(lib, kernels, M):
     assert torch.isfinite(got[rest]).all()
 
 
+@pytest.mark.parametrize("M,N", [(3, 20), (70, 300), (300, 300)])
+@pytest.mark.parametrize("block", [1, 128])
+def test_scales_are_multiplied_first(lib, kernels, M, N, block):
+    rng = np.random.default_rng(9)
+    a, b = Operand(rng, M, 128, "e4m3", 1, True), Operand(rng, N, 128, "e4m3", block, True)
+    a.codes[:, :, :128], b.codes[:, :, :128] = 0x38, 0x38  # ones
+    c = torch.empty(M, N, device=DEV)
+    for sa, sb, want in ((2.0 ** -100, 2.0 ** -40, 2.0 ** -133), (2.0 ** -100, 2.0 ** -100, 0.0), (2.0 ** 100, 2.0 ** 100, np.inf)):
+        a.scales.fill_(sa)
+        b.scales.fill_(sb)
+        lib.gemm_f8_block(M, N, 128, 1.0, *a.args(lib), *b.args(lib), 0.0, c.data_ptr(), N, 0, lib.OUTPUT_F32)
+        assert bool((c == want).all())
+
+
 def three_octaves(rng, op):
     """op with codes of magnitudes 1 to 7.5: no product of two is below 2^-13 of another, nor has bits there (they are
     multiples of 2^-6 below 2^6), so the matrix instruction cuts nothing off and a block's sum, below 2^13, is exact."""
