@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemm.so"
 ROW_MAJOR, COL_MAJOR = 0, 1
 DTYPE_SAME, DTYPE_F32 = 0, 1
 ACT_NONE, ACT_RELU, ACT_GELU = 0, 1, 2
+ACT_SILU = 3  # the calls of libgemm_layers.h only
 F8_E4M3, F8_E5M2 = 0, 1
 MX_E4M3, MX_E5M2, MX_E2M3, MX_E3M2, MX_E2M1 = 0, 1, 2, 3, 4
 MX_FORMAT = {"e4m3": MX_E4M3, "e5m2": MX_E5M2, "e2m3": MX_E2M3, "e3m2": MX_E3M2, "e2m1": MX_E2M1}
@@ -32,6 +33,10 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 INPUT_F32, INPUT_BF16, INPUT_F16 = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 ROUTE_MAX_EXPERTS, ROUTE_MAX_TOP_K, ROUTE_MAX_GROUPS = 1024, 32, 64
+# libgemm_layers.h
+WEIGHTS_SAME, WEIGHTS_E4M3, WEIGHTS_E5M2 = 0, 1, 2
+LAYER_MAX_TOKENS, LAYER_MAX_EXPERTS, LAYER_MAX_TOP_K = 64, 1024, 32
+ORTHOGONALIZE_MAX_STEPS = 32
 
 _lib = None
 
@@ -147,6 +152,31 @@ def library() -> ctypes.CDLL:
         for name in ("gemm_f8_block_quantize", "gemm_f8_block", "gemm_experts_f8",
                      "gemm_experts_f8_wgrad", "gemm_experts_route", "gemm_experts_route_backward"):
             getattr(lib, name).restype = i32
+        linear = [i64, i64, i64, f32, vp, i64, vp, i64, i32, i32, vp, i32, f32, vp, i64, vp, i64,
+                  i32, vp, i64, vp, sz]
+        linear_backward = [i64, i64, i64, f32, vp, i64, vp, i64, i32, i32, vp, i64, i32, vp, i64,
+                           i32, f32, vp, vp, sz]
+        for name, args in (("gemm_linear", linear), ("gemm_linear_backward", linear_backward)):
+            getattr(lib, name).argtypes = args + [vp]
+            getattr(lib, name).restype = i32
+            getattr(lib, name + "_kernel_name").argtypes = args
+            getattr(lib, name + "_kernel_name").restype = ctypes.c_char_p
+        lib.gemm_activation_backward.argtypes = [i64, i64, vp, i64, i32, vp, i64, i32, i32, vp, i64,
+                                                 i32, f32, vp, vp, sz, vp]
+        weights = [vp, i64, i64, vp, i64, i64]
+        lib.gemm_experts_layer.argtypes = ([i64, i64, i64, i64, i64, vp, i64, i32, vp, vp, i32] +
+                                           weights + weights + [i32, f32, vp, i64, i32, vp, sz, vp])
+        lib.gemm_orthogonalize.argtypes = [i64, i64, vp, i64, i32, i64, vp, f32, f32, f32, vp, i64,
+                                           i32, i64, i64, i64, vp, sz, vp]
+        for name in ("gemm_activation_backward", "gemm_experts_layer", "gemm_orthogonalize"):
+            getattr(lib, name).restype = i32
+        lib.gemm_orthogonalize_kernel_name.argtypes = [i64, i64, i64]
+        lib.gemm_orthogonalize_kernel_name.restype = ctypes.c_char_p
+        for name, n in (("linear", 3), ("activation_backward", 2), ("experts_layer", 5),
+                        ("orthogonalize", 3)):
+            size = getattr(lib, f"gemm_{name}_workspace_size")
+            size.argtypes = [i64] * n
+            size.restype = sz
         _lib = lib
     return _lib
 
@@ -453,6 +483,113 @@ def gemm_experts_route_backward(tokens, experts, logits, ldl, in_type, score, to
                                                renormalise, scale, ids, d_weights, d_logits, ldd,
                                                _stream(stream))
     return _check(st, "gemm_experts_route_backward", raise_on_error)
+
+
+def linear_workspace_size(M, N, K) -> int:
+    """Bytes of workspace that gemm_linear and gemm_linear_backward use."""
+    return library().gemm_linear_workspace_size(M, N, K)
+
+
+def gemm_linear(M, N, K, alpha, A, lda, B, ldb, order_b, in_type, bias, act, beta, R, ldr, C, ldc,
+                type_c, Z=0, ldz=0, workspace=0, workspace_bytes=0, stream=None,
+                raise_on_error=True):
+    """C <- act(alpha*A*B + bias) + beta*R for 16-bit A and B; Z, where it is
+    given, the activation's input.  0 for a bias, R or Z that is not there."""
+    st = library().gemm_linear(M, N, K, alpha, A, lda, B, ldb, order_b, in_type, bias, act, beta, R,
+                               ldr, C, ldc, type_c, Z, ldz, workspace, workspace_bytes,
+                               _stream(stream))
+    return _check(st, "gemm_linear", raise_on_error)
+
+
+def linear_kernel_name(M, N, K, alpha, A, lda, B, ldb, order_b, in_type, bias, act, beta, R, ldr, C,
+                       ldc, type_c, Z=0, ldz=0, workspace=0, workspace_bytes=0):
+    """The kernel gemm_linear would launch (see kernel_name)."""
+    name = library().gemm_linear_kernel_name(M, N, K, alpha, A, lda, B, ldb, order_b, in_type, bias,
+                                             act, beta, R, ldr, C, ldc, type_c, Z, ldz, workspace,
+                                             workspace_bytes)
+    return None if name is None else name.decode()
+
+
+def gemm_linear_backward(M, N, K, alpha, A, lda, B, ldb, order_b, in_type, Z, ldz, act, D, ldd,
+                         type_d, beta, d_bias, workspace=0, workspace_bytes=0, stream=None,
+                         raise_on_error=True):
+    """D <- (alpha*A*B) * act'(Z) for 16-bit A and B, and d_bias (0: not
+    wanted) <- D's column sums + beta*d_bias."""
+    st = library().gemm_linear_backward(M, N, K, alpha, A, lda, B, ldb, order_b, in_type, Z, ldz,
+                                        act, D, ldd, type_d, beta, d_bias, workspace,
+                                        workspace_bytes, _stream(stream))
+    return _check(st, "gemm_linear_backward", raise_on_error)
+
+
+def linear_backward_kernel_name(M, N, K, alpha, A, lda, B, ldb, order_b, in_type, Z, ldz, act, D,
+                                ldd, type_d, beta, d_bias, workspace=0, workspace_bytes=0):
+    """The kernel gemm_linear_backward would launch (see kernel_name)."""
+    name = library().gemm_linear_backward_kernel_name(M, N, K, alpha, A, lda, B, ldb, order_b,
+                                                      in_type, Z, ldz, act, D, ldd, type_d, beta,
+                                                      d_bias, workspace, workspace_bytes)
+    return None if name is None else name.decode()
+
+
+def activation_backward_workspace_size(M, N) -> int:
+    """Bytes of workspace that gemm_activation_backward uses for d_bias."""
+    return library().gemm_activation_backward_workspace_size(M, N)
+
+
+def gemm_activation_backward(M, N, A, lda, type_a, Z, ldz, type_z, act, D, ldd, type_d, beta, d_bias,
+                             workspace=0, workspace_bytes=0, stream=None, raise_on_error=True):
+    """D <- A * act'(Z) (0: not wanted), and d_bias (0: not wanted) <- the
+    column sums + beta*d_bias."""
+    st = library().gemm_activation_backward(M, N, A, lda, type_a, Z, ldz, type_z, act, D, ldd, type_d,
+                                            beta, d_bias, workspace, workspace_bytes,
+                                            _stream(stream))
+    return _check(st, "gemm_activation_backward", raise_on_error)
+
+
+def experts_layer_workspace_size(tokens, experts, top_k, D, H) -> int:
+    """Bytes of workspace that gemm_experts_layer uses."""
+    return library().gemm_experts_layer_workspace_size(tokens, experts, top_k, D, H)
+
+
+def gemm_experts_layer(tokens, experts, top_k, D, H, X, ldx, in_type, ids, weights, type_w, up, ld_up,
+                       stride_up, scale_up, lds_up, stride_scale_up, down, ld_down, stride_down,
+                       scale_down, lds_down, stride_scale_down, act, beta, Y, ldy, type_y, workspace,
+                       workspace_bytes, stream=None, raise_on_error=True):
+    """Y_t <- the weighted sum of token t's experts' gated layers + beta*Y_t,
+    for at most LAYER_MAX_TOKENS tokens."""
+    st = library().gemm_experts_layer(tokens, experts, top_k, D, H, X, ldx, in_type, ids, weights,
+                                      type_w, up, ld_up, stride_up, scale_up, lds_up, stride_scale_up,
+                                      down, ld_down, stride_down, scale_down, lds_down,
+                                      stride_scale_down, act, beta, Y, ldy, type_y, workspace,
+                                      workspace_bytes, _stream(stream))
+    return _check(st, "gemm_experts_layer", raise_on_error)
+
+
+def orthogonalize_workspace_size(M, N, batch=1) -> int:
+    """Bytes of workspace that gemm_orthogonalize uses."""
+    return library().gemm_orthogonalize_workspace_size(M, N, batch)
+
+
+def gemm_orthogonalize(M, N, G, ldg, in_type, steps, coefficients, eps, alpha, beta, O, ldo, type_o,
+                       workspace, workspace_bytes, batch=1, stride_g=0, stride_o=0, stream=None,
+                       raise_on_error=True):
+    """O <- alpha * (G after `steps` Newton-Schulz steps) + beta*O.
+    coefficients: a, b, c of each step, or None for the usual ones."""
+    c = None
+    if coefficients is not None:
+        flat = [float(x) for step in coefficients for x in step]
+        if len(flat) != 3 * steps:
+            raise ValueError("coefficients: three for each step")
+        c = (ctypes.c_float * len(flat))(*flat)
+    st = library().gemm_orthogonalize(M, N, G, ldg, in_type, steps, c, eps, alpha, beta, O, ldo,
+                                      type_o, batch, stride_g, stride_o, workspace, workspace_bytes,
+                                      _stream(stream))
+    return _check(st, "gemm_orthogonalize", raise_on_error)
+
+
+def orthogonalize_kernel_name(M, N, batch=1):
+    """The kernel of gemm_orthogonalize's products (see kernel_name)."""
+    name = library().gemm_orthogonalize_kernel_name(M, N, batch)
+    return None if name is None else name.decode()
 
 
 def workspace_size() -> int:

@@ -1,0 +1,489 @@
+// The product with bias, activation and residual in its epilogue
+// (gemm_linear), the product with an activation's slope and column sums in
+// its epilogue (gemm_linear_backward), and the latter without a product
+// (gemm_activation_backward).
+//
+// Kernels, by the work there is (linear_choose):
+//   tile 256 / 128   256 x 256 tiles of eight waves, 128 x 128 tiles of four,
+//                    two workgroups per compute unit (tile16.hpp).  The epilogue reads and
+//                    writes whole rows of 64 columns and costs what its bytes
+//                    cost;
+//   split            the 128 x 128 tiles with K cut into slices, each slice's
+//                    sums in the workspace, joined in order by finish_kernel,
+//                    which also has the epilogue: problems of few tiles;
+//   few              up to 16 rows against a K-contiguous B: 16 columns per
+//                    workgroup, K dealt to eight waves, operands straight
+//                    into registers; bound by reading B;
+//   any              the 128 x 128 tiles with panels through registers, for
+//                    operands of any alignment.
+// Column sums: each wave (or finish workgroup) leaves the sums over its rows
+// in the workspace, and sums_kernel adds them in order: no atomics, the same
+// result on every run.
+#include "activation.hpp"
+#include "layers.hpp"
+#include "tile16.hpp"
+
+namespace libgemm {
+namespace {
+
+using namespace tile16;
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+
+struct LinearArgs {
+    int64_t M, N, K;
+    float alpha, beta, beta_bias;
+    Operand16 a, b;
+    const uint16_t *bias;
+    const void *R;
+    void *C;
+    uint16_t *Z;
+    int64_t ldr, ldc, ldz;
+    int act;
+    bool c_same;     // C (and R) have the inputs' type, else fp32
+    TileGrid grid;   // batch: slices of K
+    float *sums;     // backward: column sums by rows of blocks, N each
+    float *partial;  // split: [slice][M][ldp]
+    int64_t ldp;
+    int slices;
+};
+
+// The values of one lane's eight columns, which stay the same while it goes
+// down the rows.
+template <class T, bool BACKWARD>
+struct Finish {
+    const LinearArgs &p;
+    float column[8];  // forward: the bias; backward: the sums so far
+
+    __device__ Finish(const LinearArgs &args, int64_t n) : p(args) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) column[e] = 0.0f;
+        if (!BACKWARD && p.bias != nullptr && n < p.N)
+            load8<T>(p.bias + n, p.N - n < 8 ? int(p.N - n) : 8, column);
+    }
+    // x: the products' sums of columns n .. n + count - 1 of row m
+    __device__ void operator()(int64_t m, int64_t n, int count, float (&x)[8]) {
+        if constexpr (BACKWARD) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= p.alpha;
+            if (p.act != act::NONE) {
+                float z[8];
+                load8<T>(p.Z + m * p.ldz + n, count, z);
+                act::times_slope(p.act, z, x);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) column[e] += x[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(p.alpha, x[e], column[e]);
+            if (p.Z != nullptr) store8<T>(p.Z + m * p.ldz + n, count, x);
+            act::apply(p.act, x);
+            if (p.beta != 0.0f) {
+                float r[8];
+                load8_as<T>(p.R, m * p.ldr + n, p.c_same, count, r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(p.beta, r[e], x[e]);
+            }
+        }
+        store8_as<T>(p.C, m * p.ldc + n, p.c_same, count, x);
+    }
+    // The lanes with this lane's columns (those a multiple of `lanes` apart)
+    // add up; the first of them writes row `block` of the sums.
+    __device__ void write_sums(int64_t block, int64_t n, int lanes, int lane) {
+        if (!BACKWARD || p.sums == nullptr) return;
+        for (int d = lanes; d < 64; d *= 2)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) column[e] += __shfl_xor(column[e], d);
+        if (lane < lanes && n < p.N)
+            store8f(p.sums + block * p.N + n, p.N - n < 8 ? int(p.N - n) : 8, column);
+    }
+};
+
+// ---------------------------------------------------------------- tiles
+template <class T, class Shape, bool BACKWARD>
+__global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void tile_kernel(LinearArgs p) {
+    __shared__ __attribute__((aligned(1024))) char smem[Shape::LDS_BYTES];
+    LDS char *lds = (LDS char *)smem;
+    const TileCoord t = tile_of(p.grid, blockIdx.x);
+    const int64_t m0 = uniform(t.tm) * Shape::TM, n0 = uniform(t.tn) * Shape::TN;
+    typename Shape::Acc acc;
+    const int buf = Shape::run(p.a, p.b, p.K, m0, n0, 0, (p.K + BK - 1) / BK, lds, acc);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t mw = m0 + Shape::wave_m(wave) * Shape::WTM, nw = n0 + Shape::wave_n(wave) * Shape::WTN;
+    if (mw >= p.M || nw >= p.N) return;
+    constexpr int LANES = Shape::WTN / 8;
+    const int64_t n = nw + (lane % LANES) * 8;
+    Finish<T, BACKWARD> finish(p, n);
+    visit_tile(acc, p.M, p.N, mw, nw, lane, Shape::staging(lds, buf, wave), finish);
+    finish.write_sums(mw / Shape::WTM, n, LANES, lane);
+}
+
+// One slice of K of a tile: its sums go to the workspace.
+template <class Shape>
+__global__ __launch_bounds__(Shape::THREADS, 2) void split_kernel(LinearArgs p) {
+    __shared__ __attribute__((aligned(1024))) char smem[Shape::LDS_BYTES];
+    LDS char *lds = (LDS char *)smem;
+    const TileCoord t = tile_of(p.grid, blockIdx.x);
+    const int64_t m0 = uniform(t.tm) * Shape::TM, n0 = uniform(t.tn) * Shape::TN, z = uniform(t.batch);
+    const int64_t stages = (p.K + BK - 1) / BK;
+    typename Shape::Acc acc;
+    const int buf = Shape::run(p.a, p.b, p.K, m0, n0, stages * z / p.slices, stages * (z + 1) / p.slices, lds, acc);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t mw = m0 + Shape::wave_m(wave) * Shape::WTM, nw = n0 + Shape::wave_n(wave) * Shape::WTN;
+    if (mw >= p.M || nw >= p.N) return;
+    float *out = p.partial + z * p.M * p.ldp;
+    visit_tile(acc, p.M, p.N, mw, nw, lane, Shape::staging(lds, buf, wave),
+               [&](int64_t m, int64_t n, int count, float(&x)[8]) { store8f(out + m * p.ldp + n, count, x); });
+}
+
+// Joins the slices: 64 columns by FINISH_ROWS rows per workgroup.
+constexpr int FINISH_ROWS = 32;
+template <class T, bool BACKWARD>
+__global__ __launch_bounds__(256) void finish_kernel(LinearArgs p) {
+    __shared__ float waves[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = int64_t(blockIdx.x) * 64 + (threadIdx.x % 8) * 8;
+    const int64_t m = int64_t(blockIdx.y) * FINISH_ROWS + threadIdx.x / 8;
+    const int count = p.N - n < 8 ? int(p.N - n) : 8;
+    Finish<T, BACKWARD> finish(p, n);
+    if (m < p.M && count > 0) {
+        float x[8], part[8];
+        const float *at = p.partial + m * p.ldp + n;
+        load8f(at, count, x);
+        for (int s = 1; s < p.slices; ++s) {
+            load8f(at + s * p.M * p.ldp, count, part);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += part[e];
+        }
+        finish(m, n, count, x);
+    }
+    if (!BACKWARD || p.sums == nullptr) return;
+    for (int d = 8; d < 64; d *= 2)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) finish.column[e] += __shfl_xor(finish.column[e], d);
+    if (lane < 8)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) waves[wave][lane * 8 + e] = finish.column[e];
+    __syncthreads();
+    const int64_t j = int64_t(blockIdx.x) * 64 + lane;
+    if (wave == 0 && j < p.N)
+        p.sums[blockIdx.y * p.N + j] = waves[0][lane] + waves[1][lane] + (waves[2][lane] + waves[3][lane]);
+}
+
+// ---------------------------------------------------------------- few rows
+template <class T>
+__device__ inline f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c);
+template <>
+__device__ inline f32x4 mfma16<BF16>(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <>
+__device__ inline f32x4 mfma16<F16>(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// At most 16 rows by 16 columns, K dealt to eight waves in runs of 128.
+// Operands swapped: lane l has column 4*(l / 16) + r of row l % 16 in
+// register r.
+template <class T, bool BACKWARD>
+__global__ __launch_bounds__(512, 2) void few_kernel(LinearArgs p) {
+    constexpr int WAVES = 8, RUN = 128, STEPS = RUN / 32;
+    __shared__ f32x4 part[WAVES][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n0 = int64_t(blockIdx.x) * 16;
+    const int row = lane & 15, kq = (lane >> 4) * 8;
+    const bool has_a = row < p.M, has_b = n0 + row < p.N;
+    const uint16_t *pa = p.a.p + row * p.a.ld + kq, *pb = p.b.p + (n0 + row) * p.b.ld + kq;
+    const u32x4 zero = {0, 0, 0, 0};
+    f32x4 acc = {0, 0, 0, 0};
+    // the next run's operands are on their way while this one is multiplied
+    u32x4 a[STEPS], b[STEPS];
+    auto fetch = [&](int64_t k0) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int64_t k = k0 + 32 * s;
+            b[s] = has_b && k + kq < p.K ? *reinterpret_cast<const u32x4 *>(pb + k) : zero;
+            a[s] = has_a && k + kq < p.K ? *reinterpret_cast<const u32x4 *>(pa + k) : zero;
+        }
+    };
+    fetch(wave * RUN);
+    for (int64_t k0 = wave * RUN; k0 < p.K; k0 += WAVES * RUN) {
+        u32x4 ca[STEPS], cb[STEPS];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) ca[s] = a[s], cb[s] = b[s];
+        fetch(k0 + WAVES * RUN);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) acc = mfma16<T>(cb[s], ca[s], acc);
+    }
+    part[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+        const f32x4 o = part[w][lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += o[e];
+    }
+    // two lanes' four columns to one lane's eight: lanes 0 .. 31 finish
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int from = (lane & 15) + 32 * (lane >> 4 & 1);
+        x[e] = __shfl(acc[e], from);
+        x[4 + e] = __shfl(acc[e], from + 16);
+    }
+    const int64_t n = n0 + 8 * (lane >> 4 & 1);
+    const int count = p.N - n < 8 ? int(p.N - n) : 8;
+    Finish<T, BACKWARD> finish(p, n);
+    if (lane < 32 && row < p.M && count > 0) finish(row, n, count, x);
+    if (!BACKWARD || p.sums == nullptr) return;
+    for (int d = 1; d < 16; d *= 2)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) finish.column[e] += __shfl_xor(finish.column[e], d);
+    if (lane < 32 && row == 0 && count > 0) store8f(p.sums + n, count, finish.column);
+}
+
+// ---------------------------------------------------------------- column sums
+// dbias[j] = the sum of rows of sums[.][j], in order, + beta * dbias[j]; 32
+// columns per workgroup, eight threads to a column.
+__global__ __launch_bounds__(256) void sums_kernel(const float *sums, int64_t rows, int64_t N, float beta,
+                                                   float *dbias) {
+    __shared__ float part[8][32];
+    const int c = threadIdx.x % 32, g = threadIdx.x / 32;
+    const int64_t j = int64_t(blockIdx.x) * 32 + c;
+    float s = 0.0f;
+    if (j < N)
+        for (int64_t r = g; r < rows; r += 8) s += sums[r * N + j];
+    part[g][c] = s;
+    __syncthreads();
+    if (g != 0 || j >= N) return;
+    for (int i = 1; i < 8; ++i) s += part[i][c];
+    dbias[j] = beta != 0.0f ? __builtin_fmaf(beta, dbias[j], s) : s;
+}
+
+hipError_t launch_sums(const float *sums, int64_t rows, int64_t N, float beta, float *dbias, hipStream_t stream) {
+    sums_kernel<<<dim3(unsigned((N + 31) / 32)), dim3(256), 0, stream>>>(sums, rows, N, beta, dbias);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- without a product
+// 64 columns by AB_ROWS rows per workgroup; a thread has eight columns and
+// every 32nd row.
+constexpr int AB_ROWS = 128;
+struct ActivationArgs {
+    ActivationBackward p;
+    float *sums;
+};
+template <int TYPE>
+__device__ inline void load8_type(const void *x, int64_t at, int n, float (&v)[8]) {
+    if constexpr (TYPE == 0) load8f(static_cast<const float *>(x) + at, n, v);
+    else if constexpr (TYPE == 1) load8<BF16>(static_cast<const uint16_t *>(x) + at, n, v);
+    else load8<F16>(static_cast<const uint16_t *>(x) + at, n, v);
+}
+template <int TA, int TZ>
+__global__ __launch_bounds__(256) void activation_kernel(ActivationArgs a) {
+    const ActivationBackward &p = a.p;
+    __shared__ float waves[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = int64_t(blockIdx.x) * 64 + (threadIdx.x % 8) * 8;
+    const int count = p.N - n < 8 ? int(p.N - n) : 8;
+    float sum[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+    const int64_t end = (int64_t(blockIdx.y) + 1) * AB_ROWS < p.M ? (int64_t(blockIdx.y) + 1) * AB_ROWS : p.M;
+    if (count > 0)
+        for (int64_t m = int64_t(blockIdx.y) * AB_ROWS + threadIdx.x / 8; m < end; m += 32) {
+            float x[8], z[8];
+            load8_type<TA>(p.A, m * p.lda + n, count, x);
+            if (p.act != act::NONE) {
+                load8_type<TZ>(p.Z, m * p.ldz + n, count, z);
+                act::times_slope(p.act, z, x);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += x[e];
+            if (p.D != nullptr) {
+                const int64_t at = m * p.ldd + n;
+                if (p.type_d == 0) store8f(static_cast<float *>(p.D) + at, count, x);
+                else if (p.type_d == 1) store8<BF16>(static_cast<uint16_t *>(p.D) + at, count, x);
+                else store8<F16>(static_cast<uint16_t *>(p.D) + at, count, x);
+            }
+        }
+    if (a.sums == nullptr) return;
+    for (int d = 8; d < 64; d *= 2)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor(sum[e], d);
+    if (lane < 8)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) waves[wave][lane * 8 + e] = sum[e];
+    __syncthreads();
+    const int64_t j = int64_t(blockIdx.x) * 64 + lane;
+    if (wave == 0 && j < p.N)
+        a.sums[blockIdx.y * p.N + j] = waves[0][lane] + waves[1][lane] + (waves[2][lane] + waves[3][lane]);
+}
+
+// ---------------------------------------------------------------- launches
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Slices of K for `tiles` tiles of 128 x 128: two workgroups for each of 256
+// compute units, four stages each at least.
+int split_slices(int64_t tiles, int64_t K) {
+    const int64_t most = ceil_div(K, BK) / 4;
+    const int64_t want = 512 / tiles;
+    const int64_t s = want < most ? want : most;
+    return int(s < 1 ? 1 : s);
+}
+int64_t tiles_of(int64_t M, int64_t N, int64_t t) { return ceil_div(M, t) * ceil_div(N, t); }
+int64_t round8(int64_t n) { return ceil_div(n, 8) * 8; }
+size_t partial_bytes(int64_t M, int64_t N, int slices) { return size_t(slices) * M * round8(N) * 4; }
+// Column sums take a row for each 32 rows at least (finish_kernel).
+size_t sums_bytes(int64_t M, int64_t N) { return size_t(ceil_div(ceil_div(M, FINISH_ROWS) * N, 64) * 256); }
+
+template <class Shape, class T, bool BACKWARD>
+hipError_t run_tile(LinearArgs &a, hipStream_t stream) {
+    a.grid = TileGrid{ceil_div(a.M, Shape::TM), ceil_div(a.N, Shape::TN), 1, 8, 8};
+    if (a.grid.count() > 0x7fffffff) return hipErrorInvalidConfiguration;
+    tile_kernel<T, Shape, BACKWARD><<<dim3(unsigned(a.grid.count())), dim3(Shape::THREADS), 0, stream>>>(a);
+    return hipGetLastError();
+}
+template <class Shape, class T, bool BACKWARD>
+hipError_t run_split(LinearArgs &a, hipStream_t stream) {
+    a.grid = TileGrid{ceil_div(a.M, Shape::TM), ceil_div(a.N, Shape::TN), a.slices, 8, 8};
+    split_kernel<Shape><<<dim3(unsigned(a.grid.count())), dim3(Shape::THREADS), 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    finish_kernel<T, BACKWARD><<<dim3(unsigned(ceil_div(a.N, 64)), unsigned(ceil_div(a.M, FINISH_ROWS))), dim3(256), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <class T, bool BACKWARD, bool BKM>
+hipError_t run_kernel(LinearKernel k, LinearArgs &a, hipStream_t stream) {
+    using T256 = Tile<T, 256, 256, 2, 4, true, BKM, true>;
+    using T128 = Tile<T, 128, 128, 2, 2, true, BKM, true>;
+    using Any = Tile<T, 128, 128, 2, 2, true, BKM, false>;
+    switch (k) {
+        case LinearKernel::Tile256: return run_tile<T256, T, BACKWARD>(a, stream);
+        case LinearKernel::Tile128: return run_tile<T128, T, BACKWARD>(a, stream);
+        case LinearKernel::Any: return run_tile<Any, T, BACKWARD>(a, stream);
+        case LinearKernel::Split: return run_split<T128, T, BACKWARD>(a, stream);
+        case LinearKernel::AnySplit: return run_split<Any, T, BACKWARD>(a, stream);
+        case LinearKernel::Few16:
+            few_kernel<T, BACKWARD><<<dim3(unsigned(ceil_div(a.N, 16))), dim3(512), 0, stream>>>(a);
+            return hipGetLastError();
+        default: return hipSuccess;
+    }
+}
+
+int64_t sums_rows(LinearKernel k, int64_t M) {
+    switch (k) {
+        case LinearKernel::Few16: return 1;
+        case LinearKernel::Tile256: return ceil_div(M, 128);
+        case LinearKernel::Split:
+        case LinearKernel::AnySplit: return ceil_div(M, FINISH_ROWS);
+        default: return ceil_div(M, 64);
+    }
+}
+
+bool whole_chunks(const void *x, int64_t ld, int64_t inner) {
+    return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld % 8 == 0 && inner % 8 == 0 && ld <= MOST_LD;
+}
+
+}  // namespace
+
+const char *linear_kernel_name(LinearKernel k) {
+    switch (k) {
+        case LinearKernel::Few16: return "linear_few_16";
+        case LinearKernel::Tile256: return "linear_mfma_256";
+        case LinearKernel::Tile128: return "linear_mfma_128";
+        case LinearKernel::Split: return "linear_mfma_128_split";
+        case LinearKernel::Any: return "linear_mfma_any";
+        case LinearKernel::AnySplit: return "linear_mfma_any_split";
+        default: return "";
+    }
+}
+
+hipError_t launch_no_sums(int64_t N, float beta, float *dbias, hipStream_t stream) {
+    return launch_sums(nullptr, 0, N, beta, dbias, stream);
+}
+
+size_t linear_workspace(int64_t M, int64_t N, int64_t K) {
+    const int slices = split_slices(tiles_of(M, N, 128), K);
+    return sums_bytes(M, N) + (slices > 1 ? partial_bytes(M, N, slices) : 0) + 16;
+}
+
+LinearKernel linear_choose(const LinearProblem &p) {
+    if (p.M == 0 || p.N == 0) return LinearKernel::None;
+    const bool direct = p.K > 0 && whole_chunks(p.A, p.lda, p.K) && whole_chunks(p.B, p.ldb, p.b_kmajor ? p.K : p.N);
+    if (direct && p.b_kmajor && p.M <= 16) return LinearKernel::Few16;
+    const int64_t t128 = tiles_of(p.M, p.N, 128);
+    const int slices = p.K > 0 ? split_slices(t128, p.K) : 1;
+    const bool split = slices > 1 && p.workspace != nullptr &&
+                       p.workspace_bytes >= sums_bytes(p.M, p.N) + partial_bytes(p.M, p.N, slices);
+    if (!direct) return split ? LinearKernel::AnySplit : LinearKernel::Any;
+    if (split) return LinearKernel::Split;
+    return tiles_of(p.M, p.N, 256) >= 192 ? LinearKernel::Tile256 : LinearKernel::Tile128;
+}
+
+hipError_t launch_linear(LinearKernel k, const LinearProblem &p, hipStream_t stream) {
+    if (k == LinearKernel::None)
+        return p.dbias != nullptr && p.N > 0 ? launch_no_sums(p.N, p.beta_bias, p.dbias, stream) : hipSuccess;
+    LinearArgs a{};
+    a.M = p.M;
+    a.N = p.N;
+    a.K = p.K;
+    a.alpha = p.alpha;
+    a.beta = p.beta;
+    a.a = Operand16{static_cast<const uint16_t *>(p.A), p.lda, p.M};
+    a.b = Operand16{static_cast<const uint16_t *>(p.B), p.ldb, p.N};
+    a.bias = static_cast<const uint16_t *>(p.bias);
+    a.R = p.R;
+    a.C = p.C;
+    a.Z = static_cast<uint16_t *>(p.Z);
+    a.ldr = p.ldr;
+    a.ldc = p.ldc;
+    a.ldz = p.ldz;
+    a.act = p.act;
+    a.c_same = p.out != 0;
+    a.sums = p.dbias != nullptr ? static_cast<float *>(p.workspace) : nullptr;
+    a.ldp = round8(p.N);
+    if (k == LinearKernel::Split || k == LinearKernel::AnySplit) {
+        a.slices = split_slices(tiles_of(p.M, p.N, 128), p.K);
+        a.partial = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + sums_bytes(p.M, p.N));
+    }
+    hipError_t e;
+    if (p.in == 1) {
+        if (p.backward) e = p.b_kmajor ? run_kernel<BF16, true, true>(k, a, stream) : run_kernel<BF16, true, false>(k, a, stream);
+        else e = p.b_kmajor ? run_kernel<BF16, false, true>(k, a, stream) : run_kernel<BF16, false, false>(k, a, stream);
+    } else {
+        if (p.backward) e = p.b_kmajor ? run_kernel<F16, true, true>(k, a, stream) : run_kernel<F16, true, false>(k, a, stream);
+        else e = p.b_kmajor ? run_kernel<F16, false, true>(k, a, stream) : run_kernel<F16, false, false>(k, a, stream);
+    }
+    if (e != hipSuccess || p.dbias == nullptr) return e;
+    return launch_sums(a.sums, sums_rows(k, p.M), p.N, p.beta_bias, p.dbias, stream);
+}
+
+size_t activation_backward_workspace(int64_t M, int64_t N) { return size_t(ceil_div(M, AB_ROWS)) * N * 4 + 16; }
+
+hipError_t launch_activation_backward(const ActivationBackward &p, hipStream_t stream) {
+    ActivationArgs a{p, p.dbias != nullptr ? static_cast<float *>(p.workspace) : nullptr};
+    if (ceil_div(p.M, AB_ROWS) > 65535 || ceil_div(p.N, 64) > 0x7fffff) return hipErrorInvalidConfiguration;
+    const dim3 grid(unsigned(ceil_div(p.N, 64)), unsigned(ceil_div(p.M, AB_ROWS)));
+    auto run = [&](auto kernel) { kernel<<<grid, dim3(256), 0, stream>>>(a); };
+    switch (p.type_a * 3 + (p.act == act::NONE ? p.type_a : p.type_z)) {
+        case 0: run(activation_kernel<0, 0>); break;
+        case 1: run(activation_kernel<0, 1>); break;
+        case 2: run(activation_kernel<0, 2>); break;
+        case 3: run(activation_kernel<1, 0>); break;
+        case 4: run(activation_kernel<1, 1>); break;
+        case 5: run(activation_kernel<1, 2>); break;
+        case 6: run(activation_kernel<2, 0>); break;
+        case 7: run(activation_kernel<2, 1>); break;
+        default: run(activation_kernel<2, 2>); break;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.dbias == nullptr) return e;
+    return launch_sums(a.sums, ceil_div(p.M, AB_ROWS), p.N, p.beta, p.dbias, stream);
+}
+
+}  // namespace libgemm

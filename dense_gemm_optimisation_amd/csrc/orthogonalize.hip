@@ -1,0 +1,336 @@
+// Newton-Schulz steps that orthogonalise a matrix (gemm_orthogonalize):
+//   A = X X^T,   B = b A + c A^2,   X <- a X + B X,
+// X the matrix or its transpose with m <= n, scaled to Frobenius norm 1.
+//
+// The products run on the fp16 matrix instructions with fp32 sums.  What is kept
+// between them and why it is enough:
+//   X    two fp16 pieces, hi + lo, 22 bits: a X, whose error would grow with
+//        every step in the directions of small singular values, takes both;
+//        the products take hi;
+//   A, B one fp16 each.
+// fp16 holds three more bits than bf16 at the same rate.  Its range is no
+// matter: G enters as G * 2^e with an exponent that puts its norm into
+// [2^11, 2^12) (exactly, for a 16-bit G), and the rest of the norm is a factor
+// of the first step's epilogues; X is kept times 2^12, A times 2^12, B times
+// 2^8.
+//
+// A and B are symmetric: only tiles on and above the diagonal are computed,
+// and stored twice.  All matrices of the workspace have rows of a multiple of
+// 8 elements, their filling zero, so every product runs on direct loads.
+#include <math.h>
+
+#include "layers.hpp"
+#include "tile16.hpp"
+
+namespace libgemm {
+namespace {
+
+using namespace tile16;
+
+constexpr float X_SCALE = 4096.0f;  // 2^12, of X and of A; B's is 2^8
+constexpr int PARTS = 256;          // partial sums of squares per matrix
+
+struct OrthoArgs {
+    int64_t m, n, ldx, lda;  // m <= n; ldx = n and lda = m rounded up to 8
+    int64_t batch;
+    uint16_t *x, *next, *lo;  // X's first piece, the next step's, the second piece: m x ldx
+    uint16_t *gram, *poly;    // A and B: m x lda
+    const float *factor;      // of each matrix: the rest of the norm in the first step, else nullptr
+    float a, b, c;
+    // the last step's output
+    bool last, turned;  // turned: X is G's transpose
+    float alpha, beta;
+    void *O;
+    int64_t ldo, strideO;
+    int out;
+    int64_t tiles_m, tiles_n;  // of the launch's product; upper: on and above the diagonal
+};
+
+// ---------------------------------------------------------------- norm and input
+struct InputArgs {
+    int64_t M, N, ldg, strideG;
+    const void *G;
+    int in;
+    float eps;
+    double *parts;  // [batch][PARTS]
+    float *factor;  // [batch]
+    uint16_t *x, *lo;
+    int64_t ldx, m;
+};
+
+__device__ inline float value_of(const InputArgs &p, int64_t at) {
+    if (p.in == 0) return static_cast<const float *>(p.G)[at];
+    const uint16_t v = static_cast<const uint16_t *>(p.G)[at];
+    return p.in == 1 ? decode<BF16>(v) : decode<F16>(v);
+}
+
+__device__ inline double block_sum(double s, double *scratch) {
+    scratch[threadIdx.x] = s;
+    __syncthreads();
+    for (int d = 128; d > 0; d /= 2) {
+        if (int(threadIdx.x) < d) scratch[threadIdx.x] += scratch[threadIdx.x + d];
+        __syncthreads();
+    }
+    return scratch[0];
+}
+
+// Squares in 64 bits: fp32's would leave its range.  Part i has rows i, i +
+// PARTS, ...
+__global__ __launch_bounds__(256) void norm_kernel(InputArgs p) {
+    __shared__ double scratch[256];
+    const int64_t base = blockIdx.y * p.strideG;
+    double s = 0.0;
+    for (int64_t r = blockIdx.x; r < p.M; r += PARTS)
+        for (int64_t c = threadIdx.x; c < p.N; c += 256) {
+            const double v = value_of(p, base + r * p.ldg + c);
+            s += v * v;
+        }
+    s = block_sum(s, scratch);
+    if (threadIdx.x == 0) p.parts[blockIdx.y * PARTS + blockIdx.x] = s;
+}
+
+// 64 x 64 elements of G into X's pieces, turned where M > N.
+__global__ __launch_bounds__(256) void input_kernel(InputArgs p) {
+    __shared__ double scratch[256];
+    __shared__ float tile[64][65];
+    const int64_t batch = blockIdx.z;
+    const double norm = sqrt(block_sum(p.parts[batch * PARTS + threadIdx.x], scratch));
+    // norm * 2^e in [2^11, 2^12); the rest of 2^12 * G / max(norm, eps)
+    const bool finite = norm < 1e300;
+    const int e = finite && norm > 0.0 ? 11 - ilogb(norm) : 0;
+    const double least = norm > p.eps ? norm : double(p.eps);
+    const float factor = !finite ? NAN : norm > 0.0 ? float(ldexp(4096.0 / least, -e)) : 0.0f;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.factor[batch] = factor;
+    const bool turned = p.M > p.N;
+    const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
+    const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
+    auto put = [&](int64_t r, int64_t c, float v) {
+        if (r >= p.m || c >= p.ldx) return;
+        const int64_t at = (batch * p.m + r) * p.ldx + c;
+        const uint32_t hi = encode<F16>(v);
+        p.x[at] = uint16_t(hi);
+        p.lo[at] = uint16_t(encode<F16>(v - decode<F16>(hi)));
+    };
+    for (int i = row; i < 64; i += 4) {
+        const int64_t r = r0 + i, c = c0 + col;
+        const float v = r < p.M && c < p.N ? ldexpf(value_of(p, batch * p.strideG + r * p.ldg + c), e) : 0.0f;
+        if (turned) tile[i][col] = v;
+        else put(r, c, v);
+    }
+    if (!turned) return;
+    __syncthreads();
+    for (int i = row; i < 64; i += 4) put(c0 + i, r0 + col, tile[col][i]);
+}
+
+// ---------------------------------------------------------------- products
+enum class Step { Gram, Poly, Update };
+
+// Tile `id` of the upper triangle of T x T tiles, row by row.
+__device__ inline void upper_tile(int64_t id, int64_t T, int64_t &tm, int64_t &tn) {
+    tm = 0;
+    while (id >= T - tm) {
+        id -= T - tm;
+        ++tm;
+    }
+    tn = tm + id;
+}
+
+template <class Shape, Step STEP>
+__global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void product_kernel(OrthoArgs p) {
+    __shared__ __attribute__((aligned(1024))) char smem[Shape::LDS_BYTES];
+    LDS char *lds = (LDS char *)smem;
+    constexpr bool SYMMETRIC = STEP != Step::Update;
+    const int64_t id = xcd_remap(blockIdx.x, gridDim.x, 8), per = gridDim.x / p.batch;
+    const int64_t batch = uniform(id / per);
+    int64_t tm, tn;
+    if (SYMMETRIC) {
+        upper_tile(id - batch * per, p.tiles_m, tm, tn);
+    } else {
+        const TileCoord t = tile_of(TileGrid{p.tiles_m, p.tiles_n, 1, 8, 1}, id - batch * per);
+        tm = t.tm;
+        tn = t.tn;
+    }
+    const int64_t m0 = uniform(tm) * Shape::TM, n0 = uniform(tn) * Shape::TN;
+    uint16_t *x = p.x + batch * p.m * p.ldx, *gram = p.gram + batch * p.m * p.lda, *poly = p.poly + batch * p.m * p.lda;
+    const Operand16 xr{x, p.ldx, p.m}, xc{x, p.ldx, p.ldx}, ar{gram, p.lda, p.m}, br{poly, p.lda, p.m};
+    const int64_t K = STEP == Step::Gram ? p.ldx : p.lda;
+    const int64_t N = SYMMETRIC ? p.lda : p.ldx;
+    typename Shape::Acc acc;
+    // B's filling is columns, X has no rows for them: K = m there
+    const int64_t depth = STEP == Step::Update ? p.m : K;
+    const int buf = Shape::run(STEP == Step::Gram ? xr : STEP == Step::Poly ? ar : br,
+                               STEP == Step::Gram ? xr : STEP == Step::Poly ? ar : xc, depth, m0, n0, 0,
+                               (depth + BK - 1) / BK, lds, acc);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t mw = m0 + Shape::wave_m(wave) * Shape::WTM, nw = n0 + Shape::wave_n(wave) * Shape::WTN;
+    if (mw >= p.m || nw >= N) return;
+    const float f = p.factor != nullptr ? p.factor[batch] : 1.0f;
+    LDS float *staging = Shape::staging(lds, buf, wave);
+    if constexpr (SYMMETRIC) {
+        uint16_t *out = STEP == Step::Gram ? gram : poly;
+        visit_tile(acc, p.m, N, mw, nw, lane, staging, [&](int64_t r, int64_t c, int count, float(&v)[8]) {
+            if constexpr (STEP == Step::Gram) {
+                const float s = f * f / X_SCALE;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= s;
+            } else {
+                float g[8];
+                load8<F16>(gram + r * p.lda + c, count, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(p.c * 0x1p-16f, v[e], p.b * 0x1p-4f * g[e]);
+            }
+            store8<F16>(out + r * p.lda + c, count, v);
+            if (n0 > m0)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < p.m) out[(c + e) * p.lda + r] = uint16_t(encode<F16>(v[e]));
+        });
+    } else {
+        uint16_t *lo = p.lo + batch * p.m * p.ldx, *next = p.next + batch * p.m * p.ldx;
+        visit_tile(acc, p.m, N, mw, nw, lane, staging, [&](int64_t r, int64_t c, int count, float(&v)[8]) {
+            float h[8], l[8];
+            const int64_t at = r * p.ldx + c;
+            load8<F16>(x + at, count, h);
+            load8<F16>(lo + at, count, l);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = f * __builtin_fmaf(0x1p-8f, v[e], p.a * (h[e] + l[e]));
+            if (!p.last) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) l[e] = v[e] - decode<F16>(encode<F16>(v[e]));
+                store8<F16>(next + at, count, v);
+                store8<F16>(lo + at, count, l);
+                return;
+            }
+            const float s = p.alpha / X_SCALE;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (c + e >= p.n) continue;
+                const int64_t o = batch * p.strideO + (p.turned ? (c + e) * p.ldo + r : r * p.ldo + c + e);
+                float y = s * v[e];
+                if (p.out == 0) {
+                    float *d = static_cast<float *>(p.O) + o;
+                    *d = p.beta != 0.0f ? __builtin_fmaf(p.beta, *d, y) : y;
+                } else {
+                    uint16_t *d = static_cast<uint16_t *>(p.O) + o;
+                    if (p.beta != 0.0f) y = __builtin_fmaf(p.beta, p.out == 1 ? decode<BF16>(*d) : decode<F16>(*d), y);
+                    *d = uint16_t(p.out == 1 ? encode<BF16>(y) : encode<F16>(y));
+                }
+            }
+        });
+    }
+}
+
+// ---------------------------------------------------------------- host
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_to(int64_t n, int64_t m) { return ceil_div(n, m) * m; }
+
+struct Layout {
+    int64_t m, n, ldx, lda;
+    size_t parts, factor, x, next, lo, gram, poly, bytes;
+};
+Layout layout_of(int64_t M, int64_t N, int64_t batch) {
+    Layout l{};
+    l.m = M < N ? M : N;
+    l.n = M < N ? N : M;
+    l.ldx = round_to(l.n, 8);
+    l.lda = round_to(l.m, 8);
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t here = at;
+        at += size_t(round_to(bytes, 256));
+        return here;
+    };
+    l.parts = take(batch * PARTS * 8);
+    l.factor = take(batch * 4);
+    l.x = take(batch * l.m * l.ldx * 2);
+    l.next = take(batch * l.m * l.ldx * 2);
+    l.lo = take(batch * l.m * l.ldx * 2);
+    l.gram = take(batch * l.m * l.lda * 2);
+    l.poly = take(batch * l.m * l.lda * 2);
+    l.bytes = at;
+    return l;
+}
+
+// 256 x 256 tiles where they fill the chip.
+bool large(int64_t m, int64_t n, int64_t batch) { return ceil_div(m, 256) * ceil_div(n, 256) * batch >= 192; }
+
+template <Step STEP>
+hipError_t launch_product(OrthoArgs &a, hipStream_t stream) {
+    constexpr bool B_KMAJOR = STEP != Step::Update;
+    using Large = Tile<F16, 256, 256, 2, 4, true, B_KMAJOR, true>;
+    using Small = Tile<F16, 128, 128, 2, 2, true, B_KMAJOR, true>;
+    const int64_t cols = STEP == Step::Update ? a.n : a.m;
+    const bool big = large(a.m, cols, a.batch);
+    const int64_t side = big ? 256 : 128;
+    a.tiles_m = ceil_div(a.m, side);
+    a.tiles_n = ceil_div(cols, side);
+    const int64_t tiles = a.batch * (STEP == Step::Update ? a.tiles_m * a.tiles_n : a.tiles_m * (a.tiles_m + 1) / 2);
+    if (tiles > 0x7fffff) return hipErrorInvalidConfiguration;
+    if (big) product_kernel<Large, STEP><<<dim3(unsigned(tiles)), dim3(Large::THREADS), 0, stream>>>(a);
+    else product_kernel<Small, STEP><<<dim3(unsigned(tiles)), dim3(Small::THREADS), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+const char *orthogonalize_kernel_name(int64_t M, int64_t N, int64_t batch) {
+    if (M == 0 || N == 0 || batch == 0) return "";
+    return large(M < N ? M : N, M < N ? N : M, batch) ? "orthogonalize_mfma_256" : "orthogonalize_mfma_128";
+}
+
+size_t orthogonalize_workspace(int64_t M, int64_t N, int64_t batch) { return layout_of(M, N, batch).bytes; }
+
+hipError_t launch_orthogonalize(const Orthogonalize &p, hipStream_t stream) {
+    const Layout l = layout_of(p.M, p.N, p.batch);
+    char *w = static_cast<char *>(p.workspace);
+    auto half = [&](size_t at) { return reinterpret_cast<uint16_t *>(w + at); };
+    float *factor = reinterpret_cast<float *>(w + l.factor);
+    InputArgs in{p.M, p.N, p.ldg, p.strideG, p.G, p.in, p.eps, reinterpret_cast<double *>(w + l.parts), factor,
+                 half(l.x), half(l.lo), l.ldx, l.m};
+    // the tiles of G also cover the filling of X's rows
+    const bool turned = p.M > p.N;
+    const int64_t rows = ceil_div(turned ? l.ldx : p.M, 64), cols = ceil_div(turned ? p.N : l.ldx, 64);
+    if (rows > 65535 || cols > 0x7fffff || p.batch > 65535) return hipErrorInvalidConfiguration;
+    norm_kernel<<<dim3(PARTS, unsigned(p.batch)), dim3(256), 0, stream>>>(in);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    input_kernel<<<dim3(unsigned(cols), unsigned(rows), unsigned(p.batch)), dim3(256), 0, stream>>>(in);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    OrthoArgs a{};
+    a.m = l.m;
+    a.n = l.n;
+    a.ldx = l.ldx;
+    a.lda = l.lda;
+    a.batch = p.batch;
+    a.x = half(l.x);
+    a.next = half(l.next);
+    a.lo = half(l.lo);
+    a.gram = half(l.gram);
+    a.poly = half(l.poly);
+    a.turned = turned;
+    a.alpha = p.alpha;
+    a.beta = p.beta;
+    a.O = p.O;
+    a.ldo = p.ldo;
+    a.strideO = p.strideO;
+    a.out = p.out;
+    for (int s = 0; s < p.steps; ++s) {
+        a.factor = s == 0 ? factor : nullptr;
+        a.last = s == p.steps - 1;
+        a.a = p.coefficients != nullptr ? p.coefficients[3 * s] : 3.4445f;
+        a.b = p.coefficients != nullptr ? p.coefficients[3 * s + 1] : -4.7750f;
+        a.c = p.coefficients != nullptr ? p.coefficients[3 * s + 2] : 2.0315f;
+        e = launch_product<Step::Gram>(a, stream);
+        if (e == hipSuccess) e = launch_product<Step::Poly>(a, stream);
+        if (e == hipSuccess) e = launch_product<Step::Update>(a, stream);
+        if (e != hipSuccess) return e;
+        uint16_t *t = a.x;
+        a.x = a.next;
+        a.next = t;
+    }
+    return hipSuccess;
+}
+
+}  // namespace libgemm

@@ -149,7 +149,8 @@ typedef enum gemm_output_t {
 typedef enum gemm_activation_t {
     GEMM_ACT_NONE = 0,
     GEMM_ACT_RELU = 1, /* max(x, 0) */
-    GEMM_ACT_GELU = 2  /* x * Phi(x), Phi the standard normal distribution function */
+    GEMM_ACT_GELU = 2, /* x * Phi(x), Phi the standard normal distribution function */
+    GEMM_ACT_SILU = 3  /* x / (1 + exp(-x)); only the calls of libgemm_layers.h take it */
 } gemm_activation_t;
 
 typedef enum gemm_status_t {
