@@ -14,9 +14,23 @@
 // of the first step's epilogues; X is kept times 2^12, A times 2^12, B times
 // 2^8.
 //
-// A and B are symmetric: only tiles on and above the diagonal are computed,
-// and stored twice.  All matrices of the workspace have rows of a multiple of
-// 8 elements, their filling zero, so every product runs on direct loads.
+// What is rounded is what differs from the mean: with s the mean of A's
+// eigenvalues (|X|^2 / m) and E = A - s I, the same polynomial of X X^T is
+//   B' = (b + 2 c s) E + c E^2,   X <- (a + b s + c s^2) X + B' X,
+// and E is small once the singular values are alike, where a X and B X nearly
+// cancel.  It halves the error that E's and B's roundings leave (simulated in
+// 64 bits: 128 x 128 1.6e-3 -> 7e-4 of the Frobenius norm, 512 x 512 1.3e-3 ->
+// 6e-4).  s is the squares' sum that the step before left; it need not be exact, only the
+// same everywhere.
+//
+// Kernels:
+//   small_kernel    a matrix whose pieces fit into one workgroup's LDS and
+//                   registers: all steps in one launch, X's master in fp32 registers;
+//   norm_kernel, input_kernel, then three product_kernels per step: A and B
+//                   are symmetric, so only tiles on and above the diagonal
+//                   are computed, and stored twice.  All matrices of the
+//                   workspace have rows of a multiple of 8 elements, their
+//                   filling zero, so every product runs on direct loads.
 #include <math.h>
 
 #include "layers.hpp"
@@ -36,6 +50,9 @@ struct OrthoArgs {
     uint16_t *x, *next, *lo;  // X's first piece, the next step's, the second piece: m x ldx
     uint16_t *gram, *poly;    // A and B: m x lda
     const float *factor;      // of each matrix: the rest of the norm in the first step, else nullptr
+    float *shift;             // of each matrix: s of this step
+    float *squares;           // of each matrix and tile of the last update: the sum of X's squares
+    int64_t tiles_x;          // those tiles
     float a, b, c;
     // the last step's output
     bool last, turned;  // turned: X is G's transpose
@@ -52,8 +69,8 @@ struct InputArgs {
     const void *G;
     int in;
     float eps;
-    double *parts;  // [batch][PARTS]
-    float *factor;  // [batch]
+    double *parts;          // [batch][PARTS]
+    float *factor, *shift;  // [batch]
     uint16_t *x, *lo;
     int64_t ldx, m;
 };
@@ -98,9 +115,12 @@ __global__ __launch_bounds__(256) void input_kernel(InputArgs p) {
     // norm * 2^e in [2^11, 2^12); the rest of 2^12 * G / max(norm, eps)
     const bool finite = norm < 1e300;
     const int e = finite && norm > 0.0 ? 11 - ilogb(norm) : 0;
-    const double least = norm > p.eps ? norm : double(p.eps);
+    const double least = norm > p.eps ? norm : p.eps > 0.0f ? double(p.eps) : 1.0;
     const float factor = !finite ? NAN : norm > 0.0 ? float(ldexp(4096.0 / least, -e)) : 0.0f;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.factor[batch] = factor;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+        p.factor[batch] = factor;
+        p.shift[batch] = float((norm / least) * (norm / least) / p.m);
+    }
     const bool turned = p.M > p.N;
     const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
     const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
@@ -124,6 +144,18 @@ __global__ __launch_bounds__(256) void input_kernel(InputArgs p) {
 
 // ---------------------------------------------------------------- products
 enum class Step { Gram, Poly, Update };
+
+// O[at] <- y + beta * O[at]
+__device__ inline void put_output(const OrthoArgs &p, int64_t at, float y) {
+    if (p.out == 0) {
+        float *d = static_cast<float *>(p.O) + at;
+        *d = p.beta != 0.0f ? __builtin_fmaf(p.beta, *d, y) : y;
+    } else {
+        uint16_t *d = static_cast<uint16_t *>(p.O) + at;
+        if (p.beta != 0.0f) y = __builtin_fmaf(p.beta, p.out == 1 ? decode<BF16>(*d) : decode<F16>(*d), y);
+        *d = uint16_t(p.out == 1 ? encode<BF16>(y) : encode<F16>(y));
+    }
+}
 
 // Tile `id` of the upper triangle of T x T tiles, row by row.
 __device__ inline void upper_tile(int64_t id, int64_t T, int64_t &tm, int64_t &tn) {
@@ -155,6 +187,21 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void
     const Operand16 xr{x, p.ldx, p.m}, xc{x, p.ldx, p.ldx}, ar{gram, p.lda, p.m}, br{poly, p.lda, p.m};
     const int64_t K = STEP == Step::Gram ? p.ldx : p.lda;
     const int64_t N = SYMMETRIC ? p.lda : p.ldx;
+    // s: read, or added up (by every workgroup alike) from the last update's tiles
+    __shared__ float sums[Shape::WAVES];
+    float shift = 0.0f;
+    if (STEP != Step::Gram || p.factor != nullptr) {
+        shift = p.shift[batch];
+    } else {
+        float q = 0.0f;
+        for (int64_t i = threadIdx.x; i < p.tiles_x; i += Shape::THREADS) q += p.squares[batch * p.tiles_x + i];
+        for (int d = 1; d < 64; d *= 2) q += __shfl_xor(q, d);
+        if ((threadIdx.x & 63) == 0) sums[threadIdx.x / 64] = q;
+        __syncthreads();
+        for (int w = 0; w < Shape::WAVES; ++w) shift += sums[w];
+        shift /= X_SCALE * X_SCALE * float(p.m);
+        if (tm == 0 && tn == 0 && threadIdx.x == 0) p.shift[batch] = shift;
+    }
     typename Shape::Acc acc;
     // B's filling is columns, X has no rows for them: K = m there
     const int64_t depth = STEP == Step::Update ? p.m : K;
@@ -164,21 +211,23 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t mw = m0 + Shape::wave_m(wave) * Shape::WTM, nw = n0 + Shape::wave_n(wave) * Shape::WTN;
-    if (mw >= p.m || nw >= N) return;
+    const bool live = mw < p.m && nw < N;
+    if (SYMMETRIC && !live) return;
     const float f = p.factor != nullptr ? p.factor[batch] : 1.0f;
     LDS float *staging = Shape::staging(lds, buf, wave);
     if constexpr (SYMMETRIC) {
         uint16_t *out = STEP == Step::Gram ? gram : poly;
+        const float b = __builtin_fmaf(2.0f * p.c, shift, p.b);
         visit_tile(acc, p.m, N, mw, nw, lane, staging, [&](int64_t r, int64_t c, int count, float(&v)[8]) {
             if constexpr (STEP == Step::Gram) {
                 const float s = f * f / X_SCALE;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= s;
+                for (int e = 0; e < 8; ++e) v[e] = s * v[e] - (r == c + e ? X_SCALE * shift : 0.0f);
             } else {
                 float g[8];
                 load8<F16>(gram + r * p.lda + c, count, g);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(p.c * 0x1p-16f, v[e], p.b * 0x1p-4f * g[e]);
+                for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(p.c * 0x1p-16f, v[e], b * 0x1p-4f * g[e]);
             }
             store8<F16>(out + r * p.lda + c, count, v);
             if (n0 > m0)
@@ -188,16 +237,21 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void
         });
     } else {
         uint16_t *lo = p.lo + batch * p.m * p.ldx, *next = p.next + batch * p.m * p.ldx;
-        visit_tile(acc, p.m, N, mw, nw, lane, staging, [&](int64_t r, int64_t c, int count, float(&v)[8]) {
+        const float a = __builtin_fmaf(shift, __builtin_fmaf(shift, p.c, p.b), p.a);
+        float square = 0.0f;
+        if (live) visit_tile(acc, p.m, N, mw, nw, lane, staging, [&](int64_t r, int64_t c, int count, float(&v)[8]) {
             float h[8], l[8];
             const int64_t at = r * p.ldx + c;
             load8<F16>(x + at, count, h);
             load8<F16>(lo + at, count, l);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = f * __builtin_fmaf(0x1p-8f, v[e], p.a * (h[e] + l[e]));
+            for (int e = 0; e < 8; ++e) v[e] = f * __builtin_fmaf(0x1p-8f, v[e], a * (h[e] + l[e]));
             if (!p.last) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) l[e] = v[e] - decode<F16>(encode<F16>(v[e]));
+                for (int e = 0; e < 8; ++e) {
+                    square += v[e] * v[e];
+                    l[e] = v[e] - decode<F16>(encode<F16>(v[e]));
+                }
                 store8<F16>(next + at, count, v);
                 store8<F16>(lo + at, count, l);
                 return;
@@ -207,17 +261,190 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void
             for (int e = 0; e < 8; ++e) {
                 if (c + e >= p.n) continue;
                 const int64_t o = batch * p.strideO + (p.turned ? (c + e) * p.ldo + r : r * p.ldo + c + e);
-                float y = s * v[e];
-                if (p.out == 0) {
-                    float *d = static_cast<float *>(p.O) + o;
-                    *d = p.beta != 0.0f ? __builtin_fmaf(p.beta, *d, y) : y;
-                } else {
-                    uint16_t *d = static_cast<uint16_t *>(p.O) + o;
-                    if (p.beta != 0.0f) y = __builtin_fmaf(p.beta, p.out == 1 ? decode<BF16>(*d) : decode<F16>(*d), y);
-                    *d = uint16_t(p.out == 1 ? encode<BF16>(y) : encode<F16>(y));
-                }
+                put_output(p, o, s * v[e]);
             }
         });
+        if (p.last) return;
+        for (int d = 1; d < 64; d *= 2) square += __shfl_xor(square, d);
+        if (lane == 0) sums[wave] = square;
+        __syncthreads();
+        if (threadIdx.x != 0) return;
+        for (int w = 1; w < Shape::WAVES; ++w) square += sums[w];
+        p.squares[batch * per + tm * p.tiles_n + tn] = square;
+    }
+}
+
+// ---------------------------------------------------------------- in one workgroup
+// Blocks of 32 x 32: at most 4 x 4 of A, and MOST_BLOCKS of X, eight waves.
+constexpr int SMALL_WAVES = 8, SMALL_SIDE = 128, SMALL_BLOCKS = 6;  // X's blocks per wave
+constexpr int SMALL_LDS = 150 * 1024;                              // beside what is declared
+struct SmallArgs {
+    InputArgs in;
+    OrthoArgs p;
+    int steps;
+    float coefficients[3 * 32];
+    int pitch_x, pitch_a;  // bytes per row of X and of A, 16 more than a multiple of 64
+    int blocks_m, blocks_n;
+};
+
+// Fragments of 32 rows for 16 k from k0: K-contiguous rows, and k rows read
+// transposed.  A row is 16 bytes longer than a multiple of 64, so neighbouring
+// rows start in different banks.
+__device__ inline u32x4 frag_rows(const LDS char *base, int pitch, int row0, int k0, int lane) {
+    return *reinterpret_cast<const LDS u32x4 *>(base + (row0 + (lane & 31)) * pitch + (k0 + 8 * (lane >> 5)) * 2);
+}
+__device__ inline u32x4 frag_columns(const LDS char *base, int pitch, int col0, int k0, int lane) {
+    const int g = lane >> 5, h = (lane >> 4) & 1, ii = lane & 15;
+    u32x4 out;
+#pragma unroll
+    for (int e2 = 0; e2 < 2; ++e2) {
+        const LDS s16x4 *at = reinterpret_cast<const LDS s16x4 *>(
+            base + (k0 + g * 8 + e2 * 4 + (ii >> 2)) * pitch + (col0 + h * 16 + 4 * (ii & 3)) * 2);
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(const_cast<LDS s16x4 *>(at)));
+        out[2 * e2] = v[0];
+        out[2 * e2 + 1] = v[1];
+    }
+    return out;
+}
+__device__ inline void put4(LDS char *at, const float (&v)[4]) {
+    u32x2 w;
+    w[0] = encode<F16>(v[0]) | encode<F16>(v[1]) << 16;
+    w[1] = encode<F16>(v[2]) | encode<F16>(v[3]) << 16;
+    *reinterpret_cast<LDS u32x2 *>(at) = w;
+}
+
+// BLOCKS: of X per wave at most.
+template <int BLOCKS>
+__global__ __launch_bounds__(SMALL_WAVES * 64, 2) void small_kernel(SmallArgs a) {
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    __shared__ double scratch[SMALL_WAVES];
+    __shared__ float sums[SMALL_WAVES];
+    const InputArgs &in = a.in;
+    const OrthoArgs &p = a.p;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, T = SMALL_WAVES * 64;
+    const int64_t batch = blockIdx.x;
+    const int m = int(p.m), n = int(p.n), mp = a.blocks_m * 32, np = a.blocks_n * 32;
+    LDS char *x = (LDS char *)smem, *gram = x + mp * a.pitch_x, *poly = gram + mp * a.pitch_a;
+    // the norm, in 64 bits
+    double q = 0.0;
+    for (int i = threadIdx.x; i < m * n; i += T) {
+        const double v = value_of(in, batch * in.strideG + i / in.N * in.ldg + i % in.N);
+        q += v * v;
+    }
+    for (int d = 1; d < 64; d *= 2) q += __shfl_xor(q, d);
+    if (lane == 0) scratch[wave] = q;
+    __syncthreads();
+    q = 0.0;
+    for (int w = 0; w < SMALL_WAVES; ++w) q += scratch[w];
+    const double norm = sqrt(q), least = norm > in.eps ? norm : in.eps > 0.0f ? double(in.eps) : 1.0;
+    const float factor = norm < 1e300 ? 1.0f : NAN;
+    float shift = float((norm / least) * (norm / least) / m);
+    // a lane's part of block i: row l % 32, columns 8q + 4 (l / 32) + 0..3
+    const int r_in = lane & 31, c_in = 4 * (lane >> 5), blocks = a.blocks_m * a.blocks_n;
+    f32x16 X[BLOCKS];
+    auto store_x = [&](int i, int block) {
+        LDS char *at = x + (block / a.blocks_n * 32 + r_in) * a.pitch_x + (block % a.blocks_n * 32 + c_in) * 2;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float v[4] = {X[i][4 * u], X[i][4 * u + 1], X[i][4 * u + 2], X[i][4 * u + 3]};
+            put4(at + 16 * u, v);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < BLOCKS; ++i) {
+        const int block = wave + i * SMALL_WAVES;
+        if (block >= blocks) continue;
+        const int r = block / a.blocks_n * 32 + r_in, c = block % a.blocks_n * 32 + c_in;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const int col = c + 8 * (u / 4) + u % 4;
+            float v = 0.0f;
+            if (r < m && col < n)
+                v = factor * float(double(value_of(in, batch * in.strideG + (p.turned ? col * in.ldg + r : r * in.ldg + col))) *
+                                   (X_SCALE / least));
+            X[i][u] = v;
+        }
+        store_x(i, block);
+    }
+    __syncthreads();
+    const int blocks_a = a.blocks_m * a.blocks_m;
+    for (int step = 0; step < a.steps; ++step) {
+        const float ca = a.coefficients[3 * step], cb = a.coefficients[3 * step + 1], cc = a.coefficients[3 * step + 2];
+        for (int block = wave; block < blocks_a; block += SMALL_WAVES) {
+            const int bi = block / a.blocks_m * 32, bj = block % a.blocks_m * 32;
+            f32x16 acc = {};
+            for (int k = 0; k < np; k += 16)
+                acc = mfma32<F16>(frag_rows(x, a.pitch_x, bj, k, lane), frag_rows(x, a.pitch_x, bi, k, lane), acc);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = acc[4 * u + e] / X_SCALE;
+                    // the filling stays zero
+                    if (bi + r_in == bj + c_in + 8 * u + e && bi + r_in < m) v[e] -= X_SCALE * shift;
+                }
+                put4(gram + (bi + r_in) * a.pitch_a + (bj + c_in + 8 * u) * 2, v);
+            }
+        }
+        __syncthreads();
+        const float b = __builtin_fmaf(2.0f * cc, shift, cb);
+        for (int block = wave; block < blocks_a; block += SMALL_WAVES) {
+            const int bi = block / a.blocks_m * 32, bj = block % a.blocks_m * 32;
+            f32x16 acc = {};
+            for (int k = 0; k < mp; k += 16)
+                acc = mfma32<F16>(frag_rows(gram, a.pitch_a, bj, k, lane), frag_rows(gram, a.pitch_a, bi, k, lane), acc);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int at = (bi + r_in) * a.pitch_a + (bj + c_in + 8 * u) * 2;
+                const u32x2 g = *reinterpret_cast<const LDS u32x2 *>(gram + at);
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = __builtin_fmaf(cc * 0x1p-16f, acc[4 * u + e], b * 0x1p-4f * decode<F16>(g[e / 2] >> (16 * (e % 2)) & 0xffffu));
+                put4(poly + at, v);
+            }
+        }
+        __syncthreads();
+        const float own = __builtin_fmaf(shift, __builtin_fmaf(shift, cc, cb), ca);
+        float square = 0.0f;
+#pragma unroll
+        for (int i = 0; i < BLOCKS; ++i) {
+            const int block = wave + i * SMALL_WAVES;
+            if (block >= blocks) continue;
+            const int bi = block / a.blocks_n * 32, bj = block % a.blocks_n * 32;
+            f32x16 acc = {};
+            for (int k = 0; k < mp; k += 16)
+                acc = mfma32<F16>(frag_columns(x, a.pitch_x, bj, k, lane), frag_rows(poly, a.pitch_a, bi, k, lane), acc);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                X[i][u] = __builtin_fmaf(0x1p-8f, acc[u], own * X[i][u]);
+                square += X[i][u] * X[i][u];
+            }
+        }
+        for (int d = 1; d < 64; d *= 2) square += __shfl_xor(square, d);
+        if (lane == 0) sums[wave] = square;
+        __syncthreads();  // X has been read by every wave
+#pragma unroll
+        for (int i = 0; i < BLOCKS; ++i)
+            if (wave + i * SMALL_WAVES < blocks) store_x(i, wave + i * SMALL_WAVES);
+        shift = 0.0f;
+        for (int w = 0; w < SMALL_WAVES; ++w) shift += sums[w];
+        shift /= X_SCALE * X_SCALE * float(m);
+        __syncthreads();
+    }
+    const float s = p.alpha / X_SCALE;
+#pragma unroll
+    for (int i = 0; i < BLOCKS; ++i) {
+        const int block = wave + i * SMALL_WAVES;
+        if (block >= blocks) continue;
+        const int r = block / a.blocks_n * 32 + r_in, c = block % a.blocks_n * 32 + c_in;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const int col = c + 8 * (u / 4) + u % 4;
+            if (r < m && col < n)
+                put_output(p, batch * p.strideO + (p.turned ? col * p.ldo + r : r * p.ldo + col), s * X[i][u]);
+        }
     }
 }
 
@@ -227,7 +454,7 @@ int64_t round_to(int64_t n, int64_t m) { return ceil_div(n, m) * m; }
 
 struct Layout {
     int64_t m, n, ldx, lda;
-    size_t parts, factor, x, next, lo, gram, poly, bytes;
+    size_t parts, factor, shift, squares, x, next, lo, gram, poly, bytes;
 };
 Layout layout_of(int64_t M, int64_t N, int64_t batch) {
     Layout l{};
@@ -243,6 +470,8 @@ Layout layout_of(int64_t M, int64_t N, int64_t batch) {
     };
     l.parts = take(batch * PARTS * 8);
     l.factor = take(batch * 4);
+    l.shift = take(batch * 4);
+    l.squares = take(batch * ceil_div(l.m, 128) * ceil_div(l.n, 128) * 4);
     l.x = take(batch * l.m * l.ldx * 2);
     l.next = take(batch * l.m * l.ldx * 2);
     l.lo = take(batch * l.m * l.ldx * 2);
@@ -250,6 +479,25 @@ Layout layout_of(int64_t M, int64_t N, int64_t batch) {
     l.poly = take(batch * l.m * l.lda * 2);
     l.bytes = at;
     return l;
+}
+
+// What small_kernel needs of LDS; 0 where the matrix does not fit.
+size_t small_lds(int64_t m, int64_t n) {
+    const int64_t bm = ceil_div(m, 32), bn = ceil_div(n, 32);
+    if (m > SMALL_SIDE || bm * bn > SMALL_BLOCKS * SMALL_WAVES) return 0;
+    const int64_t bytes = bm * 32 * ((bn * 64 + 16) + 2 * (bm * 64 + 16));
+    return bytes <= SMALL_LDS ? size_t(bytes) : 0;
+}
+
+template <int BLOCKS>
+hipError_t launch_small(const SmallArgs &a, size_t lds, hipStream_t stream) {
+    if (lds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&small_kernel<BLOCKS>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, SMALL_LDS);
+        if (e != hipSuccess) return e;
+    }
+    small_kernel<BLOCKS><<<dim3(unsigned(a.p.batch)), dim3(SMALL_WAVES * 64), lds, stream>>>(a);
+    return hipGetLastError();
 }
 
 // 256 x 256 tiles where they fill the chip.
@@ -265,6 +513,7 @@ hipError_t launch_product(OrthoArgs &a, hipStream_t stream) {
     const int64_t side = big ? 256 : 128;
     a.tiles_m = ceil_div(a.m, side);
     a.tiles_n = ceil_div(cols, side);
+    if (STEP == Step::Update) a.tiles_x = a.tiles_m * a.tiles_n;
     const int64_t tiles = a.batch * (STEP == Step::Update ? a.tiles_m * a.tiles_n : a.tiles_m * (a.tiles_m + 1) / 2);
     if (tiles > 0x7fffff) return hipErrorInvalidConfiguration;
     if (big) product_kernel<Large, STEP><<<dim3(unsigned(tiles)), dim3(Large::THREADS), 0, stream>>>(a);
@@ -276,6 +525,7 @@ hipError_t launch_product(OrthoArgs &a, hipStream_t stream) {
 
 const char *orthogonalize_kernel_name(int64_t M, int64_t N, int64_t batch) {
     if (M == 0 || N == 0 || batch == 0) return "";
+    if (small_lds(M < N ? M : N, M < N ? N : M) != 0) return "orthogonalize_small";
     return large(M < N ? M : N, M < N ? N : M, batch) ? "orthogonalize_mfma_256" : "orthogonalize_mfma_128";
 }
 
@@ -286,24 +536,17 @@ hipError_t launch_orthogonalize(const Orthogonalize &p, hipStream_t stream) {
     char *w = static_cast<char *>(p.workspace);
     auto half = [&](size_t at) { return reinterpret_cast<uint16_t *>(w + at); };
     float *factor = reinterpret_cast<float *>(w + l.factor);
-    InputArgs in{p.M, p.N, p.ldg, p.strideG, p.G, p.in, p.eps, reinterpret_cast<double *>(w + l.parts), factor,
+    InputArgs in{p.M, p.N, p.ldg, p.strideG, p.G, p.in, p.eps, reinterpret_cast<double *>(w + l.parts), factor, reinterpret_cast<float *>(w + l.shift),
                  half(l.x), half(l.lo), l.ldx, l.m};
-    // the tiles of G also cover the filling of X's rows
     const bool turned = p.M > p.N;
-    const int64_t rows = ceil_div(turned ? l.ldx : p.M, 64), cols = ceil_div(turned ? p.N : l.ldx, 64);
-    if (rows > 65535 || cols > 0x7fffff || p.batch > 65535) return hipErrorInvalidConfiguration;
-    norm_kernel<<<dim3(PARTS, unsigned(p.batch)), dim3(256), 0, stream>>>(in);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    input_kernel<<<dim3(unsigned(cols), unsigned(rows), unsigned(p.batch)), dim3(256), 0, stream>>>(in);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
     OrthoArgs a{};
     a.m = l.m;
     a.n = l.n;
     a.ldx = l.ldx;
     a.lda = l.lda;
     a.batch = p.batch;
+    a.shift = in.shift;
+    a.squares = reinterpret_cast<float *>(w + l.squares);
     a.x = half(l.x);
     a.next = half(l.next);
     a.lo = half(l.lo);
@@ -316,12 +559,36 @@ hipError_t launch_orthogonalize(const Orthogonalize &p, hipStream_t stream) {
     a.ldo = p.ldo;
     a.strideO = p.strideO;
     a.out = p.out;
+    auto coefficient = [&](int s, int i) {
+        constexpr float usual[3] = {3.4445f, -4.7750f, 2.0315f};
+        return p.coefficients != nullptr ? p.coefficients[3 * s + i] : usual[i];
+    };
+    if (const size_t lds = small_lds(l.m, l.n)) {
+        SmallArgs sm{in, a, p.steps, {}, 0, 0, int(ceil_div(l.m, 32)), int(ceil_div(l.n, 32))};
+        for (int s = 0; s < 3 * p.steps; ++s) sm.coefficients[s] = coefficient(s / 3, s % 3);
+        sm.pitch_x = sm.blocks_n * 64 + 16;
+        sm.pitch_a = sm.blocks_m * 64 + 16;
+        const int blocks = sm.blocks_m * sm.blocks_n;
+        if (p.batch > 0x7fffff) return hipErrorInvalidConfiguration;
+        if (blocks <= SMALL_WAVES) return launch_small<1>(sm, lds, stream);
+        if (blocks <= 2 * SMALL_WAVES) return launch_small<2>(sm, lds, stream);
+        return launch_small<SMALL_BLOCKS>(sm, lds, stream);
+    }
+    // the tiles of G also cover the filling of X's rows
+    const int64_t rows = ceil_div(turned ? l.ldx : p.M, 64), cols = ceil_div(turned ? p.N : l.ldx, 64);
+    if (rows > 65535 || cols > 0x7fffff || p.batch > 65535) return hipErrorInvalidConfiguration;
+    norm_kernel<<<dim3(PARTS, unsigned(p.batch)), dim3(256), 0, stream>>>(in);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    input_kernel<<<dim3(unsigned(cols), unsigned(rows), unsigned(p.batch)), dim3(256), 0, stream>>>(in);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
     for (int s = 0; s < p.steps; ++s) {
         a.factor = s == 0 ? factor : nullptr;
         a.last = s == p.steps - 1;
-        a.a = p.coefficients != nullptr ? p.coefficients[3 * s] : 3.4445f;
-        a.b = p.coefficients != nullptr ? p.coefficients[3 * s + 1] : -4.7750f;
-        a.c = p.coefficients != nullptr ? p.coefficients[3 * s + 2] : 2.0315f;
+        a.a = coefficient(s, 0);
+        a.b = coefficient(s, 1);
+        a.c = coefficient(s, 2);
         e = launch_product<Step::Gram>(a, stream);
         if (e == hipSuccess) e = launch_product<Step::Poly>(a, stream);
         if (e == hipSuccess) e = launch_product<Step::Update>(a, stream);

@@ -207,13 +207,13 @@ size_t gemm_orthogonalize_workspace_size(int64_t M, int64_t N, int64_t batch);
  *   batch    matrices strideG and strideO elements apart; those of O must
  *            not overlap.
  *   workspace   gemm_orthogonalize_workspace_size() bytes.
- * The sum of squares is formed in 64 bits.  X is kept between the steps as
- * two fp16 pieces, 22 bits; the products take its first piece and fp16 roundings of
- * A and of b A + c A^2 and add in fp32, which leaves X a few 2^-11 of its
- * elements' root mean square from the exact steps': of the order of bf16's
- * own rounding.  All of A, X and b A + c A^2 are scaled by powers of two so
- * that steps whose singular values stay below 2 and whose b A + c A^2 stays
- * below 128 are within fp16's range; others give infinities or NaN.  A matrix with an
+ * The sum of squares is formed in 64 bits.  X is kept between the steps in 22
+ * bits or more.  The products take fp16 roundings of X, of E = A - s I with s the
+ * mean of A's eigenvalues, and of (b + 2 c s) E + c E^2, and add in fp32,
+ * which leaves X about 2^-10 of its elements' root mean square from the exact
+ * steps': less than bf16's own rounding.  All are scaled by powers of two so
+ * that steps whose singular values stay below 2 and whose coefficients stay
+ * below 16 in magnitude are within fp16's range; others may give infinities or NaN.  A matrix with an
  * infinity or a NaN gives NaN throughout.
  * steps in 1 .. GEMM_ORTHOGONALIZE_MAX_STEPS (GEMM_ERR_UNSUPPORTED beyond). */
 gemm_status_t gemm_orthogonalize(int64_t M, int64_t N, const void *G, int64_t ldg,

@@ -127,7 +127,7 @@ USUAL = (3.4445, -4.7750, 2.0315)
 
 def newton_schulz(g, steps, coefficients=None, eps=0.0, rounding=False):
     """The steps in 64 bits, or with the roundings that the header names: X in two fp16 pieces, the products' operands
-    in one, scaled as the header says."""
+    (X, A less its mean eigenvalue, and its polynomial) in one, scaled to use fp16's range."""
     x = g.double()
     norm = torch.linalg.matrix_norm(x).item()
     turned = x.shape[0] > x.shape[1]
@@ -139,7 +139,11 @@ def newton_schulz(g, steps, coefficients=None, eps=0.0, rounding=False):
     for i in range(steps):
         a, b, c = USUAL if coefficients is None else coefficients[i]
         hi = half(x, 12)
-        gram = half(hi @ hi.t(), 12)
+        gram = hi @ hi.t()
+        if rounding:
+            s = ((x * x).sum() / x.shape[0]).item()
+            gram = half(gram - s * torch.eye(x.shape[0], dtype=torch.float64), 12)
+            a, b = a + s * (b + s * c), b + 2 * c * s
         poly = half(b * gram + c * (gram @ gram), 8)
         x = a * x + poly @ hi
         if rounding:
