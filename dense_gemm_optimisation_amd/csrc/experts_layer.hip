@@ -1,17 +1,16 @@
 // A whole layer of experts for a few tokens (gemm_experts_layer), in two
 // kernels that each read every live expert's weights once.
 //
-//   up_kernel    h = act(Up[0 .. H) x) * (Up[H .. 2H) x): a workgroup has 16 of
-//                H's rows, both halves, of one live expert, and up to 16, 32 or 64
-//                tokens that chose it; its eight waves deal the contracted D
-//                in runs of 128 and their sums meet in LDS;
-//   down_kernel  y = sum over the token's experts of w Down h: a workgroup
+//   up_kernel    w h, h = act(Up[0 .. H) x) * (Up[H .. 2H) x): a wave has 16 of
+//                H's rows, both halves, of one live expert, and the tokens that
+//                chose it; where that leaves too few waves, up to eight share
+//                the rows' D and meet in LDS.  w h leaves as two 16-bit
+//                pieces, hi + lo, so it is not rounded to 16 bits in between;
+//   down_kernel  y = sum over the token's experts of Down (w h): a workgroup
 //                has 16 of y's columns for all tokens and goes through
 //                every live expert, its waves dealing (expert, run of H) pairs,
 //                so a token's weighted sum is formed in one place and one order:
-//                no atomics.  h is scaled by the token's weight, in fp32, and
-//                split into two 16-bit pieces, so it is not rounded to 16
-//                bits in between.
+//                no atomics.
 //
 // Bound by reading the weights.  The 16 x 16 x 32 matrix instruction takes
 // them as its 16-row operand straight from global memory (a wave reads 16
@@ -32,11 +31,16 @@ namespace {
 using namespace tile16;
 
 constexpr int WAVES = 8, RUN = 128, STEPS = RUN / 32;
+constexpr int MOST_SLOTS = LAYER_MAX_TOKENS * LAYER_MAX_TOP_K;
 
 struct LayerArgs {
     ExpertsLayer p;
-    float *h;  // [token][choice][H], fp32
+    // w h of each choice, two pieces of X's type: [token][choice][piece][ldh]; its first choice of an
+    // expert has all of the token's
+    uint16_t *h;
+    int64_t ldh;  // H rounded up to 8, the filling zero
     int live_most;
+    int slices;   // waves of up_kernel that share a block's columns
 };
 
 template <class T>
@@ -102,62 +106,66 @@ struct Run {
     }
 };
 
-// The live experts, in rising order, in `list`; returns how many.  All
-// threads of the workgroup call it.
-__device__ int find_live(const LayerArgs &a, uint32_t *bits, uint16_t *list) {
+// What a workgroup finds out from the ids: the live experts in rising order.
+struct Live {
+    uint32_t bits[LAYER_MAX_EXPERTS / 32];
+    uint16_t list[LAYER_MAX_EXPERTS];
+    int16_t ids[MOST_SLOTS];  // -1: no expert
+};
+
+// Fills it; returns how many are live.  All threads of the workgroup call it.
+__device__ int find_live(const LayerArgs &a, Live &live) {
     const int E = int(a.p.experts), slots = int(a.p.tokens * a.p.top_k), words = (E + 31) / 32;
-    for (int i = threadIdx.x; i < words; i += blockDim.x) bits[i] = 0;
+    for (int i = threadIdx.x; i < words; i += blockDim.x) live.bits[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < slots; i += blockDim.x) {
         const uint32_t e = uint32_t(a.p.ids[i]);
-        if (e < uint32_t(E)) atomicOr(&bits[e / 32], 1u << (e % 32));
+        live.ids[i] = e < uint32_t(E) ? int16_t(e) : int16_t(-1);
+        if (e < uint32_t(E)) atomicOr(&live.bits[e / 32], 1u << (e % 32));
     }
     __syncthreads();
     int before = 0, total = 0;
     const int mine = int(threadIdx.x);
     for (int i = 0; i < words; ++i) {
-        const int n = __popc(bits[i]);
+        const int n = __popc(live.bits[i]);
         if (i < mine) before += n;
         total += n;
     }
     if (mine < words)
-        for (uint32_t b = bits[mine]; b != 0; b &= b - 1) list[before++] = uint16_t(32 * mine + __ffs(b) - 1);
+        for (uint32_t b = live.bits[mine]; b != 0; b &= b - 1) live.list[before++] = uint16_t(32 * mine + __ffs(b) - 1);
     __syncthreads();
     return total;
 }
 
-// Whether token t chose expert e: its first choice of it, or -1, and the sum
-// of its weights.
-__device__ inline int choice_of(const LayerArgs &a, const int32_t *ids, int t, int e, float &w) {
+// Token t's first choice of expert e, or -1.
+__device__ inline int choice_of(const Live &live, int t, int k, int e) {
     int first = -1;
-    w = 0.0f;
-    const int k = int(a.p.top_k);
-    for (int j = 0; j < k; ++j)
-        if (ids[t * k + j] == e) {
-            w += a.p.weights[t * k + j];
-            first = first < 0 ? j : first;
-        }
+    for (int j = k - 1; j >= 0; --j)
+        if (live.ids[t * k + j] == e) first = j;
     return first;
 }
 
-// F: fragments of 16 tokens.
+// F: fragments of 16 tokens at most.  A wave has 16 rows of both halves and
+// 1 / slices of D; waves of one block of rows meet in LDS.
 template <class T, int TYPE, int F>
 __global__ __launch_bounds__(WAVES * 64) void up_kernel(LayerArgs a) {
     const ExpertsLayer &p = a.p;
-    __shared__ uint32_t bits[LAYER_MAX_EXPERTS / 32];
-    __shared__ uint16_t list[LAYER_MAX_EXPERTS];
+    __shared__ Live live;
     __shared__ int16_t token[LAYER_MAX_TOKENS], choice[LAYER_MAX_TOKENS];
     __shared__ int count_shared;
     __shared__ f32x4 part[WAVES][2][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int live = find_live(a, bits, list);
-    const int64_t which = blockIdx.x / ((p.H + 15) / 16), h0 = blockIdx.x % ((p.H + 15) / 16) * 16;
-    if (which >= live) return;
-    const int e = list[which];
+    const int slices = a.slices, per = WAVES / slices;  // blocks of 16 rows in a workgroup
+    const int groups = int((p.H + 16 * per - 1) / (16 * per));
+    const int n_live = find_live(a, live);
+    const int which = blockIdx.x / groups;
+    if (which >= n_live) return;
+    const int e = live.list[which], k = int(p.top_k);
+    const int64_t h0 = (int64_t(blockIdx.x % groups) * per + wave / slices) * 16;
+    const int slice = wave % slices;
     // the tokens that chose it, in rising order
     if (wave == 0) {
-        float w;
-        const int c = lane < p.tokens ? choice_of(a, p.ids, lane, e, w) : -1;
+        const int c = lane < p.tokens ? choice_of(live, lane, k, e) : -1;
         const uint64_t mask = __ballot(c >= 0);
         if (c >= 0) {
             const int at = __popcll(mask & ((uint64_t(1) << lane) - 1));
@@ -173,212 +181,266 @@ __global__ __launch_bounds__(WAVES * 64) void up_kernel(LayerArgs a) {
     const int ESZ = TYPE == 0 ? 2 : 1;
     const char *gate = static_cast<const char *>(p.up.w) + (e * p.up.stride + (h0 + r) * p.up.ld) * ESZ;
     const char *mult = gate + p.H * p.up.ld * ESZ;
-    for (int t0 = 0; t0 < count; t0 += 16 * F) {
-        const char *x[F];
-        bool has_x[F];
+    const char *x[F];
+    bool has_x[F];
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-            const int i = t0 + 16 * f + r;
-            has_x[f] = i < count;
-            x[f] = static_cast<const char *>(p.X) + (has_x[f] ? token[i] * p.ldx * 2 : 0);
-        }
-        f32x4 g[F], m[F];
-#pragma unroll
-        for (int f = 0; f < F; ++f) g[f] = f32x4{0, 0, 0, 0}, m[f] = f32x4{0, 0, 0, 0};
-        Run<TYPE> ng, nm;
-        ng.fetch(gate, has_h, wave * RUN, p.D, q);
-        nm.fetch(mult, has_h, wave * RUN, p.D, q);
-        for (int64_t k0 = wave * RUN; k0 < p.D; k0 += WAVES * RUN) {
-            const Run<TYPE> cg = ng, cm = nm;
-            ng.fetch(gate, has_h, k0 + WAVES * RUN, p.D, q);
-            nm.fetch(mult, has_h, k0 + WAVES * RUN, p.D, q);
-            f32x4 bg[F], bm[F];
-            if (TYPE != 0)
-#pragma unroll
-                for (int f = 0; f < F; ++f) bg[f] = f32x4{0, 0, 0, 0}, bm[f] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int64_t k = Run<TYPE>::at(s, k0, q);
-                const u32x4 og = cg.template operand<T>(s, k0, p.D, q), om = cm.template operand<T>(s, k0, p.D, q);
-#pragma unroll
-                for (int f = 0; f < F; ++f) {
-                    u32x4 xv = {0, 0, 0, 0};
-                    if (has_x[f] && k < p.D) xv = *reinterpret_cast<const u32x4 *>(x[f] + k * 2);
-                    Run<TYPE>::cut(xv, k, p.D);
-                    if (TYPE == 0) {
-                        g[f] = mfma16<T>(og, xv, g[f]);
-                        m[f] = mfma16<T>(om, xv, m[f]);
-                    } else {
-                        bg[f] = mfma16<T>(og, xv, bg[f]);
-                        bm[f] = mfma16<T>(om, xv, bm[f]);
-                    }
-                }
-            }
-            if (TYPE != 0) {
-                // the 16 rows lie in one or, where H is not a multiple of 16,
-                // the multiplied half's in two blocks of 128 rows: by row
-                const float *sc = p.up.scale + e * p.up.stride_scale + (k0 / 128) * p.up.lds;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t hr = h0 + 4 * q + i < p.H ? h0 + 4 * q + i : h0;
-                    const float sg = sc[hr / 128], sm = sc[(p.H + hr) / 128];
-#pragma unroll
-                    for (int f = 0; f < F; ++f) {
-                        g[f][i] = __builtin_fmaf(sg, bg[f][i], g[f][i]);
-                        m[f][i] = __builtin_fmaf(sm, bm[f][i], m[f][i]);
-                    }
-                }
-            }
-        }
-        // a lane's registers: rows h0 + 4q + 0..3 of token r
-#pragma unroll
-        for (int f = 0; f < F; ++f) {
-            __syncthreads();
-            part[wave][0][lane] = g[f];
-            part[wave][1][lane] = m[f];
-            __syncthreads();
-            if (wave == 0) {
-                f32x4 sg = {0, 0, 0, 0}, sm = {0, 0, 0, 0};
-#pragma unroll
-                for (int w = 0; w < WAVES; ++w) {
-                    const f32x4 og = part[w][0][lane], om = part[w][1][lane];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sg[i] += og[i], sm[i] += om[i];
-                }
-                const int i = t0 + 16 * f + r;
-                if (i < count) {
-                    float *h = a.h + (token[i] * p.top_k + choice[i]) * p.H + h0 + 4 * q;
-                    float v[4] = {sg[0], sg[1], sg[2], sg[3]};
-                    act::apply(p.act, v);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (h0 + 4 * q + j < p.H) h[j] = v[j] * sm[j];
-                }
-            }
-        }
+    for (int f = 0; f < F; ++f) {
+        has_x[f] = 16 * f + r < count;
+        x[f] = static_cast<const char *>(p.X) + (has_x[f] ? token[16 * f + r] * p.ldx * 2 : 0);
     }
-}
-
-// F: fragments of 16 tokens, F * 16 >= tokens.
-template <class T, int TYPE, int F>
-__global__ __launch_bounds__(WAVES * 64) void down_kernel(LayerArgs a) {
-    const ExpertsLayer &p = a.p;
-    __shared__ uint32_t bits[LAYER_MAX_EXPERTS / 32];
-    __shared__ uint16_t list[LAYER_MAX_EXPERTS];
-    __shared__ f32x4 part[WAVES][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int live = find_live(a, bits, list);
-    const int r = lane & 15, q = lane >> 4;
-    const int64_t d0 = int64_t(blockIdx.x) * 16;
-    const bool has_d = d0 + r < p.D;
-    const int ESZ = TYPE == 0 ? 2 : 1;
-    const char *down = static_cast<const char *>(p.down.w) + (d0 + r) * p.down.ld * ESZ;
-    const int runs = int((p.H + RUN - 1) / RUN), units = live * runs;
-    f32x4 acc[F];
+    f32x4 g[F], m[F];
 #pragma unroll
-    for (int f = 0; f < F; ++f) acc[f] = f32x4{0, 0, 0, 0};
-    Run<TYPE> next;
-    auto fetch = [&](int u) {
-        if (u < units) next.fetch(down + list[u / runs] * p.down.stride * ESZ, has_d, int64_t(u % runs) * RUN, p.H, q);
-    };
-    fetch(wave);
-    for (int u = wave; u < units; u += WAVES) {
-        const Run<TYPE> cur = next;
-        fetch(u + WAVES);
-        const int e = list[u / runs];
-        const int64_t k0 = int64_t(u % runs) * RUN;
-        float w;
-        const int c = lane < p.tokens ? choice_of(a, p.ids, lane, e, w) : -1;
-        const uint64_t mask = __ballot(c >= 0);
-        f32x4 block[F];
+    for (int f = 0; f < F; ++f) g[f] = f32x4{0, 0, 0, 0}, m[f] = f32x4{0, 0, 0, 0};
+    // the next run's weights and activations are on their way while this one
+    // is multiplied
+    Run<TYPE> ng, nm;
+    u32x4 nx[F][STEPS];
+    auto fetch = [&](int64_t k0) {
+        ng.fetch(gate, has_h, k0, p.D, q);
+        nm.fetch(mult, has_h, k0, p.D, q);
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-            block[f] = f32x4{0, 0, 0, 0};
-            if ((mask >> (16 * f) & 0xffffu) == 0) continue;  // the same for the whole wave
-            const int ct = __shfl(c, 16 * f + r);
-            const float wt = __shfl(w, 16 * f + r);
-            const float *h = a.h + ((16 * f + r) * p.top_k + ct) * p.H;
+        for (int f = 0; f < F; ++f)
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                const int64_t k = Run<TYPE>::at(s, k0, q);
-                float x[8];
+                const int64_t at = Run<TYPE>::at(s, k0, q);
+                const u32x4 zero = {0, 0, 0, 0};
+                nx[f][s] = has_x[f] && at < p.D ? *reinterpret_cast<const u32x4 *>(x[f] + at * 2) : zero;
+            }
+    };
+    fetch(slice * RUN);
+    for (int64_t k0 = slice * RUN; k0 < p.D; k0 += slices * RUN) {
+        const Run<TYPE> cg = ng, cm = nm;
+        u32x4 cx[F][STEPS];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-                if (ct >= 0 && k < p.H) load8f(h + k, p.H - k < 8 ? int(p.H - k) : 8, x);
-                float lo[8];
-                u32x4 hi;
+        for (int f = 0; f < F; ++f)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] *= wt;
-                    lo[i] = x[i] - decode<T>(encode<T>(x[i]));
-                }
-                hi = pack8<T>(x);
-                const u32x4 od = cur.template operand<T>(s, k0, p.H, q);
-                block[f] = mfma16<T>(od, pack8<T>(lo), block[f]);
-                block[f] = mfma16<T>(od, hi, block[f]);
+            for (int s = 0; s < STEPS; ++s) cx[f][s] = nx[f][s];
+        // the 16 rows of the activated half lie in one block of 128, the
+        // others' too unless H leaves a remainder of 16
+        float sg[4], sm[4];
+        if (TYPE != 0) {
+            const float *sc = p.up.scale + e * p.up.stride_scale + (k0 / 128) * p.up.lds;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t hr = h0 + 4 * q + i < p.H ? h0 + 4 * q + i : p.H - 1;
+                sg[i] = sc[hr / 128];
+                sm[i] = sc[(p.H + hr) / 128];
             }
         }
-        float sc[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-        if (TYPE != 0) {
-            // d0 is a multiple of 16: the workgroup's rows lie in one block
-            const float v = p.down.scale[e * p.down.stride_scale + (k0 / 128) * p.down.lds + d0 / 128];
-            sc[0] = sc[1] = sc[2] = sc[3] = v;
+        fetch(k0 + slices * RUN);
+        f32x4 bg[F], bm[F];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            bg[f] = TYPE == 0 ? g[f] : f32x4{0, 0, 0, 0};
+            bm[f] = TYPE == 0 ? m[f] : f32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const u32x4 og = cg.template operand<T>(s, k0, p.D, q), om = cm.template operand<T>(s, k0, p.D, q);
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                if (f > 0 && 16 * f >= count) continue;
+                u32x4 xv = cx[f][s];
+                Run<TYPE>::cut(xv, Run<TYPE>::at(s, k0, q), p.D);
+                bg[f] = mfma16<T>(og, xv, bg[f]);
+                bm[f] = mfma16<T>(om, xv, bm[f]);
+            }
         }
 #pragma unroll
         for (int f = 0; f < F; ++f)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[f][i] = TYPE == 0 ? acc[f][i] + block[f][i] : __builtin_fmaf(sc[i], block[f][i], acc[f][i]);
+            for (int i = 0; i < 4; ++i) {
+                g[f][i] = TYPE == 0 ? bg[f][i] : __builtin_fmaf(sg[i], bg[f][i], g[f][i]);
+                m[f][i] = TYPE == 0 ? bm[f][i] : __builtin_fmaf(sm[i], bm[f][i], m[f][i]);
+            }
     }
+    // a lane's registers: rows h0 + 4q + 0..3 of token r
 #pragma unroll
     for (int f = 0; f < F; ++f) {
-        __syncthreads();
-        part[wave][lane] = acc[f];
-        __syncthreads();
-        const int64_t t = 16 * f + r;
-        if (wave != 0 || t >= p.tokens) continue;
-        f32x4 s = {0, 0, 0, 0};
+        if (16 * f >= count) break;
+        if (slices > 1) {
+            if (f > 0) __syncthreads();
+            part[wave][0][lane] = g[f];
+            part[wave][1][lane] = m[f];
+            __syncthreads();
+            if (slice == 0)
+                for (int w = 1; w < slices; ++w) {
+                    const f32x4 og = part[wave + w][0][lane], om = part[wave + w][1][lane];
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            const f32x4 o = part[w][lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] += o[i];
+                    for (int i = 0; i < 4; ++i) g[f][i] += og[i], m[f][i] += om[i];
+                }
         }
+        const int at = 16 * f + r;
+        if (slice != 0 || at >= count || h0 + 4 * q >= a.ldh) continue;
+        const int t = token[at];
+        float w = 0.0f;
+        for (int j = choice[at]; j < k; ++j)
+            if (live.ids[t * k + j] == e) w += p.weights[t * k + j];
+        float v[4] = {g[f][0], g[f][1], g[f][2], g[f][3]};
+        act::apply(p.act, v);
+        uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t d = d0 + 4 * q + i, at = t * p.ldy + d;
-            if (d >= p.D) continue;
-            if (p.out == 0) {
-                float *y = static_cast<float *>(p.Y) + at;
-                *y = p.beta != 0.0f ? __builtin_fmaf(p.beta, *y, s[i]) : s[i];
-            } else {
-                uint16_t *y = static_cast<uint16_t *>(p.Y) + at;
-                *y = uint16_t(encode<T>(p.beta != 0.0f ? __builtin_fmaf(p.beta, decode<T>(*y), s[i]) : s[i]));
+            v[i] = h0 + 4 * q + i < p.H ? v[i] * m[f][i] * w : 0.0f;
+            hi[i] = encode<T>(v[i]);
+            lo[i] = encode<T>(v[i] - decode<T>(hi[i]));
+        }
+        uint16_t *h = a.h + (t * k + choice[at]) * 2 * a.ldh + h0 + 4 * q;
+        *reinterpret_cast<u32x2 *>(h) = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
+        *reinterpret_cast<u32x2 *>(h + a.ldh) = u32x2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
+    }
+}
+
+// A workgroup has 16 of y's columns; its waves deal (live expert, run of H)
+// pairs.  A pair's tokens are those of the expert, 16 to a fragment; their
+// sums are added to the tokens' in the wave's own part of LDS.
+template <class T, int TYPE>
+__global__ __launch_bounds__(WAVES * 64) void down_kernel(LayerArgs a) {
+    const ExpertsLayer &p = a.p;
+    __shared__ Live live;
+    __shared__ uint8_t token[MOST_SLOTS], choice[MOST_SLOTS];  // by live expert
+    __shared__ int16_t start[LAYER_MAX_EXPERTS + 1];
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    f32x4 *sums = reinterpret_cast<f32x4 *>(smem);  // [wave][token][four columns]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int k = int(p.top_k), tokens = int(p.tokens);
+    const int n_live = find_live(a, live);
+    const int r = lane & 15, q = lane >> 4;
+    // the first choices of each live expert, by rising token
+    for (int i = wave; i < n_live; i += WAVES) {
+        const uint64_t mask = __ballot(lane < tokens && choice_of(live, lane, k, live.list[i]) >= 0);
+        if (lane == 0) start[i + 1] = int16_t(__popcll(mask));
+    }
+    for (int i = threadIdx.x; i < WAVES * tokens * 4; i += WAVES * 64) sums[i] = f32x4{0, 0, 0, 0};
+    __syncthreads();
+    if (wave == 0) {
+        int base = 0;
+        for (int i0 = 0; i0 < n_live; i0 += 64) {
+            int v = i0 + lane < n_live ? start[i0 + lane + 1] : 0;
+            for (int d = 1; d < 64; d *= 2) {
+                const int o = __shfl_up(v, d);
+                if (lane >= d) v += o;
             }
+            if (i0 + lane < n_live) start[i0 + lane + 1] = int16_t(base + v);
+            base += __shfl(v, 63);
+        }
+        if (lane == 0) start[0] = 0;
+    }
+    __syncthreads();
+    for (int i = wave; i < n_live; i += WAVES) {
+        const int c = lane < tokens ? choice_of(live, lane, k, live.list[i]) : -1;
+        const uint64_t mask = __ballot(c >= 0);
+        if (c >= 0) {
+            const int at = start[i] + __popcll(mask & ((uint64_t(1) << lane) - 1));
+            token[at] = uint8_t(lane);
+            choice[at] = uint8_t(c);
+        }
+    }
+    __syncthreads();
+    const int64_t d0 = int64_t(blockIdx.x) * 16;
+    const bool has_d = d0 + r < p.D;
+    const int ESZ = TYPE == 0 ? 2 : 1;
+    const char *down = static_cast<const char *>(p.down.w) + (d0 + r) * p.down.ld * ESZ;
+    const int runs = int((p.H + RUN - 1) / RUN), units = n_live * runs;
+    constexpr int AHEAD = 2;
+    Run<TYPE> next[AHEAD];
+    float next_scale[AHEAD];
+    auto fetch = [&](int i, int u) {
+        if (u >= units) return;
+        const int e = live.list[u / runs];
+        const int64_t k0 = int64_t(u % runs) * RUN;
+        next[i].fetch(down + e * p.down.stride * ESZ, has_d, k0, p.H, q);
+        // 16 rows from a multiple of 16 lie in one block of 128
+        if (TYPE != 0) next_scale[i] = p.down.scale[e * p.down.stride_scale + (k0 / 128) * p.down.lds + d0 / 128];
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(i, wave + i * WAVES);
+    for (int u0 = wave; u0 < units; u0 += AHEAD * WAVES)
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int u = u0 + i * WAVES;
+            if (u >= units) break;
+            const Run<TYPE> cur = next[i];
+            const float scale = TYPE == 0 ? 1.0f : next_scale[i];
+            const int64_t k0 = int64_t(u % runs) * RUN;
+            const int first = start[u / runs], end = start[u / runs + 1];
+            for (int s0 = first; s0 < end; s0 += 16) {
+                const bool has = s0 + r < end;
+                const int t = has ? token[s0 + r] : 0;
+                const uint16_t *h = a.h + (has ? (t * k + choice[s0 + r]) * 2 * a.ldh : 0);
+                u32x4 hi[STEPS], lo[STEPS];
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    const int64_t at = Run<TYPE>::at(s, k0, q);
+                    const u32x4 zero = {0, 0, 0, 0};
+                    hi[s] = has && at < p.H ? *reinterpret_cast<const u32x4 *>(h + at) : zero;
+                    lo[s] = has && at < p.H ? *reinterpret_cast<const u32x4 *>(h + a.ldh + at) : zero;
+                }
+                if (s0 == first) fetch(i, u + AHEAD * WAVES);
+                f32x4 block = {0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    const u32x4 od = cur.template operand<T>(s, k0, p.H, q);
+                    block = mfma16<T>(od, lo[s], block);
+                    block = mfma16<T>(od, hi[s], block);
+                }
+                if (has) {
+                    f32x4 *sum = sums + (wave * tokens + t) * 4 + q;
+                    f32x4 v = *sum;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(scale, block[j], v[j]);
+                    *sum = v;
+                }
+            }
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < tokens * 16; i += WAVES * 64) {
+        const int t = i / 16;
+        const int64_t d = d0 + i % 16, at = t * p.ldy + d;
+        if (d >= p.D) continue;
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) s += reinterpret_cast<const float *>(sums)[w * tokens * 16 + i];
+        if (p.out == 0) {
+            float *y = static_cast<float *>(p.Y) + at;
+            *y = p.beta != 0.0f ? __builtin_fmaf(p.beta, *y, s) : s;
+        } else {
+            uint16_t *y = static_cast<uint16_t *>(p.Y) + at;
+            *y = uint16_t(encode<T>(p.beta != 0.0f ? __builtin_fmaf(p.beta, decode<T>(*y), s) : s));
         }
     }
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Waves that share 16 rows: as many (1, 2, 4, 8) as it takes for 16 waves on
+// each of 256 compute units when every slot has an expert of its own.
+int up_slices(int64_t live, int64_t H) {
+    const int64_t blocks = live * ceil_div(H, 16);
+    int s = 1;
+    while (s < WAVES && blocks * s < 4096) s *= 2;
+    return s;
+}
+
 template <class T, int TYPE, int F>
-hipError_t run(const LayerArgs &a, hipStream_t stream) {
-    const int64_t up = a.live_most * ceil_div(a.p.H, 16);
+hipError_t run(LayerArgs &a, hipStream_t stream) {
+    a.slices = up_slices(a.live_most, a.p.H);
+    const int64_t up = a.live_most * ceil_div(a.p.H, 16 * (WAVES / a.slices));
     if (up > 0x7fffff || ceil_div(a.p.D, 16) > 0x7fffff) return hipErrorInvalidConfiguration;
     up_kernel<T, TYPE, F><<<dim3(unsigned(up)), dim3(WAVES * 64), 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    down_kernel<T, TYPE, F><<<dim3(unsigned(ceil_div(a.p.D, 16))), dim3(WAVES * 64), 0, stream>>>(a);
+    down_kernel<T, TYPE><<<dim3(unsigned(ceil_div(a.p.D, 16))), dim3(WAVES * 64), size_t(WAVES * a.p.tokens * 64), stream>>>(a);
     return hipGetLastError();
 }
 template <class T, int TYPE>
-hipError_t run_tokens(const LayerArgs &a, hipStream_t stream) {
+hipError_t run_tokens(LayerArgs &a, hipStream_t stream) {
     if (a.p.tokens <= 16) return run<T, TYPE, 1>(a, stream);
     if (a.p.tokens <= 32) return run<T, TYPE, 2>(a, stream);
     return run<T, TYPE, 4>(a, stream);
 }
 template <class T>
-hipError_t run_type(const LayerArgs &a, hipStream_t stream) {
+hipError_t run_type(LayerArgs &a, hipStream_t stream) {
     if (a.p.type == 0) return run_tokens<T, 0>(a, stream);
     return a.p.type == 1 ? run_tokens<T, 1>(a, stream) : run_tokens<T, 2>(a, stream);
 }
@@ -386,11 +448,12 @@ hipError_t run_type(const LayerArgs &a, hipStream_t stream) {
 }  // namespace
 
 size_t experts_layer_workspace(int64_t tokens, int64_t, int64_t top_k, int64_t, int64_t H) {
-    return size_t(tokens * top_k * H * 4 + 16);
+    return size_t(tokens * top_k * 2 * ceil_div(H, 8) * 8 * 2 + 16);
 }
 
 hipError_t launch_experts_layer(const ExpertsLayer &p, hipStream_t stream) {
-    LayerArgs a{p, static_cast<float *>(p.workspace), int(p.experts < p.tokens * p.top_k ? p.experts : p.tokens * p.top_k)};
+    LayerArgs a{p, static_cast<uint16_t *>(p.workspace), ceil_div(p.H, 8) * 8,
+                int(p.experts < p.tokens * p.top_k ? p.experts : p.tokens * p.top_k), 1};
     return p.in == 1 ? run_type<BF16>(a, stream) : run_type<F16>(a, stream);
 }
 

@@ -107,7 +107,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void
     const TileCoord t = tile_of(p.grid, blockIdx.x);
     const int64_t m0 = uniform(t.tm) * Shape::TM, n0 = uniform(t.tn) * Shape::TN;
     typename Shape::Acc acc;
-    const int buf = Shape::run(p.a, p.b, p.K, m0, n0, 0, (p.K + BK - 1) / BK, lds, acc);
+    const int buf = Shape::run(p.a, p.b, p.K, m0, n0, 0, (p.K + Shape::BK - 1) / Shape::BK, lds, acc);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t mw = m0 + Shape::wave_m(wave) * Shape::WTM, nw = n0 + Shape::wave_n(wave) * Shape::WTN;
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(Shape::THREADS, 2) void split_kernel(LinearArgs p) 
     LDS char *lds = (LDS char *)smem;
     const TileCoord t = tile_of(p.grid, blockIdx.x);
     const int64_t m0 = uniform(t.tm) * Shape::TM, n0 = uniform(t.tn) * Shape::TN, z = uniform(t.batch);
-    const int64_t stages = (p.K + BK - 1) / BK;
+    const int64_t stages = (p.K + Shape::BK - 1) / Shape::BK;
     typename Shape::Acc acc;
     const int buf = Shape::run(p.a, p.b, p.K, m0, n0, stages * z / p.slices, stages * (z + 1) / p.slices, lds, acc);
     const int lane = threadIdx.x & 63;
@@ -329,7 +329,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Slices of K for `tiles` tiles of 128 x 128: two workgroups for each of 256
 // compute units, four stages each at least.
 int split_slices(int64_t tiles, int64_t K) {
-    const int64_t most = ceil_div(K, BK) / 4;
+    const int64_t most = ceil_div(K, 64) / 4;
     const int64_t want = 512 / tiles;
     const int64_t s = want < most ? want : most;
     return int(s < 1 ? 1 : s);

@@ -207,7 +207,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void
     const int64_t depth = STEP == Step::Update ? p.m : K;
     const int buf = Shape::run(STEP == Step::Gram ? xr : STEP == Step::Poly ? ar : br,
                                STEP == Step::Gram ? xr : STEP == Step::Poly ? ar : xc, depth, m0, n0, 0,
-                               (depth + BK - 1) / BK, lds, acc);
+                               (depth + Shape::BK - 1) / Shape::BK, lds, acc);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t mw = m0 + Shape::wave_m(wave) * Shape::WTM, nw = n0 + Shape::wave_n(wave) * Shape::WTN;

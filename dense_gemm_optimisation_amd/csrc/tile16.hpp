@@ -127,7 +127,6 @@ __device__ inline void store8_as(void *p, int64_t at, bool same, int n, const fl
     else store8f(static_cast<float *>(p) + at, n, x);
 }
 
-constexpr int BK = 64;
 // Leading dimensions (elements) whose tiles' offsets stay below 2^31 bytes:
 // 256 rows of a K-contiguous panel, 64 of the other.
 constexpr int64_t MOST_LD = int64_t(1) << 21;
@@ -139,8 +138,9 @@ struct Operand16 {
     int64_t ld, R;
 };
 
-template <bool KMAJOR, int ROWS, int WAVES>
+template <bool KMAJOR, int ROWS, int WAVES, int BK>
 struct Panel {
+    static constexpr int CHK = BK / 8;  // chunks per row, K-contiguous
     static constexpr int BYTES = ROWS * BK * 2;
     static constexpr int PER_WAVE = BYTES / 1024 / WAVES;  // 1 KiB pieces per wave per stage
     static constexpr int CHR = ROWS / 8;                   // chunks per k row, row-contiguous
@@ -166,8 +166,8 @@ struct Panel {
         for (int i = 0; i < PER_WAVE; ++i) {
             const int blk = wave * PER_WAVE + i;
             if (KMAJOR) {
-                const int row = blk * 8 + (lane >> 3);
-                const int c = (lane & 7) ^ swz_k<8>(row);
+                const int row = blk * (64 / CHK) + lane / CHK;
+                const int c = (lane % CHK) ^ swz_k<CHK>(row);
                 kl[i] = c * 8;
                 rl[i] = row;
                 voff[i] = row < left ? uint32_t((row * ld + c * 8) * 2) : OOB;
@@ -221,7 +221,7 @@ struct Panel {
         if (KMAJOR) {
             const int row = row0 + (lane & 31);
             const int c = kk * 2 + (lane >> 5);
-            return *reinterpret_cast<const LDS u32x4 *>(panel + row * (2 * BK) + ((c ^ swz_k<8>(row)) << 4));
+            return *reinterpret_cast<const LDS u32x4 *>(panel + row * (2 * BK) + ((c ^ swz_k<CHK>(row)) << 4));
         }
         const int g = lane >> 5, h = (lane >> 4) & 1, ii = lane & 15;
         const int col = row0 + h * 16 + 4 * (ii & 3);
@@ -241,17 +241,18 @@ struct Panel {
     }
 };
 
-template <class T, int BM_, int BN_, int WAVES_M, int WAVES_N, bool A_KMAJOR, bool B_KMAJOR, bool DIRECT>
+template <class T, int BM_, int BN_, int WAVES_M, int WAVES_N, bool A_KMAJOR, bool B_KMAJOR, bool DIRECT, int BK_ = 64, int STAGES = 2>
 struct Tile {
-    static constexpr int TM = BM_, TN = BN_;
+    static constexpr int TM = BM_, TN = BN_, BK = BK_;
     static constexpr int WAVES = WAVES_M * WAVES_N, THREADS = WAVES * 64;
     static constexpr int WTM = TM / WAVES_M, WTN = TN / WAVES_N;
     static constexpr int FM = WTM / 32, FN = WTN / 32;
-    using PA = Panel<A_KMAJOR, TM, WAVES>;
-    using PB = Panel<B_KMAJOR, TN, WAVES>;
+    using PA = Panel<A_KMAJOR, TM, WAVES, BK>;
+    using PB = Panel<B_KMAJOR, TN, WAVES, BK>;
     static constexpr int STAGE = PA::BYTES + PB::BYTES;
-    static constexpr int LDS_BYTES = 2 * STAGE;
-    static_assert(LDS_BYTES <= 160 * 1024 && WAVES * 32 * WTN * 4 <= STAGE, "LDS budget");
+    static constexpr int LDS_BYTES = STAGES * STAGE;
+    static constexpr int NEED = (WAVES * 32 * WTN * 4 + STAGE - 1) / STAGE;  // stages the epilogue uses
+    static_assert(LDS_BYTES <= 160 * 1024 && (NEED == 1 || 2 * NEED <= STAGES), "LDS budget");
     typedef f32x16 Acc[FM][FN];
 
     // Waves are dealt to the four SIMDs in turn: consecutive waves share a
@@ -259,9 +260,10 @@ struct Tile {
     // over all of them.
     static __device__ int wave_m(int wave) { return wave % WAVES_M; }
     static __device__ int wave_n(int wave) { return wave / WAVES_M; }
-    // The LDS a wave stages its rows of C in: the stage the last one does not use.
+    // The LDS a wave stages its rows of C in: stages that the last one does not use.
     static __device__ LDS float *staging(LDS char *lds, int buf, int wave) {
-        return reinterpret_cast<LDS float *>(lds + (buf ^ 1) * STAGE) + wave * 32 * WTN;
+        const int first = NEED == 1 ? (buf + 1 == STAGES ? 0 : buf + 1) : (buf >= NEED ? 0 : NEED);
+        return reinterpret_cast<LDS float *>(lds + first * STAGE) + wave * 32 * WTN;
     }
 
     static __device__ void read(u32x4 (&fa)[FM], u32x4 (&fb)[FN], const LDS char *stage, int wm, int wn,
@@ -314,13 +316,13 @@ struct Tile {
         constexpr int NREAD = FM * (A_KMAJOR ? 1 : 2) + FN * (B_KMAJOR ? 1 : 2);
         const int64_t steps = s1 - s0;
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
+        for (int st = 0; st < STAGES; ++st) {
             if (st < steps) {
                 pa.issue(lds + st * STAGE, s0 + st, K, wave);
                 pb.issue(lds + st * STAGE + PA::BYTES, s0 + st, K, wave);
             }
         }
-        wait_stages<PER_STAGE, 2>(steps > 1 ? 1 : 0);
+        wait_stages<PER_STAGE, STAGES>(int(steps - 1 < STAGES - 1 ? steps - 1 : STAGES - 1));
         __syncthreads();
         u32x4 fa[2][FM], fb[2][FN];
         read(fa[0], fb[0], lds, wm, wn, 0, lane);
@@ -338,11 +340,13 @@ struct Tile {
                 interleave_reads<NREAD, FM * FN>();
             }
             constexpr int LAST = (KK - 1) & 1;
-            wait_vmcnt<0>();
+            const int64_t later = steps - 2 - s;
+            wait_stages<PER_STAGE, STAGES>(int(later < STAGES - 2 ? later : STAGES - 2));
             wait_lgkmcnt0();
             __syncthreads();
-            read(fa[LAST ^ 1], fb[LAST ^ 1], lds + (buf ^ 1) * STAGE, wm, wn, 0, lane);
-            const int64_t refill = s0 + s + 2;
+            const int next = buf + 1 == STAGES ? 0 : buf + 1;
+            read(fa[LAST ^ 1], fb[LAST ^ 1], lds + next * STAGE, wm, wn, 0, lane);
+            const int64_t refill = s0 + s + STAGES;
             const bool more = refill < s1;
             const u32x4 ra = pa.rsrc(refill), rb = pb.rsrc(refill);
             const uint32_t la = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(stage));
@@ -362,7 +366,7 @@ struct Tile {
                         }
                     }
                 }
-            buf ^= 1;
+            buf = next;
         }
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
