@@ -145,10 +145,19 @@ __device__ inline int choice_of(const Live &live, int t, int k, int e) {
     return first;
 }
 
-// F: fragments of 16 tokens at most.  A wave has 16 rows of both halves and
+// A float at an address that is the same in the whole wave, by a scalar load:
+// loads into vector registers return in order, so a scale fetched that way
+// would wait for the weights on their way before it.
+__device__ inline float scalar_load(const float *p) {
+    typedef const float __attribute__((address_space(4))) *constant;
+    return *reinterpret_cast<constant>(static_cast<uint64_t>(uniform(reinterpret_cast<int64_t>(p))));
+}
+
+// F: fragments of 16 tokens at a time; an expert with more reads its weights
+// again, from L2.  A wave has 16 rows of both halves and
 // 1 / slices of D; waves of one block of rows meet in LDS.
-template <class T, int TYPE, int F>
-__global__ __launch_bounds__(WAVES * 64) void up_kernel(LayerArgs a) {
+template <class T, int TYPE, int F, int AHEAD>
+__global__ __launch_bounds__(WAVES * 64, 1) void up_kernel(LayerArgs a) {
     const ExpertsLayer &p = a.p;
     __shared__ Live live;
     __shared__ int16_t token[LAYER_MAX_TOKENS], choice[LAYER_MAX_TOKENS];
@@ -181,121 +190,125 @@ __global__ __launch_bounds__(WAVES * 64) void up_kernel(LayerArgs a) {
     const int ESZ = TYPE == 0 ? 2 : 1;
     const char *gate = static_cast<const char *>(p.up.w) + (e * p.up.stride + (h0 + r) * p.up.ld) * ESZ;
     const char *mult = gate + p.H * p.up.ld * ESZ;
+    // Runs of weights and activations are on their way AHEAD runs before they
+    // are multiplied.
+    Run<TYPE> ng[AHEAD], nm[AHEAD];
+    u32x4 nx[AHEAD][F][STEPS];
+    // the 16 rows of the activated half lie in one block of 128, the others'
+    // (lo .. hi) in two where H is no multiple of 16
+    float sg[AHEAD], sm_lo[AHEAD], sm_hi[AHEAD];
+    const int64_t first = h0 < p.H ? h0 : p.H - 1, last = h0 + 15 < p.H ? h0 + 15 : p.H - 1;
+    const int64_t in_gate = uniform(first / 128), in_lo = uniform((p.H + first) / 128), in_hi = uniform((p.H + last) / 128);
+    const float *scale = p.up.scale + e * p.up.stride_scale;
     const char *x[F];
     bool has_x[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-        has_x[f] = 16 * f + r < count;
-        x[f] = static_cast<const char *>(p.X) + (has_x[f] ? token[16 * f + r] * p.ldx * 2 : 0);
-    }
-    f32x4 g[F], m[F];
-#pragma unroll
-    for (int f = 0; f < F; ++f) g[f] = f32x4{0, 0, 0, 0}, m[f] = f32x4{0, 0, 0, 0};
-    // the next run's weights and activations are on their way while this one
-    // is multiplied
-    Run<TYPE> ng, nm;
-    u32x4 nx[F][STEPS];
-    auto fetch = [&](int64_t k0) {
-        ng.fetch(gate, has_h, k0, p.D, q);
-        nm.fetch(mult, has_h, k0, p.D, q);
+    auto fetch = [&](int i, int64_t k0) {
+        if (TYPE != 0 && k0 < p.D) {
+            const float *sc = scale + k0 / 128 * p.up.lds;
+            sg[i] = scalar_load(sc + in_gate);
+            sm_lo[i] = scalar_load(sc + in_lo);
+            sm_hi[i] = scalar_load(sc + in_hi);
+        }
+        ng[i].fetch(gate, has_h, k0, p.D, q);
+        nm[i].fetch(mult, has_h, k0, p.D, q);
 #pragma unroll
         for (int f = 0; f < F; ++f)
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int64_t at = Run<TYPE>::at(s, k0, q);
                 const u32x4 zero = {0, 0, 0, 0};
-                nx[f][s] = has_x[f] && at < p.D ? *reinterpret_cast<const u32x4 *>(x[f] + at * 2) : zero;
+                nx[i][f][s] = has_x[f] && at < p.D ? *reinterpret_cast<const u32x4 *>(x[f] + at * 2) : zero;
             }
     };
-    fetch(slice * RUN);
-    for (int64_t k0 = slice * RUN; k0 < p.D; k0 += slices * RUN) {
-        const Run<TYPE> cg = ng, cm = nm;
-        u32x4 cx[F][STEPS];
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) cx[f][s] = nx[f][s];
-        // the 16 rows of the activated half lie in one block of 128, the
-        // others' too unless H leaves a remainder of 16
-        float sg[4], sm[4];
-        if (TYPE != 0) {
-            const float *sc = p.up.scale + e * p.up.stride_scale + (k0 / 128) * p.up.lds;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t hr = h0 + 4 * q + i < p.H ? h0 + 4 * q + i : p.H - 1;
-                sg[i] = sc[hr / 128];
-                sm[i] = sc[(p.H + hr) / 128];
-            }
-        }
-        fetch(k0 + slices * RUN);
-        f32x4 bg[F], bm[F];
+    for (int t0 = 0; t0 < count; t0 += 16 * F) {
 #pragma unroll
         for (int f = 0; f < F; ++f) {
-            bg[f] = TYPE == 0 ? g[f] : f32x4{0, 0, 0, 0};
-            bm[f] = TYPE == 0 ? m[f] : f32x4{0, 0, 0, 0};
+            const int at = t0 + 16 * f + r;
+            has_x[f] = at < count;
+            x[f] = static_cast<const char *>(p.X) + (has_x[f] ? token[at] * p.ldx * 2 : 0);
         }
+        f32x4 g[F], m[F];
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const u32x4 og = cg.template operand<T>(s, k0, p.D, q), om = cm.template operand<T>(s, k0, p.D, q);
+        for (int f = 0; f < F; ++f) g[f] = f32x4{0, 0, 0, 0}, m[f] = f32x4{0, 0, 0, 0};
+        const int64_t stride = int64_t(slices) * RUN;
 #pragma unroll
-            for (int f = 0; f < F; ++f) {
-                if (f > 0 && 16 * f >= count) continue;
-                u32x4 xv = cx[f][s];
-                Run<TYPE>::cut(xv, Run<TYPE>::at(s, k0, q), p.D);
-                bg[f] = mfma16<T>(og, xv, bg[f]);
-                bm[f] = mfma16<T>(om, xv, bm[f]);
-            }
-        }
+        for (int i = 0; i < AHEAD; ++i) fetch(i, slice * RUN + i * stride);
+        for (int64_t k1 = slice * RUN; k1 < p.D; k1 += AHEAD * stride)
 #pragma unroll
-        for (int f = 0; f < F; ++f)
+            for (int i = 0; i < AHEAD; ++i) {
+                const int64_t k0 = k1 + i * stride;
+                if (k0 >= p.D) break;
+                const float gate_scale = sg[i], lo_scale = sm_lo[i], hi_scale = sm_hi[i];
+                f32x4 bg[F], bm[F];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                g[f][i] = TYPE == 0 ? bg[f][i] : __builtin_fmaf(sg[i], bg[f][i], g[f][i]);
-                m[f][i] = TYPE == 0 ? bm[f][i] : __builtin_fmaf(sm[i], bm[f][i], m[f][i]);
-            }
-    }
-    // a lane's registers: rows h0 + 4q + 0..3 of token r
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-        if (16 * f >= count) break;
-        if (slices > 1) {
-            if (f > 0) __syncthreads();
-            part[wave][0][lane] = g[f];
-            part[wave][1][lane] = m[f];
-            __syncthreads();
-            if (slice == 0)
-                for (int w = 1; w < slices; ++w) {
-                    const f32x4 og = part[wave + w][0][lane], om = part[wave + w][1][lane];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) g[f][i] += og[i], m[f][i] += om[i];
+                for (int f = 0; f < F; ++f) {
+                    bg[f] = TYPE == 0 ? g[f] : f32x4{0, 0, 0, 0};
+                    bm[f] = TYPE == 0 ? m[f] : f32x4{0, 0, 0, 0};
                 }
-        }
-        const int at = 16 * f + r;
-        if (slice != 0 || at >= count || h0 + 4 * q >= a.ldh) continue;
-        const int t = token[at];
-        float w = 0.0f;
-        for (int j = choice[at]; j < k; ++j)
-            if (live.ids[t * k + j] == e) w += p.weights[t * k + j];
-        float v[4] = {g[f][0], g[f][1], g[f][2], g[f][3]};
-        act::apply(p.act, v);
-        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = h0 + 4 * q + i < p.H ? v[i] * m[f][i] * w : 0.0f;
-            hi[i] = encode<T>(v[i]);
-            lo[i] = encode<T>(v[i] - decode<T>(hi[i]));
+                for (int s = 0; s < STEPS; ++s) {
+                    const u32x4 og = ng[i].template operand<T>(s, k0, p.D, q), om = nm[i].template operand<T>(s, k0, p.D, q);
+#pragma unroll
+                    for (int f = 0; f < F; ++f) {
+                        u32x4 xv = nx[i][f][s];
+                        Run<TYPE>::cut(xv, Run<TYPE>::at(s, k0, q), p.D);
+                        bg[f] = mfma16<T>(og, xv, bg[f]);
+                        bm[f] = mfma16<T>(om, xv, bm[f]);
+                    }
+                }
+                fetch(i, k0 + AHEAD * stride);
+#pragma unroll
+                for (int f = 0; f < F; ++f)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float mult_scale = (p.H + h0 + 4 * q + j) / 128 == in_lo ? lo_scale : hi_scale;
+                        g[f][j] = TYPE == 0 ? bg[f][j] : __builtin_fmaf(gate_scale, bg[f][j], g[f][j]);
+                        m[f][j] = TYPE == 0 ? bm[f][j] : __builtin_fmaf(mult_scale, bm[f][j], m[f][j]);
+                    }
+            }
+        // a lane's registers: rows h0 + 4q + 0..3 of token r
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+            if (t0 + 16 * f >= count) break;
+            if (slices > 1) {
+                if (t0 + f > 0) __syncthreads();
+                part[wave][0][lane] = g[f];
+                part[wave][1][lane] = m[f];
+                __syncthreads();
+                if (slice == 0)
+                    for (int w = 1; w < slices; ++w) {
+                        const f32x4 og = part[wave + w][0][lane], om = part[wave + w][1][lane];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) g[f][j] += og[j], m[f][j] += om[j];
+                    }
+            }
+            const int at = t0 + 16 * f + r;
+            if (slice != 0 || at >= count || h0 + 4 * q >= a.ldh) continue;
+            const int t = token[at];
+            float w = 0.0f;
+            for (int j = choice[at]; j < k; ++j)
+                if (live.ids[t * k + j] == e) w += p.weights[t * k + j];
+            float v[4] = {g[f][0], g[f][1], g[f][2], g[f][3]};
+            act::apply(p.act, v);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = h0 + 4 * q + j < p.H ? v[j] * m[f][j] * w : 0.0f;
+                hi[j] = encode<T>(v[j]);
+                lo[j] = encode<T>(v[j] - decode<T>(hi[j]));
+            }
+            uint16_t *h = a.h + (t * k + choice[at]) * 2 * a.ldh + h0 + 4 * q;
+            *reinterpret_cast<u32x2 *>(h) = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
+            *reinterpret_cast<u32x2 *>(h + a.ldh) = u32x2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
         }
-        uint16_t *h = a.h + (t * k + choice[at]) * 2 * a.ldh + h0 + 4 * q;
-        *reinterpret_cast<u32x2 *>(h) = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
-        *reinterpret_cast<u32x2 *>(h + a.ldh) = u32x2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
     }
 }
 
 // A workgroup has 16 of y's columns; its waves deal (live expert, run of H)
 // pairs.  A pair's tokens are those of the expert, 16 to a fragment; their
 // sums are added to the tokens' in the wave's own part of LDS.
-template <class T, int TYPE>
-__global__ __launch_bounds__(WAVES * 64) void down_kernel(LayerArgs a) {
+template <class T, int TYPE, int AHEAD>
+__global__ __launch_bounds__(WAVES * 64, 1) void down_kernel(LayerArgs a) {
     const ExpertsLayer &p = a.p;
     __shared__ Live live;
     __shared__ uint8_t token[MOST_SLOTS], choice[MOST_SLOTS];  // by live expert
@@ -342,7 +355,6 @@ __global__ __launch_bounds__(WAVES * 64) void down_kernel(LayerArgs a) {
     const int ESZ = TYPE == 0 ? 2 : 1;
     const char *down = static_cast<const char *>(p.down.w) + (d0 + r) * p.down.ld * ESZ;
     const int runs = int((p.H + RUN - 1) / RUN), units = n_live * runs;
-    constexpr int AHEAD = 2;
     Run<TYPE> next[AHEAD];
     float next_scale[AHEAD];
     auto fetch = [&](int i, int u) {
@@ -351,47 +363,59 @@ __global__ __launch_bounds__(WAVES * 64) void down_kernel(LayerArgs a) {
         const int64_t k0 = int64_t(u % runs) * RUN;
         next[i].fetch(down + e * p.down.stride * ESZ, has_d, k0, p.H, q);
         // 16 rows from a multiple of 16 lie in one block of 128
-        if (TYPE != 0) next_scale[i] = p.down.scale[e * p.down.stride_scale + (k0 / 128) * p.down.lds + d0 / 128];
+        if (TYPE != 0) next_scale[i] = scalar_load(p.down.scale + e * p.down.stride_scale + (k0 / 128) * p.down.lds + d0 / 128);
+    };
+    // the pieces of w h of a unit's first tokens, fetched with its weights:
+    // fetched later, they would wait for all weights asked for before
+    u32x4 hi[AHEAD][STEPS], lo[AHEAD][STEPS];
+    auto fetch_h = [&](u32x4 (&vh)[STEPS], u32x4 (&vl)[STEPS], int u, int at) {
+        // token `at` of the unit's expert
+        if (u >= units) return;
+        at += start[u / runs] + r;
+        const bool has = at < start[u / runs + 1];
+        const uint16_t *h = a.h + (has ? (token[at] * k + choice[at]) * 2 * a.ldh : 0);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int64_t from = Run<TYPE>::at(s, int64_t(u % runs) * RUN, q);
+            const u32x4 zero = {0, 0, 0, 0};
+            vh[s] = has && from < p.H ? *reinterpret_cast<const u32x4 *>(h + from) : zero;
+            vl[s] = has && from < p.H ? *reinterpret_cast<const u32x4 *>(h + a.ldh + from) : zero;
+        }
     };
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) fetch(i, wave + i * WAVES);
+    for (int i = 0; i < AHEAD; ++i) {
+        fetch(i, wave + i * WAVES);
+        fetch_h(hi[i], lo[i], wave + i * WAVES, 0);
+    }
     for (int u0 = wave; u0 < units; u0 += AHEAD * WAVES)
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int u = u0 + i * WAVES;
             if (u >= units) break;
-            const Run<TYPE> cur = next[i];
-            const float scale = TYPE == 0 ? 1.0f : next_scale[i];
             const int64_t k0 = int64_t(u % runs) * RUN;
             const int first = start[u / runs], end = start[u / runs + 1];
-            for (int s0 = first; s0 < end; s0 += 16) {
-                const bool has = s0 + r < end;
-                const int t = has ? token[s0 + r] : 0;
-                const uint16_t *h = a.h + (has ? (t * k + choice[s0 + r]) * 2 * a.ldh : 0);
-                u32x4 hi[STEPS], lo[STEPS];
+            const float scale = TYPE == 0 ? 1.0f : next_scale[i];
+            u32x4 od[STEPS];
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    const int64_t at = Run<TYPE>::at(s, k0, q);
-                    const u32x4 zero = {0, 0, 0, 0};
-                    hi[s] = has && at < p.H ? *reinterpret_cast<const u32x4 *>(h + at) : zero;
-                    lo[s] = has && at < p.H ? *reinterpret_cast<const u32x4 *>(h + a.ldh + at) : zero;
-                }
-                if (s0 == first) fetch(i, u + AHEAD * WAVES);
+            for (int s = 0; s < STEPS; ++s) od[s] = next[i].template operand<T>(s, k0, p.H, q);
+            for (int s0 = first; s0 < end; s0 += 16) {
+                if (s0 > first) fetch_h(hi[i], lo[i], u, s0 - first);
                 f32x4 block = {0, 0, 0, 0};
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s) {
-                    const u32x4 od = cur.template operand<T>(s, k0, p.H, q);
-                    block = mfma16<T>(od, lo[s], block);
-                    block = mfma16<T>(od, hi[s], block);
+                    block = mfma16<T>(od[s], lo[i][s], block);
+                    block = mfma16<T>(od[s], hi[i][s], block);
                 }
-                if (has) {
-                    f32x4 *sum = sums + (wave * tokens + t) * 4 + q;
+                if (s0 + r < end) {
+                    f32x4 *sum = sums + (wave * tokens + token[s0 + r]) * 4 + q;
                     f32x4 v = *sum;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(scale, block[j], v[j]);
                     *sum = v;
                 }
             }
+            fetch(i, u + AHEAD * WAVES);
+            fetch_h(hi[i], lo[i], u + AHEAD * WAVES, 0);
         }
     __syncthreads();
     for (int i = threadIdx.x; i < tokens * 16; i += WAVES * 64) {
@@ -422,22 +446,27 @@ int up_slices(int64_t live, int64_t H) {
     return s;
 }
 
+#ifndef UP_AHEAD
+#define UP_AHEAD 2
+#endif
+#ifndef DOWN_AHEAD
+#define DOWN_AHEAD 3
+#endif
 template <class T, int TYPE, int F>
 hipError_t run(LayerArgs &a, hipStream_t stream) {
     a.slices = up_slices(a.live_most, a.p.H);
     const int64_t up = a.live_most * ceil_div(a.p.H, 16 * (WAVES / a.slices));
     if (up > 0x7fffff || ceil_div(a.p.D, 16) > 0x7fffff) return hipErrorInvalidConfiguration;
-    up_kernel<T, TYPE, F><<<dim3(unsigned(up)), dim3(WAVES * 64), 0, stream>>>(a);
+    up_kernel<T, TYPE, F, UP_AHEAD><<<dim3(unsigned(up)), dim3(WAVES * 64), 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    down_kernel<T, TYPE><<<dim3(unsigned(ceil_div(a.p.D, 16))), dim3(WAVES * 64), size_t(WAVES * a.p.tokens * 64), stream>>>(a);
+    down_kernel<T, TYPE, DOWN_AHEAD><<<dim3(unsigned(ceil_div(a.p.D, 16))), dim3(WAVES * 64), size_t(WAVES * a.p.tokens * 64), stream>>>(a);
     return hipGetLastError();
 }
+// Two fragments at a time where an expert has more than eight tokens in the mean.
 template <class T, int TYPE>
 hipError_t run_tokens(LayerArgs &a, hipStream_t stream) {
-    if (a.p.tokens <= 16) return run<T, TYPE, 1>(a, stream);
-    if (a.p.tokens <= 32) return run<T, TYPE, 2>(a, stream);
-    return run<T, TYPE, 4>(a, stream);
+    return a.p.tokens > 16 && a.p.tokens * a.p.top_k > 8 * a.p.experts ? run<T, TYPE, 2>(a, stream) : run<T, TYPE, 1>(a, stream);
 }
 template <class T>
 hipError_t run_type(LayerArgs &a, hipStream_t stream) {
