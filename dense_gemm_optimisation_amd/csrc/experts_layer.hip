@@ -54,57 +54,100 @@ __device__ inline f32x4 mfma16<F16>(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
 // Eight codes as eight 16-bit values, exactly.
+template <class T, int TYPE, bool HIGH>
+__device__ inline uint32_t widen2(uint32_t w) {
+    if constexpr (__is_same(T, BF16)) {
+        const bf16x2 v = TYPE == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH)
+                                   : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, 1.0f, HIGH);
+        return __builtin_bit_cast(uint32_t, v);
+    } else {
+        const f16x2 v = TYPE == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HIGH)
+                                  : __builtin_amdgcn_cvt_scalef32_pk_f16_bf8(w, 1.0f, HIGH);
+        return __builtin_bit_cast(uint32_t, v);
+    }
+}
 template <class T, int TYPE>
 __device__ inline u32x4 widen(uint32_t lo, uint32_t hi) {
-    float x[8];
-    const uint32_t w[2] = {lo, hi};
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        typedef float f32x2 __attribute__((ext_vector_type(2)));
-        const f32x2 a = TYPE == 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(w[h], false) : __builtin_amdgcn_cvt_pk_f32_bf8(w[h], false);
-        const f32x2 b = TYPE == 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(w[h], true) : __builtin_amdgcn_cvt_pk_f32_bf8(w[h], true);
-        x[4 * h] = a[0], x[4 * h + 1] = a[1], x[4 * h + 2] = b[0], x[4 * h + 3] = b[1];
-    }
-    return pack8<T>(x);
+    return u32x4{widen2<T, TYPE, false>(lo), widen2<T, TYPE, true>(lo), widen2<T, TYPE, false>(hi), widen2<T, TYPE, true>(hi)};
 }
 
-// One row's weights of a run of 128 from k0, as a lane holds them: 16-bit, the
-// chunks of 8 at k0 + 32s + 8q; codes, the chunks of 16 at k0 + 64s + 16q
-// (q = lane / 16).
+__device__ inline u32x4 load16(const char *base, uint32_t offset) {
+    return *reinterpret_cast<const u32x4 *>(base + offset);
+}
+
+// Where lane q of four (lane / 16) has its eight k of step s of a run: 16-bit
+// weights are read as chunks of 8 at 32s + 8q, codes as chunks of 16 at
+// 64(s/2) + 16q, the activations in the same order.
+template <int TYPE>
+__device__ constexpr int k_of(int s, int q) {
+    return TYPE == 0 ? 32 * s + 8 * q : 64 * (s / 2) + 16 * q + 8 * (s % 2);
+}
+// Zeros for the values at K and beyond of a chunk that starts at k.
+__device__ inline void cut(u32x4 &w, int k, int K) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (k + e >= K) w[e / 2] &= e % 2 ? 0xffffu : 0xffff0000u;
+}
+
+// One row's weights of a run of 128 k, as a lane holds them.
 template <int TYPE>
 struct Run {
-    static constexpr int LOADS = TYPE == 0 ? 4 : 2;
+    static constexpr int LOADS = TYPE == 0 ? 4 : 2, PER = TYPE == 0 ? 8 : 16;
     u32x4 v[LOADS];
 
-    // Chunks that begin at K or beyond are zeros; `row` is the row's start.
-    __device__ void fetch(const char *row, bool live, int64_t k0, int64_t K, int q) {
-        constexpr int PER = TYPE == 0 ? 8 : 16;
+    // base: the rows at the run's first k (the same in the whole wave);
+    // offset: of the lane's row and chunk.
+    __device__ void fetch(const char *base, uint32_t offset) {
 #pragma unroll
-        for (int s = 0; s < LOADS; ++s) {
-            const int64_t k = k0 + s * (4 * PER) + q * PER;
-            const u32x4 zero = {0, 0, 0, 0};
-            v[s] = live && k < K ? *reinterpret_cast<const u32x4 *>(row + k * (TYPE == 0 ? 2 : 1)) : zero;
-        }
+        for (int s = 0; s < LOADS; ++s) v[s] = load16(base, offset + s * 64);
     }
-    // The operand of step s; its values at K and beyond are zeros.
+    // A last run of `left` < 128 values: chunks that start within them.
+    __device__ void fetch_part(const char *base, uint32_t offset, int left, int q) {
+        const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < LOADS; ++s) v[s] = s * 4 * PER + q * PER < left ? load16(base, offset + s * 64) : zero;
+    }
+    // The operand of step s.
     template <class T>
-    __device__ u32x4 operand(int s, int64_t k0, int64_t K, int q) const {
-        u32x4 w = TYPE == 0 ? v[s % LOADS] : widen<T, TYPE>(v[s / 2 % LOADS][2 * (s & 1)], v[s / 2 % LOADS][2 * (s & 1) + 1]);
-        cut(w, at(s, k0, q), K);
+    __device__ u32x4 operand(int s) const {
+        if constexpr (TYPE == 0) return v[s];
+        else return widen<T, TYPE>(v[s / 2][2 * (s % 2)], v[s / 2][2 * (s % 2) + 1]);
+    }
+    template <class T>
+    __device__ u32x4 operand_part(int s, int left, int q) const {
+        u32x4 w = operand<T>(s);
+        cut(w, k_of<TYPE>(s, q), left);
         return w;
     }
-    // First k of step s's chunk.
-    static __device__ int64_t at(int s, int64_t k0, int q) {
-        return TYPE == 0 ? k0 + 32 * s + 8 * q : k0 + 64 * (s >> 1) + 16 * q + 8 * (s & 1);
-    }
-    static __device__ void cut(u32x4 &w, int64_t k, int64_t K) {
-        if (k + 8 <= K) return;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (k + e >= K) w[e / 2] &= e % 2 ? 0xffffu : 0xffff0000u;
-    }
 };
+
+// The same of a run of activations, 16-bit, in the order of TYPE's weights.
+template <int TYPE>
+__device__ inline void fetch_values(u32x4 (&v)[STEPS], const char *base, uint32_t offset) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) v[s] = load16(base, offset + 2 * k_of<TYPE>(s, 0));
+}
+template <int TYPE>
+__device__ inline void fetch_values_part(u32x4 (&v)[STEPS], const char *base, uint32_t offset, int left, int q) {
+    const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        v[s] = k_of<TYPE>(s, q) < left ? load16(base, offset + 2 * k_of<TYPE>(s, 0)) : zero;
+        cut(v[s], k_of<TYPE>(s, q), left);
+    }
+}
+// Bytes from a row's start to lane q's first chunk of activations.
+template <int TYPE>
+__device__ inline uint32_t lane_bytes(int q) { return (TYPE == 0 ? 16 : 32) * q; }
+
+template <class P>
+__device__ inline P uniform_pointer(P p) {
+    return reinterpret_cast<P>(uniform(reinterpret_cast<int64_t>(p)));
+}
 
 // What a workgroup finds out from the ids: the live experts in rising order.
 struct Live {
@@ -154,8 +197,11 @@ __device__ inline float scalar_load(const float *p) {
 }
 
 // F: fragments of 16 tokens at a time; an expert with more reads its weights
-// again, from L2.  A wave has 16 rows of both halves and
-// 1 / slices of D; waves of one block of rows meet in LDS.
+// again, from L2.  A wave has 16 rows of both halves and 1 / slices of D;
+// waves of one block of rows meet in LDS.
+//
+// Rows past H and tokens past the expert's are computed from rows that are
+// there, and not stored: a row's and a token's results depend on no other.
 template <class T, int TYPE, int F, int AHEAD>
 __global__ __launch_bounds__(WAVES * 64, 1) void up_kernel(LayerArgs a) {
     const ExpertsLayer &p = a.p;
@@ -163,13 +209,13 @@ __global__ __launch_bounds__(WAVES * 64, 1) void up_kernel(LayerArgs a) {
     __shared__ int16_t token[LAYER_MAX_TOKENS], choice[LAYER_MAX_TOKENS];
     __shared__ int count_shared;
     __shared__ f32x4 part[WAVES][2][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int slices = a.slices, per = WAVES / slices;  // blocks of 16 rows in a workgroup
     const int groups = int((p.H + 16 * per - 1) / (16 * per));
     const int n_live = find_live(a, live);
     const int which = blockIdx.x / groups;
     if (which >= n_live) return;
-    const int e = live.list[which], k = int(p.top_k);
+    const int e = __builtin_amdgcn_readfirstlane(live.list[which]), k = int(p.top_k);
     const int64_t h0 = (int64_t(blockIdx.x % groups) * per + wave / slices) * 16;
     const int slice = wave % slices;
     // the tokens that chose it, in rising order
@@ -184,88 +230,108 @@ __global__ __launch_bounds__(WAVES * 64, 1) void up_kernel(LayerArgs a) {
         if (lane == 0) count_shared = __popcll(mask);
     }
     __syncthreads();
-    const int count = count_shared;
+    const int count = __builtin_amdgcn_readfirstlane(count_shared);
     const int r = lane & 15, q = lane >> 4;
-    const bool has_h = h0 + r < p.H;
-    const int ESZ = TYPE == 0 ? 2 : 1;
-    const char *gate = static_cast<const char *>(p.up.w) + (e * p.up.stride + (h0 + r) * p.up.ld) * ESZ;
-    const char *mult = gate + p.H * p.up.ld * ESZ;
-    // Runs of weights and activations are on their way AHEAD runs before they
-    // are multiplied.
-    Run<TYPE> ng[AHEAD], nm[AHEAD];
-    u32x4 nx[AHEAD][F][STEPS];
+    constexpr int ESZ = TYPE == 0 ? 2 : 1;
+    const int64_t first = h0 < p.H ? h0 : p.H - 1;
+    const int64_t row = first + r < p.H ? r : p.H - 1 - first;
+    const char *gate = uniform_pointer(static_cast<const char *>(p.up.w) + (e * p.up.stride + first * p.up.ld) * ESZ);
+    const char *mult = uniform_pointer(gate + p.H * p.up.ld * ESZ);
+    const uint32_t offset = uint32_t(row * p.up.ld * ESZ) + 16 * q;
     // the 16 rows of the activated half lie in one block of 128, the others'
     // (lo .. hi) in two where H is no multiple of 16
-    float sg[AHEAD], sm_lo[AHEAD], sm_hi[AHEAD];
-    const int64_t first = h0 < p.H ? h0 : p.H - 1, last = h0 + 15 < p.H ? h0 + 15 : p.H - 1;
+    const int64_t last = h0 + 15 < p.H ? h0 + 15 : p.H - 1;
     const int64_t in_gate = uniform(first / 128), in_lo = uniform((p.H + first) / 128), in_hi = uniform((p.H + last) / 128);
+    const int64_t in_first = in_hi * 128 - (p.H + h0);  // rows of the block of lo, where there are two
     const float *scale = p.up.scale + e * p.up.stride_scale;
-    const char *x[F];
-    bool has_x[F];
-    auto fetch = [&](int i, int64_t k0) {
-        if (TYPE != 0 && k0 < p.D) {
-            const float *sc = scale + k0 / 128 * p.up.lds;
-            sg[i] = scalar_load(sc + in_gate);
-            sm_lo[i] = scalar_load(sc + in_lo);
-            sm_hi[i] = scalar_load(sc + in_hi);
-        }
-        ng[i].fetch(gate, has_h, k0, p.D, q);
-        nm[i].fetch(mult, has_h, k0, p.D, q);
+    // Whole runs of weights and activations are on their way AHEAD runs before
+    // they are multiplied; past the last one the last is fetched again, so
+    // that nothing branches around a load.
+    Run<TYPE> ng[AHEAD], nm[AHEAD];
+    u32x4 nx[AHEAD][F][STEPS];
+    float sg[AHEAD], sm_lo[AHEAD], sm_hi[AHEAD];
+    uint32_t x[F];
+    const int whole = int(p.D / RUN), mine = (whole - slice + slices - 1) / slices;  // of the slice
+    const char *values = static_cast<const char *>(p.X);
+    auto fetch_scales = [&](int i, int64_t run) {
+        if (TYPE == 0) return;
+        const float *sc = scale + run * p.up.lds;
+        sg[i] = scalar_load(sc + in_gate);
+        sm_lo[i] = scalar_load(sc + in_lo);
+        sm_hi[i] = scalar_load(sc + in_hi);
+    };
+    auto fetch = [&](int i, int n) {
+        const int64_t run = slice + int64_t(n < mine ? n : mine - 1) * slices;
+        fetch_scales(i, run);
+        ng[i].fetch(gate + run * RUN * ESZ, offset);
+        nm[i].fetch(mult + run * RUN * ESZ, offset);
 #pragma unroll
-        for (int f = 0; f < F; ++f)
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const int64_t at = Run<TYPE>::at(s, k0, q);
-                const u32x4 zero = {0, 0, 0, 0};
-                nx[i][f][s] = has_x[f] && at < p.D ? *reinterpret_cast<const u32x4 *>(x[f] + at * 2) : zero;
-            }
+        for (int f = 0; f < F; ++f) fetch_values<TYPE>(nx[i][f], values + run * RUN * 2, x[f]);
     };
     for (int t0 = 0; t0 < count; t0 += 16 * F) {
 #pragma unroll
         for (int f = 0; f < F; ++f) {
             const int at = t0 + 16 * f + r;
-            has_x[f] = at < count;
-            x[f] = static_cast<const char *>(p.X) + (has_x[f] ? token[at] * p.ldx * 2 : 0);
+            x[f] = uint32_t(token[at < count ? at : 0] * p.ldx * 2) + lane_bytes<TYPE>(q);
         }
         f32x4 g[F], m[F];
 #pragma unroll
         for (int f = 0; f < F; ++f) g[f] = f32x4{0, 0, 0, 0}, m[f] = f32x4{0, 0, 0, 0};
-        const int64_t stride = int64_t(slices) * RUN;
+        // sums of one run (part: its `left` values) added to g and m
+        auto multiply = [&](int i, bool part, int left) {
+            f32x4 bg[F], bm[F];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) fetch(i, slice * RUN + i * stride);
-        for (int64_t k1 = slice * RUN; k1 < p.D; k1 += AHEAD * stride)
+            for (int f = 0; f < F; ++f) {
+                bg[f] = TYPE == 0 ? g[f] : f32x4{0, 0, 0, 0};
+                bm[f] = TYPE == 0 ? m[f] : f32x4{0, 0, 0, 0};
+            }
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                const int64_t k0 = k1 + i * stride;
-                if (k0 >= p.D) break;
-                const float gate_scale = sg[i], lo_scale = sm_lo[i], hi_scale = sm_hi[i];
-                f32x4 bg[F], bm[F];
+            for (int s = 0; s < STEPS; ++s) {
+                const u32x4 og = part ? ng[i].template operand_part<T>(s, left, q) : ng[i].template operand<T>(s);
+                const u32x4 om = part ? nm[i].template operand_part<T>(s, left, q) : nm[i].template operand<T>(s);
 #pragma unroll
                 for (int f = 0; f < F; ++f) {
-                    bg[f] = TYPE == 0 ? g[f] : f32x4{0, 0, 0, 0};
-                    bm[f] = TYPE == 0 ? m[f] : f32x4{0, 0, 0, 0};
+                    bg[f] = mfma16<T>(og, nx[i][f][s], bg[f]);
+                    bm[f] = mfma16<T>(om, nx[i][f][s], bm[f]);
                 }
-#pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    const u32x4 og = ng[i].template operand<T>(s, k0, p.D, q), om = nm[i].template operand<T>(s, k0, p.D, q);
-#pragma unroll
-                    for (int f = 0; f < F; ++f) {
-                        u32x4 xv = nx[i][f][s];
-                        Run<TYPE>::cut(xv, Run<TYPE>::at(s, k0, q), p.D);
-                        bg[f] = mfma16<T>(og, xv, bg[f]);
-                        bm[f] = mfma16<T>(om, xv, bm[f]);
-                    }
-                }
-                fetch(i, k0 + AHEAD * stride);
-#pragma unroll
-                for (int f = 0; f < F; ++f)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float mult_scale = (p.H + h0 + 4 * q + j) / 128 == in_lo ? lo_scale : hi_scale;
-                        g[f][j] = TYPE == 0 ? bg[f][j] : __builtin_fmaf(gate_scale, bg[f][j], g[f][j]);
-                        m[f][j] = TYPE == 0 ? bm[f][j] : __builtin_fmaf(mult_scale, bm[f][j], m[f][j]);
-                    }
             }
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                if (TYPE == 0) {
+                    g[f] = bg[f];
+                    m[f] = bm[f];
+                    continue;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float mult_scale = 4 * q + j < in_first ? sm_lo[i] : sm_hi[i];
+                    g[f][j] = __builtin_fmaf(sg[i], bg[f][j], g[f][j]);
+                    m[f][j] = __builtin_fmaf(mult_scale, bm[f][j], m[f][j]);
+                }
+            }
+        };
+        if (mine > 0) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) fetch(i, i);
+            int n = 0;
+            for (; n + AHEAD <= mine; n += AHEAD)
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    multiply(i, false, RUN);
+                    fetch(i, n + i + AHEAD);
+                }
+#pragma unroll
+            for (int i = 0; i < AHEAD - 1; ++i)
+                if (n + i < mine) multiply(i, false, RUN);
+        }
+        if (const int left = int(p.D % RUN); left != 0 && slice == whole % slices) {
+            fetch_scales(0, whole);
+            ng[0].fetch_part(gate + int64_t(whole) * RUN * ESZ, offset, left, q);
+            nm[0].fetch_part(mult + int64_t(whole) * RUN * ESZ, offset, left, q);
+#pragma unroll
+            for (int f = 0; f < F; ++f) fetch_values_part<TYPE>(nx[0][f], values + int64_t(whole) * RUN * 2, x[f], left, q);
+            multiply(0, true, left);
+        }
         // a lane's registers: rows h0 + 4q + 0..3 of token r
 #pragma unroll
         for (int f = 0; f < F; ++f) {
@@ -311,11 +377,12 @@ template <class T, int TYPE, int AHEAD>
 __global__ __launch_bounds__(WAVES * 64, 1) void down_kernel(LayerArgs a) {
     const ExpertsLayer &p = a.p;
     __shared__ Live live;
-    __shared__ uint8_t token[MOST_SLOTS], choice[MOST_SLOTS];  // by live expert
+    __shared__ uint8_t token[MOST_SLOTS];  // by live expert
+    __shared__ uint16_t slot[MOST_SLOTS];  // token * top_k + choice
     __shared__ int16_t start[LAYER_MAX_EXPERTS + 1];
     extern __shared__ __attribute__((aligned(16))) char smem[];
     f32x4 *sums = reinterpret_cast<f32x4 *>(smem);  // [wave][token][four columns]
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int k = int(p.top_k), tokens = int(p.tokens);
     const int n_live = find_live(a, live);
     const int r = lane & 15, q = lane >> 4;
@@ -346,76 +413,121 @@ __global__ __launch_bounds__(WAVES * 64, 1) void down_kernel(LayerArgs a) {
         if (c >= 0) {
             const int at = start[i] + __popcll(mask & ((uint64_t(1) << lane) - 1));
             token[at] = uint8_t(lane);
-            choice[at] = uint8_t(c);
+            slot[at] = uint16_t(lane * k + c);
         }
     }
     __syncthreads();
     const int64_t d0 = int64_t(blockIdx.x) * 16;
-    const bool has_d = d0 + r < p.D;
-    const int ESZ = TYPE == 0 ? 2 : 1;
-    const char *down = static_cast<const char *>(p.down.w) + (d0 + r) * p.down.ld * ESZ;
-    const int runs = int((p.H + RUN - 1) / RUN), units = n_live * runs;
-    Run<TYPE> next[AHEAD];
-    float next_scale[AHEAD];
-    auto fetch = [&](int i, int u) {
-        if (u >= units) return;
-        const int e = live.list[u / runs];
-        const int64_t k0 = int64_t(u % runs) * RUN;
-        next[i].fetch(down + e * p.down.stride * ESZ, has_d, k0, p.H, q);
-        // 16 rows from a multiple of 16 lie in one block of 128
-        if (TYPE != 0) next_scale[i] = scalar_load(p.down.scale + e * p.down.stride_scale + (k0 / 128) * p.down.lds + d0 / 128);
+    constexpr int ESZ = TYPE == 0 ? 2 : 1;
+    const int64_t row = d0 + r < p.D ? r : p.D - 1 - d0;  // rows past D: the last one's, not stored
+    const char *down = static_cast<const char *>(p.down.w) + d0 * p.down.ld * ESZ;
+    const uint32_t offset = uint32_t(row * p.down.ld * ESZ) + 16 * q;
+    const int runs = int(p.H / RUN), units = n_live * runs;  // whole runs
+    // Weights, and the pieces of w h of a unit's first tokens, are fetched
+    // AHEAD units before they are multiplied; pieces fetched later than the
+    // weights would wait for all weights asked for before.  Past the last unit
+    // the last is fetched again, so that nothing branches around a load.
+    struct Unit {
+        int expert, run, first, end;  // first .. end: its slots
     };
-    // the pieces of w h of a unit's first tokens, fetched with its weights:
-    // fetched later, they would wait for all weights asked for before
+    Run<TYPE> next[AHEAD];
+    Unit unit[AHEAD];
+    float next_scale[AHEAD];
     u32x4 hi[AHEAD][STEPS], lo[AHEAD][STEPS];
-    auto fetch_h = [&](u32x4 (&vh)[STEPS], u32x4 (&vl)[STEPS], int u, int at) {
-        // token `at` of the unit's expert
-        if (u >= units) return;
-        at += start[u / runs] + r;
-        const bool has = at < start[u / runs + 1];
-        const uint16_t *h = a.h + (has ? (token[at] * k + choice[at]) * 2 * a.ldh : 0);
+    // token r of the slots from `from` on; past the expert's, its first one
+    // there, which is not added to a sum
+    auto pieces_at = [&](const Unit &u, int from) {
+        return uint32_t(slot[from + r < u.end ? from + r : from] * 4 * a.ldh) + lane_bytes<TYPE>(q);
+    };
+    auto pieces_base = [&](const Unit &u) { return reinterpret_cast<const char *>(a.h + int64_t(u.run) * RUN); };
+    auto fetch_h = [&](int i, const Unit &u, int from) {
+        const uint32_t at = pieces_at(u, from);
+        fetch_values<TYPE>(hi[i], pieces_base(u), at);
+        fetch_values<TYPE>(lo[i], pieces_base(u) + 2 * a.ldh, at);
+    };
+    auto weights_base = [&](const Unit &u) {
+        const int e = __builtin_amdgcn_readfirstlane(live.list[u.expert]);
+        return down + (e * p.down.stride + int64_t(u.run) * RUN) * ESZ;
+    };
+    auto fetch_scale = [&](int i, const Unit &u) {
+        if (TYPE == 0) return;
+        const int e = __builtin_amdgcn_readfirstlane(live.list[u.expert]);
+        // 16 rows from a multiple of 16 lie in one block of 128
+        next_scale[i] = scalar_load(p.down.scale + e * p.down.stride_scale + u.run * p.down.lds + d0 / 128);
+    };
+    auto unit_of = [&](int expert, int run) {
+        return Unit{expert, run, __builtin_amdgcn_readfirstlane(start[expert]), __builtin_amdgcn_readfirstlane(start[expert + 1])};
+    };
+    // the sums of the 16 slots from s0 on, added to their tokens'
+    auto multiply = [&](int i, const u32x4 (&od)[STEPS], const Unit &u, int s0) {
+        f32x4 block = {0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            const int64_t from = Run<TYPE>::at(s, int64_t(u % runs) * RUN, q);
-            const u32x4 zero = {0, 0, 0, 0};
-            vh[s] = has && from < p.H ? *reinterpret_cast<const u32x4 *>(h + from) : zero;
-            vl[s] = has && from < p.H ? *reinterpret_cast<const u32x4 *>(h + a.ldh + from) : zero;
+            block = mfma16<T>(od[s], lo[i][s], block);
+            block = mfma16<T>(od[s], hi[i][s], block);
         }
+        if (s0 + r >= u.end) return;
+        f32x4 *sum = sums + (wave * tokens + token[s0 + r]) * 4 + q;
+        f32x4 v = *sum;
+        const float scale = TYPE == 0 ? 1.0f : next_scale[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(scale, block[j], v[j]);
+        *sum = v;
     };
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-        fetch(i, wave + i * WAVES);
-        fetch_h(hi[i], lo[i], wave + i * WAVES, 0);
-    }
-    for (int u0 = wave; u0 < units; u0 += AHEAD * WAVES)
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int u = u0 + i * WAVES;
-            if (u >= units) break;
-            const int64_t k0 = int64_t(u % runs) * RUN;
-            const int first = start[u / runs], end = start[u / runs + 1];
-            const float scale = TYPE == 0 ? 1.0f : next_scale[i];
+    if (wave < units) {
+        // the unit to fetch, and how far eight units are
+        const int on_expert = WAVES / runs, on_run = WAVES % runs;
+        int expert = wave / runs, run = wave % runs, at = wave;
+        auto fetch = [&](int i) {
+            unit[i] = unit_of(expert, run);
+            next[i].fetch(weights_base(unit[i]), offset);
+            fetch_scale(i, unit[i]);
+            fetch_h(i, unit[i], unit[i].first);
+            if (at + WAVES >= units) return;
+            at += WAVES;
+            expert += on_expert;
+            run += on_run;
+            if (run >= runs) run -= runs, ++expert;
+        };
+        auto step = [&](int i) {
             u32x4 od[STEPS];
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) od[s] = next[i].template operand<T>(s, k0, p.H, q);
-            for (int s0 = first; s0 < end; s0 += 16) {
-                if (s0 > first) fetch_h(hi[i], lo[i], u, s0 - first);
-                f32x4 block = {0, 0, 0, 0};
-#pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    block = mfma16<T>(od[s], lo[i][s], block);
-                    block = mfma16<T>(od[s], hi[i][s], block);
-                }
-                if (s0 + r < end) {
-                    f32x4 *sum = sums + (wave * tokens + token[s0 + r]) * 4 + q;
-                    f32x4 v = *sum;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(scale, block[j], v[j]);
-                    *sum = v;
-                }
+            for (int s = 0; s < STEPS; ++s) od[s] = next[i].template operand<T>(s);
+            const Unit u = unit[i];
+            multiply(i, od, u, u.first);
+            for (int s0 = u.first + 16; s0 < u.end; s0 += 16) {
+                fetch_h(i, u, s0);
+                multiply(i, od, u, s0);
             }
-            fetch(i, u + AHEAD * WAVES);
-            fetch_h(hi[i], lo[i], u + AHEAD * WAVES, 0);
+        };
+        const int mine = (units - wave + WAVES - 1) / WAVES;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) fetch(i);
+        int n = 0;
+        for (; n + AHEAD <= mine; n += AHEAD)
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                step(i);
+                fetch(i);
+            }
+#pragma unroll
+        for (int i = 0; i < AHEAD - 1; ++i)
+            if (n + i < mine) step(i);
+    }
+    if (const int left = int(p.H % RUN); left != 0)
+        for (int i = wave; i < n_live; i += WAVES) {
+            const Unit u = unit_of(i, runs);
+            next[0].fetch_part(weights_base(u), offset, left, q);
+            fetch_scale(0, u);
+            u32x4 od[STEPS];
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) od[s] = next[0].template operand_part<T>(s, left, q);
+            for (int s0 = u.first; s0 < u.end; s0 += 16) {
+                const uint32_t at = pieces_at(u, s0);
+                fetch_values_part<TYPE>(hi[0], pieces_base(u), at, left, q);
+                fetch_values_part<TYPE>(lo[0], pieces_base(u) + 2 * a.ldh, at, left, q);
+                multiply(0, od, u, s0);
+            }
         }
     __syncthreads();
     for (int i = threadIdx.x; i < tokens * 16; i += WAVES * 64) {
