@@ -184,45 +184,76 @@ __device__ inline f32x4 mfma16<F16>(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// At most 16 rows by 16 columns, K dealt to eight waves in runs of 128.
+// At most ROWS (4, 8 or 16) rows by 16 columns, K dealt to eight waves in runs of 128.
+// A wave keeps the next runs of both operands on their way into its own
+// LDS: a direct load takes four rows of 256 bytes, while loads in the matrix
+// instruction's own order would ask for one 16-byte piece of 16 rows after
+// another and keep the address unit busy three times as long.  16-byte chunk
+// c of row r lies at c ^ r, so the 16 rows of a read fall in different banks.
 // Operands swapped: lane l has column 4*(l / 16) + r of row l % 16 in
 // register r.
-template <class T, bool BACKWARD>
-__global__ __launch_bounds__(512, 2) void few_kernel(LinearArgs p) {
+template <class T, bool BACKWARD, int ROWS>
+__global__ __launch_bounds__(512, 1) void few_kernel(LinearArgs p) {
     constexpr int WAVES = 8, RUN = 128, STEPS = RUN / 32;
-    __shared__ f32x4 part[WAVES][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    constexpr int STAGE = (16 + ROWS) * 256, RING = ROWS == 16 ? 2 : ROWS == 8 ? 3 : 4, PER = 4 + ROWS / 4;
+    __shared__ __attribute__((aligned(1024))) char smem[WAVES * RING * STAGE];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = int64_t(blockIdx.x) * 16;
-    const int row = lane & 15, kq = (lane >> 4) * 8;
-    const bool has_a = row < p.M, has_b = n0 + row < p.N;
-    const uint16_t *pa = p.a.p + row * p.a.ld + kq, *pb = p.b.p + (n0 + row) * p.b.ld + kq;
-    const u32x4 zero = {0, 0, 0, 0};
+    const int row = lane & 15, q = lane >> 4;
+    LDS char *lds = (LDS char *)smem + wave * (RING * STAGE);
+    const char *pa = reinterpret_cast<const char *>(p.a.p), *pb = reinterpret_cast<const char *>(p.b.p + n0 * p.b.ld);
+    uint32_t va[ROWS / 4], vb[4];
+    int ca[4];  // this lane's chunk of each row group
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = 4 * j + q, c = row ^ r;
+        ca[j] = c * 8;
+        vb[j] = n0 + r < p.N ? uint32_t(r * p.b.ld * 2 + c * 16) : OOB;
+        if (j < ROWS / 4) va[j] = r < p.M ? uint32_t(r * p.a.ld * 2 + c * 16) : OOB;
+    }
+    const int64_t runs = (p.K + RUN - 1) / RUN, mine = (runs - wave + WAVES - 1) / WAVES;
+    auto issue = [&](int64_t n) {
+        const int64_t k0 = (wave + n * WAVES) * RUN, left = p.K - k0;
+        const u32x4 rb = dma::raw_buffer(static_cast<uint64_t>(uniform(reinterpret_cast<int64_t>(pb + 2 * k0))), 0x7fffffff);
+        const u32x4 ra = dma::raw_buffer(static_cast<uint64_t>(uniform(reinterpret_cast<int64_t>(pa + 2 * k0))), 0x7fffffff);
+        const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) + uint32_t(n % RING) * STAGE;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) direct_load16(rb, to + j * 1024, ca[j] < left ? vb[j] : OOB);
+#pragma unroll
+        for (int j = 0; j < ROWS / 4; ++j) direct_load16(ra, to + 4096 + j * 1024, ca[j] < left ? va[j] : OOB);
+    };
     f32x4 acc = {0, 0, 0, 0};
-    // the next run's operands are on their way while this one is multiplied
-    u32x4 a[STEPS], b[STEPS];
-    auto fetch = [&](int64_t k0) {
+    for (int n = 0; n < RING; ++n)
+        if (n < mine) issue(n);
+    for (int64_t n = 0; n < mine; ++n) {
+        const int64_t later = mine - 1 - n;
+        if (RING > 3 && later >= 3) wait_vmcnt<(RING > 3 ? 3 : 0) * PER>();
+        else if (RING > 2 && later >= 2) wait_vmcnt<(RING > 2 ? 2 : 0) * PER>();
+        else if (later >= 1) wait_vmcnt<PER>();
+        else wait_vmcnt<0>();
+        asm volatile("" ::: "memory");
+        const LDS char *stage = lds + int(n % RING) * STAGE;
+        u32x4 a[STEPS], b[STEPS];
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            const int64_t k = k0 + 32 * s;
-            b[s] = has_b && k + kq < p.K ? *reinterpret_cast<const u32x4 *>(pb + k) : zero;
-            a[s] = has_a && k + kq < p.K ? *reinterpret_cast<const u32x4 *>(pa + k) : zero;
+            const int ra = row % ROWS;  // columns past the rows are not stored
+            b[s] = *reinterpret_cast<const LDS u32x4 *>(stage + row * 256 + (((4 * s + q) ^ row) << 4));
+            a[s] = *reinterpret_cast<const LDS u32x4 *>(stage + 4096 + ra * 256 + (((4 * s + q) ^ ra) << 4));
         }
-    };
-    fetch(wave * RUN);
-    for (int64_t k0 = wave * RUN; k0 < p.K; k0 += WAVES * RUN) {
-        u32x4 ca[STEPS], cb[STEPS];
+        wait_lgkmcnt0();
+        asm volatile("" ::: "memory");
+        if (n + RING < mine) issue(n + RING);
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) ca[s] = a[s], cb[s] = b[s];
-        fetch(k0 + WAVES * RUN);
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) acc = mfma16<T>(cb[s], ca[s], acc);
+        for (int s = 0; s < STEPS; ++s) acc = mfma16<T>(b[s], a[s], acc);
     }
-    part[wave][lane] = acc;
+    LDS f32x4 *part = reinterpret_cast<LDS f32x4 *>((LDS char *)smem);
+    __syncthreads();  // every wave has read its runs
+    part[wave * 64 + lane] = acc;
     __syncthreads();
     if (wave != 0) return;
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) {
-        const f32x4 o = part[w][lane];
+        const f32x4 o = part[w * 64 + lane];
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] += o[e];
     }
@@ -369,7 +400,9 @@ hipError_t run_kernel(LinearKernel k, LinearArgs &a, hipStream_t stream) {
         case LinearKernel::Split: return run_split<T128, T, BACKWARD>(a, stream);
         case LinearKernel::AnySplit: return run_split<Any, T, BACKWARD>(a, stream);
         case LinearKernel::Few16:
-            few_kernel<T, BACKWARD><<<dim3(unsigned(ceil_div(a.N, 16))), dim3(512), 0, stream>>>(a);
+            if (a.M <= 4) few_kernel<T, BACKWARD, 4><<<dim3(unsigned(ceil_div(a.N, 16))), dim3(512), 0, stream>>>(a);
+            else if (a.M <= 8) few_kernel<T, BACKWARD, 8><<<dim3(unsigned(ceil_div(a.N, 16))), dim3(512), 0, stream>>>(a);
+            else few_kernel<T, BACKWARD, 16><<<dim3(unsigned(ceil_div(a.N, 16))), dim3(512), 0, stream>>>(a);
             return hipGetLastError();
         default: return hipSuccess;
     }
