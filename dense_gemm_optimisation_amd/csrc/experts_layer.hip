@@ -1,26 +1,31 @@
 // A whole layer of experts for a few tokens (gemm_experts_layer), in two
-// kernels that each read every live expert's weights once.
+// kernels that read the live experts' weights once.
 //
-//   up_kernel    w h, h = act(Up[0 .. H) x) * (Up[H .. 2H) x): a wave has 16 of
-//                H's rows, both halves, of one live expert, and the tokens that
-//                chose it; where that leaves too few waves, up to eight share
-//                the rows' D and meet in LDS.  w h leaves as two 16-bit
-//                pieces, hi + lo, so it is not rounded to 16 bits in between;
+//   up_kernel    w h, h = act(Up[0 .. H) x) * (Up[H .. 2H) x): a workgroup has an
+//                expert, up to XR of the tokens that chose it, and some
+//                blocks of 16 of H's rows, both halves.  w h leaves as two
+//                16-bit pieces, hi + lo, so it is not rounded to 16 bits in
+//                between;
 //   down_kernel  y = sum over the token's experts of Down (w h): a workgroup
 //                has 16 of y's columns for all tokens and goes through
 //                every live expert, its waves dealing (expert, run of H) pairs,
 //                so a token's weighted sum is formed in one place and one order:
 //                no atomics.
 //
-// Bound by reading the weights.  The 16 x 16 x 32 matrix instruction takes
-// them as its 16-row operand straight from global memory (a wave reads 16
-// rows of 64 bytes), with the tokens as its other 16: padded tokens cost
-// nothing that is not idle anyway.  8-bit codes are loaded 16 to a lane and
-// taken as two steps of eight, with the activations' k in the same order, and
-// widened exactly; a run of 128 has one scale.
+// Bound by reading the weights, so each wave keeps the next runs of its 16
+// rows on their way into its own part of LDS, 128 bytes of each row at a time, by direct
+// loads that take eight whole lines; the eight waves of a workgroup take
+// neighbouring runs, 1 KiB of each row together.  (Loads in the
+// matrix instruction's own order, 16 bytes of 16 rows, kept the address unit
+// busy for 51 cycles each: 32 tokens of 64 experts of 1024 x 4096 in 8 bits took 131 and 95 us
+// that way.)  The activations come the same way, behind the weights: then
+// only these loads are counted, and waiting for one run leaves the later ones in flight.
+// The 16 x 16 x 32 matrix instruction takes the weights as its 16-row
+// operand and the tokens as the other; 8-bit codes are widened exactly on the way
+// from LDS, and a run of 128 has one scale.
 //
-// Each workgroup finds the live experts from the ids by itself (at most 2048
-// of them, from L2), which saves a launch.
+// Each workgroup finds the live experts and their tokens from the ids by
+// itself (at most 2048 of them, from L2), which saves a launch.
 #include "activation.hpp"
 #include "layers.hpp"
 #include "tile16.hpp"
@@ -30,17 +35,27 @@ namespace {
 
 using namespace tile16;
 
-constexpr int WAVES = 8, RUN = 128, STEPS = RUN / 32;
-constexpr int MOST_SLOTS = LAYER_MAX_TOKENS * LAYER_MAX_TOP_K;
+constexpr int WAVES = 8, THREADS = WAVES * 64;
+
+template <int TYPE>
+struct Form {
+    static constexpr int ESZ = TYPE == 0 ? 2 : 1;  // bytes of a weight
+    static constexpr int PER = 16 / ESZ;           // weights per 16-byte chunk
+    static constexpr int RUN = 128 / ESZ;          // k of a run: 128 bytes of a row
+    static constexpr int STEPS = RUN / 32;         // matrix instructions
+    // A run's scales come with it, a float for each lane.
+    static constexpr int SCALES = TYPE == 0 ? 0 : 1, SCALE_BYTES = SCALES * 256;
+};
 
 struct LayerArgs {
     ExpertsLayer p;
-    // w h of each choice, two pieces of X's type: [token][choice][piece][ldh]; its first choice of an
-    // expert has all of the token's
+    // w h of each choice: [token * top_k + choice][run][piece][RUN] of X's type; a token's first choice
+    // of an expert has all of its weights for it
     uint16_t *h;
-    int64_t ldh;  // H rounded up to 8, the filling zero
-    int live_most;
-    int slices;   // waves of up_kernel that share a block's columns
+    int64_t ldh;  // elements of a choice
+    int ring_up, ring_down;
+    int blocks;  // of 16 rows in a workgroup of up_kernel
+    int groups;  // workgroups per expert and tokens
 };
 
 template <class T>
@@ -75,468 +90,422 @@ __device__ inline u32x4 widen(uint32_t lo, uint32_t hi) {
     return u32x4{widen2<T, TYPE, false>(lo), widen2<T, TYPE, true>(lo), widen2<T, TYPE, false>(hi), widen2<T, TYPE, true>(hi)};
 }
 
-__device__ inline u32x4 load16(const char *base, uint32_t offset) {
-    return *reinterpret_cast<const u32x4 *>(base + offset);
-}
-
-// Where lane q of four (lane / 16) has its eight k of step s of a run: 16-bit
-// weights are read as chunks of 8 at 32s + 8q, codes as chunks of 16 at
-// 64(s/2) + 16q, the activations in the same order.
+// Lane q of four (lane / 16) has eight k of each step: 16-bit weights those
+// of chunk 4s + q, 32s + 8q; codes half s % 2 of chunk 4(s / 2) + q, 64(s / 2) + 16q +
+// 8(s % 2); the activations in the same order, by their own chunks of 8.
 template <int TYPE>
-__device__ constexpr int k_of(int s, int q) {
+__device__ inline int k_of(int s, int q) {
     return TYPE == 0 ? 32 * s + 8 * q : 64 * (s / 2) + 16 * q + 8 * (s % 2);
 }
-// Zeros for the values at K and beyond of a chunk that starts at k.
+// Zeros for the values at K and beyond of eight that start at k.
 __device__ inline void cut(u32x4 &w, int k, int K) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         if (k + e >= K) w[e / 2] &= e % 2 ? 0xffffu : 0xffff0000u;
 }
 
-// One row's weights of a run of 128 k, as a lane holds them.
-template <int TYPE>
-struct Run {
-    static constexpr int LOADS = TYPE == 0 ? 4 : 2, PER = TYPE == 0 ? 8 : 16;
-    u32x4 v[LOADS];
+__device__ inline u32x4 buffer_at(const void *p) {
+    return dma::raw_buffer(static_cast<uint64_t>(uniform(reinterpret_cast<int64_t>(p))), 0x7fffffff);
+}
 
-    // base: the rows at the run's first k (the same in the whole wave);
-    // offset: of the lane's row and chunk.
-    __device__ void fetch(const char *base, uint32_t offset) {
+// 16 rows of a run of weights in LDS: 128 bytes per row, chunk c of row r at
+// c ^ swz(r).  Two direct loads of eight rows.
+template <int TYPE>
+struct Rows {
+    uint32_t voff[2];
+    int chunk[2];  // first k of this lane's chunk
+
+    // `rows` rows are there; the others are copies of the last.
+    __device__ void init(int64_t ld, int64_t rows, int lane) {
 #pragma unroll
-        for (int s = 0; s < LOADS; ++s) v[s] = load16(base, offset + s * 64);
+        for (int j = 0; j < 2; ++j) {
+            const int r = 8 * j + lane / 8, c = (lane % 8) ^ swz_k<8>(r);
+            voff[j] = uint32_t((r < rows ? r : rows - 1) * ld * Form<TYPE>::ESZ) + c * 16;
+            chunk[j] = c * Form<TYPE>::PER;
+        }
     }
-    // A last run of `left` < 128 values: chunks that start within them.
-    __device__ void fetch_part(const char *base, uint32_t offset, int left, int q) {
-        const u32x4 zero = {0, 0, 0, 0};
+    __device__ void issue(const char *base, uint32_t to, int64_t left) const {
+        const u32x4 rs = buffer_at(base);
 #pragma unroll
-        for (int s = 0; s < LOADS; ++s) v[s] = s * 4 * PER + q * PER < left ? load16(base, offset + s * 64) : zero;
-    }
-    // The operand of step s.
-    template <class T>
-    __device__ u32x4 operand(int s) const {
-        if constexpr (TYPE == 0) return v[s];
-        else return widen<T, TYPE>(v[s / 2][2 * (s % 2)], v[s / 2][2 * (s % 2) + 1]);
+        for (int j = 0; j < 2; ++j) direct_load16(rs, to + j * 1024, chunk[j] < left ? voff[j] : OOB);
     }
     template <class T>
-    __device__ u32x4 operand_part(int s, int left, int q) const {
-        u32x4 w = operand<T>(s);
-        cut(w, k_of<TYPE>(s, q), left);
-        return w;
+    static __device__ u32x4 operand(const LDS char *at, int s, int r, int q) {
+        const int c = TYPE == 0 ? 4 * s + q : 4 * (s / 2) + q;
+        const u32x4 v = *reinterpret_cast<const LDS u32x4 *>(at + r * 128 + ((c ^ swz_k<8>(r)) << 4));
+        if constexpr (TYPE == 0) return v;
+        else return s % 2 ? widen<T, TYPE>(v[2], v[3]) : widen<T, TYPE>(v[0], v[1]);
     }
 };
 
-// The same of a run of activations, 16-bit, in the order of TYPE's weights.
-template <int TYPE>
-__device__ inline void fetch_values(u32x4 (&v)[STEPS], const char *base, uint32_t offset) {
+// N rows of activations in LDS, BYTES (128, 256 or 512) per row, 16-byte
+// chunk c of row r at c ^ f(r), f(r) = swz(r) in rows of 128 bytes, r else.
+template <int N, int BYTES>
+struct Values {
+    static constexpr int LOADS = N * BYTES / 1024, CHUNKS = BYTES / 16, PER_LOAD = 64 / CHUNKS;
+    static constexpr int SIZE = N * BYTES;
+    static_assert(LOADS >= 1 && N * BYTES % 1024 == 0, "whole loads");
+    uint32_t voff[LOADS];
+    int chunk[LOADS];
+    static __device__ int swizzle(int r) { return BYTES == 128 ? swz_k<8>(r) : r & 15; }
+    static __device__ int row_of(int j, int lane) { return j * PER_LOAD + lane / CHUNKS; }
+    // start(r): byte offset of row r
+    template <class F>
+    __device__ void init(int lane, F &&start) {
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) v[s] = load16(base, offset + 2 * k_of<TYPE>(s, 0));
-}
-template <int TYPE>
-__device__ inline void fetch_values_part(u32x4 (&v)[STEPS], const char *base, uint32_t offset, int left, int q) {
-    const u32x4 zero = {0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-        v[s] = k_of<TYPE>(s, q) < left ? load16(base, offset + 2 * k_of<TYPE>(s, 0)) : zero;
-        cut(v[s], k_of<TYPE>(s, q), left);
+        for (int j = 0; j < LOADS; ++j) {
+            const int r = row_of(j, lane), c = (lane % CHUNKS) ^ swizzle(r);
+            chunk[j] = c;
+            voff[j] = start(r) + c * 16;
+        }
     }
-}
-// Bytes from a row's start to lane q's first chunk of activations.
-template <int TYPE>
-__device__ inline uint32_t lane_bytes(int q) { return (TYPE == 0 ? 16 : 32) * q; }
-
-template <class P>
-__device__ inline P uniform_pointer(P p) {
-    return reinterpret_cast<P>(uniform(reinterpret_cast<int64_t>(p)));
-}
-
-// What a workgroup finds out from the ids: the live experts in rising order.
-struct Live {
-    uint32_t bits[LAYER_MAX_EXPERTS / 32];
-    uint16_t list[LAYER_MAX_EXPERTS];
-    int16_t ids[MOST_SLOTS];  // -1: no expert
+    // live(c): whether chunk c is read; others are zeros
+    template <class F>
+    __device__ void issue(const void *base, uint32_t to, F &&live) const {
+        const u32x4 rs = buffer_at(base);
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) direct_load16(rs, to + j * 1024, live(chunk[j]) ? voff[j] : OOB);
+    }
+    static __device__ u32x4 at(const LDS char *base, int r, int c) {
+        return *reinterpret_cast<const LDS u32x4 *>(base + r * BYTES + ((c ^ swizzle(r)) << 4));
+    }
 };
 
-// Fills it; returns how many are live.  All threads of the workgroup call it.
-__device__ int find_live(const LayerArgs &a, Live &live) {
-    const int E = int(a.p.experts), slots = int(a.p.tokens * a.p.top_k), words = (E + 31) / 32;
-    for (int i = threadIdx.x; i < words; i += blockDim.x) live.bits[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < slots; i += blockDim.x) {
-        const uint32_t e = uint32_t(a.p.ids[i]);
-        live.ids[i] = e < uint32_t(E) ? int16_t(e) : int16_t(-1);
-        if (e < uint32_t(E)) atomicOr(&live.bits[e / 32], 1u << (e % 32));
-    }
-    __syncthreads();
-    int before = 0, total = 0;
-    const int mine = int(threadIdx.x);
-    for (int i = 0; i < words; ++i) {
-        const int n = __popc(live.bits[i]);
-        if (i < mine) before += n;
-        total += n;
-    }
-    if (mine < words)
-        for (uint32_t b = live.bits[mine]; b != 0; b &= b - 1) live.list[before++] = uint16_t(32 * mine + __ffs(b) - 1);
-    __syncthreads();
-    return total;
+// Waits until at most `later` stages of PER loads are in flight (later < 4).
+template <int PER>
+__device__ inline void wait_for(int later) {
+    if (later >= 3) wait_vmcnt<3 * PER>();
+    else if (later == 2) wait_vmcnt<2 * PER>();
+    else if (later == 1) wait_vmcnt<PER>();
+    else wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
 }
+
+// What a workgroup finds out from the ids, in LDS: where each expert's
+// choices (a token's first one of it) start, and its groups of up to `size` of them.
+struct Found {
+    LDS int32_t *choices;  // [experts + 1]: where they end, behind a 0
+    LDS int16_t *groups;   // [experts + 1], the same of groups
+    LDS int16_t *ids;      // [slots], -1: no expert
+    __device__ Found(LDS char *at)
+        : choices(reinterpret_cast<LDS int32_t *>(at)),
+          groups(reinterpret_cast<LDS int16_t *>(at + 4 * (LAYER_MAX_EXPERTS + 1))), ids(groups + LAYER_MAX_EXPERTS + 1) {}
+};
 
 // Token t's first choice of expert e, or -1.
-__device__ inline int choice_of(const Live &live, int t, int k, int e) {
+__device__ inline int choice_of(const LDS int16_t *ids, int t, int k, int e) {
     int first = -1;
     for (int j = k - 1; j >= 0; --j)
-        if (live.ids[t * k + j] == e) first = j;
+        if (ids[t * k + j] == e) first = j;
     return first;
 }
 
-// A float at an address that is the same in the whole wave, by a scalar load:
-// loads into vector registers return in order, so a scale fetched that way
-// would wait for the weights on their way before it.
-__device__ inline float scalar_load(const float *p) {
-    typedef const float __attribute__((address_space(4))) *constant;
-    return *reinterpret_cast<constant>(static_cast<uint64_t>(uniform(reinterpret_cast<int64_t>(p))));
+// All threads of the workgroup call it.
+__device__ void find(const ExpertsLayer &p, const Found &f, int size) {
+    const int E = int(p.experts), k = int(p.top_k), slots = int(p.tokens) * k;
+    for (int i = threadIdx.x; i <= E; i += THREADS) f.choices[i] = 0;
+    for (int i = threadIdx.x; i < slots; i += THREADS) {
+        const uint32_t e = uint32_t(p.ids[i]);
+        f.ids[i] = e < uint32_t(E) ? int16_t(e) : int16_t(-1);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < slots; i += THREADS) {
+        const int e = f.ids[i];
+        if (e < 0) continue;
+        bool first = true;
+        for (int j = i - i % k; j < i; ++j) first = first && f.ids[j] != e;
+        if (first) __hip_atomic_fetch_add(f.choices + e + 1, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        // running sums, 64 experts at a time
+        const int lane = threadIdx.x;
+        int choices = 0, groups = 0;
+        if (lane == 0) f.groups[0] = 0;
+        for (int e0 = 0; e0 < E; e0 += 64) {
+            const int e = e0 + lane;
+            int c = e < E ? f.choices[e + 1] : 0, g = (c + size - 1) / size;
+            for (int d = 1; d < 64; d *= 2) {
+                const int oc = __shfl_up(c, d), og = __shfl_up(g, d);
+                if (lane >= d) c += oc, g += og;
+            }
+            if (e < E) {
+                f.choices[e + 1] = choices + c;
+                f.groups[e + 1] = int16_t(groups + g);
+            }
+            choices += __shfl(c, 63);
+            groups += __shfl(g, 63);
+        }
+    }
+    __syncthreads();
 }
 
-// F: fragments of 16 tokens at a time; an expert with more reads its weights
-// again, from L2.  A wave has 16 rows of both halves and 1 / slices of D;
-// waves of one block of rows meet in LDS.
-//
-// Rows past H and tokens past the expert's are computed from rows that are
-// there, and not stored: a row's and a token's results depend on no other.
-template <class T, int TYPE, int F, int AHEAD>
-__global__ __launch_bounds__(WAVES * 64, 1) void up_kernel(LayerArgs a) {
+// XR: tokens of a workgroup at most.
+template <class T, int TYPE, int XR>
+__global__ __launch_bounds__(THREADS, 1) void up_kernel(LayerArgs a) {
+    using F = Form<TYPE>;
+    using X = Values<XR, F::RUN * 2>;
+    constexpr int STAGE = 4096 + X::SIZE + F::SCALE_BYTES, PER = 4 + X::LOADS + F::SCALES;
     const ExpertsLayer &p = a.p;
-    __shared__ Live live;
-    __shared__ int16_t token[LAYER_MAX_TOKENS], choice[LAYER_MAX_TOKENS];
-    __shared__ int count_shared;
-    __shared__ f32x4 part[WAVES][2][64];
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    __shared__ int16_t token[XR], choice[XR];
+    __shared__ float share[XR];
+    __shared__ int expert_shared;
+    LDS char *lds = (LDS char *)smem;
+    LDS float *part = reinterpret_cast<LDS float *>(lds + WAVES * a.ring_up * STAGE);  // [wave][half][q][token][4]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int slices = a.slices, per = WAVES / slices;  // blocks of 16 rows in a workgroup
-    const int groups = int((p.H + 16 * per - 1) / (16 * per));
-    const int n_live = find_live(a, live);
-    const int which = blockIdx.x / groups;
-    if (which >= n_live) return;
-    const int e = __builtin_amdgcn_readfirstlane(live.list[which]), k = int(p.top_k);
-    const int64_t h0 = (int64_t(blockIdx.x % groups) * per + wave / slices) * 16;
-    const int slice = wave % slices;
-    // the tokens that chose it, in rising order
+    const int k = int(p.top_k), E = int(p.experts);
+    const Found found(lds);  // where the runs will be
+    find(p, found, XR);
+    const int group = blockIdx.x / a.groups;
+    if (group >= found.groups[E]) return;
+    for (int i = threadIdx.x; i < E; i += THREADS)
+        if (found.groups[i] <= group && group < found.groups[i + 1]) expert_shared = i;
+    __syncthreads();
+    const int e = __builtin_amdgcn_readfirstlane(expert_shared);
+    const int skip = (group - found.groups[e]) * XR;  // choices of the expert's earlier groups
+    const int all = found.choices[e + 1] - found.choices[e];
+    const int count = __builtin_amdgcn_readfirstlane(all - skip < XR ? all - skip : XR);
+    // its tokens, by rising token
     if (wave == 0) {
-        const int c = lane < p.tokens ? choice_of(live, lane, k, e) : -1;
+        const int c = lane < p.tokens ? choice_of(found.ids, lane, k, e) : -1;
         const uint64_t mask = __ballot(c >= 0);
-        if (c >= 0) {
-            const int at = __popcll(mask & ((uint64_t(1) << lane) - 1));
+        const int at = __popcll(mask & ((uint64_t(1) << lane) - 1)) - skip;
+        if (c >= 0 && at >= 0 && at < XR) {
+            float w = 0.0f;
+            for (int j = c; j < k; ++j)
+                if (found.ids[lane * k + j] == e) w += p.weights[lane * k + j];
             token[at] = int16_t(lane);
             choice[at] = int16_t(c);
+            share[at] = w;
         }
-        if (lane == 0) count_shared = __popcll(mask);
     }
-    __syncthreads();
-    const int count = __builtin_amdgcn_readfirstlane(count_shared);
+    __syncthreads();  // the last read of what was found
     const int r = lane & 15, q = lane >> 4;
-    constexpr int ESZ = TYPE == 0 ? 2 : 1;
-    const int64_t first = h0 < p.H ? h0 : p.H - 1;
-    const int64_t row = first + r < p.H ? r : p.H - 1 - first;
-    const char *gate = uniform_pointer(static_cast<const char *>(p.up.w) + (e * p.up.stride + first * p.up.ld) * ESZ);
-    const char *mult = uniform_pointer(gate + p.H * p.up.ld * ESZ);
-    const uint32_t offset = uint32_t(row * p.up.ld * ESZ) + 16 * q;
-    // the 16 rows of the activated half lie in one block of 128, the others'
-    // (lo .. hi) in two where H is no multiple of 16
-    const int64_t last = h0 + 15 < p.H ? h0 + 15 : p.H - 1;
-    const int64_t in_gate = uniform(first / 128), in_lo = uniform((p.H + first) / 128), in_hi = uniform((p.H + last) / 128);
-    const int64_t in_first = in_hi * 128 - (p.H + h0);  // rows of the block of lo, where there are two
-    const float *scale = p.up.scale + e * p.up.stride_scale;
-    // Whole runs of weights and activations are on their way AHEAD runs before
-    // they are multiplied; past the last one the last is fetched again, so
-    // that nothing branches around a load.
-    Run<TYPE> ng[AHEAD], nm[AHEAD];
-    u32x4 nx[AHEAD][F][STEPS];
-    float sg[AHEAD], sm_lo[AHEAD], sm_hi[AHEAD];
-    uint32_t x[F];
-    const int whole = int(p.D / RUN), mine = (whole - slice + slices - 1) / slices;  // of the slice
-    const char *values = static_cast<const char *>(p.X);
-    auto fetch_scales = [&](int i, int64_t run) {
-        if (TYPE == 0) return;
-        const float *sc = scale + run * p.up.lds;
-        sg[i] = scalar_load(sc + in_gate);
-        sm_lo[i] = scalar_load(sc + in_lo);
-        sm_hi[i] = scalar_load(sc + in_hi);
-    };
-    auto fetch = [&](int i, int n) {
-        const int64_t run = slice + int64_t(n < mine ? n : mine - 1) * slices;
-        fetch_scales(i, run);
-        ng[i].fetch(gate + run * RUN * ESZ, offset);
-        nm[i].fetch(mult + run * RUN * ESZ, offset);
-#pragma unroll
-        for (int f = 0; f < F; ++f) fetch_values<TYPE>(nx[i][f], values + run * RUN * 2, x[f]);
-    };
-    for (int t0 = 0; t0 < count; t0 += 16 * F) {
-#pragma unroll
-        for (int f = 0; f < F; ++f) {
-            const int at = t0 + 16 * f + r;
-            x[f] = uint32_t(token[at < count ? at : 0] * p.ldx * 2) + lane_bytes<TYPE>(q);
+    const int64_t first_block = int64_t(blockIdx.x % a.groups) * a.blocks, all_blocks = (p.H + 15) / 16;
+    const int blocks = int(all_blocks - first_block < a.blocks ? all_blocks - first_block : a.blocks);
+    X x;
+    x.init(lane, [&](int row) { return uint32_t(token[row < count ? row : 0] * p.ldx * 2); });
+    const int64_t runs = (p.D + F::RUN - 1) / F::RUN;
+    const int mine = int((runs - wave + WAVES - 1) / WAVES);  // runs of each block
+    const char *up = static_cast<const char *>(p.up.w) + e * p.up.stride * F::ESZ;
+    Rows<TYPE> rows;
+    // items are (block, run) in turn; what is to be issued next
+    int issued = 0, issue_block = 0, issue_run = 0;
+    const int items = blocks * mine;
+    auto issue = [&]() {
+        const int64_t h0 = (first_block + issue_block) * 16, run = wave + int64_t(issue_run) * WAVES;
+        if (issue_run == 0) rows.init(p.up.ld, p.H - h0, lane);
+        const int64_t k0 = run * F::RUN, left = p.D - k0;
+        const char *gate = up + (h0 * p.up.ld + k0) * F::ESZ;
+        const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) + (wave * a.ring_up + issued % a.ring_up) * STAGE;
+        rows.issue(gate, to, left);
+        rows.issue(gate + p.H * p.up.ld * F::ESZ, to + 2048, left);
+        x.issue(static_cast<const uint16_t *>(p.X) + k0, to + 4096, [&](int c) { return c * 8 < left; });
+        if (TYPE != 0) {
+            // lanes 0, 1, 2: of the activated half's rows, which lie in one
+            // block of 128, and of the first and last of the others', which
+            // lie in two where H is no multiple of 16
+            const int64_t last = h0 + 15 < p.H ? h0 + 15 : p.H - 1;
+            const int64_t at = lane == 0 ? h0 / 128 : (p.H + (lane == 1 ? h0 : last)) / 128;
+            dma::direct_load4(buffer_at(p.up.scale + e * p.up.stride_scale + run * p.up.lds), to + 4096 + X::SIZE, uint32_t(at * 4));
         }
-        f32x4 g[F], m[F];
+        ++issued;
+        if (++issue_run == mine) issue_run = 0, ++issue_block;
+    };
+    for (int i = 0; i < a.ring_up && i < items; ++i) issue();
+    int done = 0;
+    for (int b = 0; b < blocks; ++b) {
+        const int64_t h0 = (first_block + b) * 16, last = h0 + 15 < p.H ? h0 + 15 : p.H - 1;
+        const int in_first = int((p.H + last) / 128 * 128 - (p.H + h0));  // the others' rows of the first of two blocks
+        f32x4 g = {0, 0, 0, 0}, m = {0, 0, 0, 0};
+        for (int i = 0; i < mine; ++i, ++done) {
+            const int64_t left = p.D - (wave + int64_t(i) * WAVES) * F::RUN;
+            wait_for<PER>(issued - 1 - done);
+            const LDS char *stage = lds + (wave * a.ring_up + done % a.ring_up) * STAGE;
+            u32x4 og[F::STEPS], om[F::STEPS], xv[F::STEPS];
 #pragma unroll
-        for (int f = 0; f < F; ++f) g[f] = f32x4{0, 0, 0, 0}, m[f] = f32x4{0, 0, 0, 0};
-        // sums of one run (part: its `left` values) added to g and m
-        auto multiply = [&](int i, bool part, int left) {
-            f32x4 bg[F], bm[F];
-#pragma unroll
-            for (int f = 0; f < F; ++f) {
-                bg[f] = TYPE == 0 ? g[f] : f32x4{0, 0, 0, 0};
-                bm[f] = TYPE == 0 ? m[f] : f32x4{0, 0, 0, 0};
+            for (int s = 0; s < F::STEPS; ++s) {
+                og[s] = Rows<TYPE>::template operand<T>(stage, s, r, q);
+                om[s] = Rows<TYPE>::template operand<T>(stage + 2048, s, r, q);
+                // columns past the group's tokens are not stored
+                xv[s] = X::at(stage + 4096, r % XR, k_of<TYPE>(s, q) / 8);
             }
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                const u32x4 og = part ? ng[i].template operand_part<T>(s, left, q) : ng[i].template operand<T>(s);
-                const u32x4 om = part ? nm[i].template operand_part<T>(s, left, q) : nm[i].template operand<T>(s);
-#pragma unroll
-                for (int f = 0; f < F; ++f) {
-                    bg[f] = mfma16<T>(og, nx[i][f][s], bg[f]);
-                    bm[f] = mfma16<T>(om, nx[i][f][s], bm[f]);
-                }
+            float sg = 1.0f, s_lo = 1.0f, s_hi = 1.0f;
+            if (TYPE != 0) {
+                const LDS float *sc = reinterpret_cast<const LDS float *>(stage + 4096 + X::SIZE);
+                sg = sc[0];
+                s_lo = sc[1];
+                s_hi = sc[2];
             }
+            wait_lgkmcnt0();
+            asm volatile("" ::: "memory");
+            if (issued < items) issue();
+            if (left < F::RUN)
 #pragma unroll
-            for (int f = 0; f < F; ++f) {
-                if (TYPE == 0) {
-                    g[f] = bg[f];
-                    m[f] = bm[f];
-                    continue;
+                for (int s = 0; s < F::STEPS; ++s) {
+                    cut(og[s], k_of<TYPE>(s, q), int(left));
+                    cut(om[s], k_of<TYPE>(s, q), int(left));
+                    cut(xv[s], k_of<TYPE>(s, q), int(left));
                 }
+            f32x4 bg = TYPE == 0 ? g : f32x4{0, 0, 0, 0}, bm = TYPE == 0 ? m : f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int s = 0; s < F::STEPS; ++s) {
+                bg = mfma16<T>(og[s], xv[s], bg);
+                bm = mfma16<T>(om[s], xv[s], bm);
+            }
+            if (TYPE == 0) {
+                g = bg;
+                m = bm;
+            } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float mult_scale = 4 * q + j < in_first ? sm_lo[i] : sm_hi[i];
-                    g[f][j] = __builtin_fmaf(sg[i], bg[f][j], g[f][j]);
-                    m[f][j] = __builtin_fmaf(mult_scale, bm[f][j], m[f][j]);
+                    g[j] = __builtin_fmaf(sg, bg[j], g[j]);
+                    m[j] = __builtin_fmaf(4 * q + j < in_first ? s_lo : s_hi, bm[j], m[j]);
                 }
             }
-        };
-        if (mine > 0) {
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) fetch(i, i);
-            int n = 0;
-            for (; n + AHEAD <= mine; n += AHEAD)
-#pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
-                    multiply(i, false, RUN);
-                    fetch(i, n + i + AHEAD);
-                }
-#pragma unroll
-            for (int i = 0; i < AHEAD - 1; ++i)
-                if (n + i < mine) multiply(i, false, RUN);
         }
-        if (const int left = int(p.D % RUN); left != 0 && slice == whole % slices) {
-            fetch_scales(0, whole);
-            ng[0].fetch_part(gate + int64_t(whole) * RUN * ESZ, offset, left, q);
-            nm[0].fetch_part(mult + int64_t(whole) * RUN * ESZ, offset, left, q);
-#pragma unroll
-            for (int f = 0; f < F; ++f) fetch_values_part<TYPE>(nx[0][f], values + int64_t(whole) * RUN * 2, x[f], left, q);
-            multiply(0, true, left);
+        // the waves' sums: lane l has rows h0 + 4(l / 16) + 0..3 of token l % 16
+        if (r < XR) {
+            *reinterpret_cast<LDS f32x4 *>(part + (wave * 2 + 0) * (16 * XR) + (q * XR + r) * 4) = g;
+            *reinterpret_cast<LDS f32x4 *>(part + (wave * 2 + 1) * (16 * XR) + (q * XR + r) * 4) = m;
         }
-        // a lane's registers: rows h0 + 4q + 0..3 of token r
+        __syncthreads();
+        const int at = (threadIdx.x / 4) % XR, j = threadIdx.x / (4 * XR) * 4 + threadIdx.x % 4;
+        if (threadIdx.x < 16 * XR && at < count) {
+            float v[1] = {0.0f}, o = 0.0f;
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-            if (t0 + 16 * f >= count) break;
-            if (slices > 1) {
-                if (t0 + f > 0) __syncthreads();
-                part[wave][0][lane] = g[f];
-                part[wave][1][lane] = m[f];
-                __syncthreads();
-                if (slice == 0)
-                    for (int w = 1; w < slices; ++w) {
-                        const f32x4 og = part[wave + w][0][lane], om = part[wave + w][1][lane];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) g[f][j] += og[j], m[f][j] += om[j];
-                    }
+            for (int w = 0; w < WAVES; ++w) {
+                v[0] += part[(w * 2 + 0) * (16 * XR) + threadIdx.x];
+                o += part[(w * 2 + 1) * (16 * XR) + threadIdx.x];
             }
-            const int at = t0 + 16 * f + r;
-            if (slice != 0 || at >= count || h0 + 4 * q >= a.ldh) continue;
-            const int t = token[at];
-            float w = 0.0f;
-            for (int j = choice[at]; j < k; ++j)
-                if (live.ids[t * k + j] == e) w += p.weights[t * k + j];
-            float v[4] = {g[f][0], g[f][1], g[f][2], g[f][3]};
             act::apply(p.act, v);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = h0 + 4 * q + j < p.H ? v[j] * m[f][j] * w : 0.0f;
-                hi[j] = encode<T>(v[j]);
-                lo[j] = encode<T>(v[j] - decode<T>(hi[j]));
-            }
-            uint16_t *h = a.h + (t * k + choice[at]) * 2 * a.ldh + h0 + 4 * q;
-            *reinterpret_cast<u32x2 *>(h) = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
-            *reinterpret_cast<u32x2 *>(h + a.ldh) = u32x2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
+            const float wh = h0 + j < p.H ? v[0] * o * share[at] : 0.0f;
+            const uint32_t hi = encode<T>(wh);
+            uint16_t *h = a.h + (token[at] * k + choice[at]) * a.ldh + (h0 + j) / F::RUN * (2 * F::RUN) + (h0 + j) % F::RUN;
+            h[0] = uint16_t(hi);
+            h[F::RUN] = uint16_t(encode<T>(wh - decode<T>(hi)));
         }
+        __syncthreads();
     }
 }
 
-// A workgroup has 16 of y's columns; its waves deal (live expert, run of H)
-// pairs.  A pair's tokens are those of the expert, 16 to a fragment; their
-// sums are added to the tokens' in the wave's own part of LDS.
-template <class T, int TYPE, int AHEAD>
-__global__ __launch_bounds__(WAVES * 64, 1) void down_kernel(LayerArgs a) {
+// A workgroup has 16 of y's columns; its waves deal (group of up to DT of an
+// expert's choices, run of H) pairs.  A pair's sums are added to the tokens'
+// in the wave's own part of LDS.
+template <class T, int TYPE, int DT>
+__global__ __launch_bounds__(THREADS, 1) void down_kernel(LayerArgs a) {
+    using F = Form<TYPE>;
+    using V = Values<DT, F::RUN * 4>;  // both pieces
+    constexpr int STAGE = 2048 + V::SIZE + F::SCALE_BYTES, PER = 2 + V::LOADS + F::SCALES;
     const ExpertsLayer &p = a.p;
-    __shared__ Live live;
-    __shared__ uint8_t token[MOST_SLOTS];  // by live expert
-    __shared__ uint16_t slot[MOST_SLOTS];  // token * top_k + choice
-    __shared__ int16_t start[LAYER_MAX_EXPERTS + 1];
-    extern __shared__ __attribute__((aligned(16))) char smem[];
-    f32x4 *sums = reinterpret_cast<f32x4 *>(smem);  // [wave][token][four columns]
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    LDS char *lds = (LDS char *)smem;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int k = int(p.top_k), tokens = int(p.tokens);
-    const int n_live = find_live(a, live);
-    const int r = lane & 15, q = lane >> 4;
-    // the first choices of each live expert, by rising token
-    for (int i = wave; i < n_live; i += WAVES) {
-        const uint64_t mask = __ballot(lane < tokens && choice_of(live, lane, k, live.list[i]) >= 0);
-        if (lane == 0) start[i + 1] = int16_t(__popcll(mask));
-    }
-    for (int i = threadIdx.x; i < WAVES * tokens * 4; i += WAVES * 64) sums[i] = f32x4{0, 0, 0, 0};
-    __syncthreads();
-    if (wave == 0) {
-        int base = 0;
-        for (int i0 = 0; i0 < n_live; i0 += 64) {
-            int v = i0 + lane < n_live ? start[i0 + lane + 1] : 0;
-            for (int d = 1; d < 64; d *= 2) {
-                const int o = __shfl_up(v, d);
-                if (lane >= d) v += o;
-            }
-            if (i0 + lane < n_live) start[i0 + lane + 1] = int16_t(base + v);
-            base += __shfl(v, 63);
-        }
-        if (lane == 0) start[0] = 0;
-    }
-    __syncthreads();
-    for (int i = wave; i < n_live; i += WAVES) {
-        const int c = lane < tokens ? choice_of(live, lane, k, live.list[i]) : -1;
+    const int k = int(p.top_k), tokens = int(p.tokens), E = int(p.experts), slots = tokens * k;
+    // behind the runs: the tokens' sums [wave][token][16], and by group its
+    // expert, where its choices start and (one more) end; by choice its place
+    LDS f32x4 *sums = reinterpret_cast<LDS f32x4 *>(lds + WAVES * a.ring_down * STAGE);
+    LDS int16_t *expert = reinterpret_cast<LDS int16_t *>(sums + WAVES * tokens * 4);
+    LDS int16_t *start = expert + slots, *place = start + slots + 1;
+    const Found found(lds);  // where the runs will be
+    find(p, found, DT);
+    const int groups = __builtin_amdgcn_readfirstlane(found.groups[E]);
+    for (int i = threadIdx.x; i < WAVES * tokens * 4; i += THREADS) sums[i] = f32x4{0, 0, 0, 0};
+    for (int e = wave; e < E; e += WAVES) {
+        const int g0 = found.groups[e], g1 = found.groups[e + 1], c0 = found.choices[e];
+        if (g0 == g1) continue;
+        const int c = lane < tokens ? choice_of(found.ids, lane, k, e) : -1;
         const uint64_t mask = __ballot(c >= 0);
-        if (c >= 0) {
-            const int at = start[i] + __popcll(mask & ((uint64_t(1) << lane) - 1));
-            token[at] = uint8_t(lane);
-            slot[at] = uint16_t(lane * k + c);
+        if (c >= 0) place[c0 + __popcll(mask & ((uint64_t(1) << lane) - 1))] = int16_t(lane * k + c);
+        if (lane < g1 - g0) {
+            expert[g0 + lane] = int16_t(e);
+            start[g0 + lane] = int16_t(c0 + lane * DT);
         }
     }
-    __syncthreads();
+    if (threadIdx.x == 0) start[groups] = int16_t(found.choices[E]);
+    __syncthreads();  // the last read of what was found
+    const int r = lane & 15, q = lane >> 4;
     const int64_t d0 = int64_t(blockIdx.x) * 16;
-    constexpr int ESZ = TYPE == 0 ? 2 : 1;
-    const int64_t row = d0 + r < p.D ? r : p.D - 1 - d0;  // rows past D: the last one's, not stored
-    const char *down = static_cast<const char *>(p.down.w) + d0 * p.down.ld * ESZ;
-    const uint32_t offset = uint32_t(row * p.down.ld * ESZ) + 16 * q;
-    const int runs = int(p.H / RUN), units = n_live * runs;  // whole runs
-    // Weights, and the pieces of w h of a unit's first tokens, are fetched
-    // AHEAD units before they are multiplied; pieces fetched later than the
-    // weights would wait for all weights asked for before.  Past the last unit
-    // the last is fetched again, so that nothing branches around a load.
+    const char *down = static_cast<const char *>(p.down.w) + d0 * p.down.ld * F::ESZ;
+    Rows<TYPE> rows;
+    rows.init(p.down.ld, p.D - d0, lane);
+    const int runs = int((p.H + F::RUN - 1) / F::RUN), units = groups * runs;
+    const int on_group = WAVES / runs, on_run = WAVES % runs;
     struct Unit {
-        int expert, run, first, end;  // first .. end: its slots
+        int group, run;
     };
-    Run<TYPE> next[AHEAD];
-    Unit unit[AHEAD];
-    float next_scale[AHEAD];
-    u32x4 hi[AHEAD][STEPS], lo[AHEAD][STEPS];
-    // token r of the slots from `from` on; past the expert's, its first one
-    // there, which is not added to a sum
-    auto pieces_at = [&](const Unit &u, int from) {
-        return uint32_t(slot[from + r < u.end ? from + r : from] * 4 * a.ldh) + lane_bytes<TYPE>(q);
+    auto advance = [&](Unit &u) {
+        u.group += on_group;
+        u.run += on_run;
+        if (u.run >= runs) u.run -= runs, ++u.group;
     };
-    auto pieces_base = [&](const Unit &u) { return reinterpret_cast<const char *>(a.h + int64_t(u.run) * RUN); };
-    auto fetch_h = [&](int i, const Unit &u, int from) {
-        const uint32_t at = pieces_at(u, from);
-        fetch_values<TYPE>(hi[i], pieces_base(u), at);
-        fetch_values<TYPE>(lo[i], pieces_base(u) + 2 * a.ldh, at);
-    };
-    auto weights_base = [&](const Unit &u) {
-        const int e = __builtin_amdgcn_readfirstlane(live.list[u.expert]);
-        return down + (e * p.down.stride + int64_t(u.run) * RUN) * ESZ;
-    };
-    auto fetch_scale = [&](int i, const Unit &u) {
-        if (TYPE == 0) return;
-        const int e = __builtin_amdgcn_readfirstlane(live.list[u.expert]);
+    Unit next{wave / runs, wave % runs}, now = next;
+    const int items = units > wave ? (units - wave + WAVES - 1) / WAVES : 0;
+    int issued = 0;
+    auto issue = [&]() {
+        const int e = __builtin_amdgcn_readfirstlane(expert[next.group]);
+        const int first = start[next.group], end = start[next.group + 1];
+        const int64_t left = p.H - int64_t(next.run) * F::RUN;
+        const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) + (wave * a.ring_down + issued % a.ring_down) * STAGE;
+        rows.issue(down + (e * p.down.stride + int64_t(next.run) * F::RUN) * F::ESZ, to, left);
+        V v;
+        // past the group's choices, its first one's, not added to a sum
+        v.init(lane, [&](int row) { return uint32_t(place[first + row < end ? first + row : first] * int(a.ldh * 2)); });
+        // chunks of eight in each piece, as far as the rows go
+        v.issue(a.h + int64_t(next.run) * (2 * F::RUN), to + 2048, [&](int c) { return c % (F::RUN / 8) * 8 < left; });
         // 16 rows from a multiple of 16 lie in one block of 128
-        next_scale[i] = scalar_load(p.down.scale + e * p.down.stride_scale + u.run * p.down.lds + d0 / 128);
+        if (TYPE != 0)
+            dma::direct_load4(buffer_at(p.down.scale + e * p.down.stride_scale + next.run * p.down.lds + d0 / 128),
+                              to + 2048 + V::SIZE, 0);
+        ++issued;
+        advance(next);
     };
-    auto unit_of = [&](int expert, int run) {
-        return Unit{expert, run, __builtin_amdgcn_readfirstlane(start[expert]), __builtin_amdgcn_readfirstlane(start[expert + 1])};
-    };
-    // the sums of the 16 slots from s0 on, added to their tokens'
-    auto multiply = [&](int i, const u32x4 (&od)[STEPS], const Unit &u, int s0) {
+    for (int i = 0; i < a.ring_down && i < items; ++i) issue();
+    for (int done = 0; done < items; ++done) {
+        const int first = start[now.group], end = start[now.group + 1];
+        const int64_t left = p.H - int64_t(now.run) * F::RUN;
+        const int t = place[first + r < end ? first + r : first] / k;
+        wait_for<PER>(issued - 1 - done);
+        const LDS char *stage = lds + (wave * a.ring_down + done % a.ring_down) * STAGE;
+        u32x4 od[F::STEPS], hi[F::STEPS], lo[F::STEPS];
+#pragma unroll
+        for (int s = 0; s < F::STEPS; ++s) {
+            od[s] = Rows<TYPE>::template operand<T>(stage, s, r, q);
+            hi[s] = V::at(stage + 2048, r % DT, k_of<TYPE>(s, q) / 8);
+            lo[s] = V::at(stage + 2048, r % DT, F::RUN / 8 + k_of<TYPE>(s, q) / 8);
+        }
+        const float scale = TYPE == 0 ? 1.0f : *reinterpret_cast<const LDS float *>(stage + 2048 + V::SIZE);
+        wait_lgkmcnt0();
+        asm volatile("" ::: "memory");
+        if (issued < items) issue();
+        // up_kernel has filled the pieces' last chunks with zeros
+        if (left < F::RUN)
+#pragma unroll
+            for (int s = 0; s < F::STEPS; ++s) cut(od[s], k_of<TYPE>(s, q), int(left));
         f32x4 block = {0, 0, 0, 0};
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            block = mfma16<T>(od[s], lo[i][s], block);
-            block = mfma16<T>(od[s], hi[i][s], block);
+        for (int s = 0; s < F::STEPS; ++s) {
+            block = mfma16<T>(od[s], lo[s], block);
+            block = mfma16<T>(od[s], hi[s], block);
         }
-        if (s0 + r >= u.end) return;
-        f32x4 *sum = sums + (wave * tokens + token[s0 + r]) * 4 + q;
-        f32x4 v = *sum;
-        const float scale = TYPE == 0 ? 1.0f : next_scale[i];
+        if (r < DT && first + r < end) {
+            LDS f32x4 *sum = sums + (wave * tokens + t) * 4 + q;
+            f32x4 v = *sum;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(scale, block[j], v[j]);
-        *sum = v;
-    };
-    if (wave < units) {
-        // the unit to fetch, and how far eight units are
-        const int on_expert = WAVES / runs, on_run = WAVES % runs;
-        int expert = wave / runs, run = wave % runs, at = wave;
-        auto fetch = [&](int i) {
-            unit[i] = unit_of(expert, run);
-            next[i].fetch(weights_base(unit[i]), offset);
-            fetch_scale(i, unit[i]);
-            fetch_h(i, unit[i], unit[i].first);
-            if (at + WAVES >= units) return;
-            at += WAVES;
-            expert += on_expert;
-            run += on_run;
-            if (run >= runs) run -= runs, ++expert;
-        };
-        auto step = [&](int i) {
-            u32x4 od[STEPS];
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) od[s] = next[i].template operand<T>(s);
-            const Unit u = unit[i];
-            multiply(i, od, u, u.first);
-            for (int s0 = u.first + 16; s0 < u.end; s0 += 16) {
-                fetch_h(i, u, s0);
-                multiply(i, od, u, s0);
-            }
-        };
-        const int mine = (units - wave + WAVES - 1) / WAVES;
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) fetch(i);
-        int n = 0;
-        for (; n + AHEAD <= mine; n += AHEAD)
-#pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                step(i);
-                fetch(i);
-            }
-#pragma unroll
-        for (int i = 0; i < AHEAD - 1; ++i)
-            if (n + i < mine) step(i);
+            for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(scale, block[j], v[j]);
+            *sum = v;
+        }
+        advance(now);
     }
-    if (const int left = int(p.H % RUN); left != 0)
-        for (int i = wave; i < n_live; i += WAVES) {
-            const Unit u = unit_of(i, runs);
-            next[0].fetch_part(weights_base(u), offset, left, q);
-            fetch_scale(0, u);
-            u32x4 od[STEPS];
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) od[s] = next[0].template operand_part<T>(s, left, q);
-            for (int s0 = u.first; s0 < u.end; s0 += 16) {
-                const uint32_t at = pieces_at(u, s0);
-                fetch_values_part<TYPE>(hi[0], pieces_base(u), at, left, q);
-                fetch_values_part<TYPE>(lo[0], pieces_base(u) + 2 * a.ldh, at, left, q);
-                multiply(0, od, u, s0);
-            }
-        }
     __syncthreads();
-    for (int i = threadIdx.x; i < tokens * 16; i += WAVES * 64) {
+    for (int i = threadIdx.x; i < tokens * 16; i += THREADS) {
         const int t = i / 16;
         const int64_t d = d0 + i % 16, at = t * p.ldy + d;
         if (d >= p.D) continue;
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) s += reinterpret_cast<const float *>(sums)[w * tokens * 16 + i];
+        for (int w = 0; w < WAVES; ++w) s += reinterpret_cast<const LDS float *>(sums)[w * tokens * 16 + i];
         if (p.out == 0) {
             float *y = static_cast<float *>(p.Y) + at;
             *y = p.beta != 0.0f ? __builtin_fmaf(p.beta, *y, s) : s;
@@ -547,38 +516,66 @@ __global__ __launch_bounds__(WAVES * 64, 1) void down_kernel(LayerArgs a) {
     }
 }
 
+// ---------------------------------------------------------------- host
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 
-// Waves that share 16 rows: as many (1, 2, 4, 8) as it takes for 16 waves on
-// each of 256 compute units when every slot has an expert of its own.
-int up_slices(int64_t live, int64_t H) {
-    const int64_t blocks = live * ceil_div(H, 16);
-    int s = 1;
-    while (s < WAVES && blocks * s < 4096) s *= 2;
-    return s;
+constexpr int MOST_LDS = 160 * 1024;
+static_assert(4 * (LAYER_MAX_EXPERTS + 1) + 2 * (LAYER_MAX_EXPERTS + 1) + 2 * LAYER_MAX_TOKENS * LAYER_MAX_TOP_K <= WAVES * 2 * 4096,
+              "what is found fits where the runs will be");
+
+// Stages of the ring: up to four, as many as fit.
+int ring_of(int64_t stage, int64_t beside) { return int(least(4, (MOST_LDS - 1024 - beside) / (WAVES * stage))); }
+
+template <class K>
+hipError_t allow_lds(K kernel, size_t bytes) {
+    if (bytes <= 64 * 1024) return hipSuccess;
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, MOST_LDS - 1024);
 }
 
-#ifndef UP_AHEAD
-#define UP_AHEAD 2
-#endif
-#ifndef DOWN_AHEAD
-#define DOWN_AHEAD 3
-#endif
-template <class T, int TYPE, int F>
-hipError_t run(LayerArgs &a, hipStream_t stream) {
-    a.slices = up_slices(a.live_most, a.p.H);
-    const int64_t up = a.live_most * ceil_div(a.p.H, 16 * (WAVES / a.slices));
-    if (up > 0x7fffff || ceil_div(a.p.D, 16) > 0x7fffff) return hipErrorInvalidConfiguration;
-    up_kernel<T, TYPE, F, UP_AHEAD><<<dim3(unsigned(up)), dim3(WAVES * 64), 0, stream>>>(a);
-    const hipError_t e = hipGetLastError();
+template <class T, int TYPE, int XR>
+hipError_t run_up(LayerArgs &a, hipStream_t stream) {
+    const ExpertsLayer &p = a.p;
+    constexpr int64_t stage = 4096 + XR * Form<TYPE>::RUN * 2 + Form<TYPE>::SCALE_BYTES, part = WAVES * 2 * 64 * XR;
+    a.ring_up = ring_of(stage, part);
+    const size_t lds = size_t(WAVES * a.ring_up * stage + part);
+    hipError_t e = allow_lds(up_kernel<T, TYPE, XR>, lds);
     if (e != hipSuccess) return e;
-    down_kernel<T, TYPE, DOWN_AHEAD><<<dim3(unsigned(ceil_div(a.p.D, 16))), dim3(WAVES * 64), size_t(WAVES * a.p.tokens * 64), stream>>>(a);
+    // groups of tokens at most; blocks so that there are about 1024 workgroups
+    const int64_t slots = p.tokens * p.top_k, groups = least(slots, least(p.experts, slots) + slots / XR);
+    const int64_t all_blocks = ceil_div(p.H, 16), blocks = groups * all_blocks / 1024;
+    a.blocks = int(blocks < 1 ? 1 : least(blocks, 8));
+    a.groups = int(ceil_div(all_blocks, a.blocks));
+    if (groups * a.groups > 0x7fffff) return hipErrorInvalidConfiguration;
+    up_kernel<T, TYPE, XR><<<dim3(unsigned(groups * a.groups)), dim3(THREADS), lds, stream>>>(a);
     return hipGetLastError();
 }
-// Two fragments at a time where an expert has more than eight tokens in the mean.
+template <class T, int TYPE, int DT>
+hipError_t run_down(LayerArgs &a, hipStream_t stream) {
+    const ExpertsLayer &p = a.p;
+    constexpr int64_t stage = 2048 + DT * Form<TYPE>::RUN * 4 + Form<TYPE>::SCALE_BYTES;
+    const int64_t beside = WAVES * p.tokens * 64 + (3 * p.tokens * p.top_k + 1) * 2;
+    a.ring_down = ring_of(stage, beside);
+    const size_t lds = size_t(WAVES * a.ring_down * stage + beside);
+    hipError_t e = allow_lds(down_kernel<T, TYPE, DT>, lds);
+    if (e != hipSuccess) return e;
+    if (ceil_div(p.D, 16) > 0x7fffff) return hipErrorInvalidConfiguration;
+    down_kernel<T, TYPE, DT><<<dim3(unsigned(ceil_div(p.D, 16))), dim3(THREADS), lds, stream>>>(a);
+    return hipGetLastError();
+}
+// A group of tokens more reads the weights again, from L2; room for more
+// leaves less of LDS for the weights on their way.
 template <class T, int TYPE>
 hipError_t run_tokens(LayerArgs &a, hipStream_t stream) {
-    return a.p.tokens > 16 && a.p.tokens * a.p.top_k > 8 * a.p.experts ? run<T, TYPE, 2>(a, stream) : run<T, TYPE, 1>(a, stream);
+    const ExpertsLayer &p = a.p;
+    a.ldh = ceil_div(p.H, Form<TYPE>::RUN) * 2 * Form<TYPE>::RUN;
+    const int64_t slots = p.tokens * p.top_k;
+    const hipError_t e = p.tokens > 8 && slots > 5 * p.experts ? run_up<T, TYPE, 16>(a, stream) : run_up<T, TYPE, 8>(a, stream);
+    if (e != hipSuccess) return e;
+#ifndef DOWN_FEW
+#define DOWN_FEW 5
+#endif
+    return p.tokens <= 4 || slots < DOWN_FEW * p.experts ? run_down<T, TYPE, 4>(a, stream) : run_down<T, TYPE, 8>(a, stream);
 }
 template <class T>
 hipError_t run_type(LayerArgs &a, hipStream_t stream) {
@@ -589,12 +586,13 @@ hipError_t run_type(LayerArgs &a, hipStream_t stream) {
 }  // namespace
 
 size_t experts_layer_workspace(int64_t tokens, int64_t, int64_t top_k, int64_t, int64_t H) {
-    return size_t(tokens * top_k * 2 * ceil_div(H, 8) * 8 * 2 + 16);
+    return size_t(tokens * top_k * 2 * ceil_div(H, 128) * 128 * 2 + 16);
 }
 
 hipError_t launch_experts_layer(const ExpertsLayer &p, hipStream_t stream) {
-    LayerArgs a{p, static_cast<uint16_t *>(p.workspace), ceil_div(p.H, 8) * 8,
-                int(p.experts < p.tokens * p.top_k ? p.experts : p.tokens * p.top_k), 1};
+    LayerArgs a{};
+    a.p = p;
+    a.h = static_cast<uint16_t *>(p.workspace);
     return p.in == 1 ? run_type<BF16>(a, stream) : run_type<F16>(a, stream);
 }
 

@@ -298,6 +298,8 @@ gemm_status_t gemm_experts_layer(int64_t tokens, int64_t experts, int64_t top_k,
                 rg = bytes_at(weights, tokens * top_k * 4);
     if (meets(ry, {rx, ru, rsu, rdn, rsd, rw, ri, rg}) || meets(rw, {rx, ru, rsu, rdn, rsd, ri, rg}))
         return GEMM_ERR_INVALID_ARG;
+    // offsets inside a workgroup's rows are 32-bit
+    if (ldx > (1 << 23) || ld_up > (1 << 25) || ld_down > (1 << 25) || H > (1 << 17)) return GEMM_ERR_UNSUPPORTED;
     ExpertsLayer p{tokens, experts, top_k, D, H, X, ldx, int(in), ids, weights, int(type), wu, wd, int(act), beta,
                    Y, ldy, int(typeY), workspace};
     return status_of(launch_experts_layer(p, stream));

@@ -172,11 +172,12 @@ size_t gemm_experts_layer_workspace_size(int64_t tokens, int64_t experts, int64_
  *   Y        tokens x D of typeY (X's type or fp32), ldy >= D; beta == 0 does
  *            not read it.  A token without experts gets beta * Y.
  *   workspace   gemm_experts_layer_workspace_size() bytes.
- * Sums are fp32, h is kept in fp32 and enters the second product as two
- * pieces of X's type, which hold 16 of its 24 bits in bf16 and 22 in fp16 (an
- * h beyond fp16's largest value, 65504, is infinite there).
+ * Sums are fp32; w h is formed in fp32 and enters the second product as two
+ * pieces of X's type, which hold 16 of its 24 bits in bf16 and 22 in fp16 (one
+ * beyond the type's largest value, 65504 in fp16, gives infinities or NaN).
  * At most GEMM_LAYER_MAX_TOKENS tokens, _EXPERTS experts and _TOP_K choices
- * (GEMM_ERR_UNSUPPORTED beyond: gemm_experts_f8 takes more tokens). */
+ * (GEMM_ERR_UNSUPPORTED beyond: gemm_experts_f8 takes more tokens); H at most
+ * 2^17, ldx 2^23, ld_up and ld_down 2^25. */
 gemm_status_t gemm_experts_layer(int64_t tokens, int64_t experts, int64_t top_k, int64_t D,
                                  int64_t H, const void *X, int64_t ldx, gemm_input_t in,
                                  const int32_t *ids, const float *weights, gemm_weights_t type,
