@@ -1,9 +1,9 @@
 // A whole layer of experts for a few tokens (gemm_experts_layer), in two
 // kernels that read the live experts' weights once.
 //
-//   up_kernel    w h, h = act(Up[0 .. H) x) * (Up[H .. 2H) x): a workgroup has an
-//                expert, up to XR of the tokens that chose it, and some
-//                blocks of 16 of H's rows, both halves.  w h leaves as two
+//   up_kernel    w h, h = act(Up[0 .. H) x) * (Up[H .. 2H) x): a workgroup takes
+//                blocks of 16 of H's rows, both halves, of an expert, for up
+//                to XR of the tokens that chose it.  w h leaves as two
 //                16-bit pieces, hi + lo, so it is not rounded to 16 bits in
 //                between;
 //   down_kernel  y = sum over the token's experts of Down (w h): a workgroup
@@ -54,8 +54,6 @@ struct LayerArgs {
     uint16_t *h;
     int64_t ldh;  // elements of a choice
     int ring_up, ring_down;
-    int blocks;  // of 16 rows in a workgroup of up_kernel
-    int groups;  // workgroups per expert and tokens
 };
 
 template <class T>
@@ -104,8 +102,19 @@ __device__ inline void cut(u32x4 &w, int k, int K) {
         if (k + e >= K) w[e / 2] &= e % 2 ? 0xffffu : 0xffff0000u;
 }
 
+// p is the same in the whole wave.
 __device__ inline u32x4 buffer_at(const void *p) {
     return dma::raw_buffer(static_cast<uint64_t>(uniform(reinterpret_cast<int64_t>(p))), 0x7fffffff);
+}
+// direct_load16 from `soffset` bytes further on: a run's place in its rows,
+// without a descriptor of its own.
+__device__ inline void direct_load16_at(u32x4 rs, uint32_t lds, uint32_t voffset, uint32_t soffset) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "buffer_load_dwordx4 %1, %2, %3 offen lds"
+        :
+        : "s"(lds), "v"(voffset), "s"(rs), "s"(soffset)
+        : "memory", "m0");
 }
 
 // 16 rows of a run of weights in LDS: 128 bytes per row, chunk c of row r at
@@ -124,10 +133,15 @@ struct Rows {
             chunk[j] = c * Form<TYPE>::PER;
         }
     }
-    __device__ void issue(const char *base, uint32_t to, int64_t left) const {
-        const u32x4 rs = buffer_at(base);
+    // left: values from the run's first one
+    __device__ void issue(u32x4 rs, uint32_t soffset, uint32_t to, int left) const {
+        if (left >= Form<TYPE>::RUN) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) direct_load16(rs, to + j * 1024, chunk[j] < left ? voff[j] : OOB);
+            for (int j = 0; j < 2; ++j) direct_load16_at(rs, to + j * 1024, voff[j], soffset);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) direct_load16_at(rs, to + j * 1024, chunk[j] < left ? voff[j] : OOB, soffset);
+        }
     }
     template <class T>
     static __device__ u32x4 operand(const LDS char *at, int s, int r, int q) {
@@ -159,12 +173,16 @@ struct Values {
             voff[j] = start(r) + c * 16;
         }
     }
-    // live(c): whether chunk c is read; others are zeros
+    // whole: every chunk is read; else those of which live(c), others are zeros
     template <class F>
-    __device__ void issue(const void *base, uint32_t to, F &&live) const {
-        const u32x4 rs = buffer_at(base);
+    __device__ void issue(u32x4 rs, uint32_t soffset, uint32_t to, bool whole, F &&live) const {
+        if (whole) {
 #pragma unroll
-        for (int j = 0; j < LOADS; ++j) direct_load16(rs, to + j * 1024, live(chunk[j]) ? voff[j] : OOB);
+            for (int j = 0; j < LOADS; ++j) direct_load16_at(rs, to + j * 1024, voff[j], soffset);
+        } else {
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) direct_load16_at(rs, to + j * 1024, live(chunk[j]) ? voff[j] : OOB, soffset);
+        }
     }
     static __device__ u32x4 at(const LDS char *base, int r, int c) {
         return *reinterpret_cast<const LDS u32x4 *>(base + r * BYTES + ((c ^ swizzle(r)) << 4));
@@ -187,10 +205,11 @@ struct Found {
     LDS int32_t *choices;  // [experts + 1]: where they end, behind a 0
     LDS int16_t *groups;   // [experts + 1], the same of groups
     LDS int16_t *ids;      // [slots], -1: no expert
-    __device__ Found(LDS char *at)
-        : choices(reinterpret_cast<LDS int32_t *>(at)),
-          groups(reinterpret_cast<LDS int16_t *>(at + 4 * (LAYER_MAX_EXPERTS + 1))), ids(groups + LAYER_MAX_EXPERTS + 1) {}
+    __device__ Found(LDS char *at, int64_t experts)
+        : choices(reinterpret_cast<LDS int32_t *>(at)), groups(reinterpret_cast<LDS int16_t *>(choices + experts + 1)),
+          ids(groups + experts + 1) {}
 };
+int64_t found_bytes(const ExpertsLayer &p) { return 6 * (p.experts + 1) + 2 * p.tokens * p.top_k; }
 
 // Token t's first choice of expert e, or -1.
 __device__ inline int choice_of(const LDS int16_t *ids, int t, int k, int e) {
@@ -240,7 +259,10 @@ __device__ void find(const ExpertsLayer &p, const Found &f, int size) {
     __syncthreads();
 }
 
-// XR: tokens of a workgroup at most.
+// XR: tokens of a group at most.  The blocks of 16 rows of all groups are dealt
+// to the workgroups in equal shares, one workgroup per compute unit: finding
+// the experts takes 4 us, which a workgroup for every few blocks paid four times over (32
+// tokens of 64 experts in 8 bits: 113 us).
 template <class T, int TYPE, int XR>
 __global__ __launch_bounds__(THREADS, 1) void up_kernel(LayerArgs a) {
     using F = Form<TYPE>;
@@ -253,140 +275,161 @@ __global__ __launch_bounds__(THREADS, 1) void up_kernel(LayerArgs a) {
     __shared__ int expert_shared;
     LDS char *lds = (LDS char *)smem;
     LDS float *part = reinterpret_cast<LDS float *>(lds + WAVES * a.ring_up * STAGE);  // [wave][half][q][token][4]
+    const Found found(reinterpret_cast<LDS char *>(part + WAVES * 2 * 16 * XR), p.experts);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int k = int(p.top_k), E = int(p.experts);
-    const Found found(lds);  // where the runs will be
     find(p, found, XR);
-    const int group = blockIdx.x / a.groups;
-    if (group >= found.groups[E]) return;
-    for (int i = threadIdx.x; i < E; i += THREADS)
-        if (found.groups[i] <= group && group < found.groups[i + 1]) expert_shared = i;
-    __syncthreads();
-    const int e = __builtin_amdgcn_readfirstlane(expert_shared);
-    const int skip = (group - found.groups[e]) * XR;  // choices of the expert's earlier groups
-    const int all = found.choices[e + 1] - found.choices[e];
-    const int count = __builtin_amdgcn_readfirstlane(all - skip < XR ? all - skip : XR);
-    // its tokens, by rising token
-    if (wave == 0) {
-        const int c = lane < p.tokens ? choice_of(found.ids, lane, k, e) : -1;
-        const uint64_t mask = __ballot(c >= 0);
-        const int at = __popcll(mask & ((uint64_t(1) << lane) - 1)) - skip;
-        if (c >= 0 && at >= 0 && at < XR) {
-            float w = 0.0f;
-            for (int j = c; j < k; ++j)
-                if (found.ids[lane * k + j] == e) w += p.weights[lane * k + j];
-            token[at] = int16_t(lane);
-            choice[at] = int16_t(c);
-            share[at] = w;
-        }
-    }
-    __syncthreads();  // the last read of what was found
     const int r = lane & 15, q = lane >> 4;
-    const int64_t first_block = int64_t(blockIdx.x % a.groups) * a.blocks, all_blocks = (p.H + 15) / 16;
-    const int blocks = int(all_blocks - first_block < a.blocks ? all_blocks - first_block : a.blocks);
-    X x;
-    x.init(lane, [&](int row) { return uint32_t(token[row < count ? row : 0] * p.ldx * 2); });
-    const int64_t runs = (p.D + F::RUN - 1) / F::RUN;
-    const int mine = int((runs - wave + WAVES - 1) / WAVES);  // runs of each block
-    const char *up = static_cast<const char *>(p.up.w) + e * p.up.stride * F::ESZ;
-    Rows<TYPE> rows;
-    // items are (block, run) in turn; what is to be issued next
-    int issued = 0, issue_block = 0, issue_run = 0;
-    const int items = blocks * mine;
-    auto issue = [&]() {
-        const int64_t h0 = (first_block + issue_block) * 16, run = wave + int64_t(issue_run) * WAVES;
-        if (issue_run == 0) rows.init(p.up.ld, p.H - h0, lane);
-        const int64_t k0 = run * F::RUN, left = p.D - k0;
-        const char *gate = up + (h0 * p.up.ld + k0) * F::ESZ;
-        const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) + (wave * a.ring_up + issued % a.ring_up) * STAGE;
-        rows.issue(gate, to, left);
-        rows.issue(gate + p.H * p.up.ld * F::ESZ, to + 2048, left);
-        x.issue(static_cast<const uint16_t *>(p.X) + k0, to + 4096, [&](int c) { return c * 8 < left; });
-        if (TYPE != 0) {
-            // lanes 0, 1, 2: of the activated half's rows, which lie in one
-            // block of 128, and of the first and last of the others', which
-            // lie in two where H is no multiple of 16
-            const int64_t last = h0 + 15 < p.H ? h0 + 15 : p.H - 1;
-            const int64_t at = lane == 0 ? h0 / 128 : (p.H + (lane == 1 ? h0 : last)) / 128;
-            dma::direct_load4(buffer_at(p.up.scale + e * p.up.stride_scale + run * p.up.lds), to + 4096 + X::SIZE, uint32_t(at * 4));
+    const int64_t all_blocks = (p.H + 15) / 16, total = found.groups[E] * all_blocks;
+    int64_t from = total * blockIdx.x / gridDim.x;
+    const int64_t until = total * (blockIdx.x + 1) / gridDim.x;
+    while (from < until) {
+        const int group = int(from / all_blocks);
+        const int64_t first_block = from % all_blocks;
+        const int blocks = int(all_blocks - first_block < until - from ? all_blocks - first_block : until - from);
+        from += blocks;
+        for (int i = threadIdx.x; i < E; i += THREADS)
+            if (found.groups[i] <= group && group < found.groups[i + 1]) expert_shared = i;
+        __syncthreads();
+        const int e = __builtin_amdgcn_readfirstlane(expert_shared);
+        const int skip = (group - found.groups[e]) * XR;  // choices of the expert's earlier groups
+        const int all = found.choices[e + 1] - found.choices[e];
+        const int count = __builtin_amdgcn_readfirstlane(all - skip < XR ? all - skip : XR);
+        // its tokens, by rising token
+        if (wave == 0) {
+            const int c = lane < p.tokens ? choice_of(found.ids, lane, k, e) : -1;
+            const uint64_t mask = __ballot(c >= 0);
+            const int at = __popcll(mask & ((uint64_t(1) << lane) - 1)) - skip;
+            if (c >= 0 && at >= 0 && at < XR) {
+                float w = 0.0f;
+                for (int j = c; j < k; ++j)
+                    if (found.ids[lane * k + j] == e) w += p.weights[lane * k + j];
+                token[at] = int16_t(lane);
+                choice[at] = int16_t(c);
+                share[at] = w;
+            }
         }
-        ++issued;
-        if (++issue_run == mine) issue_run = 0, ++issue_block;
-    };
-    for (int i = 0; i < a.ring_up && i < items; ++i) issue();
-    int done = 0;
-    for (int b = 0; b < blocks; ++b) {
-        const int64_t h0 = (first_block + b) * 16, last = h0 + 15 < p.H ? h0 + 15 : p.H - 1;
-        const int in_first = int((p.H + last) / 128 * 128 - (p.H + h0));  // the others' rows of the first of two blocks
-        f32x4 g = {0, 0, 0, 0}, m = {0, 0, 0, 0};
-        for (int i = 0; i < mine; ++i, ++done) {
-            const int64_t left = p.D - (wave + int64_t(i) * WAVES) * F::RUN;
-            wait_for<PER>(issued - 1 - done);
-            const LDS char *stage = lds + (wave * a.ring_up + done % a.ring_up) * STAGE;
-            u32x4 og[F::STEPS], om[F::STEPS], xv[F::STEPS];
-#pragma unroll
-            for (int s = 0; s < F::STEPS; ++s) {
-                og[s] = Rows<TYPE>::template operand<T>(stage, s, r, q);
-                om[s] = Rows<TYPE>::template operand<T>(stage + 2048, s, r, q);
-                // columns past the group's tokens are not stored
-                xv[s] = X::at(stage + 4096, r % XR, k_of<TYPE>(s, q) / 8);
+        __syncthreads();
+        X x;
+        x.init(lane, [&](int row) { return uint32_t(token[row < count ? row : 0] * p.ldx * 2); });
+        const int runs = int((p.D + F::RUN - 1) / F::RUN), D = int(p.D);
+        const int mine = (runs - wave + WAVES - 1) / WAVES;  // runs of each block
+        const char *up = static_cast<const char *>(p.up.w) + e * p.up.stride * F::ESZ;
+        const u32x4 values = buffer_at(p.X);
+        const uint32_t ring0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) + wave * a.ring_up * STAGE;
+        const uint32_t ring1 = ring0 + a.ring_up * STAGE;
+        Rows<TYPE> rows;
+        u32x4 gate, mult;
+        const float *scale = nullptr;
+        uint32_t scale_at = 0;
+        // items are (block, run) in turn; what is to be issued next
+        int issued = 0, issue_block = 0, issue_run = 0;
+        uint32_t to = ring0;
+        const int items = blocks * mine;
+        auto issue = [&]() {
+            const int run = wave + issue_run * WAVES;
+            if (issue_run == 0) {
+                const int64_t h0 = (first_block + issue_block) * 16;
+                rows.init(p.up.ld, p.H - h0, lane);
+                gate = buffer_at(up + h0 * p.up.ld * F::ESZ);
+                mult = buffer_at(up + (p.H + h0) * p.up.ld * F::ESZ);
+                if (TYPE != 0) {
+                    // lanes 0, 1, 2: of the activated half's rows, which lie in one
+                    // block of 128, and of the first and last of the others', which
+                    // lie in two where H is no multiple of 16
+                    const int64_t last = h0 + 15 < p.H ? h0 + 15 : p.H - 1;
+                    scale_at = uint32_t((lane == 0 ? h0 / 128 : (p.H + (lane == 1 ? h0 : last)) / 128) * 4);
+                    scale = p.up.scale + e * p.up.stride_scale + wave * p.up.lds;
+                }
             }
-            float sg = 1.0f, s_lo = 1.0f, s_hi = 1.0f;
+            const int left = D - run * F::RUN;
+            rows.issue(gate, run * 128, to, left);
+            rows.issue(mult, run * 128, to + 2048, left);
+            x.issue(values, run * (F::RUN * 2), to + 4096, left >= F::RUN, [&](int c) { return c * 8 < left; });
             if (TYPE != 0) {
-                const LDS float *sc = reinterpret_cast<const LDS float *>(stage + 4096 + X::SIZE);
-                sg = sc[0];
-                s_lo = sc[1];
-                s_hi = sc[2];
+                dma::direct_load4(buffer_at(scale), to + 4096 + X::SIZE, scale_at);
+                scale += WAVES * p.up.lds;
             }
-            wait_lgkmcnt0();
-            asm volatile("" ::: "memory");
-            if (issued < items) issue();
-            if (left < F::RUN)
+            ++issued;
+            to = to + STAGE == ring1 ? ring0 : to + STAGE;
+            if (++issue_run == mine) issue_run = 0, ++issue_block;
+        };
+        for (int i = 0; i < a.ring_up && i < items; ++i) issue();
+        int done = 0;
+        const LDS char *const first_stage = lds + wave * a.ring_up * STAGE, *stage = first_stage;
+        for (int b = 0; b < blocks; ++b) {
+            const int64_t h0 = (first_block + b) * 16, last = h0 + 15 < p.H ? h0 + 15 : p.H - 1;
+            const int in_first = int((p.H + last) / 128 * 128 - (p.H + h0));  // the others' rows of the first of two blocks
+            f32x4 g = {0, 0, 0, 0}, m = {0, 0, 0, 0};
+            for (int i = 0; i < mine; ++i, ++done) {
+                const int left = D - (wave + i * WAVES) * F::RUN;
+                wait_for<PER>(issued - 1 - done);
+                u32x4 og[F::STEPS], om[F::STEPS], xv[F::STEPS];
 #pragma unroll
                 for (int s = 0; s < F::STEPS; ++s) {
-                    cut(og[s], k_of<TYPE>(s, q), int(left));
-                    cut(om[s], k_of<TYPE>(s, q), int(left));
-                    cut(xv[s], k_of<TYPE>(s, q), int(left));
+                    og[s] = Rows<TYPE>::template operand<T>(stage, s, r, q);
+                    om[s] = Rows<TYPE>::template operand<T>(stage + 2048, s, r, q);
+                    // columns past the group's tokens are not stored
+                    xv[s] = X::at(stage + 4096, r % XR, k_of<TYPE>(s, q) / 8);
                 }
-            f32x4 bg = TYPE == 0 ? g : f32x4{0, 0, 0, 0}, bm = TYPE == 0 ? m : f32x4{0, 0, 0, 0};
+                float sg = 1.0f, s_lo = 1.0f, s_hi = 1.0f;
+                if (TYPE != 0) {
+                    const LDS float *sc = reinterpret_cast<const LDS float *>(stage + 4096 + X::SIZE);
+                    sg = sc[0];
+                    s_lo = sc[1];
+                    s_hi = sc[2];
+                }
+                wait_lgkmcnt0();
+                asm volatile("" ::: "memory");
+                if (issued < items) issue();
+                stage = stage + STAGE == first_stage + a.ring_up * STAGE ? first_stage : stage + STAGE;
+                if (left < F::RUN)
 #pragma unroll
-            for (int s = 0; s < F::STEPS; ++s) {
-                bg = mfma16<T>(og[s], xv[s], bg);
-                bm = mfma16<T>(om[s], xv[s], bm);
-            }
-            if (TYPE == 0) {
-                g = bg;
-                m = bm;
-            } else {
+                    for (int s = 0; s < F::STEPS; ++s) {
+                        cut(og[s], k_of<TYPE>(s, q), left);
+                        cut(om[s], k_of<TYPE>(s, q), left);
+                        cut(xv[s], k_of<TYPE>(s, q), left);
+                    }
+                f32x4 bg = TYPE == 0 ? g : f32x4{0, 0, 0, 0}, bm = TYPE == 0 ? m : f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    g[j] = __builtin_fmaf(sg, bg[j], g[j]);
-                    m[j] = __builtin_fmaf(4 * q + j < in_first ? s_lo : s_hi, bm[j], m[j]);
+                for (int s = 0; s < F::STEPS; ++s) {
+                    bg = mfma16<T>(og[s], xv[s], bg);
+                    bm = mfma16<T>(om[s], xv[s], bm);
+                }
+                if (TYPE == 0) {
+                    g = bg;
+                    m = bm;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        g[j] = __builtin_fmaf(sg, bg[j], g[j]);
+                        m[j] = __builtin_fmaf(4 * q + j < in_first ? s_lo : s_hi, bm[j], m[j]);
+                    }
                 }
             }
-        }
-        // the waves' sums: lane l has rows h0 + 4(l / 16) + 0..3 of token l % 16
-        if (r < XR) {
-            *reinterpret_cast<LDS f32x4 *>(part + (wave * 2 + 0) * (16 * XR) + (q * XR + r) * 4) = g;
-            *reinterpret_cast<LDS f32x4 *>(part + (wave * 2 + 1) * (16 * XR) + (q * XR + r) * 4) = m;
-        }
-        __syncthreads();
-        const int at = (threadIdx.x / 4) % XR, j = threadIdx.x / (4 * XR) * 4 + threadIdx.x % 4;
-        if (threadIdx.x < 16 * XR && at < count) {
-            float v[1] = {0.0f}, o = 0.0f;
-#pragma unroll
-            for (int w = 0; w < WAVES; ++w) {
-                v[0] += part[(w * 2 + 0) * (16 * XR) + threadIdx.x];
-                o += part[(w * 2 + 1) * (16 * XR) + threadIdx.x];
+            // the waves' sums: lane l has rows h0 + 4(l / 16) + 0..3 of token l % 16
+            if (r < XR) {
+                *reinterpret_cast<LDS f32x4 *>(part + (wave * 2 + 0) * (16 * XR) + (q * XR + r) * 4) = g;
+                *reinterpret_cast<LDS f32x4 *>(part + (wave * 2 + 1) * (16 * XR) + (q * XR + r) * 4) = m;
             }
-            act::apply(p.act, v);
-            const float wh = h0 + j < p.H ? v[0] * o * share[at] : 0.0f;
-            const uint32_t hi = encode<T>(wh);
-            uint16_t *h = a.h + (token[at] * k + choice[at]) * a.ldh + (h0 + j) / F::RUN * (2 * F::RUN) + (h0 + j) % F::RUN;
-            h[0] = uint16_t(hi);
-            h[F::RUN] = uint16_t(encode<T>(wh - decode<T>(hi)));
+            __syncthreads();
+            const int at = (threadIdx.x / 4) % XR, j = threadIdx.x / (4 * XR) * 4 + threadIdx.x % 4;
+            if (threadIdx.x < 16 * XR && at < count) {
+                float v[1] = {0.0f}, o = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) {
+                    v[0] += part[(w * 2 + 0) * (16 * XR) + threadIdx.x];
+                    o += part[(w * 2 + 1) * (16 * XR) + threadIdx.x];
+                }
+                act::apply(p.act, v);
+                const float wh = h0 + j < p.H ? v[0] * o * share[at] : 0.0f;
+                const uint32_t hi = encode<T>(wh);
+                uint16_t *h = a.h + (token[at] * k + choice[at]) * a.ldh + (h0 + j) / F::RUN * (2 * F::RUN) + (h0 + j) % F::RUN;
+                h[0] = uint16_t(hi);
+                h[F::RUN] = uint16_t(encode<T>(wh - decode<T>(hi)));
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -403,12 +446,13 @@ __global__ __launch_bounds__(THREADS, 1) void down_kernel(LayerArgs a) {
     LDS char *lds = (LDS char *)smem;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int k = int(p.top_k), tokens = int(p.tokens), E = int(p.experts), slots = tokens * k;
-    // behind the runs: the tokens' sums [wave][token][16], and by group its
-    // expert, where its choices start and (one more) end; by choice its place
+    // behind the runs: the tokens' sums [wave][token][16]; by choice, in the
+    // order of experts, where its w h starts and (by group its choices'
+    // start, number and expert) whose it is
     LDS f32x4 *sums = reinterpret_cast<LDS f32x4 *>(lds + WAVES * a.ring_down * STAGE);
-    LDS int16_t *expert = reinterpret_cast<LDS int16_t *>(sums + WAVES * tokens * 4);
-    LDS int16_t *start = expert + slots, *place = start + slots + 1;
-    const Found found(lds);  // where the runs will be
+    LDS uint32_t *from = reinterpret_cast<LDS uint32_t *>(sums + WAVES * tokens * 4), *group = from + slots;
+    LDS uint8_t *token = reinterpret_cast<LDS uint8_t *>(group + slots);
+    const Found found(lds, p.experts);  // where the runs will be
     find(p, found, DT);
     const int groups = __builtin_amdgcn_readfirstlane(found.groups[E]);
     for (int i = threadIdx.x; i < WAVES * tokens * 4; i += THREADS) sums[i] = f32x4{0, 0, 0, 0};
@@ -417,21 +461,31 @@ __global__ __launch_bounds__(THREADS, 1) void down_kernel(LayerArgs a) {
         if (g0 == g1) continue;
         const int c = lane < tokens ? choice_of(found.ids, lane, k, e) : -1;
         const uint64_t mask = __ballot(c >= 0);
-        if (c >= 0) place[c0 + __popcll(mask & ((uint64_t(1) << lane) - 1))] = int16_t(lane * k + c);
+        if (c >= 0) {
+            const int at = c0 + __popcll(mask & ((uint64_t(1) << lane) - 1));
+            from[at] = uint32_t((lane * k + c) * a.ldh * 2);
+            token[at] = uint8_t(lane);
+        }
         if (lane < g1 - g0) {
-            expert[g0 + lane] = int16_t(e);
-            start[g0 + lane] = int16_t(c0 + lane * DT);
+            const int rest = found.choices[e + 1] - c0 - lane * DT;
+            group[g0 + lane] = uint32_t(e << 16 | (rest < DT ? rest : DT) << 12 | (c0 + lane * DT));
         }
     }
-    if (threadIdx.x == 0) start[groups] = int16_t(found.choices[E]);
     __syncthreads();  // the last read of what was found
     const int r = lane & 15, q = lane >> 4;
     const int64_t d0 = int64_t(blockIdx.x) * 16;
     const char *down = static_cast<const char *>(p.down.w) + d0 * p.down.ld * F::ESZ;
     Rows<TYPE> rows;
     rows.init(p.down.ld, p.D - d0, lane);
-    const int runs = int((p.H + F::RUN - 1) / F::RUN), units = groups * runs;
+    const int runs = int((p.H + F::RUN - 1) / F::RUN), units = groups * runs, H = int(p.H);
     const int on_group = WAVES / runs, on_run = WAVES % runs;
+    const int items = units > wave ? (units - wave + WAVES - 1) / WAVES : 0;
+    const u32x4 pieces = buffer_at(a.h);
+    const uint32_t ring0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) + wave * a.ring_down * STAGE;
+    const uint32_t ring1 = ring0 + a.ring_down * STAGE;
+    // A unit is a group and a run.  What it says (`info`: expert, number and
+    // start of its choices) and where their w h starts is read from LDS
+    // before the unit before it is waited for.
     struct Unit {
         int group, run;
     };
@@ -441,33 +495,40 @@ __global__ __launch_bounds__(THREADS, 1) void down_kernel(LayerArgs a) {
         if (u.run >= runs) u.run -= runs, ++u.group;
     };
     Unit next{wave / runs, wave % runs}, now = next;
-    const int items = units > wave ? (units - wave + WAVES - 1) / WAVES : 0;
+    uint32_t next_info = 0, to = ring0;
+    V v;
     int issued = 0;
-    auto issue = [&]() {
-        const int e = __builtin_amdgcn_readfirstlane(expert[next.group]);
-        const int first = start[next.group], end = start[next.group + 1];
-        const int64_t left = p.H - int64_t(next.run) * F::RUN;
-        const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds)) + (wave * a.ring_down + issued % a.ring_down) * STAGE;
-        rows.issue(down + (e * p.down.stride + int64_t(next.run) * F::RUN) * F::ESZ, to, left);
-        V v;
+    auto look_up = [&]() {
+        next_info = group[next.group];
+        const int first = next_info & 0xfff, count = next_info >> 12 & 15;
         // past the group's choices, its first one's, not added to a sum
-        v.init(lane, [&](int row) { return uint32_t(place[first + row < end ? first + row : first] * int(a.ldh * 2)); });
+        v.init(lane, [&](int row) { return from[row < count ? first + row : first]; });
+    };
+    auto issue = [&]() {
+        const int e = __builtin_amdgcn_readfirstlane(next_info >> 16);
+        const int left = H - next.run * F::RUN;
+        rows.issue(buffer_at(down + e * p.down.stride * F::ESZ), next.run * 128, to, left);
         // chunks of eight in each piece, as far as the rows go
-        v.issue(a.h + int64_t(next.run) * (2 * F::RUN), to + 2048, [&](int c) { return c % (F::RUN / 8) * 8 < left; });
+        v.issue(pieces, next.run * (F::RUN * 4), to + 2048, left >= F::RUN, [&](int c) { return c % (F::RUN / 8) * 8 < left; });
         // 16 rows from a multiple of 16 lie in one block of 128
         if (TYPE != 0)
             dma::direct_load4(buffer_at(p.down.scale + e * p.down.stride_scale + next.run * p.down.lds + d0 / 128),
                               to + 2048 + V::SIZE, 0);
-        ++issued;
+        to = to + STAGE == ring1 ? ring0 : to + STAGE;
         advance(next);
+        if (++issued < items) look_up();
     };
+    if (items > 0) look_up();
     for (int i = 0; i < a.ring_down && i < items; ++i) issue();
+    const LDS char *const first_stage = lds + wave * a.ring_down * STAGE, *stage = first_stage;
+    uint32_t now_info = items > 0 ? group[now.group] : 0;
     for (int done = 0; done < items; ++done) {
-        const int first = start[now.group], end = start[now.group + 1];
-        const int64_t left = p.H - int64_t(now.run) * F::RUN;
-        const int t = place[first + r < end ? first + r : first] / k;
+        const int first = now_info & 0xfff, count = now_info >> 12 & 15;
+        const int t = token[r < count ? first + r : first];
+        const int left = H - now.run * F::RUN;
+        advance(now);
+        if (done + 1 < items) now_info = group[now.group];
         wait_for<PER>(issued - 1 - done);
-        const LDS char *stage = lds + (wave * a.ring_down + done % a.ring_down) * STAGE;
         u32x4 od[F::STEPS], hi[F::STEPS], lo[F::STEPS];
 #pragma unroll
         for (int s = 0; s < F::STEPS; ++s) {
@@ -479,24 +540,24 @@ __global__ __launch_bounds__(THREADS, 1) void down_kernel(LayerArgs a) {
         wait_lgkmcnt0();
         asm volatile("" ::: "memory");
         if (issued < items) issue();
+        stage = stage + STAGE == first_stage + a.ring_down * STAGE ? first_stage : stage + STAGE;
         // up_kernel has filled the pieces' last chunks with zeros
         if (left < F::RUN)
 #pragma unroll
-            for (int s = 0; s < F::STEPS; ++s) cut(od[s], k_of<TYPE>(s, q), int(left));
-        f32x4 block = {0, 0, 0, 0};
+            for (int s = 0; s < F::STEPS; ++s) cut(od[s], k_of<TYPE>(s, q), left);
+        f32x4 block = {0, 0, 0, 0}, rest = {0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < F::STEPS; ++s) {
-            block = mfma16<T>(od[s], lo[s], block);
+            rest = mfma16<T>(od[s], lo[s], rest);
             block = mfma16<T>(od[s], hi[s], block);
         }
-        if (r < DT && first + r < end) {
+        if (r < count) {
             LDS f32x4 *sum = sums + (wave * tokens + t) * 4 + q;
-            f32x4 v = *sum;
+            f32x4 y = *sum;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(scale, block[j], v[j]);
-            *sum = v;
+            for (int j = 0; j < 4; ++j) y[j] = __builtin_fmaf(scale, block[j] + rest[j], y[j]);
+            *sum = y;
         }
-        advance(now);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < tokens * 16; i += THREADS) {
@@ -521,6 +582,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 
 constexpr int MOST_LDS = 160 * 1024;
+constexpr int UNITS = 256;  // compute units of an MI355X
 static_assert(4 * (LAYER_MAX_EXPERTS + 1) + 2 * (LAYER_MAX_EXPERTS + 1) + 2 * LAYER_MAX_TOKENS * LAYER_MAX_TOP_K <= WAVES * 2 * 4096,
               "what is found fits where the runs will be");
 
@@ -537,24 +599,20 @@ template <class T, int TYPE, int XR>
 hipError_t run_up(LayerArgs &a, hipStream_t stream) {
     const ExpertsLayer &p = a.p;
     constexpr int64_t stage = 4096 + XR * Form<TYPE>::RUN * 2 + Form<TYPE>::SCALE_BYTES, part = WAVES * 2 * 64 * XR;
-    a.ring_up = ring_of(stage, part);
-    const size_t lds = size_t(WAVES * a.ring_up * stage + part);
+    const int64_t beside = part + found_bytes(p);
+    a.ring_up = ring_of(stage, beside);
+    const size_t lds = size_t(WAVES * a.ring_up * stage + beside);
     hipError_t e = allow_lds(up_kernel<T, TYPE, XR>, lds);
     if (e != hipSuccess) return e;
-    // groups of tokens at most; blocks so that there are about 1024 workgroups
-    const int64_t slots = p.tokens * p.top_k, groups = least(slots, least(p.experts, slots) + slots / XR);
-    const int64_t all_blocks = ceil_div(p.H, 16), blocks = groups * all_blocks / 1024;
-    a.blocks = int(blocks < 1 ? 1 : least(blocks, 8));
-    a.groups = int(ceil_div(all_blocks, a.blocks));
-    if (groups * a.groups > 0x7fffff) return hipErrorInvalidConfiguration;
-    up_kernel<T, TYPE, XR><<<dim3(unsigned(groups * a.groups)), dim3(THREADS), lds, stream>>>(a);
+    const int64_t blocks = p.tokens * p.top_k * ceil_div(p.H, 16);  // at most
+    up_kernel<T, TYPE, XR><<<dim3(unsigned(least(blocks, UNITS))), dim3(THREADS), lds, stream>>>(a);
     return hipGetLastError();
 }
 template <class T, int TYPE, int DT>
 hipError_t run_down(LayerArgs &a, hipStream_t stream) {
     const ExpertsLayer &p = a.p;
     constexpr int64_t stage = 2048 + DT * Form<TYPE>::RUN * 4 + Form<TYPE>::SCALE_BYTES;
-    const int64_t beside = WAVES * p.tokens * 64 + (3 * p.tokens * p.top_k + 1) * 2;
+    const int64_t beside = WAVES * p.tokens * 64 + 9 * p.tokens * p.top_k;
     a.ring_down = ring_of(stage, beside);
     const size_t lds = size_t(WAVES * a.ring_down * stage + beside);
     hipError_t e = allow_lds(down_kernel<T, TYPE, DT>, lds);
@@ -572,10 +630,7 @@ hipError_t run_tokens(LayerArgs &a, hipStream_t stream) {
     const int64_t slots = p.tokens * p.top_k;
     const hipError_t e = p.tokens > 8 && slots > 5 * p.experts ? run_up<T, TYPE, 16>(a, stream) : run_up<T, TYPE, 8>(a, stream);
     if (e != hipSuccess) return e;
-#ifndef DOWN_FEW
-#define DOWN_FEW 5
-#endif
-    return p.tokens <= 4 || slots < DOWN_FEW * p.experts ? run_down<T, TYPE, 4>(a, stream) : run_down<T, TYPE, 8>(a, stream);
+    return p.tokens <= 4 || slots <= 2 * p.experts ? run_down<T, TYPE, 4>(a, stream) : run_down<T, TYPE, 8>(a, stream);
 }
 template <class T>
 hipError_t run_type(LayerArgs &a, hipStream_t stream) {

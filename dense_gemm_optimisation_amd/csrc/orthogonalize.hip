@@ -91,16 +91,48 @@ __device__ inline double block_sum(double s, double *scratch) {
     return scratch[0];
 }
 
+// N values of G from element `at` on (fewer than N are there at a row's end).
+template <int N>
+__device__ inline void values_of(const InputArgs &p, int64_t at, int64_t there, float (&v)[N]) {
+    typedef float wide_f __attribute__((ext_vector_type(4), aligned(4)));
+    typedef uint16_t wide_h __attribute__((ext_vector_type(4), aligned(2)));
+    if (there >= N) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            if (p.in == 0) {
+                const wide_f w = *reinterpret_cast<const wide_f *>(static_cast<const float *>(p.G) + at + i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i + e] = w[e];
+            } else {
+                const wide_h w = *reinterpret_cast<const wide_h *>(static_cast<const uint16_t *>(p.G) + at + i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i + e] = p.in == 1 ? decode<BF16>(w[e]) : decode<F16>(w[e]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = e < there ? value_of(p, at + e) : 0.0f;
+    }
+}
+
 // Squares in 64 bits: fp32's would leave its range.  Part i has rows i, i +
-// PARTS, ...
+// PARTS, ...; four values per lane at a time, of four rows in turn.
 __global__ __launch_bounds__(256) void norm_kernel(InputArgs p) {
     __shared__ double scratch[256];
     const int64_t base = blockIdx.y * p.strideG;
     double s = 0.0;
-    for (int64_t r = blockIdx.x; r < p.M; r += PARTS)
-        for (int64_t c = threadIdx.x; c < p.N; c += 256) {
-            const double v = value_of(p, base + r * p.ldg + c);
-            s += v * v;
+    for (int64_t r0 = blockIdx.x; r0 < p.M; r0 += 4 * PARTS)
+        for (int64_t c = 4 * threadIdx.x; c < p.N; c += 1024) {
+            float v[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t r = r0 + i * PARTS;
+                values_of<4>(p, base + r * p.ldg + c, r < p.M ? p.N - c : 0, v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s = __builtin_fma(double(v[i][e]), double(v[i][e]), s);
         }
     s = block_sum(s, scratch);
     if (threadIdx.x == 0) p.parts[blockIdx.y * PARTS + blockIdx.x] = s;
@@ -168,7 +200,7 @@ __device__ inline void upper_tile(int64_t id, int64_t T, int64_t &tm, int64_t &t
 }
 
 template <class Shape, Step STEP>
-__global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void product_kernel(OrthoArgs p) {
+__global__ __launch_bounds__(Shape::THREADS, Shape::LDS_BYTES > 80 * 1024 ? 1 : 2) void product_kernel(OrthoArgs p) {
     __shared__ __attribute__((aligned(1024))) char smem[Shape::LDS_BYTES];
     LDS char *lds = (LDS char *)smem;
     constexpr bool SYMMETRIC = STEP != Step::Update;
@@ -230,11 +262,22 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void
                 for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(p.c * 0x1p-16f, v[e], b * 0x1p-4f * g[e]);
             }
             store8<F16>(out + r * p.lda + c, count, v);
-            if (n0 > m0)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (c + e < p.m) out[(c + e) * p.lda + r] = uint16_t(encode<F16>(v[e]));
         });
+        // the same values on the other side of the diagonal
+        if (n0 > m0)
+            visit_tile_turned(acc, p.m, p.m, mw, nw, lane, staging, [&](int64_t r, int64_t c, int count, float(&v)[8]) {
+                if constexpr (STEP == Step::Gram) {
+                    const float s = f * f / X_SCALE;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= s;
+                } else {
+                    float g[8];
+                    load8<F16>(gram + r * p.lda + c, count, g);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(p.c * 0x1p-16f, v[e], b * 0x1p-4f * g[e]);
+                }
+                store8<F16>(out + r * p.lda + c, count, v);
+            });
     } else {
         uint16_t *lo = p.lo + batch * p.m * p.ldx, *next = p.next + batch * p.m * p.ldx;
         const float a = __builtin_fmaf(shift, __builtin_fmaf(shift, p.c, p.b), p.a);
@@ -275,8 +318,8 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void
 }
 
 // ---------------------------------------------------------------- in one workgroup
-// Blocks of 32 x 32: at most 4 x 4 of A, and MOST_BLOCKS of X, eight waves.
-constexpr int SMALL_WAVES = 8, SMALL_SIDE = 128, SMALL_BLOCKS = 6;  // X's blocks per wave
+// Blocks of 32 x 32: at most 4 x 4 of A, dealt to 16 waves, and 48 of X.
+constexpr int SMALL_WAVES = 16, SMALL_SIDE = 128, SMALL_BLOCKS = 3;  // X's blocks per wave
 constexpr int SMALL_LDS = 150 * 1024;                              // beside what is declared
 struct SmallArgs {
     InputArgs in;
@@ -315,22 +358,25 @@ __device__ inline void put4(LDS char *at, const float (&v)[4]) {
 
 // BLOCKS: of X per wave at most.
 template <int BLOCKS>
-__global__ __launch_bounds__(SMALL_WAVES * 64, 2) void small_kernel(SmallArgs a) {
+__global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
     extern __shared__ __attribute__((aligned(16))) char smem[];
     __shared__ double scratch[SMALL_WAVES];
     __shared__ float sums[SMALL_WAVES];
     const InputArgs &in = a.in;
     const OrthoArgs &p = a.p;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, T = SMALL_WAVES * 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t batch = blockIdx.x;
     const int m = int(p.m), n = int(p.n), mp = a.blocks_m * 32, np = a.blocks_n * 32;
     LDS char *x = (LDS char *)smem, *gram = x + mp * a.pitch_x, *poly = gram + mp * a.pitch_a;
     // the norm, in 64 bits
     double q = 0.0;
-    for (int i = threadIdx.x; i < m * n; i += T) {
-        const double v = value_of(in, batch * in.strideG + i / in.N * in.ldg + i % in.N);
-        q += v * v;
-    }
+    for (int64_t r = wave; r < in.M; r += SMALL_WAVES)
+        for (int64_t c = 4 * lane; c < in.N; c += 256) {
+            float v[4];
+            values_of<4>(in, batch * in.strideG + r * in.ldg + c, in.N - c, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q = __builtin_fma(double(v[e]), double(v[e]), q);
+        }
     for (int d = 1; d < 64; d *= 2) q += __shfl_xor(q, d);
     if (lane == 0) scratch[wave] = q;
     __syncthreads();
@@ -356,13 +402,22 @@ __global__ __launch_bounds__(SMALL_WAVES * 64, 2) void small_kernel(SmallArgs a)
         if (block >= blocks) continue;
         const int r = block / a.blocks_n * 32 + r_in, c = block % a.blocks_n * 32 + c_in;
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            const int col = c + 8 * (u / 4) + u % 4;
-            float v = 0.0f;
-            if (r < m && col < n)
-                v = factor * float(double(value_of(in, batch * in.strideG + (p.turned ? col * in.ldg + r : r * in.ldg + col))) *
-                                   (X_SCALE / least));
-            X[i][u] = v;
+        for (int u = 0; u < 4; ++u) {
+            const int col = c + 8 * u;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (r < m && col < n) {
+                if (!p.turned) {
+                    values_of<4>(in, batch * in.strideG + r * in.ldg + col, n - col, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (col + e < n) v[e] = value_of(in, batch * in.strideG + (col + e) * in.ldg + r);
+                }
+            }
+            // a 0 times NaN is NaN, but the filling's stays out of every sum
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                X[i][4 * u + e] = r < m && col + e < n ? factor * float(double(v[e]) * (X_SCALE / least)) : 0.0f;
         }
         store_x(i, block);
     }
@@ -373,6 +428,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64, 2) void small_kernel(SmallArgs a)
         for (int block = wave; block < blocks_a; block += SMALL_WAVES) {
             const int bi = block / a.blocks_m * 32, bj = block % a.blocks_m * 32;
             f32x16 acc = {};
+#pragma unroll 2
             for (int k = 0; k < np; k += 16)
                 acc = mfma32<F16>(frag_rows(x, a.pitch_x, bj, k, lane), frag_rows(x, a.pitch_x, bi, k, lane), acc);
 #pragma unroll
@@ -392,6 +448,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64, 2) void small_kernel(SmallArgs a)
         for (int block = wave; block < blocks_a; block += SMALL_WAVES) {
             const int bi = block / a.blocks_m * 32, bj = block % a.blocks_m * 32;
             f32x16 acc = {};
+#pragma unroll 2
             for (int k = 0; k < mp; k += 16)
                 acc = mfma32<F16>(frag_rows(gram, a.pitch_a, bj, k, lane), frag_rows(gram, a.pitch_a, bi, k, lane), acc);
 #pragma unroll
@@ -414,6 +471,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64, 2) void small_kernel(SmallArgs a)
             if (block >= blocks) continue;
             const int bi = block / a.blocks_n * 32, bj = block % a.blocks_n * 32;
             f32x16 acc = {};
+#pragma unroll 2
             for (int k = 0; k < mp; k += 16)
                 acc = mfma32<F16>(frag_columns(x, a.pitch_x, bj, k, lane), frag_rows(poly, a.pitch_a, bi, k, lane), acc);
 #pragma unroll
@@ -500,25 +558,47 @@ hipError_t launch_small(const SmallArgs &a, size_t lds, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// 256 x 256 tiles where they fill the chip.
-bool large(int64_t m, int64_t n, int64_t batch) { return ceil_div(m, 256) * ceil_div(n, 256) * batch >= 192; }
+// Tiles of 256, 192 (symmetric products) or 128, whichever takes the least
+// time by whole rounds of workgroups.  REPLACE
+enum class Size { Large, Middle, Small, Few };
+Size size_of(int64_t m, int64_t n, int64_t batch, bool symmetric) {
+    auto tiles = [&](int64_t side) {
+        const int64_t r = ceil_div(m, side), c = ceil_div(n, side);
+        return batch * (symmetric ? r * (r + 1) / 2 : r * c);
+    };
+    if (tiles(128) <= 256) return Size::Few;
+    const int64_t large = ceil_div(tiles(256), 256) * 64, small = ceil_div(tiles(128), 512) * 40;
+    const int64_t middle = symmetric ? ceil_div(tiles(192), 256) * 42 : INT64_MAX;
+    if (middle < large && middle < small) return Size::Middle;
+    return large <= small ? Size::Large : Size::Small;
+}
+int64_t side_of(Size s) { return s == Size::Large ? 256 : s == Size::Middle ? 192 : 128; }
+
+template <class Shape, Step STEP>
+hipError_t launch_shape(OrthoArgs &a, int64_t tiles, hipStream_t stream) {
+    product_kernel<Shape, STEP><<<dim3(unsigned(tiles)), dim3(Shape::THREADS), 0, stream>>>(a);
+    return hipGetLastError();
+}
 
 template <Step STEP>
 hipError_t launch_product(OrthoArgs &a, hipStream_t stream) {
-    constexpr bool B_KMAJOR = STEP != Step::Update;
-    using Large = Tile<F16, 256, 256, 2, 4, true, B_KMAJOR, true>;
-    using Small = Tile<F16, 128, 128, 2, 2, true, B_KMAJOR, true>;
-    const int64_t cols = STEP == Step::Update ? a.n : a.m;
-    const bool big = large(a.m, cols, a.batch);
-    const int64_t side = big ? 256 : 128;
-    a.tiles_m = ceil_div(a.m, side);
-    a.tiles_n = ceil_div(cols, side);
-    if (STEP == Step::Update) a.tiles_x = a.tiles_m * a.tiles_n;
-    const int64_t tiles = a.batch * (STEP == Step::Update ? a.tiles_m * a.tiles_n : a.tiles_m * (a.tiles_m + 1) / 2);
+    constexpr bool SYMMETRIC = STEP != Step::Update;
+    using Large = Tile<F16, 256, 256, 2, 4, true, SYMMETRIC, true>;
+    using Middle = Tile<F16, 192, 192, 2, 2, true, true, true, 64, 3>;
+    using Small = Tile<F16, 128, 128, 2, 2, true, SYMMETRIC, true>;
+    using Few = Tile<F16, 128, 128, 2, 2, true, SYMMETRIC, true, 64, 4>;
+    const int64_t cols = SYMMETRIC ? a.m : a.n;
+    const Size size = size_of(a.m, cols, a.batch, SYMMETRIC);
+    a.tiles_m = ceil_div(a.m, side_of(size));
+    a.tiles_n = ceil_div(cols, side_of(size));
+    if (!SYMMETRIC) a.tiles_x = a.tiles_m * a.tiles_n;
+    const int64_t tiles = a.batch * (SYMMETRIC ? a.tiles_m * (a.tiles_m + 1) / 2 : a.tiles_m * a.tiles_n);
     if (tiles > 0x7fffff) return hipErrorInvalidConfiguration;
-    if (big) product_kernel<Large, STEP><<<dim3(unsigned(tiles)), dim3(Large::THREADS), 0, stream>>>(a);
-    else product_kernel<Small, STEP><<<dim3(unsigned(tiles)), dim3(Small::THREADS), 0, stream>>>(a);
-    return hipGetLastError();
+    if (size == Size::Large) return launch_shape<Large, STEP>(a, tiles, stream);
+    if (size == Size::Small) return launch_shape<Small, STEP>(a, tiles, stream);
+    if (size == Size::Few) return launch_shape<Few, STEP>(a, tiles, stream);
+    if constexpr (SYMMETRIC) return launch_shape<Middle, STEP>(a, tiles, stream);
+    return hipSuccess;
 }
 
 }  // namespace
@@ -526,7 +606,11 @@ hipError_t launch_product(OrthoArgs &a, hipStream_t stream) {
 const char *orthogonalize_kernel_name(int64_t M, int64_t N, int64_t batch) {
     if (M == 0 || N == 0 || batch == 0) return "";
     if (small_lds(M < N ? M : N, M < N ? N : M) != 0) return "orthogonalize_small";
-    return large(M < N ? M : N, M < N ? N : M, batch) ? "orthogonalize_mfma_256" : "orthogonalize_mfma_128";
+    switch (size_of(M < N ? M : N, M < N ? N : M, batch, false)) {
+        case Size::Large: return "orthogonalize_mfma_256";
+        case Size::Few: return "orthogonalize_mfma_128_few";
+        default: return "orthogonalize_mfma_128";
+    }
 }
 
 size_t orthogonalize_workspace(int64_t M, int64_t N, int64_t batch) { return layout_of(M, N, batch).bytes; }

@@ -145,7 +145,7 @@ struct Panel {
     static constexpr int PER_WAVE = BYTES / 1024 / WAVES;  // 1 KiB pieces per wave per stage
     static constexpr int CHR = ROWS / 8;                   // chunks per k row, row-contiguous
     static_assert(PER_WAVE * WAVES * 1024 == BYTES, "panel split over waves");
-    static_assert(ROWS == 128 || ROWS == 256, "the layout's swizzle");
+    static_assert(KMAJOR || ROWS == 128 || ROWS == 256, "the layout's swizzle");
     uint32_t voff[PER_WAVE];  // byte offset of this lane's chunk from the stage's base
     int kl[PER_WAVE];         // its k within the stage
     int rl[PER_WAVE];         // its first row, from r0
@@ -454,6 +454,38 @@ __device__ __forceinline__ void visit_tile(const f32x16 (&acc)[FM][FN], int64_t 
             if (m < M && count > 0) f(m, n, count, x);
         }
     }
+}
+
+// The same tile turned: f(n, m, count, x) for pieces of 8 rows of a column n,
+// count = min(8, M - m), through strips of 32 columns by up to 64 rows.
+template <int FM, int FN, class F>
+__device__ __forceinline__ void visit_tile_turned(const f32x16 (&acc)[FM][FN], int64_t M, int64_t N, int64_t mw,
+                                                  int64_t nw, int lane, LDS float *scratch, F &&f) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i0 = 0; i0 < FM; i0 += 2) {
+            constexpr int W = 64;
+            const int wide = FM - i0 < 2 ? 32 : 64;
+#pragma unroll
+            for (int i = i0; i < i0 + 2 && i < FM; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    scratch[(8 * (e / 4) + 4 * (lane >> 5) + e % 4) * W + (i - i0) * 32 + (lane & 31)] = acc[i][j][e];
+#pragma unroll 1
+            for (int it = 0; it < 4; ++it) {
+                const int r = it * 8 + lane / 8, c = (lane % 8) * 8;
+                const int64_t n = nw + j * 32 + r, m = mw + i0 * 32 + c;
+                float x[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4 v = *reinterpret_cast<const LDS f32x4 *>(scratch + r * W + c + 4 * h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
+                }
+                if (n < N && m < M && c < wide) f(n, m, M - m < 8 ? int(M - m) : 8, x);
+            }
+        }
 }
 
 }  // namespace tile16
