@@ -61,14 +61,20 @@ struct Finish {
         if (!BACKWARD && p.bias != nullptr && n < p.N)
             load8<T>(p.bias + n, p.N - n < 8 ? int(p.N - n) : 8, column);
     }
-    // x: the products' sums of columns n .. n + count - 1 of row m
-    __device__ void operator()(int64_t m, int64_t n, int count, float (&x)[8]) {
+    // What row m's columns n .. n + count - 1 read: Z, or a 16-bit residual.
+    typedef Raw8 Data;
+    __device__ void load(Data &d, int64_t m, int64_t n, int count) const {
+        if (BACKWARD && p.act != act::NONE) d.load(p.Z + m * p.ldz + n, count);
+        if (!BACKWARD && p.beta != 0.0f && p.c_same) d.load(static_cast<const uint16_t *>(p.R) + m * p.ldr + n, count);
+    }
+    // x: the products' sums of those columns
+    __device__ void operator()(int64_t m, int64_t n, int count, float (&x)[8], const Data &d) {
         if constexpr (BACKWARD) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] *= p.alpha;
             if (p.act != act::NONE) {
                 float z[8];
-                load8<T>(p.Z + m * p.ldz + n, count, z);
+                d.values<T>(z);
                 act::times_slope(p.act, z, x);
             }
 #pragma unroll
@@ -80,7 +86,8 @@ struct Finish {
             act::apply(p.act, x);
             if (p.beta != 0.0f) {
                 float r[8];
-                load8_as<T>(p.R, m * p.ldr + n, p.c_same, count, r);
+                if (p.c_same) d.values<T>(r);
+                else load8f(static_cast<const float *>(p.R) + m * p.ldr + n, count, r);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(p.beta, r[e], x[e]);
             }
@@ -133,9 +140,16 @@ __global__ __launch_bounds__(Shape::THREADS, 2) void split_kernel(LinearArgs p) 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t mw = m0 + Shape::wave_m(wave) * Shape::WTM, nw = n0 + Shape::wave_n(wave) * Shape::WTN;
     if (mw >= p.M || nw >= p.N) return;
-    float *out = p.partial + z * p.M * p.ldp;
-    visit_tile(acc, p.M, p.N, mw, nw, lane, Shape::staging(lds, buf, wave),
-               [&](int64_t m, int64_t n, int count, float(&x)[8]) { store8f(out + m * p.ldp + n, count, x); });
+    struct Store {
+        typedef Nothing Data;
+        float *out;
+        int64_t ld;
+        __device__ void load(Data &, int64_t, int64_t, int) const {}
+        __device__ void operator()(int64_t m, int64_t n, int count, const float (&x)[8], const Data &) const {
+            store8f(out + m * ld + n, count, x);
+        }
+    };
+    visit_tile(acc, p.M, p.N, mw, nw, lane, Shape::staging(lds, buf, wave), Store{p.partial + z * p.M * p.ldp, p.ldp});
 }
 
 // Joins the slices: 64 columns by FINISH_ROWS rows per workgroup.
@@ -151,13 +165,15 @@ __global__ __launch_bounds__(256) void finish_kernel(LinearArgs p) {
     if (m < p.M && count > 0) {
         float x[8], part[8];
         const float *at = p.partial + m * p.ldp + n;
+        Raw8 data;
+        finish.load(data, m, n, count);
         load8f(at, count, x);
         for (int s = 1; s < p.slices; ++s) {
             load8f(at + s * p.M * p.ldp, count, part);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += part[e];
         }
-        finish(m, n, count, x);
+        finish(m, n, count, x, data);
     }
     if (!BACKWARD || p.sums == nullptr) return;
     for (int d = 8; d < 64; d *= 2)
@@ -268,7 +284,11 @@ __global__ __launch_bounds__(512, 1) void few_kernel(LinearArgs p) {
     const int64_t n = n0 + 8 * (lane >> 4 & 1);
     const int count = p.N - n < 8 ? int(p.N - n) : 8;
     Finish<T, BACKWARD> finish(p, n);
-    if (lane < 32 && row < p.M && count > 0) finish(row, n, count, x);
+    if (lane < 32 && row < p.M && count > 0) {
+        Raw8 data;
+        finish.load(data, row, n, count);
+        finish(row, n, count, x, data);
+    }
     if (!BACKWARD || p.sums == nullptr) return;
     for (int d = 1; d < 16; d *= 2)
 #pragma unroll

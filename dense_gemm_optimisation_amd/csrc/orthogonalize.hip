@@ -116,23 +116,23 @@ __device__ inline void values_of(const InputArgs &p, int64_t at, int64_t there, 
 }
 
 // Squares in 64 bits: fp32's would leave its range.  Part i has rows i, i +
-// PARTS, ...; four values per lane at a time, of four rows in turn.
+// PARTS, ...; eight values of four rows per lane at a time.
 __global__ __launch_bounds__(256) void norm_kernel(InputArgs p) {
     __shared__ double scratch[256];
     const int64_t base = blockIdx.y * p.strideG;
     double s = 0.0;
     for (int64_t r0 = blockIdx.x; r0 < p.M; r0 += 4 * PARTS)
-        for (int64_t c = 4 * threadIdx.x; c < p.N; c += 1024) {
-            float v[4][4];
+        for (int64_t c = 8 * threadIdx.x; c < p.N; c += 2048) {
+            float v[4][8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int64_t r = r0 + i * PARTS;
-                values_of<4>(p, base + r * p.ldg + c, r < p.M ? p.N - c : 0, v[i]);
+                values_of<8>(p, base + r * p.ldg + c, r < p.M ? p.N - c : 0, v[i]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s = __builtin_fma(double(v[i][e]), double(v[i][e]), s);
+                for (int e = 0; e < 8; ++e) s = __builtin_fma(double(v[i][e]), double(v[i][e]), s);
         }
     s = block_sum(s, scratch);
     if (threadIdx.x == 0) p.parts[blockIdx.y * PARTS + blockIdx.x] = s;
@@ -189,15 +189,76 @@ __device__ inline void put_output(const OrthoArgs &p, int64_t at, float y) {
     }
 }
 
-// Tile `id` of the upper triangle of T x T tiles, row by row.
+// Tile `id` of the upper triangle of T x T tiles, row by row (in bands of six
+// rows, which share more panels on a die, 4096 x 4096 took the same time).
 __device__ inline void upper_tile(int64_t id, int64_t T, int64_t &tm, int64_t &tn) {
-    tm = 0;
-    while (id >= T - tm) {
-        id -= T - tm;
-        ++tm;
-    }
-    tn = tm + id;
+    int64_t r = 0;
+    while (id >= T - r) id -= T - r++;
+    tm = r;
+    tn = r + id;
 }
+
+// Eight values of A less its mean eigenvalue, or of B' from it.
+template <Step STEP>
+struct Symmetric {
+    typedef Raw8 Data;
+    const uint16_t *gram;
+    uint16_t *out;
+    int64_t ld;
+    float times, own;  // of the product's sums; of the diagonal (A), of A (B')
+    __device__ void load(Data &d, int64_t r, int64_t c, int count) const {
+        if (STEP == Step::Poly) d.load(gram + r * ld + c, count);
+    }
+    __device__ void operator()(int64_t r, int64_t c, int count, float (&v)[8], const Data &d) const {
+        if constexpr (STEP == Step::Gram) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = times * v[e] - (r == c + e ? own : 0.0f);
+        } else {
+            float g[8];
+            d.values<F16>(g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(times, v[e], own * g[e]);
+        }
+        store8<F16>(out + r * ld + c, count, v);
+    }
+};
+
+// Eight values of the next X, or in the last step of O.
+struct Updated {
+    struct Data {
+        Raw8 hi, lo;
+    };
+    const OrthoArgs &p;
+    const uint16_t *x;
+    uint16_t *lo, *next;
+    int64_t o;
+    float factor, own, square;
+    __device__ void load(Data &d, int64_t r, int64_t c, int count) const {
+        d.hi.load(x + r * p.ldx + c, count);
+        d.lo.load(lo + r * p.ldx + c, count);
+    }
+    __device__ void operator()(int64_t r, int64_t c, int count, float (&v)[8], const Data &d) {
+        float h[8], l[8];
+        d.hi.values<F16>(h);
+        d.lo.values<F16>(l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = factor * __builtin_fmaf(0x1p-8f, v[e], own * (h[e] + l[e]));
+        if (!p.last) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                square += v[e] * v[e];
+                l[e] = v[e] - decode<F16>(encode<F16>(v[e]));
+            }
+            store8<F16>(next + r * p.ldx + c, count, v);
+            store8<F16>(lo + r * p.ldx + c, count, l);
+            return;
+        }
+        const float s = p.alpha / X_SCALE;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < p.n) put_output(p, o + (p.turned ? (c + e) * p.ldo + r : r * p.ldo + c + e), s * v[e]);
+    }
+};
 
 template <class Shape, Step STEP>
 __global__ __launch_bounds__(Shape::THREADS, Shape::LDS_BYTES > 80 * 1024 ? 1 : 2) void product_kernel(OrthoArgs p) {
@@ -248,65 +309,19 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::LDS_BYTES > 80 * 1024 ? 1 : 
     const float f = p.factor != nullptr ? p.factor[batch] : 1.0f;
     LDS float *staging = Shape::staging(lds, buf, wave);
     if constexpr (SYMMETRIC) {
-        uint16_t *out = STEP == Step::Gram ? gram : poly;
+        typedef Symmetric<STEP> S;
         const float b = __builtin_fmaf(2.0f * p.c, shift, p.b);
-        visit_tile(acc, p.m, N, mw, nw, lane, staging, [&](int64_t r, int64_t c, int count, float(&v)[8]) {
-            if constexpr (STEP == Step::Gram) {
-                const float s = f * f / X_SCALE;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = s * v[e] - (r == c + e ? X_SCALE * shift : 0.0f);
-            } else {
-                float g[8];
-                load8<F16>(gram + r * p.lda + c, count, g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(p.c * 0x1p-16f, v[e], b * 0x1p-4f * g[e]);
-            }
-            store8<F16>(out + r * p.lda + c, count, v);
-        });
+        S put{gram, STEP == Step::Gram ? gram : poly, p.lda, STEP == Step::Gram ? f * f / X_SCALE : p.c * 0x1p-16f,
+              STEP == Step::Gram ? X_SCALE * shift : b * 0x1p-4f};
+        visit_tile(acc, p.m, N, mw, nw, lane, staging, put);
         // the same values on the other side of the diagonal
-        if (n0 > m0)
-            visit_tile_turned(acc, p.m, p.m, mw, nw, lane, staging, [&](int64_t r, int64_t c, int count, float(&v)[8]) {
-                if constexpr (STEP == Step::Gram) {
-                    const float s = f * f / X_SCALE;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= s;
-                } else {
-                    float g[8];
-                    load8<F16>(gram + r * p.lda + c, count, g);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(p.c * 0x1p-16f, v[e], b * 0x1p-4f * g[e]);
-                }
-                store8<F16>(out + r * p.lda + c, count, v);
-            });
+        if (n0 > m0) visit_tile_turned(acc, p.m, p.m, mw, nw, lane, staging, put);
     } else {
-        uint16_t *lo = p.lo + batch * p.m * p.ldx, *next = p.next + batch * p.m * p.ldx;
-        const float a = __builtin_fmaf(shift, __builtin_fmaf(shift, p.c, p.b), p.a);
-        float square = 0.0f;
-        if (live) visit_tile(acc, p.m, N, mw, nw, lane, staging, [&](int64_t r, int64_t c, int count, float(&v)[8]) {
-            float h[8], l[8];
-            const int64_t at = r * p.ldx + c;
-            load8<F16>(x + at, count, h);
-            load8<F16>(lo + at, count, l);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = f * __builtin_fmaf(0x1p-8f, v[e], a * (h[e] + l[e]));
-            if (!p.last) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    square += v[e] * v[e];
-                    l[e] = v[e] - decode<F16>(encode<F16>(v[e]));
-                }
-                store8<F16>(next + at, count, v);
-                store8<F16>(lo + at, count, l);
-                return;
-            }
-            const float s = p.alpha / X_SCALE;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (c + e >= p.n) continue;
-                const int64_t o = batch * p.strideO + (p.turned ? (c + e) * p.ldo + r : r * p.ldo + c + e);
-                put_output(p, o, s * v[e]);
-            }
-        });
+        const int64_t at = batch * p.m * p.ldx;
+        Updated put{p, x, p.lo + at, p.next + at, batch * p.strideO, f,
+                    __builtin_fmaf(shift, __builtin_fmaf(shift, p.c, p.b), p.a), 0.0f};
+        if (live) visit_tile(acc, p.m, N, mw, nw, lane, staging, put);
+        float square = put.square;
         if (p.last) return;
         for (int d = 1; d < 64; d *= 2) square += __shfl_xor(square, d);
         if (lane == 0) sums[wave] = square;
@@ -370,12 +385,18 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
     LDS char *x = (LDS char *)smem, *gram = x + mp * a.pitch_x, *poly = gram + mp * a.pitch_a;
     // the norm, in 64 bits
     double q = 0.0;
-    for (int64_t r = wave; r < in.M; r += SMALL_WAVES)
+    for (int64_t r0 = wave; r0 < in.M; r0 += 8 * SMALL_WAVES)
         for (int64_t c = 4 * lane; c < in.N; c += 256) {
-            float v[4];
-            values_of<4>(in, batch * in.strideG + r * in.ldg + c, in.N - c, v);
+            float v[8][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) q = __builtin_fma(double(v[e]), double(v[e]), q);
+            for (int i = 0; i < 8; ++i) {
+                const int64_t r = r0 + i * SMALL_WAVES;
+                values_of<4>(in, batch * in.strideG + r * in.ldg + c, r < in.M ? in.N - c : 0, v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) q = __builtin_fma(double(v[i][e]), double(v[i][e]), q);
         }
     for (int d = 1; d < 64; d *= 2) q += __shfl_xor(q, d);
     if (lane == 0) scratch[wave] = q;
@@ -428,7 +449,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
         for (int block = wave; block < blocks_a; block += SMALL_WAVES) {
             const int bi = block / a.blocks_m * 32, bj = block % a.blocks_m * 32;
             f32x16 acc = {};
-#pragma unroll 2
+#pragma unroll 4
             for (int k = 0; k < np; k += 16)
                 acc = mfma32<F16>(frag_rows(x, a.pitch_x, bj, k, lane), frag_rows(x, a.pitch_x, bi, k, lane), acc);
 #pragma unroll
@@ -448,7 +469,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
         for (int block = wave; block < blocks_a; block += SMALL_WAVES) {
             const int bi = block / a.blocks_m * 32, bj = block % a.blocks_m * 32;
             f32x16 acc = {};
-#pragma unroll 2
+#pragma unroll 4
             for (int k = 0; k < mp; k += 16)
                 acc = mfma32<F16>(frag_rows(gram, a.pitch_a, bj, k, lane), frag_rows(gram, a.pitch_a, bi, k, lane), acc);
 #pragma unroll
@@ -471,7 +492,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
             if (block >= blocks) continue;
             const int bi = block / a.blocks_n * 32, bj = block % a.blocks_n * 32;
             f32x16 acc = {};
-#pragma unroll 2
+#pragma unroll 4
             for (int k = 0; k < mp; k += 16)
                 acc = mfma32<F16>(frag_columns(x, a.pitch_x, bj, k, lane), frag_rows(poly, a.pitch_a, bi, k, lane), acc);
 #pragma unroll
@@ -558,21 +579,27 @@ hipError_t launch_small(const SmallArgs &a, size_t lds, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Tiles of 256, 192 (symmetric products) or 128, whichever takes the least
-// time by whole rounds of workgroups.  REPLACE
-enum class Size { Large, Middle, Small, Few };
+// Tiles of 256, 192 (symmetric products) or 128, whichever takes the least time
+// by whole rounds of workgroups: one of 256 or 192 per compute unit, two of 128.
+// 4096 x 4096: A and B of 192 (253 tiles) 98 and 102 us, of 256 (136) 111 and 114,
+// of 128 (528) 111 and 115; X of 256 (256 tiles) 146, of 128 160.
+// What fits into one round of one 128 tile per unit takes a ring of four stages
+// instead of two (1000 x 2049: A 26 us for 32, X 20 for 21); symmetric products
+// that leave half the units idle then take 64 tiles (A 15 us for 26, B 11 for 18).
+enum class Size { Large, Middle, Small, Few, Least };
 Size size_of(int64_t m, int64_t n, int64_t batch, bool symmetric) {
     auto tiles = [&](int64_t side) {
         const int64_t r = ceil_div(m, side), c = ceil_div(n, side);
         return batch * (symmetric ? r * (r + 1) / 2 : r * c);
     };
+    if (symmetric && tiles(128) <= 128) return Size::Least;
     if (tiles(128) <= 256) return Size::Few;
     const int64_t large = ceil_div(tiles(256), 256) * 64, small = ceil_div(tiles(128), 512) * 40;
     const int64_t middle = symmetric ? ceil_div(tiles(192), 256) * 42 : INT64_MAX;
     if (middle < large && middle < small) return Size::Middle;
     return large <= small ? Size::Large : Size::Small;
 }
-int64_t side_of(Size s) { return s == Size::Large ? 256 : s == Size::Middle ? 192 : 128; }
+int64_t side_of(Size s) { return s == Size::Large ? 256 : s == Size::Middle ? 192 : s == Size::Least ? 64 : 128; }
 
 template <class Shape, Step STEP>
 hipError_t launch_shape(OrthoArgs &a, int64_t tiles, hipStream_t stream) {
@@ -587,6 +614,7 @@ hipError_t launch_product(OrthoArgs &a, hipStream_t stream) {
     using Middle = Tile<F16, 192, 192, 2, 2, true, true, true, 64, 3>;
     using Small = Tile<F16, 128, 128, 2, 2, true, SYMMETRIC, true>;
     using Few = Tile<F16, 128, 128, 2, 2, true, SYMMETRIC, true, 64, 4>;
+    using Least = Tile<F16, 64, 64, 2, 2, true, true, true, 64, 4>;
     const int64_t cols = SYMMETRIC ? a.m : a.n;
     const Size size = size_of(a.m, cols, a.batch, SYMMETRIC);
     a.tiles_m = ceil_div(a.m, side_of(size));
@@ -597,7 +625,8 @@ hipError_t launch_product(OrthoArgs &a, hipStream_t stream) {
     if (size == Size::Large) return launch_shape<Large, STEP>(a, tiles, stream);
     if (size == Size::Small) return launch_shape<Small, STEP>(a, tiles, stream);
     if (size == Size::Few) return launch_shape<Few, STEP>(a, tiles, stream);
-    if constexpr (SYMMETRIC) return launch_shape<Middle, STEP>(a, tiles, stream);
+    if constexpr (SYMMETRIC)
+        return size == Size::Middle ? launch_shape<Middle, STEP>(a, tiles, stream) : launch_shape<Least, STEP>(a, tiles, stream);
     return hipSuccess;
 }
 

@@ -3,9 +3,8 @@
 // cores, into fp32 accumulators, and a walk over the finished tile in whole
 // pieces of rows for an epilogue.
 //
-// It is the schedule of hgemm_mfma_dma.hip (two LDS stages of 64 k, refilled
-// behind one barrier per stage, fragments double-buffered in registers) over
-// panels of any number of rows.  DIRECT panels are filled by direct
+// A ring of LDS stages of 64 k, refilled behind one barrier per stage, and
+// fragments double-buffered in registers, over panels of any number of rows.  DIRECT panels are filled by direct
 // global -> LDS loads and need whole 16-byte chunks; the others go through
 // registers and take any alignment and extent.  Both leave the same layout:
 //   K-contiguous panel: [rows][64 k], 128 bytes per row, 16-byte chunk c of
@@ -15,6 +14,8 @@
 // Addresses inside a tile are 32-bit offsets from the tile's own base, so an
 // operand may be of any size.
 #pragma once
+
+#include <type_traits>
 
 #include "dma_tile.hpp"
 
@@ -126,6 +127,44 @@ __device__ inline void store8_as(void *p, int64_t at, bool same, int n, const fl
     if (same) store8<T>(static_cast<uint16_t *>(p) + at, n, x);
     else store8f(static_cast<float *>(p) + at, n, x);
 }
+
+// The same loads, kept as they come until they are needed.
+struct Raw8 {
+    u32x4 v;
+    __device__ void load(const uint16_t *p, int n) {
+        if (n == 8) {
+            v = *reinterpret_cast<const u32x4_ea *>(p);
+        } else {
+            v = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (e < n) v[e / 2] |= uint32_t(p[e]) << (16 * (e % 2));
+        }
+    }
+    // 16-bit values
+    template <class T>
+    __device__ void values(float (&x)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = decode<T>(v[e / 2] >> (16 * (e % 2)) & 0xffffu);
+    }
+};
+// Element `it` of four, without an array in memory.
+template <class D>
+__device__ inline D pick(const D (&d)[4], int it) {
+    D r = d[0];
+    constexpr int WORDS = sizeof(D) / 4;
+    uint32_t *to = reinterpret_cast<uint32_t *>(&r);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        const uint32_t *from = reinterpret_cast<const uint32_t *>(&d[i]);
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) to[w] = it == i ? from[w] : to[w];
+    }
+    return r;
+}
+struct Nothing {
+    uint32_t unused;
+};
 
 // Leading dimensions (elements) whose tiles' offsets stay below 2^31 bytes:
 // 256 rows of a K-contiguous panel, 64 of the other.
@@ -308,12 +347,39 @@ struct Tile {
             for (int j = 0; j < FN; ++j) acc[i][j] = mfma32<T>(fb[j], fa[i], acc[i][j]);
     }
 
+    // One k step: the matrix instructions on the fragments of slot SLOT in order,
+    // and between them, evenly, the reads of the next step's fragments (step kk
+    // of `stage`) into the other slot and whatever `also(q)` issues after the
+    // q-th.  The order is kept: left to itself the compiler bunches the loads
+    // behind the instructions (192 x 192 tiles, 4096 x 4096 x 4096: 102 us, so 96).
+    template <int SLOT, class Also>
+    static __device__ __forceinline__ void step(u32x4 (&fa)[2][FM], u32x4 (&fb)[2][FN], const LDS char *stage,
+                                                int wm, int wn, int kk, int lane, Acc &acc, Also also) {
+        constexpr int N = FM * FN, READS = FM + FN;
+        constexpr int EACH = (READS + N - 1) / N, EVERY = N > READS ? N / READS : 1;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            const int i = q / FN, j = q % FN;
+            acc[i][j] = mfma32<T>(fb[SLOT][j], fa[SLOT][i], acc[i][j]);
+#pragma unroll
+            for (int u = 0; u < EACH; ++u) {
+                const int r = q / EVERY * EACH + u;  // in the order the next step uses them
+                if (q % EVERY != 0 || r >= READS) continue;
+                if (r < FN) fb[SLOT ^ 1][r] = PB::frag(stage + PA::BYTES, wn * WTN + r * 32, kk, lane);
+                else fa[SLOT ^ 1][r - FN] = PA::frag(stage, wm * WTM + (r - FN) * 32, kk, lane);
+            }
+            also(q);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
     static __device__ __forceinline__ int run_direct(const PA &pa, const PB &pb, int64_t K, int64_t s0,
                                                      int64_t s1, LDS char *lds, Acc &acc, int wm, int wn,
                                                      int wave, int lane) {
-        constexpr int KK = BK / 16;
+        constexpr int KK = BK / 16, N = FM * FN;
+        static_assert(KK % 2 == 0, "a stage's first fragments are in slot 0");
         constexpr int PER_STAGE = PA::PER_WAVE + PB::PER_WAVE;
-        constexpr int NREAD = FM * (A_KMAJOR ? 1 : 2) + FN * (B_KMAJOR ? 1 : 2);
         const int64_t steps = s1 - s0;
 #pragma unroll
         for (int st = 0; st < STAGES; ++st) {
@@ -331,48 +397,48 @@ struct Tile {
         // also says that this buffer has been read), reads that stage's first
         // fragments and refills this buffer between its matrix instructions.
         int buf = 0;
-        for (int64_t s = 0; s < steps - 1; ++s) {
+        auto nothing = [](int) {};
+        auto multiply = [&](int64_t s, auto refills) {
             LDS char *stage = lds + buf * STAGE;
+            const int next = buf + 1 == STAGES ? 0 : buf + 1;
 #pragma unroll
             for (int kk = 0; kk < KK - 1; ++kk) {
-                read(fa[(kk & 1) ^ 1], fb[(kk & 1) ^ 1], stage, wm, wn, kk + 1, lane);
-                mfmas(fa[kk & 1], fb[kk & 1], acc);
-                interleave_reads<NREAD, FM * FN>();
+                if (kk & 1) step<1>(fa, fb, stage, wm, wn, kk + 1, lane, acc, nothing);
+                else step<0>(fa, fb, stage, wm, wn, kk + 1, lane, acc, nothing);
             }
-            constexpr int LAST = (KK - 1) & 1;
-            const int64_t later = steps - 2 - s;
-            wait_stages<PER_STAGE, STAGES>(int(later < STAGES - 2 ? later : STAGES - 2));
-            wait_lgkmcnt0();
-            __syncthreads();
-            const int next = buf + 1 == STAGES ? 0 : buf + 1;
-            read(fa[LAST ^ 1], fb[LAST ^ 1], lds + next * STAGE, wm, wn, 0, lane);
-            const int64_t refill = s0 + s + STAGES;
-            const bool more = refill < s1;
-            const u32x4 ra = pa.rsrc(refill), rb = pb.rsrc(refill);
-            const uint32_t la = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(stage));
-            const int64_t kleft = K - refill * BK;
-            constexpr int PER_MFMA = (PER_STAGE + FM * FN - 1) / (FM * FN);
+            if constexpr (decltype(refills)::value) {
+                const int64_t refill = s0 + s + STAGES;
+                const u32x4 ra = pa.rsrc(refill), rb = pb.rsrc(refill);
+                const uint32_t la = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(stage));
+                const int64_t kleft = K - refill * BK;
+                wait_vmcnt<(STAGES - 2) * PER_STAGE>();
+                wait_lgkmcnt0();
+                __syncthreads();
+                step<1>(fa, fb, lds + next * STAGE, wm, wn, 0, lane, acc, [&](int q) {
+                    constexpr int EACH = (PER_STAGE + N - 1) / N;
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    acc[i][j] = mfma32<T>(fb[LAST][j], fa[LAST][i], acc[i][j]);
-                    if (more) {
-#pragma unroll
-                        for (int u = 0; u < PER_MFMA; ++u) {
-                            const int q = (i * FN + j) * PER_MFMA + u;
-                            if (q < PA::PER_WAVE) pa.load(ra, la, q, kleft, wave);
-                            else if (q < PER_STAGE) pb.load(rb, la + PA::BYTES, q - PA::PER_WAVE, kleft, wave);
-                        }
+                    for (int u = 0; u < EACH; ++u) {
+                        const int l = q * EACH + u;
+                        if (l < PA::PER_WAVE) pa.load(ra, la, l, kleft, wave);
+                        else if (l < PER_STAGE) pb.load(rb, la + PA::BYTES, l - PA::PER_WAVE, kleft, wave);
                     }
-                }
+                });
+            } else {
+                const int64_t later = steps - 2 - s;
+                wait_stages<PER_STAGE, STAGES>(int(later < STAGES - 2 ? later : STAGES - 2));
+                wait_lgkmcnt0();
+                __syncthreads();
+                step<1>(fa, fb, lds + next * STAGE, wm, wn, 0, lane, acc, nothing);
+            }
             buf = next;
-        }
+        };
+        int64_t s = 0;
+        for (; s < steps - STAGES; ++s) multiply(s, std::true_type{});
+        for (; s < steps - 1; ++s) multiply(s, std::false_type{});
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             if (kk < KK - 1) read(fa[(kk & 1) ^ 1], fb[(kk & 1) ^ 1], lds + buf * STAGE, wm, wn, kk + 1, lane);
             mfmas(fa[kk & 1], fb[kk & 1], acc);
-            interleave_reads<NREAD, FM * FN>();
         }
         return buf;
     }
@@ -417,20 +483,35 @@ struct Tile {
 };
 
 // Walks one wave's finished tile (top left at (mw, nw)) in pieces of 8
-// columns: f(m, n, count, x) for every piece with m < M and n < N, count =
+// columns: f(m, n, count, x, data) for every piece with m < M and n < N, count =
 // min(8, N - n), x its fp32 accumulators.  Each strip of 32 rows passes
 // through the wave's own LDS (chunk c of row r at c ^ (r mod 16)), so that a
 // lane's piece is contiguous and eight lanes have a row: the epilogue's loads and
 // stores move whole rows of 64 columns.  A lane sees the same columns,
 // nw + 8*(lane % (FN*4)), in every call.
+//
+// What the epilogue reads, f.load(data, m, n, count), is asked for a strip
+// ahead: read where it is needed, each of a tile's 16 pieces per lane would
+// wait for memory by itself.
 template <int FM, int FN, class F>
 __device__ __forceinline__ void visit_tile(const f32x16 (&acc)[FM][FN], int64_t M, int64_t N, int64_t mw,
                                            int64_t nw, int lane, LDS float *scratch, F &&f) {
-    constexpr int W = FN * 32, SWZ = W / 4 - 1 < 15 ? W / 4 - 1 : 15;
-    constexpr int CPR = W / 8, RPI = 64 / CPR;
+    constexpr int W = FN * 32, SWZ = W == 96 ? 7 : W / 4 - 1 < 15 ? W / 4 - 1 : 15;  // stays within the row
+    // rows of 96 columns take 12 lanes each, four rows at a time
+    constexpr int CPR = W / 8, RPI = CPR == 12 ? 4 : 64 / CPR, ITS = 32 / RPI, AHEAD = 4;
+    static_assert(32 % RPI == 0 && CPR * RPI <= 64, "strip shape");
+    typedef typename std::remove_reference_t<F>::Data Data;
     auto at = [&](int r, int col) { return scratch + r * W + (((col >> 2) ^ (r & SWZ)) << 2); };
     const int64_t n = nw + (lane % CPR) * 8;
-    const int count = N - n < 8 ? int(N - n) : 8;
+    const int count = lane >= CPR * RPI ? 0 : N - n < 8 ? int(N - n) : 8;
+    auto row_of = [&](int i, int it) { return mw + i * 32 + it * RPI + lane / CPR; };
+    Data data[2][AHEAD];
+    auto load = [&](int i, int it0, Data (&d)[AHEAD]) {
+#pragma unroll
+        for (int it = 0; it < AHEAD; ++it)
+            if (it0 + it < ITS && row_of(i, it0 + it) < M && count > 0) f.load(d[it], row_of(i, it0 + it), n, count);
+    };
+    load(0, 0, data[0]);
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -440,52 +521,75 @@ __device__ __forceinline__ void visit_tile(const f32x16 (&acc)[FM][FN], int64_t 
                 const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
                 *reinterpret_cast<LDS f32x4 *>(at(lane & 31, j * 32 + q * 8 + 4 * (lane >> 5))) = v;
             }
+#pragma unroll
+        for (int it0 = 0; it0 < ITS; it0 += AHEAD) {
+            constexpr int GROUPS = (ITS + AHEAD - 1) / AHEAD;
+            const int g = i * GROUPS + it0 / AHEAD;
+            if (it0 + AHEAD < ITS) load(i, it0 + AHEAD, data[(g + 1) % 2]);
+            else if (i + 1 < FM) load(i + 1, 0, data[(g + 1) % 2]);
 #pragma unroll 1
-        for (int it = 0; it < 32 / RPI; ++it) {
-            const int r = it * RPI + lane / CPR;
-            const int64_t m = mw + i * 32 + r;
-            float x[8];
+            for (int it = 0; it < (ITS - it0 < AHEAD ? ITS - it0 : AHEAD); ++it) {
+                const int r = (it0 + it) * RPI + lane / CPR;
+                float x[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const f32x4 v = *reinterpret_cast<const LDS f32x4 *>(at(r, (lane % CPR) * 8 + 4 * h));
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4 v = *reinterpret_cast<const LDS f32x4 *>(at(r, (lane % CPR) * 8 + 4 * h));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
+                    for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
+                }
+                const Data d = pick(data[g % 2], it);
+                if (mw + i * 32 + r < M && count > 0) f(mw + i * 32 + r, n, count, x, d);
             }
-            if (m < M && count > 0) f(m, n, count, x);
         }
     }
 }
 
-// The same tile turned: f(n, m, count, x) for pieces of 8 rows of a column n,
-// count = min(8, M - m), through strips of 32 columns by up to 64 rows.
+// The same tile turned: f(n, m, count, x, data) for pieces of 8 rows of a
+// column n, count = min(8, M - m), through strips of 32 columns by up to 64 rows.
 template <int FM, int FN, class F>
 __device__ __forceinline__ void visit_tile_turned(const f32x16 (&acc)[FM][FN], int64_t M, int64_t N, int64_t mw,
                                                   int64_t nw, int lane, LDS float *scratch, F &&f) {
+    constexpr int HIGH = FM < 2 ? 1 : 2, W = HIGH * 32, CPR = W / 8, RPI = 64 / CPR, ITS = 32 / RPI;
+    constexpr int STRIPS = (FM + HIGH - 1) / HIGH;
+    typedef typename std::remove_reference_t<F>::Data Data;
+    const int c = (lane % CPR) * 8;
+    Data data[2][4];
+    auto load = [&](int strip, Data (&d)[4]) {
+        const int j = strip / STRIPS, i0 = strip % STRIPS * HIGH;
+        const int64_t m = mw + i0 * 32 + c;
+        const bool live = m < M && i0 * 32 + c < FM * 32;
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int i0 = 0; i0 < FM; i0 += 2) {
-            constexpr int W = 64;
-            const int wide = FM - i0 < 2 ? 32 : 64;
-#pragma unroll
-            for (int i = i0; i < i0 + 2 && i < FM; ++i)
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    scratch[(8 * (e / 4) + 4 * (lane >> 5) + e % 4) * W + (i - i0) * 32 + (lane & 31)] = acc[i][j][e];
-#pragma unroll 1
-            for (int it = 0; it < 4; ++it) {
-                const int r = it * 8 + lane / 8, c = (lane % 8) * 8;
-                const int64_t n = nw + j * 32 + r, m = mw + i0 * 32 + c;
-                float x[8];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const f32x4 v = *reinterpret_cast<const LDS f32x4 *>(scratch + r * W + c + 4 * h);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
-                }
-                if (n < N && m < M && c < wide) f(n, m, M - m < 8 ? int(M - m) : 8, x);
-            }
+        for (int it = 0; it < ITS; ++it) {
+            const int64_t n = nw + j * 32 + it * RPI + lane / CPR;
+            if (live && n < N) f.load(d[it], n, m, M - m < 8 ? int(M - m) : 8);
         }
+    };
+    load(0, data[0]);
+#pragma unroll
+    for (int strip = 0; strip < FN * STRIPS; ++strip) {
+        const int j = strip / STRIPS, i0 = strip % STRIPS * HIGH;
+#pragma unroll
+        for (int i = i0; i < i0 + HIGH && i < FM; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                scratch[(8 * (e / 4) + 4 * (lane >> 5) + e % 4) * W + (i - i0) * 32 + (lane & 31)] = acc[i][j][e];
+        if (strip + 1 < FN * STRIPS) load(strip + 1, data[(strip + 1) % 2]);
+        const int64_t m = mw + i0 * 32 + c;
+        const bool live = m < M && i0 * 32 + c < FM * 32;
+#pragma unroll 1
+        for (int it = 0; it < ITS; ++it) {
+            const int r = it * RPI + lane / CPR;
+            float x[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 v = *reinterpret_cast<const LDS f32x4 *>(scratch + r * W + c + 4 * h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
+            }
+            const Data d = pick(data[strip % 2], it);
+            if (live && nw + j * 32 + r < N) f(nw + j * 32 + r, m, M - m < 8 ? int(M - m) : 8, x, d);
+        }
+    }
 }
 
 }  // namespace tile16

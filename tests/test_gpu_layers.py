@@ -470,6 +470,12 @@ def test_orthogonalize_batches(lib, M, N, batch):
     run_ortho(lib, M, N, batch=batch, beta=1.0)
 
 
+@pytest.mark.parametrize("M,N,batch", [(190, 200, 200), (250, 250, 128), (250, 130, 128), (260, 250, 60), (250, 260, 250)])
+def test_orthogonalize_every_tile(lib, M, N, batch):
+    """The symmetric products' tiles of 192, 128 in two rounds and in one, and 256."""
+    run_ortho(lib, M, N, batch=batch, steps=3)
+
+
 def test_orthogonalize_large(lib):
     """Enough tiles of 256 x 256 for the large kernel, ragged."""
     assert lib.orthogonalize_kernel_name(3600, 3590, 1) == "orthogonalize_mfma_256"
