@@ -12,12 +12,6 @@
 
 #include "arg_checks.hpp"
 #include "gemm_problem.hpp"
-
-namespace libgemm {
-// The copies of both operands of a packed plan in one launch (pack.hip).
-hipError_t launch_pack2(const PackSpec &sa, void *dst_a, const PackSpec &sb, void *dst_b,
-                        hipStream_t stream);
-}  // namespace libgemm
 #include "libgemm.h"
 
 using namespace libgemm;

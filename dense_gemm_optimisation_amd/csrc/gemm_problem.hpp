@@ -80,6 +80,9 @@ struct PackSpec {
 };
 int64_t packed_bytes(const PackSpec &s);
 hipError_t launch_pack(const PackSpec &s, void *dst, hipStream_t stream);
+// The copies of two operands in one launch.
+hipError_t launch_pack2(const PackSpec &sa, void *dst_a, const PackSpec &sb, void *dst_b,
+                        hipStream_t stream);
 
 // fp32 operands split into bf16 pieces for the three-product fp32 GEMM
 // (split_bf16.hip): Kp = K rounded up to a multiple of 8; a copy holds

@@ -36,8 +36,9 @@ struct LinearProblem {
     float beta_bias;
     void *workspace;
     size_t workspace_bytes;
+    bool packed;  // A and B are copies with rows of whole chunks, filled with zeros
 };
-enum class LinearKernel { None, Few16, Tile256, Tile128, Split, Any, AnySplit };
+enum class LinearKernel { None, Few16, Tile256, Rounds, Tile128, Split, Any, AnySplit, Packed };
 const char *linear_kernel_name(LinearKernel k);
 LinearKernel linear_choose(const LinearProblem &p);
 size_t linear_workspace(int64_t M, int64_t N, int64_t K);

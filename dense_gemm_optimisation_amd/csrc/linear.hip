@@ -8,6 +8,8 @@
 //                    two workgroups per compute unit (tile16.hpp).  The epilogue reads and
 //                    writes whole rows of 64 columns and costs what its bytes
 //                    cost;
+//   rounds           the 256 x 256 tiles where the last of several rounds is less
+//                    than half full: its tiles are cut into slices of K;
 //   split            the 128 x 128 tiles with K cut into slices, each slice's
 //                    sums in the workspace, joined in order by finish_kernel,
 //                    which also has the epilogue: problems of few tiles;
@@ -15,11 +17,13 @@
 //                    workgroup, K dealt to eight waves, operands straight
 //                    into registers; bound by reading B;
 //   any              the 128 x 128 tiles with panels through registers, for
-//                    operands of any alignment.
+//                    operands of any alignment; larger problems copy such
+//                    operands into the workspace first (pack.hip).
 // Column sums: each wave (or finish workgroup) leaves the sums over its rows
 // in the workspace, and sums_kernel adds them in order: no atomics, the same
 // result on every run.
 #include "activation.hpp"
+#include "gemm_problem.hpp"
 #include "layers.hpp"
 #include "tile16.hpp"
 
@@ -42,8 +46,9 @@ struct LinearArgs {
     int act;
     bool c_same;     // C (and R) have the inputs' type, else fp32
     TileGrid grid;   // batch: slices of K
+    int64_t first, tiles;  // of the grid, those that a launch has
     float *sums;     // backward: column sums by rows of blocks, N each
-    float *partial;  // split: [slice][M][ldp]
+    float *partial;  // split: [slice][M][ldp]; the last tiles': [slice][tile][256][256]
     int64_t ldp;
     int slices;
 };
@@ -111,7 +116,7 @@ template <class T, class Shape, bool BACKWARD>
 __global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void tile_kernel(LinearArgs p) {
     __shared__ __attribute__((aligned(1024))) char smem[Shape::LDS_BYTES];
     LDS char *lds = (LDS char *)smem;
-    const TileCoord t = tile_of(p.grid, blockIdx.x);
+    const TileCoord t = tile_of(p.grid, p.first + xcd_remap(blockIdx.x, p.tiles, 8));
     const int64_t m0 = uniform(t.tm) * Shape::TM, n0 = uniform(t.tn) * Shape::TN;
     typename Shape::Acc acc;
     const int buf = Shape::run(p.a, p.b, p.K, m0, n0, 0, (p.K + Shape::BK - 1) / Shape::BK, lds, acc);
@@ -126,7 +131,18 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::THREADS == 512 ? 1 : 2) void
     finish.write_sums(mw / Shape::WTM, n, LANES, lane);
 }
 
-// One slice of K of a tile: its sums go to the workspace.
+// What a slice of K leaves in the workspace: its sums, element (m, n) at out[m * ld + n].
+struct Partial {
+    typedef Nothing Data;
+    float *out;
+    int64_t ld;
+    __device__ void load(Data &, int64_t, int64_t, int) const {}
+    __device__ void operator()(int64_t m, int64_t n, int count, const float (&x)[8], const Data &) const {
+        store8f(out + m * ld + n, count, x);
+    }
+};
+
+// One slice of K of a tile.
 template <class Shape>
 __global__ __launch_bounds__(Shape::THREADS, 2) void split_kernel(LinearArgs p) {
     __shared__ __attribute__((aligned(1024))) char smem[Shape::LDS_BYTES];
@@ -140,16 +156,82 @@ __global__ __launch_bounds__(Shape::THREADS, 2) void split_kernel(LinearArgs p) 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t mw = m0 + Shape::wave_m(wave) * Shape::WTM, nw = n0 + Shape::wave_n(wave) * Shape::WTN;
     if (mw >= p.M || nw >= p.N) return;
-    struct Store {
-        typedef Nothing Data;
-        float *out;
-        int64_t ld;
-        __device__ void load(Data &, int64_t, int64_t, int) const {}
-        __device__ void operator()(int64_t m, int64_t n, int count, const float (&x)[8], const Data &) const {
-            store8f(out + m * ld + n, count, x);
-        }
-    };
-    visit_tile(acc, p.M, p.N, mw, nw, lane, Shape::staging(lds, buf, wave), Store{p.partial + z * p.M * p.ldp, p.ldp});
+    visit_tile(acc, p.M, p.N, mw, nw, lane, Shape::staging(lds, buf, wave), Partial{p.partial + z * p.M * p.ldp, p.ldp});
+}
+
+// One slice of K of one of the tiles from p.first on.
+template <class Shape>
+__global__ __launch_bounds__(Shape::THREADS, 1) void last_kernel(LinearArgs p) {
+    __shared__ __attribute__((aligned(1024))) char smem[Shape::LDS_BYTES];
+    LDS char *lds = (LDS char *)smem;
+    const int64_t tile = blockIdx.x / p.slices, z = blockIdx.x % p.slices;
+    const TileCoord t = tile_of(p.grid, p.first + tile);
+    const int64_t m0 = uniform(t.tm) * Shape::TM, n0 = uniform(t.tn) * Shape::TN;
+    const int64_t stages = (p.K + Shape::BK - 1) / Shape::BK;
+    typename Shape::Acc acc;
+    const int buf = Shape::run(p.a, p.b, p.K, m0, n0, stages * z / p.slices, stages * (z + 1) / p.slices, lds, acc);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t mw = m0 + Shape::wave_m(wave) * Shape::WTM, nw = n0 + Shape::wave_n(wave) * Shape::WTN;
+    if (mw >= p.M || nw >= p.N) return;
+    float *out = p.partial + (z * p.tiles + tile) * (Shape::TM * Shape::TN);
+    visit_tile(acc, p.M, p.N, mw, nw, lane, Shape::staging(lds, buf, wave), Partial{out - (m0 * Shape::TN + n0), Shape::TN});
+}
+
+// The sums of a workgroup of four waves over 64 columns, eight per lane, as row
+// `block` of the sums; n0 is the first column.
+template <class T, bool BACKWARD>
+__device__ inline void join_sums(Finish<T, BACKWARD> &finish, float (&waves)[4][64], int64_t block, int64_t n0) {
+    if (!BACKWARD || finish.p.sums == nullptr) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int d = 8; d < 64; d *= 2)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) finish.column[e] += __shfl_xor(finish.column[e], d);
+    if (lane < 8)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) waves[wave][lane * 8 + e] = finish.column[e];
+    __syncthreads();
+    if (wave == 0 && n0 + lane < finish.p.N)
+        finish.p.sums[block * finish.p.N + n0 + lane] = waves[0][lane] + waves[1][lane] + (waves[2][lane] + waves[3][lane]);
+}
+
+// Joins their slices: 64 columns of 128 rows per workgroup.
+template <class T, class Shape, bool BACKWARD>
+__global__ __launch_bounds__(256) void last_finish_kernel(LinearArgs p) {
+    __shared__ float waves[4][64];
+    const TileCoord t = tile_of(p.grid, p.first + blockIdx.z);
+    const int64_t m0 = t.tm * Shape::TM + blockIdx.y * Shape::WTM, n0 = t.tn * Shape::TN;
+    if (m0 >= p.M || n0 + blockIdx.x * 64 >= p.N) return;
+    const int64_t n = n0 + blockIdx.x * 64 + (threadIdx.x % 8) * 8;
+    const int count = p.N - n < 8 ? int(p.N - n) : 8;
+    const float *base = p.partial + blockIdx.z * (Shape::TM * Shape::TN);
+    Finish<T, BACKWARD> finish(p, n);
+    // four rows of each lane at a time: their loads all go out first
+    constexpr int ROWS = Shape::WTM / 32;
+    const float *at = base + (blockIdx.y * Shape::WTM + threadIdx.x / 8) * Shape::TN + (n - n0);
+    auto live = [&](int i) { return m0 + i * 32 + threadIdx.x / 8 < p.M && count > 0; };
+    float x[ROWS][8], part[ROWS][8];
+    Raw8 data[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        if (!live(i)) continue;
+        finish.load(data[i], m0 + i * 32 + threadIdx.x / 8, n, count);
+        load8f(at + i * 32 * Shape::TN, 8, x[i]);  // whole: the workspace's rows are
+    }
+    for (int s = 1; s < p.slices; ++s) {
+        const float *next = at + s * p.tiles * (Shape::TM * Shape::TN);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (live(i)) load8f(next + i * 32 * Shape::TN, 8, part[i]);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i][e] += part[i][e];
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+        if (live(i)) finish(m0 + i * 32 + threadIdx.x / 8, n, count, x[i], data[i]);
+    join_sums(finish, waves, m0 / Shape::WTM, n0 + blockIdx.x * 64);
 }
 
 // Joins the slices: 64 columns by FINISH_ROWS rows per workgroup.
@@ -157,7 +239,6 @@ constexpr int FINISH_ROWS = 32;
 template <class T, bool BACKWARD>
 __global__ __launch_bounds__(256) void finish_kernel(LinearArgs p) {
     __shared__ float waves[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t n = int64_t(blockIdx.x) * 64 + (threadIdx.x % 8) * 8;
     const int64_t m = int64_t(blockIdx.y) * FINISH_ROWS + threadIdx.x / 8;
     const int count = p.N - n < 8 ? int(p.N - n) : 8;
@@ -167,25 +248,15 @@ __global__ __launch_bounds__(256) void finish_kernel(LinearArgs p) {
         const float *at = p.partial + m * p.ldp + n;
         Raw8 data;
         finish.load(data, m, n, count);
-        load8f(at, count, x);
+        load8f(at, 8, x);  // whole: the workspace's rows are
         for (int s = 1; s < p.slices; ++s) {
-            load8f(at + s * p.M * p.ldp, count, part);
+            load8f(at + s * p.M * p.ldp, 8, part);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += part[e];
         }
         finish(m, n, count, x, data);
     }
-    if (!BACKWARD || p.sums == nullptr) return;
-    for (int d = 8; d < 64; d *= 2)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) finish.column[e] += __shfl_xor(finish.column[e], d);
-    if (lane < 8)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) waves[wave][lane * 8 + e] = finish.column[e];
-    __syncthreads();
-    const int64_t j = int64_t(blockIdx.x) * 64 + lane;
-    if (wave == 0 && j < p.N)
-        p.sums[blockIdx.y * p.N + j] = waves[0][lane] + waves[1][lane] + (waves[2][lane] + waves[3][lane]);
+    join_sums(finish, waves, blockIdx.y, int64_t(blockIdx.x) * 64);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -386,16 +457,48 @@ int split_slices(int64_t tiles, int64_t K) {
     return int(s < 1 ? 1 : s);
 }
 int64_t tiles_of(int64_t M, int64_t N, int64_t t) { return ceil_div(M, t) * ceil_div(N, t); }
+// Slices of K for the tiles of 256 x 256 that whole rounds of 256 leave over; 1
+// where they stay one more round.  A round takes its time however few tiles it
+// has: 4095 x 4097 x 1001 (272 tiles) 88 us in two rounds, 51 + 15 + 9 us as a
+// round, the slices of 16 tiles and their joining.
+int last_slices(int64_t M, int64_t N, int64_t K) {
+    const int64_t total = tiles_of(M, N, 256), last = total % 256;
+    if (total < 256 || last == 0) return 1;
+    const int64_t most = ceil_div(K, 64) / 4, want = 256 / last, s = want < most ? want : most;
+    return int(s < 1 ? 1 : s);
+}
 int64_t round8(int64_t n) { return ceil_div(n, 8) * 8; }
 size_t partial_bytes(int64_t M, int64_t N, int slices) { return size_t(slices) * M * round8(N) * 4; }
 // Column sums take a row for each 32 rows at least (finish_kernel).
 size_t sums_bytes(int64_t M, int64_t N) { return size_t(ceil_div(ceil_div(M, FINISH_ROWS) * N, 64) * 256); }
 
+size_t last_bytes(int64_t M, int64_t N, int slices) { return size_t(tiles_of(M, N, 256) % 256) * slices * 256 * 256 * 4; }
+
 template <class Shape, class T, bool BACKWARD>
 hipError_t run_tile(LinearArgs &a, hipStream_t stream) {
-    a.grid = TileGrid{ceil_div(a.M, Shape::TM), ceil_div(a.N, Shape::TN), 1, 8, 8};
+    a.grid = TileGrid{ceil_div(a.M, Shape::TM), ceil_div(a.N, Shape::TN), 1, 8, 1};
     if (a.grid.count() > 0x7fffffff) return hipErrorInvalidConfiguration;
-    tile_kernel<T, Shape, BACKWARD><<<dim3(unsigned(a.grid.count())), dim3(Shape::THREADS), 0, stream>>>(a);
+    a.tiles = a.grid.count();
+    tile_kernel<T, Shape, BACKWARD><<<dim3(unsigned(a.tiles)), dim3(Shape::THREADS), 0, stream>>>(a);
+    return hipGetLastError();
+}
+// Whole rounds of 256 tiles, then the rest in slices of K.
+template <class Shape, class T, bool BACKWARD>
+hipError_t run_rounds(LinearArgs &a, hipStream_t stream) {
+    a.grid = TileGrid{ceil_div(a.M, Shape::TM), ceil_div(a.N, Shape::TN), 1, 8, 1};
+    const int64_t total = a.grid.count();
+    if (total > 0x7fffffff) return hipErrorInvalidConfiguration;
+    a.tiles = total / 256 * 256;
+    tile_kernel<T, Shape, BACKWARD><<<dim3(unsigned(a.tiles)), dim3(Shape::THREADS), 0, stream>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.first = a.tiles;
+    a.tiles = total - a.first;
+    last_kernel<Shape><<<dim3(unsigned(a.tiles * a.slices)), dim3(Shape::THREADS), 0, stream>>>(a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    last_finish_kernel<T, Shape, BACKWARD>
+        <<<dim3(Shape::TN / 64, Shape::TM / Shape::WTM, unsigned(a.tiles)), dim3(256), 0, stream>>>(a);
     return hipGetLastError();
 }
 template <class Shape, class T, bool BACKWARD>
@@ -415,6 +518,7 @@ hipError_t run_kernel(LinearKernel k, LinearArgs &a, hipStream_t stream) {
     using Any = Tile<T, 128, 128, 2, 2, true, BKM, false>;
     switch (k) {
         case LinearKernel::Tile256: return run_tile<T256, T, BACKWARD>(a, stream);
+        case LinearKernel::Rounds: return run_rounds<T256, T, BACKWARD>(a, stream);
         case LinearKernel::Tile128: return run_tile<T128, T, BACKWARD>(a, stream);
         case LinearKernel::Any: return run_tile<Any, T, BACKWARD>(a, stream);
         case LinearKernel::Split: return run_split<T128, T, BACKWARD>(a, stream);
@@ -431,7 +535,8 @@ hipError_t run_kernel(LinearKernel k, LinearArgs &a, hipStream_t stream) {
 int64_t sums_rows(LinearKernel k, int64_t M) {
     switch (k) {
         case LinearKernel::Few16: return 1;
-        case LinearKernel::Tile256: return ceil_div(M, 128);
+        case LinearKernel::Tile256:
+        case LinearKernel::Rounds: return ceil_div(M, 128);
         case LinearKernel::Split:
         case LinearKernel::AnySplit: return ceil_div(M, FINISH_ROWS);
         default: return ceil_div(M, 64);
@@ -442,16 +547,50 @@ bool whole_chunks(const void *x, int64_t ld, int64_t inner) {
     return reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld % 8 == 0 && inner % 8 == 0 && ld <= MOST_LD;
 }
 
+// Copies of operands that direct loads do not take, with rows of whole lines.
+int64_t round64(int64_t n) { return ceil_div(n, 64) * 64; }
+PackSpec pack_a(const LinearProblem &p) { return {p.A, p.M, p.K, p.lda, 0, 1, p.M, round64(p.K), 2}; }
+PackSpec pack_b(const LinearProblem &p) {
+    const int64_t outer = p.b_kmajor ? p.N : p.K, inner = p.b_kmajor ? p.K : p.N;
+    return {p.B, outer, inner, p.ldb, 0, 1, outer, round64(inner), 2};
+}
+// Elements of an operand and of a copy: their offsets stay below 2^31 bytes.
+constexpr int64_t PACK_MOST = (int64_t(1) << 30) - 64;
+bool can_pack(const PackSpec &s) {
+    const int64_t ld = s.ld > s.inner_p ? s.ld : s.inner_p;
+    return s.outer <= PACK_MOST && ld <= MOST_LD && s.outer * ld <= PACK_MOST;
+}
+// Copying pays where eight tiles or more read each operand and K is not short:
+// fp16, operands with odd leading dimensions, a row-major B, copied and not:
+// 250 x 4097 x 4095 42 and 45 us, 1000 x 1001 x 1001 26 and 24, 4095 x 4097 x 65 48
+// and 40, 2049 x 2049 x 2049 54 and 71, 4095 x 16385 x 4097 657 and 952.
+bool worth_packing(int64_t M, int64_t N, int64_t K) { return M >= 1024 && N >= 1024 && K >= 512; }
+// What the kernels take beside copies.
+size_t own_bytes(int64_t M, int64_t N, int64_t K) {
+    const int slices = split_slices(tiles_of(M, N, 128), K), last = last_slices(M, N, K);
+    return sums_bytes(M, N) + (slices > 1 ? partial_bytes(M, N, slices) : 0) + (last > 1 ? last_bytes(M, N, last) : 0);
+}
+// What copies of both operands take where a row of either may not be whole chunks
+// (rows that are usually start on them).
+size_t pack_bytes(int64_t M, int64_t N, int64_t K) {
+    if (!worth_packing(M, N, K) || (K % 8 == 0 && N % 8 == 0)) return 0;
+    if (M > PACK_MOST / 512 || N > PACK_MOST / 512 || K > PACK_MOST / 512) return 0;
+    const int64_t a = M * round64(K), b = N * round64(K) > K * round64(N) ? N * round64(K) : K * round64(N);
+    return a > PACK_MOST || b > PACK_MOST ? 0 : size_t(a + b) * 2;
+}
+
 }  // namespace
 
 const char *linear_kernel_name(LinearKernel k) {
     switch (k) {
         case LinearKernel::Few16: return "linear_few_16";
         case LinearKernel::Tile256: return "linear_mfma_256";
+        case LinearKernel::Rounds: return "linear_mfma_256_rounds";
         case LinearKernel::Tile128: return "linear_mfma_128";
         case LinearKernel::Split: return "linear_mfma_128_split";
         case LinearKernel::Any: return "linear_mfma_any";
         case LinearKernel::AnySplit: return "linear_mfma_any_split";
+        case LinearKernel::Packed: return "linear_packed";
         default: return "";
     }
 }
@@ -460,27 +599,67 @@ hipError_t launch_no_sums(int64_t N, float beta, float *dbias, hipStream_t strea
     return launch_sums(nullptr, 0, N, beta, dbias, stream);
 }
 
-size_t linear_workspace(int64_t M, int64_t N, int64_t K) {
-    const int slices = split_slices(tiles_of(M, N, 128), K);
-    return sums_bytes(M, N) + (slices > 1 ? partial_bytes(M, N, slices) : 0) + 16;
+size_t linear_workspace(int64_t M, int64_t N, int64_t K) { return own_bytes(M, N, K) + pack_bytes(M, N, K) + 16; }
+
+// The problem on copies of the operands that need one, at the workspace's end;
+// false where they do not fit into it.
+static bool packed_problem(const LinearProblem &p, LinearProblem &q, PackSpec specs[2], void *dst[2], int &n) {
+    n = 0;
+    if (!worth_packing(p.M, p.N, p.K) || p.workspace == nullptr) return false;
+    q = p;
+    size_t left = p.workspace_bytes / 16 * 16;
+    auto copy = [&](const PackSpec &s, const void *&x, int64_t &ld) {
+        const size_t need = size_t(packed_bytes(s));
+        if (!can_pack(s) || need > left) return false;
+        left -= need;
+        specs[n] = s;
+        dst[n++] = static_cast<char *>(p.workspace) + left;
+        x = static_cast<char *>(p.workspace) + left;
+        ld = s.inner_p;
+        return true;
+    };
+    if (!whole_chunks(p.A, p.lda, p.K) && !copy(pack_a(p), q.A, q.lda)) return false;
+    if (!whole_chunks(p.B, p.ldb, p.b_kmajor ? p.K : p.N) && !copy(pack_b(p), q.B, q.ldb)) return false;
+    q.workspace_bytes = left;
+    q.packed = true;
+    return left >= own_bytes(p.M, p.N, p.K);
 }
 
 LinearKernel linear_choose(const LinearProblem &p) {
     if (p.M == 0 || p.N == 0) return LinearKernel::None;
-    const bool direct = p.K > 0 && whole_chunks(p.A, p.lda, p.K) && whole_chunks(p.B, p.ldb, p.b_kmajor ? p.K : p.N);
+    const bool direct = p.packed || (p.K > 0 && whole_chunks(p.A, p.lda, p.K) && whole_chunks(p.B, p.ldb, p.b_kmajor ? p.K : p.N));
     if (direct && p.b_kmajor && p.M <= 16) return LinearKernel::Few16;
+    if (!direct) {
+        LinearProblem q;
+        PackSpec specs[2];
+        void *dst[2];
+        int n;
+        if (packed_problem(p, q, specs, dst, n)) return LinearKernel::Packed;
+    }
     const int64_t t128 = tiles_of(p.M, p.N, 128);
     const int slices = p.K > 0 ? split_slices(t128, p.K) : 1;
     const bool split = slices > 1 && p.workspace != nullptr &&
                        p.workspace_bytes >= sums_bytes(p.M, p.N) + partial_bytes(p.M, p.N, slices);
     if (!direct) return split ? LinearKernel::AnySplit : LinearKernel::Any;
     if (split) return LinearKernel::Split;
+    const int last = last_slices(p.M, p.N, p.K);
+    if (last > 1 && p.workspace != nullptr && p.workspace_bytes >= sums_bytes(p.M, p.N) + last_bytes(p.M, p.N, last))
+        return LinearKernel::Rounds;
     return tiles_of(p.M, p.N, 256) >= 192 ? LinearKernel::Tile256 : LinearKernel::Tile128;
 }
 
 hipError_t launch_linear(LinearKernel k, const LinearProblem &p, hipStream_t stream) {
     if (k == LinearKernel::None)
         return p.dbias != nullptr && p.N > 0 ? launch_no_sums(p.N, p.beta_bias, p.dbias, stream) : hipSuccess;
+    if (k == LinearKernel::Packed) {
+        LinearProblem q;
+        PackSpec specs[2];
+        void *dst[2];
+        int n;
+        if (!packed_problem(p, q, specs, dst, n)) return hipErrorInvalidValue;
+        const hipError_t e = n == 2 ? launch_pack2(specs[0], dst[0], specs[1], dst[1], stream) : launch_pack(specs[0], dst[0], stream);
+        return e != hipSuccess ? e : launch_linear(linear_choose(q), q, stream);
+    }
     LinearArgs a{};
     a.M = p.M;
     a.N = p.N;
@@ -500,10 +679,10 @@ hipError_t launch_linear(LinearKernel k, const LinearProblem &p, hipStream_t str
     a.c_same = p.out != 0;
     a.sums = p.dbias != nullptr ? static_cast<float *>(p.workspace) : nullptr;
     a.ldp = round8(p.N);
-    if (k == LinearKernel::Split || k == LinearKernel::AnySplit) {
-        a.slices = split_slices(tiles_of(p.M, p.N, 128), p.K);
+    if (k == LinearKernel::Split || k == LinearKernel::AnySplit) a.slices = split_slices(tiles_of(p.M, p.N, 128), p.K);
+    if (k == LinearKernel::Rounds) a.slices = last_slices(p.M, p.N, p.K);
+    if (a.slices > 1)
         a.partial = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + sums_bytes(p.M, p.N));
-    }
     hipError_t e;
     if (p.in == 1) {
         if (p.backward) e = p.b_kmajor ? run_kernel<BF16, true, true>(k, a, stream) : run_kernel<BF16, true, false>(k, a, stream);

@@ -56,7 +56,8 @@ typedef enum gemm_weights_t {
     GEMM_WEIGHTS_E5M2 = 2
 } gemm_weights_t;
 
-/* Bytes of workspace of gemm_linear and gemm_linear_backward. */
+/* Bytes of workspace of gemm_linear and gemm_linear_backward.  From 1024 rows
+ * and columns on, where K or N is not a multiple of 8, it holds copies of A and B. */
 size_t gemm_linear_workspace_size(int64_t M, int64_t N, int64_t K);
 
 /* Z = alpha * A * B + bias,  C = act(Z) + beta * R.

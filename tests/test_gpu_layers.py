@@ -160,6 +160,23 @@ def test_linear_large_tiles(lib, kind, order, backward):
         run_linear(lib, M, N, K, kind, order, beta=1.0, keep=True, expect="linear_mfma_256")
 
 
+@pytest.mark.parametrize("kernel,M,N,K,kind,order,pad,lead", [
+    ("linear_packed", 1030, 1100, 515, "f16", "nk", 1, 1), ("linear_packed", 1100, 1025, 600, "bf16", "kn", 3, 0),
+    ("linear_packed", 1024, 1024, 1024, "bf16", "nk", 8, 3), ("linear_packed", 1030, 17001, 520, "f16", "kn", 7, 0),
+    ("linear_mfma_256_rounds", 300, 33030, 520, "bf16", "nk", 8, 0), ("linear_mfma_256_rounds", 2300, 8000, 576, "f16", "kn", 0, 0),
+])
+@pytest.mark.parametrize("backward", [False, True])
+def test_linear_copies_and_rounds(lib, kernel, M, N, K, kind, order, pad, lead, backward):
+    """Operands copied for direct loads; tiles that whole rounds leave over."""
+    expect = kernel
+    if (M, N, K) == (1024, 1024, 1024):
+        expect = "linear_mfma_any_split"  # the workspace has no room for copies of rows of whole chunks
+    if backward:
+        run_backward(lib, M, N, K, kind, order, pad=pad, lead=lead, expect=expect)
+    else:
+        run_linear(lib, M, N, K, kind, order, beta=1.0, keep=True, pad=pad, lead=lead, expect=expect)
+
+
 @pytest.mark.parametrize("M,N,K", [(16, 64, 256), (70, 136, 128), (130, 140, 71)])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_linear_in_place(lib, M, N, K, out):
