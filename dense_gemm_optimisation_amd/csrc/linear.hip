@@ -47,7 +47,8 @@ struct LinearArgs {
     bool c_same;     // C (and R) have the inputs' type, else fp32
     TileGrid grid;   // batch: slices of K
     int64_t first, tiles;  // of the grid, those that a launch has
-    float *sums;     // backward: column sums by rows of blocks, N each
+    float *sums;     // backward: column sums by rows of blocks, N each,
+    float *dbias;    // or, where one block has all rows, the result itself
     float *partial;  // split: [slice][M][ldp]; the last tiles': [slice][tile][256][256]
     int64_t ldp;
     int slices;
@@ -106,8 +107,20 @@ struct Finish {
         for (int d = lanes; d < 64; d *= 2)
 #pragma unroll
             for (int e = 0; e < 8; ++e) column[e] += __shfl_xor(column[e], d);
-        if (lane < lanes && n < p.N)
-            store8f(p.sums + block * p.N + n, p.N - n < 8 ? int(p.N - n) : 8, column);
+        if (lane < lanes && n < p.N) store_sums(block, n, p.N - n < 8 ? int(p.N - n) : 8, column);
+    }
+    __device__ void store_sums(int64_t block, int64_t n, int count, float (&v)[8]) const {
+        if (p.dbias == nullptr) {
+            store8f(p.sums + block * p.N + n, count, v);
+            return;
+        }
+        if (p.beta_bias != 0.0f) {
+            float old[8];
+            load8f(p.dbias + n, count, old);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(p.beta_bias, old[e], v[e]);
+        }
+        store8f(p.dbias + n, count, v);
     }
 };
 
@@ -178,10 +191,10 @@ __global__ __launch_bounds__(Shape::THREADS, 1) void last_kernel(LinearArgs p) {
     visit_tile(acc, p.M, p.N, mw, nw, lane, Shape::staging(lds, buf, wave), Partial{out - (m0 * Shape::TN + n0), Shape::TN});
 }
 
-// The sums of a workgroup of four waves over 64 columns, eight per lane, as row
+// The sums of a workgroup's waves over 64 columns, eight per lane, as row
 // `block` of the sums; n0 is the first column.
-template <class T, bool BACKWARD>
-__device__ inline void join_sums(Finish<T, BACKWARD> &finish, float (&waves)[4][64], int64_t block, int64_t n0) {
+template <int WAVES, class T, bool BACKWARD>
+__device__ inline void join_sums(Finish<T, BACKWARD> &finish, float (&waves)[WAVES][64], int64_t block, int64_t n0) {
     if (!BACKWARD || finish.p.sums == nullptr) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int d = 8; d < 64; d *= 2)
@@ -191,8 +204,16 @@ __device__ inline void join_sums(Finish<T, BACKWARD> &finish, float (&waves)[4][
 #pragma unroll
         for (int e = 0; e < 8; ++e) waves[wave][lane * 8 + e] = finish.column[e];
     __syncthreads();
-    if (wave == 0 && n0 + lane < finish.p.N)
-        finish.p.sums[block * finish.p.N + n0 + lane] = waves[0][lane] + waves[1][lane] + (waves[2][lane] + waves[3][lane]);
+    const int64_t n = n0 + lane * 8;
+    if (wave != 0 || lane >= 8 || n >= finish.p.N) return;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        v[e] = waves[0][lane * 8 + e];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) v[e] += waves[w][lane * 8 + e];
+    }
+    finish.store_sums(block, n, finish.p.N - n < 8 ? int(finish.p.N - n) : 8, v);
 }
 
 // Joins their slices: 64 columns of 128 rows per workgroup.
@@ -234,28 +255,30 @@ __global__ __launch_bounds__(256) void last_finish_kernel(LinearArgs p) {
     join_sums(finish, waves, m0 / Shape::WTM, n0 + blockIdx.x * 64);
 }
 
-// Joins the slices: 64 columns by FINISH_ROWS rows per workgroup.
+// Joins the slices: 64 columns by FINISH_ROWS rows per workgroup of four waves, or
+// by all rows per workgroup of sixteen.
 constexpr int FINISH_ROWS = 32;
-template <class T, bool BACKWARD>
-__global__ __launch_bounds__(256) void finish_kernel(LinearArgs p) {
-    __shared__ float waves[4][64];
+template <class T, bool BACKWARD, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void finish_kernel(LinearArgs p) {
+    __shared__ float waves[WAVES][64];
     const int64_t n = int64_t(blockIdx.x) * 64 + (threadIdx.x % 8) * 8;
-    const int64_t m = int64_t(blockIdx.y) * FINISH_ROWS + threadIdx.x / 8;
     const int count = p.N - n < 8 ? int(p.N - n) : 8;
     Finish<T, BACKWARD> finish(p, n);
-    if (m < p.M && count > 0) {
-        float x[8], part[8];
-        const float *at = p.partial + m * p.ldp + n;
-        Raw8 data;
-        finish.load(data, m, n, count);
-        load8f(at, 8, x);  // whole: the workspace's rows are
-        for (int s = 1; s < p.slices; ++s) {
-            load8f(at + s * p.M * p.ldp, 8, part);
+    const int64_t end = WAVES == 4 && (int64_t(blockIdx.y) + 1) * FINISH_ROWS < p.M ? (int64_t(blockIdx.y) + 1) * FINISH_ROWS : p.M;
+    if (count > 0)
+        for (int64_t m = int64_t(blockIdx.y) * FINISH_ROWS + threadIdx.x / 8; m < end; m += WAVES * 8) {
+            float x[8], part[8];
+            const float *at = p.partial + m * p.ldp + n;
+            Raw8 data;
+            finish.load(data, m, n, count);
+            load8f(at, 8, x);  // whole: the workspace's rows are
+            for (int s = 1; s < p.slices; ++s) {
+                load8f(at + s * p.M * p.ldp, 8, part);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += part[e];
+                for (int e = 0; e < 8; ++e) x[e] += part[e];
+            }
+            finish(m, n, count, x, data);
         }
-        finish(m, n, count, x, data);
-    }
     join_sums(finish, waves, blockIdx.y, int64_t(blockIdx.x) * 64);
 }
 
@@ -364,7 +387,7 @@ __global__ __launch_bounds__(512, 1) void few_kernel(LinearArgs p) {
     for (int d = 1; d < 16; d *= 2)
 #pragma unroll
         for (int e = 0; e < 8; ++e) finish.column[e] += __shfl_xor(finish.column[e], d);
-    if (lane < 32 && row == 0 && count > 0) store8f(p.sums + n, count, finish.column);
+    if (lane < 32 && row == 0 && count > 0) finish.store_sums(0, n, count, finish.column);
 }
 
 // ---------------------------------------------------------------- column sums
@@ -391,9 +414,11 @@ hipError_t launch_sums(const float *sums, int64_t rows, int64_t N, float beta, f
 }
 
 // ---------------------------------------------------------------- without a product
-// 64 columns by AB_ROWS rows per workgroup; a thread has eight columns and
-// every 32nd row.
-constexpr int AB_ROWS = 128;
+// 64 columns by AB_ROWS rows per workgroup of four waves; a thread has eight
+// columns and every 32nd row.  Up to AB_ALL rows, a workgroup of sixteen waves
+// takes them all and writes the column sums' result (129 x 4097: 5.0 us for 5.6
+// and 2.5 in two launches).
+constexpr int AB_ROWS = 128, AB_ALL = 512;
 struct ActivationArgs {
     ActivationBackward p;
     float *sums;
@@ -404,19 +429,19 @@ __device__ inline void load8_type(const void *x, int64_t at, int n, float (&v)[8
     else if constexpr (TYPE == 1) load8<BF16>(static_cast<const uint16_t *>(x) + at, n, v);
     else load8<F16>(static_cast<const uint16_t *>(x) + at, n, v);
 }
-template <int TA, int TZ>
-__global__ __launch_bounds__(256) void activation_kernel(ActivationArgs a) {
+template <int TA, int TZ, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void activation_kernel(ActivationArgs a) {
     const ActivationBackward &p = a.p;
-    __shared__ float waves[4][64];
+    __shared__ float waves[WAVES][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t n = int64_t(blockIdx.x) * 64 + (threadIdx.x % 8) * 8;
     const int count = p.N - n < 8 ? int(p.N - n) : 8;
     float sum[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-    const int64_t end = (int64_t(blockIdx.y) + 1) * AB_ROWS < p.M ? (int64_t(blockIdx.y) + 1) * AB_ROWS : p.M;
+    const int64_t end = WAVES == 4 && (int64_t(blockIdx.y) + 1) * AB_ROWS < p.M ? (int64_t(blockIdx.y) + 1) * AB_ROWS : p.M;
     if (count > 0)
-        for (int64_t m = int64_t(blockIdx.y) * AB_ROWS + threadIdx.x / 8; m < end; m += 32) {
+        for (int64_t m = int64_t(blockIdx.y) * AB_ROWS + threadIdx.x / 8; m < end; m += WAVES * 8) {
             float x[8], z[8];
             load8_type<TA>(p.A, m * p.lda + n, count, x);
             if (p.act != act::NONE) {
@@ -441,20 +466,26 @@ __global__ __launch_bounds__(256) void activation_kernel(ActivationArgs a) {
         for (int e = 0; e < 8; ++e) waves[wave][lane * 8 + e] = sum[e];
     __syncthreads();
     const int64_t j = int64_t(blockIdx.x) * 64 + lane;
-    if (wave == 0 && j < p.N)
-        a.sums[blockIdx.y * p.N + j] = waves[0][lane] + waves[1][lane] + (waves[2][lane] + waves[3][lane]);
+    if (wave != 0 || j >= p.N) return;
+    float s = waves[0][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) s += waves[w][lane];
+    if (WAVES == 4) a.sums[blockIdx.y * p.N + j] = s;
+    else p.dbias[j] = p.beta != 0.0f ? __builtin_fmaf(p.beta, p.dbias[j], s) : s;
 }
 
 // ---------------------------------------------------------------- launches
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Slices of K for `tiles` tiles of 128 x 128: two workgroups for each of 256
-// compute units, four stages each at least.
+// compute units, four stages each at least; two, where less than a quarter of them
+// had work (fp16, odd leading dimensions: 250 x 1000 x 515, 16 tiles, 15 us for
+// 16; but 1000 x 1001 x 1001, 64 tiles, 27 for 23).
 int split_slices(int64_t tiles, int64_t K) {
-    const int64_t most = ceil_div(K, 64) / 4;
-    const int64_t want = 512 / tiles;
-    const int64_t s = want < most ? want : most;
-    return int(s < 1 ? 1 : s);
+    const int64_t stages = ceil_div(K, 64), want = 512 / tiles, few = 64 / tiles;
+    const int64_t s = want < stages / 4 ? want : stages / 4;
+    const int64_t more = few < stages / 2 ? few : stages / 2;
+    return int(s > more ? s : more > 1 ? more : 1);
 }
 int64_t tiles_of(int64_t M, int64_t N, int64_t t) { return ceil_div(M, t) * ceil_div(N, t); }
 // Slices of K for the tiles of 256 x 256 that whole rounds of 256 leave over; 1
@@ -507,7 +538,9 @@ hipError_t run_split(LinearArgs &a, hipStream_t stream) {
     split_kernel<Shape><<<dim3(unsigned(a.grid.count())), dim3(Shape::THREADS), 0, stream>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    finish_kernel<T, BACKWARD><<<dim3(unsigned(ceil_div(a.N, 64)), unsigned(ceil_div(a.M, FINISH_ROWS))), dim3(256), 0, stream>>>(a);
+    const unsigned columns = unsigned(ceil_div(a.N, 64));
+    if (BACKWARD && a.dbias != nullptr) finish_kernel<T, BACKWARD, 16><<<dim3(columns), dim3(1024), 0, stream>>>(a);
+    else finish_kernel<T, BACKWARD, 4><<<dim3(columns, unsigned(ceil_div(a.M, FINISH_ROWS))), dim3(256), 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -532,13 +565,17 @@ hipError_t run_kernel(LinearKernel k, LinearArgs &a, hipStream_t stream) {
     }
 }
 
+// Up to so many rows, a workgroup of finish_kernel takes them all for its columns
+// and writes the column sums' result, which saves a launch (250 x 1000 in four
+// slices of K: 8.5 us, 4.1 and 2.4 us in two launches).
+constexpr int64_t ONE_BLOCK = 64;
 int64_t sums_rows(LinearKernel k, int64_t M) {
     switch (k) {
         case LinearKernel::Few16: return 1;
         case LinearKernel::Tile256:
         case LinearKernel::Rounds: return ceil_div(M, 128);
         case LinearKernel::Split:
-        case LinearKernel::AnySplit: return ceil_div(M, FINISH_ROWS);
+        case LinearKernel::AnySplit: return M <= ONE_BLOCK ? 1 : ceil_div(M, FINISH_ROWS);
         default: return ceil_div(M, 64);
     }
 }
@@ -678,6 +715,8 @@ hipError_t launch_linear(LinearKernel k, const LinearProblem &p, hipStream_t str
     a.act = p.act;
     a.c_same = p.out != 0;
     a.sums = p.dbias != nullptr ? static_cast<float *>(p.workspace) : nullptr;
+    a.dbias = sums_rows(k, p.M) == 1 ? p.dbias : nullptr;
+    a.beta_bias = p.beta_bias;
     a.ldp = round8(p.N);
     if (k == LinearKernel::Split || k == LinearKernel::AnySplit) a.slices = split_slices(tiles_of(p.M, p.N, 128), p.K);
     if (k == LinearKernel::Rounds) a.slices = last_slices(p.M, p.N, p.K);
@@ -691,7 +730,7 @@ hipError_t launch_linear(LinearKernel k, const LinearProblem &p, hipStream_t str
         if (p.backward) e = p.b_kmajor ? run_kernel<F16, true, true>(k, a, stream) : run_kernel<F16, true, false>(k, a, stream);
         else e = p.b_kmajor ? run_kernel<F16, false, true>(k, a, stream) : run_kernel<F16, false, false>(k, a, stream);
     }
-    if (e != hipSuccess || p.dbias == nullptr) return e;
+    if (e != hipSuccess || p.dbias == nullptr || a.dbias != nullptr) return e;
     return launch_sums(a.sums, sums_rows(k, p.M), p.N, p.beta_bias, p.dbias, stream);
 }
 
@@ -700,21 +739,25 @@ size_t activation_backward_workspace(int64_t M, int64_t N) { return size_t(ceil_
 hipError_t launch_activation_backward(const ActivationBackward &p, hipStream_t stream) {
     ActivationArgs a{p, p.dbias != nullptr ? static_cast<float *>(p.workspace) : nullptr};
     if (ceil_div(p.M, AB_ROWS) > 65535 || ceil_div(p.N, 64) > 0x7fffff) return hipErrorInvalidConfiguration;
-    const dim3 grid(unsigned(ceil_div(p.N, 64)), unsigned(ceil_div(p.M, AB_ROWS)));
-    auto run = [&](auto kernel) { kernel<<<grid, dim3(256), 0, stream>>>(a); };
+    const bool all = p.dbias != nullptr && p.M <= AB_ALL;
+    const unsigned columns = unsigned(ceil_div(p.N, 64));
+    auto run = [&](auto few, auto many) {
+        if (all) few<<<dim3(columns), dim3(1024), 0, stream>>>(a);
+        else many<<<dim3(columns, unsigned(ceil_div(p.M, AB_ROWS))), dim3(256), 0, stream>>>(a);
+    };
     switch (p.type_a * 3 + (p.act == act::NONE ? p.type_a : p.type_z)) {
-        case 0: run(activation_kernel<0, 0>); break;
-        case 1: run(activation_kernel<0, 1>); break;
-        case 2: run(activation_kernel<0, 2>); break;
-        case 3: run(activation_kernel<1, 0>); break;
-        case 4: run(activation_kernel<1, 1>); break;
-        case 5: run(activation_kernel<1, 2>); break;
-        case 6: run(activation_kernel<2, 0>); break;
-        case 7: run(activation_kernel<2, 1>); break;
-        default: run(activation_kernel<2, 2>); break;
+        case 0: run(activation_kernel<0, 0, 16>, activation_kernel<0, 0, 4>); break;
+        case 1: run(activation_kernel<0, 1, 16>, activation_kernel<0, 1, 4>); break;
+        case 2: run(activation_kernel<0, 2, 16>, activation_kernel<0, 2, 4>); break;
+        case 3: run(activation_kernel<1, 0, 16>, activation_kernel<1, 0, 4>); break;
+        case 4: run(activation_kernel<1, 1, 16>, activation_kernel<1, 1, 4>); break;
+        case 5: run(activation_kernel<1, 2, 16>, activation_kernel<1, 2, 4>); break;
+        case 6: run(activation_kernel<2, 0, 16>, activation_kernel<2, 0, 4>); break;
+        case 7: run(activation_kernel<2, 1, 16>, activation_kernel<2, 1, 4>); break;
+        default: run(activation_kernel<2, 2, 16>, activation_kernel<2, 2, 4>); break;
     }
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.dbias == nullptr) return e;
+    if (e != hipSuccess || p.dbias == nullptr || all) return e;
     return launch_sums(a.sums, ceil_div(p.M, AB_ROWS), p.N, p.beta, p.dbias, stream);
 }
 
