@@ -81,10 +81,11 @@ __device__ inline float value_of(const InputArgs &p, int64_t at) {
     return p.in == 1 ? decode<BF16>(v) : decode<F16>(v);
 }
 
+template <int THREADS>
 __device__ inline double block_sum(double s, double *scratch) {
     scratch[threadIdx.x] = s;
     __syncthreads();
-    for (int d = 128; d > 0; d /= 2) {
+    for (int d = THREADS / 2; d > 0; d /= 2) {
         if (int(threadIdx.x) < d) scratch[threadIdx.x] += scratch[threadIdx.x + d];
         __syncthreads();
     }
@@ -95,20 +96,18 @@ __device__ inline double block_sum(double s, double *scratch) {
 template <int N>
 __device__ inline void values_of(const InputArgs &p, int64_t at, int64_t there, float (&v)[N]) {
     typedef float wide_f __attribute__((ext_vector_type(4), aligned(4)));
-    typedef uint16_t wide_h __attribute__((ext_vector_type(4), aligned(2)));
-    if (there >= N) {
+    typedef uint16_t wide_h __attribute__((ext_vector_type(N), aligned(2)));
+    if (there >= N && p.in == 0) {
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
-            if (p.in == 0) {
-                const wide_f w = *reinterpret_cast<const wide_f *>(static_cast<const float *>(p.G) + at + i);
+            const wide_f w = *reinterpret_cast<const wide_f *>(static_cast<const float *>(p.G) + at + i);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[i + e] = w[e];
-            } else {
-                const wide_h w = *reinterpret_cast<const wide_h *>(static_cast<const uint16_t *>(p.G) + at + i);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[i + e] = p.in == 1 ? decode<BF16>(w[e]) : decode<F16>(w[e]);
-            }
+            for (int e = 0; e < 4; ++e) v[i + e] = w[e];
         }
+    } else if (there >= N) {
+        const wide_h w = *reinterpret_cast<const wide_h *>(static_cast<const uint16_t *>(p.G) + at);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = p.in == 1 ? decode<BF16>(w[e]) : decode<F16>(w[e]);
     } else {
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] = e < there ? value_of(p, at + e) : 0.0f;
@@ -116,25 +115,27 @@ __device__ inline void values_of(const InputArgs &p, int64_t at, int64_t there, 
 }
 
 // Squares in 64 bits: fp32's would leave its range.  Part i has rows i, i +
-// PARTS, ...; eight values of four rows per lane at a time.
-__global__ __launch_bounds__(256) void norm_kernel(InputArgs p) {
-    __shared__ double scratch[256];
+// PARTS, ...; eight values of eight rows per lane at a time, so that enough loads
+// are on their way (4096 x 4096 in bf16: of four rows, 256 lanes, 28 us; so 16).
+constexpr int NORM_THREADS = 512, NORM_ROWS = 8;
+__global__ __launch_bounds__(NORM_THREADS) void norm_kernel(InputArgs p) {
+    __shared__ double scratch[NORM_THREADS];
     const int64_t base = blockIdx.y * p.strideG;
     double s = 0.0;
-    for (int64_t r0 = blockIdx.x; r0 < p.M; r0 += 4 * PARTS)
-        for (int64_t c = 8 * threadIdx.x; c < p.N; c += 2048) {
-            float v[4][8];
+    for (int64_t r0 = blockIdx.x; r0 < p.M; r0 += NORM_ROWS * PARTS)
+        for (int64_t c = 8 * threadIdx.x; c < p.N; c += 8 * NORM_THREADS) {
+            float v[NORM_ROWS][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NORM_ROWS; ++i) {
                 const int64_t r = r0 + i * PARTS;
                 values_of<8>(p, base + r * p.ldg + c, r < p.M ? p.N - c : 0, v[i]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < NORM_ROWS; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s = __builtin_fma(double(v[i][e]), double(v[i][e]), s);
         }
-    s = block_sum(s, scratch);
+    s = block_sum<NORM_THREADS>(s, scratch);
     if (threadIdx.x == 0) p.parts[blockIdx.y * PARTS + blockIdx.x] = s;
 }
 
@@ -143,7 +144,7 @@ __global__ __launch_bounds__(256) void input_kernel(InputArgs p) {
     __shared__ double scratch[256];
     __shared__ float tile[64][65];
     const int64_t batch = blockIdx.z;
-    const double norm = sqrt(block_sum(p.parts[batch * PARTS + threadIdx.x], scratch));
+    const double norm = sqrt(block_sum<256>(p.parts[batch * PARTS + threadIdx.x], scratch));
     // norm * 2^e in [2^11, 2^12); the rest of 2^12 * G / max(norm, eps)
     const bool finite = norm < 1e300;
     const int e = finite && norm > 0.0 ? 11 - ilogb(norm) : 0;
@@ -186,6 +187,33 @@ __device__ inline void put_output(const OrthoArgs &p, int64_t at, float y) {
         uint16_t *d = static_cast<uint16_t *>(p.O) + at;
         if (p.beta != 0.0f) y = __builtin_fmaf(p.beta, p.out == 1 ? decode<BF16>(*d) : decode<F16>(*d), y);
         *d = uint16_t(p.out == 1 ? encode<BF16>(y) : encode<F16>(y));
+    }
+}
+
+// The same of four in a row.
+__device__ inline void put_output4(const OrthoArgs &p, int64_t at, const float (&y)[4]) {
+    typedef float wide_f __attribute__((ext_vector_type(4), aligned(4)));
+    typedef uint16_t wide_h __attribute__((ext_vector_type(4), aligned(2)));
+    if (p.out == 0) {
+        wide_f *d = reinterpret_cast<wide_f *>(static_cast<float *>(p.O) + at);
+        wide_f v = {y[0], y[1], y[2], y[3]};
+        if (p.beta != 0.0f) {
+            const wide_f old = *d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(p.beta, old[e], v[e]);
+        }
+        *d = v;
+    } else {
+        wide_h *d = reinterpret_cast<wide_h *>(static_cast<uint16_t *>(p.O) + at);
+        wide_h old = {0, 0, 0, 0}, w;
+        if (p.beta != 0.0f) old = *d;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float v = y[e];
+            if (p.beta != 0.0f) v = __builtin_fmaf(p.beta, p.out == 1 ? decode<BF16>(old[e]) : decode<F16>(old[e]), v);
+            w[e] = uint16_t(p.out == 1 ? encode<BF16>(v) : encode<F16>(v));
+        }
+        *d = w;
     }
 }
 
@@ -383,29 +411,6 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
     const int64_t batch = blockIdx.x;
     const int m = int(p.m), n = int(p.n), mp = a.blocks_m * 32, np = a.blocks_n * 32;
     LDS char *x = (LDS char *)smem, *gram = x + mp * a.pitch_x, *poly = gram + mp * a.pitch_a;
-    // the norm, in 64 bits
-    double q = 0.0;
-    for (int64_t r0 = wave; r0 < in.M; r0 += 8 * SMALL_WAVES)
-        for (int64_t c = 4 * lane; c < in.N; c += 256) {
-            float v[8][4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t r = r0 + i * SMALL_WAVES;
-                values_of<4>(in, batch * in.strideG + r * in.ldg + c, r < in.M ? in.N - c : 0, v[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) q = __builtin_fma(double(v[i][e]), double(v[i][e]), q);
-        }
-    for (int d = 1; d < 64; d *= 2) q += __shfl_xor(q, d);
-    if (lane == 0) scratch[wave] = q;
-    __syncthreads();
-    q = 0.0;
-    for (int w = 0; w < SMALL_WAVES; ++w) q += scratch[w];
-    const double norm = sqrt(q), least = norm > in.eps ? norm : in.eps > 0.0f ? double(in.eps) : 1.0;
-    const float factor = norm < 1e300 ? 1.0f : NAN;
-    float shift = float((norm / least) * (norm / least) / m);
     // a lane's part of block i: row l % 32, columns 8q + 4 (l / 32) + 0..3
     const int r_in = lane & 31, c_in = 4 * (lane >> 5), blocks = a.blocks_m * a.blocks_n;
     f32x16 X[BLOCKS];
@@ -417,16 +422,17 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
             put4(at + 16 * u, v);
         }
     };
+    // G as it is, and its norm in 64 bits
+    double q = 0.0;
 #pragma unroll
     for (int i = 0; i < BLOCKS; ++i) {
         const int block = wave + i * SMALL_WAVES;
-        if (block >= blocks) continue;
         const int r = block / a.blocks_n * 32 + r_in, c = block % a.blocks_n * 32 + c_in;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int col = c + 8 * u;
             float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (r < m && col < n) {
+            if (block < blocks && r < m && col < n) {
                 if (!p.turned) {
                     values_of<4>(in, batch * in.strideG + r * in.ldg + col, n - col, v);
                 } else {
@@ -435,19 +441,50 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
                         if (col + e < n) v[e] = value_of(in, batch * in.strideG + (col + e) * in.ldg + r);
                 }
             }
-            // a 0 times NaN is NaN, but the filling's stays out of every sum
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                X[i][4 * u + e] = r < m && col + e < n ? factor * float(double(v[e]) * (X_SCALE / least)) : 0.0f;
+            for (int e = 0; e < 4; ++e) X[i][4 * u + e] = v[e];
         }
+    }
+#pragma unroll
+    for (int i = 0; i < BLOCKS; ++i)
+#pragma unroll
+        for (int u = 0; u < 16; ++u) q = __builtin_fma(double(X[i][u]), double(X[i][u]), q);
+    for (int d = 1; d < 64; d *= 2) q += __shfl_xor(q, d);
+    if (lane == 0) scratch[wave] = q;
+    __syncthreads();
+    q = 0.0;
+    for (int w = 0; w < SMALL_WAVES; ++w) q += scratch[w];
+    const double norm = sqrt(q), least = norm > in.eps ? norm : in.eps > 0.0f ? double(in.eps) : 1.0;
+    const float factor = norm < 1e300 ? 1.0f : NAN;
+    float shift = float((norm / least) * (norm / least) / m);
+    // a 0 times NaN is NaN, but the filling's stays out of every sum
+#pragma unroll
+    for (int i = 0; i < BLOCKS; ++i) {
+        const int block = wave + i * SMALL_WAVES;
+        if (block >= blocks) continue;
+        const int r = block / a.blocks_n * 32 + r_in, c = block % a.blocks_n * 32 + c_in;
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+            X[i][u] = r < m && c + 8 * (u / 4) + u % 4 < n ? factor * float(double(X[i][u]) * (X_SCALE / least)) : 0.0f;
         store_x(i, block);
     }
     __syncthreads();
-    const int blocks_a = a.blocks_m * a.blocks_m;
+    // A and B: a block on or above the diagonal per wave, stored twice
+    const bool has = wave < a.blocks_m * (a.blocks_m + 1) / 2;
+    int bi = 0, bj = wave;
+    while (has && bj >= a.blocks_m - bi) bj -= a.blocks_m - bi++;
+    bj = 32 * (bi + bj), bi *= 32;
+    // columns c_in + 8 u .. + 3 of its row r_in
+    auto put_symmetric = [&](LDS char *to, int u, const float (&v)[4]) {
+        put4(to + (bi + r_in) * a.pitch_a + (bj + c_in + 8 * u) * 2, v);
+        if (bi == bj) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<LDS uint16_t *>(to + (bj + c_in + 8 * u + e) * a.pitch_a + (bi + r_in) * 2) = uint16_t(encode<F16>(v[e]));
+    };
     for (int step = 0; step < a.steps; ++step) {
         const float ca = a.coefficients[3 * step], cb = a.coefficients[3 * step + 1], cc = a.coefficients[3 * step + 2];
-        for (int block = wave; block < blocks_a; block += SMALL_WAVES) {
-            const int bi = block / a.blocks_m * 32, bj = block % a.blocks_m * 32;
+        if (has) {
             f32x16 acc = {};
 #pragma unroll 4
             for (int k = 0; k < np; k += 16)
@@ -461,13 +498,12 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
                     // the filling stays zero
                     if (bi + r_in == bj + c_in + 8 * u + e && bi + r_in < m) v[e] -= X_SCALE * shift;
                 }
-                put4(gram + (bi + r_in) * a.pitch_a + (bj + c_in + 8 * u) * 2, v);
+                put_symmetric(gram, u, v);
             }
         }
         __syncthreads();
         const float b = __builtin_fmaf(2.0f * cc, shift, cb);
-        for (int block = wave; block < blocks_a; block += SMALL_WAVES) {
-            const int bi = block / a.blocks_m * 32, bj = block % a.blocks_m * 32;
+        if (has) {
             f32x16 acc = {};
 #pragma unroll 4
             for (int k = 0; k < mp; k += 16)
@@ -480,7 +516,7 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     v[e] = __builtin_fmaf(cc * 0x1p-16f, acc[4 * u + e], b * 0x1p-4f * decode<F16>(g[e / 2] >> (16 * (e % 2)) & 0xffffu));
-                put4(poly + at, v);
+                put_symmetric(poly, u, v);
             }
         }
         __syncthreads();
@@ -490,11 +526,11 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
         for (int i = 0; i < BLOCKS; ++i) {
             const int block = wave + i * SMALL_WAVES;
             if (block >= blocks) continue;
-            const int bi = block / a.blocks_n * 32, bj = block % a.blocks_n * 32;
+            const int xi = block / a.blocks_n * 32, xj = block % a.blocks_n * 32;
             f32x16 acc = {};
 #pragma unroll 4
             for (int k = 0; k < mp; k += 16)
-                acc = mfma32<F16>(frag_columns(x, a.pitch_x, bj, k, lane), frag_rows(poly, a.pitch_a, bi, k, lane), acc);
+                acc = mfma32<F16>(frag_columns(x, a.pitch_x, xj, k, lane), frag_rows(poly, a.pitch_a, xi, k, lane), acc);
 #pragma unroll
             for (int u = 0; u < 16; ++u) {
                 X[i][u] = __builtin_fmaf(0x1p-8f, acc[u], own * X[i][u]);
@@ -519,10 +555,19 @@ __global__ __launch_bounds__(SMALL_WAVES * 64) void small_kernel(SmallArgs a) {
         if (block >= blocks) continue;
         const int r = block / a.blocks_n * 32 + r_in, c = block % a.blocks_n * 32 + c_in;
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            const int col = c + 8 * (u / 4) + u % 4;
-            if (r < m && col < n)
-                put_output(p, batch * p.strideO + (p.turned ? col * p.ldo + r : r * p.ldo + col), s * X[i][u]);
+        for (int u = 0; u < 4; ++u) {
+            const int col = c + 8 * u;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = s * X[i][4 * u + e];
+            if (r >= m) continue;
+            if (!p.turned && col + 3 < n) {
+                put_output4(p, batch * p.strideO + r * p.ldo + col, y);
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < n) put_output(p, batch * p.strideO + (p.turned ? (col + e) * p.ldo + r : r * p.ldo + col + e), y[e]);
         }
     }
 }
@@ -690,7 +735,7 @@ hipError_t launch_orthogonalize(const Orthogonalize &p, hipStream_t stream) {
     // the tiles of G also cover the filling of X's rows
     const int64_t rows = ceil_div(turned ? l.ldx : p.M, 64), cols = ceil_div(turned ? p.N : l.ldx, 64);
     if (rows > 65535 || cols > 0x7fffff || p.batch > 65535) return hipErrorInvalidConfiguration;
-    norm_kernel<<<dim3(PARTS, unsigned(p.batch)), dim3(256), 0, stream>>>(in);
+    norm_kernel<<<dim3(PARTS, unsigned(p.batch)), dim3(NORM_THREADS), 0, stream>>>(in);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     input_kernel<<<dim3(unsigned(cols), unsigned(rows), unsigned(p.batch)), dim3(256), 0, stream>>>(in);
