@@ -83,13 +83,12 @@ __device__ inline float value_of(const InputArgs &p, int64_t at) {
 
 template <int THREADS>
 __device__ inline double block_sum(double s, double *scratch) {
-    scratch[threadIdx.x] = s;
+    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+    if (threadIdx.x % 64 == 0) scratch[threadIdx.x / 64] = s;
     __syncthreads();
-    for (int d = THREADS / 2; d > 0; d /= 2) {
-        if (int(threadIdx.x) < d) scratch[threadIdx.x] += scratch[threadIdx.x + d];
-        __syncthreads();
-    }
-    return scratch[0];
+    s = 0.0;
+    for (int w = 0; w < THREADS / 64; ++w) s += scratch[w];
+    return s;
 }
 
 // N values of G from element `at` on (fewer than N are there at a row's end).
@@ -114,34 +113,36 @@ __device__ inline void values_of(const InputArgs &p, int64_t at, int64_t there, 
     }
 }
 
-// Squares in 64 bits: fp32's would leave its range.  Part i has rows i, i +
-// PARTS, ...; eight values of eight rows per lane at a time, so that enough loads
-// are on their way (4096 x 4096 in bf16: of four rows, 256 lanes, 28 us; so 16).
-constexpr int NORM_THREADS = 512, NORM_ROWS = 8;
+// Squares in 64 bits: fp32's would leave its range.  Eight values at a time, eight
+// such pieces per lane on their way together (4096 x 4096 in bf16: of four
+// rows, 256 lanes, 28 us; so 18).
+constexpr int NORM_THREADS = 512, NORM_PIECES = 8;
 __global__ __launch_bounds__(NORM_THREADS) void norm_kernel(InputArgs p) {
-    __shared__ double scratch[NORM_THREADS];
+    __shared__ double scratch[NORM_THREADS / 64];
     const int64_t base = blockIdx.y * p.strideG;
+    const uint32_t per_row = uint32_t((p.N + 7) / 8);
+    const int64_t pieces = p.M * per_row;
     double s = 0.0;
-    for (int64_t r0 = blockIdx.x; r0 < p.M; r0 += NORM_ROWS * PARTS)
-        for (int64_t c = 8 * threadIdx.x; c < p.N; c += 8 * NORM_THREADS) {
-            float v[NORM_ROWS][8];
+    for (int64_t i0 = int64_t(blockIdx.x) * NORM_THREADS; i0 < pieces; i0 += int64_t(NORM_PIECES) * PARTS * NORM_THREADS) {
+        float v[NORM_PIECES][8];
 #pragma unroll
-            for (int i = 0; i < NORM_ROWS; ++i) {
-                const int64_t r = r0 + i * PARTS;
-                values_of<8>(p, base + r * p.ldg + c, r < p.M ? p.N - c : 0, v[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < NORM_ROWS; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s = __builtin_fma(double(v[i][e]), double(v[i][e]), s);
+        for (int i = 0; i < NORM_PIECES; ++i) {
+            const int64_t at = i0 + int64_t(i) * PARTS * NORM_THREADS + threadIdx.x;
+            const int64_t r = at / per_row, c = (at - r * per_row) * 8;
+            values_of<8>(p, base + r * p.ldg + c, at < pieces ? p.N - c : 0, v[i]);
         }
+#pragma unroll
+        for (int i = 0; i < NORM_PIECES; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = __builtin_fma(double(v[i][e]), double(v[i][e]), s);
+    }
     s = block_sum<NORM_THREADS>(s, scratch);
     if (threadIdx.x == 0) p.parts[blockIdx.y * PARTS + blockIdx.x] = s;
 }
 
 // 64 x 64 elements of G into X's pieces, turned where M > N.
 __global__ __launch_bounds__(256) void input_kernel(InputArgs p) {
-    __shared__ double scratch[256];
+    __shared__ double scratch[4];
     __shared__ float tile[64][65];
     const int64_t batch = blockIdx.z;
     const double norm = sqrt(block_sum<256>(p.parts[batch * PARTS + threadIdx.x], scratch));
