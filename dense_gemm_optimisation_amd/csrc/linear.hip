@@ -256,7 +256,7 @@ __global__ __launch_bounds__(256) void last_finish_kernel(LinearArgs p) {
 }
 
 // Joins the slices: 64 columns by FINISH_ROWS rows per workgroup of four waves, or
-// by all rows per workgroup of sixteen.
+// by all rows per workgroup of eight.
 constexpr int FINISH_ROWS = 32;
 template <class T, bool BACKWARD, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void finish_kernel(LinearArgs p) {
@@ -539,8 +539,13 @@ hipError_t run_split(LinearArgs &a, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const unsigned columns = unsigned(ceil_div(a.N, 64));
-    if (BACKWARD && a.dbias != nullptr) finish_kernel<T, BACKWARD, 16><<<dim3(columns), dim3(1024), 0, stream>>>(a);
-    else finish_kernel<T, BACKWARD, 4><<<dim3(columns, unsigned(ceil_div(a.M, FINISH_ROWS))), dim3(256), 0, stream>>>(a);
+    if constexpr (BACKWARD) {
+        if (a.dbias != nullptr) {
+            finish_kernel<T, true, 8><<<dim3(columns), dim3(512), 0, stream>>>(a);
+            return hipGetLastError();
+        }
+    }
+    finish_kernel<T, BACKWARD, 4><<<dim3(columns, unsigned(ceil_div(a.M, FINISH_ROWS))), dim3(256), 0, stream>>>(a);
     return hipGetLastError();
 }
 

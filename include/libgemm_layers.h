@@ -25,8 +25,9 @@
  * A workspace is 16-byte aligned device memory of at least the size asked
  * for, holds nothing between calls, and is used by one call at a time: two
  * calls (or two graphs) that share an output or a workspace must be ordered
- * by the caller.  Sums are formed in fp32 in an order that only the sizes
- * decide, so a call gives the same result on every run.
+ * by the caller.  Sums are formed in fp32 in an order that the arguments
+ * decide (sizes, alignment, workspace), so a call gives the same result on
+ * every run.
  *
  * 16-bit types below are bf16 or fp16, `in` saying which (GEMM_INPUT_BF16 or
  * GEMM_INPUT_F16).  Matrices are row-major with a leading dimension unless an
