@@ -64,6 +64,8 @@ bool same_matrix(const void *a, int64_t lda, int ta, const void *b, int64_t ldb,
     return a == b && ta == tb && (lda == ldb || rows == 1);
 }
 
+// Columns that the launches of column sums take: less than 2^32 threads.
+constexpr int64_t MOST_N = int64_t(1) << 28;
 bool linear_sizes_ok(int64_t M, int64_t N, int64_t K) {
     return !any_over({M, N, K}) && !too_big(M, N) && M * N <= MOST_EXTENT / 64;
 }
@@ -74,6 +76,7 @@ gemm_status_t linear_plan(const LinearProblem &q, gemm_order_t orderB, LinearPro
     p = q;
     if (!half_ok(p.in) || !out_ok(p.out, p.in) || !act_ok(p.act) || !valid_order(orderB)) return GEMM_ERR_INVALID_ARG;
     if (any_over({p.lda, p.ldb, p.ldc}) || !linear_sizes_ok(p.M, p.N, p.K)) return GEMM_ERR_INVALID_ARG;
+    if (p.N > MOST_N) return GEMM_ERR_UNSUPPORTED;
     if (p.N == 0) return GEMM_OK;
     if (p.M == 0) return p.dbias != nullptr && misaligned(p.dbias, 4) ? GEMM_ERR_INVALID_ARG : GEMM_OK;
     Range rc;
@@ -240,6 +243,7 @@ gemm_status_t gemm_activation_backward(int64_t M, int64_t N, const void *A, int6
     if (!type_ok(typeA) || !type_ok(typeZ) || !type_ok(typeD) || !act_ok(act)) return GEMM_ERR_INVALID_ARG;
     if (any_over({lda}) || !linear_sizes_ok(M, N, 0)) return GEMM_ERR_INVALID_ARG;
     if (D == nullptr && dbias == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (N > MOST_N) return GEMM_ERR_UNSUPPORTED;
     if (N == 0) return GEMM_OK;
     if (M == 0 && dbias == nullptr) return GEMM_OK;
     if (M == 0) return misaligned(dbias, 4) ? GEMM_ERR_INVALID_ARG : status_of(launch_no_sums(N, beta, dbias, stream));

@@ -399,8 +399,17 @@ __global__ __launch_bounds__(256) void sums_kernel(const float *sums, int64_t ro
     const int c = threadIdx.x % 32, g = threadIdx.x / 32;
     const int64_t j = int64_t(blockIdx.x) * 32 + c;
     float s = 0.0f;
-    if (j < N)
-        for (int64_t r = g; r < rows; r += 8) s += sums[r * N + j];
+    if (j < N) {
+        int64_t r = g;
+        for (; r + 56 < rows; r += 64) {  // eight loads under way
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = sums[(r + 8 * i) * N + j];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[i];
+        }
+        for (; r < rows; r += 8) s += sums[r * N + j];
+    }
     part[g][c] = s;
     __syncthreads();
     if (g != 0 || j >= N) return;
@@ -422,6 +431,7 @@ constexpr int AB_ROWS = 128, AB_ALL = 512;
 struct ActivationArgs {
     ActivationBackward p;
     float *sums;
+    int64_t rows;  // per workgroup
 };
 template <int TYPE>
 __device__ inline void load8_type(const void *x, int64_t at, int n, float (&v)[8]) {
@@ -439,9 +449,9 @@ __global__ __launch_bounds__(WAVES * 64) void activation_kernel(ActivationArgs a
     float sum[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-    const int64_t end = WAVES == 4 && (int64_t(blockIdx.y) + 1) * AB_ROWS < p.M ? (int64_t(blockIdx.y) + 1) * AB_ROWS : p.M;
+    const int64_t end = (int64_t(blockIdx.y) + 1) * a.rows < p.M ? (int64_t(blockIdx.y) + 1) * a.rows : p.M;
     if (count > 0)
-        for (int64_t m = int64_t(blockIdx.y) * AB_ROWS + threadIdx.x / 8; m < end; m += WAVES * 8) {
+        for (int64_t m = int64_t(blockIdx.y) * a.rows + threadIdx.x / 8; m < end; m += WAVES * 8) {
             float x[8], z[8];
             load8_type<TA>(p.A, m * p.lda + n, count, x);
             if (p.act != act::NONE) {
@@ -505,26 +515,33 @@ size_t sums_bytes(int64_t M, int64_t N) { return size_t(ceil_div(ceil_div(M, FIN
 
 size_t last_bytes(int64_t M, int64_t N, int slices) { return size_t(tiles_of(M, N, 256) % 256) * slices * 256 * 256 * 4; }
 
+// A launch has less than 2^32 threads: so many tiles, so many columns of 16 per
+// workgroup of 512.
+constexpr int64_t MOST_TILES = int64_t(1) << 22, MOST_COLUMNS = int64_t(1) << 26;
+template <class Shape, class T, bool BACKWARD>
+hipError_t run_tiles(LinearArgs &a, int64_t count, hipStream_t stream) {
+    for (a.first = 0; a.first < count; a.first += MOST_TILES) {
+        a.tiles = count - a.first < MOST_TILES ? count - a.first : MOST_TILES;
+        tile_kernel<T, Shape, BACKWARD><<<dim3(unsigned(a.tiles)), dim3(Shape::THREADS), 0, stream>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
 template <class Shape, class T, bool BACKWARD>
 hipError_t run_tile(LinearArgs &a, hipStream_t stream) {
     a.grid = TileGrid{ceil_div(a.M, Shape::TM), ceil_div(a.N, Shape::TN), 1, 8, 1};
-    if (a.grid.count() > 0x7fffffff) return hipErrorInvalidConfiguration;
-    a.tiles = a.grid.count();
-    tile_kernel<T, Shape, BACKWARD><<<dim3(unsigned(a.tiles)), dim3(Shape::THREADS), 0, stream>>>(a);
-    return hipGetLastError();
+    return run_tiles<Shape, T, BACKWARD>(a, a.grid.count(), stream);
 }
 // Whole rounds of 256 tiles, then the rest in slices of K.
 template <class Shape, class T, bool BACKWARD>
 hipError_t run_rounds(LinearArgs &a, hipStream_t stream) {
     a.grid = TileGrid{ceil_div(a.M, Shape::TM), ceil_div(a.N, Shape::TN), 1, 8, 1};
-    const int64_t total = a.grid.count();
-    if (total > 0x7fffffff) return hipErrorInvalidConfiguration;
-    a.tiles = total / 256 * 256;
-    tile_kernel<T, Shape, BACKWARD><<<dim3(unsigned(a.tiles)), dim3(Shape::THREADS), 0, stream>>>(a);
-    hipError_t e = hipGetLastError();
+    const int64_t total = a.grid.count(), whole = total / 256 * 256;
+    hipError_t e = run_tiles<Shape, T, BACKWARD>(a, whole, stream);
     if (e != hipSuccess) return e;
-    a.first = a.tiles;
-    a.tiles = total - a.first;
+    a.first = whole;
+    a.tiles = total - whole;
     last_kernel<Shape><<<dim3(unsigned(a.tiles * a.slices)), dim3(Shape::THREADS), 0, stream>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -670,7 +687,7 @@ static bool packed_problem(const LinearProblem &p, LinearProblem &q, PackSpec sp
 LinearKernel linear_choose(const LinearProblem &p) {
     if (p.M == 0 || p.N == 0) return LinearKernel::None;
     const bool direct = p.packed || (p.K > 0 && whole_chunks(p.A, p.lda, p.K) && whole_chunks(p.B, p.ldb, p.b_kmajor ? p.K : p.N));
-    if (direct && p.b_kmajor && p.M <= 16) return LinearKernel::Few16;
+    if (direct && p.b_kmajor && p.M <= 16 && p.N <= MOST_COLUMNS) return LinearKernel::Few16;
     if (!direct) {
         LinearProblem q;
         PackSpec specs[2];
@@ -742,13 +759,14 @@ hipError_t launch_linear(LinearKernel k, const LinearProblem &p, hipStream_t str
 size_t activation_backward_workspace(int64_t M, int64_t N) { return size_t(ceil_div(M, AB_ROWS)) * N * 4 + 16; }
 
 hipError_t launch_activation_backward(const ActivationBackward &p, hipStream_t stream) {
-    ActivationArgs a{p, p.dbias != nullptr ? static_cast<float *>(p.workspace) : nullptr};
-    if (ceil_div(p.M, AB_ROWS) > 65535 || ceil_div(p.N, 64) > 0x7fffff) return hipErrorInvalidConfiguration;
-    const bool all = p.dbias != nullptr && p.M <= AB_ALL;
+    const bool all = p.dbias != nullptr && p.M <= AB_ALL && p.N <= MOST_COLUMNS;
+    // a grid has at most 65535 rows of workgroups
+    const int64_t rows = all ? p.M : AB_ROWS * ceil_div(p.M, AB_ROWS * int64_t(65535)), blocks = ceil_div(p.M, rows);
+    ActivationArgs a{p, p.dbias != nullptr ? static_cast<float *>(p.workspace) : nullptr, rows};
     const unsigned columns = unsigned(ceil_div(p.N, 64));
     auto run = [&](auto few, auto many) {
         if (all) few<<<dim3(columns), dim3(1024), 0, stream>>>(a);
-        else many<<<dim3(columns, unsigned(ceil_div(p.M, AB_ROWS))), dim3(256), 0, stream>>>(a);
+        else many<<<dim3(columns, unsigned(blocks)), dim3(256), 0, stream>>>(a);
     };
     switch (p.type_a * 3 + (p.act == act::NONE ? p.type_a : p.type_z)) {
         case 0: run(activation_kernel<0, 0, 16>, activation_kernel<0, 0, 4>); break;
@@ -763,7 +781,7 @@ hipError_t launch_activation_backward(const ActivationBackward &p, hipStream_t s
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.dbias == nullptr || all) return e;
-    return launch_sums(a.sums, ceil_div(p.M, AB_ROWS), p.N, p.beta, p.dbias, stream);
+    return launch_sums(a.sums, blocks, p.N, p.beta, p.dbias, stream);
 }
 
 }  // namespace libgemm

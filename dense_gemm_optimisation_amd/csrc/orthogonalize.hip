@@ -73,6 +73,7 @@ struct InputArgs {
     float *factor, *shift;  // [batch]
     uint16_t *x, *lo;
     int64_t ldx, m;
+    int64_t blocks, across;  // of 64 x 64, per matrix and across it
 };
 
 __device__ inline float value_of(const InputArgs &p, int64_t at) {
@@ -119,11 +120,11 @@ __device__ inline void values_of(const InputArgs &p, int64_t at, int64_t there, 
 constexpr int NORM_THREADS = 512, NORM_PIECES = 8;
 __global__ __launch_bounds__(NORM_THREADS) void norm_kernel(InputArgs p) {
     __shared__ double scratch[NORM_THREADS / 64];
-    const int64_t base = blockIdx.y * p.strideG;
+    const int64_t batch = blockIdx.x / PARTS, part = blockIdx.x % PARTS, base = batch * p.strideG;
     const uint32_t per_row = uint32_t((p.N + 7) / 8);
     const int64_t pieces = p.M * per_row;
     double s = 0.0;
-    for (int64_t i0 = int64_t(blockIdx.x) * NORM_THREADS; i0 < pieces; i0 += int64_t(NORM_PIECES) * PARTS * NORM_THREADS) {
+    for (int64_t i0 = part * NORM_THREADS; i0 < pieces; i0 += int64_t(NORM_PIECES) * PARTS * NORM_THREADS) {
         float v[NORM_PIECES][8];
 #pragma unroll
         for (int i = 0; i < NORM_PIECES; ++i) {
@@ -137,26 +138,27 @@ __global__ __launch_bounds__(NORM_THREADS) void norm_kernel(InputArgs p) {
             for (int e = 0; e < 8; ++e) s = __builtin_fma(double(v[i][e]), double(v[i][e]), s);
     }
     s = block_sum<NORM_THREADS>(s, scratch);
-    if (threadIdx.x == 0) p.parts[blockIdx.y * PARTS + blockIdx.x] = s;
+    if (threadIdx.x == 0) p.parts[batch * PARTS + part] = s;
 }
 
 // 64 x 64 elements of G into X's pieces, turned where M > N.
 __global__ __launch_bounds__(256) void input_kernel(InputArgs p) {
     __shared__ double scratch[4];
     __shared__ float tile[64][65];
-    const int64_t batch = blockIdx.z;
+    const int64_t batch = blockIdx.x / p.blocks;
+    const int64_t block = blockIdx.x % p.blocks, down = block / p.across, along = block % p.across;
     const double norm = sqrt(block_sum<256>(p.parts[batch * PARTS + threadIdx.x], scratch));
     // norm * 2^e in [2^11, 2^12); the rest of 2^12 * G / max(norm, eps)
     const bool finite = norm < 1e300;
     const int e = finite && norm > 0.0 ? 11 - ilogb(norm) : 0;
     const double least = norm > p.eps ? norm : p.eps > 0.0f ? double(p.eps) : 1.0;
     const float factor = !finite ? NAN : norm > 0.0 ? float(ldexp(4096.0 / least, -e)) : 0.0f;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    if (block == 0 && threadIdx.x == 0) {
         p.factor[batch] = factor;
         p.shift[batch] = float((norm / least) * (norm / least) / p.m);
     }
     const bool turned = p.M > p.N;
-    const int64_t r0 = int64_t(blockIdx.y) * 64, c0 = int64_t(blockIdx.x) * 64;
+    const int64_t r0 = down * 64, c0 = along * 64;
     const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
     auto put = [&](int64_t r, int64_t c, float v) {
         if (r >= p.m || c >= p.ldx) return;
@@ -678,8 +680,17 @@ hipError_t launch_product(OrthoArgs &a, hipStream_t stream) {
 
 }  // namespace
 
+// Matrices at a time, one batch after another in the same workspace: a launch has
+// less than 2^32 threads, of 256 for 64 x 64 elements, of 512 for a part of a norm.
+static int64_t most_batch(int64_t M, int64_t N) {
+    const int64_t blocks = ceil_div(M, 64) * ceil_div(N + 7, 64), most = (int64_t(1) << 23) / blocks;
+    return most < 1 ? 1 : most < 16384 ? most : 16384;
+}
+
 const char *orthogonalize_kernel_name(int64_t M, int64_t N, int64_t batch) {
     if (M == 0 || N == 0 || batch == 0) return "";
+    const int64_t most = most_batch(M, N);
+    if (batch > most) batch = most;
     if (small_lds(M < N ? M : N, M < N ? N : M) != 0) return "orthogonalize_small";
     switch (size_of(M < N ? M : N, M < N ? N : M, batch, false)) {
         case Size::Large: return "orthogonalize_mfma_256";
@@ -688,9 +699,12 @@ const char *orthogonalize_kernel_name(int64_t M, int64_t N, int64_t batch) {
     }
 }
 
-size_t orthogonalize_workspace(int64_t M, int64_t N, int64_t batch) { return layout_of(M, N, batch).bytes; }
+size_t orthogonalize_workspace(int64_t M, int64_t N, int64_t batch) {
+    const int64_t most = most_batch(M, N);
+    return layout_of(M, N, batch < most ? batch : most).bytes;
+}
 
-hipError_t launch_orthogonalize(const Orthogonalize &p, hipStream_t stream) {
+static hipError_t launch_batch(const Orthogonalize &p, hipStream_t stream) {
     const Layout l = layout_of(p.M, p.N, p.batch);
     char *w = static_cast<char *>(p.workspace);
     auto half = [&](size_t at) { return reinterpret_cast<uint16_t *>(w + at); };
@@ -728,18 +742,18 @@ hipError_t launch_orthogonalize(const Orthogonalize &p, hipStream_t stream) {
         sm.pitch_x = sm.blocks_n * 64 + 16;
         sm.pitch_a = sm.blocks_m * 64 + 16;
         const int blocks = sm.blocks_m * sm.blocks_n;
-        if (p.batch > 0x7fffff) return hipErrorInvalidConfiguration;
         if (blocks <= SMALL_WAVES) return launch_small<1>(sm, lds, stream);
         if (blocks <= 2 * SMALL_WAVES) return launch_small<2>(sm, lds, stream);
         return launch_small<SMALL_BLOCKS>(sm, lds, stream);
     }
     // the tiles of G also cover the filling of X's rows
     const int64_t rows = ceil_div(turned ? l.ldx : p.M, 64), cols = ceil_div(turned ? p.N : l.ldx, 64);
-    if (rows > 65535 || cols > 0x7fffff || p.batch > 65535) return hipErrorInvalidConfiguration;
-    norm_kernel<<<dim3(PARTS, unsigned(p.batch)), dim3(NORM_THREADS), 0, stream>>>(in);
+    in.blocks = rows * cols;
+    in.across = cols;
+    norm_kernel<<<dim3(unsigned(PARTS * p.batch)), dim3(NORM_THREADS), 0, stream>>>(in);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    input_kernel<<<dim3(unsigned(cols), unsigned(rows), unsigned(p.batch)), dim3(256), 0, stream>>>(in);
+    input_kernel<<<dim3(unsigned(in.blocks * p.batch)), dim3(256), 0, stream>>>(in);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     for (int s = 0; s < p.steps; ++s) {
@@ -755,6 +769,19 @@ hipError_t launch_orthogonalize(const Orthogonalize &p, hipStream_t stream) {
         uint16_t *t = a.x;
         a.x = a.next;
         a.next = t;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_orthogonalize(const Orthogonalize &p, hipStream_t stream) {
+    const int64_t most = most_batch(p.M, p.N);
+    for (int64_t first = 0; first < p.batch; first += most) {
+        Orthogonalize q = p;
+        q.batch = p.batch - first < most ? p.batch - first : most;
+        q.G = static_cast<const char *>(p.G) + first * p.strideG * (p.in == 0 ? 4 : 2);
+        q.O = static_cast<char *>(p.O) + first * p.strideO * (p.out == 0 ? 4 : 2);
+        const hipError_t e = launch_batch(q, stream);
+        if (e != hipSuccess) return e;
     }
     return hipSuccess;
 }

@@ -213,6 +213,16 @@ def test_linear_unusual_values(lib, M, N, K):
     assert got[:, 7].isnan().all() and not got[4:, :7].isnan().any()
 
 
+def test_linear_many_tiles(lib):
+    """More tiles than one launch takes."""
+    M = (1 << 22) * 128 + 700
+    a = torch.randint(-8, 9, (M,), dtype=torch.int8, device=DEV, generator=torch.Generator(device=DEV).manual_seed(6)).bfloat16()
+    b, c = torch.full((1,), 3.0, dtype=torch.bfloat16, device=DEV), torch.full((M,), 7.0, dtype=torch.bfloat16, device=DEV)
+    lib.gemm_linear(M, 1, 1, 1.0, a.data_ptr(), 1, b.data_ptr(), 1, 1, 1, 0, 0, 0.0, 0, 1, c.data_ptr(), 1, 1)
+    torch.cuda.synchronize()
+    assert torch.equal(c, 3 * a)
+
+
 def run_backward(lib, M, N, K, kind="bf16", order="nk", act="gelu", beta=0.0, out=None, alpha=1.0, pad=8, lead=0, in_place=False,
                  workspace=True, bias=True, seed=0, expect=None):
     out = out or kind
@@ -337,6 +347,21 @@ def test_activation_backward_shapes(lib, M, N, pad, lead, act):
 @pytest.mark.parametrize("in_place,want_d,bias", [("a", True, True), ("z", True, True), (None, False, True), (None, True, False)])
 def test_activation_backward_forms(lib, in_place, want_d, bias):
     run_activation(lib, 100, 70, ("f16", "f16", "f16"), "silu", beta=0.25, in_place=in_place, want_d=want_d, bias=bias)
+
+
+def test_activation_backward_many_rows(lib):
+    """More rows than a grid has rows of workgroups of 128; whole numbers, so every sum is exact."""
+    M, N = 65535 * 128 + 300, 8
+    g = torch.Generator(device=DEV).manual_seed(5)
+    a = torch.randint(-1, 2, (M, N), device=DEV, generator=g).bfloat16()
+    z = torch.randint(-1, 2, (M, N), device=DEV, generator=g).bfloat16()
+    d, db = torch.empty_like(a), torch.zeros(N, device=DEV)
+    ws = space(lib.activation_backward_workspace_size(M, N))
+    lib.gemm_activation_backward(M, N, a.data_ptr(), N, 1, z.data_ptr(), N, 1, 1, d.data_ptr(), N, 1, 0.0, db.data_ptr(),
+                                 ws.data_ptr(), ws.numel() * 4)
+    want = torch.where(z > 0, a, torch.zeros_like(a))
+    assert torch.equal(d, want)
+    assert torch.equal(db, want.float().sum(0, dtype=torch.float64).float())
 
 
 # ---------------------------------------------------------------- gemm_experts_layer
@@ -656,3 +681,21 @@ def test_route_and_experts_layer_captured(lib):
         assert torch.equal(c["dids"].cpu(), order.indices[:, :k].int())
         want, bound = ref.experts_layer(c["x"], c["dids"].cpu(), c["dgates"].cpu(), *c["values"], "silu", 0.0, None, "bf16", "bf16")
         close(c["my"].get(), want, bound, "Y")
+
+
+def test_orthogonalize_many_matrices(lib):
+    """More matrices than one launch takes, of a size that takes several launches a step."""
+    M, N, batch = 129, 129, 65600
+    few = torch.randn(4, M, N, generator=torch.Generator().manual_seed(8)).bfloat16().to(DEV)
+    g = few.repeat(batch // 4, 1, 1)
+    o = torch.empty_like(g)
+    ws = space(lib.orthogonalize_workspace_size(M, N, batch))
+    lib.gemm_orthogonalize(M, N, g.data_ptr(), N, 1, 1, None, 1e-7, 1.0, 0.0, o.data_ptr(), N, 1, ws.data_ptr(), ws.numel() * 4,
+                           batch=batch, stride_g=M * N, stride_o=M * N)
+    torch.cuda.synchronize()
+    for b in range(4):
+        want = ref.newton_schulz(few[b].cpu(), 1, None, 1e-7)
+        drift = torch.linalg.matrix_norm(ref.newton_schulz(few[b].cpu(), 1, None, 1e-7, rounding=True) - want)
+        # as for few matrices; every copy is off by no more
+        off = torch.linalg.matrix_norm(o[b::4].double() - want.to(DEV)).max().item()
+        assert off <= 2 * drift + (2.0 ** -16 + ref.HALF["bf16"]) * torch.linalg.matrix_norm(want)

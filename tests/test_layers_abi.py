@@ -138,7 +138,8 @@ def test_activation_backward_empty(lib):
     assert activation_call(lib, N=0, A=0) == lib.OK
     assert activation_call(lib, M=0, A=0, d_bias=0) == lib.OK
     assert activation_call(lib, M=0, d_bias=DB + 2) == lib.ERR_INVALID_ARG
-    assert activation_call(lib, M=1 << 24, N=8, lda=8, ldz=8, ldd=8, D=0, Z=Z, workspace_bytes=1 << 30) == lib.ERR_UNSUPPORTED
+    n = (1 << 28) + 1
+    assert activation_call(lib, M=1, N=n, lda=n, ldz=n, ldd=n, D=0, Z=Z, workspace_bytes=1 << 31) == lib.ERR_UNSUPPORTED
 
 
 def layer_call(lib, **k):
