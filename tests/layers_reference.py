@@ -9,11 +9,16 @@ TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 TINY = 2.0 ** -24  # below fp16's smallest normal value a step is 2^-24
 
 
+def below(z):
+    """The normal distribution function, to full relative precision in the lower tail (torch.special.ndtr is 0 there)."""
+    return 0.5 * torch.special.erfc(-z / math.sqrt(2))
+
+
 def act(z, a):
     if a == "relu":
         return torch.where(z > 0, z, 0.0)
     if a == "gelu":
-        return z * torch.special.ndtr(z)
+        return z * below(z)
     if a == "silu":
         return z * torch.sigmoid(z)
     return z
@@ -23,7 +28,7 @@ def slope(z, a):
     if a == "relu":
         return (z > 0).double()
     if a == "gelu":
-        return torch.special.ndtr(z) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        return below(z) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
     if a == "silu":
         p = torch.sigmoid(z)
         return p * (1 + z * (1 - p))
@@ -44,7 +49,7 @@ def slope_error(z, a):
     if a in ("none", "relu"):
         return torch.zeros_like(z)
     if a == "gelu":
-        terms = torch.special.ndtr(z) + (z * torch.exp(-z * z / 2)).abs()
+        terms = below(z) + (z * torch.exp(-z * z / 2)).abs()
         return terms * (2.0 ** -20 + 2.0 ** -22 * z * z / 2)
     p = torch.sigmoid(z)
     return p * (1 + z.abs()) * (2.0 ** -20 + 2.0 ** -22 * z.abs())
