@@ -687,6 +687,7 @@ static bool packed_problem(const LinearProblem &p, LinearProblem &q, PackSpec sp
 LinearKernel linear_choose(const LinearProblem &p) {
     if (p.M == 0 || p.N == 0) return LinearKernel::None;
     const bool direct = p.packed || (p.K > 0 && whole_chunks(p.A, p.lda, p.K) && whole_chunks(p.B, p.ldb, p.b_kmajor ? p.K : p.N));
+    // 16 x 4096 x 4096 6.4 us, in slices of tiles 15.6; 16 x 4096 x 16384 26 and 31
     if (direct && p.b_kmajor && p.M <= 16 && p.N <= MOST_COLUMNS) return LinearKernel::Few16;
     if (!direct) {
         LinearProblem q;
@@ -704,7 +705,10 @@ LinearKernel linear_choose(const LinearProblem &p) {
     const int last = last_slices(p.M, p.N, p.K);
     if (last > 1 && p.workspace != nullptr && p.workspace_bytes >= sums_bytes(p.M, p.N) + last_bytes(p.M, p.N, last))
         return LinearKernel::Rounds;
-    return tiles_of(p.M, p.N, 256) >= 192 ? LinearKernel::Tile256 : LinearKernel::Tile128;
+    // 128 x 128 tiles while one round takes them all, two to a compute unit (bf16, K
+    // 4096: 2560 x 2560, 400 tiles, 63 us, of 256 88; 3328 x 3328, 676 tiles, 105, of
+    // 256 93; 4096 x 4096 137 and 116)
+    return t128 <= 512 ? LinearKernel::Tile128 : LinearKernel::Tile256;
 }
 
 hipError_t launch_linear(LinearKernel k, const LinearProblem &p, hipStream_t stream) {
