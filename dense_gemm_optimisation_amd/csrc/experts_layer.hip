@@ -24,6 +24,10 @@
 // operand and the tokens as the other; 8-bit codes are widened exactly on the way
 // from LDS, and a run of 128 has one scale.
 //
+// 64 experts of 1024 x 4096: one token of eight in bf16 30 + 17 us (4.3 TB/s), 32
+// tokens in 8 bits 113 + 77 us (4.2 TB/s; there widening and the short runs' latency
+// count too: without memory 78 and 75).
+//
 // Each workgroup finds the live experts and their tokens from the ids by
 // itself (at most 2048 of them, from L2), which saves a launch.
 #include "activation.hpp"
