@@ -699,3 +699,36 @@ def test_orthogonalize_many_matrices(lib):
         # as for few matrices; every copy is off by no more
         off = torch.linalg.matrix_norm(o[b::4].double() - want.to(DEV)).max().item()
         assert off <= 2 * drift + (2.0 ** -16 + ref.HALF["bf16"]) * torch.linalg.matrix_norm(want)
+
+
+@pytest.mark.parametrize("M,N,K", [(1030, 1101, 515), (300, 33030, 520), (40, 300, 1000)])
+def test_linear_backward_captured(lib, M, N, K):
+    """Copies, tiles left over and slices from a graph, replayed on new inputs: as called, whatever the workspace held."""
+    a, b, z = (torch.empty(s, dtype=torch.float16, device=DEV) for s in ((M, K), (N, K), (M, N)))
+    d, db = torch.empty_like(z), torch.empty(N, device=DEV)
+    ws = space(lib.linear_workspace_size(M, N, K))
+
+    def call(stream=None):
+        lib.gemm_linear_backward(M, N, K, 1.0, a.data_ptr(), K, b.data_ptr(), K, lib.COL_MAJOR, 2, z.data_ptr(), N, 2, d.data_ptr(), N, 2,
+                                 0.0, db.data_ptr(), ws.data_ptr(), ws.numel() * 4, stream=stream)
+
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    for t in (a, b, z):
+        t.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        call(torch.cuda.current_stream().cuda_stream)
+    for seed in range(3):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        for t in (a, b, z):
+            t.normal_(generator=g)
+        ws.fill_(float("nan") if ws.is_floating_point() else -1)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = d.clone(), db.clone()
+        ws.fill_(0)
+        d.fill_(9), db.fill_(9)
+        call(torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], d) and torch.equal(got[1], db)
+        assert got[0].isfinite().all() and got[1].isfinite().all()
