@@ -7,7 +7,8 @@
 //   u >= 0 by reweighted least squares: 1.7e-7, 5e-7 as evaluated in fp32.  The tail
 //   keeps its relative precision, which a slope needs where Phi(x) and
 //   x * phi(x) nearly cancel.
-// SiLU(x) = x / (1 + exp(-x)).  ReLU(x) = max(x, 0), its slope at 0 is 0.
+// SiLU(x) = x / (1 + exp(-x)).  ReLU(x) = max(x, 0), its slope at 0 is 0.  A NaN
+// stays one in all of them and in their slopes.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -37,7 +38,7 @@ __device__ inline float normal_below(float x, float &e) {
 }
 
 __device__ inline float value(int a, float x) {
-    if (a == RELU) return x > 0.0f ? x : 0.0f;
+    if (a == RELU) return x <= 0.0f ? 0.0f : x;
     if (a == GELU) {
         float e;
         return x * normal_below(x, e);
@@ -47,7 +48,7 @@ __device__ inline float value(int a, float x) {
 }
 
 __device__ inline float slope(int a, float x) {
-    if (a == RELU) return x > 0.0f ? 1.0f : 0.0f;
+    if (a == RELU) return x > 0.0f ? 1.0f : x <= 0.0f ? 0.0f : x;
     if (a == GELU) {
         float e;
         const float below = normal_below(x, e);

@@ -34,6 +34,10 @@
  * order says otherwise, and take any alignment of their element size; rows
  * that start at multiples of 16 bytes with extents of a multiple of 8
  * elements run fastest.
+ *
+ * Activations are those of gemm_activation_t, evaluated in fp32.  A NaN stays a
+ * NaN in each of them and in its slope, ReLU's too (the epilogues of libgemm.h
+ * give 0 there).
  */
 #ifndef LIBGEMM_LAYERS_H
 #define LIBGEMM_LAYERS_H

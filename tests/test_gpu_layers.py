@@ -732,3 +732,62 @@ def test_linear_backward_captured(lib, M, N, K):
         torch.cuda.synchronize()
         assert torch.equal(got[0], d) and torch.equal(got[1], db)
         assert got[0].isfinite().all() and got[1].isfinite().all()
+
+
+# ---------------------------------------------------------------- infinities and NaN through the activations
+ACT = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+# few rows; tiles; tiles through registers; slices of tiles; no product
+KERNEL_SIZES = [(5, 40, 64), (130, 136, 128), (30, 75, 99), (40, 300, 1000), (9, 44, 0)]
+BIG = {"bf16": 3e38, "f16": 6e4}
+
+
+def linear_of_bias(lib, M, N, K, kind, act, bias):
+    """gemm_linear's C in fp32 and Z of small products and this bias."""
+    a, b = draw((M, K), kind, 1, 0.1), draw((N, K), kind, 2, 0.1)
+    da, db, dbias = a.to(DEV), b.to(DEV), bias.to(ref.TORCH[kind]).to(DEV)
+    c, z = torch.zeros(M, N, device=DEV), torch.zeros(M, N, dtype=ref.TORCH[kind], device=DEV)
+    ws = space(lib.linear_workspace_size(M, N, K))
+    lib.gemm_linear(M, N, K, 1.0, da.data_ptr(), K, db.data_ptr(), K, 1, INPUT[kind], dbias.data_ptr(), ACT[act], 0.0, 0, 0,
+                    c.data_ptr(), N, 0, z.data_ptr(), N, ws.data_ptr(), ws.numel() * 4)
+    torch.cuda.synchronize()
+    return c.cpu().double(), z.cpu().double(), a.double() @ b.double().t() + bias.to(ref.TORCH[kind]).double()
+
+
+def slope_of(lib, M, N, K, kind, act, z, incoming):
+    """gemm_linear_backward's D in fp32 and its column sums: row i of the gradient is incoming[i] in every column."""
+    k = max(K, 1)
+    a, b = torch.zeros(M, k, dtype=ref.TORCH[kind]), torch.zeros(N, k, dtype=ref.TORCH[kind])
+    a[:, 0], b[:, 0] = incoming.to(a.dtype), 1
+    da, db, dz = a.to(DEV), b.to(DEV), z.to(ref.TORCH[kind]).to(DEV)
+    d, sums = torch.zeros(M, N, device=DEV), torch.zeros(N, device=DEV)
+    ws = space(lib.linear_workspace_size(M, N, k))
+    lib.gemm_linear_backward(M, N, k, 1.0, da.data_ptr(), k, db.data_ptr(), k, 1, INPUT[kind], dz.data_ptr(), N, ACT[act],
+                             d.data_ptr(), N, 0, 0.0, sums.data_ptr(), ws.data_ptr(), ws.numel() * 4)
+    torch.cuda.synchronize()
+    return d.cpu().double(), sums.cpu().double()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", KERNEL_SIZES)
+def test_relu_keeps_nan(lib, M, N, K, kind):
+    """A NaN passes ReLU, and its slope there is NaN: nothing turns one into a 0."""
+    bias = torch.zeros(N)
+    bias[3], bias[N - 1] = float("nan"), float("nan")
+    c, z, pre = linear_of_bias(lib, M, N, K, kind, "relu", bias)
+    assert torch.equal(z.isnan(), pre.isnan()) and torch.equal(c.isnan(), pre.isnan())
+    d, sums = slope_of(lib, M, N, K, kind, "relu", pre, torch.ones(M))
+    assert torch.equal(d.isnan(), pre.isnan()) and torch.equal(sums.isnan(), pre.isnan().any(0))
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu"])
+def test_experts_layer_keeps_nan(lib, act):
+    """A NaN among an expert's activated weights reaches every token that chose it, and no other."""
+    ids = torch.tensor([[0, 1], [2, 3], [1, 2], [3, 0]], dtype=torch.int32)
+    c = experts_case(lib, 4, 4, 2, 72, 40, act=act, ids=ids)
+    c["stored"][0][0][1, 7, 5] = float("nan")
+    experts_call(lib, c)
+    torch.cuda.synchronize()
+    want, bound = ref.experts_layer(c["x"], ids, c["gates"], *c["values"], act, 0.0, None, "bf16", "bf16")
+    got = c["my"].get()
+    assert got[[0, 2]].isnan().all()
+    close(got[[1, 3]], want[[1, 3]], bound[[1, 3]], "Y")
