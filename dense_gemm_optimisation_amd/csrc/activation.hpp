@@ -47,18 +47,15 @@ __device__ inline float value(int a, float x) {
     return x;
 }
 
+// Of GELU and SiLU.
 __device__ inline float slope(int a, float x) {
-    if (a == RELU) return x > 0.0f ? 1.0f : x <= 0.0f ? 0.0f : x;
     if (a == GELU) {
         float e;
         const float below = normal_below(x, e);
         return __builtin_fmaf(x * 0.398942280f, e, below);
     }
-    if (a == SILU) {
-        const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-x));
-        return p * __builtin_fmaf(x, 1.0f - p, 1.0f);
-    }
-    return 1.0f;
+    const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-x));
+    return p * __builtin_fmaf(x, 1.0f - p, 1.0f);
 }
 
 // Over N values, the choice made once.
@@ -79,8 +76,9 @@ __device__ inline void apply(int a, float (&x)[N]) {
 template <int N>
 __device__ inline void times_slope(int a, const float (&z)[N], float (&x)[N]) {
     if (a == RELU) {
+        // chosen, not multiplied: an infinite or NaN gradient of a value that was cut off is 0
 #pragma unroll
-        for (int e = 0; e < N; ++e) x[e] *= slope(RELU, z[e]);
+        for (int e = 0; e < N; ++e) x[e] = z[e] > 0.0f ? x[e] : z[e] <= 0.0f ? 0.0f : z[e];
     } else if (a == GELU) {
 #pragma unroll
         for (int e = 0; e < N; ++e) x[e] *= slope(GELU, z[e]);

@@ -105,7 +105,8 @@ const char *gemm_linear_kernel_name(int64_t M, int64_t N, int64_t K, float alpha
  * of X and W1 are then products of D.
  *   A, B     as for gemm_linear.
  *   Z        M x N of A's type, ldz >= N.  Not read when act is GEMM_ACT_NONE
- *            (and may then be NULL).  ReLU's slope at 0 is 0.
+ *            (and may then be NULL).  ReLU's slope at 0 is 0; where Z <= 0 its
+ *            D is 0 whatever the gradient, infinities and NaN too.
  *   D        M x N of typeD (A's type or fp32), ldd >= N, not overlapping
  *            what is read; D may be Z itself where it has its type (the same
  *            address and leading dimension).

@@ -791,3 +791,27 @@ def test_experts_layer_keeps_nan(lib, act):
     got = c["my"].get()
     assert got[[0, 2]].isnan().all()
     close(got[[1, 3]], want[[1, 3]], bound[[1, 3]], "Y")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", KERNEL_SIZES)
+def test_relu_slope_is_a_choice(lib, M, N, K, kind):
+    """Where ReLU was off its gradient is 0, whatever comes in: infinities and NaN there do not reach D or its sums."""
+    z = draw((M, N), kind, 3).double()
+    z[:, 1], z[:, 2] = 0.0, -0.0
+    incoming = torch.ones(M)
+    incoming[1], incoming[2], incoming[4] = float("inf"), float("nan"), -float("inf")
+    z[[1, 2, 4], :6] = -z[[1, 2, 4], :6].abs()
+    d, sums = slope_of(lib, M, N, K, kind, "relu", z, incoming)
+    want = torch.where(z > 0, incoming.double()[:, None], 0.0)
+    assert torch.equal(d.nan_to_num(nan=9.0), want.nan_to_num(nan=9.0))
+    # whole numbers where every term is finite
+    assert torch.equal(sums[:6], want[:, :6].sum(0))
+    dz, da = z.to(ref.TORCH[kind]).to(DEV), incoming.to(ref.TORCH[kind])[:, None].repeat(1, N).to(DEV)
+    out, total = torch.zeros(M, N, device=DEV), torch.zeros(N, device=DEV)
+    ws = space(lib.activation_backward_workspace_size(M, N))
+    lib.gemm_activation_backward(M, N, da.data_ptr(), N, INPUT[kind], dz.data_ptr(), N, INPUT[kind], lib.ACT_RELU, out.data_ptr(), N,
+                                 0, 0.0, total.data_ptr(), ws.data_ptr(), ws.numel() * 4)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cpu().double().nan_to_num(nan=9.0), want.nan_to_num(nan=9.0))
+    assert torch.equal(total[:6].cpu().double(), want[:, :6].sum(0))
