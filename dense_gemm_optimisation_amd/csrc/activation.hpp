@@ -8,7 +8,9 @@
 //   keeps its relative precision, which a slope needs where Phi(x) and
 //   x * phi(x) nearly cancel.
 // SiLU(x) = x / (1 + exp(-x)).  ReLU(x) = max(x, 0), its slope at 0 is 0.  A NaN
-// stays one in all of them and in their slopes.
+// stays one in all of them and in their slopes.  An infinity takes the limit: a
+// factor that has reached 0 is not multiplied by it (a Z kept in fp16 is
+// infinite from 65520 on, and its slope is 1).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -41,9 +43,13 @@ __device__ inline float value(int a, float x) {
     if (a == RELU) return x <= 0.0f ? 0.0f : x;
     if (a == GELU) {
         float e;
-        return x * normal_below(x, e);
+        const float below = normal_below(x, e);
+        return below == 0.0f ? 0.0f : x * below;
     }
-    if (a == SILU) return x * __builtin_amdgcn_rcpf(1.0f + __expf(-x));
+    if (a == SILU) {
+        const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-x));
+        return p == 0.0f ? 0.0f : x * p;
+    }
     return x;
 }
 
@@ -52,10 +58,10 @@ __device__ inline float slope(int a, float x) {
     if (a == GELU) {
         float e;
         const float below = normal_below(x, e);
-        return __builtin_fmaf(x * 0.398942280f, e, below);
+        return e == 0.0f ? below : __builtin_fmaf(x * 0.398942280f, e, below);
     }
-    const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-x));
-    return p * __builtin_fmaf(x, 1.0f - p, 1.0f);
+    const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-x)), q = 1.0f - p;
+    return p * q == 0.0f ? p : p * __builtin_fmaf(x, q, 1.0f);
 }
 
 // Over N values, the choice made once.

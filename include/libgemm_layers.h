@@ -37,7 +37,8 @@
  *
  * Activations are those of gemm_activation_t, evaluated in fp32.  A NaN stays a
  * NaN in each of them and in its slope, ReLU's too (the epilogues of libgemm.h
- * give 0 there).
+ * give 0 there).  At infinities GELU and SiLU, and their slopes, take their
+ * limits.
  */
 #ifndef LIBGEMM_LAYERS_H
 #define LIBGEMM_LAYERS_H

@@ -815,3 +815,28 @@ def test_relu_slope_is_a_choice(lib, M, N, K, kind):
     torch.cuda.synchronize()
     assert torch.equal(out.cpu().double().nan_to_num(nan=9.0), want.nan_to_num(nan=9.0))
     assert torch.equal(total[:6].cpu().double(), want[:, :6].sum(0))
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", KERNEL_SIZES)
+def test_activations_at_infinity(lib, M, N, K, kind, act):
+    """GELU and SiLU take their limits at infinities (0 and +inf; slopes 0 and 1), where fp16's Z of a large value is one; NaN
+    stays NaN; the tails in between are as near as anywhere."""
+    special = [float("nan"), float("inf"), -float("inf"), BIG[kind], -BIG[kind], 30.0, -30.0, -12.0, -9.0, 100.0, -100.0]
+    bias = torch.zeros(N)
+    bias[:len(special)] = torch.tensor(special)
+    c, z, pre = linear_of_bias(lib, M, N, K, kind, act, bias)
+    want = torch.where(pre == -float("inf"), 0.0, ref.act(pre, act))
+    assert torch.equal(c.isnan(), want.isnan()) and torch.equal(c.isinf(), want.isinf())
+    assert c[:, 0].isnan().all() and (c[:, 1] == float("inf")).all() and (c[:, 2] == 0).all()
+    fine = pre.isfinite()  # the others are compared above
+    # |product| < 30: fp32's sums are off by 2^-23 of K + 8 such terms at most, and of z itself; no slope passes 1.13
+    error = 1.13 * ((K + 8) * 30 * 2.0 ** -23 * 0.01 + 2.0 ** -23 * pre.abs()) + ref.act_error(pre, act)
+    close(c[fine], want[fine], (error * 1.01 + 2.0 ** -24 * want.abs() + 2.0 ** -126)[fine], "C")
+    d, sums = slope_of(lib, M, N, K, kind, act, z, torch.ones(M))
+    s = torch.where(z == float("inf"), 1.0, torch.where(z == -float("inf"), 0.0, ref.slope(z, act)))
+    assert torch.equal(d.isnan(), s.isnan()) and torch.equal(sums.isnan(), s.isnan().any(0)) and not d.isinf().any()
+    fine = z.isfinite()
+    close(d[fine], s[fine], (ref.slope_error(z, act) + 2.0 ** -22 * s.abs() + 2.0 ** -126)[fine], "D")
+    assert (d[:, 1] == 1).all() and (d[:, 2] == 0).all()
