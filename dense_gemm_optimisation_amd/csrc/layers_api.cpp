@@ -82,7 +82,7 @@ gemm_status_t linear_plan(const LinearProblem &q, gemm_order_t orderB, LinearPro
     Range rc;
     if (!matrix_ok(p.C, p.M, p.N, p.ldc, type_bytes(p.out), rc)) return GEMM_ERR_INVALID_ARG;
     Range ra{0, 0}, rb{0, 0}, rbias{0, 0}, rr{0, 0}, rz{0, 0}, rd{0, 0};
-    if (p.alpha == 0.0f) p.K = 0;
+    if (p.alpha == 0.0f || p.K == 0) p.K = 0, p.alpha = 0.0f;  // nothing, whatever alpha is
     if (p.K > 0) {
         if (!matrix_ok(p.A, p.M, p.K, p.lda, 2, ra)) return GEMM_ERR_INVALID_ARG;
         if (!(p.b_kmajor ? matrix_ok(p.B, p.N, p.K, p.ldb, 2, rb) : matrix_ok(p.B, p.K, p.N, p.ldb, 2, rb)))

@@ -80,8 +80,8 @@ size_t gemm_linear_workspace_size(int64_t M, int64_t N, int64_t K);
  *            which gemm_linear_backward reads.
  * alpha * A * B, the bias, the activation and the residual are fp32; C and Z
  * are each rounded once, to nearest even.  alpha == 0 or K == 0: A and B are
- * not read.  N at most 2^28 here and in both gradients (GEMM_ERR_UNSUPPORTED
- * beyond).
+ * not read and the product is 0 (whatever alpha is, where K == 0).  N at most
+ * 2^28 here and in both gradients (GEMM_ERR_UNSUPPORTED beyond).
  *   workspace   gemm_linear_workspace_size() bytes.  It may be NULL (with 0
  *            bytes): calls of few rows may then run slower, and give sums in
  *            another order. */

@@ -840,3 +840,21 @@ def test_activations_at_infinity(lib, M, N, K, kind, act):
     fine = z.isfinite()
     close(d[fine], s[fine], (ref.slope_error(z, act) + 2.0 ** -22 * s.abs() + 2.0 ** -126)[fine], "D")
     assert (d[:, 1] == 1).all() and (d[:, 2] == 0).all()
+
+
+@pytest.mark.parametrize("alpha", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("M,N", [(3, 17), (130, 264)])
+def test_empty_product_whatever_alpha(lib, M, N, alpha):
+    """K = 0: there is nothing for alpha to scale."""
+    run_linear(lib, M, N, 0, alpha=1.0, beta=1.0, keep=True)
+    bi, z = draw((N,), "bf16", 4), draw((M, N), "bf16", 5)
+    b, dz = bi.to(DEV), z.to(DEV)
+    c, kept = torch.zeros(M, N, device=DEV), torch.zeros(M, N, dtype=torch.bfloat16, device=DEV)
+    lib.gemm_linear(M, N, 0, alpha, 0, 0, 0, 0, 1, 1, b.data_ptr(), 0, 0.0, 0, 0, c.data_ptr(), N, 0, kept.data_ptr(), N)
+    d, sums = torch.ones(M, N, device=DEV), torch.arange(N, dtype=torch.float32, device=DEV)
+    ws = space(lib.linear_workspace_size(M, N, 0))
+    lib.gemm_linear_backward(M, N, 0, alpha, 0, 0, 0, 0, 1, 1, dz.data_ptr(), N, 2, d.data_ptr(), N, 0, 0.5, sums.data_ptr(),
+                             ws.data_ptr(), ws.numel() * 4)
+    torch.cuda.synchronize()
+    assert torch.equal(c, b.float().expand(M, N)) and torch.equal(kept, b.expand(M, N))
+    assert not d.any() and torch.equal(sums.cpu(), torch.arange(N, dtype=torch.float32) / 2)
