@@ -12,7 +12,10 @@
 // matter: G enters as G * 2^e with an exponent that puts its norm into
 // [2^11, 2^12) (exactly, for a 16-bit G), and the rest of the norm is a factor
 // of the first step's epilogues; X is kept times 2^12, A times 2^12, B times
-// 2^8.
+// 2^8.  An X of a norm below 1/4 (G's far below eps) is kept times a larger power
+// of two, chosen before each update from the norm that it starts from and the
+// most that the step's coefficients make of it (next_scale): its digits would
+// sink into fp16's subnormals, 2.4e-2 of X at 1e-8 of eps, all of them at 1e-12.
 //
 // What is rounded is what differs from the mean: with s the mean of A's
 // eigenvalues (|X|^2 / m) and E = A - s I, the same polynomial of X X^T is
@@ -49,7 +52,9 @@ struct OrthoArgs {
     int64_t batch;
     uint16_t *x, *next, *lo;  // X's first piece, the next step's, the second piece: m x ldx
     uint16_t *gram, *poly;    // A and B: m x lda
-    const float *factor;      // of each matrix: the rest of the norm in the first step, else nullptr
+    const float *factor;      // of each matrix: what x and lo are to be multiplied by for 2^12 X
+    float *next_factor;       // the same of the next step's, written with A
+    const float *norm;        // of each matrix: X's in the first step, else nullptr
     float *shift;             // of each matrix: s of this step
     float *squares;           // of each matrix and tile of the last update: the sum of X's squares
     int64_t tiles_x;          // those tiles
@@ -69,8 +74,8 @@ struct InputArgs {
     const void *G;
     int in;
     float eps;
-    double *parts;          // [batch][PARTS]
-    float *factor, *shift;  // [batch]
+    double *parts;                 // [batch][PARTS]
+    float *factor, *shift, *norm;  // [batch]
     uint16_t *x, *lo;
     int64_t ldx, m;
     int64_t blocks, across;  // of 64 x 64, per matrix and across it
@@ -156,6 +161,7 @@ __global__ __launch_bounds__(256) void input_kernel(InputArgs p) {
     if (block == 0 && threadIdx.x == 0) {
         p.factor[batch] = factor;
         p.shift[batch] = float((norm / least) * (norm / least) / p.m);
+        p.norm[batch] = float(norm / least);
     }
     const bool turned = p.M > p.N;
     const int64_t r0 = down * 64, c0 = along * 64;
@@ -220,6 +226,15 @@ __device__ inline void put_output4(const OrthoArgs &p, int64_t at, const float (
     }
 }
 
+// 2^12 X over what the update of an X of this norm stores: 1 for a norm of 1/4 or
+// more; below, the power of two with which no element of the next X, whose norm
+// is at most |a| + |b| / 16 + |c| / 256 times this, passes 2^15.
+__device__ inline float next_scale(const OrthoArgs &p, float norm) {
+    const float most = norm * fmaxf(16.0f, fabsf(p.a) + fabsf(p.b) + fabsf(p.c));
+    const int up = most > 0.0f && most < 4.0f ? 2 - ilogbf(most) : 0;
+    return ldexpf(1.0f, -(up < 120 ? up : 120));
+}
+
 // Tile `id` of the upper triangle of T x T tiles, row by row (in bands of six
 // rows, which share more panels on a die, 4096 x 4096 took the same time).
 __device__ inline void upper_tile(int64_t id, int64_t T, int64_t &tm, int64_t &tn) {
@@ -263,7 +278,7 @@ struct Updated {
     const uint16_t *x;
     uint16_t *lo, *next;
     int64_t o;
-    float factor, own, square;
+    float factor, own, square;  // factor: of what is stored, or in the last step of 2^12 X
     __device__ void load(Data &d, int64_t r, int64_t c, int count) const {
         d.hi.load(x + r * p.ldx + c, count);
         d.lo.load(lo + r * p.ldx + c, count);
@@ -314,8 +329,13 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::LDS_BYTES > 80 * 1024 ? 1 : 
     // s: read, or added up (by every workgroup alike) from the last update's tiles
     __shared__ float sums[Shape::WAVES];
     float shift = 0.0f;
-    if (STEP != Step::Gram || p.factor != nullptr) {
+    const float f = p.factor[batch];
+    const bool first_thread = tm == 0 && tn == 0 && threadIdx.x == 0;
+    if (STEP != Step::Gram) {
         shift = p.shift[batch];
+    } else if (p.norm != nullptr) {
+        shift = p.shift[batch];
+        if (first_thread) p.next_factor[batch] = next_scale(p, p.norm[batch]);
     } else {
         float q = 0.0f;
         for (int64_t i = threadIdx.x; i < p.tiles_x; i += Shape::THREADS) q += p.squares[batch * p.tiles_x + i];
@@ -323,8 +343,13 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::LDS_BYTES > 80 * 1024 ? 1 : 
         if ((threadIdx.x & 63) == 0) sums[threadIdx.x / 64] = q;
         __syncthreads();
         for (int w = 0; w < Shape::WAVES; ++w) shift += sums[w];
-        shift /= X_SCALE * X_SCALE * float(p.m);
-        if (tm == 0 && tn == 0 && threadIdx.x == 0) p.shift[batch] = shift;
+        // what is stored has a norm that fp32's squares hold; f a power of two
+        const float norm = f * (sqrtf(shift) / X_SCALE);
+        shift = f * (f * (shift / (X_SCALE * X_SCALE * float(p.m))));
+        if (first_thread) {
+            p.shift[batch] = shift;
+            p.next_factor[batch] = next_scale(p, norm);
+        }
     }
     typename Shape::Acc acc;
     // B's filling is columns, X has no rows for them: K = m there
@@ -337,7 +362,6 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::LDS_BYTES > 80 * 1024 ? 1 : 
     const int64_t mw = m0 + Shape::wave_m(wave) * Shape::WTM, nw = n0 + Shape::wave_n(wave) * Shape::WTN;
     const bool live = mw < p.m && nw < N;
     if (SYMMETRIC && !live) return;
-    const float f = p.factor != nullptr ? p.factor[batch] : 1.0f;
     LDS float *staging = Shape::staging(lds, buf, wave);
     if constexpr (SYMMETRIC) {
         typedef Symmetric<STEP> S;
@@ -349,7 +373,8 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::LDS_BYTES > 80 * 1024 ? 1 : 
         if (n0 > m0) visit_tile_turned(acc, p.m, p.m, mw, nw, lane, staging, put);
     } else {
         const int64_t at = batch * p.m * p.ldx;
-        Updated put{p, x, p.lo + at, p.next + at, batch * p.strideO, f,
+        // the quotient of both: f itself may be next to fp32's smallest values
+        Updated put{p, x, p.lo + at, p.next + at, batch * p.strideO, p.last ? f : f / p.next_factor[batch],
                     __builtin_fmaf(shift, __builtin_fmaf(shift, p.c, p.b), p.a), 0.0f};
         if (live) visit_tile(acc, p.m, N, mw, nw, lane, staging, put);
         float square = put.square;
@@ -583,7 +608,7 @@ int64_t round_to(int64_t n, int64_t m) { return ceil_div(n, m) * m; }
 
 struct Layout {
     int64_t m, n, ldx, lda;
-    size_t parts, factor, shift, squares, x, next, lo, gram, poly, bytes;
+    size_t parts, factor[2], norm, shift, squares, x, next, lo, gram, poly, bytes;
 };
 Layout layout_of(int64_t M, int64_t N, int64_t batch) {
     Layout l{};
@@ -598,7 +623,9 @@ Layout layout_of(int64_t M, int64_t N, int64_t batch) {
         return here;
     };
     l.parts = take(batch * PARTS * 8);
-    l.factor = take(batch * 4);
+    l.factor[0] = take(batch * 4);
+    l.factor[1] = take(batch * 4);
+    l.norm = take(batch * 4);
     l.shift = take(batch * 4);
     l.squares = take(batch * ceil_div(l.m, 128) * ceil_div(l.n, 128) * 4);
     l.x = take(batch * l.m * l.ldx * 2);
@@ -710,9 +737,10 @@ static hipError_t launch_batch(const Orthogonalize &p, hipStream_t stream) {
     const Layout l = layout_of(p.M, p.N, p.batch);
     char *w = static_cast<char *>(p.workspace);
     auto half = [&](size_t at) { return reinterpret_cast<uint16_t *>(w + at); };
-    float *factor = reinterpret_cast<float *>(w + l.factor);
-    InputArgs in{p.M, p.N, p.ldg, p.strideG, p.G, p.in, p.eps, reinterpret_cast<double *>(w + l.parts), factor, reinterpret_cast<float *>(w + l.shift),
-                 half(l.x), half(l.lo), l.ldx, l.m};
+    auto floats = [&](size_t at) { return reinterpret_cast<float *>(w + at); };
+    float *factor[2] = {floats(l.factor[0]), floats(l.factor[1])};
+    InputArgs in{p.M, p.N, p.ldg, p.strideG, p.G, p.in, p.eps, reinterpret_cast<double *>(w + l.parts), factor[0],
+                 floats(l.shift), floats(l.norm), half(l.x), half(l.lo), l.ldx, l.m};
     const bool turned = p.M > p.N;
     OrthoArgs a{};
     a.m = l.m;
@@ -721,7 +749,7 @@ static hipError_t launch_batch(const Orthogonalize &p, hipStream_t stream) {
     a.lda = l.lda;
     a.batch = p.batch;
     a.shift = in.shift;
-    a.squares = reinterpret_cast<float *>(w + l.squares);
+    a.squares = floats(l.squares);
     a.x = half(l.x);
     a.next = half(l.next);
     a.lo = half(l.lo);
@@ -759,7 +787,9 @@ static hipError_t launch_batch(const Orthogonalize &p, hipStream_t stream) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     for (int s = 0; s < p.steps; ++s) {
-        a.factor = s == 0 ? factor : nullptr;
+        a.factor = factor[s % 2];
+        a.next_factor = factor[(s + 1) % 2];
+        a.norm = s == 0 ? in.norm : nullptr;
         a.last = s == p.steps - 1;
         a.a = coefficient(s, 0);
         a.b = coefficient(s, 1);

@@ -217,8 +217,9 @@ size_t gemm_orthogonalize_workspace_size(int64_t M, int64_t N, int64_t batch);
  *   batch    matrices strideG and strideO elements apart; those of O must
  *            not overlap.
  *   workspace   gemm_orthogonalize_workspace_size() bytes.
- * The sum of squares is formed in 64 bits.  X is kept between the steps in 22
- * bits or more.  The products take fp16 roundings of X, of E = A - s I with s the
+ * The sum of squares is formed in 64 bits.  X is kept between the steps to 22
+ * bits of each element or to 2^-35 of its norm, whichever is more, also where
+ * G's norm is far below eps.  The products take fp16 roundings of X, of E = A - s I with s the
  * mean of A's eigenvalues, and of (b + 2 c s) E + c E^2, and add in fp32,
  * which leaves X about 2^-10 of its elements' root mean square from the exact
  * steps': less than bf16's own rounding.  All are scaled by powers of two so

@@ -858,3 +858,49 @@ def test_empty_product_whatever_alpha(lib, M, N, alpha):
     torch.cuda.synchronize()
     assert torch.equal(c, b.float().expand(M, N)) and torch.equal(kept, b.expand(M, N))
     assert not d.any() and torch.equal(sums.cpu(), torch.arange(N, dtype=torch.float32) / 2)
+
+
+@pytest.mark.parametrize("ratio", [1e-2, 1e-4, 1e-6, 1e-8, 1e-12, 1e-20])
+@pytest.mark.parametrize("M,N,kernel", [(60, 90, "orthogonalize_small"), (150, 200, "orthogonalize_mfma_128_few"),
+                                        (260, 140, "orthogonalize_mfma_128_few")])
+def test_orthogonalize_norms_below_eps(lib, M, N, kernel, ratio):
+    """A norm far below eps: X starts as small and grows by a factor of 3.45 a step at most, and keeps its digits."""
+    assert lib.orthogonalize_kernel_name(M, N, 1) == kernel
+    steps = 5
+    x = matrix(M, N, 3, "plain").float()
+    eps = torch.tensor(torch.linalg.matrix_norm(x.double()).item() / ratio, dtype=torch.float32).item()
+    d, o = x.to(DEV), torch.zeros(M, N, device=DEV)
+    ws = space(lib.orthogonalize_workspace_size(M, N, 1))
+    lib.gemm_orthogonalize(M, N, d.data_ptr(), N, 0, steps, None, eps, 1.0, 0.0, o.data_ptr(), N, 0, ws.data_ptr(), ws.numel() * 4)
+    torch.cuda.synchronize()
+    want = ref.newton_schulz(x, steps, None, eps)
+    size = torch.linalg.matrix_norm(want).item()
+    # B X with three roundings of 2^-11 each, |B| < 4.8 |X|^2 and |X| < ratio * 3.45^4 before the last step; the four before
+    # add less than that again (|X|^2 is 12 times smaller each time).  X itself: each step rounds it to 22 bits, or in steps of
+    # 2^-24 where its norm is 2^9 or more, 190 root mean squares: below 2^-20 a step.  fp32's own: below 2^-18 over all
+    largest = min(1.0, ratio * 3.45 ** (steps - 1))
+    bound = size * (2 * 4.8 * largest ** 2 * 3 * 2.0 ** -11 + steps * 2.0 ** -20 + 2.0 ** -18)
+    assert torch.linalg.matrix_norm(o.cpu().double() - want).item() <= bound
+
+
+def test_orthogonalize_norms_of_a_batch(lib):
+    """Each matrix of a batch has a scale of its own; coefficients as large as the call promises to hold."""
+    M, N, steps = 150, 200, 3
+    coefficients = [(15.0, 15.0, -15.0), (2.0, -1.5, 0.5), (2.0, -1.5, 0.5)]
+    x = torch.stack([matrix(M, N, 5 + b, "plain") for b in range(4)])
+    x = x / torch.linalg.matrix_norm(x)[:, None, None]
+    x = (x * torch.tensor([1e-9, 0.01, 0.06, 0.0], dtype=torch.float64)[:, None, None]).float()
+    d, o = x.to(DEV), torch.zeros(4, M, N, device=DEV)
+    ws = space(lib.orthogonalize_workspace_size(M, N, 4))
+    assert lib.orthogonalize_kernel_name(M, N, 4) != "orthogonalize_small"
+    lib.gemm_orthogonalize(M, N, d.data_ptr(), N, 0, steps, coefficients, 1.0, 1.0, 0.0, o.data_ptr(), N, 0, ws.data_ptr(),
+                           ws.numel() * 4, batch=4, stride_g=M * N, stride_o=M * N)
+    torch.cuda.synchronize()
+    for b, norm in enumerate((1e-9, 0.01, 0.06)):
+        want = ref.newton_schulz(x[b], steps, coefficients, 1.0)
+        size = torch.linalg.matrix_norm(want).item()
+        # |B| < 16 |X|^2 in the first step, then 1.6 |X|^2 of an X up to 15.1 and 31 times larger; roundings as above
+        bound = size * (2 * 3 * 2.0 ** -11 * (16 * norm ** 2 + 1.6 * (15.1 * norm) ** 2 + 1.6 * min(1.0, 31 * norm) ** 2) +
+                        steps * 2.0 ** -20 + 2.0 ** -18)
+        assert torch.linalg.matrix_norm(o[b].cpu().double() - want).item() <= bound
+    assert not o[3].any()
