@@ -621,7 +621,6 @@ hipError_t run_down(LayerArgs &a, hipStream_t stream) {
     const size_t lds = size_t(WAVES * a.ring_down * stage + beside);
     hipError_t e = allow_lds(down_kernel<T, TYPE, DT>, lds);
     if (e != hipSuccess) return e;
-    if (ceil_div(p.D, 16) > 0x7fffff) return hipErrorInvalidConfiguration;
     down_kernel<T, TYPE, DT><<<dim3(unsigned(ceil_div(p.D, 16))), dim3(THREADS), lds, stream>>>(a);
     return hipGetLastError();
 }

@@ -17,10 +17,7 @@ static_assert(GEMM_LAYER_MAX_TOKENS == LAYER_MAX_TOKENS && GEMM_LAYER_MAX_EXPERT
                   GEMM_LAYER_MAX_TOP_K == LAYER_MAX_TOP_K,
               "the header's limits are the kernels'");
 
-gemm_status_t status_of(hipError_t e) {
-    if (e == hipErrorInvalidConfiguration) return GEMM_ERR_UNSUPPORTED;
-    return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
-}
+gemm_status_t status_of(hipError_t e) { return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP; }
 
 bool misaligned(const void *p, int64_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -331,7 +328,8 @@ gemm_status_t gemm_orthogonalize(int64_t M, int64_t N, const void *G, int64_t ld
     if (workspace == nullptr || misaligned(workspace, 16) || workspace_bytes < need) return GEMM_ERR_INVALID_ARG;
     const Range rw = bytes_at(workspace, int64_t(need));
     if (meets(ro, {rg, rw}) || overlap(rw, rg)) return GEMM_ERR_INVALID_ARG;
-    if (M > (1 << 20) || N > (1 << 20)) return GEMM_ERR_UNSUPPORTED;
+    // a launch has less than 2^32 threads, 256 of them for each block of 64 x 64
+    if (M > (1 << 20) || N > (1 << 20) || ceil_div(M, 64) * ceil_div(N, 64) >= (1 << 24)) return GEMM_ERR_UNSUPPORTED;
     Orthogonalize p{M, N, G, ldg, int(in), int(steps), coefficients, eps, alpha, beta, O, ldo, int(typeO),
                     batch, batch > 1 ? strideG : 0, batch > 1 ? strideO : 0, workspace};
     return status_of(launch_orthogonalize(p, stream));

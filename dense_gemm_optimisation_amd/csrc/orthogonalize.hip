@@ -698,7 +698,6 @@ hipError_t launch_product(OrthoArgs &a, hipStream_t stream) {
     a.tiles_n = ceil_div(cols, side_of(size));
     if (!SYMMETRIC) a.tiles_x = a.tiles_m * a.tiles_n;
     const int64_t tiles = a.batch * (SYMMETRIC ? a.tiles_m * (a.tiles_m + 1) / 2 : a.tiles_m * a.tiles_n);
-    if (tiles > 0x7fffff) return hipErrorInvalidConfiguration;
     if (size == Size::Large) return launch_shape<Large, STEP>(a, tiles, stream);
     if (size == Size::Small) return launch_shape<Small, STEP>(a, tiles, stream);
     if (size == Size::Few) return launch_shape<Few, STEP>(a, tiles, stream);

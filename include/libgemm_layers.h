@@ -226,7 +226,8 @@ size_t gemm_orthogonalize_workspace_size(int64_t M, int64_t N, int64_t batch);
  * that steps whose singular values stay below 2 and whose coefficients stay
  * below 16 in magnitude are within fp16's range; others may give infinities or NaN.  A matrix with an
  * infinity or a NaN gives NaN throughout.
- * steps in 1 .. GEMM_ORTHOGONALIZE_MAX_STEPS (GEMM_ERR_UNSUPPORTED beyond). */
+ * steps in 1 .. GEMM_ORTHOGONALIZE_MAX_STEPS; M and N at most 2^20, and less
+ * than 2^24 blocks of 64 x 64 in a matrix (GEMM_ERR_UNSUPPORTED beyond). */
 gemm_status_t gemm_orthogonalize(int64_t M, int64_t N, const void *G, int64_t ldg,
                                  gemm_input_t in, int64_t steps, const float *coefficients,
                                  float eps, float alpha, float beta, void *O, int64_t ldo,

@@ -215,3 +215,12 @@ def test_sizes(lib):
     assert lib.experts_layer_workspace_size(64, 8, 2, 64, 64) >= 64 * 2 * 64 * 4
     assert lib.orthogonalize_workspace_size(0, 4, 1) == 0
     assert lib.orthogonalize_workspace_size(100, 50, 2) >= 2 * (3 * 50 * 104 + 2 * 50 * 56) * 2
+
+
+def test_orthogonalize_too_large_to_launch(lib):
+    """2^24 blocks of 64 x 64 of a matrix are refused before anything is launched (a call that got past the checks would end in
+    ERR_HIP here, without a GPU)."""
+    most = lib.orthogonalize_workspace_size(1 << 20, 1 << 16, 1)
+    for M, N in ((1 << 20, 1 << 16), (1 << 16, 1 << 20), ((1 << 20) - 63, (1 << 16) - 63)):
+        assert ortho_call(lib, M=M, N=N, ldg=N, ldo=N, G=1 << 50, O=1 << 52, workspace=1 << 54,
+                          workspace_bytes=most) == lib.ERR_UNSUPPORTED
