@@ -92,6 +92,14 @@ __device__ inline u32x4 widen(uint32_t lo, uint32_t hi) {
     return u32x4{widen2<T, TYPE, false>(lo), widen2<T, TYPE, true>(lo), widen2<T, TYPE, false>(hi), widen2<T, TYPE, true>(hi)};
 }
 
+// The two pieces of w h: hi of w h * TIMES, and lo of what hi leaves out * REST.
+// fp16 has a few powers of two more below w h's usual values than above them;
+// lo is as large as hi, so it is a subnormal only where hi is.
+template <class T>
+struct Pieces {
+    static constexpr float TIMES = __is_same(T, F16) ? 0x1p-4f : 1.0f, REST = __is_same(T, F16) ? 0x1p11f : 1.0f;
+};
+
 // Lane q of four (lane / 16) has eight k of each step: 16-bit weights those
 // of chunk 4s + q, 32s + 8q; codes half s % 2 of chunk 4(s / 2) + q, 64(s / 2) + 16q +
 // 8(s % 2); the activations in the same order, by their own chunks of 8.
@@ -426,11 +434,11 @@ __global__ __launch_bounds__(THREADS, 1) void up_kernel(LayerArgs a) {
                     o += part[(w * 2 + 1) * (16 * XR) + threadIdx.x];
                 }
                 act::apply(p.act, v);
-                const float wh = h0 + j < p.H ? v[0] * o * share[at] : 0.0f;
+                const float wh = h0 + j < p.H ? v[0] * o * share[at] * Pieces<T>::TIMES : 0.0f;
                 const uint32_t hi = encode<T>(wh);
                 uint16_t *h = a.h + (token[at] * k + choice[at]) * a.ldh + (h0 + j) / F::RUN * (2 * F::RUN) + (h0 + j) % F::RUN;
                 h[0] = uint16_t(hi);
-                h[F::RUN] = uint16_t(encode<T>(wh - decode<T>(hi)));
+                h[F::RUN] = uint16_t(encode<T>((wh - decode<T>(hi)) * Pieces<T>::REST));
             }
             __syncthreads();
         }
@@ -559,7 +567,8 @@ __global__ __launch_bounds__(THREADS, 1) void down_kernel(LayerArgs a) {
             LDS f32x4 *sum = sums + (wave * tokens + t) * 4 + q;
             f32x4 y = *sum;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = __builtin_fmaf(scale, block[j] + rest[j], y[j]);
+            for (int j = 0; j < 4; ++j)
+                y[j] = __builtin_fmaf(scale / Pieces<T>::TIMES, __builtin_fmaf(1.0f / Pieces<T>::REST, rest[j], block[j]), y[j]);
             *sum = y;
         }
     }

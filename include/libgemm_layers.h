@@ -182,8 +182,9 @@ size_t gemm_experts_layer_workspace_size(int64_t tokens, int64_t experts, int64_
  *            not read it.  A token without experts gets beta * Y.
  *   workspace   gemm_experts_layer_workspace_size() bytes.
  * Sums are fp32; w h is formed in fp32 and enters the second product as two
- * pieces of X's type, which hold 16 of its 24 bits in bf16 and 22 in fp16 (one
- * beyond the type's largest value, 65504 in fp16, gives infinities or NaN).
+ * pieces of X's type, which hold 16 of its 24 bits in bf16 and 22 in fp16 (there
+ * from 2^-10 up to 2^20: below in steps of 2^-31, beyond it gives infinities
+ * or NaN).
  * At most GEMM_LAYER_MAX_TOKENS tokens, _EXPERTS experts and _TOP_K choices
  * (GEMM_ERR_UNSUPPORTED beyond: gemm_experts_f8 takes more tokens); H at most
  * 2^17, ldx 2^23, ld_up and ld_down 2^25. */

@@ -904,3 +904,24 @@ def test_orthogonalize_norms_of_a_batch(lib):
                         steps * 2.0 ** -20 + 2.0 ** -18)
         assert torch.linalg.matrix_norm(o[b].cpu().double() - want).item() <= bound
     assert not o[3].any()
+
+
+@pytest.mark.parametrize("form", ["same", "e4m3"])
+@pytest.mark.parametrize("gate,weight", [(2.0 ** -14, 64.0), (2.0 ** -20, 1024.0), (2.0 ** 18, 1.0)])
+def test_experts_layer_range_of_products(lib, form, gate, weight):
+    """fp16's w h from 2^-30 to 2^19.4, far below its smallest normal value and beyond its largest, for an fp32 Y."""
+    T, E, k, D, H = 9, 4, 2, 136, 200
+    c = experts_case(lib, T, E, k, D, H, "f16", form, act="relu", out="f32")
+    c["gates"] *= gate
+    c["dgates"].copy_(c["gates"])
+    down = c["stored"][1]
+    (down[0] if form == "same" else down[1]).mul_(weight)
+    c["values"][1] = [v * weight for v in c["values"][1]]
+    experts_call(lib, c)
+    torch.cuda.synchronize()
+    want, bound = ref.experts_layer(c["x"], c["ids"], c["gates"], *c["values"], "relu", 0.0, None, "f32", "f16")
+    # the reference allows steps of 2^-24 in w h; they are 2^-31 (2^4 times fp16's 2^-24 times 2^-11)
+    size = torch.stack([sum(c["values"][1][e].abs().sum(1) for e in row.tolist()) for row in c["ids"]])
+    bound = bound - (2.0 ** -24 - 2.0 ** -31) * size
+    assert (bound > 0).all()
+    close(c["my"].get(), want, bound, "Y")
