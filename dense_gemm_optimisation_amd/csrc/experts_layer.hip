@@ -603,9 +603,8 @@ static_assert(4 * (LAYER_MAX_EXPERTS + 1) + 2 * (LAYER_MAX_EXPERTS + 1) + 2 * LA
 int ring_of(int64_t stage, int64_t beside) { return int(least(4, (MOST_LDS - 1024 - beside) / (WAVES * stage))); }
 
 template <class K>
-hipError_t allow_lds(K kernel, size_t bytes) {
-    if (bytes <= 64 * 1024) return hipSuccess;
-    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, MOST_LDS - 1024);
+hipError_t allow(K kernel, size_t bytes, hipStream_t stream) {
+    return bytes <= 64 * 1024 ? hipSuccess : allow_lds(reinterpret_cast<const void *>(kernel), MOST_LDS - 1024, stream);
 }
 
 template <class T, int TYPE, int XR>
@@ -615,7 +614,7 @@ hipError_t run_up(LayerArgs &a, hipStream_t stream) {
     const int64_t beside = part + found_bytes(p);
     a.ring_up = ring_of(stage, beside);
     const size_t lds = size_t(WAVES * a.ring_up * stage + beside);
-    hipError_t e = allow_lds(up_kernel<T, TYPE, XR>, lds);
+    hipError_t e = allow(up_kernel<T, TYPE, XR>, lds, stream);
     if (e != hipSuccess) return e;
     const int64_t blocks = p.tokens * p.top_k * ceil_div(p.H, 16);  // at most
     up_kernel<T, TYPE, XR><<<dim3(unsigned(least(blocks, UNITS))), dim3(THREADS), lds, stream>>>(a);
@@ -628,7 +627,7 @@ hipError_t run_down(LayerArgs &a, hipStream_t stream) {
     const int64_t beside = WAVES * p.tokens * 64 + 9 * p.tokens * p.top_k;
     a.ring_down = ring_of(stage, beside);
     const size_t lds = size_t(WAVES * a.ring_down * stage + beside);
-    hipError_t e = allow_lds(down_kernel<T, TYPE, DT>, lds);
+    hipError_t e = allow(down_kernel<T, TYPE, DT>, lds, stream);
     if (e != hipSuccess) return e;
     down_kernel<T, TYPE, DT><<<dim3(unsigned(ceil_div(p.D, 16))), dim3(THREADS), lds, stream>>>(a);
     return hipGetLastError();

@@ -9,6 +9,20 @@
 
 namespace libgemm {
 
+// Lets a kernel have up to `bytes` of dynamic LDS, which beyond 64 KiB it has to
+// be allowed, on the device of `stream`; the attribute is set on the current
+// device, which need not be that one and stays what it was.
+inline hipError_t allow_lds(const void *kernel, int bytes, hipStream_t stream) {
+    int device = 0, current = 0;
+    hipError_t e = hipStreamGetDevice(stream, &device);
+    if (e == hipSuccess) e = hipGetDevice(&current);
+    if (e == hipSuccess && device != current) e = hipSetDevice(device);
+    if (e != hipSuccess) return e;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const hipError_t back = device != current ? hipSetDevice(current) : hipSuccess;
+    return e != hipSuccess ? e : back;
+}
+
 // Types: 0 fp32, 1 bf16, 2 fp16 (gemm_input_t and gemm_output_t alike).
 struct LinearProblem {
     int64_t M, N, K;  // K = 0: nothing is multiplied

@@ -648,8 +648,7 @@ size_t small_lds(int64_t m, int64_t n) {
 template <int BLOCKS>
 hipError_t launch_small(const SmallArgs &a, size_t lds, hipStream_t stream) {
     if (lds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&small_kernel<BLOCKS>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, SMALL_LDS);
+        const hipError_t e = allow_lds(reinterpret_cast<const void *>(&small_kernel<BLOCKS>), SMALL_LDS, stream);
         if (e != hipSuccess) return e;
     }
     small_kernel<BLOCKS><<<dim3(unsigned(a.p.batch)), dim3(SMALL_WAVES * 64), lds, stream>>>(a);

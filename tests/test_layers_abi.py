@@ -4,6 +4,7 @@ definitions."""
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -224,3 +225,55 @@ def test_orthogonalize_too_large_to_launch(lib):
     for M, N in ((1 << 20, 1 << 16), (1 << 16, 1 << 20), ((1 << 20) - 63, (1 << 16) - 63)):
         assert ortho_call(lib, M=M, N=N, ldg=N, ldo=N, G=1 << 50, O=1 << 52, workspace=1 << 54,
                           workspace_bytes=most) == lib.ERR_UNSUPPORTED
+
+
+# ---- the device that a call configures its kernels on
+RECORDER = r"""
+#include <stdio.h>
+#include <stddef.h>
+typedef struct { unsigned x, y, z; } dim3_t;
+static int current = 0;
+int hipGetDevice(int *d) { *d = current; return 0; }
+int hipSetDevice(int d) { current = d; return 0; }
+int hipStreamGetDevice(void *stream, int *d) { *d = stream ? 1 : current; return 0; }
+int hipFuncSetAttribute(const void *f, int a, int v) { printf("attribute %d\n", current); fflush(stdout); return 0; }
+int hipLaunchKernel(const void *f, dim3_t g, dim3_t b, void **p, size_t lds, void *stream) {
+    printf("launch %d\n", lds > 65536); fflush(stdout); return 0;
+}
+static dim3_t grid, block;
+static size_t dynamic;
+static void *on;
+int __hipPushCallConfiguration(dim3_t g, dim3_t b, size_t lds, void *stream) {
+    grid = g; block = b; dynamic = lds; on = stream; return 0;
+}
+int __hipPopCallConfiguration(dim3_t *g, dim3_t *b, size_t *lds, void **stream) {
+    *g = grid; *b = block; *lds = dynamic; *stream = on; return 0;
+}
+int hipGetLastError(void) { return 0; }
+"""
+
+
+@pytest.mark.parametrize("stream,device", [(0, 0), (0x1000, 1)])
+def test_large_lds_is_allowed_on_the_streams_device(lib, tmp_path, stream, device):
+    """A kernel of more than 64 KiB of dynamic LDS is allowed them where it runs: on the device of `stream`, which need not be
+    the current one (and that stays current).  HIP's calls are recorded, nothing runs."""
+    src, so = tmp_path / "recorder.c", tmp_path / "recorder.so"
+    src.write_text(RECORDER)
+    subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
+    call = f"""
+import ctypes, sys
+sys.path.insert(0, {ROOT!r})
+from dense_gemm_optimisation_amd import binding as lib
+p = [i << 36 for i in range(1, 9)]
+print("begin", flush=True)
+lib.gemm_orthogonalize(128, 128, p[0], 128, 0, 5, None, 0.0, 1.0, 0.0, p[1], 128, 0, p[2], 1 << 30, stream={stream})
+lib.gemm_experts_layer(1, 64, 8, 4096, 1024, p[0], 4096, 1, p[1], p[2], 0, p[3], 4096, 2048 * 4096, 0, 0, 0, p[4], 1024, 4096 * 1024,
+                       0, 0, 0, 3, 0.0, p[5], 4096, 1, p[6], 1 << 30, stream={stream})
+d = ctypes.c_int(-1)
+ctypes.CDLL({str(so)!r}).hipGetDevice(ctypes.byref(d))
+print("current", d.value, flush=True)
+"""
+    env = dict(os.environ, LD_PRELOAD=str(so))
+    out = subprocess.run([sys.executable, "-c", call], capture_output=True, text=True, check=True, env=env).stdout
+    said = out.split("begin\n")[1].splitlines()
+    assert said == [f"attribute {device}", "launch 1"] * 3 + ["current 0"]
