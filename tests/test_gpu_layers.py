@@ -925,3 +925,103 @@ def test_experts_layer_range_of_products(lib, form, gate, weight):
     bound = bound - (2.0 ** -24 - 2.0 ** -31) * size
     assert (bound > 0).all()
     close(c["my"].get(), want, bound, "Y")
+
+
+# ---------------------------------------------------------------- more stages than a ring holds
+@pytest.mark.parametrize("M,N,K,kind", [(1, 40, 10000, "bf16"), (4, 33, 8200, "f16"), (7, 50, 10000, "f16"), (8, 16, 12296, "bf16"),
+                                        (9, 70, 10000, "bf16"), (16, 100, 8200, "f16"), (16, 48, 16384, "bf16")])
+@pytest.mark.parametrize("backward", [False, True])
+def test_linear_few_rows_long_k(lib, M, N, K, kind, backward):
+    """Each wave of few_kernel has 8 to 16 runs of K, its ring 2 to 4; the last runs are partial."""
+    if backward:
+        run_backward(lib, M, N, K, kind, expect="linear_few_16", beta=1.0)
+    else:
+        run_linear(lib, M, N, K, kind, beta=1.0, keep=True, expect="linear_few_16")
+
+
+@pytest.mark.parametrize("kind,order", [("bf16", "nk"), ("f16", "kn"), ("bf16", "kn")])
+@pytest.mark.parametrize("backward", [False, True])
+def test_linear_large_tiles_long_k(lib, kind, order, backward):
+    """256 x 256 tiles whose two stages are refilled; the last stage is partial."""
+    M, N, K = 3600, 3656, 584
+    if backward:
+        run_backward(lib, M, N, K, kind, order, expect="linear_mfma_256")
+    else:
+        run_linear(lib, M, N, K, kind, order, beta=1.0, keep=True, out="f32", expect="linear_mfma_256")
+
+
+@pytest.mark.parametrize("form,kind", [("same", "bf16"), ("same", "f16"), ("e4m3", "bf16"), ("e5m2", "f16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("T,E,k,H", [(1, 4, 2, 1000), (3, 8, 2, 1000), (12, 8, 2, 1000), (32, 6, 2, 1000), (20, 2, 2, 2056)])
+def test_experts_layer_long_rows(lib, T, E, k, H, form, kind):
+    """D = 4104: each wave has 4 to 9 runs of a row, more blocks than one, and groups of one expert and the next in a workgroup;
+    H is 8 to 33 runs of each of several experts.  T by 8 and by 16 tokens at a time, and by 4 and 8."""
+    experts_check(lib, T, E, k, 4104, H, kind, form, beta=1.0)
+
+
+# ---------------------------------------------------------------- special values of matrices that take several launches
+LARGE = [(150, 200), (260, 140)]  # one as it is, one turned
+
+
+def several_launches(lib, M, N, batch=1):
+    assert lib.orthogonalize_kernel_name(M, N, batch).startswith("orthogonalize_mfma")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-12, 1.0, 1e15, 1e30, 1e36])
+@pytest.mark.parametrize("M,N", LARGE)
+def test_orthogonalize_scales_of_large(lib, M, N, scale, kind):
+    """As test_orthogonalize_scales; the smallest are subnormal."""
+    several_launches(lib, M, N)
+    run_ortho(lib, M, N, kind, scale=scale, eps=0.0)
+
+
+@pytest.mark.parametrize("M,N", LARGE)
+def test_orthogonalize_unusual_values_of_large(lib, M, N):
+    """As test_orthogonalize_unusual_values."""
+    several_launches(lib, M, N, 5)
+    x = torch.stack([matrix(M, N, i, "plain") for i in range(5)]).float()
+    x[0], x[1, 5, 6], x[2, 3, 3], x[4, M - 1, N - 1] = 0, float("inf"), float("nan"), -float("inf")
+    d, o = x.to(DEV), torch.ones(5, M, N, device=DEV)
+    ws = space(lib.orthogonalize_workspace_size(M, N, 5))
+    for eps in (0.0, 1e-7):
+        o.fill_(1)
+        lib.gemm_orthogonalize(M, N, d.data_ptr(), N, 0, 5, None, eps, 1.0, 0.5, o.data_ptr(), N, 0, ws.data_ptr(), ws.numel() * 4,
+                               batch=5, stride_g=M * N, stride_o=M * N)
+        torch.cuda.synchronize()
+        assert (o[0] == 0.5).all() and o[1].isnan().all() and o[2].isnan().all() and o[4].isnan().all()
+        want = ref.newton_schulz(x[3], 5)
+        drift = torch.linalg.matrix_norm(ref.newton_schulz(x[3], 5, rounding=True) - want)
+        off = torch.linalg.matrix_norm(o[3].cpu().double() - 0.5 - want)
+        # as run_ortho's bound; the halves of O round to 2^-24
+        assert off <= 2 * drift + 2.0 ** -16 * torch.linalg.matrix_norm(want) + 2.0 ** -24 * (M * N) ** 0.5
+
+
+@pytest.mark.parametrize("M,N", LARGE)
+def test_orthogonalize_steps_of_large(lib, M, N):
+    """As test_orthogonalize_coefficients, and every number of steps (X's two buffers change places in each)."""
+    several_launches(lib, M, N)
+    cubic = [(4.0848, -6.8946, 2.9270), (3.9505, -6.3029, 2.6377), (3.7418, -5.5913, 2.3037), (2.8769, -3.1427, 1.2046),
+             (2.8366, -3.0525, 1.2012), (1.5, -0.5, 0.0), (1.5, -0.5, 0.0), (1.5, -0.5, 0.0)]
+    x = run_ortho(lib, M, N, steps=8, coefficients=cubic)[0]
+    assert (torch.linalg.svdvals(x) - 1).abs().max() < 0.02
+    for steps in (1, 2, 3, 4, 32):
+        run_ortho(lib, M, N, steps=steps, coefficients=[(1.5, -0.5, 0.0)] * steps, beta=0.5)
+
+
+# ---------------------------------------------------------------- tokens among others
+@pytest.mark.parametrize("form,kind", [("same", "f16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("T,E", [(6, 4), (40, 3)])
+def test_experts_layer_unusual_tokens(lib, T, E, form, kind):
+    """A token with an infinity or a NaN leaves those it shares experts, and matrix instructions, with as they were."""
+    c = experts_case(lib, T, E, 2, 200, 136, kind, form)
+    c["x"][2, 7], c["x"][5, 199], c["x"][T - 1, 0] = float("nan"), float("inf"), float("nan")
+    c["mx"].view.copy_(c["x"])
+    c["dgates"][0, 0] = float("inf")
+    experts_call(lib, c)
+    torch.cuda.synchronize()
+    odd = sorted({0, 2, 5, T - 1})
+    fine = [t for t in range(T) if t not in odd]
+    want, bound = ref.experts_layer(c["x"], c["ids"], c["gates"], *c["values"], "silu", 0.0, None, kind, kind)
+    got = c["my"].get()
+    assert not got[odd].isfinite().any()
+    close(got[fine], want[fine], bound[fine], "Y")
