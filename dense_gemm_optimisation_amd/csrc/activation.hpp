@@ -9,8 +9,8 @@
 //   x * phi(x) nearly cancel.
 // SiLU(x) = x / (1 + exp(-x)).  ReLU(x) = max(x, 0), its slope at 0 is 0.  A NaN
 // stays one in all of them and in their slopes.  An infinity takes the limit: a
-// factor that has reached 0 is not multiplied by it (a Z kept in fp16 is
-// infinite from 65520 on, and its slope is 1).
+// factor that has reached 0 times it is 0 (a Z kept in fp16 is infinite from
+// 65520 on, and its slope is 1).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -21,10 +21,13 @@ namespace act {
 constexpr int NONE = 0, RELU = 1, GELU = 2, SILU = 3;
 
 #if defined(__HIPCC__)
-// e <- exp(-x^2 / 2); Phi(x)
-__device__ inline float normal_below(float x, float &e) {
-    const float u = fabsf(x);
-    const float t = __builtin_amdgcn_rcpf(1.0f + 0.28f * u);
+// min(|x|, the largest number): a factor without the infinities that a factor of
+// 0 would turn into NaN.  (A NaN's other factor is one too.)
+__device__ inline float finite(float x) { return __builtin_amdgcn_fmed3f(fabsf(x), 0.0f, __FLT_MAX__); }
+
+// q(|x|) and e <- exp(-x^2 / 2): Phi(-|x|) is their product.
+__device__ inline float normal_tail(float x, float &e) {
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.28f * fabsf(x));
     float q = 0.0247200172f;
     q = __builtin_fmaf(q, t, -0.0935932765f);
     q = __builtin_fmaf(q, t, 0.0924283286f);
@@ -35,33 +38,35 @@ __device__ inline float normal_below(float x, float &e) {
     q = __builtin_fmaf(q, t, 0.111699803f);
     q = __builtin_fmaf(q, t, 0.111703858f);
     e = __expf(-0.5f * x * x);
-    const float tail = q * t * e;
-    return x >= 0.0f ? 1.0f - tail : tail;
+    return q * t;
 }
 
+// GELU(x) = max(x, 0) - |x| Phi(-|x|).
 __device__ inline float value(int a, float x) {
     if (a == RELU) return x <= 0.0f ? 0.0f : x;
     if (a == GELU) {
         float e;
-        const float below = normal_below(x, e);
-        return below == 0.0f ? 0.0f : x * below;
+        const float q = normal_tail(x, e);
+        return __builtin_fmaf(-finite(x), q * e, fmaxf(x, 0.0f));
     }
     if (a == SILU) {
         const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-x));
-        return p == 0.0f ? 0.0f : x * p;
+        return __builtin_amdgcn_fmed3f(x, -__FLT_MAX__, __builtin_inff()) * p;
     }
     return x;
 }
 
-// Of GELU and SiLU.
+// Of GELU and SiLU.  GELU'(-u) = exp(-u^2 / 2) (q(u) - u / sqrt(2 pi)), and
+// GELU'(u) = 1 - GELU'(-u).
 __device__ inline float slope(int a, float x) {
     if (a == GELU) {
         float e;
-        const float below = normal_below(x, e);
-        return e == 0.0f ? below : __builtin_fmaf(x * 0.398942280f, e, below);
+        const float q = normal_tail(x, e);
+        const float s = e * __builtin_fmaf(finite(x), -0.398942280f, q);
+        return x >= 0.0f ? 1.0f - s : s;
     }
-    const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-x)), q = 1.0f - p;
-    return p * q == 0.0f ? p : p * __builtin_fmaf(x, q, 1.0f);
+    const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-x));
+    return p * __builtin_fmaf(__builtin_amdgcn_fmed3f(x, -__FLT_MAX__, __FLT_MAX__), 1.0f - p, 1.0f);
 }
 
 // Over N values, the choice made once.
