@@ -501,6 +501,19 @@ int split_slices(int64_t tiles, int64_t K) {
     const int64_t more = few < stages / 2 ? few : stages / 2;
     return int(s > more ? s : more > 1 ? more : 1);
 }
+// K from which slices pay for a second launch and the sums' way through memory.
+// bf16, us in slices and not: 4 tiles, K 256 7.6 and 7.5, 512 8.3 and 9.3; 32
+// tiles, 512 10.5 and 10.6, 1024 12 and 15; 64 tiles, 1024 20 and 16, 2048 25 and
+// 25, 4096 26 and 43; 128 tiles, 2048 29 and 25, 4096 34 and 44; 256 tiles, 512
+// 30 and 12, 2048 34 and 27, 4096 51 and 58, 16384 153 and 218.  Panels through
+// registers take longer a step: 16 tiles, 256 9.2 and 10; 64 tiles, 512 17 and
+// 16, 1024 22 and 26; 128 tiles, 1024 27 and 26, 2048 30 and 44; 256 tiles, 1024 32
+// and 26, 2048 42 and 45.
+int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+int64_t split_from(int64_t tiles, bool direct) {
+    if (!direct) return least(16 * tiles, 2048);
+    return tiles < 16 ? 512 : least(32 * tiles, 4096);
+}
 int64_t tiles_of(int64_t M, int64_t N, int64_t t) { return ceil_div(M, t) * ceil_div(N, t); }
 // Slices of K for the tiles of 256 x 256 that whole rounds of 256 leave over; 1
 // where they stay one more round.  A round takes its time however few tiles it
@@ -702,7 +715,7 @@ LinearKernel linear_choose(const LinearProblem &p) {
     }
     const int64_t t128 = tiles_of(p.M, p.N, 128);
     const int slices = p.K > 0 ? split_slices(t128, p.K) : 1;
-    const bool split = slices > 1 && p.workspace != nullptr &&
+    const bool split = slices > 1 && p.K >= split_from(t128, direct) && p.workspace != nullptr &&
                        p.workspace_bytes >= sums_bytes(p.M, p.N) + partial_bytes(p.M, p.N, slices);
     if (!direct) return split ? LinearKernel::AnySplit : LinearKernel::Any;
     if (split) return LinearKernel::Split;

@@ -277,3 +277,17 @@ print("current", d.value, flush=True)
     out = subprocess.run([sys.executable, "-c", call], capture_output=True, text=True, check=True, env=env).stdout
     said = out.split("begin\n")[1].splitlines()
     assert said == [f"attribute {device}", "launch 1"] * 3 + ["current 0"]
+
+
+@pytest.mark.parametrize("M,N,K,odd,split", [
+    (64, 512, 512, 0, True), (64, 512, 256, 0, False), (64, 4096, 1024, 0, True), (768, 1024, 1024, 0, False),
+    (1024, 1024, 1024, 0, False), (1024, 1024, 4096, 0, True), (1024, 2048, 1024, 0, False), (2048, 2048, 512, 0, False),
+    (2048, 2048, 2048, 0, False), (2048, 2048, 16384, 0, True), (64, 512, 256, 1, True), (1000, 1024, 512, 1, False),
+    (1000, 1024, 1024, 1, True), (900, 2048, 1024, 1, False), (900, 2048, 4096, 1, True),
+])
+def test_linear_cuts_k_where_that_pays(lib, M, N, K, odd, split):
+    """K in slices costs a second launch and the sums' way through memory: not for few steps of K, and the fewer the more tiles
+    there are."""
+    name = linear_call(lib, names=True, M=M, N=N, K=K, lda=K + odd, ldb=K + odd, ldc=N, ldr=N, ldz=N)
+    kernel = "linear_mfma_any" if odd else "linear_mfma_128"
+    assert name == kernel + ("_split" if split else "")
