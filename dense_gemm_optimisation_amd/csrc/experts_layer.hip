@@ -25,8 +25,8 @@
 // from LDS, and a run of 128 has one scale.
 //
 // 64 experts of 1024 x 4096: one token of eight in bf16 30 + 17 us (4.3 TB/s), 32
-// tokens in 8 bits 113 + 77 us (4.2 TB/s; there widening and the short runs' latency
-// count too: without memory 78 and 75).
+// tokens in 8 bits 115 + 82 us (100 to 143 and 77 to 87; 4.1 TB/s: there widening
+// and the short runs' latency count too, without memory 78 and 75).
 //
 // Each workgroup finds the live experts and their tokens from the ids by
 // itself (at most 2048 of them, from L2), which saves a launch.
@@ -273,8 +273,8 @@ __device__ void find(const ExpertsLayer &p, const Found &f, int size) {
 
 // XR: tokens of a group at most.  The blocks of 16 rows of all groups are dealt
 // to the workgroups in equal shares, one workgroup per compute unit: finding
-// the experts takes 4 us, which a workgroup for every few blocks paid four times over (32
-// tokens of 64 experts in 8 bits: 113 us).
+// the experts takes 4 us, which a workgroup for every few blocks would pay over
+// and over.
 template <class T, int TYPE, int XR>
 __global__ __launch_bounds__(THREADS, 1) void up_kernel(LayerArgs a) {
     using F = Form<TYPE>;

@@ -12,10 +12,10 @@
 //                    than half full: its tiles are cut into slices of K;
 //   split            the 128 x 128 tiles with K cut into slices, each slice's
 //                    sums in the workspace, joined in order by finish_kernel,
-//                    which also has the epilogue: problems of few tiles;
+//                    which also has the epilogue: few tiles, long K;
 //   few              up to 16 rows against a K-contiguous B: 16 columns per
-//                    workgroup, K dealt to eight waves, operands straight
-//                    into registers; bound by reading B;
+//                    workgroup, K dealt to eight waves, each with a ring of its
+//                    own in LDS; bound by reading B;
 //   any              the 128 x 128 tiles with panels through registers, for
 //                    operands of any alignment; larger problems copy such
 //                    operands into the workspace first (pack.hip).
@@ -31,8 +31,6 @@ namespace libgemm {
 namespace {
 
 using namespace tile16;
-
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 struct LinearArgs {
     int64_t M, N, K;
@@ -305,7 +303,8 @@ __device__ inline f32x4 mfma16<F16>(u32x4 a, u32x4 b, f32x4 c) {
 // another and keep the address unit busy three times as long.  16-byte chunk
 // c of row r lies at c ^ r, so the 16 rows of a read fall in different banks.
 // Operands swapped: lane l has column 4*(l / 16) + r of row l % 16 in
-// register r.  Bound by reading B: 16 x 4096 x 16384 28 us, 4.8 TB/s.
+// register r.  Bound by reading B: 16 x 4096 x 16384 28 us, 4.8 TB/s (32 from call
+// to call).
 template <class T, bool BACKWARD, int ROWS>
 __global__ __launch_bounds__(512, 1) void few_kernel(LinearArgs p) {
     constexpr int WAVES = 8, RUN = 128, STEPS = RUN / 32;
@@ -605,8 +604,8 @@ hipError_t run_kernel(LinearKernel k, LinearArgs &a, hipStream_t stream) {
 }
 
 // Up to so many rows, a workgroup of finish_kernel takes them all for its columns
-// and writes the column sums' result, which saves a launch (250 x 1000 in four
-// slices of K: 8.5 us, 4.1 and 2.4 us in two launches).
+// and writes the column sums' result, which saves a launch; for more rows it takes
+// longer than that (250 x 1000 in four slices of K: 8.5 us, 4.1 + 2.4 in two).
 constexpr int64_t ONE_BLOCK = 64;
 int64_t sums_rows(LinearKernel k, int64_t M) {
     switch (k) {
@@ -638,8 +637,9 @@ bool can_pack(const PackSpec &s) {
 }
 // Copying pays where eight tiles or more read each operand and K is not short:
 // fp16, operands with odd leading dimensions, a row-major B, copied and not:
-// 250 x 4097 x 4095 42 and 45 us, 1000 x 1001 x 1001 26 and 24, 4095 x 4097 x 65 48
-// and 40, 2049 x 2049 x 2049 54 and 71, 4095 x 16385 x 4097 657 and 952.
+// 2049 x 2049 x 2049 54 and 71 us, 4095 x 16385 x 4097 657 and 952, but 1000 x
+// 1001 x 1001 26 and 24, 4095 x 4097 x 65 48 and 40.  Fewer rows gain little (250 x
+// 4097 x 4095 42 and 45) for a workspace that holds all of B.
 bool worth_packing(int64_t M, int64_t N, int64_t K) { return M >= 1024 && N >= 1024 && K >= 512; }
 // What the kernels take beside copies.
 size_t own_bytes(int64_t M, int64_t N, int64_t K) {
@@ -704,7 +704,8 @@ static bool packed_problem(const LinearProblem &p, LinearProblem &q, PackSpec sp
 LinearKernel linear_choose(const LinearProblem &p) {
     if (p.M == 0 || p.N == 0) return LinearKernel::None;
     const bool direct = p.packed || (p.K > 0 && whole_chunks(p.A, p.lda, p.K) && whole_chunks(p.B, p.ldb, p.b_kmajor ? p.K : p.N));
-    // 16 x 4096 x 4096 6.4 us, in slices of tiles 15.6; 16 x 4096 x 16384 26 and 31
+    // 16 rows so, and 17 in slices of tiles: 4096 x 1024 4.5 and 10 us, 4096 x 4096 9.6
+    // and 17.5, 4096 x 16384 32 and 41
     if (direct && p.b_kmajor && p.M <= 16 && p.N <= MOST_COLUMNS) return LinearKernel::Few16;
     if (!direct) {
         LinearProblem q;

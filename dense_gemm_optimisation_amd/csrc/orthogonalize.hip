@@ -121,7 +121,7 @@ __device__ inline void values_of(const InputArgs &p, int64_t at, int64_t there, 
 
 // Squares in 64 bits: fp32's would leave its range.  Eight values at a time, eight
 // such pieces per lane on their way together (4096 x 4096 in bf16: of four
-// rows, 256 lanes, 28 us; so 18).
+// rows, 256 lanes, 28 us; so 17 to 19).
 constexpr int NORM_THREADS = 512, NORM_PIECES = 8;
 __global__ __launch_bounds__(NORM_THREADS) void norm_kernel(InputArgs p) {
     __shared__ double scratch[NORM_THREADS / 64];

@@ -116,12 +116,7 @@ __device__ inline void store8f(float *p, int n, const float (&x)[8]) {
             if (e < n) p[e] = x[e];
     }
 }
-// The same of a type known only when running: T where `same`, else fp32.
-template <class T>
-__device__ inline void load8_as(const void *p, int64_t at, bool same, int n, float (&x)[8]) {
-    if (same) load8<T>(static_cast<const uint16_t *>(p) + at, n, x);
-    else load8f(static_cast<const float *>(p) + at, n, x);
-}
+// In a type known only when running: T where `same`, else fp32.
 template <class T>
 __device__ inline void store8_as(void *p, int64_t at, bool same, int n, const float (&x)[8]) {
     if (same) store8<T>(static_cast<uint16_t *>(p) + at, n, x);

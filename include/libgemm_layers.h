@@ -185,9 +185,11 @@ size_t gemm_experts_layer_workspace_size(int64_t tokens, int64_t experts, int64_
  * pieces of X's type, which hold 16 of its 24 bits in bf16 and 22 in fp16 (there
  * from 2^-10 up to 2^20: below in steps of 2^-31, beyond it gives infinities
  * or NaN).
- * At most GEMM_LAYER_MAX_TOKENS tokens, _EXPERTS experts and _TOP_K choices
- * (GEMM_ERR_UNSUPPORTED beyond: gemm_experts_f8 takes more tokens); H at most
- * 2^17, ldx 2^23, ld_up and ld_down 2^25. */
+ * At least one expert, one choice, no more choices than experts, and H >= 1
+ * (GEMM_ERR_INVALID_ARG).  At most GEMM_LAYER_MAX_TOKENS tokens, _EXPERTS
+ * experts and _TOP_K choices (GEMM_ERR_UNSUPPORTED beyond: gemm_experts_f8
+ * takes more tokens, with 8-bit operands); H at most 2^17, ldx 2^23, ld_up and
+ * ld_down 2^25. */
 gemm_status_t gemm_experts_layer(int64_t tokens, int64_t experts, int64_t top_k, int64_t D,
                                  int64_t H, const void *X, int64_t ldx, gemm_input_t in,
                                  const int32_t *ids, const float *weights, gemm_weights_t type,
@@ -215,18 +217,20 @@ size_t gemm_orthogonalize_workspace_size(int64_t M, int64_t N, int64_t batch);
  *   O        M x N of typeO (any), ldo >= N; beta == 0 does not read it.
  *            O = alpha * X + beta * O is a weight's step with its decay.  O
  *            may not overlap G.
- *   batch    matrices strideG and strideO elements apart; those of O must
- *            not overlap.
+ *   batch    matrices strideG and strideO elements apart; strideO is at
+ *            least what a matrix of O spans, (M - 1)*ldo + N.
  *   workspace   gemm_orthogonalize_workspace_size() bytes.
  * The sum of squares is formed in 64 bits.  X is kept between the steps to 22
  * bits of each element or to 2^-35 of its norm, whichever is more, also where
- * G's norm is far below eps.  The products take fp16 roundings of X, of E = A - s I with s the
- * mean of A's eigenvalues, and of (b + 2 c s) E + c E^2, and add in fp32,
- * which leaves X about 2^-10 of its elements' root mean square from the exact
- * steps': less than bf16's own rounding.  All are scaled by powers of two so
- * that steps whose singular values stay below 2 and whose coefficients stay
- * below 16 in magnitude are within fp16's range; others may give infinities or NaN.  A matrix with an
- * infinity or a NaN gives NaN throughout.
+ * G's norm is far below eps.  The products take fp16 roundings of X, of E = A
+ * - s I with s the mean of A's eigenvalues, and of (b + 2 c s) E + c E^2, and
+ * add in fp32, which leaves X between 2^-16 and 2^-9 of its norm from the
+ * exact steps' (five usual steps on matrices of 64 x 64 to 2048 x 2048; random
+ * ones 2^-10 to 2^-11): about bf16's own rounding or less.  All are scaled by
+ * powers of two so that steps whose singular values stay below 2 and whose
+ * coefficients stay below 16 in magnitude are within fp16's range; others may
+ * give infinities or NaN.  A matrix with an infinity or a NaN gives NaN
+ * throughout.
  * steps in 1 .. GEMM_ORTHOGONALIZE_MAX_STEPS; M and N at most 2^20, and less
  * than 2^24 blocks of 64 x 64 in a matrix (GEMM_ERR_UNSUPPORTED beyond). */
 gemm_status_t gemm_orthogonalize(int64_t M, int64_t N, const void *G, int64_t ldg,
