@@ -262,6 +262,7 @@ def test_large_lds_is_allowed_on_the_streams_device(lib, tmp_path, stream, devic
     subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
     call = f"""
 import ctypes, sys
+recorder = ctypes.CDLL({str(so)!r}, mode=ctypes.RTLD_GLOBAL)  # before HIP's own library: its names are found first
 sys.path.insert(0, {ROOT!r})
 from dense_gemm_optimisation_amd import binding as lib
 p = [i << 36 for i in range(1, 9)]
@@ -270,11 +271,10 @@ lib.gemm_orthogonalize(128, 128, p[0], 128, 0, 5, None, 0.0, 1.0, 0.0, p[1], 128
 lib.gemm_experts_layer(1, 64, 8, 4096, 1024, p[0], 4096, 1, p[1], p[2], 0, p[3], 4096, 2048 * 4096, 0, 0, 0, p[4], 1024, 4096 * 1024,
                        0, 0, 0, 3, 0.0, p[5], 4096, 1, p[6], 1 << 30, stream={stream})
 d = ctypes.c_int(-1)
-ctypes.CDLL({str(so)!r}).hipGetDevice(ctypes.byref(d))
+recorder.hipGetDevice(ctypes.byref(d))
 print("current", d.value, flush=True)
 """
-    env = dict(os.environ, LD_PRELOAD=str(so))
-    out = subprocess.run([sys.executable, "-c", call], capture_output=True, text=True, check=True, env=env).stdout
+    out = subprocess.run([sys.executable, "-c", call], capture_output=True, text=True, check=True).stdout
     said = out.split("begin\n")[1].splitlines()
     assert said == [f"attribute {device}", "launch 1"] * 3 + ["current 0"]
 
