@@ -644,7 +644,8 @@ bool worth_packing(int64_t M, int64_t N, int64_t K) { return M >= 1024 && N >= 1
 // What the kernels take beside copies.
 size_t own_bytes(int64_t M, int64_t N, int64_t K) {
     const int slices = split_slices(tiles_of(M, N, 128), K), last = last_slices(M, N, K);
-    return sums_bytes(M, N) + (slices > 1 ? partial_bytes(M, N, slices) : 0) + (last > 1 ? last_bytes(M, N, last) : 0);
+    const bool split = slices > 1 && K >= split_from(tiles_of(M, N, 128), false);
+    return sums_bytes(M, N) + (split ? partial_bytes(M, N, slices) : 0) + (last > 1 ? last_bytes(M, N, last) : 0);
 }
 // What copies of both operands take where a row of either may not be whole chunks
 // (rows that are usually start on them).

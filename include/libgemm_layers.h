@@ -226,7 +226,7 @@ size_t gemm_orthogonalize_workspace_size(int64_t M, int64_t N, int64_t batch);
  * - s I with s the mean of A's eigenvalues, and of (b + 2 c s) E + c E^2, and
  * add in fp32, which leaves X between 2^-16 and 2^-9 of its norm from the
  * exact steps' (five usual steps on matrices of 64 x 64 to 2048 x 2048; random
- * ones 2^-10 to 2^-11): about bf16's own rounding or less.  All are scaled by
+ * ones 2^-10 to 2^-12): about bf16's own rounding or less.  All are scaled by
  * powers of two so that steps whose singular values stay below 2 and whose
  * coefficients stay below 16 in magnitude are within fp16's range; others may
  * give infinities or NaN.  A matrix with an infinity or a NaN gives NaN
